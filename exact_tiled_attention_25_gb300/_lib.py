@@ -15,6 +15,9 @@ c_float = ctypes.c_float
 c_size_t = ctypes.c_size_t
 c_void_p = ctypes.c_void_p
 c_char_p = ctypes.c_char_p
+c_longlong = ctypes.c_longlong
+c_double = ctypes.c_double
+c_strides = ctypes.POINTER(c_longlong)   # host array of element strides, or None
 
 # name -> (restype, argtypes); mirrors include/attn_gb300.h
 SIGNATURES = {
@@ -85,6 +88,16 @@ SIGNATURES = {
     "attn_fwd_fp8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                              c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_float,
                              c_void_p]),
+    "attn_cross_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
+    "attn_cross_fwd": (c_int, [c_void_p] * 7 + [c_size_t] + [c_int] * 6 + [c_float, c_int, c_void_p]),
+    "attn_cross_bwd": (c_int, [c_void_p] * 11 + [c_size_t] + [c_int] * 6 + [c_float, c_int, c_void_p]),
+    "attn_rope_table": (c_int, [c_void_p, c_void_p, c_longlong, c_int, c_double, c_double, c_longlong,
+                                c_double, c_double, c_double, c_longlong, c_void_p]),
+    "attn_rope": (c_int, [c_void_p] * 7 + [c_int] * 7 + [c_strides] * 4 + [c_int, c_int, c_int, c_void_p]),
+    "attn_block_tables": (c_int, [c_void_p] * 9 + [c_int] * 5 + [c_void_p]),
+    "attn_cache_append": (c_int, [c_void_p] * 10 + [c_int] * 8 + [c_strides] * 3 + [c_int, c_int, c_void_p]),
+    "attn_cache_append_fp8": (c_int, [c_void_p] * 14 + [c_int] * 10 + [c_strides] * 3 +
+                              [c_int, c_int, c_void_p]),
     "attn_selftest_wait_timeout": (c_int, [ctypes.c_uint, c_void_p]),
     "attn_get_device_status": (c_int, [c_void_p]),
     "attn_status_string": (c_char_p, [c_int]),

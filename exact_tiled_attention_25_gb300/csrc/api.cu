@@ -5,6 +5,7 @@
 #include <string>
 
 #include "common.h"
+#include "rope.h"
 #include "sm103_prims.cuh"
 
 namespace attn {
@@ -78,6 +79,45 @@ attn_status_t check_ptrs(std::initializer_list<const void*> ptrs) {
     if (p == nullptr) return fail(ATTN_ERR_INVALID_ARG, "null tensor pointer");
     if (!aligned16(p)) return fail(ATTN_ERR_INVALID_ARG, "tensor pointer not 16-byte aligned");
   }
+  return ATTN_OK;
+}
+
+attn_status_t check_dtype(attn_dtype_t dtype) {
+  if (dtype != ATTN_BF16 && dtype != ATTN_FP16)
+    return fail(ATTN_ERR_INVALID_ARG, "dtype must be ATTN_BF16 or ATTN_FP16");
+  return ATTN_OK;
+}
+
+attn_status_t check_ints(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 3u) != 0)
+      return fail(ATTN_ERR_INVALID_ARG, "integer arrays must be non-null and 4-byte aligned");
+  return ATTN_OK;
+}
+
+// Rows of 16-bit values: heads >= 1 of d values, strides in elements that keep
+// every row 16-byte aligned.  An output's strides are positive.
+attn_status_t check_row_strides(std::initializer_list<long long> strides, bool output) {
+  for (long long x : strides)
+    if (x < (output ? 1 : 0) || (x & 7) != 0)
+      return fail(ATTN_ERR_INVALID_ARG,
+                  "strides must be non-negative (of outputs: positive) multiples of 8 elements");
+  return ATTN_OK;
+}
+
+attn_status_t check_rope(const float* cos, const float* sin, int d, int rot_dim, int max_pos, int interleaved) {
+  if (rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0)
+    return fail(ATTN_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [16, d]");
+  if (max_pos < 1) return fail(ATTN_ERR_INVALID_ARG, "the rotary tables need max_pos >= 1 rows");
+  if (interleaved != 0 && interleaved != 1)
+    return fail(ATTN_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  return check_ptrs({cos, sin});
+}
+
+attn_status_t check_page_size(int page_size, int least) {
+  if (page_size < least || page_size > 65536 || (page_size & (page_size - 1)) != 0)
+    return fail(ATTN_ERR_INVALID_ARG,
+                "page_size must be a power of two in [" + std::to_string(least) + ", 65536]");
   return ATTN_OK;
 }
 
@@ -683,6 +723,275 @@ attn_status_t attn_fwd_fp8_gqa(const uint8_t* q8, const uint8_t* k8, const uint8
   return launch_fwd_fp8(p, stream);
 }
 
+// Shape checks shared by the cross-attention entry points.
+static attn_status_t check_cross(int B, int H, int H_kv, int N_q, int N_k, int d, const int* kv_lens) {
+  attn_status_t s;
+  if (N_k < 1) return fail(ATTN_ERR_INVALID_ARG, "N_k must be >= 1");
+  if ((s = check_shape(B, H, N_q, d, 0)) != ATTN_OK) return s;
+  if ((s = check_heads(H, H_kv)) != ATTN_OK) return s;
+  if (static_cast<double>(B) * H_kv * N_k * d >= 2147483648.0)
+    return fail(ATTN_ERR_INVALID_ARG, "B*H_kv*N_k*d must be < 2^31");
+  if (B > 65535 || H > 65535) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
+  if (reinterpret_cast<uintptr_t>(kv_lens) & 3u)
+    return fail(ATTN_ERR_INVALID_ARG, "kv_lens must be 4-byte aligned");
+  return ATTN_OK;
+}
+
+size_t attn_cross_workspace_size(int B, int H, int H_kv, int N_q, int N_k, int d) {
+  if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || N_q < 1 || N_k < 1 || d < 1) return 0;
+  return cross_workspace_bytes(B, H, N_q, d, cross_plan(B, H, H_kv, N_q, N_k, d));
+}
+
+attn_status_t attn_cross_fwd(const void* q, const void* k, const void* v, const int* kv_lens, void* o,
+                             float* lse, void* workspace, size_t workspace_bytes, int B, int H, int H_kv,
+                             int N_q, int N_k, int d, float softmax_scale, attn_dtype_t dtype,
+                             cudaStream_t stream) {
+  g_last_error.clear();
+  attn_status_t s;
+  if ((s = check_cross(B, H, H_kv, N_q, N_k, d, kv_lens)) != ATTN_OK) return s;
+  if ((s = check_ptrs({q, k, v, o, lse})) != ATTN_OK) return s;
+  if ((s = check_scale(softmax_scale)) != ATTN_OK) return s;
+  if ((s = check_dtype(dtype)) != ATTN_OK) return s;
+  const CrossPlan plan = cross_plan(B, H, H_kv, N_q, N_k, d);
+  const size_t need = cross_workspace_bytes(B, H, N_q, d, plan);
+  if (need > 0) {
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+      return fail(ATTN_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned");
+    if (workspace_bytes < need)
+      return fail(ATTN_ERR_INVALID_ARG, "workspace smaller than attn_cross_workspace_size()");
+  }
+  if ((s = check_device()) != ATTN_OK) return s;
+  FwdParams p{q, k, v, o, lse, B, H, N_q, d, H_kv, nullptr, 0, 0, softmax_scale,
+              dtype == ATTN_FP16 ? 1 : 0, N_k, kv_lens};
+  return plan.splits > 0 ? launch_cross_split(p, plan, workspace, stream) : launch_cross_fwd(p, stream);
+}
+
+attn_status_t attn_cross_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                             const float* lse, const int* kv_lens, void* dq, void* dk, void* dv,
+                             void* workspace, size_t workspace_bytes, int B, int H, int H_kv, int N_q,
+                             int N_k, int d, float softmax_scale, attn_dtype_t dtype,
+                             cudaStream_t stream) {
+  g_last_error.clear();
+  attn_status_t s;
+  if ((s = check_cross(B, H, H_kv, N_q, N_k, d, kv_lens)) != ATTN_OK) return s;
+  if ((s = check_ptrs({q, k, v, o, dout, lse, dq, dk, dv, workspace})) != ATTN_OK) return s;
+  if ((s = check_scale(softmax_scale)) != ATTN_OK) return s;
+  if ((s = check_dtype(dtype)) != ATTN_OK) return s;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(ATTN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (workspace_bytes < attn_bwd_workspace_size(B, H, N_q, d))
+    return fail(ATTN_ERR_INVALID_ARG, "workspace smaller than attn_bwd_workspace_size(B, H, N_q, d)");
+  if (d == 256) return fail(ATTN_ERR_UNSUPPORTED, "the backward pass supports d = 64 and 128");
+  if ((s = check_device()) != ATTN_OK) return s;
+  const BwdWorkspace w = bwd_workspace_layout(B, H, N_q, d);
+  char* ws = static_cast<char*>(workspace);
+  BwdParams p{q, k, v, o, dout, lse, dq, dk, dv, reinterpret_cast<float*>(ws + w.dq_acc),
+              reinterpret_cast<float*>(ws + w.lse2), reinterpret_cast<float*>(ws + w.delta),
+              B, H, N_q, d, H_kv, nullptr, 0, 0, softmax_scale, dtype == ATTN_FP16 ? 1 : 0, N_k, kv_lens};
+  return launch_cross_bwd(p, stream);
+}
+
+attn_status_t attn_rope_table(float* rope_cos, float* rope_sin, long long n, int rot_dim, double base,
+                              double factor, long long orig_len, double low, double high,
+                              double attn_factor, long long first, cudaStream_t stream) {
+  g_last_error.clear();
+  attn_status_t s;
+  if (rot_dim < 16 || rot_dim > 256 || rot_dim % 16 != 0)
+    return fail(ATTN_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [16, 256]");
+  if (n < 1 || first < 0 || first > 2147483647LL || n > 2147483647LL || first + n > 2147483648LL)
+    return fail(ATTN_ERR_INVALID_ARG, "positions first .. first + n - 1 must lie in [0, 2^31)");
+  if (!(base > 1.0) || !std::isfinite(base)) return fail(ATTN_ERR_INVALID_ARG, "base must be finite and > 1");
+  if (!(factor >= 1.0) || !std::isfinite(factor))
+    return fail(ATTN_ERR_INVALID_ARG, "factor must be finite and >= 1");
+  if (orig_len < 0 || orig_len > 2147483647LL)
+    return fail(ATTN_ERR_INVALID_ARG, "orig_len must lie in [0, 2^31)");
+  if (orig_len > 0 && (!(low >= 0.0) || !(high > low) || !std::isfinite(high)))
+    return fail(ATTN_ERR_INVALID_ARG, "0 <= low < high, in turns of the original context");
+  if (!(attn_factor > 0.0) || !std::isfinite(attn_factor))
+    return fail(ATTN_ERR_INVALID_ARG, "attn_factor must be positive and finite");
+  if ((s = check_ptrs({rope_cos, rope_sin})) != ATTN_OK) return s;
+  if ((s = check_device()) != ATTN_OK) return s;
+  return launch_rope_table(rope_cos, rope_sin, n, rot_dim, base, factor, orig_len, low, high, attn_factor,
+                           first, stream);
+}
+
+attn_status_t attn_rope(const void* q, void* q_out, const void* k, void* k_out, const float* rope_cos,
+                        const float* rope_sin, const int* positions, int B, int N, int H, int H_kv, int d,
+                        int rot_dim, int max_pos, const long long* q_strides, const long long* q_out_strides,
+                        const long long* k_strides, const long long* k_out_strides, int interleaved,
+                        int inverse, attn_dtype_t dtype, cudaStream_t stream) {
+  g_last_error.clear();
+  attn_status_t s;
+  if ((s = check_shape(B, H, N, d, 0)) != ATTN_OK) return s;
+  if (H_kv < 0 || static_cast<double>(B) * H_kv * N * d >= 2147483648.0)
+    return fail(ATTN_ERR_INVALID_ARG, "H_kv must be >= 0 (0: no k) and B*H_kv*N*d < 2^31");
+  if ((s = check_rope(rope_cos, rope_sin, d, rot_dim, max_pos, interleaved)) != ATTN_OK) return s;
+  if (inverse != 0 && inverse != 1) return fail(ATTN_ERR_INVALID_ARG, "inverse must be 0 or 1");
+  if ((s = check_dtype(dtype)) != ATTN_OK) return s;
+  if ((s = check_ptrs({q, q_out})) != ATTN_OK) return s;
+  if (H_kv > 0 && (s = check_ptrs({k, k_out})) != ATTN_OK) return s;
+  if (reinterpret_cast<uintptr_t>(positions) & 3u)
+    return fail(ATTN_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+  RopeKParams p{};
+  auto put = [&](int t, const void* src, void* dst, int heads, const long long* si, const long long* so) {
+    const long long row = d, head = static_cast<long long>(N) * d, batch = head * heads;
+    p.src[t] = static_cast<const uint16_t*>(src);
+    p.dst[t] = static_cast<uint16_t*>(dst);
+    p.heads[t] = heads;
+    p.sb[t] = si ? si[0] : batch, p.sh[t] = si ? si[1] : head, p.st[t] = si ? si[2] : row;
+    p.db[t] = so ? so[0] : batch, p.dh[t] = so ? so[1] : head, p.dt[t] = so ? so[2] : row;
+    attn_status_t r = check_row_strides({p.sb[t], p.sh[t], p.st[t]}, false);
+    return r != ATTN_OK ? r : check_row_strides({p.db[t], p.dh[t], p.dt[t]}, true);
+  };
+  if ((s = put(0, q, q_out, H, q_strides, q_out_strides)) != ATTN_OK) return s;
+  if (H_kv > 0 && (s = put(1, k, k_out, H_kv, k_strides, k_out_strides)) != ATTN_OK) return s;
+  if ((s = check_device()) != ATTN_OK) return s;
+  p.rotated = 2;
+  p.cos = rope_cos, p.sin = rope_sin, p.positions = positions;
+  p.B = B, p.N = N, p.d = d, p.rot = rot_dim, p.max_pos = max_pos, p.inverse = inverse;
+  return launch_rope(p, dtype == ATTN_FP16, interleaved, stream);
+}
+
+attn_status_t attn_block_tables(int* block_table, const int* old_lens, const int* new_lens,
+                                const int* free_pages, int* seq_lens, int* cu_seqlens, long long* slots,
+                                int* positions, int* used, int B, int max_pages, int n_free, int page_size,
+                                int capacity, cudaStream_t stream) {
+  g_last_error.clear();
+  attn_status_t s;
+  if (B < 1 || max_pages < 1 || n_free < 0 || capacity < 0)
+    return fail(ATTN_ERR_INVALID_ARG, "B and max_pages must be >= 1, n_free and capacity >= 0");
+  if ((s = check_page_size(page_size, 8)) != ATTN_OK) return s;
+  if (static_cast<long long>(max_pages) * page_size > 2147483647LL)
+    return fail(ATTN_ERR_INVALID_ARG, "max_pages * page_size must be < 2^31");
+  if ((s = check_ints({block_table, old_lens, new_lens, seq_lens, cu_seqlens, used})) != ATTN_OK) return s;
+  if (n_free > 0 && (s = check_ints({free_pages})) != ATTN_OK) return s;
+  if (capacity > 0) {
+    if ((s = check_ints({positions})) != ATTN_OK) return s;
+    if (slots == nullptr || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+      return fail(ATTN_ERR_INVALID_ARG, "slots must be non-null and 8-byte aligned");
+  }
+  // every block reads the lengths while the first one writes seq_lens
+  if (seq_lens == old_lens || seq_lens == new_lens)
+    return fail(ATTN_ERR_INVALID_ARG, "seq_lens must not be old_lens or new_lens");
+  if ((s = check_device()) != ATTN_OK) return s;
+  return launch_block_tables({block_table, old_lens, new_lens, free_pages, seq_lens, cu_seqlens, slots,
+                              positions, used, B, max_pages, n_free, page_size, capacity},
+                             stream);
+}
+
+// Checks and parameters shared by the two cache appends: rows of new tokens
+// [total, heads, d] with {token, head} strides, q [total, H, d] optional.
+static attn_status_t append_common(RopeKParams* p, const void* q, void* q_out, const void* k, const void* v,
+                                   const void* k_cache, const void* v_cache, const float* rope_cos,
+                                   const float* rope_sin, int total, int H, int H_kv, int d, int rot_dim,
+                                   int max_pos, int num_pages, int page_size, const long long* q_strides,
+                                   const long long* k_strides, const long long* v_strides, int interleaved,
+                                   attn_dtype_t dtype) {
+  attn_status_t s;
+  if (total < 0 || H < 0 || H_kv < 1 || num_pages < 1)
+    return fail(ATTN_ERR_INVALID_ARG, "total and H must be >= 0, H_kv and num_pages >= 1");
+  if (d != 64 && d != 128 && d != 256) return fail(ATTN_ERR_INVALID_ARG, "d must be 64, 128 or 256");
+  if (static_cast<double>(num_pages) * page_size * H_kv * d >= 9.0e15)
+    return fail(ATTN_ERR_INVALID_ARG, "cache too large");
+  if (static_cast<double>(total) * (H > H_kv ? H : H_kv) * d >= 2147483648.0)
+    return fail(ATTN_ERR_INVALID_ARG, "total*H*d must be < 2^31");
+  if (interleaved != 0 && interleaved != 1)
+    return fail(ATTN_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  if ((s = check_dtype(dtype)) != ATTN_OK) return s;
+  if ((s = check_ptrs({k_cache, v_cache})) != ATTN_OK) return s;
+  if (total > 0 && (s = check_ptrs({k, v})) != ATTN_OK) return s;
+  if ((rope_cos == nullptr) != (rope_sin == nullptr))
+    return fail(ATTN_ERR_INVALID_ARG, "give both rope_cos and rope_sin, or neither");
+  if (rope_cos && (s = check_rope(rope_cos, rope_sin, d, rot_dim, max_pos, interleaved)) != ATTN_OK) return s;
+  if (H > 0) {
+    if (!rope_cos) return fail(ATTN_ERR_INVALID_ARG, "q is only rotated: it needs rope_cos and rope_sin");
+    if (total > 0 && (s = check_ptrs({q, q_out})) != ATTN_OK) return s;
+  }
+  auto put = [&](int t, const void* src, int heads, const long long* strides) {
+    p->src[t] = static_cast<const uint16_t*>(src);
+    p->heads[t] = heads;
+    p->st[t] = strides ? strides[0] : static_cast<long long>(heads) * d;
+    p->sh[t] = strides ? strides[1] : d;
+    return check_row_strides({p->st[t], p->sh[t]}, false);
+  };
+  if (H > 0 && (s = put(0, q, H, q_strides)) != ATTN_OK) return s;
+  if ((s = put(1, k, H_kv, k_strides)) != ATTN_OK) return s;
+  if ((s = put(2, v, H_kv, v_strides)) != ATTN_OK) return s;
+  p->dst[0] = static_cast<uint16_t*>(q_out);
+  p->dh[0] = d, p->dt[0] = static_cast<long long>(H) * d;
+  p->rotated = rope_cos ? 2 : 0;
+  p->cos = rope_cos, p->sin = rope_sin;
+  p->B = 1, p->N = total, p->d = d, p->rot = rope_cos ? rot_dim : 0, p->max_pos = max_pos;
+  return ATTN_OK;
+}
+
+attn_status_t attn_cache_append(const void* q, void* q_out, const void* k, const void* v, void* k_cache,
+                                void* v_cache, const long long* slots, const float* rope_cos,
+                                const float* rope_sin, const int* positions, int total, int H, int H_kv,
+                                int d, int rot_dim, int max_pos, int num_pages, int page_size,
+                                const long long* q_strides, const long long* k_strides,
+                                const long long* v_strides, int interleaved, attn_dtype_t dtype,
+                                cudaStream_t stream) {
+  g_last_error.clear();
+  attn_status_t s;
+  if ((s = check_page_size(page_size, 8)) != ATTN_OK) return s;
+  RopeKParams p{};
+  if ((s = append_common(&p, q, q_out, k, v, k_cache, v_cache, rope_cos, rope_sin, total, H, H_kv, d,
+                         rot_dim, max_pos, num_pages, page_size, q_strides, k_strides, v_strides,
+                         interleaved, dtype)) != ATTN_OK)
+    return s;
+  if (total > 0) {
+    if (slots == nullptr || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+      return fail(ATTN_ERR_INVALID_ARG, "slots must be non-null and 8-byte aligned");
+    if (rope_cos && (s = check_ints({positions})) != ATTN_OK) return s;
+  }
+  if ((s = check_device()) != ATTN_OK) return s;
+  if (total == 0) return ATTN_OK;
+  p.dst[1] = static_cast<uint16_t*>(k_cache);
+  p.dst[2] = static_cast<uint16_t*>(v_cache);
+  p.positions = positions;
+  p.slots = slots;
+  p.num_slots = static_cast<long long>(num_pages) * page_size;
+  return launch_rope(p, dtype == ATTN_FP16, interleaved, stream);
+}
+
+attn_status_t attn_cache_append_fp8(const void* q, void* q_out, const void* k, const void* v,
+                                    uint8_t* k_cache, uint8_t* v_cache, float* k_descale, float* v_descale,
+                                    const int* block_table, const int* seq_lens, const int* cu_seqlens,
+                                    const float* rope_cos, const float* rope_sin,
+                                    const float* hadamard_signs, int B, int total, int H, int H_kv, int d,
+                                    int rot_dim, int max_pos, int num_pages, int page_size, int max_pages,
+                                    const long long* q_strides, const long long* k_strides,
+                                    const long long* v_strides, int interleaved, attn_dtype_t dtype,
+                                    cudaStream_t stream) {
+  g_last_error.clear();
+  attn_status_t s;
+  if (B < 1 || max_pages < 1) return fail(ATTN_ERR_INVALID_ARG, "B and max_pages must be >= 1");
+  if ((s = check_page_size(page_size, 16)) != ATTN_OK) return s;
+  if (static_cast<long long>(max_pages) * page_size > 2147483647LL)
+    return fail(ATTN_ERR_INVALID_ARG, "max_pages * page_size must be < 2^31");
+  RopeKParams p{};
+  if ((s = append_common(&p, q, q_out, k, v, k_cache, v_cache, rope_cos, rope_sin, total, H, H_kv, d,
+                         rot_dim, max_pos, num_pages, page_size, q_strides, k_strides, v_strides,
+                         interleaved, dtype)) != ATTN_OK)
+    return s;
+  if (d != 128) return fail(ATTN_ERR_UNSUPPORTED, "the FP8 cache supports d = 128");
+  if ((s = check_ptrs({k_descale, v_descale})) != ATTN_OK) return s;
+  if (hadamard_signs && !aligned16(hadamard_signs))
+    return fail(ATTN_ERR_INVALID_ARG, "hadamard_signs not 16-byte aligned");
+  if ((s = check_ints({block_table, seq_lens, cu_seqlens})) != ATTN_OK) return s;
+  if ((s = check_device()) != ATTN_OK) return s;
+  if (total == 0) return ATTN_OK;
+  const AppendFp8Params a{k, v, p.st[1], p.sh[1], p.st[2], p.sh[2], k_cache, v_cache, k_descale, v_descale,
+                          block_table, seq_lens, cu_seqlens, rope_cos, rope_sin, hadamard_signs, nullptr,
+                          B, total, H_kv, num_pages, page_size, max_pages, p.rot, max_pos};
+  p.heads[1] = p.heads[2] = 0;
+  p.cu_seqlens = cu_seqlens;
+  p.seq_lens = seq_lens;
+  p.requests = B;
+  return launch_append_fp8(a, p, dtype == ATTN_FP16, interleaved, stream);
+}
+
 attn_status_t attn_selftest_wait_timeout(unsigned limit_us, cudaStream_t stream) {
   g_last_error.clear();
   attn_status_t s;
@@ -719,8 +1028,13 @@ attn_status_t attn_get_device_status(cudaStream_t stream) {
   if (value == kDevBadSeqlens)
     return fail(ATTN_ERR_INVALID_ARG,
                 "cu_seqlens inconsistent (an entry outside [0, total], decreasing, or a sequence "
-                "longer than max_seqlen), or a decode seq_lens / block_table entry out of range; "
+                "longer than max_seqlen), a kv_lens entry outside [0, N_k], or a decode seq_lens / "
+                "block_table entry out of range; "
                 "those sequences or pages were skipped");
+  if (value == kDevBadTables)
+    return fail(ATTN_ERR_INVALID_ARG,
+                "request lengths, free pages, slots, table entries or positions that do not fit the "
+                "block table, the cache or the rotary tables; those tokens were skipped");
   return fail(ATTN_ERR_TIMEOUT, std::string("kernel wait timed out in role ") +
                                     (role < 8 ? roles[role] : "?") + " (code " +
                                     std::to_string(value) + ")");

@@ -115,7 +115,9 @@ struct Bars {
   int abort_flag;
   int q_items;     // Q slots the producer filled (for draining after an abort)
   int do_items;    // dO slots the producer filled
+  uint64_t kv_clean;   // cross attention: rows of K and V behind the keys are zeroed
 };
+static_assert(sizeof(Bars) <= 256, "barrier area overflow");
 
 struct BwdKParams {
   void* dk;
@@ -133,6 +135,8 @@ struct BwdKParams {
   int group;               // query heads per key/value head
   float scale;
   float scale_log2;
+  int Nk;                  // cross attention: keys of every sequence (N counts queries)
+  const int* kv_lens;      // cross attention: keys each batch entry sees, or nullptr
 };
 
 // Sequence b of a packed batch: first token and length, or false when its
@@ -237,7 +241,13 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------ main ----
-template <int D, bool CAUSAL, bool FP16, bool PACKED>
+// CROSS: keys of another length than the queries (K, V, dK, dV [B, H_kv, Nk, d]),
+// of which batch entry b sees the first kv_lens[b]; rows of dK and dV behind
+// them are written as zeros.  The rows of K and V there may hold anything, NaN
+// included, so the compute warps zero them in shared memory before the first
+// product: zero rows give S = dP = 0, and P is set to 0 for them as for rows
+// past the tensor.
+template <int D, bool CAUSAL, bool FP16, bool PACKED, bool CROSS = false>
 __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -259,7 +269,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   // One CTA per (key tile j, key/value head hk, batch b).  Causal: a 1-D grid
   // ordered by work, key tile 0 (which meets every query tile) of every head
   // first.  Non-causal: (tile, head, batch).
-  const int ntiles = (kp.N + C::BN - 1) / C::BN;
+  const int ntiles = ((CROSS ? kp.Nk : kp.N) + C::BN - 1) / C::BN;
   const int j = CAUSAL ? static_cast<int>(blockIdx.x / (gridDim.x / ntiles)) : static_cast<int>(blockIdx.x);
   const int bhk = CAUSAL ? static_cast<int>(blockIdx.x % (gridDim.x / ntiles))
                          : static_cast<int>(blockIdx.z * kp.H_kv + blockIdx.y);
@@ -274,6 +284,29 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       return;
     }
     if (j * C::BN >= N) return;
+  }
+  int Nkv = N;                             // keys this batch entry sees
+  bool clean = false;                      // rows of this key tile to zero
+  if constexpr (CROSS) {
+    static_assert(!CAUSAL && !PACKED, "cross attention is neither causal nor packed");
+    Nkv = kp.Nk;
+    if (kp.kv_lens) {
+      const int n = kp.kv_lens[b];
+      const bool bad = n < 0 || n > kp.Nk;
+      if (bad && threadIdx.x == 0 && j == 0) atomicCAS(kp.status, 0, kDevBadSeqlens);
+      Nkv = bad ? 0 : n;
+    }
+    if (j * C::BN >= Nkv) {
+      // no key of this tile is seen: its rows of dK and dV are zero
+      const int rows = min(C::BN, kp.Nk - j * C::BN);
+      const size_t first = (static_cast<size_t>(bhk) * kp.Nk + j * C::BN) * D;
+      uint4* zk = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kp.dk) + first);
+      uint4* zv = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kp.dv) + first);
+      for (int x = threadIdx.x; x < rows * (D / 8); x += C::THREADS)
+        zk[x] = zv[x] = make_uint4(0u, 0u, 0u, 0u);
+      return;
+    }
+    clean = Nkv < kp.Nk && (j + 1) * C::BN > Nkv;
   }
   const int nQ = (N + C::BM - 1) / C::BM;
   const int i0 = CAUSAL ? j : 0;
@@ -300,6 +333,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     mbar_init(&bars.dq_free, 256);
     mbar_init(&bars.dkv_full, 1);
     mbar_init(&bars.drain, 1);
+    if constexpr (CROSS) mbar_init(&bars.kv_clean, 256);
     bars.abort_flag = 0;
     bars.q_items = 0;
     bars.do_items = 0;
@@ -432,6 +466,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       // warpgroups form P^T(n), and their dS phase starts as soon as P^T(n) is
       // written; the P phase of step n+1 overlaps dK(n), dQ(n).
       bool ok = mbar_wait(&bars.kv_full, 0, ab, kDevTimeoutMma) && wait_q(0);
+      if constexpr (CROSS) ok = ok && (!clean || mbar_wait(&bars.kv_clean, 0, ab, kDevTimeoutMma));
       if (ok) {
         tc_fence_after_sync();
         issue_s(slot_q(0));
@@ -491,12 +526,25 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     const int k = quarter * 32 + lane;               // key row of the tile = TMEM lane
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const int key_g = j * C::BN + k;
-    const bool key_ok = key_g < N;
+    const bool key_ok = key_g < Nkv;
     const float c2 = kp.scale_log2;
     const uint32_t sDSrow = smem_u32(smem + C::OFF_DS) + h * C::CHUNK + k * 128;
     bool ok = true;
+    if constexpr (CROSS) {
+      if (clean) {
+        // on a timeout nothing is signalled, and every other wait gives up too
+        ok = mbar_wait(&bars.kv_full, 0, ab, kDevTimeoutSoftmax);
+        if (ok) {
+          const int row0 = Nkv - j * C::BN;
+          zero_tile_rows<C::CH, C::CHUNK>(smem + C::OFF_K, row0, threadIdx.x, 256);
+          zero_tile_rows<C::CH, C::CHUNK>(smem + C::OFF_V, row0, threadIdx.x, 256);
+          fence_proxy_async_smem();
+          mbar_arrive(&bars.kv_clean);
+        }
+      }
+    }
     int i = i0;                                      // query tile of step n
-    for (int n = 0; n < nsteps; ++n, i = (i + 1 == nQ) ? i0 : i + 1) {
+    for (int n = 0; (!CROSS || ok) && n < nsteps; ++n, i = (i + 1 == nQ) ? i0 : i + 1) {
       const int st = n % C::NQS;
       const float4* nlse4 = reinterpret_cast<const float4*>(smem + C::OFF_LD + st * 1024);  // -L log2 e
       const float4* ndvec4 = nlse4 + 32;                                                  // -D
@@ -605,7 +653,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       const float mul = h ? kp.scale : 1.f;
       // [B, H_kv, N, d], or [total, H_kv, d] for a packed batch
       const size_t krow = PACKED ? static_cast<size_t>(seq0 + key_g) * kp.H_kv + hk
-                                 : static_cast<size_t>(bhk) * N + key_g;
+                                 : static_cast<size_t>(bhk) * (CROSS ? kp.Nk : N) + key_g;
       uint16_t* dst_row = static_cast<uint16_t*>(h ? kp.dk : kp.dv) + krow * D;
 #pragma unroll 1
       for (int c0 = 0; c0 < D / 32; ++c0) {
@@ -615,11 +663,12 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float a = __uint_as_float(v[2 * e]) * mul;
-          const float b = __uint_as_float(v[2 * e + 1]) * mul;
+          float a = __uint_as_float(v[2 * e]) * mul;
+          float b = __uint_as_float(v[2 * e + 1]) * mul;
+          if (CROSS && !key_ok) a = b = 0.f;   // behind the keys, whatever dO holds
           pk[e] = FP16 ? cvt_pack_f16(a, b) : cvt_pack_bf16(a, b);
         }
-        if (key_ok) {
+        if (CROSS ? key_g < kp.Nk : key_ok) {
           uint4* dst = reinterpret_cast<uint4*>(dst_row + c0 * 32);
 #pragma unroll
           for (int x = 0; x < 4; ++x)
@@ -708,7 +757,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   }
 }
 
-template <int D, bool CAUSAL, bool FP16, bool PACKED>
+template <int D, bool CAUSAL, bool FP16, bool PACKED, bool CROSS = false>
 attn_status_t launch_bwd_t(const BwdParams& p, cudaStream_t stream) {
   using C = BwdCfg<D>;
   const int Npad = (p.N + 127) / 128 * 128;
@@ -725,7 +774,8 @@ attn_status_t launch_bwd_t(const BwdParams& p, cudaStream_t stream) {
   }
   // 2. main
   {
-    auto kern = bwd_main_kernel<D, CAUSAL, FP16, PACKED>;
+    auto kern = bwd_main_kernel<D, CAUSAL, FP16, PACKED, CROSS>;
+    const int N_keys = CROSS ? p.N_k : p.N;
     attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES);
     if (s != ATTN_OK) return s;
     CUtensorMap tq, tk, tv, tdo, tdq;
@@ -749,8 +799,8 @@ attn_status_t launch_bwd_t(const BwdParams& p, cudaStream_t stream) {
       const uint64_t pq = static_cast<uint64_t>(p.B) * p.H, pkv = static_cast<uint64_t>(p.B) * p.H_kv;
       if ((s = make_tmap_3d(&tq, p.q, 2, D, p.N, pq, 64, 128)) != ATTN_OK) return s;
       if ((s = make_tmap_3d(&tdo, p.dout, 2, D, p.N, pq, 64, 128)) != ATTN_OK) return s;
-      if ((s = make_tmap_3d(&tk, p.k, 2, D, p.N, pkv, 64, 128)) != ATTN_OK) return s;
-      if ((s = make_tmap_3d(&tv, p.v, 2, D, p.N, pkv, 64, 128)) != ATTN_OK) return s;
+      if ((s = make_tmap_3d(&tk, p.k, 2, D, N_keys, pkv, 64, 128)) != ATTN_OK) return s;
+      if ((s = make_tmap_3d(&tv, p.v, 2, D, N_keys, pkv, 64, 128)) != ATTN_OK) return s;
       // float32 dQ accumulator [B * H, N, d]: reduce boxes of 32 rows x 32 columns
       if ((s = make_tmap_3d(&tdq, p.dq_acc, 4, D, p.N, pq, 32, 32)) != ATTN_OK) return s;
     }
@@ -758,8 +808,8 @@ attn_status_t launch_bwd_t(const BwdParams& p, cudaStream_t stream) {
     if (!status) return fail(ATTN_ERR_CUDA, "status word unavailable");
     BwdKParams kp{p.dk,  p.dv,    p.dq_acc, p.lse2, p.delta, status,        p.cu_seqlens,
                   p.N,   Npad,    p.total,  p.H,    p.H_kv,  p.H / p.H_kv,  p.scale,
-                  p.scale * kLog2e};
-    const unsigned ntiles = static_cast<unsigned>((p.N + 127) / 128);
+                  p.scale * kLog2e, N_keys, p.kv_lens};
+    const unsigned ntiles = static_cast<unsigned>((N_keys + 127) / 128);
     const dim3 grid = CAUSAL ? dim3(ntiles * p.H_kv * p.B, 1, 1) : dim3(ntiles, p.H_kv, p.B);
     kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(tq, tk, tv, tdo, tdq, kp);
     cudaError_t e = cudaGetLastError();
@@ -803,6 +853,19 @@ attn_status_t launch_bwd(const BwdParams& p, cudaStream_t stream) {
   switch (p.d) {
     case 64: return launch_bwd_d<64>(p, stream);
     case 128: return launch_bwd_d<128>(p, stream);
+  }
+  return fail(ATTN_ERR_UNSUPPORTED, "the backward pass supports d = 64 and 128");
+}
+
+attn_status_t launch_cross_bwd(const BwdParams& p, cudaStream_t stream) {
+  if (p.H > 65535 || p.B > 65535) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
+  switch (p.d) {
+    case 64:
+      return p.fp16 ? launch_bwd_t<64, false, true, false, true>(p, stream)
+                    : launch_bwd_t<64, false, false, false, true>(p, stream);
+    case 128:
+      return p.fp16 ? launch_bwd_t<128, false, true, false, true>(p, stream)
+                    : launch_bwd_t<128, false, false, false, true>(p, stream);
   }
   return fail(ATTN_ERR_UNSUPPORTED, "the backward pass supports d = 64 and 128");
 }

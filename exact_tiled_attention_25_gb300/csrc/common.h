@@ -54,6 +54,8 @@ struct FwdParams {
   int causal;
   float scale;
   int fp16;   // 0 = bf16, 1 = fp16
+  int N_k = 0;                     // cross attention: keys per sequence (N counts queries)
+  const int* kv_lens = nullptr;    // cross attention: device [B] keys seen, or nullptr (all N_k)
 };
 
 struct BwdParams {
@@ -76,6 +78,8 @@ struct BwdParams {
   int causal;
   float scale;
   int fp16;
+  int N_k = 0;                     // cross attention, as in FwdParams
+  const int* kv_lens = nullptr;
 };
 
 struct Fp8QuantParams {
@@ -120,6 +124,9 @@ attn_status_t launch_fwd_sched(const FwdParams& p, int sched, cudaStream_t strea
 // Persistent forward (cluster launch control) for packed causal batches.
 attn_status_t launch_fwd_persistent(const FwdParams& p, cudaStream_t stream);
 attn_status_t launch_bwd(const BwdParams& p, cudaStream_t stream);
+// Cross attention (N_k keys): one query tile pair per CTA, and its backward.
+attn_status_t launch_cross_fwd(const FwdParams& p, cudaStream_t stream);
+attn_status_t launch_cross_bwd(const BwdParams& p, cudaStream_t stream);
 attn_status_t launch_fp8_quantize(const Fp8QuantParams& p, cudaStream_t stream);
 attn_status_t launch_fwd_fp8(const Fp8FwdParams& p, cudaStream_t stream);
 
@@ -211,5 +218,27 @@ inline size_t decode_workspace_bytes(int B, int H, int H_kv, int n_q, int d, int
 }
 
 attn_status_t launch_decode(const DecodeParams& p, cudaStream_t stream);
+
+// How a cross-attention forward runs.  splits > 0: the split kernel (decode.cu)
+// on tiles of 128 query rows of one key/value head (its G * N_q rows together)
+// with the keys in `splits` ranges; splits = 0: the forward kernel (fwd.cu).
+struct CrossPlan {
+  int splits, tiles_per_split, qtiles;
+};
+inline CrossPlan cross_plan(int B, int H, int H_kv, int N_q, int N_k, int d) {
+  const long long rows = static_cast<long long>(H / H_kv) * N_q;
+  const long long qtiles = (rows + 127) / 128;
+  if (d == 256 || qtiles > 1) return {0, 0, 0};
+  const DecodeSplits sp = decode_splits(B, H_kv * static_cast<int>(qtiles), N_k);
+  return {sp.splits, sp.tiles_per_split, static_cast<int>(qtiles)};
+}
+// The split kernel's float32 partial O and log-sum-exp (none for one split).
+inline size_t cross_workspace_bytes(int B, int H, int N_q, int d, const CrossPlan& plan) {
+  if (plan.splits <= 1) return 0;
+  const size_t rows = static_cast<size_t>(B) * H * N_q * plan.splits;
+  return align_up(rows * d * sizeof(float), 256) + align_up(rows * sizeof(float), 256);
+}
+attn_status_t launch_cross_split(const FwdParams& p, const CrossPlan& plan, void* workspace,
+                                 cudaStream_t stream);
 
 }  // namespace attn

@@ -101,6 +101,8 @@ struct FwdKParams {
   int H;
   int group;               // query heads per key/value head
   float scale_log2;   // softmax_scale * log2(e)
+  int Nk;                  // cross attention: keys of every sequence (N counts queries)
+  const int* kv_lens;      // cross attention: keys each batch entry may see, or nullptr (all)
 };
 
 __device__ __forceinline__ float lg2_approx(float x) {
@@ -112,8 +114,13 @@ __device__ __forceinline__ float lg2_approx(float x) {
 // PACKED: a batch of sequences packed back to back ([total, H, d], LSE
 // [H, total], offsets cu_seqlens); otherwise [B, H, N, d] and LSE [B, H, N].
 // SCHED: 0, or kSchedOneTile / kSchedEager (measurement variants).
+// CROSS: keys of another length than the queries, K and V [B, H_kv, Nk, d], of
+// which batch entry b sees the first kv_lens[b].  The rows behind them may hold
+// anything, NaN included: their scores are replaced by -inf, and their rows of
+// V, which meet P = 0 in the second product (0 * NaN = NaN), are zeroed in
+// shared memory before it.
 template <int D, bool CAUSAL, bool FP16, bool PACKED, int SCHED = 0,
-          int NQ_ = ((SCHED & kSchedOneTile) || D > 128) ? 1 : 2>
+          int NQ_ = ((SCHED & kSchedOneTile) || D > 128) ? 1 : 2, bool CROSS = false>
 __global__ void __launch_bounds__(FwdCfg<D, NQ_>::THREADS, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const FwdKParams kp) {
@@ -166,7 +173,27 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ_>::THREADS, 1)
     N = end - seq0;
     if (g * NQ * BM >= N) return;
   }
-  const int nKtot = (N + BN - 1) / BN;
+  int Nkv = N;                             // keys this batch entry sees
+  if constexpr (CROSS) {
+    static_assert(!CAUSAL && !PACKED, "cross attention is neither causal nor packed");
+    Nkv = kp.Nk;
+    if (kp.kv_lens) {
+      const int n = kp.kv_lens[blockIdx.z];
+      const bool bad = n < 0 || n > kp.Nk;
+      if (bad && threadIdx.x == 0) atomicCAS(kp.status, 0, kDevBadSeqlens);
+      Nkv = bad ? 0 : n;
+    }
+    if (Nkv == 0) {
+      // no key: O = 0 and LSE = -inf for the CTA's rows
+      const int row0 = g * NQ * BM, rows = min(NQ * BM, N - row0);
+      const size_t first = static_cast<size_t>(bh) * N + row0;
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kp.o) + first * D);
+      for (int i = threadIdx.x; i < rows * (D / 8); i += C::THREADS) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = threadIdx.x; i < rows; i += C::THREADS) kp.lse[first + i] = -INFINITY;
+      return;
+    }
+  }
+  const int nKtot = (Nkv + BN - 1) / BN;
 
   int nK[NQ];
   int nKmax = 0;
@@ -403,8 +430,8 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ_>::THREADS, 1)
       tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
       tmem_ld_wait();
       const int kbase = j * BN + 64 * h;
-      if ((CAUSAL && j == qt) || kbase + 64 > N) {
-        const int lim = (CAUSAL ? min(N, row_g + 1) : N) - kbase;
+      if ((CAUSAL && j == qt) || kbase + 64 > Nkv) {
+        const int lim = (CAUSAL ? min(Nkv, row_g + 1) : Nkv) - kbase;
 #pragma unroll
         for (int c = 0; c < 64; ++c)
           if (c >= lim) sr[c] = __float_as_uint(-INFINITY);
@@ -466,6 +493,21 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ_>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
           tmem_st32(tO + c0 * 32, o);
+        }
+      }
+      if constexpr (CROSS) {
+        // the last tile's rows of V behind the keys (rows past the tensor are
+        // zero already); with two query tiles both write the same zeros
+        if (Nkv < kp.Nk && (j + 1) * BN > Nkv) {
+          const int item = 2 * j + 1;
+          if (__any_sync(0xffffffffu, !mbar_wait(&kv_full[item % NSLOT], (item / NSLOT) & 1, ab,
+                                                 kDevTimeoutSoftmax))) {
+            ok = false;
+            break;
+          }
+          zero_tile_rows<C::CH, C::CHUNK_BYTES>(sKV + (item % NSLOT) * C::TILE_BYTES, Nkv - j * BN,
+                                                (warp % 8) * 32 + lane, 256);
+          fence_proxy_async_smem();
         }
       }
       tmem_st_wait();
@@ -582,6 +624,29 @@ attn_status_t launch_fwd_t(const FwdParams& p, cudaStream_t stream) {
   return ATTN_OK;
 }
 
+// Cross attention: N query rows against N_k keys (p.N, p.N_k).
+template <int D, bool FP16>
+attn_status_t launch_cross_t(const FwdParams& p, cudaStream_t stream) {
+  using C = FwdCfg<D>;
+  auto kern = fwd_kernel<D, false, FP16, false, 0, C::NQ, true>;
+  attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES);
+  if (s != ATTN_OK) return s;
+  CUtensorMap tq, tk, tv;
+  const uint64_t planes_kv = static_cast<uint64_t>(p.B) * p.H_kv;
+  if ((s = make_tmap_3d(&tq, p.q, 2, D, p.N, static_cast<uint64_t>(p.B) * p.H, 64, BM)) != ATTN_OK) return s;
+  if ((s = make_tmap_3d(&tk, p.k, 2, D, p.N_k, planes_kv, 64, BN)) != ATTN_OK) return s;
+  if ((s = make_tmap_3d(&tv, p.v, 2, D, p.N_k, planes_kv, 64, BN)) != ATTN_OK) return s;
+  int* status = device_status_word();
+  if (!status) return fail(ATTN_ERR_CUDA, "status word unavailable");
+  FwdKParams kp{p.o, p.lse, status, nullptr, p.N, 0, p.H, p.H / p.H_kv, p.scale * 1.4426950408889634f,
+                p.N_k, p.kv_lens};
+  const dim3 grid((p.N + BM * C::NQ - 1) / (BM * C::NQ), p.H, p.B);
+  kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(tq, tk, tv, kp);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail_cuda(e, "cross attention kernel launch");
+  return ATTN_OK;
+}
+
 template <int D, bool PACKED>
 attn_status_t launch_fwd_dp(const FwdParams& p, cudaStream_t stream) {
   if (p.causal)
@@ -608,6 +673,15 @@ attn_status_t launch_fwd(const FwdParams& p, cudaStream_t stream) {
     case 64: return launch_fwd_d<64>(p, stream);
     case 128: return launch_fwd_d<128>(p, stream);
     case 256: return launch_fwd_d<256>(p, stream);
+  }
+  return fail(ATTN_ERR_INVALID_ARG, "d must be 64, 128 or 256");
+}
+
+attn_status_t launch_cross_fwd(const FwdParams& p, cudaStream_t stream) {
+  switch (p.d) {
+    case 64: return p.fp16 ? launch_cross_t<64, true>(p, stream) : launch_cross_t<64, false>(p, stream);
+    case 128: return p.fp16 ? launch_cross_t<128, true>(p, stream) : launch_cross_t<128, false>(p, stream);
+    case 256: return p.fp16 ? launch_cross_t<256, true>(p, stream) : launch_cross_t<256, false>(p, stream);
   }
   return fail(ATTN_ERR_INVALID_ARG, "d must be 64, 128 or 256");
 }

@@ -27,6 +27,8 @@ enum : int {
   kDevTimeoutSelftest = 0x700, // the wait of attn_selftest_wait_timeout
   kDevBadSeqlens = 0x800,      // cu_seqlens entry outside [0, total], decreasing, or a
                                // sequence longer than max_seqlen: that sequence is skipped
+  kDevBadTables = 0x900,       // request lengths, free pages, slots or positions that do not
+                               // fit their tables: those tokens are skipped
 };
 
 // Wall-clock budget for any single barrier wait (nanoseconds).  Every
@@ -473,6 +475,20 @@ __device__ __forceinline__ void st_shared_v4(uint32_t saddr, uint32_t a, uint32_
 }
 
 // ------------------------------------------------------------ arithmetic ----
+// Zero rows [row0, 128) of a tile of 128 rows, stored as CH chunks of 128 bytes
+// per row (the 128-byte swizzle moves pieces only within a row, so whole rows
+// can be cleared without it).  The caller's nthreads threads, tid 0 ..
+// nthreads - 1, share the work; a proxy fence must follow before the tensor
+// core reads the tile.
+template <int CH, int CHUNK_BYTES>
+__device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int row0, int tid, int nthreads) {
+  const int pieces = (128 - row0) * 8;
+  for (int i = tid; i < pieces * CH; i += nthreads) {
+    const int c = i / pieces, at = i - c * pieces;
+    st_shared_v4(smem_u32(tile + c * CHUNK_BYTES + row0 * 128 + at * 16), 0u, 0u, 0u, 0u);
+  }
+}
+
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

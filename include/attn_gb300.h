@@ -565,10 +565,202 @@ attn_status_t attn_fwd_fp8_gqa(const uint8_t* q8, const uint8_t* k8, const uint8
                                cudaStream_t stream);
 
 /*
+ * attn_cross_workspace_size -- bytes of device scratch attn_cross_fwd needs (the
+ * partial results of its key ranges when there are few query rows; 0 for most
+ * shapes).  Returns 0 for invalid sizes.
+ */
+size_t attn_cross_workspace_size(int B, int H, int H_kv, int N_q, int N_k, int d);
+
+/*
+ * attn_cross_fwd -- cross attention: N_q query rows against N_k keys and values
+ * of another sequence (a decoder's queries, an encoder's states).
+ *   q, o       : [B, H, N_q, d] in `dtype`;   lse : [B, H, N_q] float32.
+ *   k, v       : [B, H_kv, N_k, d]; query head h reads head h / (H / H_kv).
+ *   kv_lens    : DEVICE int32 [B], 0 <= kv_lens[b] <= N_k: batch entry b sees its
+ *                first kv_lens[b] keys; NULL: all N_k.  What the rows behind them
+ *                hold does not matter (NaN and infinities included).  An entry
+ *                out of range counts as 0 and is reported by
+ *                attn_get_device_status() as ATTN_ERR_INVALID_ARG.
+ *   A batch entry without keys gets O = 0 and LSE = -inf.
+ *   workspace  : at least attn_cross_workspace_size() bytes, 256-byte aligned;
+ *                NULL where that is 0.  Calls that overlap on the GPU (two
+ *                streams, two captured graphs) need one each.
+ * No mask but kv_lens.  d = 64, 128 or 256; B, H <= 65535.  N_q = 1 is a decode
+ * step; few query rows are spread over the machine by ranges of keys.
+ * Source: exact attention ("FlashAttention-3: Hopper Asynchrony and FP8
+ * Attention", "Symbol Map") with a score matrix of N_q rows and N_k columns.
+ */
+attn_status_t attn_cross_fwd(const void* q, const void* k, const void* v, const int* kv_lens, void* o,
+                             float* lse, void* workspace, size_t workspace_bytes, int B, int H,
+                             int H_kv, int N_q, int N_k, int d, float softmax_scale,
+                             attn_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * attn_cross_bwd -- dQ, dK, dV of sum(O * dO) for attn_cross_fwd.
+ *   q, o, dout, dq : [B, H, N_q, d];   k, v, dk, dv : [B, H_kv, N_k, d];   lse and
+ *   kv_lens as there.  dK and dV rows behind kv_lens[b] are written as zeros, and
+ *   dQ of a batch entry without keys is zero.
+ *   workspace : attn_bwd_workspace_size(B, H, N_q, d) bytes, 256-byte aligned.
+ * d = 64 or 128.  dK and dV are sums in a fixed order; dQ adds one float32
+ * term per 128 keys in any order, as attn_bwd does, so its last bits may differ
+ * between runs when N_k > 128.
+ * Source: as attn_bwd.
+ */
+attn_status_t attn_cross_bwd(const void* q, const void* k, const void* v, const void* o,
+                             const void* dout, const float* lse, const int* kv_lens, void* dq,
+                             void* dk, void* dv, void* workspace, size_t workspace_bytes, int B, int H,
+                             int H_kv, int N_q, int N_k, int d, float softmax_scale,
+                             attn_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * attn_rope_table -- cosines and sines of rotary positions first .. first + n - 1.
+ *   rope_cos, rope_sin : DEVICE float32 [n, rot_dim / 2] (written):
+ *       attn_factor * cos(p theta'_i), attn_factor * sin(p theta'_i),  p = first + row,
+ *       theta_i = base^(-2 i / rot_dim),
+ *       theta'_i = theta_i (g_i + (1 - g_i) / factor),
+ *       g_i = clamp((orig_len theta_i / (2 pi) - low) / (high - low), 0, 1),
+ *             or 0 when orig_len = 0.
+ *   factor = 1 is the plain ladder; factor > 1 stretches a model trained on
+ *   orig_len positions: with orig_len = 0 every frequency is divided by it
+ *   (position interpolation), else only those that make few turns within orig_len
+ *   (none kept below `low` turns, all from `high` on).
+ * rot_dim: a multiple of 16 in [16, 256]; positions in [0, 2^31); base > 1;
+ * factor >= 1; 0 <= low < high (used when orig_len > 0); attn_factor > 0.
+ * Source: the tables that attn_fp8_quantize_rope and attn_rope take.
+ */
+attn_status_t attn_rope_table(float* rope_cos, float* rope_sin, long long n, int rot_dim, double base,
+                              double factor, long long orig_len, double low, double high,
+                              double attn_factor, long long first, cudaStream_t stream);
+
+/*
+ * attn_rope -- rotary position embedding of 16-bit queries and keys.
+ *   q, q_out : rows of d values for B batch entries, H heads, N tokens;  k, k_out
+ *              the same with H_kv heads (H_kv = 0: no k, the pointers are unused).
+ *              The output may be the input (in place, with the same strides);
+ *              other overlaps are not allowed.
+ *   *_strides: HOST arrays {batch, head, token} of element strides, or NULL for
+ *              contiguous [B, heads, N, d].  {0, d, heads * d} with B = 1 is a
+ *              packed batch [total, heads, d]; larger token strides read rows of a
+ *              fused projection in place.  Multiples of 8; output strides > 0.
+ *   rope_cos, rope_sin : DEVICE float32 [max_pos, rot_dim / 2].
+ *   positions: DEVICE int32 [B, N], or NULL (token n is at position n).  Rows of
+ *              a negative position (padding) are copied; one at or past max_pos is
+ *              copied and reported by attn_get_device_status().
+ *   The first rot_dim columns of a row are rotated, the others copied: with c, s =
+ *   rope_cos[p][i], rope_sin[p][i] the pair (x, y) becomes (x c - y s, y c + x s);
+ *   pair i is columns (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved = 1.
+ *   inverse  : 1 = with -s: the gradient of the rotation (dq from dq_out).
+ * d = 64, 128 or 256; rot_dim a multiple of 16 in [16, d].
+ * Source: "FlashAttention-3: Hopper Asynchrony and FP8 Attention", section "FP8
+ * accuracy controls" (rotary embedding in front of attention); the rotation of
+ * attn_fp8_quantize_rope for the 16-bit kernels.
+ */
+attn_status_t attn_rope(const void* q, void* q_out, const void* k, void* k_out, const float* rope_cos,
+                        const float* rope_sin, const int* positions, int B, int N, int H, int H_kv,
+                        int d, int rot_dim, int max_pos, const long long* q_strides,
+                        const long long* q_out_strides, const long long* k_strides,
+                        const long long* k_out_strides, int interleaved, int inverse,
+                        attn_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * attn_block_tables -- block table, slot map and offsets of the next step, on the
+ * device, from the requests' lengths.
+ *   block_table : int32 [B, max_pages]; entries of pages that old tokens occupy are
+ *                 read, entries of new pages are written, others left as they are.
+ *   old_lens,
+ *   new_lens    : int32 [B]: tokens in the cache, tokens this step adds (0 allowed).
+ *   free_pages  : int32 [n_free]: free physical pages; new pages take them from the
+ *                 front, requests in order, pages of a request in order.
+ *   seq_lens    : int32 [B] (written) old_lens + new_lens, for the paged decode;
+ *                 must not be old_lens or new_lens.
+ *   cu_seqlens  : int32 [B + 1] (written) offsets of each request's new tokens.
+ *   slots       : int64 [capacity] (written) page * page_size + offset of each new
+ *                 token, requests in order; -1 behind the last one.
+ *   positions   : int32 [capacity] (written) position of each new token in its
+ *                 request; -1 behind the last one.
+ *   used        : int32 [1] (written) free pages taken.
+ * A request whose lengths are negative or exceed max_pages * page_size adds nothing
+ * (its seq_lens is old_lens, or 0 if that is out of range); pages that free_pages
+ * cannot give become -1 in the table, with slots -1; tokens past `capacity` are
+ * left out of slots and positions.  All are reported by attn_get_device_status()
+ * as ATTN_ERR_INVALID_ARG.
+ * page_size a power of two in [8, 65536]; B <= 16384; capacity may be 0.
+ * Source: the block table of attn_decode_paged ("FlashAttention 3 Hardware
+ * Acceleration: ...", section "Memory Fragmentation").
+ */
+attn_status_t attn_block_tables(int* block_table, const int* old_lens, const int* new_lens,
+                                const int* free_pages, int* seq_lens, int* cu_seqlens,
+                                long long* slots, int* positions, int* used, int B, int max_pages,
+                                int n_free, int page_size, int capacity, cudaStream_t stream);
+
+/*
+ * attn_cache_append -- new keys and values into a 16-bit paged cache, with the
+ * rotary embedding of keys and queries on the way.
+ *   k, v     : new tokens' rows, H_kv heads of d values; k_strides, v_strides: HOST
+ *              {token, head} element strides (multiples of 8) or NULL for
+ *              [total, H_kv, d].
+ *   k_cache,
+ *   v_cache  : [num_pages, page_size, H_kv, d] in `dtype`; token t goes to row
+ *              slots[t] (page * page_size + offset), the others stay as they are.
+ *   slots    : DEVICE int64 [total]; -1 = no row (padding); other values outside the
+ *              cache are skipped and reported by attn_get_device_status().  Slots of
+ *              one call differ from one another.
+ *   rope_cos, rope_sin, positions, interleaved : as attn_rope, positions [total]; both
+ *              tables NULL = no rotation (positions unused).
+ *   q, q_out : queries to rotate in the same launch, q with {token, head} q_strides,
+ *              q_out [total, H, d]; H = 0: none.  Needs the tables.  q_out may be q
+ *              when q is contiguous.
+ * d = 64, 128 or 256; page_size a power of two in [8, 65536]; total may be 0.
+ * Source: as attn_decode_paged, whose cache this fills.
+ */
+attn_status_t attn_cache_append(const void* q, void* q_out, const void* k, const void* v, void* k_cache,
+                                void* v_cache, const long long* slots, const float* rope_cos,
+                                const float* rope_sin, const int* positions, int total, int H, int H_kv,
+                                int d, int rot_dim, int max_pos, int num_pages, int page_size,
+                                const long long* q_strides, const long long* k_strides,
+                                const long long* v_strides, int interleaved, attn_dtype_t dtype,
+                                cudaStream_t stream);
+
+/*
+ * attn_cache_append_fp8 -- new keys and values into the e4m3 paged cache of
+ * attn_decode_paged_fp8, one descale per (page, key/value head).
+ *   k, v, q, q_out, strides, interleaved : as attn_cache_append.  Keys are rotated
+ *                 (rope_cos and rope_sin given), then multiplied by M = diag(signs)
+ *                 H_d / sqrt(d) (hadamard_signs given), in float32, then quantised.
+ *   block_table : DEVICE int32 [B, max_pages];  seq_lens : DEVICE int32 [B], the new
+ *                 tokens counted;  cu_seqlens : DEVICE int32 [B + 1]: request b's new
+ *                 tokens are rows [cu_seqlens[b], cu_seqlens[b+1]) at its last
+ *                 positions.  attn_block_tables writes all three.  A page that
+ *                 receives tokens belongs to one request.
+ *   For a page and head with new rows x:  descale' = max(descale, amax|x| / 448), the
+ *   old descale counting as 0 when the page's first token is among the new ones, and 1
+ *   if all is 0;  code = e4m3_rn_satfinite(x / descale').  When the descale grows,
+ *   codes of the page's earlier tokens become e4m3_rn(code * (descale / descale')),
+ *   one more rounding each time.  The rest of a page that starts here is cleared
+ *   to 0; rows behind the new tokens of other pages are left as they are.
+ *   Values are expected finite.
+ * Requests that do not fit (offsets, lengths, pages out of range) are skipped and
+ * reported by attn_get_device_status() as ATTN_ERR_INVALID_ARG; keys at or past
+ * max_pos are stored unrotated and reported.
+ * d = 128; page_size a power of two in [16, 65536]; total = cu_seqlens[B], may be 0.
+ * Source: as attn_decode_paged_fp8, whose cache this fills, with the block scaling
+ * of attn_fp8_quantize.
+ */
+attn_status_t attn_cache_append_fp8(const void* q, void* q_out, const void* k, const void* v,
+                                    uint8_t* k_cache, uint8_t* v_cache, float* k_descale,
+                                    float* v_descale, const int* block_table, const int* seq_lens,
+                                    const int* cu_seqlens, const float* rope_cos,
+                                    const float* rope_sin, const float* hadamard_signs, int B, int total,
+                                    int H, int H_kv, int d, int rot_dim, int max_pos, int num_pages,
+                                    int page_size, int max_pages, const long long* q_strides,
+                                    const long long* k_strides, const long long* v_strides,
+                                    int interleaved, attn_dtype_t dtype, cudaStream_t stream);
+
+/*
  * attn_get_device_status -- synchronises `stream`, then reads and clears the
  * current device's status word.  ATTN_OK, ATTN_ERR_TIMEOUT (a kernel gave up
  * on an internal wait; attn_last_error() names the role), ATTN_ERR_INVALID_ARG
- * (a packed or paged call met offsets, lengths or pages out of range and
+ * (a call met offsets, lengths, pages, slots or positions out of range and
  * skipped them), ATTN_ERR_ARCH, or ATTN_ERR_CUDA.
  * Source: the pages list failure modes ("FlashAttention-3: Hopper Asynchrony
  * and FP8 Attention", section "Where It Breaks") and ask that problems be

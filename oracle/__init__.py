@@ -24,6 +24,8 @@ from .varlen import (attention_forward_gqa, attention_backward_gqa,
                      attention_forward_varlen, attention_backward_varlen)
 from .decode import (attention_decode_paged, attention_decode_paged_fp8,
                      dequantize_paged_cache, quantize_paged_cache)
+from .serving import (append_fp8, attention_cross_backward, attention_cross_forward, block_tables,
+                      key_rows, rope_rotate, rope_table)
 
 __all__ = [
     "attention_forward", "attention_backward", "attention_probs", "attention_forward_rows",
@@ -33,4 +35,6 @@ __all__ = [
     "attention_forward_gqa", "attention_backward_gqa",
     "attention_forward_varlen", "attention_backward_varlen", "attention_decode_paged",
     "attention_decode_paged_fp8", "quantize_paged_cache", "dequantize_paged_cache",
+    "append_fp8", "attention_cross_backward", "attention_cross_forward", "block_tables", "key_rows",
+    "rope_rotate", "rope_table",
 ]

@@ -1,0 +1,159 @@
+"""Host-side refusals of the cross-attention, rotary and cache entry points: every
+bad argument is turned away before anything is launched."""
+import ctypes
+
+import pytest
+
+S3, S2 = ctypes.c_longlong * 3, ctypes.c_longlong * 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from exact_tiled_attention_25_gb300 import build, _lib
+    build.build()
+    return _lib.load()
+
+
+def _cross_fwd(lib, q=16, k=16, v=16, lens=None, o=16, l=16, ws=256, wsb=1 << 40, B=1, H=4, Hkv=2, Nq=300, Nk=200,
+               d=128, scale=0.1, dt=0):
+    return lib.attn_cross_fwd(q, k, v, lens, o, l, ws, wsb, B, H, Hkv, Nq, Nk, d, scale, dt, None)
+
+
+def _cross_bwd(lib, q=16, k=16, v=16, o=16, do=16, l=16, lens=None, dq=16, dk=16, dv=16, ws=256, wsb=1 << 40, B=1, H=4,
+               Hkv=2, Nq=300, Nk=200, d=128, scale=0.1, dt=0):
+    return lib.attn_cross_bwd(q, k, v, o, do, l, lens, dq, dk, dv, ws, wsb, B, H, Hkv, Nq, Nk, d, scale, dt, None)
+
+
+CROSS = [(dict(Nk=0), "N_k"), (dict(Nq=0), "N"), (dict(d=96), "d must"), (dict(Hkv=3), "H_kv"),
+         (dict(scale=0.0), "scale"), (dict(scale=float("nan")), "scale"), (dict(dt=2), "dtype"), (dict(k=0), "null"),
+         (dict(q=8), "aligned"), (dict(lens=2), "kv_lens"), (dict(Nk=1 << 24), "2^31")]
+
+
+@pytest.mark.parametrize("call", [_cross_fwd, _cross_bwd])
+@pytest.mark.parametrize("kwargs,why", CROSS)
+def test_cross_refusals(lib, call, kwargs, why):
+    assert call(lib, **kwargs) == 1
+    assert why in lib.attn_last_error().decode()
+
+
+def test_cross_workspaces(lib):
+    assert lib.attn_cross_workspace_size(1, 3, 2, 1, 10, 64) == 0          # H_kv does not divide H
+    need = lib.attn_cross_workspace_size(1, 4, 2, 1, 8192, 128)
+    assert need > 0
+    few = dict(Nq=1, Nk=8192)
+    assert _cross_fwd(lib, wsb=need - 1, **few) == 1 and b"workspace" in lib.attn_last_error()
+    assert _cross_fwd(lib, ws=None, **few) == 1 and b"workspace" in lib.attn_last_error()
+    assert _cross_fwd(lib, ws=16, **few) == 1 and b"256-byte" in lib.attn_last_error()
+    need = lib.attn_bwd_workspace_size(1, 4, 300, 128)
+    assert _cross_bwd(lib, wsb=need - 1) == 1 and b"workspace" in lib.attn_last_error()
+    assert _cross_bwd(lib, ws=16) == 1 and b"256-byte" in lib.attn_last_error()
+    assert _cross_bwd(lib, d=256) == 2
+    assert _cross_fwd(lib, B=65536, H=1, Hkv=1, Nq=1, Nk=1, d=64) == 2
+
+
+def _rope(lib, q=16, qo=16, k=16, ko=16, c=16, s=16, pos=None, B=1, N=4, H=2, Hkv=1, d=64, rot=64, mp=8, st=None,
+          ot=None, il=0, inv=0, dt=0):
+    return lib.attn_rope(q, qo, k, ko, c, s, pos, B, N, H, Hkv, d, rot, mp, st, ot, None, None, il, inv, dt, None)
+
+
+@pytest.mark.parametrize("kwargs,why", [
+    (dict(rot=24), "rot_dim"), (dict(rot=80), "rot_dim"), (dict(rot=0), "rot_dim"), (dict(mp=0), "max_pos"),
+    (dict(il=2), "interleaved"), (dict(inv=2), "inverse"), (dict(dt=3), "dtype"), (dict(q=0), "null"),
+    (dict(c=0), "null"), (dict(ko=0), "null"), (dict(k=4), "aligned"), (dict(pos=2), "positions"),
+    (dict(N=0), "N"), (dict(d=80), "d must"), (dict(Hkv=-1), "H_kv"),
+    (dict(st=S3(64, 64, 60)), "strides"), (dict(st=S3(64, -64, 64)), "strides"), (dict(ot=S3(64, 64, 0)), "strides"),
+])
+def test_rope_refusals(lib, kwargs, why):
+    assert _rope(lib, **kwargs) == 1
+    assert why in lib.attn_last_error().decode()
+
+
+def _table(lib, c=16, s=16, n=8, rot=64, base=1e4, f=1.0, ol=0, lo=1.0, hi=32.0, af=1.0, first=0):
+    return lib.attn_rope_table(c, s, n, rot, base, f, ol, lo, hi, af, first, None)
+
+
+@pytest.mark.parametrize("kwargs,why", [
+    (dict(n=0), "positions"), (dict(first=-1), "positions"), (dict(first=2 ** 31 - 4, n=8), "positions"),
+    (dict(rot=8), "rot_dim"), (dict(rot=272), "rot_dim"), (dict(base=1.0), "base"), (dict(base=float("inf")), "base"),
+    (dict(f=0.5), "factor"), (dict(f=float("nan")), "factor"), (dict(ol=-1), "orig_len"),
+    (dict(ol=10, lo=2.0, hi=2.0), "low"), (dict(ol=10, lo=-1.0), "low"), (dict(af=0.0), "attn_factor"),
+    (dict(c=0), "null"),
+])
+def test_rope_table_refusals(lib, kwargs, why):
+    assert _table(lib, **kwargs) == 1
+    assert why in lib.attn_last_error().decode()
+
+
+def _tables(lib, bt=16, old=16, new=32, free=16, sl=64, cu=16, slots=16, pos=16, used=16, B=2, mp=4, nf=4, ps=16, cap=8):
+    return lib.attn_block_tables(bt, old, new, free, sl, cu, slots, pos, used, B, mp, nf, ps, cap, None)
+
+
+@pytest.mark.parametrize("kwargs,why", [
+    (dict(ps=24), "page_size"), (dict(ps=4), "page_size"), (dict(B=0), "B"), (dict(nf=-1), "n_free"),
+    (dict(cap=-1), "capacity"), (dict(mp=1 << 28), "max_pages"), (dict(bt=0), "integer"), (dict(free=0), "integer"),
+    (dict(pos=0), "integer"), (dict(slots=4), "slots"), (dict(sl=16), "seq_lens"), (dict(sl=32), "seq_lens"),
+])
+def test_block_table_refusals(lib, kwargs, why):
+    assert _tables(lib, **kwargs) == 1
+    assert why in lib.attn_last_error().decode()
+
+
+def _append(lib, q=16, qo=16, k=16, v=16, kc=16, vc=16, slots=16, c=16, s=16, pos=16, total=4, H=2, Hkv=1, d=64,
+            rot=64, mp=8, pages=4, ps=16, qs=None, ks=None, vs=None, il=0, dt=0):
+    return lib.attn_cache_append(q, qo, k, v, kc, vc, slots, c, s, pos, total, H, Hkv, d, rot, mp, pages, ps, qs, ks,
+                                 vs, il, dt, None)
+
+
+def _append8(lib, q=16, qo=16, k=16, v=16, kc=16, vc=16, kd=16, vd=16, bt=16, sl=16, cu=16, c=16, s=16, sg=16, B=1,
+             total=4, H=2, Hkv=1, d=128, rot=64, mp=8, pages=4, ps=16, maxp=2, qs=None, ks=None, vs=None, il=0, dt=0):
+    return lib.attn_cache_append_fp8(q, qo, k, v, kc, vc, kd, vd, bt, sl, cu, c, s, sg, B, total, H, Hkv, d, rot, mp,
+                                     pages, ps, maxp, qs, ks, vs, il, dt, None)
+
+
+@pytest.mark.parametrize("call", [_append, _append8])
+@pytest.mark.parametrize("kwargs,why", [
+    (dict(ps=12), "page_size"), (dict(total=-1), "total"), (dict(pages=0), "num_pages"), (dict(d=96), "d must"),
+    (dict(rot=40), "rot_dim"), (dict(s=0), "both"), (dict(c=0, s=0), "needs rope_cos"), (dict(k=0), "null"),
+    (dict(kc=8), "aligned"), (dict(qo=0), "null"), (dict(ks=S2(64, 4)), "strides"), (dict(vs=S2(-64, 64)), "strides"),
+    (dict(il=3), "interleaved"), (dict(dt=5), "dtype"), (dict(total=1 << 28), "2^31"),
+])
+def test_append_refusals(lib, call, kwargs, why):
+    assert call(lib, **kwargs) == 1
+    assert why in lib.attn_last_error().decode()
+
+
+def test_append_own_refusals(lib):
+    assert _append(lib, slots=4) == 1 and b"slots" in lib.attn_last_error()
+    assert _append(lib, pos=0) == 1 and b"integer" in lib.attn_last_error()
+    assert _append8(lib, ps=8) == 1 and b"page_size" in lib.attn_last_error()
+    assert _append8(lib, d=64) == 2
+    assert _append8(lib, sg=4) == 1 and b"hadamard" in lib.attn_last_error()
+    assert _append8(lib, kd=0) == 1 and _append8(lib, bt=0) == 1 and _append8(lib, B=0) == 1
+
+
+def test_python_refusals():
+    """Shapes and types that the binding turns away by itself."""
+    import torch
+    import exact_tiled_attention_25_gb300 as attn
+    bf = dict(dtype=torch.bfloat16)
+    c = torch.zeros(8, 32)
+    with pytest.raises(ValueError, match="q's B and d"):
+        attn._cross_shapes(torch.zeros(1, 2, 3, 64, **bf), torch.zeros(2, 2, 3, 64, **bf), torch.zeros(2, 2, 3, 64, **bf))
+    with pytest.raises(ValueError, match="bfloat16"):
+        attn._cross_shapes(*(torch.zeros(1, 2, 3, 64) for _ in range(3)))
+    with pytest.raises(ValueError, match="contiguous"):
+        attn._cross_shapes(torch.zeros(1, 3, 2, 64, **bf).transpose(1, 2), *(torch.zeros(1, 2, 3, 64, **bf),) * 2)
+    with pytest.raises(ValueError, match="kv_lens"):
+        attn._kv_lens(torch.zeros(3), 3)
+    with pytest.raises(ValueError, match="rows"):
+        attn._row_strides(torch.zeros(4, 64, 2).transpose(1, 2), "q")
+    assert attn._row_strides(torch.zeros(512).as_strided((4, 1, 64), (128, 3, 1)), "q") == [128, 64]
+    rows = torch.zeros(4, 6, 64, **bf)
+    with pytest.raises(ValueError, match="caches"):
+        attn._append_rows(rows, rows, None, None, (3, 16, 2, 64))
+    with pytest.raises(ValueError, match="k and v"):
+        attn._append_rows(rows, rows[:, :2], None, None, (3, 16, 6, 64))
+    with pytest.raises(ValueError, match="q_out"):
+        attn._append_rows(rows, rows, None, rows, (3, 16, 6, 64))
+    with pytest.raises(ValueError, match="rope_sin"):
+        attn._rope_tables(c, torch.zeros(8, 16))

@@ -1,0 +1,261 @@
+"""Cross attention parity (forward, backward, single tokens) against the float64
+oracle on the same 16-bit values, element by element.
+
+Tolerances.  u = 2^-8 (bfloat16) or 2^-11 (float16) bounds one rounding.
+ O     = sum_j P~_j v_j / l with each P~ rounded once, then rounded itself:
+         |dO| <= u (sum_j p_j |v_j|) + u |O|.
+ dV    = sum_i P~_i dO_i, rounded:   u sum_i p_i |dO_i| + u |dV|.
+ dS~   = rnd(P~ (dP - D~)):          p |dP - D| 2u + p |dD|, and D~ takes the
+         rounded O:                  |dD_i| <= sum_c |dO_ic| |dO-tolerance_ic|.
+ dQ    = scale sum_j dS~_j k_j, rounded:  scale sum_j |d dS_j| |k_j| + u |dQ|; dK likewise.
+float16 probabilities and dS below 2^-14 are subnormal: each is off by at most
+2^-25 more (the probabilities before the division by l >= 1).  A tenth on top
+covers second-order terms and the float32 arithmetic (exponentials to 2^-21)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import workloads
+from gpu_util import LSE_ABS, check_status, dev, guarded, lib
+
+pytestmark = pytest.mark.gpu
+U = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+SUB = {"bf16": 0.0, "fp16": 2.0 ** -25}
+
+
+@pytest.fixture(scope="module")
+def attn():
+    return lib()
+
+
+def _inputs(seed, B, H, H_kv, N_q, N_k, d, dtype):
+    q, do = workloads.normal(seed, (B, H, N_q, d), 2)
+    k, v = workloads.normal(seed + 1, (B, H_kv, N_k, d), 2)
+    return tuple(workloads.round_to(x, dtype) for x in (q, k, v, do))
+
+
+def _forward_bound(q, k, v, o, scale, lens, dtype):
+    a, _ = oracle.attention_cross_forward(q, k, np.abs(v), scale, lens)
+    return 1.1 * (U[dtype] * (a + np.abs(o)) + SUB[dtype] * k.shape[2] * np.abs(v).max()) + 1e-6
+
+
+def _backward_bounds(q, k, v, do, o, o_tol, grads, scale, lens, dtype):
+    u, sub = U[dtype], SUB[dtype]
+    B, H = q.shape[:2]
+    G = H // k.shape[1]
+    tq, tk, tv = np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape)
+    for b in range(B):
+        n = k.shape[2] if lens is None else int(lens[b])
+        if n == 0:
+            continue
+        for h in range(H):
+            j = h // G
+            p, _, _ = oracle.attention_probs(q[b, h], k[b, j, :n], scale)
+            dp = do[b, h] @ v[b, j, :n].T
+            gap = np.abs(dp - (do[b, h] * o[b, h]).sum(1, keepdims=True))
+            eds = 2 * u * p * gap + p * (np.abs(do[b, h]) * o_tol[b, h]).sum(1, keepdims=True) + sub * (1 + gap)
+            tq[b, h] = scale * eds @ np.abs(k[b, j, :n])
+            tk[b, j, :n] += scale * eds.T @ np.abs(q[b, h])
+            tv[b, j, :n] += (u * p + sub).T @ np.abs(do[b, h])
+    return [1.1 * (t + u * np.abs(g)) + 1e-6 for t, g in zip((tq, tk, tv), grads)]
+
+
+def _within(got, ref, tol, what):
+    x = got.double().cpu().numpy()
+    assert np.all(np.isfinite(x)), what
+    over = np.abs(x - ref) - tol
+    at = np.unravel_index(np.argmax(over), over.shape)
+    assert over[at] <= 0, (what, at, x[at], ref[at], tol[at])
+
+
+def _lse_close(lse, ref):
+    x = lse.double().cpu().numpy()
+    seen = np.isfinite(ref)
+    assert np.array_equal(np.isneginf(x), ~seen)
+    assert np.abs(x[seen] - ref[seen]).max(initial=0.0) <= LSE_ABS
+
+
+def _check(attn, B, H, H_kv, N_q, N_k, d, dtype="bf16", lens=None, seed=900, backward=True, dirty=True):
+    q, k, v, do = _inputs(seed, B, H, H_kv, N_q, N_k, d, dtype)
+    scale = 1 / np.sqrt(d)
+    f = [workloads.as_f64(t) for t in (q, k, v, do)]
+    o_ref, l_ref = oracle.attention_cross_forward(*f[:3], scale, lens)
+    gq, gk, gv, gdo = (t.to(dev()) for t in (q, k, v, do))
+    if lens is not None and dirty:
+        # what stands behind the keys must not matter
+        for b, n in enumerate(lens):
+            gk[b, :, n:], gv[b, :, n:] = float("nan"), float("inf")
+    tl = None if lens is None else torch.tensor(lens, dtype=torch.int32, device=dev())
+    o, co = guarded((B, H, N_q, d), q.dtype, -7.0)
+    lse, cl = guarded((B, H, N_q), torch.float32, -7.0)
+    attn.attn_cross_fwd(gq, gk, gv, tl, softmax_scale=scale, o=o, lse=lse)
+    check_status(attn)
+    co()
+    cl()
+    tol = _forward_bound(*f[:3], o_ref, scale, lens, dtype)
+    _within(o, o_ref, tol, "o")
+    _lse_close(lse, l_ref)
+    if not backward:
+        return
+    grads = oracle.attention_cross_backward(*f, scale, lens)
+    outs = [guarded(t.shape, t.dtype, -7.0) for t in (q, k, v)]
+    attn.attn_cross_bwd(gq, gk, gv, o, gdo, lse, tl, softmax_scale=scale, dq=outs[0][0], dk=outs[1][0], dv=outs[2][0])
+    check_status(attn)
+    tols = _backward_bounds(*f, o_ref, tol, grads, scale, lens, dtype)
+    for (x, check), ref, t, what in zip(outs, grads, tols, ("dq", "dk", "dv")):
+        check()
+        _within(x, ref, t, what)
+    if lens is not None:
+        for b, n in enumerate(lens):
+            assert not outs[1][0][b, :, n:].any() and not outs[2][0][b, :, n:].any()
+
+
+@pytest.mark.parametrize("N_q,N_k", [(1, 1), (1, 129), (7, 128), (128, 1), (129, 127), (257, 300), (300, 64)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_lengths(attn, N_q, N_k, d):
+    _check(attn, 1, 2, 2, N_q, N_k, d)
+
+
+@pytest.mark.parametrize("H,H_kv", [(4, 1), (6, 3), (8, 2)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_grouped_heads(attn, H, H_kv, dtype):
+    _check(attn, 2, H, H_kv, 70, 200, 128, dtype, seed=910)
+    _check(attn, 2, H, H_kv, 3, 333, 64, dtype, seed=911)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N_q", [1, 40, 300])
+def test_key_lengths(attn, d, N_q):
+    """Empty, one key, both sides of a tile's border, all: with NaN and infinities behind."""
+    _check(attn, 8, 2, 1, N_q, 300, d, lens=[0, 1, 127, 128, 129, 256, 299, 300], seed=920)
+
+
+def test_key_lengths_fp16_all_empty(attn):
+    _check(attn, 2, 2, 2, 5, 130, 64, "fp16", lens=[0, 0], seed=930)
+    _check(attn, 2, 2, 2, 200, 130, 128, "fp16", lens=[0, 77], seed=931)
+
+
+@pytest.mark.parametrize("N_q", [1, 200])
+def test_wide_head_forward(attn, N_q):
+    _check(attn, 2, 4, 2, N_q, 333, 256, lens=[333, 100], backward=False, seed=940)
+
+
+def test_split_key_ranges(attn):
+    """One query over many keys: several ranges, some of them behind the keys."""
+    _check(attn, 3, 4, 2, 1, 5000, 128, lens=[5000, 130, 0], backward=False, seed=950)
+    _check(attn, 1, 8, 1, 16, 3333, 64, "fp16", backward=False, seed=951)
+
+
+def test_large_scores(attn):
+    """Scores that grow along the keys by far more than the lazy rescale's 2^8."""
+    q, k, v, do = _inputs(960, 1, 2, 2, 130, 400, 64, "bf16")
+    k = (k.float() * torch.linspace(0.1, 8, 400)[:, None]).to(torch.bfloat16)
+    f = [workloads.as_f64(t) for t in (q, k, v)]
+    ref, l = oracle.attention_cross_forward(*f, 0.5)
+    for rows in (slice(0, 130), slice(0, 1)):
+        o, lse = attn.attn_cross_fwd(q[:, :, rows].contiguous().to(dev()), k.to(dev()), v.to(dev()), softmax_scale=0.5)
+        check_status(attn)
+        _within(o, ref[:, :, rows], _forward_bound(*f, ref, 0.5, None, "bf16")[:, :, rows], "o")
+        _lse_close(lse, l[:, :, rows])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_gradient_by_differences(attn, dtype):
+    """The kernel's gradients along random directions against central differences of
+    sum(O dO) in float64 (step 1e-5: truncation below 1e-6 here); the sum of the
+    elements' bounds bounds the error."""
+    scale, lens = 0.2, [50]
+    q, k, v, do = _inputs(970, 1, 2, 1, 40, 60, 64, dtype)
+    f = [workloads.as_f64(t) for t in (q, k, v, do)]
+    tl = torch.tensor(lens, dtype=torch.int32, device=dev())
+    gq, gk, gv, gdo = (t.to(dev()) for t in (q, k, v, do))
+    o, lse = attn.attn_cross_fwd(gq, gk, gv, tl, softmax_scale=scale)
+    got = attn.attn_cross_bwd(gq, gk, gv, o, gdo, lse, tl, softmax_scale=scale)
+    check_status(attn)
+    o_ref, _ = oracle.attention_cross_forward(*f[:3], scale, lens)
+    tols = _backward_bounds(*f, o_ref, _forward_bound(*f[:3], o_ref, scale, lens, dtype),
+                            oracle.attention_cross_backward(*f, scale, lens), scale, lens, dtype)
+    rng = np.random.default_rng(971)
+    for i in range(3):
+        way = np.where(rng.random(f[i].shape) < 0.5, -1.0, 1.0)
+        ends = []
+        for sign in (1e-5, -1e-5):
+            moved = list(f)
+            moved[i] = f[i] + sign * way
+            ends.append((oracle.attention_cross_forward(*moved[:3], scale, lens)[0] * f[3]).sum())
+        slope = (ends[0] - ends[1]) / 2e-5
+        mine = (got[i].double().cpu().numpy() * way).sum()
+        assert abs(mine - slope) <= tols[i].sum() + 1e-5, (i, mine, slope)
+
+
+def test_bad_lengths_are_reported_and_count_as_empty(attn):
+    q, k, v, do = (t.to(dev()) for t in _inputs(980, 3, 2, 2, 200, 150, 64, "bf16"))
+    for rows in (1, 200):
+        qq, dd = q[:, :, :rows].contiguous(), do[:, :, :rows].contiguous()
+        lens = torch.tensor([-1, 151, 150], dtype=torch.int32, device=dev())
+        o, lse = attn.attn_cross_fwd(qq, k, v, lens)
+        assert attn.attn_get_device_status() == attn.ATTN_ERR_INVALID_ARG
+        assert not o[:2].any() and torch.isneginf(lse[:2]).all() and torch.isfinite(lse[2]).all()
+        dq, dk, dv = attn.attn_cross_bwd(qq, k, v, o, dd, lse, lens)
+        assert attn.attn_get_device_status() == attn.ATTN_ERR_INVALID_ARG
+        assert not dq[:2].any() and not dk[:2].any() and not dv[:2].any() and dk[2].any()
+    assert attn.attn_get_device_status() == 0
+
+
+@pytest.mark.parametrize("N_q", [1, 200])
+def test_graph_replay_stream_and_repeat(attn, N_q):
+    """Two captured graphs with their own workspaces, replayed on two streams with new
+    inputs, give the eager call's bits."""
+    B, H, H_kv, N_k, d = 2, 4, 2, 1500, 64
+    runs = []
+    for i in range(2):
+        q, k, v, _ = (t.to(dev()) for t in _inputs(990 + 2 * i, B, H, H_kv, N_q, N_k, d, "bf16"))
+        lens = torch.tensor([N_k - i, 700], dtype=torch.int32, device=dev())
+        need = attn.attn_cross_workspace_size(B, H, H_kv, N_q, N_k, d)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev()) if need else None
+        o, lse = torch.empty_like(q), torch.empty(B, H, N_q, device=dev())
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            attn.attn_cross_fwd(q, k, v, lens, o=o, lse=lse, workspace=ws)
+        runs.append((graph, stream, q, k, v, lens, o, lse))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, stream, q, *_ in runs:
+            with torch.cuda.stream(stream):
+                q.mul_(-1)
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, q, k, v, lens, o, lse in runs:
+        ref_o, ref_l = attn.attn_cross_fwd(q, k, v, lens)
+        assert torch.equal(o, ref_o) and torch.equal(lse, ref_l)
+    check_status(attn)
+
+
+def test_host_tensors(attn):
+    q, k, v, do = _inputs(995, 1, 2, 1, 20, 30, 64, "bf16")
+    lens = torch.tensor([25], dtype=torch.int32)
+    o, lse = attn.attn_cross_fwd(q, k, v, lens)
+    dq, dk, dv = attn.attn_cross_bwd(q, k, v, o, do, lse, lens)
+    assert all(t.device.type == "cpu" for t in (o, lse, dq, dk, dv))
+    f = [workloads.as_f64(t) for t in (q, k, v)]
+    ref, _ = oracle.attention_cross_forward(*f, 64 ** -0.5, [25])
+    _within(o, ref, _forward_bound(*f, ref, 64 ** -0.5, [25], "bf16"), "o")
+    with pytest.raises(ValueError, match="current CUDA device"):
+        attn.attn_cross_fwd(q.to(dev()), k, v.to(dev()))
+    with pytest.raises(ValueError, match="o must be"):
+        attn.attn_cross_fwd(q.to(dev()), k.to(dev()), v.to(dev()), o=torch.empty(1, 2, 20, 32, device=dev()).bfloat16())
+
+
+def test_self_attention_is_the_same_arithmetic(attn):
+    """N_q = N_k without lengths: the plain forward's bits."""
+    q, k, v, do = (t.to(dev()) for t in _inputs(997, 2, 4, 4, 700, 700, 128, "bf16"))
+    o, lse = attn.attn_cross_fwd(q, k, v)
+    ref = attn.attn_fwd(q, k, v)
+    assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+    dk, dv = attn.attn_cross_bwd(q, k, v, o, do, lse)[1:]
+    check = attn.attn_bwd(q, k, v, o, do, lse)
+    assert torch.equal(dk, check[1]) and torch.equal(dv, check[2])
+    check_status(attn)
