@@ -15,6 +15,7 @@ current stream, and the outputs are copied back to the CPU.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -748,33 +749,40 @@ def attn_fp8_quantize_ex(q, k, v, rope_cos=None, rope_sin=None, hadamard_signs=N
     return tuple(outs), tuple(desc)
 
 
-def _on_gpu(**tensors):
-    """The tensors are used where they are (some are written in place): all on the
-    current CUDA device, 16-byte aligned."""
+# The calls below are short on the GPU, so their host side is kept short too.
+
+def _on_gpu(names: str, *tensors) -> int:
+    """Tensors that are used where they are (some are written in place): all on the
+    current CUDA device, whose index is returned."""
     dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda or t.device.index != dev:
-            raise ValueError(f"{name} must be on the current CUDA device")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            bad = [n for n, x in zip(names.split(), tensors) if x is t][0]
+            raise ValueError(f"{bad} must be on the current CUDA device")
+    return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """Handle of the given stream, or of the device's current one (looked up directly:
+    building the Stream object of torch.cuda.current_stream() takes 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _like(t, name, shape, dtype):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
 
 
 def _kv_lens(lens, B):
-    if lens is not None and (lens.dtype != torch.int32 or tuple(lens.shape) != (B,)
-                             or not lens.is_contiguous()):
+    if lens is not None and (lens.dtype != torch.int32 or lens.shape != (B,) or not lens.is_contiguous()):
         raise ValueError("kv_lens must be contiguous int32 [B]")
 
 
 def _cross_shapes(q, k, v):
     B, H, N_q, d = _shape4(q, "q")
     Bk, H_kv, N_k, dk = _shape4(k, "k")
-    if (Bk, dk) != (B, d) or _shape4(v, "v") != (B, H_kv, N_k, d):
-        raise ValueError("k and v must be [B, H_kv, N_k, d] with q's B and d")
+    if Bk != B or dk != d or v.shape != k.shape or not v.is_contiguous():
+        raise ValueError("k and v must be contiguous [B, H_kv, N_k, d] with q's B and d")
     if q.dtype not in _DTYPES or k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k, v must all be bfloat16 or all float16")
     return B, H, H_kv, N_q, N_k, d
@@ -790,14 +798,12 @@ def attn_cross_fwd(q, k, v, kv_lens=None, softmax_scale: float | None = None, o=
     entry b sees the first kv_lens[b] (int32 [B]; None: all).  Returns O
     [B, H, N_q, d] and LSE float32 [B, H, N_q]; O = 0, LSE = -inf without keys."""
     lib = _lib.load()
-    host = q.device.type == "cpu"
+    host = not q.is_cuda
     if host:
-        ins, _ = _to_device([q, k, v] + ([kv_lens] if kv_lens is not None else []))
-        q, k, v = ins[:3]
-        kv_lens = ins[3] if kv_lens is not None else None
+        (q, k, v, kv_lens), host = _move([q, k, v, kv_lens])
     B, H, H_kv, N_q, N_k, d = _cross_shapes(q, k, v)
     _kv_lens(kv_lens, B)
-    scale = 1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale)
+    dev = _on_gpu("q k v kv_lens o lse workspace", q, k, v, kv_lens, o, lse, workspace)
     if o is None:
         o = torch.empty_like(q)
     else:
@@ -810,10 +816,10 @@ def attn_cross_fwd(q, k, v, kv_lens=None, softmax_scale: float | None = None, o=
         need = lib.attn_cross_workspace_size(B, H, H_kv, N_q, N_k, d)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _on_gpu(q=q, k=k, v=v, kv_lens=kv_lens, o=o, lse=lse, workspace=workspace)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    code = lib.attn_cross_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), _ptr(lse), _ptr(workspace),
-                              nbytes, B, H, H_kv, N_q, N_k, d, scale, _DTYPES[q.dtype], _stream(stream))
+    code = lib.attn_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_lens), o.data_ptr(), lse.data_ptr(),
+                              _ptr(workspace), 0 if workspace is None else workspace.nbytes, B, H, H_kv, N_q, N_k, d,
+                              d ** -0.5 if softmax_scale is None else softmax_scale, _DTYPES[q.dtype],
+                              _raw_stream(stream, dev))
     _check(code, "attn_cross_fwd")
     if host:
         return o.cpu(), lse.cpu()
@@ -825,42 +831,46 @@ def attn_cross_bwd(q, k, v, o, dout, lse, kv_lens=None, softmax_scale: float | N
     """Backward of attn_cross_fwd: returns dQ [B, H, N_q, d], dK, dV [B, H_kv, N_k, d]
     (zero behind kv_lens)."""
     lib = _lib.load()
-    host = q.device.type == "cpu"
+    host = not q.is_cuda
     if host:
-        ins, _ = _to_device([q, k, v, o, dout, lse] + ([kv_lens] if kv_lens is not None else []))
-        q, k, v, o, dout, lse = ins[:6]
-        kv_lens = ins[6] if kv_lens is not None else None
+        (q, k, v, o, dout, lse, kv_lens), host = _move([q, k, v, o, dout, lse, kv_lens])
     B, H, H_kv, N_q, N_k, d = _cross_shapes(q, k, v)
     _like(o, "o", q.shape, q.dtype)
     _like(dout, "dout", q.shape, q.dtype)
     _like(lse, "lse", (B, H, N_q), torch.float32)
     _kv_lens(kv_lens, B)
-    scale = 1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale)
-    out = []
-    for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
-        if t is None:
-            t = torch.empty_like(like)
-        else:
-            _like(t, name, like.shape, like.dtype)
-        out.append(t)
-    dq, dk, dv = out
+    dev = _on_gpu("q k v o dout lse kv_lens dq dk dv workspace",
+                  q, k, v, o, dout, lse, kv_lens, dq, dk, dv, workspace)
+    if dq is None:
+        dq = torch.empty_like(q)
+    else:
+        _like(dq, "dq", q.shape, q.dtype)
+    if dk is None:
+        dk = torch.empty_like(k)
+    else:
+        _like(dk, "dk", k.shape, k.dtype)
+    if dv is None:
+        dv = torch.empty_like(v)
+    else:
+        _like(dv, "dv", v.shape, v.dtype)
     if workspace is None:
-        workspace = torch.empty(lib.attn_bwd_workspace_size(B, H, N_q, d), dtype=torch.uint8,
-                                device=q.device)
-    _on_gpu(q=q, k=k, v=v, o=o, dout=dout, lse=lse, kv_lens=kv_lens, dq=dq, dk=dk, dv=dv,
-            workspace=workspace)
-    code = lib.attn_cross_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(kv_lens),
-                              _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), B, H, H_kv, N_q, N_k, d, scale,
-                              _DTYPES[q.dtype], _stream(stream))
+        workspace = torch.empty(lib.attn_bwd_workspace_size(B, H, N_q, d), dtype=torch.uint8, device=q.device)
+    code = lib.attn_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(),
+                              _ptr(kv_lens), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
+                              workspace.nbytes, B, H, H_kv, N_q, N_k, d,
+                              d ** -0.5 if softmax_scale is None else softmax_scale, _DTYPES[q.dtype],
+                              _raw_stream(stream, dev))
     _check(code, "attn_cross_bwd")
     if host:
         return dq.cpu(), dk.cpu(), dv.cpu()
     return dq, dk, dv
 
 
-_Strides3 = ctypes.c_longlong * 3
-_Strides2 = ctypes.c_longlong * 2
+def _move(tensors):
+    """CPU tensors (None: absent) on the current device, when every one is on the CPU."""
+    moved, host = _to_device([t for t in tensors if t is not None])
+    it = iter(moved)
+    return [None if t is None else next(it) for t in tensors], host
 
 
 def attn_rope_table(n: int, rot_dim: int, base: float = 10000.0, factor: float = 1.0, orig_len: int = 0,
@@ -872,19 +882,25 @@ def attn_rope_table(n: int, rot_dim: int, base: float = 10000.0, factor: float =
     positions (wholly below `low` turns); attn_factor multiplies both tables."""
     lib = _lib.load()
     shape = (int(n), int(rot_dim) // 2)
-    dev = torch.device("cuda", torch.cuda.current_device())
     if min(shape) < 1:
         raise ValueError("n and rot_dim must be positive")
-    rope_cos = torch.empty(shape, dtype=torch.float32, device=dev) if rope_cos is None else rope_cos
-    rope_sin = torch.empty(shape, dtype=torch.float32, device=dev) if rope_sin is None else rope_sin
+    dev = _on_gpu("rope_cos rope_sin", rope_cos, rope_sin)
+    if rope_cos is None:
+        rope_cos = torch.empty(shape, dtype=torch.float32, device=torch.device("cuda", dev))
+    if rope_sin is None:
+        rope_sin = torch.empty(shape, dtype=torch.float32, device=torch.device("cuda", dev))
     _like(rope_cos, "rope_cos", shape, torch.float32)
     _like(rope_sin, "rope_sin", shape, torch.float32)
-    _on_gpu(rope_cos=rope_cos, rope_sin=rope_sin)
-    code = lib.attn_rope_table(_ptr(rope_cos), _ptr(rope_sin), int(n), int(rot_dim), float(base), float(factor),
-                               int(orig_len), float(low), float(high), float(attn_factor), int(first),
-                               _stream(stream))
+    code = lib.attn_rope_table(rope_cos.data_ptr(), rope_sin.data_ptr(), int(n), int(rot_dim), base, factor,
+                               int(orig_len), low, high, attn_factor, int(first), _raw_stream(stream, dev))
     _check(code, "attn_rope_table")
     return rope_cos, rope_sin
+
+
+@functools.lru_cache(maxsize=4096)
+def _strides(*steps):
+    """Host array of element strides (read only)."""
+    return (ctypes.c_longlong * len(steps))(*steps)
 
 
 def _rope_tables(rope_cos, rope_sin):
@@ -899,9 +915,20 @@ def _rope_tables(rope_cos, rope_sin):
 def _row_strides(t, name):
     """Strides of all dimensions but the last; one of extent 1 may have any stride,
     and is given as a row's length."""
-    if t.stride(-1) != 1:
+    *steps, last = t.stride()
+    if last != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    return [x if n > 1 else t.shape[-1] for x, n in zip(t.stride()[:-1], t.shape)]
+    if 1 in t.shape:
+        return [x if n > 1 else t.shape[-1] for x, n in zip(steps, t.shape)]
+    return steps
+
+
+def _rope_strides(t, name, packed):
+    """{batch, head, token} strides, or None for contiguous [B, heads, N, d]."""
+    if not packed and t.is_contiguous():
+        return None
+    step = _row_strides(t, name)
+    return _strides(t.shape[-1], step[1], step[0]) if packed else _strides(*step)
 
 
 def attn_rope(q, k, rope_cos, rope_sin, positions=None, interleaved: bool = False, inverse: bool = False,
@@ -911,48 +938,42 @@ def attn_rope(q, k, rope_cos, rope_sin, positions=None, interleaved: bool = Fals
     index; negative: copied).  The tensors may be strided views with contiguous rows;
     q_out, k_out may be the inputs (in place).  inverse = True is the gradient."""
     lib = _lib.load()
-    host = q.device.type == "cpu"
+    host = not q.is_cuda
     if host:
-        some = [t for t in (q, k, rope_cos, rope_sin, positions) if t is not None]
-        moved = dict(zip(map(id, some), _to_device(some)[0]))
-        q, k, rope_cos, rope_sin, positions = (None if t is None else moved[id(t)]
-                                               for t in (q, k, rope_cos, rope_sin, positions))
+        (q, k, rope_cos, rope_sin, positions), host = _move([q, k, rope_cos, rope_sin, positions])
     max_pos, rot_dim = _rope_tables(rope_cos, rope_sin)
     packed = q.dim() == 3
-    if q.dim() not in (3, 4):
+    if packed:
+        (N, H, d), B = q.shape, 1
+    elif q.dim() == 4:
+        B, H, N, d = q.shape
+    else:
         raise ValueError("q must be [B, H, N, d] or packed [total, H, d]")
     if q.dtype not in _DTYPES:
         raise ValueError("q and k must be bfloat16 or float16")
-    if packed:
-        (N, H, d), B = q.shape, 1
-    else:
-        B, H, N, d = q.shape
-    H_kv = 0
-    if k is not None:
-        H_kv = k.shape[1]
-        if k.dtype != q.dtype or tuple(k.shape) != ((N, H_kv, d) if packed else (B, H_kv, N, d)):
-            raise ValueError("k must match q in dtype and shape, up to its heads")
+    if q.numel() == 0:
+        raise ValueError("q is empty")
+    dev = _on_gpu("q k rope_cos rope_sin positions q_out k_out", q, k, rope_cos, rope_sin, positions, q_out, k_out)
     if positions is not None:
         _like(positions, "positions", (N,) if packed else (B, N), torch.int32)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    strides = []
-    for t, name, like in ((q, "q", q), (q_out, "q_out", q), (k, "k", k), (k_out, "k_out", k)):
-        if like is None:
-            strides.append(None)
-            continue
-        if t.dtype != like.dtype or t.shape != like.shape:
-            raise ValueError(f"{name} must match its input in shape and dtype")
-        step = _row_strides(t, name)
-        strides.append(_Strides3(d, step[1], step[0]) if packed else _Strides3(*step))
-    _on_gpu(q=q, k=k, rope_cos=rope_cos, rope_sin=rope_sin, positions=positions, q_out=q_out, k_out=k_out)
-    if q.numel() == 0:
-        raise ValueError("q is empty")
-    code = lib.attn_rope(_ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), _ptr(rope_cos), _ptr(rope_sin),
-                         _ptr(positions), B, N, H, H_kv, d, rot_dim, max_pos, *strides, int(bool(interleaved)),
-                         int(bool(inverse)), _DTYPES[q.dtype], _stream(stream))
+    elif q_out.dtype != q.dtype or q_out.shape != q.shape:
+        raise ValueError("q_out must match q in shape and dtype")
+    H_kv, ks, kos = 0, None, None
+    if k is not None:
+        H_kv = k.shape[1]
+        if k.dtype != q.dtype or k.shape != ((N, H_kv, d) if packed else (B, H_kv, N, d)):
+            raise ValueError("k must match q in dtype and shape, up to its heads")
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        elif k_out.dtype != k.dtype or k_out.shape != k.shape:
+            raise ValueError("k_out must match k in shape and dtype")
+        ks, kos = _rope_strides(k, "k", packed), _rope_strides(k_out, "k_out", packed)
+    code = lib.attn_rope(q.data_ptr(), q_out.data_ptr(), _ptr(k), _ptr(k_out), rope_cos.data_ptr(), rope_sin.data_ptr(),
+                         _ptr(positions), B, N, H, H_kv, d, rot_dim, max_pos, _rope_strides(q, "q", packed),
+                         _rope_strides(q_out, "q_out", packed), ks, kos, bool(interleaved), bool(inverse),
+                         _DTYPES[q.dtype], _raw_stream(stream, dev))
     _check(code, "attn_rope")
     if host:
         return q_out.cpu(), None if k_out is None else k_out.cpu()
@@ -967,34 +988,33 @@ def attn_block_tables(block_table, old_lens, new_lens, free_pages, page_size: in
     positions int32 [capacity] of the new tokens (-1 behind the last) and used [1],
     the free pages taken."""
     lib = _lib.load()
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
+    if block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("block_table must be [B, max_pages] and free_pages a vector")
     B, max_pages = block_table.shape
-    capacity = int(capacity)
-    if capacity < 0 or free_pages.dim() != 1:
-        raise ValueError("capacity must be >= 0 and free_pages a vector")
+    if capacity < 0:
+        raise ValueError("capacity must be >= 0")
     i32 = torch.int32
-    _like(block_table, "block_table", (B, max_pages), i32)
+    _like(block_table, "block_table", block_table.shape, i32)
     _like(old_lens, "old_lens", (B,), i32)
     _like(new_lens, "new_lens", (B,), i32)
     _like(free_pages, "free_pages", free_pages.shape, i32)
+    dev = _on_gpu("block_table old_lens new_lens free_pages seq_lens cu_seqlens slots positions used",
+                  block_table, old_lens, new_lens, free_pages, seq_lens, cu_seqlens, slots, positions, used)
+    device = block_table.device
     out = []
     for t, name, n, dtype in ((seq_lens, "seq_lens", B, i32), (cu_seqlens, "cu_seqlens", B + 1, i32),
-                              (slots, "slots", capacity, torch.int64),
-                              (positions, "positions", capacity, i32), (used, "used", 1, i32)):
+                              (slots, "slots", capacity, torch.int64), (positions, "positions", capacity, i32),
+                              (used, "used", 1, i32)):
         if t is None:
-            t = torch.empty(n, dtype=dtype, device=block_table.device)
+            t = torch.empty(n, dtype=dtype, device=device)
         else:
             _like(t, name, (n,), dtype)
         out.append(t)
-    seq_lens, cu_seqlens, slots, positions, used = out
-    _on_gpu(block_table=block_table, old_lens=old_lens, new_lens=new_lens, free_pages=free_pages,
-            seq_lens=seq_lens, cu_seqlens=cu_seqlens, slots=slots, positions=positions, used=used)
-    code = lib.attn_block_tables(_ptr(block_table), _ptr(old_lens), _ptr(new_lens), _ptr(free_pages),
-                                 _ptr(seq_lens), _ptr(cu_seqlens), _ptr(slots), _ptr(positions), _ptr(used),
-                                 B, max_pages, free_pages.numel(), int(page_size), capacity, _stream(stream))
+    code = lib.attn_block_tables(block_table.data_ptr(), old_lens.data_ptr(), new_lens.data_ptr(),
+                                 free_pages.data_ptr(), *[t.data_ptr() for t in out], B, max_pages,
+                                 free_pages.shape[0], page_size, capacity, _raw_stream(stream, dev))
     _check(code, "attn_block_tables")
-    return seq_lens, cu_seqlens, slots, positions, used
+    return tuple(out)
 
 
 def _append_rows(k, v, q, q_out, cache_shape):
@@ -1002,22 +1022,21 @@ def _append_rows(k, v, q, q_out, cache_shape):
     if k.dim() != 3 or k.shape != v.shape or k.dtype not in _DTYPES or v.dtype != k.dtype:
         raise ValueError("k and v must be bfloat16 or float16 [total, H_kv, d]")
     total, H_kv, d = k.shape
-    if len(cache_shape) != 4 or tuple(cache_shape[2:]) != (H_kv, d):
+    if len(cache_shape) != 4 or cache_shape[2:] != (H_kv, d):
         raise ValueError("the caches must be [num_pages, page_size, H_kv, d]")
-    strides = [None, _Strides2(*_row_strides(k, "k")), _Strides2(*_row_strides(v, "v"))]
-    H = 0
+    qs, H = None, 0
     if q is not None:
         H = q.shape[1] if q.dim() == 3 else -1
-        if tuple(q.shape) != (total, H, d) or q.dtype != k.dtype:
+        if q.shape != (total, H, d) or q.dtype != k.dtype:
             raise ValueError("q must be [total, H, d] in k's dtype")
-        strides[0] = _Strides2(*_row_strides(q, "q"))
+        qs = _strides(*_row_strides(q, "q"))
         if q_out is None:
             q_out = torch.empty((total, H, d), dtype=q.dtype, device=q.device)
         else:
-            _like(q_out, "q_out", (total, H, d), q.dtype)
+            _like(q_out, "q_out", q.shape, q.dtype)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    return total, H, H_kv, d, strides, q_out
+    return total, H, H_kv, d, (qs, _strides(*_row_strides(k, "k")), _strides(*_row_strides(v, "v"))), q_out
 
 
 def attn_cache_append(k, v, k_cache, v_cache, slots, rope_cos=None, rope_sin=None, positions=None, q=None,
@@ -1027,21 +1046,23 @@ def attn_cache_append(k, v, k_cache, v_cache, slots, rope_cos=None, rope_sin=Non
     rows positions (int32 [total]) when given.  q [total, H, d] is rotated in the same
     launch; returns q_out (None without q).  k, v, q may be strided views."""
     lib = _lib.load()
+    dev = _on_gpu("k v k_cache v_cache slots rope_cos rope_sin positions q q_out",
+                  k, v, k_cache, v_cache, slots, rope_cos, rope_sin, positions, q, q_out)
     total, H, H_kv, d, strides, q_out = _append_rows(k, v, q, q_out, k_cache.shape)
+    num_pages, page_size = k_cache.shape[:2]
     _like(k_cache, "k_cache", k_cache.shape, k.dtype)
     _like(v_cache, "v_cache", k_cache.shape, k.dtype)
     _like(slots, "slots", (total,), torch.int64)
-    max_pos, rot_dim = (0, 0) if rope_cos is None else _rope_tables(rope_cos, rope_sin)
+    max_pos = rot_dim = 0
     if rope_cos is not None:
+        max_pos, rot_dim = _rope_tables(rope_cos, rope_sin)
         if positions is None:
             raise ValueError("rotation needs positions")
         _like(positions, "positions", (total,), torch.int32)
-    _on_gpu(k=k, v=v, k_cache=k_cache, v_cache=v_cache, slots=slots, rope_cos=rope_cos, rope_sin=rope_sin,
-            positions=positions, q=q, q_out=q_out)
-    code = lib.attn_cache_append(_ptr(q), _ptr(q_out), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
-                                 _ptr(slots), _ptr(rope_cos), _ptr(rope_sin), _ptr(positions), total, H, H_kv,
-                                 d, rot_dim, max_pos, k_cache.shape[0], k_cache.shape[1], *strides,
-                                 int(bool(interleaved)), _DTYPES[k.dtype], _stream(stream))
+    code = lib.attn_cache_append(_ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+                                 v_cache.data_ptr(), slots.data_ptr(), _ptr(rope_cos), _ptr(rope_sin),
+                                 _ptr(positions), total, H, H_kv, d, rot_dim, max_pos, num_pages, page_size, *strides,
+                                 bool(interleaved), _DTYPES[k.dtype], _raw_stream(stream, dev))
     _check(code, "attn_cache_append")
     return q_out
 
@@ -1056,6 +1077,8 @@ def attn_cache_append_fp8(k, v, k_cache, v_cache, k_descale, v_descale, block_ta
     and transformed when tables and signs are given; q is rotated as in
     attn_cache_append.  Returns q_out (None without q)."""
     lib = _lib.load()
+    dev = _on_gpu("k v k_cache v_cache k_descale v_descale block_table seq_lens cu_seqlens rope_cos rope_sin hadamard_signs q q_out",
+                  k, v, k_cache, v_cache, k_descale, v_descale, block_table, seq_lens, cu_seqlens, rope_cos, rope_sin, hadamard_signs, q, q_out)
     total, H, H_kv, d, strides, q_out = _append_rows(k, v, q, q_out, k_cache.shape)
     num_pages, page_size = k_cache.shape[:2]
     _like(k_cache, "k_cache", k_cache.shape, torch.uint8)
@@ -1065,19 +1088,17 @@ def attn_cache_append_fp8(k, v, k_cache, v_cache, k_descale, v_descale, block_ta
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
     B, max_pages = block_table.shape
-    _like(block_table, "block_table", (B, max_pages), torch.int32)
+    _like(block_table, "block_table", block_table.shape, torch.int32)
     _like(seq_lens, "seq_lens", (B,), torch.int32)
     _like(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32)
     if hadamard_signs is not None:
         _like(hadamard_signs, "hadamard_signs", (d,), torch.float32)
     max_pos, rot_dim = (0, 0) if rope_cos is None else _rope_tables(rope_cos, rope_sin)
-    _on_gpu(k=k, v=v, k_cache=k_cache, v_cache=v_cache, k_descale=k_descale, v_descale=v_descale,
-            block_table=block_table, seq_lens=seq_lens, cu_seqlens=cu_seqlens, rope_cos=rope_cos,
-            rope_sin=rope_sin, hadamard_signs=hadamard_signs, q=q, q_out=q_out)
-    code = lib.attn_cache_append_fp8(_ptr(q), _ptr(q_out), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
-                                     _ptr(k_descale), _ptr(v_descale), _ptr(block_table), _ptr(seq_lens),
-                                     _ptr(cu_seqlens), _ptr(rope_cos), _ptr(rope_sin), _ptr(hadamard_signs),
-                                     B, total, H, H_kv, d, rot_dim, max_pos, num_pages, page_size, max_pages,
-                                     *strides, int(bool(interleaved)), _DTYPES[k.dtype], _stream(stream))
+    code = lib.attn_cache_append_fp8(_ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+                                     v_cache.data_ptr(), k_descale.data_ptr(), v_descale.data_ptr(),
+                                     block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(),
+                                     _ptr(rope_cos), _ptr(rope_sin), _ptr(hadamard_signs), B, total, H, H_kv, d,
+                                     rot_dim, max_pos, num_pages, page_size, max_pages, *strides, bool(interleaved),
+                                     _DTYPES[k.dtype], _raw_stream(stream, dev))
     _check(code, "attn_cache_append_fp8")
     return q_out

@@ -142,93 +142,252 @@ __global__ void __launch_bounds__(kTabThreads)
 }
 
 // ========================================================== e4m3 append ====
-// One block per (page that receives tokens, key/value head, keys or values).
-// The page's new rows are rotated and transformed (keys), their amax gives
+// For every page that receives tokens and every plane of it (a key/value head,
+// keys or values), the page's new rows are rotated and transformed (keys); their
+// amax gives
 //   descale' = max(descale, amax / 448)       (a page whose first token is among
 //                                              the new ones starts from 0),
 // codes = e4m3_rn_satfinite(x / descale'); when the descale grows, the codes of
 // the page's older tokens become e4m3_rn(code * (descale / descale')); the
 // unused rest of a page that starts here is cleared, so the decode never meets
-// another request's codes or a NaN there.  A page belongs to one block per head,
-// so there are no atomics and the result does not depend on any order.
-// A warp holds a row as 32 lanes x 4 values, as the FP8 pre-pass does.
-constexpr int kF8MaxThreads = 256;
-constexpr int kF8Rows = 8;         // rows a warp keeps in registers between the two passes
-
-// Request whose pages include unit u: request b's units start at
-// cu[b] / page_size + 2 b, which leaves it at least as many as the pages that
-// its cu[b + 1] - cu[b] tokens can touch.  A 32-way search, in every warp.
-__device__ __forceinline__ int unit_owner(const int* cu, int B, int page_shift, long long u, int lane) {
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int at = lo + lane * step;
-    const bool below = at < hi && (static_cast<long long>(cu[at]) >> page_shift) + 2ll * at <= u;
-    const uint32_t m = __ballot_sync(0xffffffffu, below || lane == 0);
-    lo += (31 - __clz(m)) * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
+// another request's codes or a NaN there.  One owner per page and plane: no
+// atomics, and no order on which the result could depend.
+//
+// Eight lanes hold a row: lane u the columns 8u .. 8u + 7 and 64 + 8u .. 64 + 8u +
+// 7 (two 16-byte loads), so a full-width rotation pairs values of one lane and
+// only three of the transform's seven stages cross lanes (12 shuffles a row; a
+// warp per row takes 24).  Stages run in the pre-pass's order: same bits.
+constexpr int kF8Threads = 256;    // of the few-rows variant
+constexpr int kF8MaxThreads = 512;
 
 template <bool FP16>
-__device__ __forceinline__ float4 widen4(uint2 w) {
-  if (FP16) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-    return make_float4(a.x, a.y, b.x, b.y);
+__device__ __forceinline__ void widen16(const uint4& a, const uint4& b, float (&x)[16]) {
+  float lo[8], hi[8];
+  unpack16<FP16>(a, lo);
+  unpack16<FP16>(b, hi);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = lo[i];
+    x[8 + i] = hi[i];
   }
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
 }
 
-// Row of keys in the lanes of a warp: rotated by the table row of `pos`, then
-// transformed by M = diag(signs) H_128 / sqrt(128).
+// Eight table values from column i of a row's table entries.
+__device__ __forceinline__ void load8(const float* t, size_t at, float (&x)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(t + at));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(t + at) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+// A key row held by eight lanes: rotated by the tables' row `pos`, then
+// transformed by M = diag(signs) H_128 / sqrt(128); `flip`: bit i set where the
+// sign of the lane's value i is -1.  Every lane of the warp takes part.
 template <bool INTERLEAVED>
-__device__ __forceinline__ float4 key_row(float4 v, const AppendFp8Params& p, int pos, int lane,
-                                          const float4& s4) {
+__device__ __forceinline__ void key_row(float (&x)[16], const AppendFp8Params& p, int pos, int u,
+                                        uint32_t flip) {
   if (p.cos) {
-    const bool turn = 4 * lane < p.rot && pos < p.max_pos;
-    const size_t row = static_cast<size_t>(turn ? pos : 0) * (p.rot / 2);
+    const bool inside = pos < p.max_pos;
+    const size_t row = static_cast<size_t>(inside ? pos : 0) * (p.rot / 2);
     if (INTERLEAVED) {
-      if (turn) {
-        const float2 c = __ldg(reinterpret_cast<const float2*>(p.cos + row) + lane);
-        const float2 s = __ldg(reinterpret_cast<const float2*>(p.sin + row) + lane);
-        v = make_float4(fmaf(-v.y, s.x, v.x * c.x), fmaf(v.x, s.x, v.y * c.x),
-                        fmaf(-v.w, s.y, v.z * c.y), fmaf(v.z, s.y, v.w * c.y));
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int col = 64 * w + 8 * u;
+        if (!inside || col >= p.rot) continue;
+        const float4 c = __ldg(reinterpret_cast<const float4*>(p.cos + row + col / 2));
+        const float4 s = __ldg(reinterpret_cast<const float4*>(p.sin + row + col / 2));
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a = x[8 * w + 2 * e], b = x[8 * w + 2 * e + 1];
+          x[8 * w + 2 * e] = fmaf(-b, ss[e], a * cc[e]);
+          x[8 * w + 2 * e + 1] = fmaf(a, ss[e], b * cc[e]);
+        }
+      }
+    } else if (p.rot == 128) {
+      // the pair of column c < 64 is column c + 64: both in this lane
+      if (inside) {
+        float c[8], s[8];
+        load8(p.cos, row + 8 * u, c);
+        load8(p.sin, row + 8 * u, s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float a = x[e], b = x[8 + e];
+          x[e] = fmaf(-b, s[e], a * c[e]);
+          x[8 + e] = fmaf(a, s[e], b * c[e]);
+        }
       }
     } else {
-      const int half = p.rot / 8;                    // lanes of one half
-      const bool lower = lane < half;
-      const int other = turn ? (lower ? lane + half : lane - half) : lane;
-      const float ox = __shfl_sync(0xffffffffu, v.x, other);
-      const float oy = __shfl_sync(0xffffffffu, v.y, other);
-      const float oz = __shfl_sync(0xffffffffu, v.z, other);
-      const float ow = __shfl_sync(0xffffffffu, v.w, other);
-      if (turn) {
-        const int i = lower ? lane : lane - half;
-        const float4 c = __ldg(reinterpret_cast<const float4*>(p.cos + row) + i);
-        const float4 s = __ldg(reinterpret_cast<const float4*>(p.sin + row) + i);
-        const float sg = lower ? -1.f : 1.f;         // x c - y s, and y c + x s
-        v = make_float4(fmaf(sg * ox, s.x, v.x * c.x), fmaf(sg * oy, s.y, v.y * c.y),
-                        fmaf(sg * oz, s.z, v.z * c.z), fmaf(sg * ow, s.w, v.w * c.w));
+      // vector j (columns 8j .. 8j + 7) pairs with vector j +- rot / 16
+      const int nv = p.rot / 16;
+      float other[16];
+      bool turn[2], lower[2];
+      int at[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int j = u + 8 * w;
+        turn[w] = j < 2 * nv;
+        lower[w] = j < nv;
+        at[w] = lower[w] ? j : j - nv;               // vector of the table row
+        const int pj = turn[w] ? (lower[w] ? j + nv : j - nv) : j;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float a = __shfl_sync(0xffffffffu, x[e], pj & 7, 8);
+          const float b = __shfl_sync(0xffffffffu, x[8 + e], pj & 7, 8);
+          other[8 * w + e] = pj < 8 ? a : b;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (!turn[w] || !inside) continue;
+        float c[8], s[8];
+        load8(p.cos, row + 8 * at[w], c);
+        load8(p.sin, row + 8 * at[w], s);
+        const float sg = lower[w] ? -1.f : 1.f;      // x c - y s, and y c + x s
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[8 * w + e] = fmaf(sg * other[8 * w + e], s[e], x[8 * w + e] * c[e]);
       }
     }
   }
   if (p.signs) {
-    uint64_t p01 = fmul2(pack2(v.x, v.y), pack2(s4.x, s4.y));
-    uint64_t p23 = fmul2(pack2(v.z, v.w), pack2(s4.z, s4.w));
-    wht128_row(p01, p23, lane);
+    uint64_t y[8];                                   // pairs of neighbouring columns
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = __uint_as_float(__float_as_uint(x[2 * i]) ^ ((flip >> (2 * i) & 1u) << 31));
+      const float b = __uint_as_float(__float_as_uint(x[2 * i + 1]) ^ ((flip >> (2 * i + 1) & 1u) << 31));
+      y[i] = pack2(a + b, a - b);                    // span 1
+    }
+    const uint64_t neg = pack2(-1.f, -1.f);
+    auto in_lane = [&](int i, int j) {
+      const uint64_t a = y[i], b = y[j];
+      y[i] = fadd2(a, b);
+      y[j] = ffma2(neg, b, a);
+    };
+    in_lane(0, 1), in_lane(2, 3), in_lane(4, 5), in_lane(6, 7);   // span 2
+    in_lane(0, 2), in_lane(1, 3), in_lane(4, 6), in_lane(5, 7);   // span 4
+#pragma unroll
+    for (int m = 1; m < 8; m <<= 1) {                // spans 8, 16, 32: across lanes
+      const float sg = (u & m) ? -1.f : 1.f;
+      const uint64_t sg2 = pack2(sg, sg);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        y[i] = ffma2(sg2, y[i], pack2(__shfl_xor_sync(0xffffffffu, lo2(y[i]), m),
+                                      __shfl_xor_sync(0xffffffffu, hi2(y[i]), m)));
+    }
     const uint64_t isd2 = pack2(0.08838834764831845f, 0.08838834764831845f);   // 1 / sqrt(128)
-    p01 = fmul2(p01, isd2);
-    p23 = fmul2(p23, isd2);
-    v = make_float4(lo2(p01), hi2(p01), lo2(p23), hi2(p23));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) in_lane(i, i + 4);   // span 64
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y[i] = fmul2(y[i], isd2);
+      x[2 * i] = lo2(y[i]);
+      x[2 * i + 1] = hi2(y[i]);
+    }
   }
-  return v;
 }
 
-__device__ __forceinline__ float amax4(float m, const float4& v) {
-  return fmax3(m, fmax3(fabsf(v.x), fabsf(v.y), fabsf(v.z)), fabsf(v.w));
+// One page and plane: where its new rows come from and its codes go.
+struct AppendSite {
+  bool ok;                // it receives rows
+  bool is_v;
+  int page0;              // position of the page's first row
+  int first, end;         // page rows [first, end) are new
+  const uint16_t* src;    // row x of the page: src + x * st, this lane's columns
+  long long st;
+  uint8_t* dst;           // row x: dst + x * dstep, this lane's columns
+  size_t dstep;
+  float* descale;
+  float before;
+};
+
+// Request b's pages are units cu[b] / page_size + 2 b and on: at least as many units
+// as its cu[b + 1] - cu[b] tokens can touch pages.  The owner of a unit is found by
+// an eight-way search in every group of eight lanes.
+__device__ __forceinline__ AppendSite append_site(const AppendFp8Params& p, long long unit, int hv,
+                                                  int page_shift, int u) {
+  constexpr int D = 128;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = p.B;
+  while (__any_sync(0xffffffffu, hi - lo > 1)) {
+    const int step = (hi - lo + 7) / 8;
+    const int at = lo + u * step;
+    const bool below = u == 0 || (at < hi && (static_cast<long long>(p.cu_seqlens[at]) >> page_shift) + 2ll * at <= unit);
+    const uint32_t m = __ballot_sync(0xffffffffu, below) >> (lane & 24) & 0xffu;
+    if (hi - lo > 1) {
+      lo += (31 - __clz(m)) * step;
+      hi = min(hi, lo + step);
+    }
+  }
+  AppendSite s;
+  s.ok = false;
+  s.is_v = hv >= p.H_kv;
+  s.first = s.end = 0;
+  const int b = lo;
+  const int c0 = p.cu_seqlens[b], c1 = p.cu_seqlens[b + 1];
+  const int len = p.seq_lens[b];
+  const int add = c1 - c0;
+  const bool bad = c0 < 0 || c1 < c0 || c1 > p.total || len < add ||
+                   len > static_cast<long long>(p.max_pages) * p.page_size;
+  if (bad) {
+    if (u == 0) atomicCAS(p.status, 0, kDevBadTables);
+    return s;
+  }
+  const int start = len - add;                       // first new position
+  const long long lp = (start >> page_shift) + (unit - ((static_cast<long long>(c0) >> page_shift) + 2ll * b));
+  if (add == 0 || lp < 0 || (lp << page_shift) >= len) return s;
+  const int phys = p.block_table[static_cast<size_t>(b) * p.max_pages + lp];
+  if (phys < 0 || phys >= p.num_pages) {
+    if (u == 0) atomicCAS(p.status, 0, kDevBadTables);
+    return s;
+  }
+  const int h = s.is_v ? hv - p.H_kv : hv;
+  s.ok = true;
+  s.page0 = static_cast<int>(lp << page_shift);
+  s.first = max(start, s.page0) - s.page0;
+  s.end = min(len - s.page0, p.page_size);
+  s.st = s.is_v ? p.vt : p.kt;
+  // row x of the page is token c0 + (page0 + x - start)
+  s.src = static_cast<const uint16_t*>(s.is_v ? p.v : p.k) + (s.is_v ? p.vh : p.kh) * h +
+          s.st * (c0 + (s.page0 - start)) + 8 * u;
+  s.dst = (s.is_v ? p.v_cache : p.k_cache) +
+          (static_cast<size_t>(phys) * p.page_size * p.H_kv + h) * D + 8 * u;
+  s.dstep = static_cast<size_t>(p.H_kv) * D;
+  s.descale = (s.is_v ? p.v_descale : p.k_descale) + static_cast<size_t>(phys) * p.H_kv + h;
+  s.before = s.first == 0 ? 0.f : *s.descale;
+  if (p.cos && !s.is_v && u == 0 && s.page0 + s.end > p.max_pos) atomicCAS(p.status, 0, kDevBadTables);
+  return s;
+}
+
+struct Raw16 {
+  uint4 a, b;
+};
+__device__ __forceinline__ Raw16 load_row(const AppendSite& s, int x) {
+  const uint4* at = reinterpret_cast<const uint4*>(s.src + s.st * x);
+  return {__ldg(at), __ldg(at + 8)};
+}
+
+__device__ __forceinline__ float amax16(const float (&x)[16]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) m = fmax3(m, fabsf(x[i]), fabsf(x[i + 1]));
+  return m;
+}
+
+__device__ __forceinline__ float new_descale(float before, float amax) {
+  const float after = fmaxf(before, __fdiv_rn(amax, 448.f));
+  return after == 0.f ? 1.f : after;
+}
+
+// Codes of a row, with the quotients rounded as divisions by `after`.
+__device__ __forceinline__ void store_row(const AppendSite& s, int x, const float (&v)[16], uint64_t y2,
+                                          uint64_t nb2) {
+  uint2* at = reinterpret_cast<uint2*>(s.dst + s.dstep * x);
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+    at[8 * w] = make_uint2(
+        quantise4(pack2(v[8 * w], v[8 * w + 1]), pack2(v[8 * w + 2], v[8 * w + 3]), y2, nb2),
+        quantise4(pack2(v[8 * w + 4], v[8 * w + 5]), pack2(v[8 * w + 6], v[8 * w + 7]), y2, nb2));
 }
 
 // Two e4m3 codes as exact float32 values.
@@ -238,128 +397,210 @@ __device__ __forceinline__ float2 widen_e4m3x2(uint32_t codes) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
   return __half22float2(*reinterpret_cast<const __half2*>(&h2));
 }
+__device__ __forceinline__ uint32_t scale_codes(uint32_t w, float ratio) {
+  const float2 a = widen_e4m3x2(w & 0xffffu), c = widen_e4m3x2(w >> 16);
+  return cvt_pack_e4m3x4(a.x * ratio, a.y * ratio, c.x * ratio, c.y * ratio);
+}
 
-template <bool FP16, bool INTERLEAVED>
-__device__ __forceinline__ void append_fp8_block(const AppendFp8Params& p, long long unit, int hv,
-                                                 int page_shift) {
-  constexpr int D = 128;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int warps = blockDim.x >> 5;
-  __shared__ float warp_max[kF8MaxThreads / 32];
-  const int b = unit_owner(p.cu_seqlens, p.B, page_shift, unit, lane);
-  const int c0 = p.cu_seqlens[b], c1 = p.cu_seqlens[b + 1];
-  const int len = p.seq_lens[b];
-  const int add = c1 - c0;
-  if (c0 < 0 || c1 < c0 || c1 > p.total || len < add ||
-      len > static_cast<long long>(p.max_pages) * p.page_size) {
-    if (threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadTables);
-    return;
-  }
-  const int start = len - add;                       // first new position
-  const long long lp = (start >> page_shift) + (unit - ((static_cast<long long>(c0) >> page_shift) + 2ll * b));
-  if (add == 0 || lp < 0 || lp << page_shift >= len) return;
-  const int phys = p.block_table[static_cast<size_t>(b) * p.max_pages + lp];
-  if (phys < 0 || phys >= p.num_pages) {
-    if (threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadTables);
-    return;
-  }
-  const int page0 = static_cast<int>(lp << page_shift);
-  const int first = max(start, page0) - page0;       // page rows [first, end) are new
-  const int end = min(len - page0, p.page_size);
-  const bool is_v = hv >= p.H_kv;
-  const int h = is_v ? hv - p.H_kv : hv;
-  const uint16_t* src = static_cast<const uint16_t*>(is_v ? p.v : p.k);
-  const long long st = is_v ? p.vt : p.kt;
-  // row x of the page is token c0 + (page0 + x - start)
-  src += (is_v ? p.vh : p.kh) * h + st * (c0 + (page0 - start));
-  uint8_t* dst = (is_v ? p.v_cache : p.k_cache) + (static_cast<size_t>(phys) * p.page_size * p.H_kv + h) * D;
-  const size_t dstep = static_cast<size_t>(p.H_kv) * D;
-  float* descale = (is_v ? p.v_descale : p.k_descale) + static_cast<size_t>(phys) * p.H_kv + h;
-  const float before = first == 0 ? 0.f : *descale;
-  float4 s4 = make_float4(1.f, 1.f, 1.f, 1.f);
-  if (p.signs && !is_v) s4 = __ldg(reinterpret_cast<const float4*>(p.signs) + lane);
-  if (p.cos && !is_v && threadIdx.x == 0 && page0 + end > p.max_pos) atomicCAS(p.status, 0, kDevBadTables);
-
-  auto load = [&](int x) {
-    return __ldg(reinterpret_cast<const uint2*>(src + st * x) + lane);
-  };
-  auto finish = [&](uint2 w, int x) {
-    const float4 v = widen4<FP16>(w);
-    return is_v ? v : key_row<INTERLEAVED>(v, p, page0 + x, lane, s4);
-  };
-  // pass 1: the rows' amax; a warp's first kF8Rows rows stay in registers
-  float4 kept[kF8Rows];
-  uint2 raw[kF8Rows];
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < kF8Rows; ++i) {
-    const int x = first + warp + i * warps;
-    raw[i] = x < end ? load(x) : make_uint2(0u, 0u);
-  }
-#pragma unroll
-  for (int i = 0; i < kF8Rows; ++i) {
-    const int x = first + warp + i * warps;
-    if (x < end) {                                   // the same for the whole warp
-      kept[i] = finish(raw[i], x);
-      amax = amax4(amax, kept[i]);
+// The page's other rows, row x = from, from + by, ...: cleared behind the new ones of
+// a page that starts here, requantised before them when the descale grew.
+__device__ __forceinline__ void other_rows(const AppendSite& s, float after, int page_size, int from, int by) {
+  if (s.first == 0) {
+    for (int x = s.end + from; x < page_size; x += by) {
+      uint2* at = reinterpret_cast<uint2*>(s.dst + s.dstep * x);
+      at[0] = at[8] = make_uint2(0u, 0u);
     }
-  }
-  for (int x = first + warp + kF8Rows * warps; x < end; x += warps) amax = amax4(amax, finish(load(x), x));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (lane == 0) warp_max[warp] = amax;
-  __syncthreads();                                   // also: every thread has read the old descale
-  for (int w = 0; w < warps; ++w) amax = fmaxf(amax, warp_max[w]);
-  float after = fmaxf(before, __fdiv_rn(amax, 448.f));
-  if (after == 0.f) after = 1.f;
-  if (threadIdx.x == 0) *descale = after;
-  const float rcp = __fdiv_rn(1.f, after);
-  const uint64_t y2 = pack2(rcp, rcp), nb2 = pack2(-after, -after);
-  // pass 2: codes
-  auto store = [&](const float4& v, int x) {
-    reinterpret_cast<uint32_t*>(dst + dstep * x)[lane] =
-        quantise4(pack2(v.x, v.y), pack2(v.z, v.w), y2, nb2);
-  };
-#pragma unroll
-  for (int i = 0; i < kF8Rows; ++i) {
-    const int x = first + warp + i * warps;
-    if (x < end) store(kept[i], x);
-  }
-  for (int x = first + warp + kF8Rows * warps; x < end; x += warps) store(finish(load(x), x), x);
-  if (first == 0) {
-    for (int x = end + warp; x < p.page_size; x += warps)
-      reinterpret_cast<uint32_t*>(dst + dstep * x)[lane] = 0u;
-  } else if (after > before) {
-    const float ratio = __fdiv_rn(before, after);
+  } else if (after > s.before) {
+    const float ratio = __fdiv_rn(s.before, after);
 #pragma unroll 4
-    for (int x = warp; x < first; x += warps) {
-      uint32_t* at = reinterpret_cast<uint32_t*>(dst + dstep * x) + lane;
-      const uint32_t w = *at;
-      const float2 a = widen_e4m3x2(w & 0xffffu), c = widen_e4m3x2(w >> 16);
-      *at = cvt_pack_e4m3x4(a.x * ratio, a.y * ratio, c.x * ratio, c.y * ratio);
+    for (int x = from; x < s.first; x += by) {
+      uint2* at = reinterpret_cast<uint2*>(s.dst + s.dstep * x);
+      const uint2 a = at[0], b = at[8];
+      at[0] = make_uint2(scale_codes(a.x, ratio), scale_codes(a.y, ratio));
+      at[8] = make_uint2(scale_codes(b.x, ratio), scale_codes(b.y, ratio));
     }
   }
 }
 
-// Blocks [0, units * 2 H_kv): pages; the rest rotate query rows.
+// Bits of the lane's sixteen negative signs.
+__device__ __forceinline__ uint32_t sign_bits(const AppendFp8Params& p, int u) {
+  uint32_t flip = 0;
+  if (p.signs) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (__ldg(p.signs + (i < 8 ? 8 * u + i : 64 + 8 * u + i - 8)) < 0.f) flip |= 1u << i;
+  }
+  return flip;
+}
+
+// 16 bytes to shared memory without passing registers, zeros if !valid (the source
+// must be a readable address all the same); seen by this thread after the wait.
+__device__ __forceinline__ void copy16_async(void* smem_dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// Many rows per page: one block per page and plane, blockDim / 8 rows at a time.
+// SWEEPS = 4: each thread copies the raw values of its first 4 rows into its own
+// slots of shared memory, all at once, and reads them back for the amax pass and
+// again for the code pass; the transform runs twice, which costs less than holding
+// float32 rows would in occupancy (registers for 4 raw rows spilled).  Rows of
+// larger pages are read again, from L2.  SWEEPS = 1: a page is one row per
+// thread, whose values stay in registers.
+template <bool FP16, bool INTERLEAVED, int SWEEPS>
+__global__ void __launch_bounds__(kF8MaxThreads, 2)
+    append_fp8_pages_kernel(const AppendFp8Params p, int page_shift) {
+  extern __shared__ uint4 raw_sh[];                  // [SWEEPS][2][blockDim], SWEEPS > 1
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int u = lane & 7;
+  const int by = blockDim.x >> 3, mine = threadIdx.x >> 3;
+  __shared__ float warp_max[kF8MaxThreads / 32];
+  const AppendSite s = append_site(p, blockIdx.x / (2 * p.H_kv), blockIdx.x % (2 * p.H_kv), page_shift, u);
+  if (!s.ok) return;                                 // the same for the whole block
+  if constexpr (SWEEPS > 1) {
+#pragma unroll
+    for (int i = 0; i < SWEEPS; ++i) {
+      const int x = s.first + mine + i * by;
+      const bool valid = x < s.end;
+      const uint4* at = reinterpret_cast<const uint4*>(s.src + s.st * (valid ? x : s.first));
+      copy16_async(raw_sh + (2 * i) * blockDim.x + threadIdx.x, at, valid);
+      copy16_async(raw_sh + (2 * i + 1) * blockDim.x + threadIdx.x, at + 8, valid);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  }
+  const uint32_t flip = s.is_v ? 0u : sign_bits(p, u);
+  float v[16];
+  // row s.first + mine + i * by into v; lanes past the new rows go along with zeros
+  // (the transform's shuffles are warp-wide)
+  auto finish = [&](int i, bool staged) {
+    const int x = s.first + mine + i * by;
+    Raw16 r{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    if (staged) r = {raw_sh[(2 * i) * blockDim.x + threadIdx.x], raw_sh[(2 * i + 1) * blockDim.x + threadIdx.x]};
+    else if (x < s.end) r = load_row(s, x);
+    widen16<FP16>(r.a, r.b, v);
+    if (!s.is_v) key_row<INTERLEAVED>(v, p, s.page0 + x, u, flip);
+  };
+  const int warp_first = s.first + (warp << 2);      // first row of the warp's first sweep
+  const int sweeps = warp_first < s.end ? (s.end - warp_first + by - 1) / by : 0;   // of this warp
+  float amax = 0.f;
+  int i = 0;
+  if constexpr (SWEEPS > 1) {
+    auto staged_max = [&](int at) {
+      finish(at, true);
+      amax = fmaxf(amax, amax16(v));
+    };
+    copies_wait<3>();
+    if (sweeps > 0) staged_max(0);
+    copies_wait<2>();
+    if (sweeps > 1) staged_max(1);
+    copies_wait<1>();
+    if (sweeps > 2) staged_max(2);
+    copies_wait<0>();
+    if (sweeps > 3) staged_max(3);
+    i = SWEEPS;
+  }
+  for (; i < sweeps; ++i) {
+    finish(i, false);
+    amax = fmaxf(amax, amax16(v));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (lane == 0) warp_max[warp] = amax;
+  __syncthreads();                                   // also: every thread has read the old descale
+  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) amax = fmaxf(amax, warp_max[w]);
+  const float after = new_descale(s.before, amax);
+  if (threadIdx.x == 0) *s.descale = after;
+  const float rcp = __fdiv_rn(1.f, after);
+  const uint64_t y2 = pack2(rcp, rcp), nb2 = pack2(-after, -after);
+  for (i = 0; i < sweeps; ++i) {
+    if (SWEEPS > 1 || sweeps > 1) finish(i, SWEEPS > 1 && i < SWEEPS);   // else still in v
+    const int x = s.first + mine + i * by;
+    if (x < s.end) store_row(s, x, v, y2, nb2);
+  }
+  other_rows(s, after, p.page_size, mine, by);
+}
+
+// Few rows per page (a decode step): eight lanes per page and plane, so the planes
+// of a page share a block and its lookups; blocks behind them rotate query rows.
 template <bool FP16, bool INTERLEAVED>
-__global__ void __launch_bounds__(kF8MaxThreads)
-    append_fp8_kernel(const AppendFp8Params p, int page_shift, long long page_blocks,
-                      const RopeKParams q, unsigned q_columns) {
-  const long long x = blockIdx.x;
-  if (x >= page_blocks) {
-    const unsigned at = static_cast<unsigned>(x - page_blocks);
+__global__ void __launch_bounds__(kF8Threads)
+    append_fp8_rows_kernel(const AppendFp8Params p, int page_shift, long long sites, unsigned site_blocks,
+                           const RopeKParams q, unsigned q_columns) {
+  if (blockIdx.x >= site_blocks) {
+    const unsigned at = blockIdx.x - site_blocks;
     rope_block<FP16, INTERLEAVED>(q, at % q_columns, at / q_columns);
     return;
   }
+  const int u = threadIdx.x & 7;
+  const long long site = static_cast<long long>(blockIdx.x) * (kF8Threads / 8) + (threadIdx.x >> 3);
   const int planes = 2 * p.H_kv;
-  append_fp8_block<FP16, INTERLEAVED>(p, x / planes, static_cast<int>(x % planes), page_shift);
+  // past the last site: a unit that no request reaches
+  AppendSite s = append_site(p, site < sites ? site / planes : 0, static_cast<int>(site % planes), page_shift, u);
+  if (site >= sites) s.ok = false;
+  if (!s.ok) s.first = s.end = 0;
+  const uint32_t flip = sign_bits(p, u);
+  const int rows = s.end - s.first;
+  const int most = __reduce_max_sync(0xffffffffu, rows);
+  float v[16];
+  auto finish = [&](int i) {
+    const int x = s.first + i;
+    const Raw16 r = i < rows ? load_row(s, x) : Raw16{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    widen16<FP16>(r.a, r.b, v);
+    // lanes of values go along (the transform's shuffles are warp-wide)
+    float k[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) k[e] = v[e];
+    key_row<INTERLEAVED>(k, p, i < rows ? s.page0 + x : 0, u, flip);
+    if (!s.is_v) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = k[e];
+    }
+  };
+  float amax = 0.f;
+  for (int i = 0; i < most; ++i) {
+    finish(i);
+    if (i < rows) amax = fmaxf(amax, amax16(v));
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const float after = new_descale(s.before, amax);
+  const float rcp = __fdiv_rn(1.f, after);
+  const uint64_t y2 = pack2(rcp, rcp), nb2 = pack2(-after, -after);
+  for (int i = 0; i < most; ++i) {
+    if (most > 1) finish(i);
+    if (i < rows) store_row(s, s.first + i, v, y2, nb2);
+  }
+  __syncwarp();                                      // every lane has read the old descale
+  if (s.ok) {
+    if (u == 0) *s.descale = after;
+    other_rows(s, after, p.page_size, 0, 1);
+  }
 }
 
 int shift_of(int page_size) {
   int s = 0;
   while ((1 << s) < page_size) ++s;
   return s;
+}
+
+template <bool FP16, bool INTERLEAVED>
+attn_status_t launch_append_pages(const AppendFp8Params& p, int page_shift, unsigned grid, int threads,
+                                  cudaStream_t stream) {
+  if (p.page_size * 8 <= kF8MaxThreads) {
+    append_fp8_pages_kernel<FP16, INTERLEAVED, 1><<<grid, threads, 0, stream>>>(p, page_shift);
+    return ATTN_OK;
+  }
+  constexpr int smem = 4 * 2 * kF8MaxThreads * static_cast<int>(sizeof(uint4));
+  auto kern = append_fp8_pages_kernel<FP16, INTERLEAVED, 4>;
+  const attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), smem);
+  if (s != ATTN_OK) return s;
+  kern<<<grid, threads, smem, stream>>>(p, page_shift);
+  return ATTN_OK;
 }
 
 }  // namespace
@@ -369,8 +610,10 @@ attn_status_t launch_block_tables(const TablesParams& p, cudaStream_t stream) {
   int* status = device_status_word();
   if (!status) return fail(ATTN_ERR_CUDA, "status word unavailable");
   const int smem = 2 * (p.B + 1) * static_cast<int>(sizeof(int));
-  attn_status_t s = set_smem(reinterpret_cast<const void*>(block_tables_kernel), 2 * (kTabMaxB + 1) * 4);
-  if (s != ATTN_OK) return s;
+  if (smem > 48 * 1024) {
+    const attn_status_t s = set_smem(reinterpret_cast<const void*>(block_tables_kernel), 2 * (kTabMaxB + 1) * 4);
+    if (s != ATTN_OK) return s;
+  }
   // one thread per token, at most two blocks per SM
   long long blocks = (static_cast<long long>(p.capacity) + kTabThreads - 1) / kTabThreads;
   blocks = blocks < 1 ? 1 : blocks > 304 ? 304 : blocks;
@@ -387,26 +630,47 @@ attn_status_t launch_append_fp8(AppendFp8Params p, RopeKParams q, int fp16, int 
   if (!p.status) return fail(ATTN_ERR_CUDA, "status word unavailable");
   const int shift = shift_of(p.page_size);
   const long long units = (static_cast<long long>(p.total) >> shift) + 2ll * p.B;
-  const long long page_blocks = units * 2 * p.H_kv;
-  RopeGrid g{1, 0};
-  if (q.heads[0] > 0) g = rope_grid(&q);
-  q.status = p.status;
-  const long long blocks = page_blocks + g.columns * g.chunks;
-  if (blocks > 2147483647LL) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
-  static_assert(kF8MaxThreads == kRopeThreads, "one block size for both roles");
-  const int threads = kF8MaxThreads;
-  const unsigned grid = static_cast<unsigned>(blocks);
-#define ATTN_APPEND(F, I) append_fp8_kernel<F, I><<<grid, threads, 0, stream>>>( \
-      p, shift, page_blocks, q, static_cast<unsigned>(g.columns))
-  if (fp16) {
-    if (interleaved) ATTN_APPEND(true, true);
-    else ATTN_APPEND(true, false);
-  } else {
-    if (interleaved) ATTN_APPEND(false, true);
-    else ATTN_APPEND(false, false);
-  }
+  const long long sites = units * 2 * p.H_kv;
+  if (sites > 2147483647LL) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
+  cudaError_t e;
+  // Up to 4 new tokens per request on average: the few-rows kernel, query rows in
+  // the same launch.  More: a block per page and plane.
+  if (p.total <= 4ll * p.B) {
+    RopeGrid g{1, 0};
+    q.status = p.status;
+    if (q.heads[0] > 0) g = rope_grid(&q);
+    const long long site_blocks = (sites + kF8Threads / 8 - 1) / (kF8Threads / 8);
+    if (site_blocks + g.columns * g.chunks > 2147483647LL)
+      return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
+    static_assert(kF8Threads == kRopeThreads, "one block size for both roles");
+    const unsigned grid = static_cast<unsigned>(site_blocks + g.columns * g.chunks);
+#define ATTN_APPEND(F, I)                                                       \
+  append_fp8_rows_kernel<F, I><<<grid, kF8Threads, 0, stream>>>(                \
+      p, shift, sites, static_cast<unsigned>(site_blocks), q, static_cast<unsigned>(g.columns))
+    if (fp16) {
+      if (interleaved) ATTN_APPEND(true, true);
+      else ATTN_APPEND(true, false);
+    } else {
+      if (interleaved) ATTN_APPEND(false, true);
+      else ATTN_APPEND(false, false);
+    }
 #undef ATTN_APPEND
-  const cudaError_t e = cudaGetLastError();
+  } else {
+    if (q.heads[0] > 0) {
+      const attn_status_t s = launch_rope(q, fp16, interleaved, stream);
+      if (s != ATTN_OK) return s;
+    }
+    // eight threads per row of a page, up to 64 rows at a time
+    const int threads = p.page_size * 8 < kF8MaxThreads ? p.page_size * 8 : kF8MaxThreads;
+    const unsigned grid = static_cast<unsigned>(sites);
+#define ATTN_APPEND(F, I) launch_append_pages<F, I>(p, shift, grid, threads, stream)
+    attn_status_t s;
+    if (fp16) s = interleaved ? ATTN_APPEND(true, true) : ATTN_APPEND(true, false);
+    else s = interleaved ? ATTN_APPEND(false, true) : ATTN_APPEND(false, false);
+#undef ATTN_APPEND
+    if (s != ATTN_OK) return s;
+  }
+  e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "FP8 append kernel launch");
   return ATTN_OK;
 }

@@ -5,11 +5,15 @@
 // controls", fuses the rotation with the Hadamard transform of the FP8 pre-pass
 // (fp8.cu) and leaves its definition to the caller's tables; this is the same
 // rotation for the 16-bit kernels, forward and inverse.
+#include <cmath>
+
 #include "common.h"
 #include "rope.cuh"
 
 namespace attn {
 namespace {
+
+constexpr double kTwoPi = 6.283185307179586476925;
 
 template <bool FP16, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeKParams p) {
@@ -22,39 +26,40 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeKParams p)
 // linearly in r_i between (interpolation "by parts", section 3.2 of "YaRN:
 // Efficient Context Window Extension of Large Language Models",
 // arXiv:2309.00071); orig_len = 0 divides every frequency (position
-// interpolation, arXiv:2306.15595).  The angle p * theta reaches 1e6 rad, where
-// a float32 angle would be off by 0.06, so theta and the angle are float64,
-// reduced to [-pi, pi] before the float32 sine and cosine.
-// Bound: the writes, 8 bytes per entry; the float64 work is one product, one
-// rounding and one fused multiply-add per entry, the power one per column.
+// interpolation, arXiv:2306.15595).
+//
+// The angle p * theta reaches 1e6 rad, where a float32 angle would be off by
+// 0.06, and float64 arithmetic runs at 1/64 of the float32 rate here.  So the
+// frequency is held in turns per position as a 64-bit binary fraction F, which the
+// host computes in float64 (at most 128 of them, passed by value): the product
+// p * F modulo 2^64 is the angle modulo one turn, exactly, in integers.  Its upper
+// 32 bits, as a signed number of half turns, are what sincospif takes.  F is off by
+// at most 2^-53 of itself, the cut to 32 bits by 2^-33 of a turn.
+// Bound: instruction issue, close to the writes (8 bytes per entry).
+struct RopeTurns {
+  unsigned long long f[128];
+};
+
 __global__ void __launch_bounds__(256)
     rope_table_kernel(float* __restrict__ cos_out, float* __restrict__ sin_out, long long n, int half,
-                      double base, double factor, double orig_len, double low, double high,
-                      float attn_factor, long long first, int rows_per_block) {
-  const int cols = min(half, 256);
-  const int lanes = 256 / cols;                     // rows written at a time
-  const int i0 = threadIdx.x % cols;
-  const int sub = threadIdx.x / cols;
+                      const __grid_constant__ RopeTurns turns, float attn_factor, unsigned first,
+                      int rows_per_block) {
+  const int lanes = 256 / half;                     // rows written at a time
+  const int i = static_cast<int>(threadIdx.x) % half;
+  const int sub = static_cast<int>(threadIdx.x) / half;
   if (sub >= lanes) return;
+  const unsigned long long f = turns.f[i];
   const long long r0 = static_cast<long long>(blockIdx.x) * rows_per_block;
   const long long r1 = r0 + rows_per_block < n ? r0 + rows_per_block : n;
-  for (int i = i0; i < half; i += cols) {
-    double theta = pow(base, -static_cast<double>(i) / half);
-    double keep = 0.0;
-    if (orig_len > 0.0) {
-      keep = (orig_len * theta * 0.15915494309189533577 - low) / (high - low);
-      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
-    }
-    theta *= keep + (1.0 - keep) / factor;
-    for (long long r = r0 + sub; r < r1; r += lanes) {
-      const double a = static_cast<double>(first + r) * theta;
-      const double turns = rint(a * 0.15915494309189533577);
-      const float x = static_cast<float>(fma(turns, -6.28318530717958647693, a));
-      float sn, cs;
-      sincosf(x, &sn, &cs);
-      cos_out[r * half + i] = cs * attn_factor;
-      sin_out[r * half + i] = sn * attn_factor;
-    }
+  unsigned long long angle = f * (static_cast<unsigned long long>(first) + r0 + sub);
+  const unsigned long long step = f * lanes;
+  for (long long r = r0 + sub; r < r1; r += lanes, angle += step) {
+    // the nearest multiple of 2^-32 turns, as half turns in [-1, 1)
+    const int half_turns = static_cast<int>((angle + 0x80000000ull) >> 32);
+    float sn, cs;
+    sincospif(static_cast<float>(half_turns) * 4.656612873077392578125e-10f, &sn, &cs);
+    cos_out[r * half + i] = cs * attn_factor;
+    sin_out[r * half + i] = sn * attn_factor;
   }
 }
 
@@ -82,14 +87,26 @@ attn_status_t launch_rope(RopeKParams p, int fp16, int interleaved, cudaStream_t
 attn_status_t launch_rope_table(float* cos_out, float* sin_out, long long n, int rot, double base,
                                 double factor, long long orig_len, double low, double high,
                                 double attn_factor, long long first, cudaStream_t stream) {
-  // a block computes its columns' powers once, for up to 64 rows
+  const int half = rot / 2;
+  RopeTurns turns;
+  for (int i = 0; i < half; ++i) {
+    double theta = std::pow(base, -static_cast<double>(i) / half);
+    double keep = 0.0;
+    if (orig_len > 0) {
+      keep = (static_cast<double>(orig_len) * theta / kTwoPi - low) / (high - low);
+      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+    }
+    theta *= keep + (1.0 - keep) / factor;
+    // below 1 / (2 pi) turns per position, times 2^64
+    turns.f[i] = static_cast<unsigned long long>(std::ldexp(theta / kTwoPi, 64));
+  }
+  // eight blocks per SM, at least 8 rows each
   long long rows = (n + 152 * 8 - 1) / (152 * 8);
-  rows = rows < 8 ? 8 : rows > 64 ? 64 : rows;
+  rows = rows < 8 ? 8 : rows;
   const long long blocks = (n + rows - 1) / rows;
-  if (blocks > 2147483647LL) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
   rope_table_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-      cos_out, sin_out, n, rot / 2, base, factor, static_cast<double>(orig_len), low, high,
-      static_cast<float>(attn_factor), first, static_cast<int>(rows));
+      cos_out, sin_out, n, half, turns, static_cast<float>(attn_factor), static_cast<unsigned>(first),
+      static_cast<int>(rows));
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "rotary table launch");
   return ATTN_OK;
