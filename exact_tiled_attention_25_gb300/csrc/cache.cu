@@ -181,11 +181,11 @@ __device__ __forceinline__ void load8(const float* t, size_t at, float (&x)[8]) 
 }
 
 // A key row held by eight lanes: rotated by the tables' row `pos`, then
-// transformed by M = diag(signs) H_128 / sqrt(128); `flip`: bit i set where the
-// sign of the lane's value i is -1.  Every lane of the warp takes part.
+// transformed by M = diag(signs) H_128 / sqrt(128), the signs in shared memory.
+// Every lane of the warp takes part.
 template <bool INTERLEAVED>
 __device__ __forceinline__ void key_row(float (&x)[16], const AppendFp8Params& p, int pos, int u,
-                                        uint32_t flip) {
+                                        const float* signs) {
   if (p.cos) {
     const bool inside = pos < p.max_pos;
     const size_t row = static_cast<size_t>(inside ? pos : 0) * (p.rot / 2);
@@ -253,10 +253,12 @@ __device__ __forceinline__ void key_row(float (&x)[16], const AppendFp8Params& p
   if (p.signs) {
     uint64_t y[8];                                   // pairs of neighbouring columns
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = __uint_as_float(__float_as_uint(x[2 * i]) ^ ((flip >> (2 * i) & 1u) << 31));
-      const float b = __uint_as_float(__float_as_uint(x[2 * i + 1]) ^ ((flip >> (2 * i + 1) & 1u) << 31));
-      y[i] = pack2(a + b, a - b);                    // span 1
+    for (int i = 0; i < 4; ++i) {
+      const float4 sg = *reinterpret_cast<const float4*>(signs + (i < 2 ? 8 * u + 4 * i : 64 + 8 * u + 4 * (i - 2)));
+      const uint64_t a = fmul2(pack2(x[4 * i], x[4 * i + 1]), pack2(sg.x, sg.y));
+      const uint64_t c = fmul2(pack2(x[4 * i + 2], x[4 * i + 3]), pack2(sg.z, sg.w));
+      y[2 * i] = pack2(lo2(a) + hi2(a), lo2(a) - hi2(a));           // span 1
+      y[2 * i + 1] = pack2(lo2(c) + hi2(c), lo2(c) - hi2(c));
     }
     const uint64_t neg = pack2(-1.f, -1.f);
     auto in_lane = [&](int i, int j) {
@@ -293,9 +295,9 @@ struct AppendSite {
   bool is_v;
   int page0;              // position of the page's first row
   int first, end;         // page rows [first, end) are new
-  const uint16_t* src;    // row x of the page: src + x * st, this lane's columns
+  const uint16_t* src;    // row x of the page: src + x * st
   long long st;
-  uint8_t* dst;           // row x: dst + x * dstep, this lane's columns
+  uint8_t* dst;           // row x: dst + x * dstep (the caller adds its lanes' columns to both)
   size_t dstep;
   float* descale;
   float before;
@@ -349,9 +351,9 @@ __device__ __forceinline__ AppendSite append_site(const AppendFp8Params& p, long
   s.st = s.is_v ? p.vt : p.kt;
   // row x of the page is token c0 + (page0 + x - start)
   s.src = static_cast<const uint16_t*>(s.is_v ? p.v : p.k) + (s.is_v ? p.vh : p.kh) * h +
-          s.st * (c0 + (s.page0 - start)) + 8 * u;
+          s.st * (c0 + (s.page0 - start));
   s.dst = (s.is_v ? p.v_cache : p.k_cache) +
-          (static_cast<size_t>(phys) * p.page_size * p.H_kv + h) * D + 8 * u;
+          (static_cast<size_t>(phys) * p.page_size * p.H_kv + h) * D;
   s.dstep = static_cast<size_t>(p.H_kv) * D;
   s.descale = (s.is_v ? p.v_descale : p.k_descale) + static_cast<size_t>(phys) * p.H_kv + h;
   s.before = s.first == 0 ? 0.f : *s.descale;
@@ -422,15 +424,23 @@ __device__ __forceinline__ void other_rows(const AppendSite& s, float after, int
   }
 }
 
-// Bits of the lane's sixteen negative signs.
-__device__ __forceinline__ uint32_t sign_bits(const AppendFp8Params& p, int u) {
-  uint32_t flip = 0;
-  if (p.signs) {
+// Largest magnitude of a raw row's sixteen values, in packed 16-bit maxima (exact).
+template <bool FP16>
+__device__ __forceinline__ float raw_amax(const Raw16& r) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  float2 m;
+  if (FP16) {
+    __half2 t = __habs2(*reinterpret_cast<const __half2*>(&w[0]));
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (__ldg(p.signs + (i < 8 ? 8 * u + i : 64 + 8 * u + i - 8)) < 0.f) flip |= 1u << i;
+    for (int i = 1; i < 8; ++i) t = __hmax2(t, __habs2(*reinterpret_cast<const __half2*>(&w[i])));
+    m = __half22float2(t);
+  } else {
+    __nv_bfloat162 t = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t = __hmax2(t, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+    m = __bfloat1622float2(t);
   }
-  return flip;
+  return fmaxf(m.x, m.y);
 }
 
 // 16 bytes to shared memory without passing registers, zeros if !valid (the source
@@ -452,16 +462,39 @@ __device__ __forceinline__ void copies_wait() {
 // float32 rows would in occupancy (registers for 4 raw rows spilled).  Rows of
 // larger pages are read again, from L2.  SWEEPS = 1: a page is one row per
 // thread, whose values stay in registers.
+// Bound: instruction issue and shuffles of the key rows (some 330 instructions per
+// 4 rows and pass), while rotating the query rows is bound by DRAM; q_blocks blocks
+// of that, spread evenly among the others, use what these leave.
 template <bool FP16, bool INTERLEAVED, int SWEEPS>
 __global__ void __launch_bounds__(kF8MaxThreads, 2)
-    append_fp8_pages_kernel(const AppendFp8Params p, int page_shift) {
+    append_fp8_pages_kernel(const AppendFp8Params p, int page_shift, const RopeKParams q, unsigned q_blocks,
+                            unsigned q_columns) {
   extern __shared__ uint4 raw_sh[];                  // [SWEEPS][2][blockDim], SWEEPS > 1
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int u = lane & 7;
   const int by = blockDim.x >> 3, mine = threadIdx.x >> 3;
   __shared__ float warp_max[kF8MaxThreads / 32];
-  const AppendSite s = append_site(p, blockIdx.x / (2 * p.H_kv), blockIdx.x % (2 * p.H_kv), page_shift, u);
+  __shared__ __align__(16) float signs[128];
+  __shared__ AppendSite site_sh;
+  // query blocks among the first blockIdx.x blocks, and among one more
+  const unsigned before_q = static_cast<unsigned>(static_cast<unsigned long long>(blockIdx.x) * q_blocks / gridDim.x);
+  const unsigned with_q = static_cast<unsigned>((blockIdx.x + 1ull) * q_blocks / gridDim.x);
+  if (with_q > before_q) {
+    rope_block<FP16, INTERLEAVED, 2>(q, before_q % q_columns, before_q / q_columns);
+    return;
+  }
+  const unsigned at_site = blockIdx.x - before_q;
+  if (warp == 0) {
+    const AppendSite found = append_site(p, at_site / (2 * p.H_kv), at_site % (2 * p.H_kv), page_shift, u);
+    if (lane == 0) site_sh = found;
+  } else if (p.signs && warp == 1) {
+    *reinterpret_cast<float4*>(signs + 4 * lane) = __ldg(reinterpret_cast<const float4*>(p.signs) + lane);
+  }
+  __syncthreads();
+  AppendSite s = site_sh;
   if (!s.ok) return;                                 // the same for the whole block
+  s.src += 8 * u;
+  s.dst += 8 * u;
   if constexpr (SWEEPS > 1) {
 #pragma unroll
     for (int i = 0; i < SWEEPS; ++i) {
@@ -473,41 +506,41 @@ __global__ void __launch_bounds__(kF8MaxThreads, 2)
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
   }
-  const uint32_t flip = s.is_v ? 0u : sign_bits(p, u);
   float v[16];
-  // row s.first + mine + i * by into v; lanes past the new rows go along with zeros
-  // (the transform's shuffles are warp-wide)
-  auto finish = [&](int i, bool staged) {
+  // row s.first + mine + i * by, zeros past the new rows (the transform's shuffles are
+  // warp-wide, so those lanes go along)
+  auto row = [&](int i, bool staged) -> Raw16 {
+    if (staged)
+      return {raw_sh[(2 * i) * blockDim.x + threadIdx.x], raw_sh[(2 * i + 1) * blockDim.x + threadIdx.x]};
     const int x = s.first + mine + i * by;
-    Raw16 r{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-    if (staged) r = {raw_sh[(2 * i) * blockDim.x + threadIdx.x], raw_sh[(2 * i + 1) * blockDim.x + threadIdx.x]};
-    else if (x < s.end) r = load_row(s, x);
+    return x < s.end ? load_row(s, x) : Raw16{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  };
+  auto finish = [&](int i, const Raw16& r) {
     widen16<FP16>(r.a, r.b, v);
-    if (!s.is_v) key_row<INTERLEAVED>(v, p, s.page0 + x, u, flip);
+    if (!s.is_v) key_row<INTERLEAVED>(v, p, s.page0 + s.first + mine + i * by, u, signs);
+  };
+  // values need no transform before their amax, unless v holds them till the end
+  auto max_of = [&](int i, const Raw16& r) {
+    if (SWEEPS > 1 && s.is_v) return raw_amax<FP16>(r);
+    finish(i, r);
+    return amax16(v);
   };
   const int warp_first = s.first + (warp << 2);      // first row of the warp's first sweep
   const int sweeps = warp_first < s.end ? (s.end - warp_first + by - 1) / by : 0;   // of this warp
   float amax = 0.f;
   int i = 0;
   if constexpr (SWEEPS > 1) {
-    auto staged_max = [&](int at) {
-      finish(at, true);
-      amax = fmaxf(amax, amax16(v));
-    };
     copies_wait<3>();
-    if (sweeps > 0) staged_max(0);
+    if (sweeps > 0) amax = fmaxf(amax, max_of(0, row(0, true)));
     copies_wait<2>();
-    if (sweeps > 1) staged_max(1);
+    if (sweeps > 1) amax = fmaxf(amax, max_of(1, row(1, true)));
     copies_wait<1>();
-    if (sweeps > 2) staged_max(2);
+    if (sweeps > 2) amax = fmaxf(amax, max_of(2, row(2, true)));
     copies_wait<0>();
-    if (sweeps > 3) staged_max(3);
+    if (sweeps > 3) amax = fmaxf(amax, max_of(3, row(3, true)));
     i = SWEEPS;
   }
-  for (; i < sweeps; ++i) {
-    finish(i, false);
-    amax = fmaxf(amax, amax16(v));
-  }
+  for (; i < sweeps; ++i) amax = fmaxf(amax, max_of(i, row(i, false)));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if (lane == 0) warp_max[warp] = amax;
@@ -518,7 +551,7 @@ __global__ void __launch_bounds__(kF8MaxThreads, 2)
   const float rcp = __fdiv_rn(1.f, after);
   const uint64_t y2 = pack2(rcp, rcp), nb2 = pack2(-after, -after);
   for (i = 0; i < sweeps; ++i) {
-    if (SWEEPS > 1 || sweeps > 1) finish(i, SWEEPS > 1 && i < SWEEPS);   // else still in v
+    if (SWEEPS > 1 || sweeps > 1) finish(i, row(i, SWEEPS > 1 && i < SWEEPS));   // else still in v
     const int x = s.first + mine + i * by;
     if (x < s.end) store_row(s, x, v, y2, nb2);
   }
@@ -531,6 +564,7 @@ template <bool FP16, bool INTERLEAVED>
 __global__ void __launch_bounds__(kF8Threads)
     append_fp8_rows_kernel(const AppendFp8Params p, int page_shift, long long sites, unsigned site_blocks,
                            const RopeKParams q, unsigned q_columns) {
+  __shared__ __align__(16) float signs[128];
   if (blockIdx.x >= site_blocks) {
     const unsigned at = blockIdx.x - site_blocks;
     rope_block<FP16, INTERLEAVED>(q, at % q_columns, at / q_columns);
@@ -543,7 +577,13 @@ __global__ void __launch_bounds__(kF8Threads)
   AppendSite s = append_site(p, site < sites ? site / planes : 0, static_cast<int>(site % planes), page_shift, u);
   if (site >= sites) s.ok = false;
   if (!s.ok) s.first = s.end = 0;
-  const uint32_t flip = sign_bits(p, u);
+  s.src += 8 * u;
+  s.dst += 8 * u;
+  if (p.signs) {
+    if (threadIdx.x < 32)
+      *reinterpret_cast<float4*>(signs + 4 * threadIdx.x) = __ldg(reinterpret_cast<const float4*>(p.signs) + threadIdx.x);
+    __syncthreads();
+  }
   const int rows = s.end - s.first;
   const int most = __reduce_max_sync(0xffffffffu, rows);
   float v[16];
@@ -555,7 +595,7 @@ __global__ void __launch_bounds__(kF8Threads)
     float k[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) k[e] = v[e];
-    key_row<INTERLEAVED>(k, p, i < rows ? s.page0 + x : 0, u, flip);
+    key_row<INTERLEAVED>(k, p, i < rows ? s.page0 + x : 0, u, signs);
     if (!s.is_v) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = k[e];
@@ -589,17 +629,26 @@ int shift_of(int page_size) {
 }
 
 template <bool FP16, bool INTERLEAVED>
-attn_status_t launch_append_pages(const AppendFp8Params& p, int page_shift, unsigned grid, int threads,
+attn_status_t launch_append_pages(const AppendFp8Params& p, int page_shift, RopeKParams q, long long sites,
                                   cudaStream_t stream) {
+  // eight threads per row of a page, up to 64 rows at a time
+  const int threads = p.page_size * 8 < kF8MaxThreads ? p.page_size * 8 : kF8MaxThreads;
+  RopeGrid g{1, 0};
+  q.status = p.status;
+  if (q.heads[0] > 0) g = rope_grid(&q, threads);
+  const long long q_blocks = g.columns * g.chunks;
+  if (sites + q_blocks > 2147483647LL) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
+  const unsigned grid = static_cast<unsigned>(sites + q_blocks), columns = static_cast<unsigned>(g.columns);
+  const unsigned qb = static_cast<unsigned>(q_blocks);
   if (p.page_size * 8 <= kF8MaxThreads) {
-    append_fp8_pages_kernel<FP16, INTERLEAVED, 1><<<grid, threads, 0, stream>>>(p, page_shift);
+    append_fp8_pages_kernel<FP16, INTERLEAVED, 1><<<grid, threads, 0, stream>>>(p, page_shift, q, qb, columns);
     return ATTN_OK;
   }
   constexpr int smem = 4 * 2 * kF8MaxThreads * static_cast<int>(sizeof(uint4));
   auto kern = append_fp8_pages_kernel<FP16, INTERLEAVED, 4>;
   const attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), smem);
   if (s != ATTN_OK) return s;
-  kern<<<grid, threads, smem, stream>>>(p, page_shift);
+  kern<<<grid, threads, smem, stream>>>(p, page_shift, q, qb, columns);
   return ATTN_OK;
 }
 
@@ -656,14 +705,7 @@ attn_status_t launch_append_fp8(AppendFp8Params p, RopeKParams q, int fp16, int 
     }
 #undef ATTN_APPEND
   } else {
-    if (q.heads[0] > 0) {
-      const attn_status_t s = launch_rope(q, fp16, interleaved, stream);
-      if (s != ATTN_OK) return s;
-    }
-    // eight threads per row of a page, up to 64 rows at a time
-    const int threads = p.page_size * 8 < kF8MaxThreads ? p.page_size * 8 : kF8MaxThreads;
-    const unsigned grid = static_cast<unsigned>(sites);
-#define ATTN_APPEND(F, I) launch_append_pages<F, I>(p, shift, grid, threads, stream)
+#define ATTN_APPEND(F, I) launch_append_pages<F, I>(p, shift, q, sites, stream)
     attn_status_t s;
     if (fp16) s = interleaved ? ATTN_APPEND(true, true) : ATTN_APPEND(true, false);
     else s = interleaved ? ATTN_APPEND(false, true) : ATTN_APPEND(false, false);

@@ -51,12 +51,12 @@ __device__ __forceinline__ uint4 pack16(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Work of one block: tokens of block column `bx`, heads of chunk `chunk`.
-template <bool FP16, bool INTERLEAVED>
+// Work of one block: tokens of block column `bx`, heads of chunk `chunk`, kHeads of
+// them at a time.
+template <bool FP16, bool INTERLEAVED, int kHeads = 4>
 __device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, int chunk) {
-  constexpr int kHeads = 4;
   const int units = p.d / 16;                       // 4, 8 or 16: divides the block
-  const int tokens = kRopeThreads / units;
+  const int tokens = static_cast<int>(blockDim.x) / units;
   const int u = static_cast<int>(threadIdx.x) % units;
   const long long tk = bx * tokens + static_cast<int>(threadIdx.x) / units;
   if (tk >= static_cast<long long>(p.B) * p.N) return;
@@ -189,8 +189,8 @@ struct RopeGrid {
   long long columns;
   int chunks;
 };
-inline RopeGrid rope_grid(RopeKParams* p) {
-  const int tokens = kRopeThreads / (p->d / 16);
+inline RopeGrid rope_grid(RopeKParams* p, int threads = kRopeThreads) {
+  const int tokens = threads / (p->d / 16);
   RopeGrid g;
   g.columns = (static_cast<long long>(p->B) * p->N + tokens - 1) / tokens;
   const int all = p->heads[0] + p->heads[1] + p->heads[2];
