@@ -739,7 +739,7 @@ static attn_status_t check_cross(int B, int H, int H_kv, int N_q, int N_k, int d
 
 size_t attn_cross_workspace_size(int B, int H, int H_kv, int N_q, int N_k, int d) {
   if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || N_q < 1 || N_k < 1 || d < 1) return 0;
-  return cross_workspace_bytes(B, H, N_q, d, cross_plan(B, H, H_kv, N_q, N_k, d));
+  return cross_workspace_bytes(H, H_kv, N_q, d, cross_plan(B, H, H_kv, N_q, N_k, d));
 }
 
 attn_status_t attn_cross_fwd(const void* q, const void* k, const void* v, const int* kv_lens, void* o,
@@ -753,7 +753,7 @@ attn_status_t attn_cross_fwd(const void* q, const void* k, const void* v, const 
   if ((s = check_scale(softmax_scale)) != ATTN_OK) return s;
   if ((s = check_dtype(dtype)) != ATTN_OK) return s;
   const CrossPlan plan = cross_plan(B, H, H_kv, N_q, N_k, d);
-  const size_t need = cross_workspace_bytes(B, H, N_q, d, plan);
+  const size_t need = cross_workspace_bytes(H, H_kv, N_q, d, plan);
   if (need > 0) {
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
       return fail(ATTN_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned");
@@ -763,7 +763,7 @@ attn_status_t attn_cross_fwd(const void* q, const void* k, const void* v, const 
   if ((s = check_device()) != ATTN_OK) return s;
   FwdParams p{q, k, v, o, lse, B, H, N_q, d, H_kv, nullptr, 0, 0, softmax_scale,
               dtype == ATTN_FP16 ? 1 : 0, N_k, kv_lens};
-  return plan.splits > 0 ? launch_cross_split(p, plan, workspace, stream) : launch_cross_fwd(p, stream);
+  return plan.ctas > 0 ? launch_cross_rows(p, plan, workspace, stream) : launch_cross_fwd(p, stream);
 }
 
 attn_status_t attn_cross_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout,

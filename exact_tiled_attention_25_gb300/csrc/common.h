@@ -219,26 +219,28 @@ inline size_t decode_workspace_bytes(int B, int H, int H_kv, int n_q, int d, int
 
 attn_status_t launch_decode(const DecodeParams& p, cudaStream_t stream);
 
-// How a cross-attention forward runs.  splits > 0: the split kernel (decode.cu)
-// on tiles of 128 query rows of one key/value head (its G * N_q rows together)
-// with the keys in `splits` ranges; splits = 0: the forward kernel (fwd.cu).
+// How a cross-attention forward runs.  ctas > 0: the rows kernel (cross.cu), that many
+// CTAs sharing the tiles of all keys, for tiles of 128 query rows of one key/value
+// head (its G * N_q rows together); ctas = 0: the forward kernel (fwd.cu).
 struct CrossPlan {
-  int splits, tiles_per_split, qtiles;
+  int ctas, qtiles;
 };
+constexpr int kCrossMaxB = 4096;   // batch entries of the rows kernel (4 bytes of shared memory each)
 inline CrossPlan cross_plan(int B, int H, int H_kv, int N_q, int N_k, int d) {
   const long long rows = static_cast<long long>(H / H_kv) * N_q;
   const long long qtiles = (rows + 127) / 128;
-  if (d == 256 || qtiles > 1) return {0, 0, 0};
-  const DecodeSplits sp = decode_splits(B, H_kv * static_cast<int>(qtiles), N_k);
-  return {sp.splits, sp.tiles_per_split, static_cast<int>(qtiles)};
+  if (d == 256 || qtiles > 1 || B > kCrossMaxB) return {0, 0};
+  const long long tiles = static_cast<long long>(B) * H_kv * qtiles * ((N_k + 127) / 128);
+  return {static_cast<int>(tiles < 152 ? tiles : 152), static_cast<int>(qtiles)};
 }
-// The split kernel's float32 partial O and log-sum-exp (none for one split).
-inline size_t cross_workspace_bytes(int B, int H, int N_q, int d, const CrossPlan& plan) {
-  if (plan.splits <= 1) return 0;
-  const size_t rows = static_cast<size_t>(B) * H * N_q * plan.splits;
+// The rows kernel's float32 partial O and log-sum-exps, two per CTA.
+inline size_t cross_workspace_bytes(int H, int H_kv, int N_q, int d, const CrossPlan& plan) {
+  if (plan.ctas <= 1) return 0;
+  const size_t seg = static_cast<size_t>(H / H_kv) * N_q;
+  const size_t rows = 2ull * plan.ctas * (seg < 128 ? seg : 128);
   return align_up(rows * d * sizeof(float), 256) + align_up(rows * sizeof(float), 256);
 }
-attn_status_t launch_cross_split(const FwdParams& p, const CrossPlan& plan, void* workspace,
-                                 cudaStream_t stream);
+attn_status_t launch_cross_rows(const FwdParams& p, const CrossPlan& plan, void* workspace,
+                                cudaStream_t stream);
 
 }  // namespace attn

@@ -1,0 +1,681 @@
+// Cross attention of few query rows: the tiles of all keys dealt out evenly.
+//
+// A decode step, or a short decoder sequence, against encoder states is bound by
+// reading K and V once.  The G * N_q query rows of a key/value head (G = H / H_kv),
+// contiguous in [B, H, N_q, d], form tiles of up to 128 rows; a segment is one such
+// tile with the keys of its batch entry, kv_lens[b] of them in tiles of 128.
+//
+//  * All tiles of all segments stand in one line, and CTA c of C (one per SM)
+//    takes an even share, [c T / C, (c + 1) T / C): lengths differ between batch
+//    entries, and one CTA per segment left SMs idle in the last wave (B = 32,
+//    H_kv = 8, N_k = 2048, half of it to all of it seen: 42 us).
+//  * A CTA walks through the parts of segments in its share without draining its
+//    ring of K and V tiles between them; scores and outputs are double-buffered
+//    in tensor memory, so a part's output is written while the next part's first
+//    products run.
+//  * A segment inside one share is finished there.  One that crosses shares
+//    leaves float32 partial outputs and log-sum-exps, at most two per CTA, which a
+//    second kernel merges; its launch overlaps the first kernel.
+//
+// Roles as in the paged decode: key and value producer warps, one MMA warp, four
+// softmax warps (a thread per query row).
+#include <cmath>
+
+#include "common.h"
+#include "sm103_prims.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kSmemLimit = 232448;
+constexpr int BM = 128;   // query rows of a tile
+constexpr int BN = 128;   // keys of a tile
+
+// QROWS: rows of Q held in shared memory, 16 or 128.  The score product always
+// reads 128; behind 16 it meets ring memory, whose garbage stays in its own rows of
+// S, P and O, which nothing reads.  At d = 128 two full Q tiles would leave a ring
+// of four tiles, 16 rows leave six.
+template <int D, int QROWS>
+struct CrossCfg {
+  static constexpr int CH = D / 64;
+  static constexpr int CHUNK = 128 * 128;
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int QCHUNK = QROWS * 128;
+  static constexpr int QTILE = QROWS * D * 2;
+  static constexpr int LENS = 4 * (kCrossMaxB + 1);      // tile prefix sums
+  static constexpr int NSLOT_FIT = (kSmemLimit - 2048 - LENS - 2 * QTILE) / TILE;
+  static constexpr int NSLOT = NSLOT_FIT > 10 ? 10 : NSLOT_FIT;
+  static constexpr int SMEM = 1024 + 2 * QTILE + NSLOT * TILE;   // two Q tiles and the ring
+  static constexpr int THREADS = 7 * 32;
+  static constexpr int LOAD_WARP = 4;
+  static constexpr int MMA_WARP = 5;
+  static constexpr int LOAD_V_WARP = 6;
+  __host__ __device__ static constexpr uint32_t S_COL(int buf) { return 128u * buf; }
+  __host__ __device__ static constexpr uint32_t O_COL(int buf) { return 256u + static_cast<uint32_t>(D) * buf; }
+  static_assert(NSLOT >= 4 && O_COL(1) + D <= 512, "ring or tensor memory");
+  static_assert(QCHUNK % 1024 == 0, "swizzle atoms");
+};
+
+struct CrossKParams {
+  const int* kv_lens;      // [B], or nullptr: Nk
+  void* o;
+  float* lse;
+  float* o_part;           // [2 C][rows of a segment][D]
+  float* lse_part;         // [2 C][rows of a segment]
+  int* status;
+  int B, H_kv, Nk;
+  int rows;                // G * N_q: query rows of a key/value head
+  int segs;                // segments per batch entry: H_kv * query tiles
+  int qtiles;
+  int seg_rows;            // rows of a partial result: min(rows, 128)
+  float scale_log2;
+};
+
+__device__ __forceinline__ float lg2f_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Keys that batch entry b sees; an entry out of range counts as none.
+__device__ __forceinline__ int keys_of(const int* kv_lens, int b, int Nk) {
+  if (!kv_lens) return Nk;
+  const int n = __ldg(kv_lens + b);
+  return n < 0 || n > Nk ? 0 : n;
+}
+
+// First tile of CTA c's share of T tiles.  At most T CTAs get one, so none of
+// theirs is empty; the others' start at T.
+__device__ __forceinline__ int share_start(int c, int C, int T) {
+  C = min(C, T);
+  return c >= C ? T : static_cast<int>(static_cast<long long>(c) * T / C);
+}
+
+// A walk over the parts of segments in a share.  pre[b]: tiles of one segment of
+// the batch entries before b.
+struct Cursor {
+  const int* pre;
+  int segs, B;
+  int b, y, j;      // batch entry, segment of it, tile of the segment
+  int left;         // tiles of the share from here on
+  __device__ __forceinline__ int tiles() const { return pre[b + 1] - pre[b]; }
+  // at the part's first tile: the part's tiles
+  __device__ __forceinline__ int part() const { return min(tiles() - j, left); }
+  __device__ __forceinline__ void next_part(int n) {
+    left -= n;
+    j = 0;
+    if (++y == segs) {
+      y = 0;
+      do {
+        ++b;
+      } while (b < B && pre[b + 1] == pre[b]);
+    }
+  }
+};
+
+__device__ __forceinline__ Cursor cursor_at(const int* pre, int segs, int B, int g, int left) {
+  int lo = 0, hi = B;      // last entry whose tiles start at or before g
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<long long>(pre[mid]) * segs <= g) lo = mid;
+    else hi = mid;
+  }
+  Cursor c{pre, segs, B, lo, 0, 0, left};
+  const int rem = g - pre[lo] * segs;
+  const int n = c.tiles();
+  if (n > 0) {
+    c.y = rem / n;
+    c.j = rem - c.y * n;
+  }
+  return c;
+}
+
+template <int D, bool FP16, int QROWS>
+__global__ void __launch_bounds__(CrossCfg<D, QROWS>::THREADS, 1)
+    cross_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const CrossKParams kp) {
+  using C = CrossCfg<D, QROWS>;
+  constexpr int NSLOT = C::NSLOT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + 2 * C::QTILE;
+
+  __shared__ __align__(8) uint64_t q_full[2];
+  __shared__ __align__(8) uint64_t q_empty[2];
+  __shared__ __align__(8) uint64_t kv_full[NSLOT];
+  __shared__ __align__(8) uint64_t kv_empty[NSLOT];
+  __shared__ __align__(8) uint64_t s_full[2];
+  __shared__ __align__(8) uint64_t p_full[2];
+  __shared__ __align__(8) uint64_t pv_done;
+  __shared__ __align__(8) uint64_t o_full[2];
+  __shared__ __align__(8) uint64_t o_empty[2];
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+  __shared__ int issued_sh[2];      // items that a producer issued: keys, values
+  __shared__ int parts_sh;          // Q tiles issued
+  __shared__ int warp_sum[C::THREADS / 32];
+  __shared__ int pre[kCrossMaxB + 1];
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+
+  // the merging kernel may start its prologue (it waits for this grid's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- tiles of a segment of the batch entries before each
+  {
+    const int per = (kp.B + C::THREADS - 1) / C::THREADS;
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, kp.B), b1 = min(b0 + per, kp.B);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      if (kp.kv_lens && blockIdx.x == 0) {
+        const int n = __ldg(kp.kv_lens + b);
+        if (n < 0 || n > kp.Nk) atomicCAS(kp.status, 0, kDevBadSeqlens);
+      }
+      sum += (keys_of(kp.kv_lens, b, kp.Nk) + BN - 1) / BN;
+    }
+    int scan = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += t;
+    }
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+    int base = scan - sum;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    for (int b = b0; b < b1; ++b) {
+      pre[b] = base;
+      base += (keys_of(kp.kv_lens, b, kp.Nk) + BN - 1) / BN;
+    }
+    if (b1 == kp.B && b0 < b1) pre[kp.B] = base;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_empty[i], 128);
+    }
+    mbar_init(&pv_done, 1);
+    for (int s = 0; s < NSLOT; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    mbar_init(&drain_bar, 1);
+    abort_sh = 0;
+    issued_sh[0] = issued_sh[1] = parts_sh = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::MMA_WARP) {
+    tmem_alloc(&tmem_base_sh, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = tmem_base_sh;
+  const Abort ab{&abort_sh, kp.status};
+  const int T = pre[kp.B] * kp.segs;
+  const int g0 = share_start(blockIdx.x, gridDim.x, T);
+  const int total = share_start(blockIdx.x + 1, gridDim.x, T) - g0;   // tiles of this CTA
+  Cursor cur = cursor_at(pre, kp.segs, kp.B, g0, total);
+
+  if (warp == C::LOAD_WARP || warp == C::LOAD_V_WARP) {
+    // ------------------------------------------------------------ producers
+    // Lane c issues column chunk c of a tile; two warps stream into the ring (one
+    // issuing warp cannot keep HBM busy).  Item 2 n is the n-th K tile of the
+    // share, item 2 n + 1 its V tile.
+    const int kv = warp == C::LOAD_WARP ? 0 : 1;
+    if (lane == 0 && kv == 0) {
+      prefetch_tmap(&tmQ);
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+    }
+    int n = 0, part = 0;
+    bool ok = true;
+    while (ok && cur.left > 0) {
+      const int take = cur.part();
+      const int hk = cur.y / kp.qtiles;
+      if (kv == 0) {
+        int go = 1;
+        if (lane == 0) {
+          if (part >= 2 && !mbar_wait(&q_empty[part & 1], ((part >> 1) - 1) & 1, ab, kDevTimeoutLoad)) go = 0;
+          else mbar_arrive_expect_tx(&q_full[part & 1], C::QTILE);
+        }
+        if (!__shfl_sync(0xffffffffu, go, 0)) break;
+        if (lane < C::CH)
+          tma_load_3d(sQ + (part & 1) * C::QTILE + lane * C::QCHUNK, &tmQ, &q_full[part & 1], lane * 64,
+                      hk * kp.rows + (cur.y - hk * kp.qtiles) * BM, cur.b);
+        ++part;
+      }
+      for (int i = 0; i < take; ++i, ++n) {
+        const int item = 2 * n + kv;
+        const int slot = item % NSLOT, use = item / NSLOT;
+        int go = 1;
+        if (lane == 0) {
+          if (use >= 1 && !mbar_wait(&kv_empty[slot], (use - 1) & 1, ab, kDevTimeoutLoad)) go = 0;
+          else mbar_arrive_expect_tx(&kv_full[slot], C::TILE);
+        }
+        if (!__shfl_sync(0xffffffffu, go, 0)) {
+          ok = false;
+          break;
+        }
+        if (lane < C::CH)
+          tma_load_4d(sKV + slot * C::TILE + lane * C::CHUNK, kv ? &tmV : &tmK, &kv_full[slot], lane * 64,
+                      (cur.j + i) * BN, hk, cur.b);
+      }
+      cur.next_part(take);
+    }
+    if (lane == 0) {
+      issued_sh[kv] = n;
+      if (kv == 0) parts_sh = part;
+    }
+  } else if (warp == C::MMA_WARP) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0 && total > 0) {
+      constexpr Elt E = FP16 ? Elt::F16 : Elt::BF16;
+      constexpr uint32_t idS = idesc_f16(E, 128, BN, false, false);
+      constexpr uint32_t idPV = idesc_f16(E, 128, D, false, true);
+      const uint64_t qdesc0 = sdesc_sw128(smem_u32(sQ), 16, 1024);             // K-major Q
+      const uint64_t kdesc0 = sdesc_sw128(smem_u32(sKV), 16, 1024);            // K-major K
+      const uint64_t vdesc0 = sdesc_sw128(smem_u32(sKV), C::CHUNK, 1024);      // MN-major V
+      // cursors of the score products (two tiles ahead) and of the P V products
+      Cursor ahead = cur;
+      int s_part = 0, s_left = ahead.part(), s_n = 0, s_take = s_left;
+      bool s_first = true;
+      // S(n) = Q K_n^T into buffer n % 2, n = s_n
+      auto issue_s = [&]() -> bool {
+        if (s_first && !mbar_wait(&q_full[s_part & 1], (s_part >> 1) & 1, ab, kDevTimeoutMma)) return false;
+        s_first = false;
+        const int item = 2 * s_n, slot = item % NSLOT;
+        if (!mbar_wait(&kv_full[slot], (item / NSLOT) & 1, ab, kDevTimeoutMma)) return false;
+        tc_fence_after_sync();
+        const uint64_t qdesc = opaque(sdesc_add(qdesc0, (s_part & 1) * C::QTILE));
+        const uint64_t kdesc = opaque(sdesc_add(kdesc0, slot * C::TILE));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          mma_f16_ss(tmem + C::S_COL(s_n & 1), sdesc_add(qdesc, (kk / 4) * C::QCHUNK + (kk % 4) * 32),
+                     sdesc_add(kdesc, (kk / 4) * C::CHUNK + (kk % 4) * 32), idS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&s_full[s_n & 1]);
+        if (item + NSLOT < 2 * total) mma_commit(&kv_empty[slot]);
+        ++s_n;
+        if (--s_left == 0) {
+          mma_commit(&q_empty[s_part & 1]);      // the part's Q has been read
+          ahead.next_part(s_take);
+          ++s_part;
+          s_first = true;
+          if (ahead.left > 0) s_left = s_take = ahead.part();
+        }
+        return true;
+      };
+      bool ok = issue_s();
+      if (ok && total > 1) ok = issue_s();
+      int part = 0;
+      for (int n = 0; n < total && ok; ++part) {
+        const int take = cur.part();
+        const uint32_t o_col = C::O_COL(part & 1);
+        for (int i = 0; i < take && ok; ++i, ++n) {
+          // O += P(n) V_n, P(n) packed 16-bit in columns [0, 64) of buffer n % 2
+          const int item = 2 * n + 1, slot = item % NSLOT;
+          if (!(ok = mbar_wait(&kv_full[slot], (item / NSLOT) & 1, ab, kDevTimeoutMma))) break;
+          const uint64_t vdesc = opaque(sdesc_add(vdesc0, slot * C::TILE));
+          if (!(ok = mbar_wait(&p_full[n & 1], (n >> 1) & 1, ab, kDevTimeoutMma))) break;
+          // the buffer's output of two parts ago has been read
+          if (i == 0 && part >= 2 &&
+              !(ok = mbar_wait(&o_empty[part & 1], ((part >> 1) - 1) & 1, ab, kDevTimeoutMma)))
+            break;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_f16_ts(tmem + o_col, tmem + C::S_COL(n & 1) + 8 * kk, sdesc_add(vdesc, kk * 16 * 128), idPV,
+                       (i > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&pv_done);
+          if (item + NSLOT < 2 * total) mma_commit(&kv_empty[slot]);
+          if (i == take - 1) mma_commit(&o_full[part & 1]);
+          if (n + 2 < total) ok = issue_s();
+        }
+        cur.next_part(take);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int r = warp * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
+    const float c2 = kp.scale_log2;
+    bool ok = true;
+    // output of a finished part: where it goes, and its row's statistics
+    struct Done {
+      int part, b, y;
+      bool whole, last;
+      float m, l;
+    } done{-1, 0, 0, false, false, 0.f, 0.f};
+    auto write_out = [&]() -> bool {
+      const int buf = done.part & 1;
+      if (__any_sync(0xffffffffu, !mbar_wait(&o_full[buf], (done.part >> 1) & 1, ab, kDevTimeoutEpilogue)))
+        return false;
+      tc_fence_after_sync();
+      const int hk = done.y / kp.qtiles;
+      const int row = (done.y - hk * kp.qtiles) * BM + r;     // of the head's G * N_q rows
+      const bool row_ok = row < kp.rows;
+      // rows of a key/value head are contiguous in [B, H, N_q]
+      const size_t at = (static_cast<size_t>(done.b) * kp.H_kv + hk) * kp.rows + row;
+      const int slot = 2 * blockIdx.x + (done.last ? 1 : 0);
+      const float inv_l = 1.f / done.l;
+#pragma unroll 1
+      for (int c0 = 0; c0 < D / 32; ++c0) {
+        uint32_t o[32];
+        tmem_ld32(tmem + lane_addr + C::O_COL(buf) + c0 * 32, o);
+        tmem_ld_wait();
+        if (!row_ok) continue;
+        if (done.whole) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kp.o) + at * D + c0 * 32);
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float x = __uint_as_float(o[2 * i]) * inv_l, z = __uint_as_float(o[2 * i + 1]) * inv_l;
+            pk[i] = FP16 ? cvt_pack_f16(x, z) : cvt_pack_bf16(x, z);
+          }
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+        } else {
+          float4* dst = reinterpret_cast<float4*>(
+              kp.o_part + (static_cast<size_t>(slot) * kp.seg_rows + r) * D + c0 * 32);
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
+                                 __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
+        }
+      }
+      if (row_ok) {
+        float* dst = done.whole ? kp.lse + at : kp.lse_part + static_cast<size_t>(slot) * kp.seg_rows + r;
+        *dst = (done.m * c2 + lg2f_approx(done.l)) * 0.69314718055994530942f;
+      }
+      tc_fence_before_sync();
+      mbar_arrive(&o_empty[buf]);
+      return true;
+    };
+    int n = 0, part = 0;
+    while (ok && cur.left > 0) {
+      const int take = cur.part();
+      const int len = keys_of(kp.kv_lens, cur.b, kp.Nk);
+      float m_ref = -INFINITY, l = 0.f;
+      // a warp without query rows only keeps the others' pace
+      const bool live = (cur.y % kp.qtiles) * BM + warp * 32 < kp.rows;
+      for (int i = 0; i < take; ++i, ++n) {
+        if (__any_sync(0xffffffffu, !mbar_wait(&s_full[n & 1], (n >> 1) & 1, ab, kDevTimeoutSoftmax))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const int lim = len - (cur.j + i) * BN;        // keys of this tile that are seen
+        if (live) {
+        const uint32_t tS = tmem + lane_addr + C::S_COL(n & 1);
+        uint32_t sr[BN];
+#pragma unroll
+        for (int c0 = 0; c0 < BN / 32; ++c0)
+          tmem_ld32(tS + c0 * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0 * 32]));
+        tmem_ld_wait();
+        if (lim < BN) {
+#pragma unroll
+          for (int c = 0; c < BN; ++c)
+            if (c >= lim) sr[c] = __float_as_uint(-INFINITY);
+        }
+        float mx[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+          mx[u] = fmax3(__uint_as_float(sr[8 * u]), __uint_as_float(sr[8 * u + 1]),
+                        fmax3(__uint_as_float(sr[8 * u + 2]), __uint_as_float(sr[8 * u + 3]),
+                              fmax3(__uint_as_float(sr[8 * u + 4]), __uint_as_float(sr[8 * u + 5]),
+                                    fmaxf(__uint_as_float(sr[8 * u + 6]), __uint_as_float(sr[8 * u + 7])))));
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mx[u] = fmaxf(mx[u], mx[u + 8]);
+        const float m_new = fmaxf(m_ref, fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
+                                               fmaxf(mx[6], mx[7])));
+        // lazy rescale: the exponent reference moves when the maximum grew by over 2^8
+        const bool need = (m_new - m_ref) * c2 > 8.f;
+        float alpha = 1.f;
+        if (need) {
+          alpha = ex2_approx((m_ref - m_new) * c2);
+          l *= alpha;
+          m_ref = m_new;
+        }
+        const float neg = (m_ref == -INFINITY) ? 0.f : -m_ref * c2;
+        const uint64_t cc = pack2(c2, c2);
+        const uint64_t nn = pack2(neg, neg);
+        uint64_t acc0 = 0, acc1 = 0;
+#pragma unroll
+        for (int c0 = 0; c0 < BN / 32; ++c0) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int c = c0 * 32 + 2 * e;
+            const uint64_t y = ffma2(pack2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), cc, nn);
+            const float p0 = ex2_approx(lo2(y));
+            const float p1 = ex2_approx(hi2(y));
+            if (e & 1) acc1 = fadd2(acc1, pack2(p0, p1));
+            else acc0 = fadd2(acc0, pack2(p0, p1));
+            pk[e] = FP16 ? cvt_pack_f16(p0, p1) : cvt_pack_bf16(p0, p1);
+          }
+          // packed P of keys [32 c0, +32) -> columns [16 c0, +16)
+          tmem_st16(tS + c0 * 16, pk);
+        }
+        const uint64_t acc = fadd2(acc0, acc1);
+        l += lo2(acc) + hi2(acc);
+        if (i > 0 && __any_sync(0xffffffffu, need)) {
+          // rescale O once P(n - 1) V has landed; this tile's product is issued
+          // only after the arrive below
+          if (__any_sync(0xffffffffu, !mbar_wait(&pv_done, (n - 1) & 1, ab, kDevTimeoutSoftmax))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t tO = tmem + lane_addr + C::O_COL(part & 1);
+#pragma unroll 1
+          for (int c0 = 0; c0 < D / 32; ++c0) {
+            uint32_t o[32];
+            tmem_ld32(tO + c0 * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(tO + c0 * 32, o);
+          }
+        }
+        }
+        if (lim < BN && len < kp.Nk) {
+          // rows of V behind the keys may hold anything: they meet P = 0 in the
+          // product, so they are zeroed first (0 * NaN = NaN)
+          const int item = 2 * n + 1;
+          if (__any_sync(0xffffffffu, !mbar_wait(&kv_full[item % NSLOT], (item / NSLOT) & 1, ab,
+                                                 kDevTimeoutSoftmax))) {
+            ok = false;
+            break;
+          }
+          zero_tile_rows<C::CH, C::CHUNK>(sKV + (item % NSLOT) * C::TILE, lim, r, 128);
+          fence_proxy_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(&p_full[n & 1]);
+        // the part before this one, while this tile's products run
+        if (i == 0 && part > 0 && !write_out()) {
+          ok = false;
+          break;
+        }
+      }
+      if (!ok) break;
+      done = Done{part, cur.b, cur.y, take == cur.tiles(), part > 0, m_ref, l};
+      cur.next_part(take);
+      ++part;
+    }
+    if (ok && part > 0) write_out();
+    // batch entries without keys: O = 0 and LSE = -inf
+    const size_t rows_b = static_cast<size_t>(kp.H_kv) * kp.rows;
+    for (int b = blockIdx.x; b < kp.B; b += gridDim.x) {
+      if (pre[b + 1] != pre[b]) continue;
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kp.o) + b * rows_b * D);
+      for (size_t i = r; i < rows_b * (D / 8); i += 128) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (size_t i = r; i < rows_b; i += 128) kp.lse[b * rows_b + i] = -INFINITY;
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before_sync();
+  __syncthreads();
+  if (abort_sh) {
+    // let every copy and MMA this CTA issued land before the memory goes away
+    if ((warp == C::LOAD_WARP || warp == C::LOAD_V_WARP) && lane == 0) {
+      const int kv = warp == C::LOAD_WARP ? 0 : 1;
+      for (int i = issued_sh[kv] - 1; i >= 0 && 2 * i + kv >= 2 * issued_sh[kv] - 2 * NSLOT; --i) {
+        const int item = 2 * i + kv;
+        mbar_wait_drain(&kv_full[item % NSLOT], (item / NSLOT) & 1);
+      }
+      if (kv == 0)
+        for (int i = parts_sh - 1; i >= 0 && i >= parts_sh - 2; --i) mbar_wait_drain(&q_full[i & 1], (i >> 1) & 1);
+    }
+    if (warp == C::MMA_WARP && lane == 0) {
+      mma_commit(&drain_bar);
+      mbar_wait_drain(&drain_bar, 0);
+    }
+    __syncthreads();
+  }
+  if (warp == C::MMA_WARP) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Segments that cross shares: LSE = log sum_c exp(lse_c) and O = sum_c exp(lse_c -
+// LSE) O_c over the CTAs whose shares they touch.  One block per segment.
+template <int D, bool FP16>
+__global__ void __launch_bounds__(128)
+    cross_merge_kernel(const CrossKParams kp, int C) {
+  __shared__ int sums[2][4];
+  const int b = blockIdx.y, y = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // tiles of a segment of the entries before b, and of all
+  int before = 0, all = 0;
+  for (int i = threadIdx.x; i < kp.B; i += 128) {
+    const int n = (keys_of(kp.kv_lens, i, kp.Nk) + BN - 1) / BN;
+    all += n;
+    if (i < b) before += n;
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  all = __reduce_add_sync(0xffffffffu, all);
+  if (lane == 0) {
+    sums[0][warp] = before;
+    sums[1][warp] = all;
+  }
+  __syncthreads();
+  before = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3];
+  const int T = (sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3]) * kp.segs;
+  const int nt = (keys_of(kp.kv_lens, b, kp.Nk) + BN - 1) / BN;
+  // every block waits: one that returned before the first kernel's end could let the
+  // stream's next kernel start too early
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (nt == 0) return;
+  const int g0 = before * kp.segs + y * nt, g1 = g0 + nt - 1;
+  // CTA whose share holds tile g: the last c with c T / C <= g
+  C = min(C, T);
+  const int c0 = static_cast<int>(((g0 + 1ll) * C - 1) / T), c1 = static_cast<int>(((g1 + 1ll) * C - 1) / T);
+  if (c0 == c1) return;
+  // a share's first part is its slot 0, a later one its slot 1; the segment is a
+  // later part only where it starts inside a share
+  const int slot0 = 2 * c0 + (share_start(c0, C, T) == g0 ? 0 : 1);
+  const int hk = y / kp.qtiles;
+  const int row0 = (y - hk * kp.qtiles) * BM;
+  const int rows = min(BM, kp.rows - row0);
+  constexpr int PER = 4;                             // columns per thread
+  constexpr int TPR = D / PER;                       // threads per row
+  for (int r = threadIdx.x / TPR; r < rows; r += 128 / TPR) {
+    const int col = (threadIdx.x % TPR) * PER;
+    float mx = -INFINITY;
+    for (int c = c0; c <= c1; ++c)
+      mx = fmaxf(mx, kp.lse_part[static_cast<size_t>(c == c0 ? slot0 : 2 * c) * kp.seg_rows + r]);
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; ++c) {
+      const size_t at = static_cast<size_t>(c == c0 ? slot0 : 2 * c) * kp.seg_rows + r;
+      const float w = expf(kp.lse_part[at] - mx);
+      const float4 o = *reinterpret_cast<const float4*>(kp.o_part + at * D + col);
+      sum += w;
+      acc.x = fmaf(w, o.x, acc.x);
+      acc.y = fmaf(w, o.y, acc.y);
+      acc.z = fmaf(w, o.z, acc.z);
+      acc.w = fmaf(w, o.w, acc.w);
+    }
+    const float inv = 1.f / sum;
+    const size_t at = (static_cast<size_t>(b) * kp.H_kv + hk) * kp.rows + row0 + r;
+    const uint2 pk = FP16 ? make_uint2(cvt_pack_f16(acc.x * inv, acc.y * inv), cvt_pack_f16(acc.z * inv, acc.w * inv))
+                          : make_uint2(cvt_pack_bf16(acc.x * inv, acc.y * inv), cvt_pack_bf16(acc.z * inv, acc.w * inv));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(kp.o) + at * D + col) = pk;
+    if (col == 0) kp.lse[at] = mx + logf(sum);
+  }
+}
+
+template <int D, bool FP16, int QROWS>
+attn_status_t launch_cross_rows_t(const FwdParams& p, const CrossPlan& plan, void* workspace,
+                                  cudaStream_t stream) {
+  using C = CrossCfg<D, QROWS>;
+  auto kern = cross_rows_kernel<D, FP16, QROWS>;
+  attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), C::SMEM);
+  if (s != ATTN_OK) return s;
+  CUtensorMap tq, tk, tv;
+  // Q: {d, H * N_q rows, B}; K, V: {d, N_k, H_kv, B}
+  if ((s = make_tmap_3d(&tq, p.q, 2, D, static_cast<uint64_t>(p.H) * p.N, p.B, 64, QROWS)) != ATTN_OK) return s;
+  const uint64_t row_b = 2ull * D, head_b = row_b * p.N_k, batch_b = head_b * p.H_kv;
+  if ((s = make_tmap_4d(&tk, p.k, 2, D, p.N_k, p.H_kv, p.B, row_b, head_b, batch_b, 64, BN)) != ATTN_OK) return s;
+  if ((s = make_tmap_4d(&tv, p.v, 2, D, p.N_k, p.H_kv, p.B, row_b, head_b, batch_b, 64, BN)) != ATTN_OK) return s;
+  int* status = device_status_word();
+  if (!status) return fail(ATTN_ERR_CUDA, "status word unavailable");
+  const int rows = p.H / p.H_kv * p.N;
+  const int seg_rows = rows < BM ? rows : BM;
+  const size_t part_rows = 2ull * plan.ctas * seg_rows;
+  char* ws = static_cast<char*>(workspace);
+  CrossKParams kp{p.kv_lens, p.o, p.lse, reinterpret_cast<float*>(ws),
+                  reinterpret_cast<float*>(ws + align_up(part_rows * D * sizeof(float), 256)), status,
+                  p.B, p.H_kv, p.N_k, rows, p.H_kv * plan.qtiles, plan.qtiles, seg_rows,
+                  p.scale * 1.4426950408889634f};
+  kern<<<plan.ctas, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, kp);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail_cuda(e, "cross attention rows kernel launch");
+  // launched while the first kernel runs; it waits for its end before reading
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kp.segs, p.B);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, cross_merge_kernel<D, FP16>, kp, plan.ctas);
+  if (e != cudaSuccess) return fail_cuda(e, "cross attention merge kernel launch");
+  return ATTN_OK;
+}
+
+}  // namespace
+
+attn_status_t launch_cross_rows(const FwdParams& p, const CrossPlan& plan, void* workspace,
+                                cudaStream_t stream) {
+  const bool few = p.H / p.H_kv * p.N <= 16;
+#define ATTN_CROSS_ROWS(D, F)                                                   \
+  return few ? launch_cross_rows_t<D, F, 16>(p, plan, workspace, stream)        \
+             : launch_cross_rows_t<D, F, 128>(p, plan, workspace, stream)
+  if (p.d == 64) {
+    if (p.fp16) ATTN_CROSS_ROWS(64, true);
+    ATTN_CROSS_ROWS(64, false);
+  }
+  if (p.fp16) ATTN_CROSS_ROWS(128, true);
+  ATTN_CROSS_ROWS(128, false);
+#undef ATTN_CROSS_ROWS
+}
+
+}  // namespace attn

@@ -77,11 +77,6 @@ struct DecKParams {
   const float* v_descale;
   const float* signs;       // d values +-1 of the key transform, or nullptr
   int H_kv, page_shift;
-  // cross attention only: key/value rows of every batch entry, query tiles per
-  // key/value head, and the outputs (written directly when there is one split)
-  int Nk, qtiles;
-  uint16_t* o;
-  float* lse;
 };
 
 __device__ __forceinline__ float lg2_dec(float x) {
@@ -106,9 +101,7 @@ __device__ __forceinline__ float lg2_dec(float x) {
 // holding other data, released through their empty barrier like a used slot.
 // load_items[kv] receives the item count the warp reached (its own items are
 // those of parity kv below it).
-// CONTIG: keys and values [B, H_kv, Nk, d] instead of pages: "page" b of
-// page_size 2^30 for every box of 128 rows.
-template <int NSLOT, int CH, int CHUNK, int TILE, int SHIFT, bool CONTIG = false>
+template <int NSLOT, int CH, int CHUNK, int TILE, int SHIFT>
 __device__ __forceinline__ void decode_produce(const CUtensorMap* tmK, const CUtensorMap* tmV,
                                                uint8_t* sKV, uint64_t* kv_full, uint64_t* kv_empty,
                                                const DecKParams& kp, const int* table, int j0,
@@ -124,7 +117,6 @@ __device__ __forceinline__ void decode_produce(const CUtensorMap* tmK, const CUt
   // raw table entry of box 32 w + lane (checked when its window comes into use)
   auto load_window = [&](int w) -> int {
     if (!in_seq(w)) return kp.num_pages;
-    if constexpr (CONTIG) return static_cast<int>(blockIdx.z);
     return __ldg(table + (((j0 * nbox + w * 32 + lane) * kp.box_rows) >> kp.page_shift));
   };
   // physical page of box 32 w + lane: num_pages (a zero-filled box) past the
@@ -196,11 +188,7 @@ __device__ __forceinline__ void decode_drain_items(uint64_t* kv_full, int issued
     if ((i & 1) == kv_own) mbar_wait_drain(&kv_full[(i + SHIFT) % NSLOT], parity(i));
 }
 
-// CROSS: cross attention of a few query rows.  Keys and values are contiguous
-// [B, H_kv, Nk, d], batch entry b sees the first kv_lens (seq_lens) of them or
-// all, and the G * n_q query rows of a key/value head, which are contiguous,
-// take any number of 128-row tiles (blockIdx.y = key/value head x tile).
-template <int D, bool FP16, bool CROSS = false>
+template <int D, bool FP16>
 __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
     decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ CUtensorMap tmK,
@@ -228,35 +216,22 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
   const int split = blockIdx.x;
-  const int hk = CROSS ? static_cast<int>(blockIdx.y) / kp.qtiles : static_cast<int>(blockIdx.y);
-  const int row0 = CROSS ? (static_cast<int>(blockIdx.y) - hk * kp.qtiles) * DBM : 0;   // tile's first row
+  const int hk = blockIdx.y;
   const int b = blockIdx.z;
-  int len = CROSS && !kp.seq_lens ? kp.Nk : kp.seq_lens[b];
-  if (len < 0 || (CROSS ? len > kp.Nk : len > kp.max_pages * kp.page_size)) {
+  const int len = kp.seq_lens[b];
+  if (len < 0 || len > kp.max_pages * kp.page_size) {
     if (threadIdx.x == 0) atomicCAS(kp.status, 0, kDevBadSeqlens);
-    if (!CROSS) return;
-    len = 0;
+    return;
   }
   const int ntiles = (len + DBN - 1) / DBN;
   const int j0 = split * kp.tiles_per_split;
   const int nK = max(0, min(ntiles, j0 + kp.tiles_per_split) - j0);
   const int r = warp * 32 + lane;             // query-tile row of a softmax thread
   const int gq = r / kp.n_q, tq = r - gq * kp.n_q;
-  const size_t prow = CROSS ? (static_cast<size_t>(b) * kp.H + hk * kp.group) * kp.n_q + row0 + r
-                            : (static_cast<size_t>(b) * kp.H + hk * kp.group + gq) * kp.n_q + tq;
-  const bool row_ok = row0 + r < kp.rows_real;
+  const size_t prow = (static_cast<size_t>(b) * kp.H + hk * kp.group + gq) * kp.n_q + tq;
   if (nK == 0) {
     // no keys in this split: it contributes nothing to the merge
-    if (warp < 4 && row_ok) {
-      if (CROSS && kp.splits == 1) {
-        uint4* dst = reinterpret_cast<uint4*>(kp.o + prow * D);
-#pragma unroll
-        for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0u, 0u, 0u, 0u);
-        kp.lse[prow] = -INFINITY;
-      } else {
-        kp.lse_part[prow * kp.splits + split] = -INFINITY;
-      }
-    }
+    if (warp < 4 && r < kp.rows_real) kp.lse_part[prow * kp.splits + split] = -INFINITY;
     return;
   }
   const int total_items = 2 * nK;              // K_0, V_0, K_1, V_1, ... of this split
@@ -298,9 +273,9 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
       mbar_arrive_expect_tx(&q_full, C::TILE);
 #pragma unroll
       for (int c = 0; c < C::CH; ++c)
-        tma_load_3d(sQ + c * C::CHUNK, &tmQ, &q_full, c * 64, hk * kp.group * kp.n_q + row0, b);
+        tma_load_3d(sQ + c * C::CHUNK, &tmQ, &q_full, c * 64, hk * kp.group * kp.n_q, b);
     }
-    decode_produce<NSLOT, C::CH, C::CHUNK, C::TILE, 0, CROSS>(
+    decode_produce<NSLOT, C::CH, C::CHUNK, C::TILE, 0>(
         &tmK, &tmV, sKV, kv_full, kv_empty, kp, kp.block_table + static_cast<size_t>(b) * kp.max_pages,
         j0, nK, len, hk, lane, ab, kv_own, load_items_sh);
   } else if (warp == C::MMA_WARP) {
@@ -356,7 +331,7 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
     const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
     const float c2 = kp.scale_log2;
     // keys this row may see: all of the sequence, or (causal) up to its position
-    const int vis_end = !CROSS && kp.causal ? min(len, len - kp.n_q + tq + 1) : len;
+    const int vis_end = kp.causal ? min(len, len - kp.n_q + tq + 1) : len;
     float m_ref = -INFINITY;
     float l = 0.f;
     bool ok = true;
@@ -440,20 +415,6 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
           tmem_st32(tmem + lane_addr + C::O_COL + c0 * 32, o);
         }
       }
-      if constexpr (CROSS) {
-        // rows of V behind the keys may hold anything: they meet P = 0 in the
-        // product, so they are zeroed first (0 * NaN = NaN)
-        if (len < kp.Nk && kbase + DBN > len) {
-          const int item = 2 * j + 1;
-          if (__any_sync(0xffffffffu, !mbar_wait(&kv_full[item % NSLOT], (item / NSLOT) & 1, ab,
-                                                 kDevTimeoutSoftmax))) {
-            ok = false;
-            break;
-          }
-          zero_tile_rows<C::CH, C::CHUNK>(sKV + (item % NSLOT) * C::TILE, len - kbase, r, 128);
-          fence_proxy_async_smem();
-        }
-      }
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(&p_full[j & 1]);
@@ -468,20 +429,7 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
         uint32_t o[32];
         tmem_ld32(tmem + lane_addr + C::O_COL + c0 * 32, o);
         tmem_ld_wait();
-        if (CROSS && kp.splits == 1) {
-          if (row_ok) {
-            uint4* d4 = reinterpret_cast<uint4*>(kp.o + prow * D + c0 * 32);
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float a = __uint_as_float(o[2 * i]) * inv_l, c = __uint_as_float(o[2 * i + 1]) * inv_l;
-              pk[i] = FP16 ? cvt_pack_f16(a, c) : cvt_pack_bf16(a, c);
-            }
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              d4[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
-          }
-        } else if (row_ok) {
+        if (r < kp.rows_real) {
           float4* d4 = reinterpret_cast<float4*>(dst + c0 * 32);
 #pragma unroll
           for (int v = 0; v < 8; ++v)
@@ -489,10 +437,9 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
                                 __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
         }
       }
-      if (row_ok) {
-        float* out = CROSS && kp.splits == 1 ? kp.lse + prow : kp.lse_part + prow * kp.splits + split;
-        *out = l > 0.f ? (m_ref * c2 + lg2_dec(l)) * 0.69314718055994530942f : -INFINITY;
-      }
+      if (r < kp.rows_real)
+        kp.lse_part[prow * kp.splits + split] =
+            l > 0.f ? (m_ref * c2 + lg2_dec(l)) * 0.69314718055994530942f : -INFINITY;
     }
   }
 
@@ -1654,55 +1601,7 @@ attn_status_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
   return ATTN_OK;
 }
 
-// Cross attention of few query rows: the key range split over CTAs, joined by
-// the combine kernel when there is more than one split.
-template <int D, bool FP16>
-attn_status_t launch_cross_split_t(const FwdParams& p, const CrossPlan& plan, void* workspace,
-                                   cudaStream_t stream) {
-  using C = DecCfg<D>;
-  auto kern = decode_split_kernel<D, FP16, true>;
-  attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), C::SMEM);
-  if (s != ATTN_OK) return s;
-  CUtensorMap tq, tk, tv;
-  const int group = p.H / p.H_kv;
-  const long long rows = static_cast<long long>(p.B) * p.H * p.N;
-  if ((s = make_tmap_3d(&tq, p.q, 2, D, static_cast<uint64_t>(p.H) * p.N, p.B, 64, DBM)) != ATTN_OK) return s;
-  const uint64_t row_b = 2ull * D, head_b = row_b * p.N_k, batch_b = head_b * p.H_kv;
-  if ((s = make_tmap_4d(&tk, p.k, 2, D, p.N_k, p.H_kv, p.B, row_b, head_b, batch_b, 64, DBN)) != ATTN_OK) return s;
-  if ((s = make_tmap_4d(&tv, p.v, 2, D, p.N_k, p.H_kv, p.B, row_b, head_b, batch_b, 64, DBN)) != ATTN_OK) return s;
-  int* status = device_status_word();
-  if (!status) return fail(ATTN_ERR_CUDA, "status word unavailable");
-  char* ws = static_cast<char*>(workspace);
-  float* o_part = reinterpret_cast<float*>(ws);
-  float* lse_part = reinterpret_cast<float*>(
-      ws + align_up(static_cast<size_t>(rows) * plan.splits * D * sizeof(float), 256));
-  DecKParams kp{nullptr, p.kv_lens, o_part, lse_part, status,
-                p.H, group, p.N, group * p.N,
-                1, 1 << 30, DBN, p.B,
-                plan.splits, plan.tiles_per_split, 0, p.scale * 1.4426950408889634f,
-                nullptr, nullptr, nullptr, p.H_kv, 30,
-                p.N_k, plan.qtiles, static_cast<uint16_t*>(p.o), p.lse};
-  kern<<<dim3(plan.splits, p.H_kv * plan.qtiles, p.B), C::THREADS, C::SMEM, stream>>>(tq, tk, tv, kp);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail_cuda(e, "cross attention split kernel launch");
-  if (plan.splits == 1) return ATTN_OK;
-  decode_combine_kernel<D, FP16><<<static_cast<unsigned>((rows * 32 + 255) / 256), 256, 0, stream>>>(
-      o_part, lse_part, static_cast<uint16_t*>(p.o), p.lse, rows, plan.splits);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return fail_cuda(e, "cross attention combine kernel launch");
-  return ATTN_OK;
-}
-
 }  // namespace
-
-attn_status_t launch_cross_split(const FwdParams& p, const CrossPlan& plan, void* workspace,
-                                 cudaStream_t stream) {
-  if (p.d == 64)
-    return p.fp16 ? launch_cross_split_t<64, true>(p, plan, workspace, stream)
-                  : launch_cross_split_t<64, false>(p, plan, workspace, stream);
-  return p.fp16 ? launch_cross_split_t<128, true>(p, plan, workspace, stream)
-                : launch_cross_split_t<128, false>(p, plan, workspace, stream);
-}
 
 attn_status_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
   if (p.B > 65535 || p.H_kv > 65535) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
