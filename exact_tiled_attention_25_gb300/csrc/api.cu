@@ -193,12 +193,12 @@ attn_status_t make_tmap_3d(CUtensorMap* map, const void* base, int elem_bytes, u
 attn_status_t make_tmap_4d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t inner,
                            uint64_t rows, uint64_t heads, uint64_t batches, uint64_t row_bytes,
                            uint64_t head_bytes, uint64_t batch_bytes, uint32_t box_inner,
-                           uint32_t box_rows) {
+                           uint32_t box_rows, uint32_t box_heads) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   cuuint64_t dims[4] = {inner, rows, heads, batches};
   cuuint64_t strides[3] = {row_bytes, head_bytes, batch_bytes};
-  cuuint32_t box[4] = {box_inner, box_rows, 1, 1};
+  cuuint32_t box[4] = {box_inner, box_rows, box_heads, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUtensorMapDataType dt = elem_bytes == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                            : elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16

@@ -31,12 +31,12 @@ attn_status_t make_tmap_3d(CUtensorMap* map, const void* base, int elem_bytes, u
                            uint32_t box_rows);
 
 // 4-D map over {d, rows, heads, batches} with byte strides for rows, heads and
-// batches (each a multiple of 16); box {box_inner, box_rows, 1, 1}, 128-byte
-// swizzle.  Covers [B, H, N, d] and packed [total, H, d] alike.
+// batches (each a multiple of 16); box {box_inner, box_rows, box_heads, 1},
+// 128-byte swizzle.  Covers [B, H, N, d] and packed [total, H, d] alike.
 attn_status_t make_tmap_4d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t inner,
                            uint64_t rows, uint64_t heads, uint64_t batches, uint64_t row_bytes,
                            uint64_t head_bytes, uint64_t batch_bytes, uint32_t box_inner,
-                           uint32_t box_rows);
+                           uint32_t box_rows, uint32_t box_heads = 1);
 
 // Opt a kernel into more than 48 KB of dynamic shared memory (once per kernel).
 attn_status_t set_smem(const void* kernel, int bytes);

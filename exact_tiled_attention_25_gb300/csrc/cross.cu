@@ -31,21 +31,31 @@ constexpr int kSmemLimit = 232448;
 constexpr int BM = 128;   // query rows of a tile
 constexpr int BN = 128;   // keys of a tile
 
-// QROWS: rows of Q held in shared memory, 16 or 128.  The score product always
-// reads 128; behind 16 it meets ring memory, whose garbage stays in its own rows of
-// S, P and O, which nothing reads.  At d = 128 two full Q tiles would leave a ring
-// of four tiles, 16 rows leave six.
-template <int D, int QROWS>
+// FEW: at most 16 query rows.  They are laid into the query tile four times, at rows
+// 0, 32, 64 and 96, so every softmax warp finds them in its own quarter of tensor
+// memory; warp w takes keys [32 w, 32 w + 32) of each tile, with statistics of its
+// own and zeros as its probabilities of the other keys, and the four partial outputs
+// are added when a part ends.  (One warp with all 128 keys of a tile needs some
+// 1400 cycles a tile, most of them exponentials: at d = 64 that is more than the
+// tile's share of HBM time, 5.0 TB/s.)  The gaps behind the four copies hold the
+// other Q buffer's four.
+// Otherwise: 128 query rows, a thread per row.
+template <int D, bool FEW>
 struct CrossCfg {
   static constexpr int CH = D / 64;
   static constexpr int CHUNK = 128 * 128;
   static constexpr int TILE = 128 * D * 2;
-  static constexpr int QCHUNK = QROWS * 128;
-  static constexpr int QTILE = QROWS * D * 2;
+  static constexpr int QROWS = FEW ? 16 : 128;           // rows of a copy's box
+  static constexpr int COPIES = FEW ? 4 : 1;
+  static constexpr int QBYTES = COPIES * QROWS * D * 2;  // copied per part
+  static constexpr int QSTEP = FEW ? QROWS * 128 : TILE; // from one Q buffer to the other
+  static constexpr int QSMEM = FEW ? TILE : 2 * TILE;
+  static constexpr int XCH = FEW ? 4 * 16 * 65 * 4 + 4 * 16 * 8 : 0;   // the sum of the four outputs
   static constexpr int LENS = 4 * (kCrossMaxB + 1);      // tile prefix sums
-  static constexpr int NSLOT_FIT = (kSmemLimit - 2048 - LENS - 2 * QTILE) / TILE;
+  static constexpr int NSLOT_FIT = (kSmemLimit - 2048 - LENS - XCH - QSMEM) / TILE;
   static constexpr int NSLOT = NSLOT_FIT > 10 ? 10 : NSLOT_FIT;
-  static constexpr int SMEM = 1024 + 2 * QTILE + NSLOT * TILE;   // two Q tiles and the ring
+  // a product reads 128 rows from its Q buffer: the second one's end in the ring
+  static constexpr int SMEM = 1024 + QSMEM + NSLOT * TILE;
   static constexpr int THREADS = 7 * 32;
   static constexpr int LOAD_WARP = 4;
   static constexpr int MMA_WARP = 5;
@@ -53,7 +63,6 @@ struct CrossCfg {
   __host__ __device__ static constexpr uint32_t S_COL(int buf) { return 128u * buf; }
   __host__ __device__ static constexpr uint32_t O_COL(int buf) { return 256u + static_cast<uint32_t>(D) * buf; }
   static_assert(NSLOT >= 4 && O_COL(1) + D <= 512, "ring or tensor memory");
-  static_assert(QCHUNK % 1024 == 0, "swizzle atoms");
 };
 
 struct CrossKParams {
@@ -130,17 +139,17 @@ __device__ __forceinline__ Cursor cursor_at(const int* pre, int segs, int B, int
   return c;
 }
 
-template <int D, bool FP16, int QROWS>
-__global__ void __launch_bounds__(CrossCfg<D, QROWS>::THREADS, 1)
+template <int D, bool FP16, bool FEW>
+__global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
     cross_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const CrossKParams kp) {
-  using C = CrossCfg<D, QROWS>;
+  using C = CrossCfg<D, FEW>;
   constexpr int NSLOT = C::NSLOT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;
-  uint8_t* sKV = smem + 2 * C::QTILE;
+  uint8_t* sKV = smem + C::QSMEM;
 
   __shared__ __align__(8) uint64_t q_full[2];
   __shared__ __align__(8) uint64_t q_empty[2];
@@ -158,6 +167,9 @@ __global__ void __launch_bounds__(CrossCfg<D, QROWS>::THREADS, 1)
   __shared__ int parts_sh;          // Q tiles issued
   __shared__ int warp_sum[C::THREADS / 32];
   __shared__ int pre[kCrossMaxB + 1];
+  __shared__ float xch[FEW ? 4 : 1][16][65];       // 64 columns of the four outputs
+  __shared__ float2 stat[FEW ? 4 : 1][16];         // their maxima and sums
+  __shared__ __align__(8) uint64_t xch_bar;        // the softmax threads meet around them
 
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
@@ -165,17 +177,54 @@ __global__ void __launch_bounds__(CrossCfg<D, QROWS>::THREADS, 1)
   // the merging kernel may start its prologue (it waits for this grid's end)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- tiles of a segment of the batch entries before each
+  // ---- prologue: tiles of a segment of the batch entries before each, while the
+  // barriers are set up, tensor memory is allocated and the tensor maps arrive
+  const int per = (kp.B + C::THREADS - 1) / C::THREADS;
+  const int b0 = min(static_cast<int>(threadIdx.x) * per, kp.B), b1 = min(b0 + per, kp.B);
+  const int first_len = kp.kv_lens && b0 < b1 ? __ldg(kp.kv_lens + b0) : kp.Nk;
+  if (warp == C::MMA_WARP) {
+    tmem_alloc(&tmem_base_sh, 512);
+    tmem_relinquish();
+  } else if (threadIdx.x == C::LOAD_WARP * 32) {
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+    prefetch_tmap(&tmQ);
+  } else if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_empty[i], 128);
+    }
+    mbar_init(&pv_done, 1);
+    if constexpr (FEW) mbar_init(&xch_bar, 128);
+    for (int s = 0; s < NSLOT; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    mbar_init(&drain_bar, 1);
+    abort_sh = 0;
+    issued_sh[0] = issued_sh[1] = parts_sh = 0;
+    fence_mbar_init();
+  }
   {
-    const int per = (kp.B + C::THREADS - 1) / C::THREADS;
-    const int b0 = min(static_cast<int>(threadIdx.x) * per, kp.B), b1 = min(b0 + per, kp.B);
+    auto tiles_of = [&](int b) {
+      const int n = b == b0 ? first_len : __ldg(kp.kv_lens + b);
+      return n < 0 || n > kp.Nk ? 0 : (n + BN - 1) / BN;
+    };
     int sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      if (kp.kv_lens && blockIdx.x == 0) {
-        const int n = __ldg(kp.kv_lens + b);
-        if (n < 0 || n > kp.Nk) atomicCAS(kp.status, 0, kDevBadSeqlens);
+    if (kp.kv_lens) {
+      for (int b = b0; b < b1; ++b) {
+        if (blockIdx.x == 0) {
+          const int n = b == b0 ? first_len : __ldg(kp.kv_lens + b);
+          if (n < 0 || n > kp.Nk) atomicCAS(kp.status, 0, kDevBadSeqlens);
+        }
+        sum += tiles_of(b);
       }
-      sum += (keys_of(kp.kv_lens, b, kp.Nk) + BN - 1) / BN;
+    } else {
+      sum = (b1 - b0) * ((kp.Nk + BN - 1) / BN);
     }
     int scan = sum;
 #pragma unroll
@@ -189,32 +238,9 @@ __global__ void __launch_bounds__(CrossCfg<D, QROWS>::THREADS, 1)
     for (int w = 0; w < warp; ++w) base += warp_sum[w];
     for (int b = b0; b < b1; ++b) {
       pre[b] = base;
-      base += (keys_of(kp.kv_lens, b, kp.Nk) + BN - 1) / BN;
+      base += kp.kv_lens ? tiles_of(b) : (kp.Nk + BN - 1) / BN;
     }
     if (b1 == kp.B && b0 < b1) pre[kp.B] = base;
-  }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
-      mbar_init(&o_full[i], 1);
-      mbar_init(&o_empty[i], 128);
-    }
-    mbar_init(&pv_done, 1);
-    for (int s = 0; s < NSLOT; ++s) {
-      mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
-    }
-    mbar_init(&drain_bar, 1);
-    abort_sh = 0;
-    issued_sh[0] = issued_sh[1] = parts_sh = 0;
-    fence_mbar_init();
-  }
-  if (warp == C::MMA_WARP) {
-    tmem_alloc(&tmem_base_sh, 512);
-    tmem_relinquish();
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -228,51 +254,48 @@ __global__ void __launch_bounds__(CrossCfg<D, QROWS>::THREADS, 1)
 
   if (warp == C::LOAD_WARP || warp == C::LOAD_V_WARP) {
     // ------------------------------------------------------------ producers
-    // Lane c issues column chunk c of a tile; two warps stream into the ring (one
-    // issuing warp cannot keep HBM busy).  Item 2 n is the n-th K tile of the
-    // share, item 2 n + 1 its V tile.
-    const int kv = warp == C::LOAD_WARP ? 0 : 1;
-    if (lane == 0 && kv == 0) {
-      prefetch_tmap(&tmQ);
-      prefetch_tmap(&tmK);
-      prefetch_tmap(&tmV);
-    }
-    int n = 0, part = 0;
-    bool ok = true;
-    while (ok && cur.left > 0) {
-      const int take = cur.part();
-      const int hk = cur.y / kp.qtiles;
-      if (kv == 0) {
-        int go = 1;
-        if (lane == 0) {
-          if (part >= 2 && !mbar_wait(&q_empty[part & 1], ((part >> 1) - 1) & 1, ab, kDevTimeoutLoad)) go = 0;
-          else mbar_arrive_expect_tx(&q_full[part & 1], C::QTILE);
-        }
-        if (!__shfl_sync(0xffffffffu, go, 0)) break;
-        if (lane < C::CH)
-          tma_load_3d(sQ + (part & 1) * C::QTILE + lane * C::QCHUNK, &tmQ, &q_full[part & 1], lane * 64,
-                      hk * kp.rows + (cur.y - hk * kp.qtiles) * BM, cur.b);
-        ++part;
-      }
-      for (int i = 0; i < take; ++i, ++n) {
-        const int item = 2 * n + kv;
-        const int slot = item % NSLOT, use = item / NSLOT;
-        int go = 1;
-        if (lane == 0) {
-          if (use >= 1 && !mbar_wait(&kv_empty[slot], (use - 1) & 1, ab, kDevTimeoutLoad)) go = 0;
-          else mbar_arrive_expect_tx(&kv_full[slot], C::TILE);
-        }
-        if (!__shfl_sync(0xffffffffu, go, 0)) {
-          ok = false;
-          break;
-        }
-        if (lane < C::CH)
-          tma_load_4d(sKV + slot * C::TILE + lane * C::CHUNK, kv ? &tmV : &tmK, &kv_full[slot], lane * 64,
-                      (cur.j + i) * BN, hk, cur.b);
-      }
-      cur.next_part(take);
-    }
+    // Two threads stream into the ring, one copy per tile (its 64-column chunks are a
+    // dimension of the map's box).  Item 2 n is the n-th K tile of the share, item
+    // 2 n + 1 its V tile.  The part's Q follows its first K tile's copy: HBM first.
     if (lane == 0) {
+      const int kv = warp == C::LOAD_WARP ? 0 : 1;
+      int n = 0, part = 0;
+      bool ok = true;
+      while (ok && cur.left > 0) {
+        const int take = cur.part();
+        const int hk = cur.y / kp.qtiles;
+        for (int i = 0; i < take; ++i) {
+          const int item = 2 * n + kv;
+          const int slot = item % NSLOT, use = item / NSLOT;
+          if (use >= 1 && !mbar_wait(&kv_empty[slot], (use - 1) & 1, ab, kDevTimeoutLoad)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&kv_full[slot], C::TILE);
+          tma_load_4d(sKV + slot * C::TILE, kv ? &tmV : &tmK, &kv_full[slot], 0, (cur.j + i) * BN, 0,
+                      cur.b * kp.H_kv + hk);
+          ++n;
+          if (kv == 0 && i == 0) {
+            if (part >= 2 && !mbar_wait(&q_empty[part & 1], ((part >> 1) - 1) & 1, ab, kDevTimeoutLoad)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&q_full[part & 1], C::QBYTES);
+            uint8_t* dst = sQ + (part & 1) * C::QSTEP;
+            const int row = hk * kp.rows + (cur.y - hk * kp.qtiles) * BM;
+            if constexpr (FEW) {
+              // a box is 16 rows of one 64-column chunk
+              for (int c = 0; c < C::CH; ++c)
+                for (int x = 0; x < 4; ++x)
+                  tma_load_4d(dst + c * C::CHUNK + x * 32 * 128, &tmQ, &q_full[part & 1], 0, row, c, cur.b);
+            } else {
+              tma_load_4d(dst, &tmQ, &q_full[part & 1], 0, row, 0, cur.b);
+            }
+            ++part;
+          }
+        }
+        cur.next_part(take);
+      }
       issued_sh[kv] = n;
       if (kv == 0) parts_sh = part;
     }
@@ -296,12 +319,12 @@ __global__ void __launch_bounds__(CrossCfg<D, QROWS>::THREADS, 1)
         const int item = 2 * s_n, slot = item % NSLOT;
         if (!mbar_wait(&kv_full[slot], (item / NSLOT) & 1, ab, kDevTimeoutMma)) return false;
         tc_fence_after_sync();
-        const uint64_t qdesc = opaque(sdesc_add(qdesc0, (s_part & 1) * C::QTILE));
+        const uint64_t qdesc = opaque(sdesc_add(qdesc0, (s_part & 1) * C::QSTEP));
         const uint64_t kdesc = opaque(sdesc_add(kdesc0, slot * C::TILE));
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          mma_f16_ss(tmem + C::S_COL(s_n & 1), sdesc_add(qdesc, (kk / 4) * C::QCHUNK + (kk % 4) * 32),
-                     sdesc_add(kdesc, (kk / 4) * C::CHUNK + (kk % 4) * 32), idS, kk > 0 ? 1u : 0u);
+          const uint32_t off = (kk / 4) * C::CHUNK + (kk % 4) * 32;
+          mma_f16_ss(tmem + C::S_COL(s_n & 1), sdesc_add(qdesc, off), sdesc_add(kdesc, off), idS, kk > 0 ? 1u : 0u);
         }
         mma_commit(&s_full[s_n & 1]);
         if (item + NSLOT < 2 * total) mma_commit(&kv_empty[slot]);
@@ -346,7 +369,11 @@ __global__ void __launch_bounds__(CrossCfg<D, QROWS>::THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
+    // Thread r: query row r, all keys of a tile; or (FEW) query row lane, keys [32
+    // warp, 32 warp + 32).
     const int r = warp * 32 + lane;
+    constexpr int W = FEW ? 32 : BN;                 // keys of a thread in a tile
+    const int k0 = FEW ? 32 * warp : 0;
     const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
     const float c2 = kp.scale_log2;
     bool ok = true;
@@ -356,47 +383,96 @@ __global__ void __launch_bounds__(CrossCfg<D, QROWS>::THREADS, 1)
       bool whole, last;
       float m, l;
     } done{-1, 0, 0, false, false, 0.f, 0.f};
+    auto store_lse = [&](size_t at, size_t part_at, float m, float l) {
+      *(done.whole ? kp.lse + at : kp.lse_part + part_at) =
+          (m * c2 + lg2f_approx(l)) * 0.69314718055994530942f;
+    };
+    // all softmax threads meet (an mbarrier, whose wait ends when another warp gave up)
+    uint32_t met = 0;
+    auto meet = [&]() -> bool {
+      mbar_arrive(&xch_bar);
+      const bool came = !__any_sync(0xffffffffu, !mbar_wait(&xch_bar, met & 1, ab, kDevTimeoutEpilogue));
+      ++met;
+      return came;
+    };
     auto write_out = [&]() -> bool {
       const int buf = done.part & 1;
       if (__any_sync(0xffffffffu, !mbar_wait(&o_full[buf], (done.part >> 1) & 1, ab, kDevTimeoutEpilogue)))
         return false;
       tc_fence_after_sync();
       const int hk = done.y / kp.qtiles;
-      const int row = (done.y - hk * kp.qtiles) * BM + r;     // of the head's G * N_q rows
-      const bool row_ok = row < kp.rows;
+      const int row0 = (done.y - hk * kp.qtiles) * BM;        // of the head's G * N_q rows
       // rows of a key/value head are contiguous in [B, H, N_q]
-      const size_t at = (static_cast<size_t>(done.b) * kp.H_kv + hk) * kp.rows + row;
-      const int slot = 2 * blockIdx.x + (done.last ? 1 : 0);
-      const float inv_l = 1.f / done.l;
+      const size_t at0 = (static_cast<size_t>(done.b) * kp.H_kv + hk) * kp.rows + row0;
+      const size_t part0 = static_cast<size_t>(2 * blockIdx.x + (done.last ? 1 : 0)) * kp.seg_rows;
+      if constexpr (FEW) {
+        // weights of the four outputs of row `lane`: exp(m_w - m) / sum_w exp(m_w - m) l_w
+        if (lane < 16) stat[warp][lane] = make_float2(done.m, done.l);
+        if (!meet()) return false;
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = fmaxf(m, stat[w][lane & 15].x);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) l += ex2_approx((stat[w][lane & 15].x - m) * c2) * stat[w][lane & 15].y;
+        const float weight = ex2_approx((done.m - m) * c2) / l;
+        if (warp == 0 && lane < kp.rows) store_lse(at0 + lane, part0 + lane, m, l);
 #pragma unroll 1
-      for (int c0 = 0; c0 < D / 32; ++c0) {
-        uint32_t o[32];
-        tmem_ld32(tmem + lane_addr + C::O_COL(buf) + c0 * 32, o);
-        tmem_ld_wait();
-        if (!row_ok) continue;
-        if (done.whole) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kp.o) + at * D + c0 * 32);
-          uint32_t pk[16];
+        for (int c0 = 0; c0 < D / 64; ++c0) {
+          if (c0 > 0 && !meet()) return false;       // the round before has been read
+          uint32_t o[64];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float x = __uint_as_float(o[2 * i]) * inv_l, z = __uint_as_float(o[2 * i + 1]) * inv_l;
-            pk[i] = FP16 ? cvt_pack_f16(x, z) : cvt_pack_bf16(x, z);
+          for (int x = 0; x < 2; ++x)
+            tmem_ld32(tmem + lane_addr + C::O_COL(buf) + c0 * 64 + x * 32,
+                      *reinterpret_cast<uint32_t(*)[32]>(&o[32 * x]));
+          tmem_ld_wait();
+          if (lane < 16) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) xch[warp][lane][i] = __uint_as_float(o[i]) * weight;
           }
+          if (!meet()) return false;
+          // rows warp, warp + 4, ...: lane = columns lane and lane + 32
+          for (int x = warp; x < kp.rows; x += 4) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
-        } else {
-          float4* dst = reinterpret_cast<float4*>(
-              kp.o_part + (static_cast<size_t>(slot) * kp.seg_rows + r) * D + c0 * 32);
-#pragma unroll
-          for (int v = 0; v < 8; ++v)
-            dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
-                                 __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
+            for (int i = lane; i < 64; i += 32) {
+              const float sum = (xch[0][x][i] + xch[1][x][i]) + (xch[2][x][i] + xch[3][x][i]);
+              if (done.whole) {
+                const uint32_t pk = FP16 ? cvt_pack_f16(sum, 0.f) : cvt_pack_bf16(sum, 0.f);
+                static_cast<uint16_t*>(kp.o)[(at0 + x) * D + c0 * 64 + i] = static_cast<uint16_t>(pk);
+              } else {
+                kp.o_part[(part0 + x) * D + c0 * 64 + i] = sum;
+              }
+            }
+          }
         }
-      }
-      if (row_ok) {
-        float* dst = done.whole ? kp.lse + at : kp.lse_part + static_cast<size_t>(slot) * kp.seg_rows + r;
-        *dst = (done.m * c2 + lg2f_approx(done.l)) * 0.69314718055994530942f;
+      } else {
+        const bool row_ok = row0 + r < kp.rows;
+        const float inv_l = 1.f / done.l;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D / 32; ++c0) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_addr + C::O_COL(buf) + c0 * 32, o);
+          tmem_ld_wait();
+          if (!row_ok) continue;
+          if (done.whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kp.o) + (at0 + r) * D + c0 * 32);
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float x = __uint_as_float(o[2 * i]) * inv_l, z = __uint_as_float(o[2 * i + 1]) * inv_l;
+              pk[i] = FP16 ? cvt_pack_f16(x, z) : cvt_pack_bf16(x, z);
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+          } else {
+            float4* dst = reinterpret_cast<float4*>(kp.o_part + (part0 + r) * D + c0 * 32);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
+                                   __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
+          }
+        }
+        if (row_ok) store_lse(at0 + r, part0 + r, done.m, done.l);
       }
       tc_fence_before_sync();
       mbar_arrive(&o_empty[buf]);
@@ -408,8 +484,10 @@ __global__ void __launch_bounds__(CrossCfg<D, QROWS>::THREADS, 1)
       const int len = keys_of(kp.kv_lens, cur.b, kp.Nk);
       float m_ref = -INFINITY, l = 0.f;
       // a warp without query rows only keeps the others' pace
-      const bool live = (cur.y % kp.qtiles) * BM + warp * 32 < kp.rows;
+      const bool live = FEW || (cur.y % kp.qtiles) * BM + warp * 32 < kp.rows;
       for (int i = 0; i < take; ++i, ++n) {
+        // a warp that gives up stops arriving at p_full (and where the warps meet), so
+        // the others' next wait ends too
         if (__any_sync(0xffffffffu, !mbar_wait(&s_full[n & 1], (n >> 1) & 1, ab, kDevTimeoutSoftmax))) {
           ok = false;
           break;
@@ -417,77 +495,79 @@ __global__ void __launch_bounds__(CrossCfg<D, QROWS>::THREADS, 1)
         tc_fence_after_sync();
         const int lim = len - (cur.j + i) * BN;        // keys of this tile that are seen
         if (live) {
-        const uint32_t tS = tmem + lane_addr + C::S_COL(n & 1);
-        uint32_t sr[BN];
+          const uint32_t tS = tmem + lane_addr + C::S_COL(n & 1);
+          uint32_t sr[W];
 #pragma unroll
-        for (int c0 = 0; c0 < BN / 32; ++c0)
-          tmem_ld32(tS + c0 * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0 * 32]));
-        tmem_ld_wait();
-        if (lim < BN) {
+          for (int c0 = 0; c0 < W / 32; ++c0)
+            tmem_ld32(tS + k0 + c0 * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0 * 32]));
+          tmem_ld_wait();
+          if (lim < k0 + W) {
 #pragma unroll
-          for (int c = 0; c < BN; ++c)
-            if (c >= lim) sr[c] = __float_as_uint(-INFINITY);
-        }
-        float mx[16];
-#pragma unroll
-        for (int u = 0; u < 16; ++u)
-          mx[u] = fmax3(__uint_as_float(sr[8 * u]), __uint_as_float(sr[8 * u + 1]),
-                        fmax3(__uint_as_float(sr[8 * u + 2]), __uint_as_float(sr[8 * u + 3]),
-                              fmax3(__uint_as_float(sr[8 * u + 4]), __uint_as_float(sr[8 * u + 5]),
-                                    fmaxf(__uint_as_float(sr[8 * u + 6]), __uint_as_float(sr[8 * u + 7])))));
-#pragma unroll
-        for (int u = 0; u < 8; ++u) mx[u] = fmaxf(mx[u], mx[u + 8]);
-        const float m_new = fmaxf(m_ref, fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
-                                               fmaxf(mx[6], mx[7])));
-        // lazy rescale: the exponent reference moves when the maximum grew by over 2^8
-        const bool need = (m_new - m_ref) * c2 > 8.f;
-        float alpha = 1.f;
-        if (need) {
-          alpha = ex2_approx((m_ref - m_new) * c2);
-          l *= alpha;
-          m_ref = m_new;
-        }
-        const float neg = (m_ref == -INFINITY) ? 0.f : -m_ref * c2;
-        const uint64_t cc = pack2(c2, c2);
-        const uint64_t nn = pack2(neg, neg);
-        uint64_t acc0 = 0, acc1 = 0;
-#pragma unroll
-        for (int c0 = 0; c0 < BN / 32; ++c0) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int c = c0 * 32 + 2 * e;
-            const uint64_t y = ffma2(pack2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), cc, nn);
-            const float p0 = ex2_approx(lo2(y));
-            const float p1 = ex2_approx(hi2(y));
-            if (e & 1) acc1 = fadd2(acc1, pack2(p0, p1));
-            else acc0 = fadd2(acc0, pack2(p0, p1));
-            pk[e] = FP16 ? cvt_pack_f16(p0, p1) : cvt_pack_bf16(p0, p1);
+            for (int c = 0; c < W; ++c)
+              if (k0 + c >= lim) sr[c] = __float_as_uint(-INFINITY);
           }
-          // packed P of keys [32 c0, +32) -> columns [16 c0, +16)
-          tmem_st16(tS + c0 * 16, pk);
-        }
-        const uint64_t acc = fadd2(acc0, acc1);
-        l += lo2(acc) + hi2(acc);
-        if (i > 0 && __any_sync(0xffffffffu, need)) {
-          // rescale O once P(n - 1) V has landed; this tile's product is issued
-          // only after the arrive below
-          if (__any_sync(0xffffffffu, !mbar_wait(&pv_done, (n - 1) & 1, ab, kDevTimeoutSoftmax))) {
-            ok = false;
-            break;
+          float m_new = m_ref;
+#pragma unroll
+          for (int u = 0; u < W / 8; ++u)
+            m_new = fmaxf(m_new, fmax3(fmax3(__uint_as_float(sr[8 * u]), __uint_as_float(sr[8 * u + 1]),
+                                             __uint_as_float(sr[8 * u + 2])),
+                                       fmax3(__uint_as_float(sr[8 * u + 3]), __uint_as_float(sr[8 * u + 4]),
+                                             __uint_as_float(sr[8 * u + 5])),
+                                       fmaxf(__uint_as_float(sr[8 * u + 6]), __uint_as_float(sr[8 * u + 7]))));
+          // lazy rescale: the exponent reference moves when the maximum grew by over 2^8
+          const bool need = (m_new - m_ref) * c2 > 8.f;
+          float alpha = 1.f;
+          if (need) {
+            alpha = ex2_approx((m_ref - m_new) * c2);
+            l *= alpha;
+            m_ref = m_new;
           }
-          tc_fence_after_sync();
-          const uint32_t tO = tmem + lane_addr + C::O_COL(part & 1);
+          const float neg = (m_ref == -INFINITY) ? 0.f : -m_ref * c2;
+          const uint64_t cc = pack2(c2, c2);
+          const uint64_t nn = pack2(neg, neg);
+          uint64_t acc0 = 0, acc1 = 0;
+#pragma unroll
+          for (int c0 = 0; c0 < W / 32; ++c0) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int c = c0 * 32 + 2 * e;
+              const uint64_t y = ffma2(pack2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), cc, nn);
+              const float p0 = ex2_approx(lo2(y));
+              const float p1 = ex2_approx(hi2(y));
+              if (e & 1) acc1 = fadd2(acc1, pack2(p0, p1));
+              else acc0 = fadd2(acc0, pack2(p0, p1));
+              pk[e] = FP16 ? cvt_pack_f16(p0, p1) : cvt_pack_bf16(p0, p1);
+            }
+            // packed P of keys [k, +32) -> columns [k / 2, +16)
+            tmem_st16(tS + k0 / 2 + c0 * 16, pk);
+          }
+          if constexpr (FEW) {
+            const uint32_t zero[16] = {};
+#pragma unroll
+            for (int x = 1; x < 4; ++x) tmem_st16(tS + 16 * ((warp + x) & 3), zero);
+          }
+          const uint64_t acc = fadd2(acc0, acc1);
+          l += lo2(acc) + hi2(acc);
+          if (i > 0 && __any_sync(0xffffffffu, need)) {
+            // rescale O once P(n - 1) V has landed; this tile's product is issued
+            // only after the arrive below
+            if (__any_sync(0xffffffffu, !mbar_wait(&pv_done, (n - 1) & 1, ab, kDevTimeoutSoftmax))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint32_t tO = tmem + lane_addr + C::O_COL(part & 1);
 #pragma unroll 1
-          for (int c0 = 0; c0 < D / 32; ++c0) {
-            uint32_t o[32];
-            tmem_ld32(tO + c0 * 32, o);
-            tmem_ld_wait();
+            for (int c0 = 0; c0 < D / 32; ++c0) {
+              uint32_t o[32];
+              tmem_ld32(tO + c0 * 32, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(tO + c0 * 32, o);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(tO + c0 * 32, o);
+            }
           }
-        }
         }
         if (lim < BN && len < kp.Nk) {
           // rows of V behind the keys may hold anything: they meet P = 0 in the
@@ -553,16 +633,22 @@ __global__ void __launch_bounds__(CrossCfg<D, QROWS>::THREADS, 1)
 }
 
 // Segments that cross shares: LSE = log sum_c exp(lse_c) and O = sum_c exp(lse_c -
-// LSE) O_c over the CTAs whose shares they touch.  One block per segment.
+// LSE) O_c over the CTAs whose shares they touch, with a running maximum.  One block
+// per segment and kMergeRows of its rows, D / 4 threads per row; four partial
+// results are loaded at a time.
+constexpr int kMergeThreads = 128;
+template <int D>
+constexpr int kMergeRows = kMergeThreads / (D / 4);
+
 template <int D, bool FP16>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kMergeThreads)
     cross_merge_kernel(const CrossKParams kp, int C) {
   __shared__ int sums[2][4];
-  const int b = blockIdx.y, y = blockIdx.x;
+  const int b = blockIdx.z, y = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // tiles of a segment of the entries before b, and of all
   int before = 0, all = 0;
-  for (int i = threadIdx.x; i < kp.B; i += 128) {
+  for (int i = threadIdx.x; i < kp.B; i += kMergeThreads) {
     const int n = (keys_of(kp.kv_lens, i, kp.Nk) + BN - 1) / BN;
     all += n;
     if (i < b) before += n;
@@ -577,62 +663,78 @@ __global__ void __launch_bounds__(128)
   before = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3];
   const int T = (sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3]) * kp.segs;
   const int nt = (keys_of(kp.kv_lens, b, kp.Nk) + BN - 1) / BN;
-  // every block waits: one that returned before the first kernel's end could let the
-  // stream's next kernel start too early
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (nt == 0) return;
   const int g0 = before * kp.segs + y * nt, g1 = g0 + nt - 1;
   // CTA whose share holds tile g: the last c with c T / C <= g
   C = min(C, T);
-  const int c0 = static_cast<int>(((g0 + 1ll) * C - 1) / T), c1 = static_cast<int>(((g1 + 1ll) * C - 1) / T);
-  if (c0 == c1) return;
+  const int c0 = nt ? static_cast<int>(((g0 + 1ll) * C - 1) / T) : 0;
+  const int c1 = nt ? static_cast<int>(((g1 + 1ll) * C - 1) / T) : 0;
   // a share's first part is its slot 0, a later one its slot 1; the segment is a
   // later part only where it starts inside a share
-  const int slot0 = 2 * c0 + (share_start(c0, C, T) == g0 ? 0 : 1);
+  const int slot0 = 2 * c0 + (nt == 0 || share_start(c0, C, T) == g0 ? 0 : 1);
   const int hk = y / kp.qtiles;
   const int row0 = (y - hk * kp.qtiles) * BM;
-  const int rows = min(BM, kp.rows - row0);
-  constexpr int PER = 4;                             // columns per thread
-  constexpr int TPR = D / PER;                       // threads per row
-  for (int r = threadIdx.x / TPR; r < rows; r += 128 / TPR) {
-    const int col = (threadIdx.x % TPR) * PER;
-    float mx = -INFINITY;
-    for (int c = c0; c <= c1; ++c)
-      mx = fmaxf(mx, kp.lse_part[static_cast<size_t>(c == c0 ? slot0 : 2 * c) * kp.seg_rows + r]);
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) {
-      const size_t at = static_cast<size_t>(c == c0 ? slot0 : 2 * c) * kp.seg_rows + r;
-      const float w = expf(kp.lse_part[at] - mx);
-      const float4 o = *reinterpret_cast<const float4*>(kp.o_part + at * D + col);
-      sum += w;
-      acc.x = fmaf(w, o.x, acc.x);
-      acc.y = fmaf(w, o.y, acc.y);
-      acc.z = fmaf(w, o.z, acc.z);
-      acc.w = fmaf(w, o.w, acc.w);
+  const int r = blockIdx.y * kMergeRows<D> + threadIdx.x / (D / 4);
+  const int col = (threadIdx.x % (D / 4)) * 4;
+  // every block waits: one that returned before the first kernel's end could let the
+  // stream's next kernel start too early
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c0 == c1 || r >= min(BM, kp.rows - row0)) return;
+  float m = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0; c <= c1; c += 4) {
+    float lse[4];
+    float4 o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lse[i] = -INFINITY;
+      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + i <= c1) {
+        const size_t at = static_cast<size_t>(c + i == c0 ? slot0 : 2 * (c + i)) * kp.seg_rows + r;
+        lse[i] = kp.lse_part[at];
+        o[i] = *reinterpret_cast<const float4*>(kp.o_part + at * D + col);
+      }
     }
-    const float inv = 1.f / sum;
-    const size_t at = (static_cast<size_t>(b) * kp.H_kv + hk) * kp.rows + row0 + r;
-    const uint2 pk = FP16 ? make_uint2(cvt_pack_f16(acc.x * inv, acc.y * inv), cvt_pack_f16(acc.z * inv, acc.w * inv))
-                          : make_uint2(cvt_pack_bf16(acc.x * inv, acc.y * inv), cvt_pack_bf16(acc.z * inv, acc.w * inv));
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(kp.o) + at * D + col) = pk;
-    if (col == 0) kp.lse[at] = mx + logf(sum);
+    const float m_new = fmaxf(m, fmaxf(fmaxf(lse[0], lse[1]), fmaxf(lse[2], lse[3])));
+    const float keep = m == -INFINITY ? 0.f : expf(m - m_new);
+    sum *= keep;
+    acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float w = lse[i] == -INFINITY ? 0.f : expf(lse[i] - m_new);
+      sum += w;
+      acc.x = fmaf(w, o[i].x, acc.x);
+      acc.y = fmaf(w, o[i].y, acc.y);
+      acc.z = fmaf(w, o[i].z, acc.z);
+      acc.w = fmaf(w, o[i].w, acc.w);
+    }
+    m = m_new;
   }
+  const float inv = 1.f / sum;
+  const size_t at = (static_cast<size_t>(b) * kp.H_kv + hk) * kp.rows + row0 + r;
+  const uint2 pk = FP16 ? make_uint2(cvt_pack_f16(acc.x * inv, acc.y * inv), cvt_pack_f16(acc.z * inv, acc.w * inv))
+                        : make_uint2(cvt_pack_bf16(acc.x * inv, acc.y * inv), cvt_pack_bf16(acc.z * inv, acc.w * inv));
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(kp.o) + at * D + col) = pk;
+  if (col == 0) kp.lse[at] = m + logf(sum);
 }
 
-template <int D, bool FP16, int QROWS>
+template <int D, bool FP16, bool FEW>
 attn_status_t launch_cross_rows_t(const FwdParams& p, const CrossPlan& plan, void* workspace,
                                   cudaStream_t stream) {
-  using C = CrossCfg<D, QROWS>;
-  auto kern = cross_rows_kernel<D, FP16, QROWS>;
+  using C = CrossCfg<D, FEW>;
+  auto kern = cross_rows_kernel<D, FP16, FEW>;
   attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), C::SMEM);
   if (s != ATTN_OK) return s;
   CUtensorMap tq, tk, tv;
-  // Q: {d, H * N_q rows, B}; K, V: {d, N_k, H_kv, B}
-  if ((s = make_tmap_3d(&tq, p.q, 2, D, static_cast<uint64_t>(p.H) * p.N, p.B, 64, QROWS)) != ATTN_OK) return s;
-  const uint64_t row_b = 2ull * D, head_b = row_b * p.N_k, batch_b = head_b * p.H_kv;
-  if ((s = make_tmap_4d(&tk, p.k, 2, D, p.N_k, p.H_kv, p.B, row_b, head_b, batch_b, 64, BN)) != ATTN_OK) return s;
-  if ((s = make_tmap_4d(&tv, p.v, 2, D, p.N_k, p.H_kv, p.B, row_b, head_b, batch_b, 64, BN)) != ATTN_OK) return s;
+  // {64 columns, rows, 64-column chunks, planes}: one box holds every chunk
+  const uint64_t row_b = 2ull * D, q_rows = static_cast<uint64_t>(p.H) * p.N;
+  const uint64_t planes = static_cast<uint64_t>(p.B) * p.H_kv;
+  if ((s = make_tmap_4d(&tq, p.q, 2, 64, q_rows, C::CH, p.B, row_b, 128, row_b * q_rows, 64, C::QROWS,
+                        FEW ? 1 : C::CH)) != ATTN_OK)
+    return s;
+  if ((s = make_tmap_4d(&tk, p.k, 2, 64, p.N_k, C::CH, planes, row_b, 128, row_b * p.N_k, 64, BN, C::CH)) != ATTN_OK)
+    return s;
+  if ((s = make_tmap_4d(&tv, p.v, 2, 64, p.N_k, C::CH, planes, row_b, 128, row_b * p.N_k, 64, BN, C::CH)) != ATTN_OK)
+    return s;
   int* status = device_status_word();
   if (!status) return fail(ATTN_ERR_CUDA, "status word unavailable");
   const int rows = p.H / p.H_kv * p.N;
@@ -648,8 +750,8 @@ attn_status_t launch_cross_rows_t(const FwdParams& p, const CrossPlan& plan, voi
   if (e != cudaSuccess) return fail_cuda(e, "cross attention rows kernel launch");
   // launched while the first kernel runs; it waits for its end before reading
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kp.segs, p.B);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(kp.segs, (seg_rows + kMergeRows<D> - 1) / kMergeRows<D>, p.B);
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -667,8 +769,8 @@ attn_status_t launch_cross_rows(const FwdParams& p, const CrossPlan& plan, void*
                                 cudaStream_t stream) {
   const bool few = p.H / p.H_kv * p.N <= 16;
 #define ATTN_CROSS_ROWS(D, F)                                                   \
-  return few ? launch_cross_rows_t<D, F, 16>(p, plan, workspace, stream)        \
-             : launch_cross_rows_t<D, F, 128>(p, plan, workspace, stream)
+  return few ? launch_cross_rows_t<D, F, true>(p, plan, workspace, stream)      \
+             : launch_cross_rows_t<D, F, false>(p, plan, workspace, stream)
   if (p.d == 64) {
     if (p.fp16) ATTN_CROSS_ROWS(64, true);
     ATTN_CROSS_ROWS(64, false);
