@@ -221,16 +221,33 @@ attn_status_t launch_decode(const DecodeParams& p, cudaStream_t stream);
 
 // How a cross-attention forward runs.  ctas > 0: the rows kernel (cross.cu), that many
 // CTAs sharing the tiles of all keys, for tiles of 128 query rows of one key/value
-// head (its G * N_q rows together); ctas = 0: the forward kernel (fwd.cu).
+// head (its G * N_q rows together); ctas = 0: the forward kernel (fwd.cu), one CTA
+// per 256 query rows of one query head with all keys.
 struct CrossPlan {
   int ctas, qtiles;
 };
-constexpr int kCrossMaxB = 4096;   // batch entries of the rows kernel (4 bytes of shared memory each)
+constexpr int kCrossMaxB = 2048;   // batch entries of the rows kernel (8 bytes of shared memory each)
+// The smaller of two modelled times, in microseconds, fitted to both kernels at d = 64
+// and 128, N_k = 512 .. 4096 and N_q = 1 .. 1024 (bfloat16, K and V in L2):
+//  forward: waves of 152 CTAs x (3.5 + 1.4 or 1.55 per key tile), a tenth more per
+//           tile when both of a CTA's query tiles are in use;
+//  rows:    a start and a merge, the tiles of one CTA's share, and 2 or more for
+//           every segment it finishes (its output leaves tensor memory row by row).
+// 16 heads, N_k = 4096, d = 128: N_q = 1: 51 us (forward), 17 (rows); 512: 56, 44;
+// 1024: 57, 74.  8 x 16 heads, N_k = 512: N_q = 1: 10, 13.
 inline CrossPlan cross_plan(int B, int H, int H_kv, int N_q, int N_k, int d) {
+  if (d > 128 || B > kCrossMaxB) return {0, 0};
   const long long rows = static_cast<long long>(H / H_kv) * N_q;
-  const long long qtiles = (rows + 127) / 128;
-  if (d == 256 || qtiles > 1 || B > kCrossMaxB) return {0, 0};
-  const long long tiles = static_cast<long long>(B) * H_kv * qtiles * ((N_k + 127) / 128);
+  const long long qtiles = (rows + 127) / 128, ktiles = (N_k + 127) / 128;
+  const long long segs = static_cast<long long>(B) * H_kv * qtiles, tiles = segs * ktiles;
+  const long long fwd_ctas = static_cast<long long>(B) * H * ((N_q + 255) / 256);
+  const double fwd = static_cast<double>((fwd_ctas + 151) / 152) *
+                     (3.5 + ktiles * (d == 64 ? 1.4 : 1.55) * (N_q > 128 ? 1.1 : 1.0));
+  const bool few = rows <= 16;
+  const double share = static_cast<double>((tiles + 151) / 152), ends = static_cast<double>((segs + 151) / 152);
+  const double shared = d == 64 ? 9.0 + share * (few ? 0.75 : 0.95) + ends * (few ? 0.3 : 2.0)
+                                : (few ? 10.0 : 12.0) + share * (few ? 1.0 : 1.16) + ends * (few ? 0.3 : 2.7);
+  if (fwd <= shared || tiles > 2147483647LL || H_kv * qtiles > 2147483647LL) return {0, 0};
   return {static_cast<int>(tiles < 152 ? tiles : 152), static_cast<int>(qtiles)};
 }
 // The rows kernel's float32 partial O and log-sum-exps, two per CTA.

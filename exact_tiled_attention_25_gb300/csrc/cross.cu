@@ -17,8 +17,10 @@
 //    leaves float32 partial outputs and log-sum-exps, at most two per CTA, which a
 //    second kernel merges; its launch overlaps the first kernel.
 //
-// Roles as in the paged decode: key and value producer warps, one MMA warp, four
-// softmax warps (a thread per query row).
+// Roles: key and value producer warps, an MMA warp for the score products and one for
+// the P V products (issuing a product or a commit costs a thread some hundred cycles:
+// one thread for both took 1.04 us a tile at d = 64, where HBM delivers one in 0.75),
+// four softmax warps.
 #include <cmath>
 
 #include "common.h"
@@ -51,15 +53,16 @@ struct CrossCfg {
   static constexpr int QSTEP = FEW ? QROWS * 128 : TILE; // from one Q buffer to the other
   static constexpr int QSMEM = FEW ? TILE : 2 * TILE;
   static constexpr int XCH = FEW ? 4 * 16 * 65 * 4 + 4 * 16 * 8 : 0;   // the sum of the four outputs
-  static constexpr int LENS = 4 * (kCrossMaxB + 1);      // tile prefix sums
+  static constexpr int LENS = 8 * (kCrossMaxB + 1);      // lengths and tile prefix sums
   static constexpr int NSLOT_FIT = (kSmemLimit - 2048 - LENS - XCH - QSMEM) / TILE;
   static constexpr int NSLOT = NSLOT_FIT > 10 ? 10 : NSLOT_FIT;
   // a product reads 128 rows from its Q buffer: the second one's end in the ring
   static constexpr int SMEM = 1024 + QSMEM + NSLOT * TILE;
-  static constexpr int THREADS = 7 * 32;
+  static constexpr int THREADS = 8 * 32;
   static constexpr int LOAD_WARP = 4;
-  static constexpr int MMA_WARP = 5;
+  static constexpr int MMA_S_WARP = 5;
   static constexpr int LOAD_V_WARP = 6;
+  static constexpr int MMA_PV_WARP = 7;
   __host__ __device__ static constexpr uint32_t S_COL(int buf) { return 128u * buf; }
   __host__ __device__ static constexpr uint32_t O_COL(int buf) { return 256u + static_cast<uint32_t>(D) * buf; }
   static_assert(NSLOT >= 4 && O_COL(1) + D <= 512, "ring or tensor memory");
@@ -157,16 +160,16 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
   __shared__ __align__(8) uint64_t kv_empty[NSLOT];
   __shared__ __align__(8) uint64_t s_full[2];
   __shared__ __align__(8) uint64_t p_full[2];
-  __shared__ __align__(8) uint64_t pv_done;
   __shared__ __align__(8) uint64_t o_full[2];
   __shared__ __align__(8) uint64_t o_empty[2];
-  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ __align__(8) uint64_t drain_bar[2];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
   __shared__ int issued_sh[2];      // items that a producer issued: keys, values
   __shared__ int parts_sh;          // Q tiles issued
   __shared__ int warp_sum[C::THREADS / 32];
   __shared__ int pre[kCrossMaxB + 1];
+  __shared__ int lens[kCrossMaxB];
   __shared__ float xch[FEW ? 4 : 1][16][65];       // 64 columns of the four outputs
   __shared__ float2 stat[FEW ? 4 : 1][16];         // their maxima and sums
   __shared__ __align__(8) uint64_t xch_bar;        // the softmax threads meet around them
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
   const int per = (kp.B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, kp.B), b1 = min(b0 + per, kp.B);
   const int first_len = kp.kv_lens && b0 < b1 ? __ldg(kp.kv_lens + b0) : kp.Nk;
-  if (warp == C::MMA_WARP) {
+  if (warp == C::MMA_S_WARP) {
     tmem_alloc(&tmem_base_sh, 512);
     tmem_relinquish();
   } else if (threadIdx.x == C::LOAD_WARP * 32) {
@@ -198,33 +201,27 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
       mbar_init(&o_full[i], 1);
       mbar_init(&o_empty[i], 128);
     }
-    mbar_init(&pv_done, 1);
     if constexpr (FEW) mbar_init(&xch_bar, 128);
     for (int s = 0; s < NSLOT; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 1);
     }
-    mbar_init(&drain_bar, 1);
+    mbar_init(&drain_bar[0], 1);
+    mbar_init(&drain_bar[1], 1);
     abort_sh = 0;
     issued_sh[0] = issued_sh[1] = parts_sh = 0;
     fence_mbar_init();
   }
   {
-    auto tiles_of = [&](int b) {
-      const int n = b == b0 ? first_len : __ldg(kp.kv_lens + b);
-      return n < 0 || n > kp.Nk ? 0 : (n + BN - 1) / BN;
-    };
     int sum = 0;
-    if (kp.kv_lens) {
-      for (int b = b0; b < b1; ++b) {
-        if (blockIdx.x == 0) {
-          const int n = b == b0 ? first_len : __ldg(kp.kv_lens + b);
-          if (n < 0 || n > kp.Nk) atomicCAS(kp.status, 0, kDevBadSeqlens);
-        }
-        sum += tiles_of(b);
+    for (int b = b0; b < b1; ++b) {
+      int n = b == b0 ? first_len : kp.kv_lens ? __ldg(kp.kv_lens + b) : kp.Nk;
+      if (n < 0 || n > kp.Nk) {
+        if (blockIdx.x == 0) atomicCAS(kp.status, 0, kDevBadSeqlens);
+        n = 0;
       }
-    } else {
-      sum = (b1 - b0) * ((kp.Nk + BN - 1) / BN);
+      lens[b] = n;
+      sum += (n + BN - 1) / BN;
     }
     int scan = sum;
 #pragma unroll
@@ -238,7 +235,7 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
     for (int w = 0; w < warp; ++w) base += warp_sum[w];
     for (int b = b0; b < b1; ++b) {
       pre[b] = base;
-      base += kp.kv_lens ? tiles_of(b) : (kp.Nk + BN - 1) / BN;
+      base += (lens[b] + BN - 1) / BN;
     }
     if (b1 == kp.B && b0 < b1) pre[kp.B] = base;
   }
@@ -299,53 +296,51 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
       issued_sh[kv] = n;
       if (kv == 0) parts_sh = part;
     }
-  } else if (warp == C::MMA_WARP) {
-    // ------------------------------------------------------------ MMA issue
-    if (lane == 0 && total > 0) {
-      constexpr Elt E = FP16 ? Elt::F16 : Elt::BF16;
-      constexpr uint32_t idS = idesc_f16(E, 128, BN, false, false);
-      constexpr uint32_t idPV = idesc_f16(E, 128, D, false, true);
+  } else if (warp == C::MMA_S_WARP) {
+    // ------------------------------------------------------------ S = Q K^T
+    // S(n) into buffer n % 2, once the P V product of tile n - 2 has read its
+    // probabilities there (the phase of that value slot's empty barrier).  The
+    // softmax hands the key slot back when it sees S(n).
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_f16(FP16 ? Elt::F16 : Elt::BF16, 128, BN, false, false);
       const uint64_t qdesc0 = sdesc_sw128(smem_u32(sQ), 16, 1024);             // K-major Q
       const uint64_t kdesc0 = sdesc_sw128(smem_u32(sKV), 16, 1024);            // K-major K
-      const uint64_t vdesc0 = sdesc_sw128(smem_u32(sKV), C::CHUNK, 1024);      // MN-major V
-      // cursors of the score products (two tiles ahead) and of the P V products
-      Cursor ahead = cur;
-      int s_part = 0, s_left = ahead.part(), s_n = 0, s_take = s_left;
-      bool s_first = true;
-      // S(n) = Q K_n^T into buffer n % 2, n = s_n
-      auto issue_s = [&]() -> bool {
-        if (s_first && !mbar_wait(&q_full[s_part & 1], (s_part >> 1) & 1, ab, kDevTimeoutMma)) return false;
-        s_first = false;
-        const int item = 2 * s_n, slot = item % NSLOT;
-        if (!mbar_wait(&kv_full[slot], (item / NSLOT) & 1, ab, kDevTimeoutMma)) return false;
-        tc_fence_after_sync();
-        const uint64_t qdesc = opaque(sdesc_add(qdesc0, (s_part & 1) * C::QSTEP));
-        const uint64_t kdesc = opaque(sdesc_add(kdesc0, slot * C::TILE));
+      bool ok = true;
+      for (int n = 0, part = 0; n < total && ok; ++part) {
+        const int take = cur.part();
+        if (!(ok = mbar_wait(&q_full[part & 1], (part >> 1) & 1, ab, kDevTimeoutMma))) break;
+        const uint64_t qdesc = opaque(sdesc_add(qdesc0, (part & 1) * C::QSTEP));
+        for (int i = 0; i < take; ++i, ++n) {
+          const int item = 2 * n, slot = item % NSLOT;
+          if (!(ok = mbar_wait(&kv_full[slot], (item / NSLOT) & 1, ab, kDevTimeoutMma))) break;
+          const int old = 2 * n - 3;             // item of V of tile n - 2
+          if (n >= 2 && !(ok = mbar_wait(&kv_empty[old % NSLOT], (old / NSLOT) & 1, ab, kDevTimeoutMma))) break;
+          tc_fence_after_sync();
+          const uint64_t kdesc = opaque(sdesc_add(kdesc0, slot * C::TILE));
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * C::CHUNK + (kk % 4) * 32;
-          mma_f16_ss(tmem + C::S_COL(s_n & 1), sdesc_add(qdesc, off), sdesc_add(kdesc, off), idS, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * C::CHUNK + (kk % 4) * 32;
+            mma_f16_ss(tmem + C::S_COL(n & 1), sdesc_add(qdesc, off), sdesc_add(kdesc, off), idS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&s_full[n & 1]);
         }
-        mma_commit(&s_full[s_n & 1]);
-        if (item + NSLOT < 2 * total) mma_commit(&kv_empty[slot]);
-        ++s_n;
-        if (--s_left == 0) {
-          mma_commit(&q_empty[s_part & 1]);      // the part's Q has been read
-          ahead.next_part(s_take);
-          ++s_part;
-          s_first = true;
-          if (ahead.left > 0) s_left = s_take = ahead.part();
-        }
-        return true;
-      };
-      bool ok = issue_s();
-      if (ok && total > 1) ok = issue_s();
-      int part = 0;
-      for (int n = 0; n < total && ok; ++part) {
+        if (ok) mma_commit(&q_empty[part & 1]);  // the part's Q has been read
+        cur.next_part(take);
+      }
+    }
+  } else if (warp == C::MMA_PV_WARP) {
+    // ------------------------------------------------------------ O += P V
+    // P(n) packed 16-bit in columns [0, 64) of buffer n % 2, O of a part in buffer
+    // part % 2.  Every use of a value slot gets its phase on the empty barrier: the
+    // producer, the score products and the rescale wait for it.
+    if (lane == 0) {
+      constexpr uint32_t idPV = idesc_f16(FP16 ? Elt::F16 : Elt::BF16, 128, D, false, true);
+      const uint64_t vdesc0 = sdesc_sw128(smem_u32(sKV), C::CHUNK, 1024);      // MN-major V
+      bool ok = true;
+      for (int n = 0, part = 0; n < total && ok; ++part) {
         const int take = cur.part();
         const uint32_t o_col = C::O_COL(part & 1);
-        for (int i = 0; i < take && ok; ++i, ++n) {
-          // O += P(n) V_n, P(n) packed 16-bit in columns [0, 64) of buffer n % 2
+        for (int i = 0; i < take; ++i, ++n) {
           const int item = 2 * n + 1, slot = item % NSLOT;
           if (!(ok = mbar_wait(&kv_full[slot], (item / NSLOT) & 1, ab, kDevTimeoutMma))) break;
           const uint64_t vdesc = opaque(sdesc_add(vdesc0, slot * C::TILE));
@@ -359,10 +354,8 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
           for (int kk = 0; kk < BN / 16; ++kk)
             mma_f16_ts(tmem + o_col, tmem + C::S_COL(n & 1) + 8 * kk, sdesc_add(vdesc, kk * 16 * 128), idPV,
                        (i > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&pv_done);
-          if (item + NSLOT < 2 * total) mma_commit(&kv_empty[slot]);
+          mma_commit(&kv_empty[slot]);
           if (i == take - 1) mma_commit(&o_full[part & 1]);
-          if (n + 2 < total) ok = issue_s();
         }
         cur.next_part(take);
       }
@@ -481,7 +474,7 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
     int n = 0, part = 0;
     while (ok && cur.left > 0) {
       const int take = cur.part();
-      const int len = keys_of(kp.kv_lens, cur.b, kp.Nk);
+      const int len = lens[cur.b];
       float m_ref = -INFINITY, l = 0.f;
       // a warp without query rows only keeps the others' pace
       const bool live = FEW || (cur.y % kp.qtiles) * BM + warp * 32 < kp.rows;
@@ -493,6 +486,7 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
           break;
         }
         tc_fence_after_sync();
+        if (r == 0) mbar_arrive(&kv_empty[(2 * n) % NSLOT]);   // K of tile n has been read
         const int lim = len - (cur.j + i) * BN;        // keys of this tile that are seen
         if (live) {
           const uint32_t tS = tmem + lane_addr + C::S_COL(n & 1);
@@ -552,7 +546,9 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
           if (i > 0 && __any_sync(0xffffffffu, need)) {
             // rescale O once P(n - 1) V has landed; this tile's product is issued
             // only after the arrive below
-            if (__any_sync(0xffffffffu, !mbar_wait(&pv_done, (n - 1) & 1, ab, kDevTimeoutSoftmax))) {
+            const int old = 2 * n - 1;           // item of V of tile n - 1
+            if (__any_sync(0xffffffffu, !mbar_wait(&kv_empty[old % NSLOT], (old / NSLOT) & 1, ab,
+                                                   kDevTimeoutSoftmax))) {
               ok = false;
               break;
             }
@@ -620,13 +616,14 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
       if (kv == 0)
         for (int i = parts_sh - 1; i >= 0 && i >= parts_sh - 2; --i) mbar_wait_drain(&q_full[i & 1], (i >> 1) & 1);
     }
-    if (warp == C::MMA_WARP && lane == 0) {
-      mma_commit(&drain_bar);
-      mbar_wait_drain(&drain_bar, 0);
+    if ((warp == C::MMA_S_WARP || warp == C::MMA_PV_WARP) && lane == 0) {
+      uint64_t* bar = &drain_bar[warp == C::MMA_S_WARP ? 0 : 1];
+      mma_commit(bar);
+      mbar_wait_drain(bar, 0);
     }
     __syncthreads();
   }
-  if (warp == C::MMA_WARP) {
+  if (warp == C::MMA_S_WARP) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }

@@ -147,6 +147,29 @@ def test_split_key_ranges(attn):
     _check(attn, 1, 8, 1, 16, 3333, 64, "fp16", backward=False, seed=951)
 
 
+@pytest.mark.parametrize("d,dtype", [(64, "fp16"), (128, "bf16")])
+def test_shares_over_several_query_tiles(attn, d, dtype):
+    """A few hundred rows per key/value head over many keys: segments of several query
+    tiles that begin and end inside shares, some batch entries without keys."""
+    _check(attn, 3, 4, 2, 70, 2000, d, dtype, lens=[1999, 0, 700], backward=False, seed=952)
+    _check(attn, 1, 2, 1, 130, 3000, d, dtype, backward=False, seed=953)
+
+
+def test_many_entries(attn):
+    """More batch entries than threads, most of them short or empty; and more than the
+    shared plan takes."""
+    lens = [(7 * b) % 5 * 30 for b in range(600)]
+    _check(attn, 600, 2, 1, 1, 400, 64, lens=lens, backward=False, seed=954)
+    B = 2049
+    q, k, v, _ = _inputs(955, B, 1, 1, 1, 3, 64, "bf16")
+    o, lse = attn.attn_cross_fwd(q.to(dev()), k.to(dev()), v.to(dev()))
+    check_status(attn)
+    f = [workloads.as_f64(t) for t in (q, k, v)]
+    ref, l = oracle.attention_cross_forward(*f, 64 ** -0.5)
+    _within(o, ref, _forward_bound(*f, ref, 64 ** -0.5, None, "bf16"), "o")
+    _lse_close(lse, l)
+
+
 def test_large_scores(attn):
     """Scores that grow along the keys by far more than the lazy rescale's 2^8."""
     q, k, v, do = _inputs(960, 1, 2, 2, 130, 400, 64, "bf16")
