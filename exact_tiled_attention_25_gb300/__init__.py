@@ -50,7 +50,7 @@ __all__ = ["AttnError", "attn_fwd", "attn_fwd_schedule", "attn_fwd_gqa", "attn_f
            "attn_fwd_fp8_gqa", "attn_fwd_fp8_schedule", "attn_selftest_exp2", "attn_fp8_quantize_varlen", "attn_fwd_fp8_varlen",
            "attn_fp8_quantize_bf16", "attn_fp8_quantize_ex",
            "attn_decode_paged", "attn_decode_paged_fp8", "attn_decode_workspace_size",
-           "attn_cross_fwd", "attn_cross_bwd", "attn_cross_workspace_size",
+           "attn_cross_fwd", "attn_cross_bwd", "attn_cross_workspace_size", "attn_cross_bwd_workspace_size",
            "attn_rope", "attn_rope_table", "attn_block_tables",
            "attn_cache_append", "attn_cache_append_fp8",
            "attn_get_device_status",
@@ -792,6 +792,10 @@ def attn_cross_workspace_size(B: int, H: int, H_kv: int, N_q: int, N_k: int, d: 
     return int(_lib.load().attn_cross_workspace_size(B, H, H_kv, N_q, N_k, d))
 
 
+def attn_cross_bwd_workspace_size(B: int, H: int, N_q: int, N_k: int, d: int) -> int:
+    return int(_lib.load().attn_cross_bwd_workspace_size(B, H, N_q, N_k, d))
+
+
 def attn_cross_fwd(q, k, v, kv_lens=None, softmax_scale: float | None = None, o=None, lse=None,
                    workspace=None, stream=None):
     """Cross attention: q [B, H, N_q, d] against k, v [B, H_kv, N_k, d], of which
@@ -854,7 +858,8 @@ def attn_cross_bwd(q, k, v, o, dout, lse, kv_lens=None, softmax_scale: float | N
     else:
         _like(dv, "dv", v.shape, v.dtype)
     if workspace is None:
-        workspace = torch.empty(lib.attn_bwd_workspace_size(B, H, N_q, d), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(lib.attn_cross_bwd_workspace_size(B, H, N_q, N_k, d), dtype=torch.uint8,
+                                device=q.device)
     code = lib.attn_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(),
                               _ptr(kv_lens), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
                               workspace.nbytes, B, H, H_kv, N_q, N_k, d,

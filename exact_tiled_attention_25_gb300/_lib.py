@@ -89,6 +89,7 @@ SIGNATURES = {
                              c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_float,
                              c_void_p]),
     "attn_cross_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
+    "attn_cross_bwd_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
     "attn_cross_fwd": (c_int, [c_void_p] * 7 + [c_size_t] + [c_int] * 6 + [c_float, c_int, c_void_p]),
     "attn_cross_bwd": (c_int, [c_void_p] * 11 + [c_size_t] + [c_int] * 6 + [c_float, c_int, c_void_p]),
     "attn_rope_table": (c_int, [c_void_p, c_void_p, c_longlong, c_int, c_double, c_double, c_longlong,

@@ -766,6 +766,11 @@ attn_status_t attn_cross_fwd(const void* q, const void* k, const void* v, const 
   return plan.ctas > 0 ? launch_cross_rows(p, plan, workspace, stream) : launch_cross_fwd(p, stream);
 }
 
+size_t attn_cross_bwd_workspace_size(int B, int H, int N_q, int N_k, int d) {
+  if (B < 1 || H < 1 || N_q < 1 || N_k < 1 || d < 1) return 0;
+  return cross_bwd_plan(B, H, N_q, N_k, d).total;
+}
+
 attn_status_t attn_cross_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout,
                              const float* lse, const int* kv_lens, void* dq, void* dk, void* dv,
                              void* workspace, size_t workspace_bytes, int B, int H, int H_kv, int N_q,
@@ -779,16 +784,17 @@ attn_status_t attn_cross_bwd(const void* q, const void* k, const void* v, const 
   if ((s = check_dtype(dtype)) != ATTN_OK) return s;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(ATTN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  if (workspace_bytes < attn_bwd_workspace_size(B, H, N_q, d))
-    return fail(ATTN_ERR_INVALID_ARG, "workspace smaller than attn_bwd_workspace_size(B, H, N_q, d)");
+  const CrossBwdPlan plan = cross_bwd_plan(B, H, N_q, N_k, d);
+  if (workspace_bytes < plan.total)
+    return fail(ATTN_ERR_INVALID_ARG, "workspace smaller than attn_cross_bwd_workspace_size()");
   if (d == 256) return fail(ATTN_ERR_UNSUPPORTED, "the backward pass supports d = 64 and 128");
+  if (plan.steps > 2147483647LL) return fail(ATTN_ERR_UNSUPPORTED, "over 2^31 tile pairs");
   if ((s = check_device()) != ATTN_OK) return s;
-  const BwdWorkspace w = bwd_workspace_layout(B, H, N_q, d);
   char* ws = static_cast<char*>(workspace);
-  BwdParams p{q, k, v, o, dout, lse, dq, dk, dv, reinterpret_cast<float*>(ws + w.dq_acc),
-              reinterpret_cast<float*>(ws + w.lse2), reinterpret_cast<float*>(ws + w.delta),
+  BwdParams p{q, k, v, o, dout, lse, dq, dk, dv, reinterpret_cast<float*>(ws + plan.w.dq_acc),
+              reinterpret_cast<float*>(ws + plan.w.lse2), reinterpret_cast<float*>(ws + plan.w.delta),
               B, H, N_q, d, H_kv, nullptr, 0, 0, softmax_scale, dtype == ATTN_FP16 ? 1 : 0, N_k, kv_lens};
-  return launch_cross_bwd(p, stream);
+  return launch_cross_bwd(p, reinterpret_cast<float*>(ws + plan.part), plan.ctas, stream);
 }
 
 attn_status_t attn_rope_table(float* rope_cos, float* rope_sin, long long n, int rot_dim, double base,

@@ -28,74 +28,12 @@
 //     the float32 accumulator with a TMA reduce-add, so the reduction runs in
 //     the TMA unit and L2 instead of as per-thread atomics.
 //  3. convert: dQ = scale * accumulator, rounded to the 16-bit type.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <cmath>
 
-#include "common.h"
-#include "sm103_prims.cuh"
+#include "bwd_parts.cuh"
 
 namespace attn {
 namespace {
-
-constexpr int kSmemLimit = 232448;
-constexpr float kLog2e = 1.4426950408889634f;
-
-__host__ __device__ constexpr int cmin(int a, int b) { return a < b ? a : b; }
-
-template <int D>
-struct BwdCfg {
-  static constexpr int BM = 128;                 // query rows per step
-  static constexpr int BN = 128;                 // keys per CTA
-  static constexpr int CH = D / 64;              // 128-byte chunks per row
-  static constexpr int CHUNK = 128 * 128;        // one 128-row x 128-byte chunk
-  static constexpr int TILE = 128 * D * 2;       // a K, V, Q or dO tile
-  // Q_i (with its row vectors) and dO_i have rings of their own: Q_i is read
-  // by S^T(i) early and dK late, dO_i only by dP^T(i) and dV.  At d = 128 one
-  // dO slot is all that fits next to the dQ staging buffers.
-  static constexpr int NQS = 2;                  // Q ring slots
-  static constexpr int NDS = (D == 128) ? 1 : 2; // dO ring slots
-  static constexpr int OFF_K = 0;
-  static constexpr int OFF_V = TILE;
-  static constexpr int OFF_Q = 2 * TILE;
-  static constexpr int OFF_DO = OFF_Q + NQS * TILE;
-  static constexpr int OFF_DS = OFF_DO + NDS * TILE;      // dS^T, 128 keys x 128 queries
-  // dQ staging: one 32-query x 32-column float32 box (4 KB, 128-byte swizzle)
-  // per reduce warp, handed to a TMA reduce-add into the float32 accumulator
-  static constexpr int STG_BOX = 32 * 32 * 4;
-  static constexpr int OFF_STG = OFF_DS + 2 * CHUNK;
-  static constexpr int OFF_LD = OFF_STG + 8 * STG_BOX;    // per Q slot: L*log2e[128], D[128]
-  static constexpr int OFF_BAR = OFF_LD + NQS * 1024;
-  static constexpr int NEED = OFF_BAR + 256;
-  static constexpr int SMEM_BYTES = cmin(kSmemLimit, NEED + 1024);
-  static constexpr int SLACK = SMEM_BYTES - NEED;   // room to align the base to 1024
-  // TMEM columns: S^T/P^T [0,128), dP^T/dS^T [128,256), dV, dK.  At d = 128
-  // there is no room left, so dQ reuses the dP^T columns (after dK has read
-  // dS^T there); at d = 64 dQ has its own columns.  dQ is stored with one
-  // query per TMEM lane.
-  static constexpr bool DQ_IN_DP = (D == 128);
-  static constexpr uint32_t S_COL = 0;
-  static constexpr uint32_t DP_COL = 128;
-  static constexpr uint32_t DV_COL = 256;
-  static constexpr uint32_t DK_COL = 256 + D;
-  static constexpr uint32_t DQ_COL = DQ_IN_DP ? DP_COL : 256 + 2 * D;
-  // Warps 0-7: two compute warpgroups (one per half of the 128 query columns);
-  // warps 8-15: two reduce warpgroups (one per half of dQ's columns);
-  // warp 16: TMA producer; warp 17: MMA issuer.
-  static constexpr int THREADS = 576;
-  static constexpr int LOAD_WARP = 16;
-  static constexpr int MMA_WARP = 17;
-  // Packed 16-bit P^T / dS^T of query half h sit in columns [64 h, 64 h + 32) of
-  // the S^T / dP^T region, inside the half's own fp32 columns, so each
-  // warpgroup overwrites only scores it has already read.
-  __host__ __device__ static constexpr uint32_t half_col(int kk) {
-    return 64u * static_cast<uint32_t>(kk / 4) + 8u * static_cast<uint32_t>(kk % 4);
-  }
-  static_assert(DQ_COL + D <= 512 && DK_COL + D <= 512, "TMEM overflow");
-  static_assert(SLACK >= 0, "shared memory overflow");
-  static_assert(OFF_STG % 1024 == 0, "staging boxes need 1024-byte alignment (swizzle atoms)");
-};
 
 struct Bars {
   uint64_t kv_full;
@@ -115,9 +53,7 @@ struct Bars {
   int abort_flag;
   int q_items;     // Q slots the producer filled (for draining after an abort)
   int do_items;    // dO slots the producer filled
-  uint64_t kv_clean;   // cross attention: rows of K and V behind the keys are zeroed
 };
-static_assert(sizeof(Bars) <= 256, "barrier area overflow");
 
 struct BwdKParams {
   void* dk;
@@ -135,85 +71,7 @@ struct BwdKParams {
   int group;               // query heads per key/value head
   float scale;
   float scale_log2;
-  int Nk;                  // cross attention: keys of every sequence (N counts queries)
-  const int* kv_lens;      // cross attention: keys each batch entry sees, or nullptr
 };
-
-// Sequence b of a packed batch: first token and length, or false when its
-// offsets do not fit (outside [0, total], decreasing, or longer than max_len).
-__device__ __forceinline__ bool packed_seq(const int* cu, int b, int total, int max_len, int& s0,
-                                           int& len) {
-  s0 = cu[b];
-  const int e = cu[b + 1];
-  if (s0 < 0 || e < s0 || e > total || e - s0 > max_len) return false;
-  len = e - s0;
-  return true;
-}
-
-// ------------------------------------------------------------------ prep ----
-// One group of D/8 lanes per row; each lane holds 8 consecutive elements.
-// Rows of O, dO and dQ are [B, H, N, d] or, for a packed batch (PACKED),
-// [total, H, d] with LSE [H, total].
-template <int D, bool FP16, bool PACKED>
-__global__ void __launch_bounds__(256)
-    bwd_prep_kernel(const uint16_t* __restrict__ o, const uint16_t* __restrict__ dout,
-                    const float* __restrict__ lse, float* __restrict__ lse2,
-                    float* __restrict__ delta, float* __restrict__ dq_acc, int N, int Npad,
-                    long long total_rows_pad, int H, const int* __restrict__ cu_seqlens,
-                    int total) {
-  constexpr int L = D / 8;
-  constexpr int ROWS_PER_WARP = 32 / L;
-  const int lane = threadIdx.x & 31;
-  const int sub = lane / L;
-  const int li = lane % L;
-  const long long warp_global = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
-  const long long prow = warp_global * ROWS_PER_WARP + sub;   // padded row index
-  if (prow >= total_rows_pad) return;
-  const long long bh = prow / Npad;
-  const int n = static_cast<int>(prow - bh * Npad);
-  int len = N;
-  long long row, lrow;     // row of O / dO / dQ, index into LSE
-  if constexpr (PACKED) {
-    const int b = static_cast<int>(bh / H), h = static_cast<int>(bh % H);
-    int s0 = 0;
-    if (!packed_seq(cu_seqlens, b, total, N, s0, len)) len = 0;   // reported by the main kernel
-    row = (static_cast<long long>(s0) + n) * H + h;
-    lrow = static_cast<long long>(h) * total + s0 + n;
-  } else {
-    row = bh * N + n;
-    lrow = row;
-  }
-  float acc = 0.f;
-  if (n < len) {
-    const uint4 a = reinterpret_cast<const uint4*>(o + row * D)[li];
-    const uint4 b = reinterpret_cast<const uint4*>(dout + row * D)[li];
-    const uint32_t av[4] = {a.x, a.y, a.z, a.w};
-    const uint32_t bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float2 fa, fb;
-      if (FP16) {
-        fa = __half22float2(*reinterpret_cast<const __half2*>(&av[e]));
-        fb = __half22float2(*reinterpret_cast<const __half2*>(&bv[e]));
-      } else {
-        fa = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&av[e]));
-        fb = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv[e]));
-      }
-      acc = fmaf(fa.x, fb.x, acc);
-      acc = fmaf(fa.y, fb.y, acc);
-    }
-    float4* z = reinterpret_cast<float4*>(dq_acc + row * D) + 2 * li;
-    z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
-    z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-#pragma unroll
-  for (int off = L / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-  if (li == 0) {
-    // stored negated so the main kernel adds them with packed f32x2 FMAs
-    delta[prow] = (n < len) ? -acc : 0.f;
-    lse2[prow] = (n < len) ? -lse[lrow] * kLog2e : -INFINITY;
-  }
-}
 
 // --------------------------------------------------------------- convert ----
 template <bool FP16>
@@ -241,13 +99,7 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------ main ----
-// CROSS: keys of another length than the queries (K, V, dK, dV [B, H_kv, Nk, d]),
-// of which batch entry b sees the first kv_lens[b]; rows of dK and dV behind
-// them are written as zeros.  The rows of K and V there may hold anything, NaN
-// included, so the compute warps zero them in shared memory before the first
-// product: zero rows give S = dP = 0, and P is set to 0 for them as for rows
-// past the tensor.
-template <int D, bool CAUSAL, bool FP16, bool PACKED, bool CROSS = false>
+template <int D, bool CAUSAL, bool FP16, bool PACKED>
 __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -269,7 +121,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   // One CTA per (key tile j, key/value head hk, batch b).  Causal: a 1-D grid
   // ordered by work, key tile 0 (which meets every query tile) of every head
   // first.  Non-causal: (tile, head, batch).
-  const int ntiles = ((CROSS ? kp.Nk : kp.N) + C::BN - 1) / C::BN;
+  const int ntiles = (kp.N + C::BN - 1) / C::BN;
   const int j = CAUSAL ? static_cast<int>(blockIdx.x / (gridDim.x / ntiles)) : static_cast<int>(blockIdx.x);
   const int bhk = CAUSAL ? static_cast<int>(blockIdx.x % (gridDim.x / ntiles))
                          : static_cast<int>(blockIdx.z * kp.H_kv + blockIdx.y);
@@ -284,29 +136,6 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       return;
     }
     if (j * C::BN >= N) return;
-  }
-  int Nkv = N;                             // keys this batch entry sees
-  bool clean = false;                      // rows of this key tile to zero
-  if constexpr (CROSS) {
-    static_assert(!CAUSAL && !PACKED, "cross attention is neither causal nor packed");
-    Nkv = kp.Nk;
-    if (kp.kv_lens) {
-      const int n = kp.kv_lens[b];
-      const bool bad = n < 0 || n > kp.Nk;
-      if (bad && threadIdx.x == 0 && j == 0) atomicCAS(kp.status, 0, kDevBadSeqlens);
-      Nkv = bad ? 0 : n;
-    }
-    if (j * C::BN >= Nkv) {
-      // no key of this tile is seen: its rows of dK and dV are zero
-      const int rows = min(C::BN, kp.Nk - j * C::BN);
-      const size_t first = (static_cast<size_t>(bhk) * kp.Nk + j * C::BN) * D;
-      uint4* zk = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kp.dk) + first);
-      uint4* zv = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kp.dv) + first);
-      for (int x = threadIdx.x; x < rows * (D / 8); x += C::THREADS)
-        zk[x] = zv[x] = make_uint4(0u, 0u, 0u, 0u);
-      return;
-    }
-    clean = Nkv < kp.Nk && (j + 1) * C::BN > Nkv;
   }
   const int nQ = (N + C::BM - 1) / C::BM;
   const int i0 = CAUSAL ? j : 0;
@@ -333,7 +162,6 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     mbar_init(&bars.dq_free, 256);
     mbar_init(&bars.dkv_full, 1);
     mbar_init(&bars.drain, 1);
-    if constexpr (CROSS) mbar_init(&bars.kv_clean, 256);
     bars.abort_flag = 0;
     bars.q_items = 0;
     bars.do_items = 0;
@@ -466,7 +294,6 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       // warpgroups form P^T(n), and their dS phase starts as soon as P^T(n) is
       // written; the P phase of step n+1 overlaps dK(n), dQ(n).
       bool ok = mbar_wait(&bars.kv_full, 0, ab, kDevTimeoutMma) && wait_q(0);
-      if constexpr (CROSS) ok = ok && (!clean || mbar_wait(&bars.kv_clean, 0, ab, kDevTimeoutMma));
       if (ok) {
         tc_fence_after_sync();
         issue_s(slot_q(0));
@@ -526,25 +353,12 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     const int k = quarter * 32 + lane;               // key row of the tile = TMEM lane
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const int key_g = j * C::BN + k;
-    const bool key_ok = key_g < Nkv;
+    const bool key_ok = key_g < N;
     const float c2 = kp.scale_log2;
     const uint32_t sDSrow = smem_u32(smem + C::OFF_DS) + h * C::CHUNK + k * 128;
     bool ok = true;
-    if constexpr (CROSS) {
-      if (clean) {
-        // on a timeout nothing is signalled, and every other wait gives up too
-        ok = mbar_wait(&bars.kv_full, 0, ab, kDevTimeoutSoftmax);
-        if (ok) {
-          const int row0 = Nkv - j * C::BN;
-          zero_tile_rows<C::CH, C::CHUNK>(smem + C::OFF_K, row0, threadIdx.x, 256);
-          zero_tile_rows<C::CH, C::CHUNK>(smem + C::OFF_V, row0, threadIdx.x, 256);
-          fence_proxy_async_smem();
-          mbar_arrive(&bars.kv_clean);
-        }
-      }
-    }
     int i = i0;                                      // query tile of step n
-    for (int n = 0; (!CROSS || ok) && n < nsteps; ++n, i = (i + 1 == nQ) ? i0 : i + 1) {
+    for (int n = 0; n < nsteps; ++n, i = (i + 1 == nQ) ? i0 : i + 1) {
       const int st = n % C::NQS;
       const float4* nlse4 = reinterpret_cast<const float4*>(smem + C::OFF_LD + st * 1024);  // -L log2 e
       const float4* ndvec4 = nlse4 + 32;                                                  // -D
@@ -653,7 +467,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       const float mul = h ? kp.scale : 1.f;
       // [B, H_kv, N, d], or [total, H_kv, d] for a packed batch
       const size_t krow = PACKED ? static_cast<size_t>(seq0 + key_g) * kp.H_kv + hk
-                                 : static_cast<size_t>(bhk) * (CROSS ? kp.Nk : N) + key_g;
+                                 : static_cast<size_t>(bhk) * N + key_g;
       uint16_t* dst_row = static_cast<uint16_t*>(h ? kp.dk : kp.dv) + krow * D;
 #pragma unroll 1
       for (int c0 = 0; c0 < D / 32; ++c0) {
@@ -663,12 +477,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float a = __uint_as_float(v[2 * e]) * mul;
-          float b = __uint_as_float(v[2 * e + 1]) * mul;
-          if (CROSS && !key_ok) a = b = 0.f;   // behind the keys, whatever dO holds
+          const float a = __uint_as_float(v[2 * e]) * mul;
+          const float b = __uint_as_float(v[2 * e + 1]) * mul;
           pk[e] = FP16 ? cvt_pack_f16(a, b) : cvt_pack_bf16(a, b);
         }
-        if (CROSS ? key_g < kp.Nk : key_ok) {
+        if (key_ok) {
           uint4* dst = reinterpret_cast<uint4*>(dst_row + c0 * 32);
 #pragma unroll
           for (int x = 0; x < 4; ++x)
@@ -757,7 +570,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   }
 }
 
-template <int D, bool CAUSAL, bool FP16, bool PACKED, bool CROSS = false>
+template <int D, bool CAUSAL, bool FP16, bool PACKED>
 attn_status_t launch_bwd_t(const BwdParams& p, cudaStream_t stream) {
   using C = BwdCfg<D>;
   const int Npad = (p.N + 127) / 128 * 128;
@@ -774,8 +587,7 @@ attn_status_t launch_bwd_t(const BwdParams& p, cudaStream_t stream) {
   }
   // 2. main
   {
-    auto kern = bwd_main_kernel<D, CAUSAL, FP16, PACKED, CROSS>;
-    const int N_keys = CROSS ? p.N_k : p.N;
+    auto kern = bwd_main_kernel<D, CAUSAL, FP16, PACKED>;
     attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES);
     if (s != ATTN_OK) return s;
     CUtensorMap tq, tk, tv, tdo, tdq;
@@ -799,8 +611,8 @@ attn_status_t launch_bwd_t(const BwdParams& p, cudaStream_t stream) {
       const uint64_t pq = static_cast<uint64_t>(p.B) * p.H, pkv = static_cast<uint64_t>(p.B) * p.H_kv;
       if ((s = make_tmap_3d(&tq, p.q, 2, D, p.N, pq, 64, 128)) != ATTN_OK) return s;
       if ((s = make_tmap_3d(&tdo, p.dout, 2, D, p.N, pq, 64, 128)) != ATTN_OK) return s;
-      if ((s = make_tmap_3d(&tk, p.k, 2, D, N_keys, pkv, 64, 128)) != ATTN_OK) return s;
-      if ((s = make_tmap_3d(&tv, p.v, 2, D, N_keys, pkv, 64, 128)) != ATTN_OK) return s;
+      if ((s = make_tmap_3d(&tk, p.k, 2, D, p.N, pkv, 64, 128)) != ATTN_OK) return s;
+      if ((s = make_tmap_3d(&tv, p.v, 2, D, p.N, pkv, 64, 128)) != ATTN_OK) return s;
       // float32 dQ accumulator [B * H, N, d]: reduce boxes of 32 rows x 32 columns
       if ((s = make_tmap_3d(&tdq, p.dq_acc, 4, D, p.N, pq, 32, 32)) != ATTN_OK) return s;
     }
@@ -808,8 +620,8 @@ attn_status_t launch_bwd_t(const BwdParams& p, cudaStream_t stream) {
     if (!status) return fail(ATTN_ERR_CUDA, "status word unavailable");
     BwdKParams kp{p.dk,  p.dv,    p.dq_acc, p.lse2, p.delta, status,        p.cu_seqlens,
                   p.N,   Npad,    p.total,  p.H,    p.H_kv,  p.H / p.H_kv,  p.scale,
-                  p.scale * kLog2e, N_keys, p.kv_lens};
-    const unsigned ntiles = static_cast<unsigned>((N_keys + 127) / 128);
+                  p.scale * kLog2e};
+    const unsigned ntiles = static_cast<unsigned>((p.N + 127) / 128);
     const dim3 grid = CAUSAL ? dim3(ntiles * p.H_kv * p.B, 1, 1) : dim3(ntiles, p.H_kv, p.B);
     kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(tq, tk, tv, tdo, tdq, kp);
     cudaError_t e = cudaGetLastError();
@@ -853,19 +665,6 @@ attn_status_t launch_bwd(const BwdParams& p, cudaStream_t stream) {
   switch (p.d) {
     case 64: return launch_bwd_d<64>(p, stream);
     case 128: return launch_bwd_d<128>(p, stream);
-  }
-  return fail(ATTN_ERR_UNSUPPORTED, "the backward pass supports d = 64 and 128");
-}
-
-attn_status_t launch_cross_bwd(const BwdParams& p, cudaStream_t stream) {
-  if (p.H > 65535 || p.B > 65535) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
-  switch (p.d) {
-    case 64:
-      return p.fp16 ? launch_bwd_t<64, false, true, false, true>(p, stream)
-                    : launch_bwd_t<64, false, false, false, true>(p, stream);
-    case 128:
-      return p.fp16 ? launch_bwd_t<128, false, true, false, true>(p, stream)
-                    : launch_bwd_t<128, false, false, false, true>(p, stream);
   }
   return fail(ATTN_ERR_UNSUPPORTED, "the backward pass supports d = 64 and 128");
 }

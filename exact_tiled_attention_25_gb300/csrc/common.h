@@ -124,9 +124,10 @@ attn_status_t launch_fwd_sched(const FwdParams& p, int sched, cudaStream_t strea
 // Persistent forward (cluster launch control) for packed causal batches.
 attn_status_t launch_fwd_persistent(const FwdParams& p, cudaStream_t stream);
 attn_status_t launch_bwd(const BwdParams& p, cudaStream_t stream);
-// Cross attention (N_k keys): one query tile pair per CTA, and its backward.
+// Cross attention (N_k keys): one query tile pair per CTA, and its backward on `ctas`
+// CTAs with `part` for their partial dK and dV.
 attn_status_t launch_cross_fwd(const FwdParams& p, cudaStream_t stream);
-attn_status_t launch_cross_bwd(const BwdParams& p, cudaStream_t stream);
+attn_status_t launch_cross_bwd(const BwdParams& p, float* part, int ctas, cudaStream_t stream);
 attn_status_t launch_fp8_quantize(const Fp8QuantParams& p, cudaStream_t stream);
 attn_status_t launch_fwd_fp8(const Fp8FwdParams& p, cudaStream_t stream);
 
@@ -259,5 +260,24 @@ inline size_t cross_workspace_bytes(int H, int H_kv, int N_q, int d, const Cross
 }
 attn_status_t launch_cross_rows(const FwdParams& p, const CrossPlan& plan, void* workspace,
                                 cudaStream_t stream);
+
+// The cross-attention backward's CTAs, sharing the steps of all key tiles (a step: a key
+// tile with a query tile of one query head), and its scratch: the backward's, then
+// two float32 pairs of dV and dK tiles per CTA.
+struct CrossBwdPlan {
+  long long steps;      // with every key seen
+  int ctas;
+  BwdWorkspace w;
+  size_t part, total;   // byte offset of the pairs, bytes of all
+};
+inline CrossBwdPlan cross_bwd_plan(int B, int H, int N_q, int N_k, int d) {
+  CrossBwdPlan c;
+  c.steps = static_cast<long long>(B) * H * ((N_q + 127) / 128) * ((N_k + 127) / 128);
+  c.ctas = static_cast<int>(c.steps < 152 ? c.steps : 152);
+  c.w = bwd_workspace_layout(B, H, N_q, d);
+  c.part = c.w.total;
+  c.total = c.part + 2ull * c.ctas * 2 * 128 * d * sizeof(float);
+  return c;
+}
 
 }  // namespace attn

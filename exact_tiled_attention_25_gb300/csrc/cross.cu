@@ -445,8 +445,7 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
           uint32_t o[32];
           tmem_ld32(tmem + lane_addr + C::O_COL(buf) + c0 * 32, o);
           tmem_ld_wait();
-          if (!row_ok) continue;
-          if (done.whole) {
+          if (row_ok && done.whole) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kp.o) + (at0 + r) * D + c0 * 32);
             uint32_t pk[16];
 #pragma unroll
@@ -457,7 +456,7 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
 #pragma unroll
             for (int v = 0; v < 4; ++v)
               dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
-          } else {
+          } else if (row_ok) {
             float4* dst = reinterpret_cast<float4*>(kp.o_part + (part0 + r) * D + c0 * 32);
 #pragma unroll
             for (int v = 0; v < 8; ++v)

@@ -600,12 +600,14 @@ attn_status_t attn_cross_fwd(const void* q, const void* k, const void* v, const 
  *   q, o, dout, dq : [B, H, N_q, d];   k, v, dk, dv : [B, H_kv, N_k, d];   lse and
  *   kv_lens as there.  dK and dV rows behind kv_lens[b] are written as zeros, and
  *   dQ of a batch entry without keys is zero.
- *   workspace : attn_bwd_workspace_size(B, H, N_q, d) bytes, 256-byte aligned.
+ *   workspace : attn_cross_bwd_workspace_size() bytes, 256-byte aligned; calls that
+ *               overlap on the GPU need one each.
  * d = 64 or 128.  dK and dV are sums in a fixed order; dQ adds one float32
  * term per 128 keys in any order, as attn_bwd does, so its last bits may differ
  * between runs when N_k > 128.
  * Source: as attn_bwd.
  */
+size_t attn_cross_bwd_workspace_size(int B, int H, int N_q, int N_k, int d);
 attn_status_t attn_cross_bwd(const void* q, const void* k, const void* v, const void* o,
                              const void* dout, const float* lse, const int* kv_lens, void* dq,
                              void* dk, void* dv, void* workspace, size_t workspace_bytes, int B, int H,

@@ -44,7 +44,9 @@ def test_cross_workspaces(lib):
     assert _cross_fwd(lib, wsb=need - 1, **few) == 1 and b"workspace" in lib.attn_last_error()
     assert _cross_fwd(lib, ws=None, **few) == 1 and b"workspace" in lib.attn_last_error()
     assert _cross_fwd(lib, ws=16, **few) == 1 and b"256-byte" in lib.attn_last_error()
-    need = lib.attn_bwd_workspace_size(1, 4, 300, 128)
+    need = lib.attn_cross_bwd_workspace_size(1, 4, 300, 200, 128)
+    assert need > lib.attn_bwd_workspace_size(1, 4, 300, 128)
+    assert lib.attn_cross_bwd_workspace_size(1, 4, 0, 200, 128) == 0
     assert _cross_bwd(lib, wsb=need - 1) == 1 and b"workspace" in lib.attn_last_error()
     assert _cross_bwd(lib, ws=16) == 1 and b"256-byte" in lib.attn_last_error()
     assert _cross_bwd(lib, d=256) == 2
