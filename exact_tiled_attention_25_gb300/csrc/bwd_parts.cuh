@@ -84,13 +84,15 @@ __device__ __forceinline__ bool packed_seq(const int* cu, int b, int total, int 
 // One group of D/8 lanes per row; each lane holds 8 consecutive elements.
 // Rows of O, dO and dQ are [B, H, N, d] or, for a packed batch (PACKED),
 // [total, H, d] with LSE [H, total].
-template <int D, bool FP16, bool PACKED>
+// RELEASE: the main kernel may start its prologue while this one runs.
+template <int D, bool FP16, bool PACKED, bool RELEASE = false>
 __global__ void __launch_bounds__(256)
     bwd_prep_kernel(const uint16_t* __restrict__ o, const uint16_t* __restrict__ dout,
                     const float* __restrict__ lse, float* __restrict__ lse2,
                     float* __restrict__ delta, float* __restrict__ dq_acc, int N, int Npad,
                     long long total_rows_pad, int H, const int* __restrict__ cu_seqlens,
                     int total) {
+  if constexpr (RELEASE) release_dependents();
   constexpr int L = D / 8;
   constexpr int ROWS_PER_WARP = 32 / L;
   const int lane = threadIdx.x & 31;

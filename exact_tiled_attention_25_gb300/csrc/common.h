@@ -38,6 +38,24 @@ attn_status_t make_tmap_4d(CUtensorMap* map, const void* base, int elem_bytes, u
                            uint64_t head_bytes, uint64_t batch_bytes, uint32_t box_inner,
                            uint32_t box_rows, uint32_t box_heads = 1);
 
+// Launch a kernel that may start before the stream's previous kernel has ended (it
+// calls wait_for_previous_kernel() before it uses that one's results).
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                             Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Opt a kernel into more than 48 KB of dynamic shared memory (once per kernel).
 attn_status_t set_smem(const void* kernel, int bytes);
 

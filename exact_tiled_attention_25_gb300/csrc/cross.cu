@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
   const int lane = threadIdx.x % 32;
 
   // the merging kernel may start its prologue (it waits for this grid's end)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  release_dependents();
 
   // ---- prologue: tiles of a segment of the batch entries before each, while the
   // barriers are set up, tensor memory is allocated and the tensor maps arrive
@@ -671,9 +671,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int row0 = (y - hk * kp.qtiles) * BM;
   const int r = blockIdx.y * kMergeRows<D> + threadIdx.x / (D / 4);
   const int col = (threadIdx.x % (D / 4)) * 4;
-  // every block waits: one that returned before the first kernel's end could let the
-  // stream's next kernel start too early
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous_kernel();
   if (c0 == c1 || r >= min(BM, kp.rows - row0)) return;
   float m = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -744,17 +742,8 @@ attn_status_t launch_cross_rows_t(const FwdParams& p, const CrossPlan& plan, voi
   kern<<<plan.ctas, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, kp);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "cross attention rows kernel launch");
-  // launched while the first kernel runs; it waits for its end before reading
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kp.segs, (seg_rows + kMergeRows<D> - 1) / kMergeRows<D>, p.B);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, cross_merge_kernel<D, FP16>, kp, plan.ctas);
+  e = launch_dependent(cross_merge_kernel<D, FP16>, dim3(kp.segs, (seg_rows + kMergeRows<D> - 1) / kMergeRows<D>, p.B),
+                       kMergeThreads, 0, stream, kp, plan.ctas);
   if (e != cudaSuccess) return fail_cuda(e, "cross attention merge kernel launch");
   return ATTN_OK;
 }

@@ -79,6 +79,22 @@ __device__ __forceinline__ int seen_keys(const int* kv_lens, int b, int Nk) {
   return n < 0 || n > Nk ? 0 : n;
 }
 
+// CTAs that get a share of `segs` segments of nsteps steps, of the grid's `ctas`.
+// Loading a segment's K and V, its first step's latency and its output cost about
+// kPartSteps steps (8 us), and shares that cross segments pay that at least twice.
+// So with fewer segments than CTAs every segment may be cut into m equal parts, one
+// CTA each; otherwise, or where even shares of all CTAs come out ahead, all of them.
+// (31 tiles x 4 heads, 12 steps each, d = 64: one part each 27 us, even shares 32.)
+constexpr int kPartSteps = 5;
+__device__ __forceinline__ int share_count(int segs, int nsteps, int ctas) {
+  const int m = min(ctas / max(segs, 1), nsteps);
+  if (m == 0) return ctas;
+  const long long T = static_cast<long long>(segs) * nsteps;
+  const int even = static_cast<int>((T + ctas - 1) / ctas);
+  const int even_cost = even + kPartSteps * ((even + nsteps - 1) / nsteps + 1);
+  return (nsteps + m - 1) / m + kPartSteps <= even_cost ? segs * m : ctas;
+}
+
 // First step of CTA c's share of T steps; at most T CTAs get one.
 __device__ __forceinline__ int step_share(int c, int C, int T) {
   C = min(C, T);
@@ -126,6 +142,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   if (pad > static_cast<uint32_t>(C::SLACK)) {
     // Cannot place the swizzled tiles: report and leave before touching anything.
     if (threadIdx.x == 0) atomicCAS(kp.status, 0, kDevSmemMisaligned);
+    wait_for_previous_kernel();
     return;
   }
   uint8_t* smem = smem_raw + pad;
@@ -194,9 +211,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     all += warp_sum[w];
   }
   const int T = all * kp.H_kv * nsteps;
-  const int g0 = step_share(blockIdx.x, gridDim.x, T);
-  const int total = step_share(blockIdx.x + 1, gridDim.x, T) - g0;   // steps of this CTA
+  const int ctas = share_count(all * kp.H_kv, nsteps, gridDim.x);
+  const int g0 = step_share(blockIdx.x, ctas, T);
+  const int total = step_share(blockIdx.x + 1, ctas, T) - g0;        // steps of this CTA
   const int seg0 = g0 / nsteps;                                      // its first segment
+  release_dependents();
   if (total > 0 && seg0 >= base * kp.H_kv && seg0 < (base + sum) * kp.H_kv) {
     int at = base, b = b0;
     while (true) {
@@ -208,6 +227,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     bars.start[0] = b;
     bars.start[1] = seg0 - at * kp.H_kv;
   }
+  wait_for_previous_kernel();      // row vectors, and the dQ accumulator's zeros
   __syncthreads();
   const uint32_t tmem = bars.tmem_base;
   const Abort ab{&bars.abort_flag, kp.status};
@@ -216,9 +236,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     w.keys = seen_keys(kp.kv_lens, w.b, kp.Nk);
     // the CTA in whose share the first segment starts: the last c with c T / C <= start
     const long long start = static_cast<long long>(seg0) * nsteps;
-    const int ctas = min(static_cast<int>(gridDim.x), T);
-    const int c0 = static_cast<int>(((start + 1) * ctas - 1) / T);
-    w.rot = static_cast<int>(start - step_share(c0, ctas, T)) % nsteps;
+    const int C0 = min(ctas, T);
+    const int c0 = static_cast<int>(((start + 1) * C0 - 1) / T);
+    w.rot = static_cast<int>(start - step_share(c0, C0, T)) % nsteps;
   }
 
   // Every barrier's phase below follows the CTA's own count of steps (n) or of
@@ -621,7 +641,7 @@ constexpr int kJoinRows = 16;
 template <int D, bool FP16>
 __global__ void __launch_bounds__(256)
     cross_bwd_join_kernel(const XBwdKParams kp, int ctas, int ktiles, unsigned join_blocks,
-                          const float* __restrict__ acc, uint16_t* __restrict__ dq, long long n8) {
+                          const float* acc, uint16_t* dq, long long n8) {
   auto pack8 = [](const float4& a, const float4& b, float m) {
     return FP16 ? make_uint4(cvt_pack_f16(a.x * m, a.y * m), cvt_pack_f16(a.z * m, a.w * m),
                              cvt_pack_f16(b.x * m, b.y * m), cvt_pack_f16(b.z * m, b.w * m))
@@ -629,6 +649,7 @@ __global__ void __launch_bounds__(256)
                              cvt_pack_bf16(b.x * m, b.y * m), cvt_pack_bf16(b.z * m, b.w * m));
   };
   if (blockIdx.x >= join_blocks) {
+    wait_for_previous_kernel();
     const unsigned blocks = gridDim.x - join_blocks;
     for (long long i = static_cast<long long>(blockIdx.x - join_blocks) * 256 + threadIdx.x; i < n8;
          i += static_cast<long long>(blocks) * 256) {
@@ -670,7 +691,7 @@ __global__ void __launch_bounds__(256)
   if (j < kt) {
     const int T = all * kp.H_kv * nsteps;
     const long long g0 = static_cast<long long>(before * kp.H_kv + hk * kt + j) * nsteps, g1 = g0 + nsteps - 1;
-    const int C = min(ctas, T);
+    const int C = min(share_count(all * kp.H_kv, nsteps, ctas), T);
     // CTA whose share holds step g: the last c with c T / C <= g
     c0 = static_cast<int>(((g0 + 1) * C - 1) / T);
     c1 = static_cast<int>(((g1 + 1) * C - 1) / T);
@@ -678,6 +699,7 @@ __global__ void __launch_bounds__(256)
     // part only where it starts inside a share
     slot0 = 2 * c0 + (step_share(c0, C, T) == g0 ? 0 : 1);
   }
+  wait_for_previous_kernel();
   const int rows = min(kJoinRows, kp.Nk - j * 128 - r0);
   const size_t first = (static_cast<size_t>(bhk) * kp.Nk + j * 128 + r0) * D;
   for (int i = threadIdx.x; i < 2 * rows * (D / 8); i += 256) {
@@ -722,7 +744,7 @@ attn_status_t launch_cross_bwd_t(const BwdParams& p, float* part, int ctas, cuda
   {
     constexpr int rows_per_block = 8 * (32 / (D / 8));
     const long long blocks = (rows_pad + rows_per_block - 1) / rows_per_block;
-    bwd_prep_kernel<D, FP16, false><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+    bwd_prep_kernel<D, FP16, false, true><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
         static_cast<const uint16_t*>(p.o), static_cast<const uint16_t*>(p.dout), p.lse, p.lse2,
         p.delta, p.dq_acc, p.N, Npad, rows_pad, p.H, nullptr, 0);
     e = cudaGetLastError();
@@ -744,8 +766,7 @@ attn_status_t launch_cross_bwd_t(const BwdParams& p, float* part, int ctas, cuda
     if ((s = make_tmap_3d(&tk, p.k, 2, D, p.N_k, pkv, 64, 128)) != ATTN_OK) return s;
     if ((s = make_tmap_3d(&tv, p.v, 2, D, p.N_k, pkv, 64, 128)) != ATTN_OK) return s;
     if ((s = make_tmap_3d(&tdq, p.dq_acc, 4, D, p.N, pq, 32, 32)) != ATTN_OK) return s;
-    kern<<<ctas, C::THREADS, C::SMEM_BYTES, stream>>>(tq, tk, tv, tdo, tdq, kp);
-    e = cudaGetLastError();
+    e = launch_dependent(kern, dim3(ctas), C::THREADS, C::SMEM_BYTES, stream, tq, tk, tv, tdo, tdq, kp);
     if (e != cudaSuccess) return fail_cuda(e, "cross-attention backward main launch");
   }
   // 3. join dK and dV, convert dQ
@@ -754,9 +775,8 @@ attn_status_t launch_cross_bwd_t(const BwdParams& p, float* part, int ctas, cuda
   const long long n8 = static_cast<long long>(p.B) * p.H * p.N * D / 8;
   const long long want = (n8 + 255) / 256;
   const long long convert = want < 152 * 16 ? want : 152 * 16;
-  cross_bwd_join_kernel<D, FP16><<<static_cast<unsigned>(join + convert), 256, 0, stream>>>(
-      kp, ctas, ktiles, static_cast<unsigned>(join), p.dq_acc, static_cast<uint16_t*>(p.dq), n8);
-  e = cudaGetLastError();
+  e = launch_dependent(cross_bwd_join_kernel<D, FP16>, dim3(static_cast<unsigned>(join + convert)), 256, 0, stream,
+                       kp, ctas, ktiles, static_cast<unsigned>(join), p.dq_acc, static_cast<uint16_t*>(p.dq), n8);
   if (e != cudaSuccess) return fail_cuda(e, "cross-attention backward join launch");
   return ATTN_OK;
 }

@@ -150,6 +150,18 @@ __device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity) 
   }
 }
 
+// Dependent launches: a kernel launched with the programmatic-serialisation attribute
+// may start once every block of the kernel before it has released it (or ended), and
+// waits for that kernel's end, its writes included, before it touches them.  Every
+// block of such a kernel waits, also one with nothing to do: if all ended early, the
+// stream's next kernel could overtake the first.
+__device__ __forceinline__ void release_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Named barrier over a subset of warps (ids 1..15; 0 is __syncthreads).
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
