@@ -180,16 +180,24 @@ __device__ __forceinline__ void load8(const float* t, size_t at, float (&x)[8]) 
   x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
-// A key row held by eight lanes: rotated by the tables' row `pos`, then
+// What happens to a key row before it is quantised, fixed per kernel.
+enum : int {
+  kPlain = 0,          // not rotated
+  kHalves = 1,         // all 128 columns, column c with c + 64
+  kHalvesPart = 2,     // the first rot < 128 columns, column c with c + rot / 2
+  kNeighbours = 3,     // the first rot columns, column 2 c with 2 c + 1
+};
+
+// A key row held by eight lanes: rotated by the tables' row `pos`, then (SIGNS)
 // transformed by M = diag(signs) H_128 / sqrt(128), the signs in shared memory.
 // Every lane of the warp takes part.
-template <bool INTERLEAVED>
+template <int MODE, bool SIGNS>
 __device__ __forceinline__ void key_row(float (&x)[16], const AppendFp8Params& p, int pos, int u,
                                         const float* signs) {
-  if (p.cos) {
+  if constexpr (MODE != kPlain) {
     const bool inside = pos < p.max_pos;
-    const size_t row = static_cast<size_t>(inside ? pos : 0) * (p.rot / 2);
-    if (INTERLEAVED) {
+    const size_t row = static_cast<size_t>(inside ? pos : 0) * (MODE == kHalves ? 64 : p.rot / 2);
+    if constexpr (MODE == kNeighbours) {
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const int col = 64 * w + 8 * u;
@@ -204,12 +212,12 @@ __device__ __forceinline__ void key_row(float (&x)[16], const AppendFp8Params& p
           x[8 * w + 2 * e + 1] = fmaf(a, ss[e], b * cc[e]);
         }
       }
-    } else if (p.rot == 128) {
-      // the pair of column c < 64 is column c + 64: both in this lane
+    } else if constexpr (MODE == kHalves) {
+      // both columns of a pair are in this lane
+      float c[8], s[8];
+      load8(p.cos, row + 8 * u, c);
+      load8(p.sin, row + 8 * u, s);
       if (inside) {
-        float c[8], s[8];
-        load8(p.cos, row + 8 * u, c);
-        load8(p.sin, row + 8 * u, s);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float a = x[e], b = x[8 + e];
@@ -250,7 +258,7 @@ __device__ __forceinline__ void key_row(float (&x)[16], const AppendFp8Params& p
       }
     }
   }
-  if (p.signs) {
+  if constexpr (SIGNS) {
     uint64_t y[8];                                   // pairs of neighbouring columns
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -443,33 +451,26 @@ __device__ __forceinline__ float raw_amax(const Raw16& r) {
   return fmaxf(m.x, m.y);
 }
 
-// 16 bytes to shared memory without passing registers, zeros if !valid (the source
-// must be a readable address all the same); seen by this thread after the wait.
-__device__ __forceinline__ void copy16_async(void* smem_dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-template <int PENDING>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
-}
+// Many rows per page: one block per page and plane, blockDim / 8 = 64 rows at a time
+// (fewer for smaller pages).  STAGED: up to 4 such sweeps are copied into shared memory
+// at once, every thread its own values.  A key row's transform costs some 300
+// instructions per 4 rows, which bounds this kernel, so it runs once: sweeps 0 to 2
+// go back to shared memory as float32, sweep 3 stays in registers until the amax is
+// known (transforming twice measured 62 us against 41 for 16 K rows of 8 heads).
+// Rows of pages beyond 256 are read and transformed again, from L2.
+// Query rows are rotated by q_blocks other blocks, bound by DRAM and spread among
+// these.  One of them has to keep HBM busy beside a page's block (registers leave
+// room for two), so its rows too come through shared memory, seven heads in flight.
+constexpr int kSweeps = 4;
+constexpr int kSlot = 4 * kF8MaxThreads;                        // 16-byte words of a sweep
+constexpr int kStagedBytes = (3 * kSlot + kSlot / 2) * 16;      // the last one's stay raw
+static_assert(kStagedBytes == 7 * 2 * 16 * kF8MaxThreads, "seven slots of the rotation");
 
-// Many rows per page: one block per page and plane, blockDim / 8 rows at a time.
-// SWEEPS = 4: each thread copies the raw values of its first 4 rows into its own
-// slots of shared memory, all at once, and reads them back for the amax pass and
-// again for the code pass; the transform runs twice, which costs less than holding
-// float32 rows would in occupancy (registers for 4 raw rows spilled).  Rows of
-// larger pages are read again, from L2.  SWEEPS = 1: a page is one row per
-// thread, whose values stay in registers.
-// Bound: instruction issue and shuffles of the key rows (some 330 instructions per
-// 4 rows and pass), while rotating the query rows is bound by DRAM; q_blocks blocks
-// of that, spread evenly among the others, use what these leave.
-template <bool FP16, bool INTERLEAVED, int SWEEPS>
+template <bool FP16, int MODE, bool SIGNS, bool STAGED>
 __global__ void __launch_bounds__(kF8MaxThreads, 2)
     append_fp8_pages_kernel(const AppendFp8Params p, int page_shift, const RopeKParams q, unsigned q_blocks,
                             unsigned q_columns) {
-  extern __shared__ uint4 raw_sh[];                  // [SWEEPS][2][blockDim], SWEEPS > 1
+  extern __shared__ uint4 stage[];                   // sweep i: words [i kSlot + part blockDim + thread]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int u = lane & 7;
   const int by = blockDim.x >> 3, mine = threadIdx.x >> 3;
@@ -480,14 +481,14 @@ __global__ void __launch_bounds__(kF8MaxThreads, 2)
   const unsigned before_q = static_cast<unsigned>(static_cast<unsigned long long>(blockIdx.x) * q_blocks / gridDim.x);
   const unsigned with_q = static_cast<unsigned>((blockIdx.x + 1ull) * q_blocks / gridDim.x);
   if (with_q > before_q) {
-    rope_block<FP16, INTERLEAVED, 2>(q, before_q % q_columns, before_q / q_columns);
+    rope_block<FP16, MODE == kNeighbours, 2, STAGED ? 7 : 0>(q, before_q % q_columns, before_q / q_columns, stage);
     return;
   }
   const unsigned at_site = blockIdx.x - before_q;
   if (warp == 0) {
     const AppendSite found = append_site(p, at_site / (2 * p.H_kv), at_site % (2 * p.H_kv), page_shift, u);
     if (lane == 0) site_sh = found;
-  } else if (p.signs && warp == 1) {
+  } else if (SIGNS && warp == 1) {
     *reinterpret_cast<float4*>(signs + 4 * lane) = __ldg(reinterpret_cast<const float4*>(p.signs) + lane);
   }
   __syncthreads();
@@ -495,52 +496,68 @@ __global__ void __launch_bounds__(kF8MaxThreads, 2)
   if (!s.ok) return;                                 // the same for the whole block
   s.src += 8 * u;
   s.dst += 8 * u;
-  if constexpr (SWEEPS > 1) {
+  uint4* const my = stage + threadIdx.x;
+  const int step = blockDim.x;
+  if constexpr (STAGED) {
 #pragma unroll
-    for (int i = 0; i < SWEEPS; ++i) {
+    for (int i = 0; i < kSweeps; ++i) {
       const int x = s.first + mine + i * by;
       const bool valid = x < s.end;
       const uint4* at = reinterpret_cast<const uint4*>(s.src + s.st * (valid ? x : s.first));
-      copy16_async(raw_sh + (2 * i) * blockDim.x + threadIdx.x, at, valid);
-      copy16_async(raw_sh + (2 * i + 1) * blockDim.x + threadIdx.x, at + 8, valid);
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      copy16_async(my + i * kSlot, at, valid);
+      copy16_async(my + i * kSlot + step, at + 8, valid);
+      copies_commit();
     }
   }
+  const int warp_first = s.first + (warp << 2);      // first row of the warp's first sweep
+  const int sweeps = warp_first < s.end ? (s.end - warp_first + by - 1) / by : 0;   // of this warp
   float v[16];
   // row s.first + mine + i * by, zeros past the new rows (the transform's shuffles are
   // warp-wide, so those lanes go along)
-  auto row = [&](int i, bool staged) -> Raw16 {
-    if (staged)
-      return {raw_sh[(2 * i) * blockDim.x + threadIdx.x], raw_sh[(2 * i + 1) * blockDim.x + threadIdx.x]};
+  auto raw_row = [&](int i) -> Raw16 {
     const int x = s.first + mine + i * by;
     return x < s.end ? load_row(s, x) : Raw16{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
   };
   auto finish = [&](int i, const Raw16& r) {
     widen16<FP16>(r.a, r.b, v);
-    if (!s.is_v) key_row<INTERLEAVED>(v, p, s.page0 + s.first + mine + i * by, u, signs);
+    if (!s.is_v) key_row<MODE, SIGNS>(v, p, s.page0 + s.first + mine + i * by, u, signs);
   };
-  // values need no transform before their amax, unless v holds them till the end
-  auto max_of = [&](int i, const Raw16& r) {
-    if (SWEEPS > 1 && s.is_v) return raw_amax<FP16>(r);
-    finish(i, r);
-    return amax16(v);
-  };
-  const int warp_first = s.first + (warp << 2);      // first row of the warp's first sweep
-  const int sweeps = warp_first < s.end ? (s.end - warp_first + by - 1) / by : 0;   // of this warp
   float amax = 0.f;
   int i = 0;
-  if constexpr (SWEEPS > 1) {
+  if constexpr (STAGED) {
+    auto staged = [&](int at) {
+      const Raw16 r{my[at * kSlot], my[at * kSlot + step]};
+      if (s.is_v) {
+        amax = fmaxf(amax, raw_amax<FP16>(r));       // values are widened when stored
+        return;
+      }
+      finish(at, r);
+      amax = fmaxf(amax, amax16(v));
+      if (at == kSweeps - 1) return;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        my[at * kSlot + e * step] = make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
+                                               __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
+    };
     copies_wait<3>();
-    if (sweeps > 0) amax = fmaxf(amax, max_of(0, row(0, true)));
+    if (sweeps > 0) staged(0);
     copies_wait<2>();
-    if (sweeps > 1) amax = fmaxf(amax, max_of(1, row(1, true)));
+    if (sweeps > 1) staged(1);
     copies_wait<1>();
-    if (sweeps > 2) amax = fmaxf(amax, max_of(2, row(2, true)));
+    if (sweeps > 2) staged(2);
     copies_wait<0>();
-    if (sweeps > 3) amax = fmaxf(amax, max_of(3, row(3, true)));
-    i = SWEEPS;
+    // rows beyond the staged ones before the last staged sweep, which stays in v
+    for (i = kSweeps; i < sweeps; ++i) {
+      finish(i, raw_row(i));
+      amax = fmaxf(amax, amax16(v));
+    }
+    if (sweeps > 3) staged(3);
+  } else {
+    for (; i < sweeps; ++i) {
+      finish(i, raw_row(i));
+      amax = fmaxf(amax, amax16(v));
+    }
   }
-  for (; i < sweeps; ++i) amax = fmaxf(amax, max_of(i, row(i, false)));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if (lane == 0) warp_max[warp] = amax;
@@ -550,24 +567,51 @@ __global__ void __launch_bounds__(kF8MaxThreads, 2)
   if (threadIdx.x == 0) *s.descale = after;
   const float rcp = __fdiv_rn(1.f, after);
   const uint64_t y2 = pack2(rcp, rcp), nb2 = pack2(-after, -after);
-  for (i = 0; i < sweeps; ++i) {
-    if (SWEEPS > 1 || sweeps > 1) finish(i, row(i, SWEEPS > 1 && i < SWEEPS));   // else still in v
-    const int x = s.first + mine + i * by;
+  auto store = [&](int at) {
+    const int x = s.first + mine + at * by;
     if (x < s.end) store_row(s, x, v, y2, nb2);
+  };
+  if constexpr (STAGED) {
+    if (sweeps > 3) {
+      if (s.is_v) widen16<FP16>(my[3 * kSlot], my[3 * kSlot + step], v);
+      store(3);
+    }
+    for (int at = 0; at < min(sweeps, 3); ++at) {
+      if (s.is_v) {
+        widen16<FP16>(my[at * kSlot], my[at * kSlot + step], v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint4 w = my[at * kSlot + e * step];
+          v[4 * e] = __uint_as_float(w.x), v[4 * e + 1] = __uint_as_float(w.y);
+          v[4 * e + 2] = __uint_as_float(w.z), v[4 * e + 3] = __uint_as_float(w.w);
+        }
+      }
+      store(at);
+    }
+    for (i = kSweeps; i < sweeps; ++i) {
+      finish(i, raw_row(i));
+      store(i);
+    }
+  } else {
+    for (i = 0; i < sweeps; ++i) {
+      if (sweeps > 1) finish(i, raw_row(i));         // one sweep: still in v
+      store(i);
+    }
   }
   other_rows(s, after, p.page_size, mine, by);
 }
 
 // Few rows per page (a decode step): eight lanes per page and plane, so the planes
 // of a page share a block and its lookups; blocks behind them rotate query rows.
-template <bool FP16, bool INTERLEAVED>
+template <bool FP16, int MODE, bool SIGNS>
 __global__ void __launch_bounds__(kF8Threads)
     append_fp8_rows_kernel(const AppendFp8Params p, int page_shift, long long sites, unsigned site_blocks,
                            const RopeKParams q, unsigned q_columns) {
   __shared__ __align__(16) float signs[128];
   if (blockIdx.x >= site_blocks) {
     const unsigned at = blockIdx.x - site_blocks;
-    rope_block<FP16, INTERLEAVED>(q, at % q_columns, at / q_columns);
+    rope_block<FP16, MODE == kNeighbours>(q, at % q_columns, at / q_columns);
     return;
   }
   const int u = threadIdx.x & 7;
@@ -579,7 +623,7 @@ __global__ void __launch_bounds__(kF8Threads)
   if (!s.ok) s.first = s.end = 0;
   s.src += 8 * u;
   s.dst += 8 * u;
-  if (p.signs) {
+  if constexpr (SIGNS) {
     if (threadIdx.x < 32)
       *reinterpret_cast<float4*>(signs + 4 * threadIdx.x) = __ldg(reinterpret_cast<const float4*>(p.signs) + threadIdx.x);
     __syncthreads();
@@ -595,7 +639,7 @@ __global__ void __launch_bounds__(kF8Threads)
     float k[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) k[e] = v[e];
-    key_row<INTERLEAVED>(k, p, i < rows ? s.page0 + x : 0, u, signs);
+    key_row<MODE, SIGNS>(k, p, i < rows ? s.page0 + x : 0, u, signs);
     if (!s.is_v) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = k[e];
@@ -628,28 +672,51 @@ int shift_of(int page_size) {
   return s;
 }
 
-template <bool FP16, bool INTERLEAVED>
-attn_status_t launch_append_pages(const AppendFp8Params& p, int page_shift, RopeKParams q, long long sites,
-                                  cudaStream_t stream) {
-  // eight threads per row of a page, up to 64 rows at a time
-  const int threads = p.page_size * 8 < kF8MaxThreads ? p.page_size * 8 : kF8MaxThreads;
-  RopeGrid g{1, 0};
+template <bool FP16, int MODE, bool SIGNS>
+attn_status_t launch_append_t(const AppendFp8Params& p, RopeKParams q, int page_shift, long long sites,
+                              cudaStream_t stream) {
   q.status = p.status;
-  if (q.heads[0] > 0) g = rope_grid(&q, threads);
+  // Up to 4 new tokens per request on average: eight lanes per page and plane.  More: a
+  // block each, eight threads per row of a page, up to 64 rows at a time.
+  const bool few = p.total <= 4ll * p.B;
+  const int threads = few ? kF8Threads : p.page_size * 8 < kF8MaxThreads ? p.page_size * 8 : kF8MaxThreads;
+  RopeGrid g{1, 0};
+  if (q.heads[0] > 0) g = rope_grid(&q, threads, few ? 152 * 8 : 152 * 2);
   const long long q_blocks = g.columns * g.chunks;
-  if (sites + q_blocks > 2147483647LL) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
-  const unsigned grid = static_cast<unsigned>(sites + q_blocks), columns = static_cast<unsigned>(g.columns);
+  const long long own = few ? (sites + kF8Threads / 8 - 1) / (kF8Threads / 8) : sites;
+  if (own + q_blocks > 2147483647LL) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
+  const unsigned grid = static_cast<unsigned>(own + q_blocks), columns = static_cast<unsigned>(g.columns);
   const unsigned qb = static_cast<unsigned>(q_blocks);
-  if (p.page_size * 8 <= kF8MaxThreads) {
-    append_fp8_pages_kernel<FP16, INTERLEAVED, 1><<<grid, threads, 0, stream>>>(p, page_shift, q, qb, columns);
-    return ATTN_OK;
+  if (few) {
+    append_fp8_rows_kernel<FP16, MODE, SIGNS><<<grid, threads, 0, stream>>>(p, page_shift, sites,
+                                                                           static_cast<unsigned>(own), q, columns);
+  } else if (p.page_size * 8 <= kF8MaxThreads) {
+    append_fp8_pages_kernel<FP16, MODE, SIGNS, false><<<grid, threads, 0, stream>>>(p, page_shift, q, qb, columns);
+  } else {
+    auto kern = append_fp8_pages_kernel<FP16, MODE, SIGNS, true>;
+    const attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), kStagedBytes);
+    if (s != ATTN_OK) return s;
+    kern<<<grid, threads, kStagedBytes, stream>>>(p, page_shift, q, qb, columns);
   }
-  constexpr int smem = 4 * 2 * kF8MaxThreads * static_cast<int>(sizeof(uint4));
-  auto kern = append_fp8_pages_kernel<FP16, INTERLEAVED, 4>;
-  const attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), smem);
-  if (s != ATTN_OK) return s;
-  kern<<<grid, threads, smem, stream>>>(p, page_shift, q, qb, columns);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail_cuda(e, "FP8 append kernel launch");
   return ATTN_OK;
+}
+
+template <bool FP16, int MODE>
+attn_status_t launch_append_m(const AppendFp8Params& p, const RopeKParams& q, int page_shift, long long sites,
+                              cudaStream_t stream) {
+  return p.signs ? launch_append_t<FP16, MODE, true>(p, q, page_shift, sites, stream)
+                 : launch_append_t<FP16, MODE, false>(p, q, page_shift, sites, stream);
+}
+
+template <bool FP16>
+attn_status_t launch_append(const AppendFp8Params& p, const RopeKParams& q, int interleaved, int page_shift,
+                            long long sites, cudaStream_t stream) {
+  if (!p.cos) return launch_append_m<FP16, kPlain>(p, q, page_shift, sites, stream);
+  if (interleaved) return launch_append_m<FP16, kNeighbours>(p, q, page_shift, sites, stream);
+  return p.rot == 128 ? launch_append_m<FP16, kHalves>(p, q, page_shift, sites, stream)
+                      : launch_append_m<FP16, kHalvesPart>(p, q, page_shift, sites, stream);
 }
 
 }  // namespace
@@ -677,44 +744,13 @@ attn_status_t launch_append_fp8(AppendFp8Params p, RopeKParams q, int fp16, int 
                                 cudaStream_t stream) {
   p.status = device_status_word();
   if (!p.status) return fail(ATTN_ERR_CUDA, "status word unavailable");
+  static_assert(kF8Threads == kRopeThreads, "one block size for both roles");
   const int shift = shift_of(p.page_size);
   const long long units = (static_cast<long long>(p.total) >> shift) + 2ll * p.B;
   const long long sites = units * 2 * p.H_kv;
   if (sites > 2147483647LL) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
-  cudaError_t e;
-  // Up to 4 new tokens per request on average: the few-rows kernel, query rows in
-  // the same launch.  More: a block per page and plane.
-  if (p.total <= 4ll * p.B) {
-    RopeGrid g{1, 0};
-    q.status = p.status;
-    if (q.heads[0] > 0) g = rope_grid(&q);
-    const long long site_blocks = (sites + kF8Threads / 8 - 1) / (kF8Threads / 8);
-    if (site_blocks + g.columns * g.chunks > 2147483647LL)
-      return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
-    static_assert(kF8Threads == kRopeThreads, "one block size for both roles");
-    const unsigned grid = static_cast<unsigned>(site_blocks + g.columns * g.chunks);
-#define ATTN_APPEND(F, I)                                                       \
-  append_fp8_rows_kernel<F, I><<<grid, kF8Threads, 0, stream>>>(                \
-      p, shift, sites, static_cast<unsigned>(site_blocks), q, static_cast<unsigned>(g.columns))
-    if (fp16) {
-      if (interleaved) ATTN_APPEND(true, true);
-      else ATTN_APPEND(true, false);
-    } else {
-      if (interleaved) ATTN_APPEND(false, true);
-      else ATTN_APPEND(false, false);
-    }
-#undef ATTN_APPEND
-  } else {
-#define ATTN_APPEND(F, I) launch_append_pages<F, I>(p, shift, q, sites, stream)
-    attn_status_t s;
-    if (fp16) s = interleaved ? ATTN_APPEND(true, true) : ATTN_APPEND(true, false);
-    else s = interleaved ? ATTN_APPEND(false, true) : ATTN_APPEND(false, false);
-#undef ATTN_APPEND
-    if (s != ATTN_OK) return s;
-  }
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return fail_cuda(e, "FP8 append kernel launch");
-  return ATTN_OK;
+  return fp16 ? launch_append<true>(p, q, interleaved, shift, sites, stream)
+              : launch_append<false>(p, q, interleaved, shift, sites, stream);
 }
 
 }  // namespace attn

@@ -42,19 +42,54 @@ __device__ __forceinline__ void unpack16(const uint4& v, float (&x)[8]) {
   }
 }
 
+// Two neighbouring 16-bit values as a float32 pair, and back.
 template <bool FP16>
-__device__ __forceinline__ uint4 pack16(const float (&x)[8]) {
-  uint32_t w[4];
+__device__ __forceinline__ uint64_t widen2(uint32_t w) {
+  if (FP16) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return pack2(f.x, f.y);
+  }
+  return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <bool FP16>
+__device__ __forceinline__ uint32_t narrow2(uint64_t x) {
+  return FP16 ? cvt_pack_f16(lo2(x), hi2(x)) : cvt_pack_bf16(lo2(x), hi2(x));
+}
+
+// Eight pairs: (a_i, b_i) of the two vectors, or neighbours within each (a: pairs 0 to
+// 3, b: 4 to 7); cc, ss, ns: cos, sin and -sin of pairs (0, 1), (2, 3), ...
+template <bool FP16, bool INTERLEAVED>
+__device__ __forceinline__ void rotate16(uint4& a, uint4& b, const uint64_t (&cc)[4], const uint64_t (&ss)[4],
+                                         const uint64_t (&ns)[4]) {
+  uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
+  uint32_t* wb = reinterpret_cast<uint32_t*>(&b);
+  if constexpr (INTERLEAVED) {
+    auto turn = [](uint32_t w, float c, float s) {
+      const uint64_t x = widen2<FP16>(w);
+      return narrow2<FP16>(pack2(fmaf(-hi2(x), s, lo2(x) * c), fmaf(lo2(x), s, hi2(x) * c)));
+    };
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = FP16 ? cvt_pack_f16(x[2 * i], x[2 * i + 1]) : cvt_pack_bf16(x[2 * i], x[2 * i + 1]);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i) {
+      wa[i] = turn(wa[i], i & 1 ? hi2(cc[i / 2]) : lo2(cc[i / 2]), i & 1 ? hi2(ss[i / 2]) : lo2(ss[i / 2]));
+      wb[i] = turn(wb[i], i & 1 ? hi2(cc[2 + i / 2]) : lo2(cc[2 + i / 2]),
+                   i & 1 ? hi2(ss[2 + i / 2]) : lo2(ss[2 + i / 2]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t x = widen2<FP16>(wa[i]), y = widen2<FP16>(wb[i]);
+      wa[i] = narrow2<FP16>(ffma2(y, ns[i], fmul2(x, cc[i])));
+      wb[i] = narrow2<FP16>(ffma2(x, ss[i], fmul2(y, cc[i])));
+    }
+  }
 }
 
 // Work of one block: tokens of block column `bx`, heads of chunk `chunk`, kHeads of
-// them at a time.
-template <bool FP16, bool INTERLEAVED, int kHeads = 4>
-__device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, int chunk) {
+// them at a time.  SLOTS > 0: rows of the first tensor (no other is given) come through
+// shared memory, SLOTS heads in flight, every thread its own 32 bytes of each; for
+// kernels that cannot give the loads registers (stage: SLOTS * 2 * blockDim words).
+template <bool FP16, bool INTERLEAVED, int kHeads = 4, int SLOTS = 0>
+__device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, int chunk, uint4* stage = nullptr) {
   const int units = p.d / 16;                       // 4, 8 or 16: divides the block
   const int tokens = static_cast<int>(blockDim.x) / units;
   const int u = static_cast<int>(threadIdx.x) % units;
@@ -62,7 +97,7 @@ __device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, i
   if (tk >= static_cast<long long>(p.B) * p.N) return;
   const long long b = tk / p.N, n = tk - b * p.N;
   bool turn = p.rotated > 0 && 16 * u < p.rot;
-  float c[8], s[8];
+  float c[8] = {}, s[8] = {};
   if (p.rotated > 0) {
     int pos = static_cast<int>(n);
     if (p.positions) {
@@ -109,93 +144,85 @@ __device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, i
   const bool halves = !INTERLEAVED && p.rotated > 0 && 16 * u < p.rot;
   const int off_a = halves ? 8 * u : 16 * u;
   const int off_b = halves ? p.rot / 2 + 8 * u : 16 * u + 8;
-  const int all = p.heads[0] + p.heads[1] + p.heads[2];
-  const int h_end = min(all, (chunk + 1) * p.heads_per_chunk);
-  for (int h0 = chunk * p.heads_per_chunk; h0 < h_end; h0 += kHeads) {
-    uint4 va[kHeads], vb[kHeads];
-    uint16_t* out[kHeads];
-    bool rot[kHeads];
+  // cos and sin of the pairs of two neighbouring elements
+  uint64_t cc[4], ss[4], ns[4];
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      out[i] = nullptr;
-      int h = h0 + i;
-      if (h >= h_end) continue;
-      int t = 0;
-      if (h >= p.heads[0]) {
-        h -= p.heads[0];
-        t = 1;
-        if (h >= p.heads[1]) {
-          h -= p.heads[1];
-          t = 2;
+  for (int i = 0; i < 4; ++i) {
+    cc[i] = pack2(c[2 * i], c[2 * i + 1]);
+    ss[i] = pack2(s[2 * i], s[2 * i + 1]);
+    ns[i] = pack2(-s[2 * i], -s[2 * i + 1]);
+  }
+  const int lo = chunk * p.heads_per_chunk, hi = lo + p.heads_per_chunk;
+  int before = 0;                                   // heads of the tensors before
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    const int h0 = max(lo - before, 0), h1 = min(hi - before, p.heads[t]);
+    before += p.heads[t];
+    if (h0 >= h1 || (p.slots && t > 0 && slot < 0)) continue;
+    const bool rotate = turn && t < p.rotated;
+    const uint16_t* in = p.src[t] + b * p.sb[t] + n * p.st[t] + h0 * p.sh[t];
+    const bool cache = p.slots && t > 0;
+    uint16_t* out = cache ? p.dst[t] + (slot * p.heads[1] + h0) * p.d
+                          : p.dst[t] + b * p.db[t] + n * p.dt[t] + h0 * p.dh[t];
+    const long long step_in = p.sh[t], step_out = cache ? p.d : p.dh[t];
+    if constexpr (SLOTS > 0) {
+      const int words = static_cast<int>(blockDim.x);
+      auto copy = [&](int k) {
+        if (h0 + k < h1) {
+          uint4* dst = stage + (k % SLOTS) * 2 * words + threadIdx.x;
+          copy16_async(dst, in + k * step_in + off_a, true);
+          copy16_async(dst + words, in + k * step_in + off_b, true);
         }
+        copies_commit();
+      };
+#pragma unroll
+      for (int k = 0; k < SLOTS; ++k) copy(k);
+      for (int k = 0; k < h1 - h0; ++k) {
+        copies_wait<SLOTS - 1>();
+        const uint4* src = stage + (k % SLOTS) * 2 * words + threadIdx.x;
+        uint4 va = src[0], vb = src[words];
+        if (rotate) rotate16<FP16, INTERLEAVED>(va, vb, cc, ss, ns);
+        *reinterpret_cast<uint4*>(out + k * step_out + off_a) = va;
+        *reinterpret_cast<uint4*>(out + k * step_out + off_b) = vb;
+        copy(k + SLOTS);
       }
-      rot[i] = turn && t < p.rotated;
-      // selects, not indexed parameter arrays: t is only known at run time
-      const uint16_t* src = t == 0 ? p.src[0] : t == 1 ? p.src[1] : p.src[2];
-      uint16_t* dst = t == 0 ? p.dst[0] : t == 1 ? p.dst[1] : p.dst[2];
-      const long long sb = t == 0 ? p.sb[0] : t == 1 ? p.sb[1] : p.sb[2];
-      const long long sh = t == 0 ? p.sh[0] : t == 1 ? p.sh[1] : p.sh[2];
-      const long long st = t == 0 ? p.st[0] : t == 1 ? p.st[1] : p.st[2];
-      if (p.slots && t > 0) {
-        if (slot < 0) continue;
-        out[i] = dst + (slot * p.heads[1] + h) * p.d;
-      } else {
-        const long long db = t == 0 ? p.db[0] : p.db[1];
-        const long long dh = t == 0 ? p.dh[0] : p.dh[1];
-        const long long dt = t == 0 ? p.dt[0] : p.dt[1];
-        out[i] = dst + b * db + h * dh + n * dt;
-      }
-      const uint16_t* in = src + b * sb + h * sh + n * st;
-      va[i] = *reinterpret_cast<const uint4*>(in + off_a);
-      vb[i] = *reinterpret_cast<const uint4*>(in + off_b);
-    }
+      copies_wait<0>();
+    } else {
+      for (int h = h0; h < h1; h += kHeads) {
+        uint4 va[kHeads], vb[kHeads];
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      if (!out[i]) continue;
-      if (rot[i]) {
-        float x[8], y[8];
-        unpack16<FP16>(va[i], x);
-        unpack16<FP16>(vb[i], y);
-        if (INTERLEAVED) {
-          // x: pairs 0 .. 3, y: pairs 4 .. 7 of the thread's eight
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x0 = x[2 * e], x1 = x[2 * e + 1], y0 = y[2 * e], y1 = y[2 * e + 1];
-            x[2 * e] = fmaf(-x1, s[e], x0 * c[e]);
-            x[2 * e + 1] = fmaf(x0, s[e], x1 * c[e]);
-            y[2 * e] = fmaf(-y1, s[4 + e], y0 * c[4 + e]);
-            y[2 * e + 1] = fmaf(y0, s[4 + e], y1 * c[4 + e]);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x0 = x[e], y0 = y[e];
-            x[e] = fmaf(-y0, s[e], x0 * c[e]);
-            y[e] = fmaf(x0, s[e], y0 * c[e]);
-          }
+        for (int i = 0; i < kHeads; ++i) {
+          if (h + i >= h1) break;
+          va[i] = *reinterpret_cast<const uint4*>(in + i * step_in + off_a);
+          vb[i] = *reinterpret_cast<const uint4*>(in + i * step_in + off_b);
         }
-        va[i] = pack16<FP16>(x);
-        vb[i] = pack16<FP16>(y);
+        in += kHeads * step_in;
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+          if (h + i >= h1) break;
+          if (rotate) rotate16<FP16, INTERLEAVED>(va[i], vb[i], cc, ss, ns);
+          *reinterpret_cast<uint4*>(out + i * step_out + off_a) = va[i];
+          *reinterpret_cast<uint4*>(out + i * step_out + off_b) = vb[i];
+        }
+        out += kHeads * step_out;
       }
-      *reinterpret_cast<uint4*>(out[i] + off_a) = va[i];
-      *reinterpret_cast<uint4*>(out[i] + off_b) = vb[i];
     }
   }
 }
 
-// Blocks of rope_block: token columns, and head chunks so that a call of few
-// tokens still fills the machine.
+// Blocks of rope_block: token columns, and head chunks of at least 4 so that a call of
+// few tokens still fills the machine.
 struct RopeGrid {
   long long columns;
   int chunks;
 };
-inline RopeGrid rope_grid(RopeKParams* p, int threads = kRopeThreads) {
+inline RopeGrid rope_grid(RopeKParams* p, int threads = kRopeThreads, int least_blocks = 152 * 8) {
   const int tokens = threads / (p->d / 16);
   RopeGrid g;
   g.columns = (static_cast<long long>(p->B) * p->N + tokens - 1) / tokens;
   const int all = p->heads[0] + p->heads[1] + p->heads[2];
   int per = all;
-  while (per > 4 && g.columns * ((all + per - 1) / per) < 152 * 8) per = (per + 1) / 2;
+  while (per > 4 && g.columns * ((all + per - 1) / per) < least_blocks) per = (per + 1) / 2;
   p->heads_per_chunk = per;
   g.chunks = (all + per - 1) / per;
   return g;

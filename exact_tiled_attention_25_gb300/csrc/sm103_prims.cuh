@@ -150,6 +150,21 @@ __device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity) 
   }
 }
 
+// 16 bytes to shared memory without passing registers, zeros if !valid (the source
+// must be a readable address all the same); seen by this thread after the wait.
+__device__ __forceinline__ void copy16_async(void* smem_dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
 // Dependent launches: a kernel launched with the programmatic-serialisation attribute
 // may start once every block of the kernel before it has released it (or ended), and
 // waits for that kernel's end, its writes included, before it touches them.  Every

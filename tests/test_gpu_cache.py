@@ -185,7 +185,7 @@ def _random_cache(seed, num, page, H_kv):
     return codes, rng.uniform(0.004, 0.01, (num, H_kv)).astype(np.float32)
 
 
-@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("page", [16, 64, 256, 512])
 @pytest.mark.parametrize("old,new", [([0], [1]), ([5, 0, 64, 130], [1, 1, 1, 1]), ([0, 15, 16, 250], [300, 2, 0, 700])])
 @pytest.mark.parametrize("rot,signs", [(0, False), (128, False), (48, True), (0, True)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
