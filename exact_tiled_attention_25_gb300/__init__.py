@@ -14,8 +14,6 @@ current stream, and the outputs are copied back to the CPU.
 """
 from __future__ import annotations
 
-import ctypes
-import functools
 import math
 
 import torch
@@ -749,43 +747,20 @@ def attn_fp8_quantize_ex(q, k, v, rope_cos=None, rope_sin=None, hadamard_signs=N
     return tuple(outs), tuple(desc)
 
 
-# The calls below are short on the GPU, so their host side is kept short too.
+# The calls below are short on the GPU: their checks, outputs and C calls are compiled
+# (csrc/native.cpp).
 
-def _on_gpu(names: str, *tensors) -> int:
-    """Tensors that are used where they are (some are written in place): all on the
-    current CUDA device, whose index is returned."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            bad = [n for n, x in zip(names.split(), tensors) if x is t][0]
-            raise ValueError(f"{bad} must be on the current CUDA device")
-    return dev
+def _binding():
+    return _lib.native(_check)
 
 
-def _raw_stream(stream, dev: int) -> int:
-    """Handle of the given stream, or of the device's current one (looked up directly:
-    building the Stream object of torch.cuda.current_stream() takes 3 us)."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _like(t, name, shape, dtype):
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
-
-
-def _kv_lens(lens, B):
-    if lens is not None and (lens.dtype != torch.int32 or lens.shape != (B,) or not lens.is_contiguous()):
-        raise ValueError("kv_lens must be contiguous int32 [B]")
-
-
-def _cross_shapes(q, k, v):
-    B, H, N_q, d = _shape4(q, "q")
-    Bk, H_kv, N_k, dk = _shape4(k, "k")
-    if Bk != B or dk != d or v.shape != k.shape or not v.is_contiguous():
-        raise ValueError("k and v must be contiguous [B, H_kv, N_k, d] with q's B and d")
-    if q.dtype not in _DTYPES or k.dtype != q.dtype or v.dtype != q.dtype:
-        raise ValueError("q, k, v must all be bfloat16 or all float16")
-    return B, H, H_kv, N_q, N_k, d
+def _moved(call, tensors, *rest):
+    """call(*tensors, *rest) with the CPU tensors (None: absent) copied to the current
+    device, and its results copied back; a mixture goes on to the call's own refusal."""
+    moved, host = _to_device([t for t in tensors if t is not None])
+    it = iter(moved)
+    out = call(*[None if t is None else next(it) for t in tensors], *rest)
+    return tuple(None if t is None else t.cpu() for t in out) if host else out
 
 
 def attn_cross_workspace_size(B: int, H: int, H_kv: int, N_q: int, N_k: int, d: int) -> int:
@@ -801,81 +776,20 @@ def attn_cross_fwd(q, k, v, kv_lens=None, softmax_scale: float | None = None, o=
     """Cross attention: q [B, H, N_q, d] against k, v [B, H_kv, N_k, d], of which
     entry b sees the first kv_lens[b] (int32 [B]; None: all).  Returns O
     [B, H, N_q, d] and LSE float32 [B, H, N_q]; O = 0, LSE = -inf without keys."""
-    lib = _lib.load()
-    host = not q.is_cuda
-    if host:
-        (q, k, v, kv_lens), host = _move([q, k, v, kv_lens])
-    B, H, H_kv, N_q, N_k, d = _cross_shapes(q, k, v)
-    _kv_lens(kv_lens, B)
-    dev = _on_gpu("q k v kv_lens o lse workspace", q, k, v, kv_lens, o, lse, workspace)
-    if o is None:
-        o = torch.empty_like(q)
-    else:
-        _like(o, "o", q.shape, q.dtype)
-    if lse is None:
-        lse = torch.empty((B, H, N_q), dtype=torch.float32, device=q.device)
-    else:
-        _like(lse, "lse", (B, H, N_q), torch.float32)
-    if workspace is None:
-        need = lib.attn_cross_workspace_size(B, H, H_kv, N_q, N_k, d)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    code = lib.attn_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_lens), o.data_ptr(), lse.data_ptr(),
-                              _ptr(workspace), 0 if workspace is None else workspace.nbytes, B, H, H_kv, N_q, N_k, d,
-                              d ** -0.5 if softmax_scale is None else softmax_scale, _DTYPES[q.dtype],
-                              _raw_stream(stream, dev))
-    _check(code, "attn_cross_fwd")
-    if host:
-        return o.cpu(), lse.cpu()
-    return o, lse
+    call = _binding().cross_fwd
+    if not q.is_cuda:
+        return _moved(call, (q, k, v, kv_lens), softmax_scale, o, lse, workspace, stream)
+    return call(q, k, v, kv_lens, softmax_scale, o, lse, workspace, stream)
 
 
 def attn_cross_bwd(q, k, v, o, dout, lse, kv_lens=None, softmax_scale: float | None = None, dq=None,
                    dk=None, dv=None, workspace=None, stream=None):
     """Backward of attn_cross_fwd: returns dQ [B, H, N_q, d], dK, dV [B, H_kv, N_k, d]
     (zero behind kv_lens)."""
-    lib = _lib.load()
-    host = not q.is_cuda
-    if host:
-        (q, k, v, o, dout, lse, kv_lens), host = _move([q, k, v, o, dout, lse, kv_lens])
-    B, H, H_kv, N_q, N_k, d = _cross_shapes(q, k, v)
-    _like(o, "o", q.shape, q.dtype)
-    _like(dout, "dout", q.shape, q.dtype)
-    _like(lse, "lse", (B, H, N_q), torch.float32)
-    _kv_lens(kv_lens, B)
-    dev = _on_gpu("q k v o dout lse kv_lens dq dk dv workspace",
-                  q, k, v, o, dout, lse, kv_lens, dq, dk, dv, workspace)
-    if dq is None:
-        dq = torch.empty_like(q)
-    else:
-        _like(dq, "dq", q.shape, q.dtype)
-    if dk is None:
-        dk = torch.empty_like(k)
-    else:
-        _like(dk, "dk", k.shape, k.dtype)
-    if dv is None:
-        dv = torch.empty_like(v)
-    else:
-        _like(dv, "dv", v.shape, v.dtype)
-    if workspace is None:
-        workspace = torch.empty(lib.attn_cross_bwd_workspace_size(B, H, N_q, N_k, d), dtype=torch.uint8,
-                                device=q.device)
-    code = lib.attn_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(),
-                              _ptr(kv_lens), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
-                              workspace.nbytes, B, H, H_kv, N_q, N_k, d,
-                              d ** -0.5 if softmax_scale is None else softmax_scale, _DTYPES[q.dtype],
-                              _raw_stream(stream, dev))
-    _check(code, "attn_cross_bwd")
-    if host:
-        return dq.cpu(), dk.cpu(), dv.cpu()
-    return dq, dk, dv
-
-
-def _move(tensors):
-    """CPU tensors (None: absent) on the current device, when every one is on the CPU."""
-    moved, host = _to_device([t for t in tensors if t is not None])
-    it = iter(moved)
-    return [None if t is None else next(it) for t in tensors], host
+    call = _binding().cross_bwd
+    if not q.is_cuda:
+        return _moved(call, (q, k, v, o, dout, lse, kv_lens), softmax_scale, dq, dk, dv, workspace, stream)
+    return call(q, k, v, o, dout, lse, kv_lens, softmax_scale, dq, dk, dv, workspace, stream)
 
 
 def attn_rope_table(n: int, rot_dim: int, base: float = 10000.0, factor: float = 1.0, orig_len: int = 0,
@@ -885,55 +799,8 @@ def attn_rope_table(n: int, rot_dim: int, base: float = 10000.0, factor: float =
     first + n - 1.  factor > 1 stretches them for a longer context: every frequency
     (orig_len = 0), or only those that turn fewer than `high` times within orig_len
     positions (wholly below `low` turns); attn_factor multiplies both tables."""
-    lib = _lib.load()
-    shape = (int(n), int(rot_dim) // 2)
-    if min(shape) < 1:
-        raise ValueError("n and rot_dim must be positive")
-    dev = _on_gpu("rope_cos rope_sin", rope_cos, rope_sin)
-    if rope_cos is None:
-        rope_cos = torch.empty(shape, dtype=torch.float32, device=torch.device("cuda", dev))
-    if rope_sin is None:
-        rope_sin = torch.empty(shape, dtype=torch.float32, device=torch.device("cuda", dev))
-    _like(rope_cos, "rope_cos", shape, torch.float32)
-    _like(rope_sin, "rope_sin", shape, torch.float32)
-    code = lib.attn_rope_table(rope_cos.data_ptr(), rope_sin.data_ptr(), int(n), int(rot_dim), base, factor,
-                               int(orig_len), low, high, attn_factor, int(first), _raw_stream(stream, dev))
-    _check(code, "attn_rope_table")
-    return rope_cos, rope_sin
-
-
-@functools.lru_cache(maxsize=4096)
-def _strides(*steps):
-    """Host array of element strides (read only)."""
-    return (ctypes.c_longlong * len(steps))(*steps)
-
-
-def _rope_tables(rope_cos, rope_sin):
-    """(max_pos, rot_dim) of a pair of tables."""
-    if rope_cos.dim() != 2:
-        raise ValueError("rope_cos must be [positions, rot_dim / 2]")
-    _like(rope_cos, "rope_cos", rope_cos.shape, torch.float32)
-    _like(rope_sin, "rope_sin", rope_cos.shape, torch.float32)
-    return rope_cos.shape[0], 2 * rope_cos.shape[1]
-
-
-def _row_strides(t, name):
-    """Strides of all dimensions but the last; one of extent 1 may have any stride,
-    and is given as a row's length."""
-    *steps, last = t.stride()
-    if last != 1:
-        raise ValueError(f"{name}'s rows must be contiguous")
-    if 1 in t.shape:
-        return [x if n > 1 else t.shape[-1] for x, n in zip(steps, t.shape)]
-    return steps
-
-
-def _rope_strides(t, name, packed):
-    """{batch, head, token} strides, or None for contiguous [B, heads, N, d]."""
-    if not packed and t.is_contiguous():
-        return None
-    step = _row_strides(t, name)
-    return _strides(t.shape[-1], step[1], step[0]) if packed else _strides(*step)
+    return _binding().rope_table(n, rot_dim, base, factor, orig_len, low, high, attn_factor, first, rope_cos,
+                                rope_sin, stream)
 
 
 def attn_rope(q, k, rope_cos, rope_sin, positions=None, interleaved: bool = False, inverse: bool = False,
@@ -942,47 +809,10 @@ def attn_rope(q, k, rope_cos, rope_sin, positions=None, interleaved: bool = Fals
     or packed [total, H, d]; positions int32 [B, N] or [total] (None: the token's
     index; negative: copied).  The tensors may be strided views with contiguous rows;
     q_out, k_out may be the inputs (in place).  inverse = True is the gradient."""
-    lib = _lib.load()
-    host = not q.is_cuda
-    if host:
-        (q, k, rope_cos, rope_sin, positions), host = _move([q, k, rope_cos, rope_sin, positions])
-    max_pos, rot_dim = _rope_tables(rope_cos, rope_sin)
-    packed = q.dim() == 3
-    if packed:
-        (N, H, d), B = q.shape, 1
-    elif q.dim() == 4:
-        B, H, N, d = q.shape
-    else:
-        raise ValueError("q must be [B, H, N, d] or packed [total, H, d]")
-    if q.dtype not in _DTYPES:
-        raise ValueError("q and k must be bfloat16 or float16")
-    if q.numel() == 0:
-        raise ValueError("q is empty")
-    dev = _on_gpu("q k rope_cos rope_sin positions q_out k_out", q, k, rope_cos, rope_sin, positions, q_out, k_out)
-    if positions is not None:
-        _like(positions, "positions", (N,) if packed else (B, N), torch.int32)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif q_out.dtype != q.dtype or q_out.shape != q.shape:
-        raise ValueError("q_out must match q in shape and dtype")
-    H_kv, ks, kos = 0, None, None
-    if k is not None:
-        H_kv = k.shape[1]
-        if k.dtype != q.dtype or k.shape != ((N, H_kv, d) if packed else (B, H_kv, N, d)):
-            raise ValueError("k must match q in dtype and shape, up to its heads")
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        elif k_out.dtype != k.dtype or k_out.shape != k.shape:
-            raise ValueError("k_out must match k in shape and dtype")
-        ks, kos = _rope_strides(k, "k", packed), _rope_strides(k_out, "k_out", packed)
-    code = lib.attn_rope(q.data_ptr(), q_out.data_ptr(), _ptr(k), _ptr(k_out), rope_cos.data_ptr(), rope_sin.data_ptr(),
-                         _ptr(positions), B, N, H, H_kv, d, rot_dim, max_pos, _rope_strides(q, "q", packed),
-                         _rope_strides(q_out, "q_out", packed), ks, kos, bool(interleaved), bool(inverse),
-                         _DTYPES[q.dtype], _raw_stream(stream, dev))
-    _check(code, "attn_rope")
-    if host:
-        return q_out.cpu(), None if k_out is None else k_out.cpu()
-    return q_out, k_out
+    call = _binding().rope
+    if not q.is_cuda:
+        return _moved(call, (q, k, rope_cos, rope_sin, positions), interleaved, inverse, q_out, k_out, stream)
+    return call(q, k, rope_cos, rope_sin, positions, interleaved, inverse, q_out, k_out, stream)
 
 
 def attn_block_tables(block_table, old_lens, new_lens, free_pages, page_size: int, capacity: int,
@@ -992,56 +822,8 @@ def attn_block_tables(block_table, old_lens, new_lens, free_pages, page_size: in
     free_pages).  Returns seq_lens [B], cu_seqlens [B + 1], slots int64 [capacity] and
     positions int32 [capacity] of the new tokens (-1 behind the last) and used [1],
     the free pages taken."""
-    lib = _lib.load()
-    if block_table.dim() != 2 or free_pages.dim() != 1:
-        raise ValueError("block_table must be [B, max_pages] and free_pages a vector")
-    B, max_pages = block_table.shape
-    if capacity < 0:
-        raise ValueError("capacity must be >= 0")
-    i32 = torch.int32
-    _like(block_table, "block_table", block_table.shape, i32)
-    _like(old_lens, "old_lens", (B,), i32)
-    _like(new_lens, "new_lens", (B,), i32)
-    _like(free_pages, "free_pages", free_pages.shape, i32)
-    dev = _on_gpu("block_table old_lens new_lens free_pages seq_lens cu_seqlens slots positions used",
-                  block_table, old_lens, new_lens, free_pages, seq_lens, cu_seqlens, slots, positions, used)
-    device = block_table.device
-    out = []
-    for t, name, n, dtype in ((seq_lens, "seq_lens", B, i32), (cu_seqlens, "cu_seqlens", B + 1, i32),
-                              (slots, "slots", capacity, torch.int64), (positions, "positions", capacity, i32),
-                              (used, "used", 1, i32)):
-        if t is None:
-            t = torch.empty(n, dtype=dtype, device=device)
-        else:
-            _like(t, name, (n,), dtype)
-        out.append(t)
-    code = lib.attn_block_tables(block_table.data_ptr(), old_lens.data_ptr(), new_lens.data_ptr(),
-                                 free_pages.data_ptr(), *[t.data_ptr() for t in out], B, max_pages,
-                                 free_pages.shape[0], page_size, capacity, _raw_stream(stream, dev))
-    _check(code, "attn_block_tables")
-    return tuple(out)
-
-
-def _append_rows(k, v, q, q_out, cache_shape):
-    """Sizes, strides and q_out of an append: k, v [total, H_kv, d], q [total, H, d]."""
-    if k.dim() != 3 or k.shape != v.shape or k.dtype not in _DTYPES or v.dtype != k.dtype:
-        raise ValueError("k and v must be bfloat16 or float16 [total, H_kv, d]")
-    total, H_kv, d = k.shape
-    if len(cache_shape) != 4 or cache_shape[2:] != (H_kv, d):
-        raise ValueError("the caches must be [num_pages, page_size, H_kv, d]")
-    qs, H = None, 0
-    if q is not None:
-        H = q.shape[1] if q.dim() == 3 else -1
-        if q.shape != (total, H, d) or q.dtype != k.dtype:
-            raise ValueError("q must be [total, H, d] in k's dtype")
-        qs = _strides(*_row_strides(q, "q"))
-        if q_out is None:
-            q_out = torch.empty((total, H, d), dtype=q.dtype, device=q.device)
-        else:
-            _like(q_out, "q_out", q.shape, q.dtype)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    return total, H, H_kv, d, (qs, _strides(*_row_strides(k, "k")), _strides(*_row_strides(v, "v"))), q_out
+    return _binding().block_tables(block_table, old_lens, new_lens, free_pages, page_size, capacity, seq_lens,
+                                  cu_seqlens, slots, positions, used, stream)
 
 
 def attn_cache_append(k, v, k_cache, v_cache, slots, rope_cos=None, rope_sin=None, positions=None, q=None,
@@ -1050,26 +832,8 @@ def attn_cache_append(k, v, k_cache, v_cache, slots, rope_cos=None, rope_sin=Non
     none) of the caches [num_pages, page_size, H_kv, d], keys rotated by the tables'
     rows positions (int32 [total]) when given.  q [total, H, d] is rotated in the same
     launch; returns q_out (None without q).  k, v, q may be strided views."""
-    lib = _lib.load()
-    dev = _on_gpu("k v k_cache v_cache slots rope_cos rope_sin positions q q_out",
-                  k, v, k_cache, v_cache, slots, rope_cos, rope_sin, positions, q, q_out)
-    total, H, H_kv, d, strides, q_out = _append_rows(k, v, q, q_out, k_cache.shape)
-    num_pages, page_size = k_cache.shape[:2]
-    _like(k_cache, "k_cache", k_cache.shape, k.dtype)
-    _like(v_cache, "v_cache", k_cache.shape, k.dtype)
-    _like(slots, "slots", (total,), torch.int64)
-    max_pos = rot_dim = 0
-    if rope_cos is not None:
-        max_pos, rot_dim = _rope_tables(rope_cos, rope_sin)
-        if positions is None:
-            raise ValueError("rotation needs positions")
-        _like(positions, "positions", (total,), torch.int32)
-    code = lib.attn_cache_append(_ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
-                                 v_cache.data_ptr(), slots.data_ptr(), _ptr(rope_cos), _ptr(rope_sin),
-                                 _ptr(positions), total, H, H_kv, d, rot_dim, max_pos, num_pages, page_size, *strides,
-                                 bool(interleaved), _DTYPES[k.dtype], _raw_stream(stream, dev))
-    _check(code, "attn_cache_append")
-    return q_out
+    return _binding().cache_append(k, v, k_cache, v_cache, slots, rope_cos, rope_sin, positions, q, interleaved,
+                                  q_out, stream)
 
 
 def attn_cache_append_fp8(k, v, k_cache, v_cache, k_descale, v_descale, block_table, seq_lens, cu_seqlens,
@@ -1081,29 +845,5 @@ def attn_cache_append_fp8(k, v, k_cache, v_cache, k_descale, v_descale, block_ta
     page_size, H_kv, 128] with descales float32 [num_pages, H_kv].  Keys are rotated
     and transformed when tables and signs are given; q is rotated as in
     attn_cache_append.  Returns q_out (None without q)."""
-    lib = _lib.load()
-    dev = _on_gpu("k v k_cache v_cache k_descale v_descale block_table seq_lens cu_seqlens rope_cos rope_sin hadamard_signs q q_out",
-                  k, v, k_cache, v_cache, k_descale, v_descale, block_table, seq_lens, cu_seqlens, rope_cos, rope_sin, hadamard_signs, q, q_out)
-    total, H, H_kv, d, strides, q_out = _append_rows(k, v, q, q_out, k_cache.shape)
-    num_pages, page_size = k_cache.shape[:2]
-    _like(k_cache, "k_cache", k_cache.shape, torch.uint8)
-    _like(v_cache, "v_cache", k_cache.shape, torch.uint8)
-    _like(k_descale, "k_descale", (num_pages, H_kv), torch.float32)
-    _like(v_descale, "v_descale", (num_pages, H_kv), torch.float32)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    B, max_pages = block_table.shape
-    _like(block_table, "block_table", block_table.shape, torch.int32)
-    _like(seq_lens, "seq_lens", (B,), torch.int32)
-    _like(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32)
-    if hadamard_signs is not None:
-        _like(hadamard_signs, "hadamard_signs", (d,), torch.float32)
-    max_pos, rot_dim = (0, 0) if rope_cos is None else _rope_tables(rope_cos, rope_sin)
-    code = lib.attn_cache_append_fp8(_ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
-                                     v_cache.data_ptr(), k_descale.data_ptr(), v_descale.data_ptr(),
-                                     block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(),
-                                     _ptr(rope_cos), _ptr(rope_sin), _ptr(hadamard_signs), B, total, H, H_kv, d,
-                                     rot_dim, max_pos, num_pages, page_size, max_pages, *strides, bool(interleaved),
-                                     _DTYPES[k.dtype], _raw_stream(stream, dev))
-    _check(code, "attn_cache_append_fp8")
-    return q_out
+    return _binding().cache_append_fp8(k, v, k_cache, v_cache, k_descale, v_descale, block_table, seq_lens,
+                                      cu_seqlens, rope_cos, rope_sin, hadamard_signs, q, interleaved, q_out, stream)

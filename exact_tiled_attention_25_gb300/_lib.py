@@ -8,7 +8,7 @@ from __future__ import annotations
 import ctypes
 import os
 
-from .build import LIB_PATH
+from .build import LIB_PATH, NATIVE_PATH
 
 c_int = ctypes.c_int
 c_float = ctypes.c_float
@@ -106,6 +106,7 @@ SIGNATURES = {
 }
 
 _LIB = None
+_NATIVE = None
 
 
 def load(path: str | None = None):
@@ -126,3 +127,18 @@ def load(path: str | None = None):
     if path is None:
         _LIB = lib
     return lib
+
+
+def native(on_error):
+    """The compiled part of the binding, tied to the library; on_error(code, name)
+    raises for a status other than 0."""
+    global _NATIVE
+    if _NATIVE is None:
+        load()
+        import torch  # noqa: F401  (its libraries have to be loaded first)
+        if not os.path.exists(NATIVE_PATH):
+            raise RuntimeError(f"{NATIVE_PATH} is not built; run exact_tiled_attention_25_gb300.build.build()")
+        from . import _native
+        _native.bind(LIB_PATH, on_error)
+        _NATIVE = _native
+    return _NATIVE

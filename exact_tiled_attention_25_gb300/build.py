@@ -1,7 +1,9 @@
 """In-tree build of libattn_gb300.so for sm_103a.
 
 Every ``csrc/*.cu`` file is compiled by nvcc in parallel into ``_build/`` and
-linked into ``libattn_gb300.so`` next to this file.  The CUDA runtime is linked
+linked into ``libattn_gb300.so`` next to this file; ``csrc/native.cpp``, the compiled
+part of the Python binding, becomes ``_native.so`` beside it (host code only, with
+PyTorch's headers).  The CUDA runtime is linked
 statically and the driver is reached through the runtime's entry-point query,
 so the library also loads (for symbol checks) on a machine without a GPU
 driver.  Objects are rebuilt only when a source or header is newer.
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
@@ -21,6 +24,8 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libattn_gb300.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 INCLUDE_DIR = os.path.join(os.path.dirname(PKG_DIR), "include")
+NATIVE_SRC = os.path.join(CSRC, "native.cpp")
+NATIVE_PATH = os.path.join(PKG_DIR, "_native.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -56,6 +61,31 @@ def _compile(nvcc: str, src: str, obj: str, verbose: bool):
     return obj
 
 
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _compile_native(nvcc: str, verbose: bool):
+    import torch
+    root = _torch_dir()
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    includes = [INCLUDE_DIR, os.path.join(root, "include"),
+                os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = NATIVE_PATH + ".tmp"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in includes],
+           NATIVE_SRC, "-o", tmp, f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"the binding did not compile:\n{res.stdout}\n{res.stderr}")
+    if verbose and (res.stdout or res.stderr):
+        sys.stderr.write(res.stdout + res.stderr)
+    os.replace(tmp, NATIVE_PATH)
+
+
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     """Compile (as needed) and link the library; return its path."""
     nvcc = _nvcc()
@@ -69,10 +99,16 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
         objs.append(obj)
         if _stale(obj, [src, *headers]):
             todo.append((src, obj))
-    if todo:
-        workers = jobs or min(len(todo), os.cpu_count() or 4)
+    # rebuilt for another PyTorch too
+    native = _stale(NATIVE_PATH, [NATIVE_SRC, os.path.join(INCLUDE_DIR, "attn_gb300.h"),
+                                  os.path.join(_torch_dir(), "version.py")])
+    if todo or native:
+        workers = jobs or min(len(todo) + native, os.cpu_count() or 4)
         with cf.ThreadPoolExecutor(max_workers=workers) as ex:
-            list(ex.map(lambda so: _compile(nvcc, so[0], so[1], verbose), todo))
+            jobs_ = [ex.submit(_compile_native, nvcc, verbose)] if native else []
+            jobs_ += [ex.submit(_compile, nvcc, src, obj, verbose) for src, obj in todo]
+            for job in jobs_:
+                job.result()
     if todo or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + ".tmp"
         cmd = [nvcc, *ARCH_FLAGS, "-shared", "-cudart", "static", "-o", tmp, *objs]

@@ -134,28 +134,62 @@ def test_append_own_refusals(lib):
 
 
 def test_python_refusals():
-    """Shapes and types that the binding turns away by itself."""
+    """Shapes and types that the binding turns away by itself, before it looks for a device."""
     import torch
     import exact_tiled_attention_25_gb300 as attn
-    bf = dict(dtype=torch.bfloat16)
+    nat = attn._binding()
+    bf, i32 = dict(dtype=torch.bfloat16), dict(dtype=torch.int32)
+
+    def cross(q, k, v, lens=None, o=None):
+        nat.cross_fwd(q, k, v, lens, None, o, None, None, None)
+
+    x = torch.zeros(1, 2, 3, 64, **bf)
+    for args, why in (((x, x.expand(2, 2, 3, 64).contiguous(), x), "q's B and d"),
+                      ((x.float(), x.float(), x.float()), "bfloat16"), ((x, x, x.half()), "bfloat16"),
+                      ((x.transpose(1, 2), x, x), "contiguous"), ((x[0], x, x), r"\[B, H, N, d\]"),
+                      ((x, x, x, torch.zeros(1)), "kv_lens"), ((x, x, x, torch.zeros(2, **i32)), "kv_lens"),
+                      ((x, None, x), "k is missing"), ((x, x, x), "current CUDA device")):
+        with pytest.raises(ValueError, match=why):
+            cross(*args)
+    with pytest.raises(TypeError, match="v must be a tensor"):
+        cross(x, x, 3)
+    with pytest.raises(TypeError, match="expected 9 arguments"):
+        nat.cross_fwd(x)
+    with pytest.raises(ValueError, match="lse must be"):
+        nat.cross_bwd(x, x, x, x, x, torch.zeros(1, 2, 4), *[None] * 7)
     c = torch.zeros(8, 32)
-    with pytest.raises(ValueError, match="q's B and d"):
-        attn._cross_shapes(torch.zeros(1, 2, 3, 64, **bf), torch.zeros(2, 2, 3, 64, **bf), torch.zeros(2, 2, 3, 64, **bf))
-    with pytest.raises(ValueError, match="bfloat16"):
-        attn._cross_shapes(*(torch.zeros(1, 2, 3, 64) for _ in range(3)))
-    with pytest.raises(ValueError, match="contiguous"):
-        attn._cross_shapes(torch.zeros(1, 3, 2, 64, **bf).transpose(1, 2), *(torch.zeros(1, 2, 3, 64, **bf),) * 2)
-    with pytest.raises(ValueError, match="kv_lens"):
-        attn._kv_lens(torch.zeros(3), 3)
-    with pytest.raises(ValueError, match="rows"):
-        attn._row_strides(torch.zeros(4, 64, 2).transpose(1, 2), "q")
-    assert attn._row_strides(torch.zeros(512).as_strided((4, 1, 64), (128, 3, 1)), "q") == [128, 64]
-    rows = torch.zeros(4, 6, 64, **bf)
-    with pytest.raises(ValueError, match="caches"):
-        attn._append_rows(rows, rows, None, None, (3, 16, 2, 64))
-    with pytest.raises(ValueError, match="k and v"):
-        attn._append_rows(rows, rows[:, :2], None, None, (3, 16, 6, 64))
-    with pytest.raises(ValueError, match="q_out"):
-        attn._append_rows(rows, rows, None, rows, (3, 16, 6, 64))
-    with pytest.raises(ValueError, match="rope_sin"):
-        attn._rope_tables(c, torch.zeros(8, 16))
+    rope = lambda q, k=None, cos=c, sin=c, pos=None, qo=None, ko=None: nat.rope(q, k, cos, sin, pos, False, False, qo, ko, None)
+    for args, why in (((x, None, c, torch.zeros(8, 16)), "rope_sin"), ((x, None, c[0], c[0]), "rope_cos"),
+                      ((x, None, None), "rope_cos is missing"), ((x[0, 0],), "packed"), ((x.float(),), "float16"), ((x[:, :0],), "empty"),
+                      ((x, x[:, :, :2]), "k must match"), ((x, x[0]), "k must match"), ((x, None, c, c, torch.zeros(3, **i32)), "positions"),
+                      ((x, None, c, c, None, x.half()), "q_out"), ((x, None, c, c, None, None, x), "k_out"),
+                      ((x,), "current CUDA device")):
+        with pytest.raises(ValueError, match=why):
+            rope(*args)
+    rows, cache, slots = torch.zeros(4, 6, 64, **bf), torch.zeros(3, 16, 6, 64, **bf), torch.zeros(4, dtype=torch.int64)
+
+    def append(k=rows, v=rows, kc=cache, vc=cache, slots=slots, cos=None, sin=None, pos=None, q=None, qo=None):
+        nat.cache_append(k, v, kc, vc, slots, cos, sin, pos, q, False, qo, None)
+
+    for kw, why in ((dict(kc=cache[:, :, :2]), "caches"), (dict(v=rows[:, :2]), "k and v"), (dict(qo=rows), "q_out"),
+                    (dict(k=torch.zeros(4, 64, 6, **bf).transpose(1, 2)), "rows"), (dict(slots=slots.int()), "slots"),
+                    (dict(cos=c, sin=c), "positions"), (dict(cos=c), "both"), (dict(q=rows[:3]), "q must be"),
+                    (dict(vc=cache.half()), "v_cache"), (dict(), "current CUDA device")):
+        with pytest.raises(ValueError, match=why):
+            append(**kw)
+    v8 = torch.zeros(3, 16, 6, 64, dtype=torch.uint8)
+    d8, bt, lens = torch.zeros(3, 6), torch.zeros(2, 2, **i32), torch.zeros(2, **i32)
+    for i, (bad, why) in enumerate(((cache, "k_cache"), (v8, "v_descale"), (v8, "block_table"), (v8, "cu_seqlens"),
+                                    (v8, "current CUDA device"))):
+        with pytest.raises(ValueError, match=why):
+            nat.cache_append_fp8(rows, rows, bad, v8, d8, d8[:2] if i == 1 else d8, bt[0] if i == 2 else bt, lens,
+                                 lens if i == 3 else torch.zeros(3, **i32), None, None, None, None, False, None, None)
+    for args, why in (((bt, lens, lens, lens, 16, -1), "capacity"), ((bt[0], lens, lens, lens, 16, 4), "max_pages"),
+                      ((bt, lens.long(), lens, lens, 16, 4), "old_lens"), ((bt, lens, lens, lens, 2 ** 40, 4), "page_size"),
+                      ((bt, lens, lens, lens, 16, 4), "current CUDA device")):
+        with pytest.raises(ValueError, match=why):
+            nat.block_tables(*args, *[None] * 6)
+    with pytest.raises(ValueError, match="positive"):
+        nat.rope_table(0, 64, 1e4, 1.0, 0, 1.0, 32.0, 1.0, 0, None, None, None)
+    with pytest.raises(TypeError):
+        nat.rope_table(4, 64, "x", 1.0, 0, 1.0, 32.0, 1.0, 0, None, None, None)
