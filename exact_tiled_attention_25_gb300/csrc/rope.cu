@@ -35,15 +35,30 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeKParams p)
 // p * F modulo 2^64 is the angle modulo one turn, exactly, in integers.  Its upper
 // 32 bits, as a signed number of half turns, are what sincospif takes.  F is off by
 // at most 2^-53 of itself, the cut to 32 bits by 2^-33 of a turn.
-// Bound: instruction issue, close to the writes (8 bytes per entry).
+//
+// A thread owns a column.  Every eighth of its rows takes the sine and cosine of its
+// own angle, the seven behind it the sum formulas with those of 1 .. 7 row steps,
+// computed once per thread: one composition, so at most 2^-23 of error on top.
+// Bound: the writes, 8 bytes per entry.  131072 x 64 entries: 238 us with float64
+// angles, 17.4 us with a sine and cosine per entry, 12.7 us so (5.3 TB/s).
 struct RopeTurns {
   unsigned long long f[128];
 };
+
+// cos and sin of an angle in turns, as a 64-bit binary fraction.
+__device__ __forceinline__ float2 cos_sin_turns(unsigned long long angle) {
+  // the nearest multiple of 2^-32 turns, as half turns in [-1, 1)
+  const int half_turns = static_cast<int>((angle + 0x80000000ull) >> 32);
+  float sn, cs;
+  sincospif(static_cast<float>(half_turns) * 4.656612873077392578125e-10f, &sn, &cs);
+  return make_float2(cs, sn);
+}
 
 __global__ void __launch_bounds__(256)
     rope_table_kernel(float* __restrict__ cos_out, float* __restrict__ sin_out, long long n, int half,
                       const __grid_constant__ RopeTurns turns, float attn_factor, unsigned first,
                       int rows_per_block) {
+  constexpr int kRun = 8;
   const int lanes = 256 / half;                     // rows written at a time
   const int i = static_cast<int>(threadIdx.x) % half;
   const int sub = static_cast<int>(threadIdx.x) / half;
@@ -51,15 +66,24 @@ __global__ void __launch_bounds__(256)
   const unsigned long long f = turns.f[i];
   const long long r0 = static_cast<long long>(blockIdx.x) * rows_per_block;
   const long long r1 = r0 + rows_per_block < n ? r0 + rows_per_block : n;
-  unsigned long long angle = f * (static_cast<unsigned long long>(first) + r0 + sub);
   const unsigned long long step = f * lanes;
-  for (long long r = r0 + sub; r < r1; r += lanes, angle += step) {
-    // the nearest multiple of 2^-32 turns, as half turns in [-1, 1)
-    const int half_turns = static_cast<int>((angle + 0x80000000ull) >> 32);
-    float sn, cs;
-    sincospif(static_cast<float>(half_turns) * 4.656612873077392578125e-10f, &sn, &cs);
-    cos_out[r * half + i] = cs * attn_factor;
-    sin_out[r * half + i] = sn * attn_factor;
+  float2 by[kRun];
+#pragma unroll
+  for (int k = 1; k < kRun; ++k) by[k] = cos_sin_turns(step * k);
+  unsigned long long angle = f * (static_cast<unsigned long long>(first) + r0 + sub);
+  for (long long r = r0 + sub; r < r1; r += kRun * lanes, angle += step * kRun) {
+    float2 b = cos_sin_turns(angle);
+    b = make_float2(b.x * attn_factor, b.y * attn_factor);
+    float* c = cos_out + r * half + i;
+    float* s = sin_out + r * half + i;
+    *c = b.x;
+    *s = b.y;
+#pragma unroll
+    for (int k = 1; k < kRun; ++k) {
+      if (r + k * lanes >= r1) break;
+      c[k * lanes * half] = fmaf(-b.y, by[k].y, b.x * by[k].x);
+      s[k * lanes * half] = fmaf(b.x, by[k].y, b.y * by[k].x);
+    }
   }
 }
 
@@ -100,8 +124,8 @@ attn_status_t launch_rope_table(float* cos_out, float* sin_out, long long n, int
     // below 1 / (2 pi) turns per position, times 2^64
     turns.f[i] = static_cast<unsigned long long>(std::ldexp(theta / kTwoPi, 64));
   }
-  // eight blocks per SM, at least 8 rows each
-  long long rows = (n + 152 * 8 - 1) / (152 * 8);
+  // four blocks per SM, at least 8 rows each
+  long long rows = (n + 152 * 4 - 1) / (152 * 4);
   rows = rows < 8 ? 8 : rows;
   const long long blocks = (n + rows - 1) / rows;
   rope_table_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
