@@ -415,6 +415,18 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
           tmem_st32(tmem + lane_addr + C::O_COL + c0 * 32, o);
         }
       }
+      // slots of the last page behind the sequence may hold anything: their rows of V
+      // meet P = 0 in the product, so they are zeroed first (0 * NaN = NaN)
+      if (kbase + DBN > len) {
+        const int item = 2 * j + 1;
+        if (__any_sync(0xffffffffu, !mbar_wait(&kv_full[item % NSLOT], (item / NSLOT) & 1, ab,
+                                               kDevTimeoutSoftmax))) {
+          ok = false;
+          break;
+        }
+        zero_tile_rows<C::CH, C::CHUNK>(sKV + (item % NSLOT) * C::TILE, len - kbase, r, 128);
+        fence_proxy_async_smem();
+      }
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(&p_full[j & 1]);

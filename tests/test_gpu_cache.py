@@ -408,6 +408,31 @@ def test_decoder_layer_steps(attn, fp8):
         assert torch.isneginf(cl[1]).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_paged_decode_over_pages_never_cleared(attn, d, dtype):
+    """Slots behind a sequence (rest of its last page, free pages) hold NaN and infinities:
+    the decode's result is the one over clean pages, bit for bit."""
+    lens, page = [1, 63, 64, 65, 129, 300], 64
+    kc, vc, table = workloads.paged_cache(80, lens, page, 2, d)
+    q = workloads.round_to(workloads.normal(81, (len(lens), 8, 1, d)), dtype).to(dev())
+    outs = []
+    for dirty in (False, True):
+        k, v = (workloads.round_to(x, dtype).to(dev()) for x in (kc, vc))
+        if dirty:
+            used = torch.zeros(k.shape[:2], dtype=torch.bool)
+            for b, n in enumerate(lens):
+                for t in range(n):
+                    used[table[b, t // page], t % page] = True
+            k[~used.to(dev())] = float("nan")
+            v[~used.to(dev())] = float("nan")
+            v[~used.to(dev())][::2] = float("inf")
+        outs.append(attn.attn_decode_paged(q, k, v, torch.from_numpy(table).to(dev()), _i32(lens), max(lens)))
+        check_status(attn)
+    assert torch.isfinite(outs[1][0].float()).all()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
 def test_training_layer(attn):
     """Rotation, causal attention and cross attention forward and backward, chained, against
     the oracle's chain (gradient tolerance of the attention tests)."""
