@@ -756,11 +756,13 @@ def _binding():
 
 def _moved(call, tensors, *rest):
     """call(*tensors, *rest) with the CPU tensors (None: absent) copied to the current
-    device, and its results copied back; a mixture goes on to the call's own refusal."""
-    moved, host = _to_device([t for t in tensors if t is not None])
-    it = iter(moved)
-    out = call(*[None if t is None else next(it) for t in tensors], *rest)
-    return tuple(None if t is None else t.cpu() for t in out) if host else out
+    device, and its results copied back, all on the call's stream (the last argument);
+    a mixture goes on to the call's own refusal."""
+    with torch.cuda.stream(rest[-1]):
+        moved, host = _to_device([t for t in tensors if t is not None])
+        it = iter(moved)
+        out = call(*[None if t is None else next(it) for t in tensors], *rest)
+        return tuple(None if t is None else t.cpu() for t in out) if host else out
 
 
 def attn_cross_workspace_size(B: int, H: int, H_kv: int, N_q: int, N_k: int, d: int) -> int:

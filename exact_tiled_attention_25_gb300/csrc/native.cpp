@@ -11,6 +11,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -86,9 +87,13 @@ void like(const Arg& a, at::IntArrayRef shape, at::ScalarType type) {
     throw Refused(std::string(a.name) + " must be contiguous " + c10::toString(type) + " " + shape_text(shape));
 }
 
-// The current CUDA device, where every tensor of a call has to be.
+// The current CUDA device, where every tensor of a call has to be, and the call's
+// stream.  Outputs and scratch are allocated as that stream's: freed scratch is not
+// handed to another stream while the kernel that uses it may still run.
 struct Device {
   c10::DeviceIndex index = -1;
+  cudaStream_t stream = nullptr;
+  bool other = false;      // not the current stream
   void check(const Arg& a) {
     if (!a) return;
     if (a.t.is_cuda() && index < 0) index = c10::cuda::current_device();
@@ -96,12 +101,24 @@ struct Device {
       throw Refused(std::string(a.name) + " must be on the current CUDA device");
   }
   template <typename... A>
-  explicit Device(const A&... args) {
+  explicit Device(PyObject* stream_arg, const A&... args) {
     (check(args), ...);
     if (index < 0) index = c10::cuda::current_device();
+    stream = c10::cuda::getCurrentCUDAStream(index).stream();
+    if (stream_arg == Py_None) return;
+    PyObject* h = PyObject_GetAttrString(stream_arg, "cuda_stream");
+    if (!h) throw Raised{};
+    void* p = PyLong_AsVoidPtr(h);
+    Py_DECREF(h);
+    if (!p && PyErr_Occurred()) throw Raised{};
+    other = static_cast<cudaStream_t>(p) != stream;
+    stream = static_cast<cudaStream_t>(p);
   }
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, index)));
+    const at::TensorOptions as = at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, index));
+    if (!other) return at::empty(shape, as);
+    const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(stream, index));
+    return at::empty(shape, as);
   }
   // a given output of that shape and type, or a new one
   void output(Arg& a, at::IntArrayRef shape, at::ScalarType type) const {
@@ -110,15 +127,6 @@ struct Device {
   }
   void workspace(Arg& a, size_t bytes) const {
     if (!a && bytes > 0) a.t = empty({static_cast<int64_t>(bytes)}, at::kByte);
-  }
-  cudaStream_t stream(PyObject* o) const {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(index).stream();
-    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-    if (!h) throw Raised{};
-    void* p = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    if (!p && PyErr_Occurred()) throw Raised{};
-    return static_cast<cudaStream_t>(p);
   }
 };
 
@@ -223,14 +231,13 @@ PyObject* cross_fwd(PyObject* const* a) {
   Arg q("q", a[0]), k("k", a[1]), v("v", a[2]), lens("kv_lens", a[3]), o("o", a[5]), lse("lse", a[6]), ws("workspace", a[7]);
   const CrossShape s = cross_shape(q, k, v, lens);
   const float scale = scale_of(a[4], s.d);
-  const Device dev(q, k, v, lens, o, lse, ws);
+  const Device dev(a[8], q, k, v, lens, o, lse, ws);
   dev.output(o, q.t.sizes(), q.t.scalar_type());
   dev.output(lse, {s.B, s.H, s.N_q}, at::kFloat);
   dev.workspace(ws, api.attn_cross_workspace_size(s.B, s.H, s.H_kv, s.N_q, s.N_k, s.d));
-  const cudaStream_t stream = dev.stream(a[8]);
   call("attn_cross_fwd", [&] {
     return api.attn_cross_fwd(q.ptr(), k.ptr(), v.ptr(), lens.as<int>(), o.ptr(), lse.as<float>(), ws.ptr(),
-                              ws ? ws.t.nbytes() : 0, s.B, s.H, s.H_kv, s.N_q, s.N_k, s.d, scale, dtype_of(q.t), stream);
+                              ws ? ws.t.nbytes() : 0, s.B, s.H, s.H_kv, s.N_q, s.N_k, s.d, scale, dtype_of(q.t), dev.stream);
   });
   return tuple({&o, &lse});
 }
@@ -243,16 +250,15 @@ PyObject* cross_bwd(PyObject* const* a) {
   like(dout, q.t.sizes(), q.t.scalar_type());
   like(lse, {s.B, s.H, s.N_q}, at::kFloat);
   const float scale = scale_of(a[7], s.d);
-  const Device dev(q, k, v, o, dout, lse, lens, dq, dk, dv, ws);
+  const Device dev(a[12], q, k, v, o, dout, lse, lens, dq, dk, dv, ws);
   dev.output(dq, q.t.sizes(), q.t.scalar_type());
   dev.output(dk, k.t.sizes(), q.t.scalar_type());
   dev.output(dv, k.t.sizes(), q.t.scalar_type());
   dev.workspace(ws, api.attn_cross_bwd_workspace_size(s.B, s.H, s.N_q, s.N_k, s.d));
-  const cudaStream_t stream = dev.stream(a[12]);
   call("attn_cross_bwd", [&] {
     return api.attn_cross_bwd(q.ptr(), k.ptr(), v.ptr(), o.ptr(), dout.ptr(), lse.as<float>(), lens.as<int>(), dq.ptr(),
                               dk.ptr(), dv.ptr(), ws.ptr(), ws ? ws.t.nbytes() : 0, s.B, s.H, s.H_kv, s.N_q, s.N_k, s.d,
-                              scale, dtype_of(q.t), stream);
+                              scale, dtype_of(q.t), dev.stream);
   });
   return tuple({&dq, &dk, &dv});
 }
@@ -301,12 +307,11 @@ PyObject* rope_table(PyObject* const* a) {
   Arg cos("rope_cos", a[9]), sin("rope_sin", a[10]);
   if (cos) like(cos, {n, rot / 2}, at::kFloat);
   if (sin) like(sin, {n, rot / 2}, at::kFloat);
-  const Device dev(cos, sin);
+  const Device dev(a[11], cos, sin);
   dev.output(cos, {n, rot / 2}, at::kFloat);
   dev.output(sin, {n, rot / 2}, at::kFloat);
-  const cudaStream_t stream = dev.stream(a[11]);
   call("attn_rope_table", [&] {
-    return api.attn_rope_table(cos.as<float>(), sin.as<float>(), n, rot, base, factor, orig, low, high, attn, first, stream);
+    return api.attn_rope_table(cos.as<float>(), sin.as<float>(), n, rot, base, factor, orig, low, high, attn, first, dev.stream);
   });
   return tuple({&cos, &sin});
 }
@@ -339,16 +344,15 @@ PyObject* rope(PyObject* const* a) {
     if (*x && (x->t.sizes() != in.t.sizes() || x->t.scalar_type() != in.t.scalar_type()))
       throw Refused(std::string(x->name) + " must match its input in shape and dtype");
   }
-  const Device dev(q, k, cos, sin, pos, qo, ko);
+  const Device dev(a[9], q, k, cos, sin, pos, qo, ko);
   if (!qo) qo.t = dev.empty(q.t.sizes(), q.t.scalar_type());
   if (k && !ko) ko.t = dev.empty(k.t.sizes(), q.t.scalar_type());
   const Strides3 sq(q, packed), sqo(qo, packed), sk(k ? k : q, packed), sko(k ? ko : qo, packed);
   const int inter = truth(a[5]), inv = truth(a[6]);
-  const cudaStream_t stream = dev.stream(a[9]);
   call("attn_rope", [&] {
     return api.attn_rope(q.ptr(), qo.ptr(), k.ptr(), ko.ptr(), cos.as<float>(), sin.as<float>(), pos.as<int>(),
                          extent(B), extent(N), extent(H), extent(H_kv), extent(d), tab.rot, tab.max_pos, sq.s, sqo.s, sk.s,
-                         sko.s, inter, inv, dtype_of(q.t), stream);
+                         sko.s, inter, inv, dtype_of(q.t), dev.stream);
   });
   return tuple({&qo, &ko});
 }
@@ -365,17 +369,16 @@ PyObject* block_tables(PyObject* const* a) {
   like(old, {B}, at::kInt);
   like(add, {B}, at::kInt);
   like(free_, free_.t.sizes(), at::kInt);
-  const Device dev(bt, old, add, free_, lens, cu, slots, pos, used);
+  const Device dev(a[11], bt, old, add, free_, lens, cu, slots, pos, used);
   dev.output(lens, {B}, at::kInt);
   dev.output(cu, {B + 1}, at::kInt);
   dev.output(slots, {cap}, at::kLong);
   dev.output(pos, {cap}, at::kInt);
   dev.output(used, {1}, at::kInt);
-  const cudaStream_t stream = dev.stream(a[11]);
   call("attn_block_tables", [&] {
     return api.attn_block_tables(bt.as<int>(), old.as<int>(), add.as<int>(), free_.as<int>(), lens.as<int>(), cu.as<int>(),
                                  slots.as<long long>(), pos.as<int>(), used.as<int>(), B, max_pages, extent(free_.size(0)),
-                                 page, cap, stream);
+                                 page, cap, dev.stream);
   });
   return tuple({&lens, &cu, &slots, &pos, &used});
 }
@@ -419,15 +422,14 @@ PyObject* cache_append(PyObject* const* a) {
     require(static_cast<bool>(pos), "rotation needs positions");
     like(pos, {r.total}, at::kInt);
   }
-  const Device dev(k, v, kc, vc, slots, cos, sin, pos, q, qo);
+  const Device dev(a[11], k, v, kc, vc, slots, cos, sin, pos, q, qo);
   if (q) dev.output(qo, {r.total, r.H, r.d}, k.t.scalar_type());
   const int inter = truth(a[9]);
-  const cudaStream_t stream = dev.stream(a[11]);
   call("attn_cache_append", [&] {
     return api.attn_cache_append(q.ptr(), qo.ptr(), k.ptr(), v.ptr(), kc.ptr(), vc.ptr(), slots.as<long long>(),
                                  cos.as<float>(), sin.as<float>(), pos.as<int>(), r.total, r.H, r.H_kv, r.d, tab.rot,
                                  tab.max_pos, extent(kc.size(0)), extent(kc.size(1)), r.qs, r.ks, r.vs, inter,
-                                 dtype_of(k.t), stream);
+                                 dtype_of(k.t), dev.stream);
   });
   return qo ? THPVariable_Wrap(qo.t) : Py_NewRef(Py_None);
 }
@@ -448,16 +450,15 @@ PyObject* cache_append_fp8(PyObject* const* a) {
   like(cu, {B + 1}, at::kInt);
   if (signs) like(signs, {r.d}, at::kFloat);
   const Tables tab(cos, sin);
-  const Device dev(k, v, kc, vc, kd, vd, bt, lens, cu, cos, sin, signs, q, qo);
+  const Device dev(a[15], k, v, kc, vc, kd, vd, bt, lens, cu, cos, sin, signs, q, qo);
   if (q) dev.output(qo, {r.total, r.H, r.d}, k.t.scalar_type());
   const int inter = truth(a[13]);
-  const cudaStream_t stream = dev.stream(a[15]);
   call("attn_cache_append_fp8", [&] {
     return api.attn_cache_append_fp8(q.ptr(), qo.ptr(), k.ptr(), v.ptr(), kc.as<uint8_t>(), vc.as<uint8_t>(),
                                      kd.as<float>(), vd.as<float>(), bt.as<int>(), lens.as<int>(), cu.as<int>(),
                                      cos.as<float>(), sin.as<float>(), signs.as<float>(), B, r.total, r.H, r.H_kv, r.d,
                                      tab.rot, tab.max_pos, extent(kc.size(0)), extent(kc.size(1)), extent(bt.size(1)),
-                                     r.qs, r.ks, r.vs, inter, dtype_of(k.t), stream);
+                                     r.qs, r.ks, r.vs, inter, dtype_of(k.t), dev.stream);
   });
   return qo ? THPVariable_Wrap(qo.t) : Py_NewRef(Py_None);
 }

@@ -302,3 +302,26 @@ def test_self_attention_is_the_same_arithmetic(attn):
     for x, y in zip(grads, attn.attn_bwd(q, k, v, o, do, lse)):
         assert torch.all((x.float() - y.float()).abs() <= 2.0 ** -7 * y.float().abs() + 1e-5)
     check_status(attn)
+
+
+def test_explicit_stream(attn):
+    """Calls on a stream that is not the current one, their scratch and outputs freed at once
+    while the current stream allocates and writes: nothing of theirs is handed out early."""
+    B, H, N_q, N_k, d = 2, 8, 96, 2000, 128
+    q, k, v, do = (t.to(dev()) for t in _inputs(998, B, H, H, N_q, N_k, d, "bf16"))
+    want = attn.attn_cross_fwd(q, k, v)
+    grads = attn.attn_cross_bwd(q, k, v, want[0], do, want[1])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        o, lse = attn.attn_cross_fwd(q, k, v, stream=side)
+        dq, dk, dv = attn.attn_cross_bwd(q, k, v, o, do, lse, stream=side)
+        del dq
+        for n in (q.numel() * 2, 1 << 20, attn.attn_cross_bwd_workspace_size(B, H, N_q, N_k, d)):
+            torch.empty(n, dtype=torch.uint8, device=dev()).fill_(255)
+        side.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        assert torch.equal(dk, grads[1]) and torch.equal(dv, grads[2])
+    o, lse = attn.attn_cross_fwd(q.cpu(), k.cpu(), v.cpu(), stream=side)
+    assert torch.equal(o, want[0].cpu())
+    check_status(attn)

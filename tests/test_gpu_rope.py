@@ -165,3 +165,20 @@ def test_host_tensors_and_graph(attn):
     torch.cuda.synchronize()
     assert torch.equal(oq.cpu(), qo) and torch.equal(ok.cpu(), ko)
     check_status(attn)
+
+
+def test_explicit_stream(attn):
+    q = torch.from_numpy(workloads.normal(8, (700, 32, 128))).to(dev(), torch.bfloat16)
+    side = torch.cuda.Stream()
+    cos, sin = attn.attn_rope_table(700, 128, stream=side)
+    side.synchronize()
+    want, _ = attn.attn_rope(q, None, cos, sin)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        c, s = attn.attn_rope_table(700, 128, stream=side)
+        got, _ = attn.attn_rope(q, None, c, s, stream=side)
+        del c, s
+        torch.empty(700 * 64, device=dev()).fill_(9.0)
+        side.synchronize()
+        assert torch.equal(got, want)
+    check_status(attn)
