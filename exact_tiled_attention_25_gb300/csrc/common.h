@@ -56,6 +56,24 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Launch a grid of clusters of `cluster` blocks.
+template <typename... Params, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(Params...), int grid, int cluster, int threads, int smem,
+                           cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Opt a kernel into more than 48 KB of dynamic shared memory (once per kernel).
 attn_status_t set_smem(const void* kernel, int bytes);
 
@@ -238,24 +256,28 @@ inline size_t decode_workspace_bytes(int B, int H, int H_kv, int n_q, int d, int
 
 attn_status_t launch_decode(const DecodeParams& p, cudaStream_t stream);
 
-// How a cross-attention forward runs.  ctas > 0: the rows kernel (cross.cu), that many
-// CTAs sharing the tiles of all keys, for tiles of 128 query rows of one key/value
-// head (its G * N_q rows together); ctas = 0: the forward kernel (fwd.cu), one CTA
-// per 256 query rows of one query head with all keys.
+// How a cross-attention forward runs.  ctas > 0: the rows kernel (cross.cu) on tiles of
+// 128 query rows of one key/value head (its G * N_q rows together), that many CTAs
+// sharing the tiles of all keys, or in clusters of `cluster` CTAs, one for each
+// query tile's keys; ctas = 0: the forward kernel (fwd.cu), one CTA per 256 query rows of
+// one query head with all keys.
 struct CrossPlan {
-  int ctas, qtiles;
+  int ctas, qtiles, cluster;
 };
 constexpr int kCrossMaxB = 2048;   // batch entries of the rows kernel (8 bytes of shared memory each)
-// The smaller of two modelled times, in microseconds, fitted to both kernels at d = 64
+// The smallest of three modelled times, in microseconds, fitted to the kernels at d = 64
 // and 128, N_k = 512 .. 4096 and N_q = 1 .. 1024 (bfloat16, K and V in L2):
 //  forward: waves of 152 CTAs x (3.5 + 1.4 or 1.55 per key tile), a tenth more per
 //           tile when both of a CTA's query tiles are in use;
-//  rows:    a start and a merge, the tiles of one CTA's share, and 2 or more for
-//           every segment it finishes (its output leaves tensor memory row by row).
+//  shared:  a start and a merge, the tiles of one CTA's share, and 2 or more for
+//           every segment it finishes (its output leaves tensor memory row by row);
+//  cluster: waves of the clusters that run at a time (they do not fill every SM: 152, 76,
+//           46, 36, 28, 23, 15 and 15 of 1 to 8 CTAs) x (a start, one CTA's tiles of its
+//           segment and their merge).
 // 16 heads, N_k = 4096, d = 128: N_q = 1: 51 us (forward), 17 (rows); 512: 56, 44;
 // 1024: 57, 74.  8 x 16 heads, N_k = 512: N_q = 1: 10, 13.
 inline CrossPlan cross_plan(int B, int H, int H_kv, int N_q, int N_k, int d) {
-  if (d > 128 || B > kCrossMaxB) return {0, 0};
+  if (d > 128) return {0, 0, 0};
   const long long rows = static_cast<long long>(H / H_kv) * N_q;
   const long long qtiles = (rows + 127) / 128, ktiles = (N_k + 127) / 128;
   const long long segs = static_cast<long long>(B) * H_kv * qtiles, tiles = segs * ktiles;
@@ -266,12 +288,29 @@ inline CrossPlan cross_plan(int B, int H, int H_kv, int N_q, int N_k, int d) {
   const double share = static_cast<double>((tiles + 151) / 152), ends = static_cast<double>((segs + 151) / 152);
   const double shared = d == 64 ? 9.0 + share * (few ? 0.75 : 0.95) + ends * (few ? 0.3 : 2.0)
                                 : (few ? 10.0 : 12.0) + share * (few ? 1.0 : 1.16) + ends * (few ? 0.3 : 2.7);
-  if (fwd <= shared || tiles > 2147483647LL || H_kv * qtiles > 2147483647LL) return {0, 0};
-  return {static_cast<int>(tiles < 152 ? tiles : 152), static_cast<int>(qtiles)};
+  if (tiles > 2147483647LL || H_kv * qtiles > 2147483647LL || segs > 2147483647LL / 8) return {0, 0, 0};
+  CrossPlan plan{0, static_cast<int>(qtiles), 0};
+  double best = fwd;
+  if (shared < best && B <= kCrossMaxB) {
+    best = shared;
+    plan.ctas = static_cast<int>(tiles < 152 ? tiles : 152);
+  }
+  constexpr int at_a_time[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+  for (int c = 1; c <= 8; ++c) {
+    const double waves = static_cast<double>((segs + at_a_time[c] - 1) / at_a_time[c]);
+    const double t = waves * (d == 64 ? (few ? 6.5 : 8.5) + (ktiles + c - 1) / c * (few ? 0.75 : 0.95)
+                                      : (few ? 7.5 : 10.7) + (ktiles + c - 1) / c * (few ? 1.0 : 1.16));
+    if (t < best) {
+      best = t;
+      plan.cluster = c;
+      plan.ctas = static_cast<int>(segs * c);
+    }
+  }
+  return plan;
 }
 // The rows kernel's float32 partial O and log-sum-exps, two per CTA.
 inline size_t cross_workspace_bytes(int H, int H_kv, int N_q, int d, const CrossPlan& plan) {
-  if (plan.ctas <= 1) return 0;
+  if (plan.ctas <= 1 || plan.cluster > 0) return 0;
   const size_t seg = static_cast<size_t>(H / H_kv) * N_q;
   const size_t rows = 2ull * plan.ctas * (seg < 128 ? seg : 128);
   return align_up(rows * d * sizeof(float), 256) + align_up(rows * sizeof(float), 256);

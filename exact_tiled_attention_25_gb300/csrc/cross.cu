@@ -16,6 +16,10 @@
 //  * A segment inside one share is finished there.  One that crosses shares
 //    leaves float32 partial outputs and log-sum-exps, at most two per CTA, which a
 //    second kernel merges; its launch overlaps the first kernel.
+//  * With few segments, a cluster of up to eight CTAs takes one instead and merges its
+//    partial outputs through distributed shared memory: one launch, no scratch, no
+//    prefix sums.  (1 x 16 heads, N_q = 1, N_k = 1500, d = 64: 9.4 us shared, 8.0 so;
+//    2 x 16 heads, N_k = 4096: 13.7 and 12.3.)
 //
 // Roles: key and value producer warps, an MMA warp for the score products and one for
 // the P V products (issuing a product or a commit costs a thread some hundred cycles:
@@ -115,6 +119,7 @@ struct Cursor {
   __device__ __forceinline__ int part() const { return min(tiles() - j, left); }
   __device__ __forceinline__ void next_part(int n) {
     left -= n;
+    if (left <= 0) return;
     j = 0;
     if (++y == segs) {
       y = 0;
@@ -142,7 +147,9 @@ __device__ __forceinline__ Cursor cursor_at(const int* pre, int segs, int B, int
   return c;
 }
 
-template <int D, bool FP16, bool FEW>
+// CLUSTER: the cluster's CTAs share one segment, batch entry and segment of it from
+// the cluster's index.
+template <int D, bool FP16, bool FEW, bool CLUSTER>
 __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
     cross_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const CrossKParams kp) {
@@ -168,8 +175,9 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
   __shared__ int issued_sh[2];      // items that a producer issued: keys, values
   __shared__ int parts_sh;          // Q tiles issued
   __shared__ int warp_sum[C::THREADS / 32];
-  __shared__ int pre[kCrossMaxB + 1];
-  __shared__ int lens[kCrossMaxB];
+  __shared__ int pre_sh[(CLUSTER ? 1 : kCrossMaxB) + 1];
+  __shared__ int lens_sh[CLUSTER ? 1 : kCrossMaxB];
+  __shared__ float lse_sh[CLUSTER ? BM : 1];       // of the partial output in the ring's place
   __shared__ float xch[FEW ? 4 : 1][16][65];       // 64 columns of the four outputs
   __shared__ float2 stat[FEW ? 4 : 1][16];         // their maxima and sums
   __shared__ __align__(8) uint64_t xch_bar;        // the softmax threads meet around them
@@ -178,11 +186,15 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
   const int lane = threadIdx.x % 32;
 
   // the merging kernel may start its prologue (it waits for this grid's end)
-  release_dependents();
+  if constexpr (!CLUSTER) release_dependents();
 
   // ---- prologue: tiles of a segment of the batch entries before each, while the
   // barriers are set up, tensor memory is allocated and the tensor maps arrive
-  const int per = (kp.B + C::THREADS - 1) / C::THREADS;
+  const int ranks = CLUSTER ? static_cast<int>(cluster_size()) : 1;
+  const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+  const int seg = static_cast<int>(blockIdx.x) / ranks;            // CLUSTER: of all
+  const int my_b = CLUSTER ? seg / kp.segs : 0;
+  const int per = CLUSTER ? 0 : (kp.B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, kp.B), b1 = min(b0 + per, kp.B);
   const int first_len = kp.kv_lens && b0 < b1 ? __ldg(kp.kv_lens + b0) : kp.Nk;
   if (warp == C::MMA_S_WARP) {
@@ -212,7 +224,18 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
     issued_sh[0] = issued_sh[1] = parts_sh = 0;
     fence_mbar_init();
   }
-  {
+  if constexpr (CLUSTER) {
+    if (threadIdx.x == 32) {
+      int n = kp.kv_lens ? __ldg(kp.kv_lens + my_b) : kp.Nk;
+      if (n < 0 || n > kp.Nk) {
+        if (seg % kp.segs == 0 && rank == 0) atomicCAS(kp.status, 0, kDevBadSeqlens);
+        n = 0;
+      }
+      lens_sh[0] = n;
+      pre_sh[0] = 0;
+      pre_sh[1] = (n + BN - 1) / BN;
+    }
+  } else {
     int sum = 0;
     for (int b = b0; b < b1; ++b) {
       int n = b == b0 ? first_len : kp.kv_lens ? __ldg(kp.kv_lens + b) : kp.Nk;
@@ -220,7 +243,7 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
         if (blockIdx.x == 0) atomicCAS(kp.status, 0, kDevBadSeqlens);
         n = 0;
       }
-      lens[b] = n;
+      lens_sh[b] = n;
       sum += (n + BN - 1) / BN;
     }
     int scan = sum;
@@ -234,20 +257,32 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
     int base = scan - sum;
     for (int w = 0; w < warp; ++w) base += warp_sum[w];
     for (int b = b0; b < b1; ++b) {
-      pre[b] = base;
-      base += (lens[b] + BN - 1) / BN;
+      pre_sh[b] = base;
+      base += (lens_sh[b] + BN - 1) / BN;
     }
-    if (b1 == kp.B && b0 < b1) pre[kp.B] = base;
+    if (b1 == kp.B && b0 < b1) pre_sh[kp.B] = base;
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = tmem_base_sh;
   const Abort ab{&abort_sh, kp.status};
-  const int T = pre[kp.B] * kp.segs;
-  const int g0 = share_start(blockIdx.x, gridDim.x, T);
-  const int total = share_start(blockIdx.x + 1, gridDim.x, T) - g0;   // tiles of this CTA
-  Cursor cur = cursor_at(pre, kp.segs, kp.B, g0, total);
+  // indexed by batch entry; a cluster's has one
+  const int* const pre = pre_sh - my_b;
+  const int* const lens = lens_sh - my_b;
+  int g0, total;                                   // first tile and tiles of this CTA
+  Cursor cur;
+  if constexpr (CLUSTER) {
+    const int nt = pre_sh[1];
+    g0 = rank * nt / ranks;
+    total = (rank + 1) * nt / ranks - g0;
+    cur = Cursor{pre, kp.segs, kp.B, my_b, seg % kp.segs, g0, total};
+  } else {
+    const int T = pre[kp.B] * kp.segs;
+    g0 = share_start(blockIdx.x, gridDim.x, T);
+    total = share_start(blockIdx.x + 1, gridDim.x, T) - g0;
+    cur = cursor_at(pre, kp.segs, kp.B, g0, total);
+  }
 
   if (warp == C::LOAD_WARP || warp == C::LOAD_V_WARP) {
     // ------------------------------------------------------------ producers
@@ -376,8 +411,12 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
       bool whole, last;
       float m, l;
     } done{-1, 0, 0, false, false, 0.f, 0.f};
+    // partial outputs: the workspace's, or this CTA's for its cluster (the ring is free by
+    // then: every copy has been consumed)
+    float* const o_part = CLUSTER ? reinterpret_cast<float*>(sKV) : kp.o_part;
+    float* const lse_part = CLUSTER ? lse_sh : kp.lse_part;
     auto store_lse = [&](size_t at, size_t part_at, float m, float l) {
-      *(done.whole ? kp.lse + at : kp.lse_part + part_at) =
+      *(done.whole ? kp.lse + at : lse_part + part_at) =
           (m * c2 + lg2f_approx(l)) * 0.69314718055994530942f;
     };
     // all softmax threads meet (an mbarrier, whose wait ends when another warp gave up)
@@ -397,7 +436,7 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
       const int row0 = (done.y - hk * kp.qtiles) * BM;        // of the head's G * N_q rows
       // rows of a key/value head are contiguous in [B, H, N_q]
       const size_t at0 = (static_cast<size_t>(done.b) * kp.H_kv + hk) * kp.rows + row0;
-      const size_t part0 = static_cast<size_t>(2 * blockIdx.x + (done.last ? 1 : 0)) * kp.seg_rows;
+      const size_t part0 = CLUSTER ? 0 : static_cast<size_t>(2 * blockIdx.x + (done.last ? 1 : 0)) * kp.seg_rows;
       if constexpr (FEW) {
         // weights of the four outputs of row `lane`: exp(m_w - m) / sum_w exp(m_w - m) l_w
         if (lane < 16) stat[warp][lane] = make_float2(done.m, done.l);
@@ -432,7 +471,7 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
                 const uint32_t pk = FP16 ? cvt_pack_f16(sum, 0.f) : cvt_pack_bf16(sum, 0.f);
                 static_cast<uint16_t*>(kp.o)[(at0 + x) * D + c0 * 64 + i] = static_cast<uint16_t>(pk);
               } else {
-                kp.o_part[(part0 + x) * D + c0 * 64 + i] = sum;
+                o_part[(part0 + x) * D + c0 * 64 + i] = sum;
               }
             }
           }
@@ -457,7 +496,7 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
             for (int v = 0; v < 4; ++v)
               dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
           } else if (row_ok) {
-            float4* dst = reinterpret_cast<float4*>(kp.o_part + (part0 + r) * D + c0 * 32);
+            float4* dst = reinterpret_cast<float4*>(o_part + (part0 + r) * D + c0 * 32);
 #pragma unroll
             for (int v = 0; v < 8; ++v)
               dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
@@ -586,14 +625,17 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
         }
       }
       if (!ok) break;
-      done = Done{part, cur.b, cur.y, take == cur.tiles(), part > 0, m_ref, l};
+      done = Done{part, cur.b, cur.y, !CLUSTER && take == cur.tiles(), part > 0, m_ref, l};
       cur.next_part(take);
       ++part;
     }
     if (ok && part > 0) write_out();
-    // batch entries without keys: O = 0 and LSE = -inf
+    if constexpr (CLUSTER) {
+      if (total == 0) lse_sh[r] = -INFINITY;
+    }
+    // batch entries without keys: O = 0 and LSE = -inf (a cluster's merge finds them)
     const size_t rows_b = static_cast<size_t>(kp.H_kv) * kp.rows;
-    for (int b = blockIdx.x; b < kp.B; b += gridDim.x) {
+    for (int b = blockIdx.x; !CLUSTER && b < kp.B; b += gridDim.x) {
       if (pre[b + 1] != pre[b]) continue;
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kp.o) + b * rows_b * D);
       for (size_t i = r; i < rows_b * (D / 8); i += 128) dst[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -625,6 +667,39 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
   if (warp == C::MMA_S_WARP) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
+  }
+  if constexpr (CLUSTER) {
+    // every thread of every CTA comes here, after an abort too.  The cluster's threads
+    // share the segment's rows, four columns each.
+    cluster_sync();
+    const int y = seg % kp.segs, hk = y / kp.qtiles, row0 = (y - hk * kp.qtiles) * BM;
+    const size_t at0 = (static_cast<size_t>(my_b) * kp.H_kv + hk) * kp.rows + row0;
+    const int items = min(BM, kp.rows - row0) * (D / 4);
+    for (int x = rank * C::THREADS + threadIdx.x; x < items; x += ranks * C::THREADS) {
+      const int r = x / (D / 4), c4 = x % (D / 4);
+      float lse[8], m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lse[i] = i < ranks ? ld_cluster_f32(smem_u32(lse_sh + r), i) : -INFINITY;
+        m = fmaxf(m, lse[i]);
+      }
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (lse[i] == -INFINITY) continue;           // no keys: nothing was written there
+        const float w = expf(lse[i] - m);
+        const float4 o = ld_cluster_v4(smem_u32(reinterpret_cast<float*>(sKV) + r * D + 4 * c4), i);
+        sum += w;
+        acc = make_float4(fmaf(w, o.x, acc.x), fmaf(w, o.y, acc.y), fmaf(w, o.z, acc.z), fmaf(w, o.w, acc.w));
+      }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const uint2 pk = FP16 ? make_uint2(cvt_pack_f16(acc.x * inv, acc.y * inv), cvt_pack_f16(acc.z * inv, acc.w * inv))
+                            : make_uint2(cvt_pack_bf16(acc.x * inv, acc.y * inv), cvt_pack_bf16(acc.z * inv, acc.w * inv));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(kp.o) + (at0 + r) * D + 4 * c4) = pk;
+      if (c4 == 0) kp.lse[at0 + r] = m + logf(sum);   // -inf without keys
+    }
+    cluster_sync();                                  // the others may still be reading here
   }
 }
 
@@ -715,7 +790,7 @@ template <int D, bool FP16, bool FEW>
 attn_status_t launch_cross_rows_t(const FwdParams& p, const CrossPlan& plan, void* workspace,
                                   cudaStream_t stream) {
   using C = CrossCfg<D, FEW>;
-  auto kern = cross_rows_kernel<D, FP16, FEW>;
+  auto kern = plan.cluster ? cross_rows_kernel<D, FP16, FEW, true> : cross_rows_kernel<D, FP16, FEW, false>;
   attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), C::SMEM);
   if (s != ATTN_OK) return s;
   CUtensorMap tq, tk, tv;
@@ -739,8 +814,13 @@ attn_status_t launch_cross_rows_t(const FwdParams& p, const CrossPlan& plan, voi
                   reinterpret_cast<float*>(ws + align_up(part_rows * D * sizeof(float), 256)), status,
                   p.B, p.H_kv, p.N_k, rows, p.H_kv * plan.qtiles, plan.qtiles, seg_rows,
                   p.scale * 1.4426950408889634f};
+  cudaError_t e;
+  if (plan.cluster) {
+    e = launch_cluster(kern, plan.ctas, plan.cluster, C::THREADS, C::SMEM, stream, tq, tk, tv, kp);
+    return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "cross attention rows kernel launch");
+  }
   kern<<<plan.ctas, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, kp);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "cross attention rows kernel launch");
   e = launch_dependent(cross_merge_kernel<D, FP16>, dim3(kp.segs, (seg_rows + kMergeRows<D> - 1) / kMergeRows<D>, p.B),
                        kMergeThreads, 0, stream, kp, plan.ctas);

@@ -12,7 +12,8 @@
 //    an even share.  One CTA per segment, as in the self-attention pass, would
 //    leave a short encoder or few key/value heads on a handful of SMs, and the key
 //    tiles of two long ones in a last, half-empty wave (B = 2, H = 16, H_kv = 4, N_q =
-//    8192, N_k = 4096 and 3072, d = 128: 1003 us).
+//    8192, N_k = 4096 with a quarter of the second entry's keys unseen, d = 128: 1003 us
+//    so, 803 shared).
 //  * Step n of a segment that starts when its CTA has done t steps is query step (t + n)
 //    mod the segment's steps: CTAs on the same heads read the same Q and dO tiles at
 //    about the same time, from L2.  (In each segment's own order they read them

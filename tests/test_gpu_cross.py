@@ -131,6 +131,15 @@ def test_key_lengths(attn, d, N_q):
     _check(attn, 8, 2, 1, N_q, 300, d, lens=[0, 1, 127, 128, 129, 256, 299, 300], seed=920)
 
 
+@pytest.mark.parametrize("H_kv,N_k", [(4, 700), (7, 4096), (8, 1500), (10, 2500), (4, 500), (23, 1500),
+                                      (30, 1500), (50, 800), (4, 8192)])
+@pytest.mark.parametrize("N_q", [1, 40])
+def test_segments_and_their_keys(attn, H_kv, N_k, N_q):
+    """Few to many segments of few to many tiles: a cluster of each size per segment, and none."""
+    _check(attn, 2, H_kv, H_kv, N_q, N_k, 64, lens=[N_k - 1, 130], seed=925, backward=False)
+    _check(attn, 2, H_kv, H_kv, N_q, N_k, 64, "fp16", lens=[0, N_k], seed=926, backward=False)
+
+
 def test_key_lengths_fp16_all_empty(attn):
     _check(attn, 2, 2, 2, 5, 130, 64, "fp16", lens=[0, 0], seed=930)
     _check(attn, 2, 2, 2, 200, 130, 128, "fp16", lens=[0, 77], seed=931)
@@ -292,8 +301,8 @@ def test_host_tensors(attn):
 
 
 def test_self_attention_is_the_same_arithmetic(attn):
-    """N_q = N_k without lengths: the plain forward's bits."""
-    q, k, v, do = (t.to(dev()) for t in _inputs(997, 2, 4, 4, 700, 700, 128, "bf16"))
+    """N_q = N_k without lengths, in a shape that the forward kernel takes: the plain forward's bits."""
+    q, k, v, do = (t.to(dev()) for t in _inputs(997, 2, 16, 16, 700, 700, 128, "bf16"))
     o, lse = attn.attn_cross_fwd(q, k, v)
     ref = attn.attn_fwd(q, k, v)
     assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
