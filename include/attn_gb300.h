@@ -744,7 +744,9 @@ attn_status_t attn_cache_append(const void* q, void* q_out, const void* k, const
  * Requests that do not fit (offsets, lengths, pages out of range) are skipped and
  * reported by attn_get_device_status() as ATTN_ERR_INVALID_ARG; keys at or past
  * max_pos are stored unrotated and reported.
- * d = 128; page_size a power of two in [16, 65536]; total = cu_seqlens[B], may be 0.
+ * total >= cu_seqlens[B]: rows behind the last request are padding, not stored (their
+ * query rows are copied).  total may be 0.
+ * d = 128; page_size a power of two in [16, 65536].
  * Source: as attn_decode_paged_fp8, whose cache this fills, with the block scaling
  * of attn_fp8_quantize.
  */

@@ -283,6 +283,24 @@ def test_append_fp8_zero_rows_and_bad_requests(attn):
     check_status(attn)
 
 
+@pytest.mark.parametrize("new", [[1, 0, 1], [40, 0, 9]])
+def test_append_fp8_rows_behind_the_last_request(attn, new):
+    """Padding behind cu_seqlens[B] (NaN): nothing of it is stored, its query rows are copied."""
+    H, H_kv, d, page, pad = 4, 2, 128, 16, 7
+    bt, (lens, cu, _, _, _), num, q, k, v = _step(attn, 12, [0, 5, 15], new, page, H, H_kv, d, torch.bfloat16)
+    cos, sin = _rope(64, d)
+    caches = []
+    for rows in (0, pad):
+        more = lambda t: torch.cat([t, torch.full((rows, *t.shape[1:]), float("nan"), device=dev(), dtype=t.dtype)])
+        kc, vc = (torch.full((num, page, H_kv, d), 0x33, dtype=torch.uint8, device=dev()) for _ in range(2))
+        ks, vs = (torch.full((num, H_kv), 0.5, device=dev()) for _ in range(2))
+        qo = attn.attn_cache_append_fp8(more(k), more(v), kc, vc, ks, vs, bt, lens, cu, cos, sin, _signs(), q=more(q))
+        check_status(attn)
+        assert qo.shape[0] == sum(new) + rows and qo[sum(new):].isnan().all()
+        caches.append((kc, vc, ks, vs, qo[:sum(new)]))
+    assert all(torch.equal(a, b) for a, b in zip(*caches))
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_decoder_layer_steps(attn, fp8):
     """A prompt and decode steps of an encoder-decoder layer: tables, append with
