@@ -185,9 +185,6 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
 
-  // the merging kernel may start its prologue (it waits for this grid's end)
-  if constexpr (!CLUSTER) release_dependents();
-
   // ---- prologue: tiles of a segment of the batch entries before each, while the
   // barriers are set up, tensor memory is allocated and the tensor maps arrive
   const int ranks = CLUSTER ? static_cast<int>(cluster_size()) : 1;
@@ -196,7 +193,6 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
   const int my_b = CLUSTER ? seg / kp.segs : 0;
   const int per = CLUSTER ? 0 : (kp.B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, kp.B), b1 = min(b0 + per, kp.B);
-  const int first_len = kp.kv_lens && b0 < b1 ? __ldg(kp.kv_lens + b0) : kp.Nk;
   if (warp == C::MMA_S_WARP) {
     tmem_alloc(&tmem_base_sh, 512);
     tmem_relinquish();
@@ -224,9 +220,14 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
     issued_sh[0] = issued_sh[1] = parts_sh = 0;
     fence_mbar_init();
   }
+  // This launch may have overtaken the end of the stream's previous kernel: from here on
+  // that is over, and the next one may come up behind this one in the same way.  The
+  // merging kernel reads kv_lens at once, so it is released no earlier.
+  wait_for_previous_kernel();
+  release_dependents();
   if constexpr (CLUSTER) {
     if (threadIdx.x == 32) {
-      int n = kp.kv_lens ? __ldg(kp.kv_lens + my_b) : kp.Nk;
+      int n = kp.kv_lens ? ld_l2_s32(kp.kv_lens + my_b) : kp.Nk;
       if (n < 0 || n > kp.Nk) {
         if (seg % kp.segs == 0 && rank == 0) atomicCAS(kp.status, 0, kDevBadSeqlens);
         n = 0;
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
   } else {
     int sum = 0;
     for (int b = b0; b < b1; ++b) {
-      int n = b == b0 ? first_len : kp.kv_lens ? __ldg(kp.kv_lens + b) : kp.Nk;
+      int n = kp.kv_lens ? ld_l2_s32(kp.kv_lens + b) : kp.Nk;
       if (n < 0 || n > kp.Nk) {
         if (blockIdx.x == 0) atomicCAS(kp.status, 0, kDevBadSeqlens);
         n = 0;
@@ -715,6 +716,7 @@ template <int D, bool FP16>
 __global__ void __launch_bounds__(kMergeThreads)
     cross_merge_kernel(const CrossKParams kp, int C) {
   __shared__ int sums[2][4];
+  release_dependents();
   const int b = blockIdx.z, y = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // tiles of a segment of the entries before b, and of all
@@ -816,14 +818,13 @@ attn_status_t launch_cross_rows_t(const FwdParams& p, const CrossPlan& plan, voi
                   p.scale * 1.4426950408889634f};
   cudaError_t e;
   if (plan.cluster) {
-    e = launch_cluster(kern, plan.ctas, plan.cluster, C::THREADS, C::SMEM, stream, tq, tk, tv, kp);
+    e = launch_dependent(kern, dim3(plan.ctas), C::THREADS, C::SMEM, stream, plan.cluster, tq, tk, tv, kp);
     return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "cross attention rows kernel launch");
   }
-  kern<<<plan.ctas, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, kp);
-  e = cudaGetLastError();
+  e = launch_dependent(kern, dim3(plan.ctas), C::THREADS, C::SMEM, stream, 0, tq, tk, tv, kp);
   if (e != cudaSuccess) return fail_cuda(e, "cross attention rows kernel launch");
   e = launch_dependent(cross_merge_kernel<D, FP16>, dim3(kp.segs, (seg_rows + kMergeRows<D> - 1) / kMergeRows<D>, p.B),
-                       kMergeThreads, 0, stream, kp, plan.ctas);
+                       kMergeThreads, 0, stream, 0, kp, plan.ctas);
   if (e != cudaSuccess) return fail_cuda(e, "cross attention merge kernel launch");
   return ATTN_OK;
 }

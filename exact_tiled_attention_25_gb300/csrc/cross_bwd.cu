@@ -767,7 +767,7 @@ attn_status_t launch_cross_bwd_t(const BwdParams& p, float* part, int ctas, cuda
     if ((s = make_tmap_3d(&tk, p.k, 2, D, p.N_k, pkv, 64, 128)) != ATTN_OK) return s;
     if ((s = make_tmap_3d(&tv, p.v, 2, D, p.N_k, pkv, 64, 128)) != ATTN_OK) return s;
     if ((s = make_tmap_3d(&tdq, p.dq_acc, 4, D, p.N, pq, 32, 32)) != ATTN_OK) return s;
-    e = launch_dependent(kern, dim3(ctas), C::THREADS, C::SMEM_BYTES, stream, tq, tk, tv, tdo, tdq, kp);
+    e = launch_dependent(kern, dim3(ctas), C::THREADS, C::SMEM_BYTES, stream, 0, tq, tk, tv, tdo, tdq, kp);
     if (e != cudaSuccess) return fail_cuda(e, "cross-attention backward main launch");
   }
   // 3. join dK and dV, convert dQ
@@ -776,7 +776,7 @@ attn_status_t launch_cross_bwd_t(const BwdParams& p, float* part, int ctas, cuda
   const long long n8 = static_cast<long long>(p.B) * p.H * p.N * D / 8;
   const long long want = (n8 + 255) / 256;
   const long long convert = want < 152 * 16 ? want : 152 * 16;
-  e = launch_dependent(cross_bwd_join_kernel<D, FP16>, dim3(static_cast<unsigned>(join + convert)), 256, 0, stream,
+  e = launch_dependent(cross_bwd_join_kernel<D, FP16>, dim3(static_cast<unsigned>(join + convert)), 256, 0, stream, 0,
                        kp, ctas, ktiles, static_cast<unsigned>(join), p.dq_acc, static_cast<uint16_t*>(p.dq), n8);
   if (e != cudaSuccess) return fail_cuda(e, "cross-attention backward join launch");
   return ATTN_OK;

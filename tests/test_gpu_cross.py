@@ -285,6 +285,62 @@ def test_graph_replay_stream_and_repeat(attn, N_q):
     check_status(attn)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("B,H_kv,N_k", [(1, 16, 1500), (24, 8, 700), (2, 2, 20000)])
+def test_inputs_written_by_the_kernel_before(attn, B, H_kv, N_k, captured):
+    """Few-rows calls (a cluster per segment, shared tiles) start before the stream's previous
+    kernel has ended.  Inputs, the lengths too, written right before each call, its output read
+    and they overwritten right behind it, in a graph also from another stream and after a memset:
+    the bits of calls with pauses between."""
+    sets, want = [], []
+    for i in range(3):
+        q, k, v, _ = (t.to(dev()) for t in _inputs(1010 + 2 * i, B, H_kv, H_kv, 1, N_k, 64, "bf16"))
+        lens = torch.tensor([(N_k - 37 * (b + 5 * i)) % (N_k + 1) for b in range(B)], dtype=torch.int32, device=dev())
+        sets.append((q, k, v, lens))
+        torch.cuda.synchronize()
+        want.append(attn.attn_cross_fwd(q, k, v, lens))
+        torch.cuda.synchronize()
+    check_status(attn)
+    now = [torch.zeros_like(t) for t in sets[0]]
+    outs = [torch.zeros_like(t).expand(9, *t.shape).contiguous() for t in want[0]]
+    need = attn.attn_cross_workspace_size(B, H_kv, H_kv, 1, N_k, 64)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev())
+    o, lse = (torch.empty_like(t) for t in want[0])
+
+    def run(side=None):
+        here = torch.cuda.current_stream()
+        for i in range(9):
+            for to, source in zip(now, sets[i % 3]):
+                if side is None:
+                    torch.mul(source, 1, out=to)
+                    continue
+                side.wait_stream(here)               # the next input from the other stream
+                with torch.cuda.stream(side):
+                    torch.mul(source, 1, out=to)
+            if side is not None:
+                ws.zero_()
+                here.wait_stream(side)               # the call has to wait for both
+            attn.attn_cross_fwd(*now, o=o, lse=lse, workspace=ws)
+            for to, source in zip(outs, (o, lse)):
+                torch.mul(source, 1, out=to[i])
+
+    if captured:
+        stream, side = torch.cuda.Stream(), torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            run(side)
+        for _ in range(3):
+            graph.replay()
+    else:
+        run()
+    torch.cuda.synchronize()
+    check_status(attn)
+    for i in range(9):
+        for got, ref in zip(outs, want[i % 3]):
+            assert torch.equal(got[i], ref), i
+
+
 def test_host_tensors(attn):
     q, k, v, do = _inputs(995, 1, 2, 1, 20, 30, 64, "bf16")
     lens = torch.tensor([25], dtype=torch.int32)
