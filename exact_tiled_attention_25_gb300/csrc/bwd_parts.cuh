@@ -84,15 +84,19 @@ __device__ __forceinline__ bool packed_seq(const int* cu, int b, int total, int 
 // One group of D/8 lanes per row; each lane holds 8 consecutive elements.
 // Rows of O, dO and dQ are [B, H, N, d] or, for a packed batch (PACKED),
 // [total, H, d] with LSE [H, total].
-// RELEASE: the main kernel may start its prologue while this one runs.
-template <int D, bool FP16, bool PACKED, bool RELEASE = false>
+// CHAINED: a dependent launch, so O, dO and the LSE, which the kernel before may have
+// written, are read past the L1 cache; the main kernel may start its prologue meanwhile.
+template <int D, bool FP16, bool PACKED, bool CHAINED = false>
 __global__ void __launch_bounds__(256)
     bwd_prep_kernel(const uint16_t* __restrict__ o, const uint16_t* __restrict__ dout,
                     const float* __restrict__ lse, float* __restrict__ lse2,
                     float* __restrict__ delta, float* __restrict__ dq_acc, int N, int Npad,
                     long long total_rows_pad, int H, const int* __restrict__ cu_seqlens,
                     int total) {
-  if constexpr (RELEASE) release_dependents();
+  if constexpr (CHAINED) {
+    wait_for_previous_kernel();
+    release_dependents();
+  }
   constexpr int L = D / 8;
   constexpr int ROWS_PER_WARP = 32 / L;
   const int lane = threadIdx.x & 31;
@@ -117,8 +121,10 @@ __global__ void __launch_bounds__(256)
   }
   float acc = 0.f;
   if (n < len) {
-    const uint4 a = reinterpret_cast<const uint4*>(o + row * D)[li];
-    const uint4 b = reinterpret_cast<const uint4*>(dout + row * D)[li];
+    const uint4* const ao = reinterpret_cast<const uint4*>(o + row * D) + li;
+    const uint4* const bo = reinterpret_cast<const uint4*>(dout + row * D) + li;
+    const uint4 a = CHAINED ? __ldcg(ao) : *ao;
+    const uint4 b = CHAINED ? __ldcg(bo) : *bo;
     const uint32_t av[4] = {a.x, a.y, a.z, a.w};
     const uint32_t bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -143,7 +149,7 @@ __global__ void __launch_bounds__(256)
   if (li == 0) {
     // stored negated so the main kernel adds them with packed f32x2 FMAs
     delta[prow] = (n < len) ? -acc : 0.f;
-    lse2[prow] = (n < len) ? -lse[lrow] * kLog2e : -INFINITY;
+    lse2[prow] = (n < len) ? -(CHAINED ? __ldcg(lse + lrow) : lse[lrow]) * kLog2e : -INFINITY;
   }
 }
 

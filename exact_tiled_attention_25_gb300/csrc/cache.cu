@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kF8MaxThreads, 2)
   const unsigned before_q = static_cast<unsigned>(static_cast<unsigned long long>(blockIdx.x) * q_blocks / gridDim.x);
   const unsigned with_q = static_cast<unsigned>((blockIdx.x + 1ull) * q_blocks / gridDim.x);
   if (with_q > before_q) {
-    rope_block<FP16, MODE == kNeighbours, 2, STAGED ? 7 : 0>(q, before_q % q_columns, before_q / q_columns, stage);
+    rope_block<FP16, MODE == kNeighbours, false, 2, STAGED ? 7 : 0>(q, before_q % q_columns, before_q / q_columns, stage);
     return;
   }
   const unsigned at_site = blockIdx.x - before_q;
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kF8Threads)
   __shared__ __align__(16) float signs[128];
   if (blockIdx.x >= site_blocks) {
     const unsigned at = blockIdx.x - site_blocks;
-    rope_block<FP16, MODE == kNeighbours>(q, at % q_columns, at / q_columns);
+    rope_block<FP16, MODE == kNeighbours, false>(q, at % q_columns, at / q_columns);
     return;
   }
   const int u = threadIdx.x & 7;

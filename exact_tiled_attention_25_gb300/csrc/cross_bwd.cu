@@ -745,10 +745,9 @@ attn_status_t launch_cross_bwd_t(const BwdParams& p, float* part, int ctas, cuda
   {
     constexpr int rows_per_block = 8 * (32 / (D / 8));
     const long long blocks = (rows_pad + rows_per_block - 1) / rows_per_block;
-    bwd_prep_kernel<D, FP16, false, true><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-        static_cast<const uint16_t*>(p.o), static_cast<const uint16_t*>(p.dout), p.lse, p.lse2,
-        p.delta, p.dq_acc, p.N, Npad, rows_pad, p.H, nullptr, 0);
-    e = cudaGetLastError();
+    e = launch_dependent(bwd_prep_kernel<D, FP16, false, true>, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, 0,
+                         static_cast<const uint16_t*>(p.o), static_cast<const uint16_t*>(p.dout), p.lse, p.lse2,
+                         p.delta, p.dq_acc, p.N, Npad, rows_pad, p.H, nullptr, 0);
     if (e != cudaSuccess) return fail_cuda(e, "cross-attention backward prep launch");
   }
   int* status = device_status_word();

@@ -176,9 +176,10 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ_>::THREADS, 1)
   int Nkv = N;                             // keys this batch entry sees
   if constexpr (CROSS) {
     static_assert(!CAUSAL && !PACKED, "cross attention is neither causal nor packed");
+    wait_for_previous_kernel();            // a dependent launch: its start overlaps that one's end
     Nkv = kp.Nk;
     if (kp.kv_lens) {
-      const int n = kp.kv_lens[blockIdx.z];
+      const int n = ld_l2_s32(kp.kv_lens + blockIdx.z);
       const bool bad = n < 0 || n > kp.Nk;
       if (bad && threadIdx.x == 0) atomicCAS(kp.status, 0, kDevBadSeqlens);
       Nkv = bad ? 0 : n;
@@ -641,8 +642,7 @@ attn_status_t launch_cross_t(const FwdParams& p, cudaStream_t stream) {
   FwdKParams kp{p.o, p.lse, status, nullptr, p.N, 0, p.H, p.H / p.H_kv, p.scale * 1.4426950408889634f,
                 p.N_k, p.kv_lens};
   const dim3 grid((p.N + BM * C::NQ - 1) / (BM * C::NQ), p.H, p.B);
-  kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(tq, tk, tv, kp);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(kern, grid, C::THREADS, C::SMEM_BYTES, stream, 0, tq, tk, tv, kp);
   if (e != cudaSuccess) return fail_cuda(e, "cross attention kernel launch");
   return ATTN_OK;
 }

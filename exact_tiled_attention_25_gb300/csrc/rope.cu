@@ -17,7 +17,8 @@ constexpr double kTwoPi = 6.283185307179586476925;
 
 template <bool FP16, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeKParams p) {
-  rope_block<FP16, INTERLEAVED>(p, blockIdx.x, blockIdx.y);
+  wait_for_previous_kernel();      // a dependent launch: its start overlaps that one's end
+  rope_block<FP16, INTERLEAVED, true>(p, blockIdx.x, blockIdx.y);
 }
 
 // Table row r holds position p = first + r.  Frequency theta_i = base^(-2i/rot)
@@ -40,7 +41,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeKParams p)
 // own angle, the seven behind it the sum formulas with those of 1 .. 7 row steps,
 // computed once per thread: one composition, so at most 2^-23 of error on top.
 // Bound: the writes, 8 bytes per entry.  131072 x 64 entries: 238 us with float64
-// angles, 17.4 us with a sine and cosine per entry, 12.7 us so (5.3 TB/s).
+// angles, 17.4 us with a sine and cosine per entry, 12.2 us so (5.5 TB/s).
 struct RopeTurns {
   unsigned long long f[128];
 };
@@ -62,7 +63,10 @@ __global__ void __launch_bounds__(256)
   const int lanes = 256 / half;                     // rows written at a time
   const int i = static_cast<int>(threadIdx.x) % half;
   const int sub = static_cast<int>(threadIdx.x) / half;
-  if (sub >= lanes) return;
+  if (sub >= lanes) {
+    wait_for_previous_kernel();
+    return;
+  }
   const unsigned long long f = turns.f[i];
   const long long r0 = static_cast<long long>(blockIdx.x) * rows_per_block;
   const long long r1 = r0 + rows_per_block < n ? r0 + rows_per_block : n;
@@ -71,6 +75,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int k = 1; k < kRun; ++k) by[k] = cos_sin_turns(step * k);
   unsigned long long angle = f * (static_cast<unsigned long long>(first) + r0 + sub);
+  wait_for_previous_kernel();      // a dependent launch: it may still be reading the tables' memory
   for (long long r = r0 + sub; r < r1; r += kRun * lanes, angle += step * kRun) {
     float2 b = cos_sin_turns(angle);
     b = make_float2(b.x * attn_factor, b.y * attn_factor);
@@ -96,14 +101,9 @@ attn_status_t launch_rope(RopeKParams p, int fp16, int interleaved, cudaStream_t
   if (g.columns > 2147483647LL || g.chunks > 65535)
     return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
   const dim3 grid(static_cast<unsigned>(g.columns), g.chunks);
-  if (fp16) {
-    if (interleaved) rope_kernel<true, true><<<grid, kRopeThreads, 0, stream>>>(p);
-    else rope_kernel<true, false><<<grid, kRopeThreads, 0, stream>>>(p);
-  } else {
-    if (interleaved) rope_kernel<false, true><<<grid, kRopeThreads, 0, stream>>>(p);
-    else rope_kernel<false, false><<<grid, kRopeThreads, 0, stream>>>(p);
-  }
-  const cudaError_t e = cudaGetLastError();
+  auto kern = fp16 ? interleaved ? rope_kernel<true, true> : rope_kernel<true, false>
+                   : interleaved ? rope_kernel<false, true> : rope_kernel<false, false>;
+  const cudaError_t e = launch_dependent(kern, grid, kRopeThreads, 0, stream, 0, p);
   if (e != cudaSuccess) return fail_cuda(e, "rotary kernel launch");
   return ATTN_OK;
 }
@@ -128,10 +128,9 @@ attn_status_t launch_rope_table(float* cos_out, float* sin_out, long long n, int
   long long rows = (n + 152 * 4 - 1) / (152 * 4);
   rows = rows < 8 ? 8 : rows;
   const long long blocks = (n + rows - 1) / rows;
-  rope_table_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-      cos_out, sin_out, n, half, turns, static_cast<float>(attn_factor), static_cast<unsigned>(first),
-      static_cast<int>(rows));
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(rope_table_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, 0,
+                                         cos_out, sin_out, n, half, turns, static_cast<float>(attn_factor),
+                                         static_cast<unsigned>(first), static_cast<int>(rows));
   if (e != cudaSuccess) return fail_cuda(e, "rotary table launch");
   return ATTN_OK;
 }

@@ -84,11 +84,18 @@ __device__ __forceinline__ void rotate16(uint4& a, uint4& b, const uint64_t (&cc
   }
 }
 
+// A load; of a dependent launch (DEPENDENT), which may have started before its inputs were
+// written, past the L1 cache.
+template <bool DEPENDENT, typename T>
+__device__ __forceinline__ T load_input(const T* p) {
+  return DEPENDENT ? __ldcg(p) : *p;
+}
+
 // Work of one block: tokens of block column `bx`, heads of chunk `chunk`, kHeads of
 // them at a time.  SLOTS > 0: rows of the first tensor (no other is given) come through
 // shared memory, SLOTS heads in flight, every thread its own 32 bytes of each; for
 // kernels that cannot give the loads registers (stage: SLOTS * 2 * blockDim words).
-template <bool FP16, bool INTERLEAVED, int kHeads = 4, int SLOTS = 0>
+template <bool FP16, bool INTERLEAVED, bool DEPENDENT, int kHeads = 4, int SLOTS = 0>
 __device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, int chunk, uint4* stage = nullptr) {
   const int units = p.d / 16;                       // 4, 8 or 16: divides the block
   const int tokens = static_cast<int>(blockDim.x) / units;
@@ -101,7 +108,7 @@ __device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, i
   if (p.rotated > 0) {
     int pos = static_cast<int>(n);
     if (p.positions) {
-      pos = p.positions[tk];
+      pos = load_input<DEPENDENT>(p.positions + tk);
     } else if (p.cu_seqlens) {
       int lo = 0, hi = p.requests;
       while (hi - lo > 1) {
@@ -121,8 +128,8 @@ __device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, i
       const size_t at = static_cast<size_t>(pos) * (p.rot / 2) + 8 * u;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float4 cv = __ldg(reinterpret_cast<const float4*>(p.cos + at) + i);
-        const float4 sv = __ldg(reinterpret_cast<const float4*>(p.sin + at) + i);
+        const float4 cv = load_input<DEPENDENT>(reinterpret_cast<const float4*>(p.cos + at) + i);
+        const float4 sv = load_input<DEPENDENT>(reinterpret_cast<const float4*>(p.sin + at) + i);
         c[4 * i] = cv.x, c[4 * i + 1] = cv.y, c[4 * i + 2] = cv.z, c[4 * i + 3] = cv.w;
         s[4 * i] = sv.x, s[4 * i + 1] = sv.y, s[4 * i + 2] = sv.z, s[4 * i + 3] = sv.w;
       }
@@ -134,7 +141,7 @@ __device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, i
   }
   long long slot = 0;
   if (p.slots) {
-    slot = p.slots[n];
+    slot = load_input<DEPENDENT>(p.slots + n);
     if (slot >= p.num_slots || slot < -1) {
       if (u == 0 && chunk == 0) atomicCAS(p.status, 0, kDevBadTables);
       slot = -1;
@@ -193,8 +200,8 @@ __device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, i
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) {
           if (h + i >= h1) break;
-          va[i] = *reinterpret_cast<const uint4*>(in + i * step_in + off_a);
-          vb[i] = *reinterpret_cast<const uint4*>(in + i * step_in + off_b);
+          va[i] = load_input<DEPENDENT>(reinterpret_cast<const uint4*>(in + i * step_in + off_a));
+          vb[i] = load_input<DEPENDENT>(reinterpret_cast<const uint4*>(in + i * step_in + off_b));
         }
         in += kHeads * step_in;
 #pragma unroll

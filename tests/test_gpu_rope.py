@@ -182,3 +182,48 @@ def test_explicit_stream(attn):
         side.synchronize()
         assert torch.equal(got, want)
     check_status(attn)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_rows_and_tables_written_by_the_kernel_before(attn, captured):
+    """The kernels start before the stream's previous one has ended: tables, positions and rows
+    of other contents in the same memory right before each call, in place and not, give the
+    bits of calls with pauses between."""
+    B, H, N, d = 2, 6, 700, 128
+    sets, want = [], []
+    for i in range(3):
+        q, k = (torch.from_numpy(workloads.normal(60 + 2 * i + j, (B, H, N, d))).to(dev(), torch.bfloat16) for j in range(2))
+        pos = torch.randint(0, 900, (B, N), dtype=torch.int32, device=dev(), generator=torch.Generator(dev()).manual_seed(i))
+        cos, sin = attn.attn_rope_table(900, d, base=10000.0 + i, first=7 * i)
+        torch.cuda.synchronize()
+        sets.append((q, k, pos))
+        want.append((*attn.attn_rope(q, k, cos, sin, pos), cos, sin))
+        torch.cuda.synchronize()
+    q, k, pos = now = [torch.zeros_like(t) for t in sets[0]]
+    cos, sin = (torch.zeros(900, d // 2, device=dev()) for _ in range(2))
+    outs = [t.expand(6, *t.shape).contiguous() for t in want[0]]
+
+    def run():
+        for i in range(6):
+            for to, source in zip(now, sets[i % 3]):
+                torch.mul(source, 1, out=to)
+            attn.attn_rope_table(900, d, base=10000.0 + i % 3, first=7 * (i % 3), rope_cos=cos, rope_sin=sin)
+            attn.attn_rope(q, k, cos, sin, pos, q_out=q, k_out=k)
+            for to, source in zip(outs, (q, k, cos, sin)):
+                torch.mul(source, 1, out=to[i])
+            attn.attn_rope(q, k, cos, sin, pos, q_out=q, k_out=k, inverse=True)
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            run()
+        for _ in range(3):
+            graph.replay()
+    else:
+        run()
+    torch.cuda.synchronize()
+    check_status(attn)
+    for i in range(6):
+        for got, ref in zip(outs, want[i % 3]):
+            assert torch.equal(got[i], ref), i
