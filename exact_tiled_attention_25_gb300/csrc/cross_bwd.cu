@@ -13,7 +13,7 @@
 //    leave a short encoder or few key/value heads on a handful of SMs, and the key
 //    tiles of two long ones in a last, half-empty wave (B = 2, H = 16, H_kv = 4, N_q =
 //    8192, N_k = 4096 with a quarter of the second entry's keys unseen, d = 128: 1003 us
-//    so, 803 shared).
+//    so, 803 shared, both with the 16-bit P below).
 //  * Step n of a segment that starts when its CTA has done t steps is query step (t + n)
 //    mod the segment's steps: CTAs on the same heads read the same Q and dO tiles at
 //    about the same time, from L2.  (In each segment's own order they read them
@@ -26,10 +26,10 @@
 //    warps zero them in shared memory before a segment's first product: then S = dP =
 //    0 there, and P is set to 0 as for rows past the tensor.
 //
-// P is rounded to 16 bits once for both products that use it, as in bwd.cu: 64
-// float32 values more per thread do not fit the 96 registers that 18 warps leave.
-// dQ and dK then carry two roundings before their own (relative 0.0029 in bfloat16,
-// 0.0017 of it the output's).
+// P is rounded to 16 bits for dV = P^T dO; dS takes it in 24 (64 float32 values per
+// thread and the packed ones do not fit the 96 registers that 18 warps leave), so dQ and
+// dK carry the rounding of dS and their own: relative 0.0024 in bfloat16, 0.0017 of it
+// the output's.  With the 16-bit P for both, as in bwd.cu: 0.0029, and 1 to 2 % less time.
 #include <cmath>
 
 #include "bwd_parts.cuh"
@@ -424,35 +424,42 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         // phase A: P^T = exp2(S^T c - L log2 e), written back as 16-bit
         if (!(ok = mbar_wait(&bars.s_full, n & 1, ab, kDevTimeoutSoftmax))) break;
         tc_fence_after_sync();
-        uint32_t pb[32];                             // this half's P^T, packed pairs
+        // this half's P^T for dS, the upper 24 bits of each float, four in three words
+        uint32_t p24[48];
         const uint64_t cc = pack2(c2, c2);
+        auto probabilities = [&](int c, const uint32_t* sv) {     // queries [64 h + 16 c, +16)
+          const int qb = 64 * h + 16 * c;
+          uint32_t pb[8];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {                // queries [64 h + 32 x, +32): one load, one wait
-          uint32_t svv[32];
-          tmem_ld32(tmem + lane_addr + C::S_COL + 64 * h + 32 * x, svv);
-          tmem_ld_wait();
+          for (int e = 0; e < 16; e += 4) {
+            const float4 l4 = nlse4[(qb + e) / 4];
+            const uint64_t y0 = ffma2(pack2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), cc,
+                                      pack2(l4.x, l4.y));
+            const uint64_t y1 = ffma2(pack2(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), cc,
+                                      pack2(l4.z, l4.w));
+            float p[4] = {ex2_approx(lo2(y0)), ex2_approx(hi2(y0)), ex2_approx(lo2(y1)), ex2_approx(hi2(y1))};
 #pragma unroll
-          for (int c = 2 * x; c < 2 * x + 2; ++c) {  // queries [64 h + 16 c, +16)
-            const int qb = 64 * h + 16 * c;
-            const uint32_t* sv = svv + 16 * (c - 2 * x);
+            for (int u = 0; u < 4; ++u)
+              if (!key_ok) p[u] = 0.f;
+            pb[e / 2] = FP16 ? cvt_pack_f16(p[0], p[1]) : cvt_pack_bf16(p[0], p[1]);
+            pb[e / 2 + 1] = FP16 ? cvt_pack_f16(p[2], p[3]) : cvt_pack_bf16(p[2], p[3]);
+            uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 l4 = nlse4[(qb + e) / 4];
-              const uint64_t y0 = ffma2(pack2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), cc,
-                                        pack2(l4.x, l4.y));
-              const uint64_t y1 = ffma2(pack2(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), cc,
-                                        pack2(l4.z, l4.w));
-              float p[4] = {ex2_approx(lo2(y0)), ex2_approx(hi2(y0)), ex2_approx(lo2(y1)), ex2_approx(hi2(y1))};
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                if (!key_ok) p[u] = 0.f;
-              pb[(16 * c + e) / 2] = FP16 ? cvt_pack_f16(p[0], p[1]) : cvt_pack_bf16(p[0], p[1]);
-              pb[(16 * c + e) / 2 + 1] = FP16 ? cvt_pack_f16(p[2], p[3]) : cvt_pack_bf16(p[2], p[3]);
-            }
-            // packed P^T of queries [qb, qb + 16) -> columns [64 h + 8 c, +8)
-            tmem_st_x8(tmem + lane_addr + C::S_COL + 64 * h + 8 * c,
-                       *reinterpret_cast<const uint32_t(*)[8]>(&pb[8 * c]));
+            for (int u = 0; u < 4; ++u) w[u] = __float_as_uint(p[u]);
+            uint32_t* const at = p24 + (16 * c + e) / 4 * 3;
+            at[0] = __byte_perm(w[0], w[1], 0x5321);
+            at[1] = __byte_perm(w[1], w[2], 0x6532);
+            at[2] = __byte_perm(w[2], w[3], 0x7653);
           }
+          // packed P^T of queries [qb, qb + 16) -> columns [64 h + 8 c, +8)
+          tmem_st_x8(tmem + lane_addr + C::S_COL + 64 * h + 8 * c, pb);
+        };
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t sv[16];
+          tmem_ld16(tmem + lane_addr + C::S_COL + 64 * h + 16 * c, sv);
+          tmem_ld_wait();
+          probabilities(c, sv);
         }
         tmem_st_wait();
         tc_fence_before_sync();
@@ -461,50 +468,42 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         // dS^T buffer (for dQ)
         if (!(ok = mbar_wait(&bars.dp_full, n & 1, ab, kDevTimeoutSoftmax))) break;
         tc_fence_after_sync();
+        auto differences = [&](int c, const uint32_t* dpv) {      // queries [64 h + 16 c, +16)
+          const int qb = 64 * h + 16 * c;
+          uint32_t dd[8];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t dpvv[32];
-          tmem_ld32(tmem + lane_addr + C::DP_COL + 64 * h + 32 * x, dpvv);
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 2 * x; c < 2 * x + 2; ++c) {
-            const int qb = 64 * h + 16 * c;
-            const uint32_t* dpv = dpvv + 16 * (c - 2 * x);
-            uint32_t dd[8];
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 d4 = ndvec4[(qb + e) / 4];
-              // unpack here, not earlier: keeps packed registers live instead of floats
-              const uint32_t pw0 = opaque32(pb[(16 * c + e) / 2]);
-              const uint32_t pw1 = opaque32(pb[(16 * c + e) / 2 + 1]);
-              uint64_t pa, pc;
-              if (FP16) {
-                const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&pw0));
-                const float2 fc = __half22float2(*reinterpret_cast<const __half2*>(&pw1));
-                pa = pack2(fa.x, fa.y);
-                pc = pack2(fc.x, fc.y);
-              } else {
-                // a bf16 value is the upper half of the float32 with the same bits
-                pa = pack2(__uint_as_float(pw0 << 16), __uint_as_float(pw0 & 0xffff0000u));
-                pc = pack2(__uint_as_float(pw1 << 16), __uint_as_float(pw1 & 0xffff0000u));
-              }
-              const uint64_t dsa = fmul2(pa, fadd2(pack2(__uint_as_float(dpv[e]), __uint_as_float(dpv[e + 1])),
-                                                   pack2(d4.x, d4.y)));
-              const uint64_t dsc = fmul2(pc, fadd2(pack2(__uint_as_float(dpv[e + 2]), __uint_as_float(dpv[e + 3])),
-                                                   pack2(d4.z, d4.w)));
-              dd[e / 2] = FP16 ? cvt_pack_f16(lo2(dsa), hi2(dsa)) : cvt_pack_bf16(lo2(dsa), hi2(dsa));
-              dd[e / 2 + 1] = FP16 ? cvt_pack_f16(lo2(dsc), hi2(dsc)) : cvt_pack_bf16(lo2(dsc), hi2(dsc));
-            }
-            tmem_st_x8(tmem + lane_addr + C::DP_COL + 64 * h + 8 * c, dd);
-            // dS^T row k, queries [qb, qb + 16) = 16-byte pieces 2c and 2c + 1 of
-            // chunk h, placed with the 128-byte swizzle
-#pragma unroll
-            for (int pc = 0; pc < 2; ++pc) {
-              const uint32_t piece = static_cast<uint32_t>(2 * c + pc);
-              st_shared_v4(sDSrow + ((piece ^ (k & 7)) * 16), dd[4 * pc], dd[4 * pc + 1], dd[4 * pc + 2],
-                           dd[4 * pc + 3]);
-            }
+          for (int e = 0; e < 16; e += 4) {
+            const float4 d4 = ndvec4[(qb + e) / 4];
+            // widened here, not earlier: keeps packed registers live instead of floats.  What
+            // stands in the lowest byte is 2^-15 of the value at most.
+            const uint32_t* const at = p24 + (16 * c + e) / 4 * 3;
+            const uint32_t w0 = opaque32(at[0]), w1 = opaque32(at[1]), w2 = opaque32(at[2]);
+            const uint64_t pa = pack2(__uint_as_float(__byte_perm(w0, w0, 0x2100)),
+                                      __uint_as_float(__byte_perm(w0, w1, 0x5433)));
+            const uint64_t pc = pack2(__uint_as_float(__byte_perm(w1, w2, 0x4322)), __uint_as_float(w2));
+            const uint64_t dsa = fmul2(pa, fadd2(pack2(__uint_as_float(dpv[e]), __uint_as_float(dpv[e + 1])),
+                                                 pack2(d4.x, d4.y)));
+            const uint64_t dsc = fmul2(pc, fadd2(pack2(__uint_as_float(dpv[e + 2]), __uint_as_float(dpv[e + 3])),
+                                                 pack2(d4.z, d4.w)));
+            dd[e / 2] = FP16 ? cvt_pack_f16(lo2(dsa), hi2(dsa)) : cvt_pack_bf16(lo2(dsa), hi2(dsa));
+            dd[e / 2 + 1] = FP16 ? cvt_pack_f16(lo2(dsc), hi2(dsc)) : cvt_pack_bf16(lo2(dsc), hi2(dsc));
           }
+          tmem_st_x8(tmem + lane_addr + C::DP_COL + 64 * h + 8 * c, dd);
+          // dS^T row k, queries [qb, qb + 16) = 16-byte pieces 2c and 2c + 1 of
+          // chunk h, placed with the 128-byte swizzle
+#pragma unroll
+          for (int pc2 = 0; pc2 < 2; ++pc2) {
+            const uint32_t piece = static_cast<uint32_t>(2 * c + pc2);
+            st_shared_v4(sDSrow + ((piece ^ (k & 7)) * 16), dd[4 * pc2], dd[4 * pc2 + 1], dd[4 * pc2 + 2],
+                         dd[4 * pc2 + 3]);
+          }
+        };
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t dpv[16];
+          tmem_ld16(tmem + lane_addr + C::DP_COL + 64 * h + 16 * c, dpv);
+          tmem_ld_wait();
+          differences(c, dpv);
         }
         tmem_st_wait();
         fence_proxy_async_smem();

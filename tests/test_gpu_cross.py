@@ -5,8 +5,8 @@ Tolerances.  u = 2^-8 (bfloat16) or 2^-11 (float16) bounds one rounding.
  O     = sum_j P~_j v_j / l with each P~ rounded once, then rounded itself:
          |dO| <= u (sum_j p_j |v_j|) + u |O|.
  dV    = sum_i P~_i dO_i, rounded:   u sum_i p_i |dO_i| + u |dV|.
- dS~   = rnd(P~ (dP - D~)):          p |dP - D| 2u + p |dD|, and D~ takes the
-         rounded O:                  |dD_i| <= sum_c |dO_ic| |dO-tolerance_ic|.
+ dS~   = rnd(P^ (dP - D~)), P^ to 2^-15:  p |dP - D| (u + 2^-14) + p |dD|, and D~ takes
+         the rounded O:              |dD_i| <= sum_c |dO_ic| |dO-tolerance_ic|.
  dQ    = scale sum_j dS~_j k_j, rounded:  scale sum_j |d dS_j| |k_j| + u |dQ|; dK likewise.
 float16 probabilities and dS below 2^-14 are subnormal: each is off by at most
 2^-25 more (the probabilities before the division by l >= 1).  A tenth on top
@@ -54,7 +54,7 @@ def _backward_bounds(q, k, v, do, o, o_tol, grads, scale, lens, dtype):
             p, _, _ = oracle.attention_probs(q[b, h], k[b, j, :n], scale)
             dp = do[b, h] @ v[b, j, :n].T
             gap = np.abs(dp - (do[b, h] * o[b, h]).sum(1, keepdims=True))
-            eds = 2 * u * p * gap + p * (np.abs(do[b, h]) * o_tol[b, h]).sum(1, keepdims=True) + sub * (1 + gap)
+            eds = (u + 2.0 ** -14) * p * gap + p * (np.abs(do[b, h]) * o_tol[b, h]).sum(1, keepdims=True) + sub * (1 + gap)
             tq[b, h] = scale * eds @ np.abs(k[b, j, :n])
             tk[b, j, :n] += scale * eds.T @ np.abs(q[b, h])
             tv[b, j, :n] += (u * p + sub).T @ np.abs(do[b, h])
@@ -409,10 +409,21 @@ def test_self_attention_is_the_same_arithmetic(attn):
     ref = attn.attn_fwd(q, k, v)
     assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
     grads = attn.attn_cross_bwd(q, k, v, o, do, lse)
-    # float32 sums in another order: the same but for one rounding to bfloat16 of each
-    for x, y in zip(grads, attn.attn_bwd(q, k, v, o, do, lse)):
-        assert torch.all((x.float() - y.float()).abs() <= 2.0 ** -7 * y.float().abs() + 1e-5)
+    plain = attn.attn_bwd(q, k, v, o, do, lse)
     check_status(attn)
+    # dV: float32 sums in another order, then one rounding to bfloat16 of each.  dQ, dK: attn_bwd
+    # forms dS from P rounded to bfloat16, this one from P in 24 bits, both round dS: the two lie
+    # at most (the bound of the one) + (that and u p |dP - D| more, below twice it) apart.
+    assert torch.all((grads[2].float() - plain[2].float()).abs() <= 2.0 ** -7 * plain[2].float().abs() + 1e-5)
+    one = [t[:1, :2].contiguous() for t in (q, k, v, do)]
+    f = [workloads.as_f64(t.cpu()) for t in one]
+    scale = 128 ** -0.5
+    o_ref, _ = oracle.attention_cross_forward(*f[:3], scale)
+    ref = oracle.attention_cross_backward(*f, scale)
+    tols = _backward_bounds(*f, o_ref, _forward_bound(*f[:3], o_ref, scale, None, "bf16"), ref, scale, None, "bf16")
+    for x, y, t in zip(grads[:2], plain[:2], tols):
+        gap = (x[:1, :2].double() - y[:1, :2].double()).abs().cpu().numpy()
+        assert np.all(gap <= 3 * t)
 
 
 def test_explicit_stream(attn):
