@@ -4,6 +4,8 @@
 // Hardware Acceleration: Hopper GPU Strategies for Long-Context Enterprise
 // Inference Optimization", section "Memory Fragmentation", describes the cache
 // in fixed-size blocks; the paged decode (decode.cu) reads what these write.
+#include <cmath>
+
 #include "common.h"
 #include "fp8_row.cuh"
 #include "rope.cuh"
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(kTabThreads)
 // 7 (two 16-byte loads), so a full-width rotation pairs values of one lane and
 // only three of the transform's seven stages cross lanes (12 shuffles a row; a
 // warp per row takes 24).  Stages run in the pre-pass's order: same bits.
-constexpr int kF8Threads = 256;    // of the few-rows variant
+constexpr int kF8Threads = 64;     // of the few-rows variant
 constexpr int kF8MaxThreads = 512;
 
 template <bool FP16>
@@ -312,17 +314,24 @@ struct AppendSite {
 };
 
 // Request b's pages are units cu[b] / page_size + 2 b and on: at least as many units
-// as its cu[b + 1] - cu[b] tokens can touch pages.  The owner of a unit is found by
-// an eight-way search in every group of eight lanes.
+// as its cu[b + 1] - cu[b] tokens can touch pages.  Its pages with more than kFewRows new
+// rows (MANY) are units cu[b] / (kFewRows + 1) and on: the first page that has as many, and
+// those behind it.  The owner of a unit is found by an eight-way search in every group of
+// eight lanes.
+constexpr int kFewRows = 8;
+template <bool MANY>
 __device__ __forceinline__ AppendSite append_site(const AppendFp8Params& p, long long unit, int hv,
                                                   int page_shift, int u) {
   constexpr int D = 128;
+  auto first_unit = [&](int b, int cu) -> long long {
+    return MANY ? cu / (kFewRows + 1) : (static_cast<long long>(cu) >> page_shift) + 2ll * b;
+  };
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = p.B;
   while (__any_sync(0xffffffffu, hi - lo > 1)) {
     const int step = (hi - lo + 7) / 8;
     const int at = lo + u * step;
-    const bool below = u == 0 || (at < hi && (static_cast<long long>(p.cu_seqlens[at]) >> page_shift) + 2ll * at <= unit);
+    const bool below = u == 0 || (at < hi && first_unit(at, p.cu_seqlens[at]) <= unit);
     const uint32_t m = __ballot_sync(0xffffffffu, below) >> (lane & 24) & 0xffu;
     if (hi - lo > 1) {
       lo += (31 - __clz(m)) * step;
@@ -344,18 +353,19 @@ __device__ __forceinline__ AppendSite append_site(const AppendFp8Params& p, long
     return s;
   }
   const int start = len - add;                       // first new position
-  const long long lp = (start >> page_shift) + (unit - ((static_cast<long long>(c0) >> page_shift) + 2ll * b));
-  if (add == 0 || lp < 0 || (lp << page_shift) >= len) return s;
+  long long lp = (start >> page_shift) + (unit - first_unit(b, c0));
+  if (MANY && p.page_size - (start & (p.page_size - 1)) <= kFewRows) ++lp;
+  if (add == 0 || lp < (start >> page_shift) || (lp << page_shift) >= len) return s;
   const int phys = p.block_table[static_cast<size_t>(b) * p.max_pages + lp];
   if (phys < 0 || phys >= p.num_pages) {
     if (u == 0) atomicCAS(p.status, 0, kDevBadTables);
     return s;
   }
   const int h = s.is_v ? hv - p.H_kv : hv;
-  s.ok = true;
   s.page0 = static_cast<int>(lp << page_shift);
   s.first = max(start, s.page0) - s.page0;
   s.end = min(len - s.page0, p.page_size);
+  s.ok = !MANY || s.end - s.first > kFewRows;
   s.st = s.is_v ? p.vt : p.kt;
   // row x of the page is token c0 + (page0 + x - start)
   s.src = static_cast<const uint16_t*>(s.is_v ? p.v : p.k) + (s.is_v ? p.vh : p.kh) * h +
@@ -413,21 +423,22 @@ __device__ __forceinline__ uint32_t scale_codes(uint32_t w, float ratio) {
 }
 
 // The page's other rows, row x = from, from + by, ...: cleared behind the new ones of
-// a page that starts here, requantised before them when the descale grew.
-__device__ __forceinline__ void other_rows(const AppendSite& s, float after, int page_size, int from, int by) {
+// a page that starts here, requantised before them when the descale grew.  Lane u of the
+// eight takes codes 16 u .. 16 u + 15.
+__device__ __forceinline__ void other_rows(const AppendSite& s, float after, int page_size, int from, int by, int u) {
+  uint8_t* const at = s.dst + 8 * u;                 // s.dst is at column 8 u
   if (s.first == 0) {
-    for (int x = s.end + from; x < page_size; x += by) {
-      uint2* at = reinterpret_cast<uint2*>(s.dst + s.dstep * x);
-      at[0] = at[8] = make_uint2(0u, 0u);
-    }
+#pragma unroll 4
+    for (int x = s.end + from; x < page_size; x += by)
+      *reinterpret_cast<uint4*>(at + s.dstep * x) = make_uint4(0u, 0u, 0u, 0u);
   } else if (after > s.before) {
     const float ratio = __fdiv_rn(s.before, after);
 #pragma unroll 4
     for (int x = from; x < s.first; x += by) {
-      uint2* at = reinterpret_cast<uint2*>(s.dst + s.dstep * x);
-      const uint2 a = at[0], b = at[8];
-      at[0] = make_uint2(scale_codes(a.x, ratio), scale_codes(a.y, ratio));
-      at[8] = make_uint2(scale_codes(b.x, ratio), scale_codes(b.y, ratio));
+      uint4* const row = reinterpret_cast<uint4*>(at + s.dstep * x);
+      const uint4 c = *row;
+      *row = make_uint4(scale_codes(c.x, ratio), scale_codes(c.y, ratio), scale_codes(c.z, ratio),
+                        scale_codes(c.w, ratio));
     }
   }
 }
@@ -451,26 +462,30 @@ __device__ __forceinline__ float raw_amax(const Raw16& r) {
   return fmaxf(m.x, m.y);
 }
 
-// Many rows per page: one block per page and plane, blockDim / 8 = 64 rows at a time
-// (fewer for smaller pages).  STAGED: up to 4 such sweeps are copied into shared memory
-// at once, every thread its own values.  A key row's transform costs some 300
-// instructions per 4 rows, which bounds this kernel, so it runs once: sweeps 0 to 2
-// go back to shared memory as float32, sweep 3 stays in registers until the amax is
-// known (transforming twice measured 62 us against 41 for 16 K rows of 8 heads).
-// Rows of pages beyond 256 are read and transformed again, from L2.
+// Many rows per page: one block per page and plane, eight threads per row and a quarter
+// of the page (8 to 64 rows) at a time: up to four such sweeps are copied into shared
+// memory at once, every thread its own values.  A key row's transform costs some 300
+// instructions per 4 rows, which bounds this kernel, so it runs once: all sweeps but the
+// last staged one go back to shared memory as float32, that one stays in registers until
+// the amax is known (transforming twice measured 62 us against 41 for 16 K rows of 8
+// heads).  Rows of pages beyond 256 are read and transformed again, from L2.
+// Small blocks for small pages, so that an SM holds many in different phases.  8 prompts
+// of 2048 in pages of 16, 32, 64, 128: 73, 65, 66, 71 us; with a sweep as large as the page
+// allows (up to 512 threads) 81, 87, 96, 88.  256 requests that bring 3 or 60 tokens each:
+// 28 and 68.  (Clusters of such blocks for pages of 256: 91 us, one of 512 threads 78.)
 // Query rows are rotated by q_blocks other blocks, bound by DRAM and spread among
-// these.  One of them has to keep HBM busy beside a page's block (registers leave
-// room for two), so its rows too come through shared memory, seven heads in flight.
+// these.  One of them has to keep HBM busy beside a page's block, so its rows too come
+// through shared memory, seven heads in flight.
 constexpr int kSweeps = 4;
-constexpr int kSlot = 4 * kF8MaxThreads;                        // 16-byte words of a sweep
-constexpr int kStagedBytes = (3 * kSlot + kSlot / 2) * 16;      // the last one's stay raw
-static_assert(kStagedBytes == 7 * 2 * 16 * kF8MaxThreads, "seven slots of the rotation");
+// 16-byte words of shared memory per thread: three sweeps as float32, the last one raw
+constexpr int kStagedWords = 3 * 4 + 2;
+static_assert(kStagedWords == 7 * 2, "seven slots of the rotation");
 
-template <bool FP16, int MODE, bool SIGNS, bool STAGED>
+template <bool FP16, int MODE, bool SIGNS, bool MANY>
 __global__ void __launch_bounds__(kF8MaxThreads, 2)
     append_fp8_pages_kernel(const AppendFp8Params p, int page_shift, const RopeKParams q, unsigned q_blocks,
                             unsigned q_columns) {
-  extern __shared__ uint4 stage[];                   // sweep i: words [i kSlot + part blockDim + thread]
+  extern __shared__ uint4 stage[];                   // sweep i: words [(4 i + part) blockDim + thread]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int u = lane & 7;
   const int by = blockDim.x >> 3, mine = threadIdx.x >> 3;
@@ -481,33 +496,36 @@ __global__ void __launch_bounds__(kF8MaxThreads, 2)
   const unsigned before_q = static_cast<unsigned>(static_cast<unsigned long long>(blockIdx.x) * q_blocks / gridDim.x);
   const unsigned with_q = static_cast<unsigned>((blockIdx.x + 1ull) * q_blocks / gridDim.x);
   if (with_q > before_q) {
-    rope_block<FP16, MODE == kNeighbours, false, 2, STAGED ? 7 : 0>(q, before_q % q_columns, before_q / q_columns, stage);
+    rope_block<FP16, MODE == kNeighbours, false, 2, 7>(q, before_q % q_columns, before_q / q_columns, stage);
     return;
   }
   const unsigned at_site = blockIdx.x - before_q;
   if (warp == 0) {
-    const AppendSite found = append_site(p, at_site / (2 * p.H_kv), at_site % (2 * p.H_kv), page_shift, u);
+    const AppendSite found = append_site<MANY>(p, at_site / (2 * p.H_kv), at_site % (2 * p.H_kv), page_shift, u);
     if (lane == 0) site_sh = found;
   } else if (SIGNS && warp == 1) {
     *reinterpret_cast<float4*>(signs + 4 * lane) = __ldg(reinterpret_cast<const float4*>(p.signs) + lane);
   }
   __syncthreads();
   AppendSite s = site_sh;
+  // MANY: a dependent launch beside the few-rows kernel, which writes other pages; only its
+  // end has to be waited for
+  if constexpr (MANY) {
+    if (!s.ok) wait_for_previous_kernel();
+  }
   if (!s.ok) return;                                 // the same for the whole block
   s.src += 8 * u;
   s.dst += 8 * u;
   uint4* const my = stage + threadIdx.x;
-  const int step = blockDim.x;
-  if constexpr (STAGED) {
+  const int step = blockDim.x, slot = 4 * step;
 #pragma unroll
-    for (int i = 0; i < kSweeps; ++i) {
-      const int x = s.first + mine + i * by;
-      const bool valid = x < s.end;
-      const uint4* at = reinterpret_cast<const uint4*>(s.src + s.st * (valid ? x : s.first));
-      copy16_async(my + i * kSlot, at, valid);
-      copy16_async(my + i * kSlot + step, at + 8, valid);
-      copies_commit();
-    }
+  for (int i = 0; i < kSweeps; ++i) {
+    const int x = s.first + mine + i * by;
+    const bool valid = x < s.end;
+    const uint4* at = reinterpret_cast<const uint4*>(s.src + s.st * (valid ? x : s.first));
+    copy16_async(my + i * slot, at, valid);
+    copy16_async(my + i * slot + step, at + 8, valid);
+    copies_commit();
   }
   const int warp_first = s.first + (warp << 2);      // first row of the warp's first sweep
   const int sweeps = warp_first < s.end ? (s.end - warp_first + by - 1) / by : 0;   // of this warp
@@ -523,41 +541,34 @@ __global__ void __launch_bounds__(kF8MaxThreads, 2)
     if (!s.is_v) key_row<MODE, SIGNS>(v, p, s.page0 + s.first + mine + i * by, u, signs);
   };
   float amax = 0.f;
-  int i = 0;
-  if constexpr (STAGED) {
-    auto staged = [&](int at) {
-      const Raw16 r{my[at * kSlot], my[at * kSlot + step]};
-      if (s.is_v) {
-        amax = fmaxf(amax, raw_amax<FP16>(r));       // values are widened when stored
-        return;
-      }
-      finish(at, r);
-      amax = fmaxf(amax, amax16(v));
-      if (at == kSweeps - 1) return;
+  const int held = min(sweeps, kSweeps) - 1;         // the last staged sweep stays in v
+  auto staged = [&](int at) {
+    const Raw16 r{my[at * slot], my[at * slot + step]};
+    if (s.is_v) {
+      amax = fmaxf(amax, raw_amax<FP16>(r));         // values are widened when stored
+      return;
+    }
+    finish(at, r);
+    amax = fmaxf(amax, amax16(v));
+    if (at == held) return;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        my[at * kSlot + e * step] = make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
-                                               __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
-    };
-    copies_wait<3>();
-    if (sweeps > 0) staged(0);
-    copies_wait<2>();
-    if (sweeps > 1) staged(1);
-    copies_wait<1>();
-    if (sweeps > 2) staged(2);
-    copies_wait<0>();
-    // rows beyond the staged ones before the last staged sweep, which stays in v
-    for (i = kSweeps; i < sweeps; ++i) {
-      finish(i, raw_row(i));
-      amax = fmaxf(amax, amax16(v));
-    }
-    if (sweeps > 3) staged(3);
-  } else {
-    for (; i < sweeps; ++i) {
-      finish(i, raw_row(i));
-      amax = fmaxf(amax, amax16(v));
-    }
+    for (int e = 0; e < 4; ++e)
+      my[at * slot + e * step] = make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
+                                            __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
+  };
+  copies_wait<3>();
+  if (sweeps > 0) staged(0);
+  copies_wait<2>();
+  if (sweeps > 1) staged(1);
+  copies_wait<1>();
+  if (sweeps > 2) staged(2);
+  copies_wait<0>();
+  // rows beyond the staged ones before the last staged sweep
+  for (int i = kSweeps; i < sweeps; ++i) {
+    finish(i, raw_row(i));
+    amax = fmaxf(amax, amax16(v));
   }
+  if (sweeps > 3) staged(3);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if (lane == 0) warp_max[warp] = amax;
@@ -571,44 +582,42 @@ __global__ void __launch_bounds__(kF8MaxThreads, 2)
     const int x = s.first + mine + at * by;
     if (x < s.end) store_row(s, x, v, y2, nb2);
   };
-  if constexpr (STAGED) {
-    if (sweeps > 3) {
-      if (s.is_v) widen16<FP16>(my[3 * kSlot], my[3 * kSlot + step], v);
-      store(3);
-    }
-    for (int at = 0; at < min(sweeps, 3); ++at) {
-      if (s.is_v) {
-        widen16<FP16>(my[at * kSlot], my[at * kSlot + step], v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint4 w = my[at * kSlot + e * step];
-          v[4 * e] = __uint_as_float(w.x), v[4 * e + 1] = __uint_as_float(w.y);
-          v[4 * e + 2] = __uint_as_float(w.z), v[4 * e + 3] = __uint_as_float(w.w);
-        }
-      }
-      store(at);
-    }
-    for (i = kSweeps; i < sweeps; ++i) {
-      finish(i, raw_row(i));
-      store(i);
-    }
-  } else {
-    for (i = 0; i < sweeps; ++i) {
-      if (sweeps > 1) finish(i, raw_row(i));         // one sweep: still in v
-      store(i);
-    }
+  if (held >= 0) {
+    if (s.is_v) widen16<FP16>(my[held * slot], my[held * slot + step], v);
+    store(held);
   }
-  other_rows(s, after, p.page_size, mine, by);
+  for (int at = 0; at < held; ++at) {
+    if (s.is_v) {
+      widen16<FP16>(my[at * slot], my[at * slot + step], v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint4 w = my[at * slot + e * step];
+        v[4 * e] = __uint_as_float(w.x), v[4 * e + 1] = __uint_as_float(w.y);
+        v[4 * e + 2] = __uint_as_float(w.z), v[4 * e + 3] = __uint_as_float(w.w);
+      }
+    }
+    store(at);
+  }
+  for (int i = kSweeps; i < sweeps; ++i) {
+    finish(i, raw_row(i));
+    store(i);
+  }
+  other_rows(s, after, p.page_size, mine, by, u);
+  if constexpr (MANY) wait_for_previous_kernel();
 }
 
 // Few rows per page (a decode step): eight lanes per page and plane, so the planes
-// of a page share a block and its lookups; blocks behind them rotate query rows.
+// of a page share a block and its lookups; blocks behind them rotate query rows.  Pages with
+// more than most_rows new rows are left to append_fp8_pages_kernel.  Small blocks spread a
+// few requests' pages, which may have to be cleared or requantised, over the machine (64
+// requests, pages of 64 and of 256: 5.5 and 7.6 us; in blocks of 256 threads 5.7 and 11.7).
 template <bool FP16, int MODE, bool SIGNS>
 __global__ void __launch_bounds__(kF8Threads)
     append_fp8_rows_kernel(const AppendFp8Params p, int page_shift, long long sites, unsigned site_blocks,
-                           const RopeKParams q, unsigned q_columns) {
+                           const RopeKParams q, unsigned q_columns, int most_rows) {
   __shared__ __align__(16) float signs[128];
+  if (most_rows < p.page_size) release_dependents();
   if (blockIdx.x >= site_blocks) {
     const unsigned at = blockIdx.x - site_blocks;
     rope_block<FP16, MODE == kNeighbours, false>(q, at % q_columns, at / q_columns);
@@ -618,8 +627,8 @@ __global__ void __launch_bounds__(kF8Threads)
   const long long site = static_cast<long long>(blockIdx.x) * (kF8Threads / 8) + (threadIdx.x >> 3);
   const int planes = 2 * p.H_kv;
   // past the last site: a unit that no request reaches
-  AppendSite s = append_site(p, site < sites ? site / planes : 0, static_cast<int>(site % planes), page_shift, u);
-  if (site >= sites) s.ok = false;
+  AppendSite s = append_site<false>(p, site < sites ? site / planes : 0, static_cast<int>(site % planes), page_shift, u);
+  if (site >= sites || s.end - s.first > most_rows) s.ok = false;
   if (!s.ok) s.first = s.end = 0;
   s.src += 8 * u;
   s.dst += 8 * u;
@@ -662,7 +671,7 @@ __global__ void __launch_bounds__(kF8Threads)
   __syncwarp();                                      // every lane has read the old descale
   if (s.ok) {
     if (u == 0) *s.descale = after;
-    other_rows(s, after, p.page_size, 0, 1);
+    other_rows(s, after, p.page_size, 0, 1, u);
   }
 }
 
@@ -676,29 +685,53 @@ template <bool FP16, int MODE, bool SIGNS>
 attn_status_t launch_append_t(const AppendFp8Params& p, RopeKParams q, int page_shift, long long sites,
                               cudaStream_t stream) {
   q.status = p.status;
-  // Up to 4 new tokens per request on average: eight lanes per page and plane.  More: a
-  // block each, eight threads per row of a page, up to 64 rows at a time.
-  const bool few = p.total <= 4ll * p.B;
-  const int threads = few ? kF8Threads : p.page_size * 8 < kF8MaxThreads ? p.page_size * 8 : kF8MaxThreads;
+  // Three ways: all pages by eight lanes per plane; all by blocks per plane; or the first for
+  // pages of few new rows and the second for the others.  The times are fitted to 16 to 256 rows
+  // a page, 1 to 1024 requests and 8 heads.  Eight lanes: a start and the page's other rows, the
+  // rows one after the other (which page they stand in is not known here; one a page is
+  // assumed where there are no more tokens than requests), and their number.  Blocks: as
+  // many as fit at a time, those of pages that no token reaches among them.
+  // Pages of 64, us by lanes, by blocks, by both: 64 requests with a token each 5.5, 7.7, -;
+  // 256: 6.7, 22, -; 256 with 4 each 12, 24, 15; 16 of which two bring up to 30 33, 5.4, -; 256 of
+  // which 32 bring up to 20 26, 24, 13.
+  const int quarter = p.page_size / 4 * 8;           // threads of a sweep of a quarter of the page
+  const int page_threads = quarter < 64 ? 64 : quarter > kF8MaxThreads ? kF8MaxThreads : quarter;
+  const double at_a_time = 152.0 * (1024 / page_threads);
+  const long long many = p.total / (kFewRows + 1) * 2 * p.H_kv;
+  const double lanes = 3.5 + 0.015 * p.page_size + 4.6e-4 * p.total * 2 * p.H_kv;
+  const double blocks = 2.0 + (2.5 + 20.0 / p.page_size) * std::fmax(1.0, sites / at_a_time);
+  const double both = lanes + 2.0 + 1.7 * (many / at_a_time);
+  enum { kLanes, kBlocks, kBoth } how = p.total <= p.B ? lanes <= blocks ? kLanes : kBlocks
+                                                       : both <= blocks ? kBoth : kBlocks;
+  const int threads = how == kBlocks ? page_threads : kF8Threads;
   RopeGrid g{1, 0};
-  if (q.heads[0] > 0) g = rope_grid(&q, threads, few ? 152 * 8 : 152 * 2);
+  if (q.heads[0] > 0) g = rope_grid(&q, threads, how == kBlocks ? 152 * 2 : 152 * 8);
   const long long q_blocks = g.columns * g.chunks;
-  const long long own = few ? (sites + kF8Threads / 8 - 1) / (kF8Threads / 8) : sites;
+  const long long own = how == kBlocks ? sites : (sites + kF8Threads / 8 - 1) / (kF8Threads / 8);
   if (own + q_blocks > 2147483647LL) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
   const unsigned grid = static_cast<unsigned>(own + q_blocks), columns = static_cast<unsigned>(g.columns);
   const unsigned qb = static_cast<unsigned>(q_blocks);
-  if (few) {
-    append_fp8_rows_kernel<FP16, MODE, SIGNS><<<grid, threads, 0, stream>>>(p, page_shift, sites,
-                                                                           static_cast<unsigned>(own), q, columns);
-  } else if (p.page_size * 8 <= kF8MaxThreads) {
-    append_fp8_pages_kernel<FP16, MODE, SIGNS, false><<<grid, threads, 0, stream>>>(p, page_shift, q, qb, columns);
-  } else {
-    auto kern = append_fp8_pages_kernel<FP16, MODE, SIGNS, true>;
-    const attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), kStagedBytes);
+  const int page_smem = kStagedWords * 16 * page_threads;
+  cudaError_t e = cudaSuccess;
+  if (how == kBlocks) {
+    auto kern = append_fp8_pages_kernel<FP16, MODE, SIGNS, false>;
+    const attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), kStagedWords * 16 * kF8MaxThreads);
     if (s != ATTN_OK) return s;
-    kern<<<grid, threads, kStagedBytes, stream>>>(p, page_shift, q, qb, columns);
+    kern<<<grid, page_threads, page_smem, stream>>>(p, page_shift, q, qb, columns);
+    e = cudaGetLastError();
+  } else {
+    const bool rest = how == kBoth && many > 0;
+    append_fp8_rows_kernel<FP16, MODE, SIGNS><<<grid, threads, 0, stream>>>(
+        p, page_shift, sites, static_cast<unsigned>(own), q, columns, rest ? kFewRows : p.page_size);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && rest) {
+      auto kern = append_fp8_pages_kernel<FP16, MODE, SIGNS, true>;
+      const attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), kStagedWords * 16 * kF8MaxThreads);
+      if (s != ATTN_OK) return s;
+      e = launch_dependent(kern, dim3(static_cast<unsigned>(many)), page_threads, page_smem, stream, 0, p, page_shift, q,
+                           0u, 1u);
+    }
   }
-  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "FP8 append kernel launch");
   return ATTN_OK;
 }
@@ -744,7 +777,6 @@ attn_status_t launch_append_fp8(AppendFp8Params p, RopeKParams q, int fp16, int 
                                 cudaStream_t stream) {
   p.status = device_status_word();
   if (!p.status) return fail(ATTN_ERR_CUDA, "status word unavailable");
-  static_assert(kF8Threads == kRopeThreads, "one block size for both roles");
   const int shift = shift_of(p.page_size);
   const long long units = (static_cast<long long>(p.total) >> shift) + 2ll * p.B;
   const long long sites = units * 2 * p.H_kv;

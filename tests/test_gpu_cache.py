@@ -283,6 +283,42 @@ def test_append_fp8_zero_rows_and_bad_requests(attn):
     check_status(attn)
 
 
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("top", [1, 3, 60])
+def test_append_fp8_of_a_batch_is_its_requests_one_by_one(attn, page, top):
+    """Hundreds of requests, most with a token or none, some with up to `top` (8, 9 and 10 of one
+    page, across a border, a whole page), whichever way the call takes them: the bytes of one
+    call per request."""
+    H_kv, d, B = 8, 128, 300
+    rng = np.random.default_rng(80 + top)
+    new = rng.integers(0, 2, B)
+    for i in range(0, B, 7):
+        new[i] = rng.integers(1, top + 1)
+    if top > 8:
+        new[1:6] = [8, 9, 10, page, page + 9]
+    old = rng.integers(0, 3 * page, B)
+    old[1:6] = [2 * page, page - 8, page - 9, 0, page - 9]
+    bt, (lens, cu, slots, pos, _), num, _, k, v = _step(attn, 81, old.tolist(), new.tolist(), page, 1, H_kv, d, torch.bfloat16)
+    cos, sin = _rope(1200, d)
+    sg = _signs()
+    state = (torch.randint(0, 0x7E, (num, page, H_kv, d), dtype=torch.uint8, device=dev()),
+             torch.randint(0, 0x7E, (num, page, H_kv, d), dtype=torch.uint8, device=dev()),
+             torch.rand(num, H_kv, device=dev()) * 0.02, torch.rand(num, H_kv, device=dev()) * 0.02)
+    one = [t.clone() for t in state]
+    all_ = [t.clone() for t in state]
+    attn.attn_cache_append_fp8(k, v, *all_, bt, lens, cu, cos, sin, sg)
+    check_status(attn)
+    first = np.concatenate([[0], np.cumsum(new)])
+    for b in range(B):
+        n = int(new[b])
+        if n:
+            at = slice(first[b], first[b] + n)
+            attn.attn_cache_append_fp8(k[at], v[at], *one, bt[b:b + 1], lens[b:b + 1], _i32([0, n]), cos, sin, sg)
+    check_status(attn)
+    for x, y, was in zip(all_, one, state):
+        assert torch.equal(x, y) and not torch.equal(x, was)
+
+
 @pytest.mark.parametrize("new", [[1, 0, 1], [40, 0, 9]])
 def test_append_fp8_rows_behind_the_last_request(attn, new):
     """Padding behind cu_seqlens[B] (NaN): nothing of it is stored, its query rows are copied."""
