@@ -285,9 +285,9 @@ def test_graph_replay_stream_and_repeat(attn, N_q):
     check_status(attn)
 
 
-@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("how", ["one stream", "two streams", "captured"])
 @pytest.mark.parametrize("B,H_kv,N_k", [(1, 16, 1500), (24, 8, 700), (2, 2, 20000)])
-def test_inputs_written_by_the_kernel_before(attn, B, H_kv, N_k, captured):
+def test_inputs_written_by_the_kernel_before(attn, B, H_kv, N_k, how):
     """Few-rows calls (a cluster per segment, shared tiles) start before the stream's previous
     kernel has ended.  Inputs, the lengths too, written right before each call, its output read
     and they overwritten right behind it, in a graph also from another stream and after a memset:
@@ -312,7 +312,7 @@ def test_inputs_written_by_the_kernel_before(attn, B, H_kv, N_k, captured):
         for i in range(9):
             for to, source in zip(now, sets[i % 3]):
                 if side is None:
-                    torch.mul(source, 1, out=to)
+                    to.copy_(source) if i % 2 else torch.mul(source, 1, out=to)
                     continue
                 side.wait_stream(here)               # the next input from the other stream
                 with torch.cuda.stream(side):
@@ -324,8 +324,9 @@ def test_inputs_written_by_the_kernel_before(attn, B, H_kv, N_k, captured):
             for to, source in zip(outs, (o, lse)):
                 torch.mul(source, 1, out=to[i])
 
-    if captured:
-        stream, side = torch.cuda.Stream(), torch.cuda.Stream()
+    side = torch.cuda.Stream()
+    if how == "captured":
+        stream = torch.cuda.Stream()
         graph = torch.cuda.CUDAGraph()
         torch.cuda.synchronize()
         with torch.cuda.graph(graph, stream=stream):
@@ -333,7 +334,7 @@ def test_inputs_written_by_the_kernel_before(attn, B, H_kv, N_k, captured):
         for _ in range(3):
             graph.replay()
     else:
-        run()
+        run(side if how == "two streams" else None)
     torch.cuda.synchronize()
     check_status(attn)
     for i in range(9):
