@@ -823,7 +823,7 @@ def attn_block_tables(block_table, old_lens, new_lens, free_pages, page_size: in
     pages in block_table [B, max_pages] (in place, taken from the front of the int32
     free_pages).  Returns seq_lens [B], cu_seqlens [B + 1], slots int64 [capacity] and
     positions int32 [capacity] of the new tokens (-1 behind the last) and used [1],
-    the free pages taken."""
+    the free pages taken; those not given are parts of one allocation."""
     return _binding().block_tables(block_table, old_lens, new_lens, free_pages, page_size, capacity, seq_lens,
                                   cu_seqlens, slots, positions, used, stream)
 

@@ -121,6 +121,35 @@ struct Device {
     const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(stream, index));
     return at::detail::empty_cuda(shape, type, on, std::nullopt);
   }
+  // Several small outputs, those not given as parts of one allocation (an allocation and
+  // its release take most of a microsecond each).
+  struct Wanted {
+    Arg* a;
+    std::vector<int64_t> shape;
+    at::ScalarType type;
+    size_t at = 0;
+  };
+  void outputs(std::vector<Wanted> all) const {
+    size_t bytes = 0;
+    for (Wanted& w : all) {
+      if (*w.a) {
+        like(*w.a, w.shape, w.type);
+        continue;
+      }
+      w.at = bytes;
+      bytes += (c10::multiply_integers(w.shape) * c10::elementSize(w.type) + 255) / 256 * 256;
+    }
+    at::Tensor whole;
+    for (Wanted& w : all) {
+      if (*w.a) continue;
+      if (!whole.defined()) whole = empty({static_cast<int64_t>(bytes)}, at::kByte);
+      w.a->t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
+                                                        c10::scalarTypeToTypeMeta(w.type));
+      c10::TensorImpl* t = w.a->t.unsafeGetTensorImpl();
+      t->set_sizes_contiguous(w.shape);
+      t->set_storage_offset(static_cast<int64_t>(w.at / c10::elementSize(w.type)));
+    }
+  }
   // a given output of that shape and type, or a new one
   void output(Arg& a, at::IntArrayRef shape, at::ScalarType type) const {
     if (a) like(a, shape, type);
@@ -371,11 +400,11 @@ PyObject* block_tables(PyObject* const* a) {
   like(add, {B}, at::kInt);
   like(free_, free_.t.sizes(), at::kInt);
   const Device dev(a[11], bt, old, add, free_, lens, cu, slots, pos, used);
-  dev.output(lens, {B}, at::kInt);
-  dev.output(cu, {B + 1}, at::kInt);
-  dev.output(slots, {cap}, at::kLong);
-  dev.output(pos, {cap}, at::kInt);
-  dev.output(used, {1}, at::kInt);
+  dev.outputs({{&lens, {B}, at::kInt},
+               {&cu, {B + 1}, at::kInt},
+               {&slots, {cap}, at::kLong},
+               {&pos, {cap}, at::kInt},
+               {&used, {1}, at::kInt}});
   call("attn_block_tables", [&] {
     return api.attn_block_tables(bt.as<int>(), old.as<int>(), add.as<int>(), free_.as<int>(), lens.as<int>(), cu.as<int>(),
                                  slots.as<long long>(), pos.as<int>(), used.as<int>(), B, max_pages, extent(free_.size(0)),
