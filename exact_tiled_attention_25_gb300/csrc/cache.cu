@@ -15,7 +15,7 @@ namespace {
 
 // ============================================================ block tables ====
 constexpr int kTabThreads = 512;
-constexpr int kTabMaxB = 16384;   // 8 bytes of shared memory per request
+constexpr int kTabMaxB = 16384;   // 12 bytes of shared memory per request
 
 // Exclusive prefix sums of new tokens and new pages over all requests, in every
 // block (the requests' lengths are a few KB of L2 hits, cheaper than a second
@@ -23,69 +23,80 @@ constexpr int kTabMaxB = 16384;   // 8 bytes of shared memory per request
 // tokens in ceil(old / page_size) pages; its new pages take consecutive entries
 // of the free list, requests in order.  New table entries are taken from the
 // free list directly, so no block reads what another writes.
-// Bound: latency -- a launch, the scan's barriers and one dependent chain of
-// loads (length, table entry, store).
+// Bound: latency -- a launch, the lengths, the scan's barriers, and per token a binary
+// search in shared memory, a table entry and the stores.
+// A dependent launch: it reads past the L1 cache.
 __global__ void __launch_bounds__(kTabThreads)
     block_tables_kernel(const TablesParams p, int* status, int page_shift) {
   extern __shared__ int tab_sh[];
   int* cu = tab_sh;                  // [B + 1] first new token of each request
-  int* pg = tab_sh + p.B + 1;        // [B + 1] first free-list entry of each request
+  int* pg = cu + p.B + 1;            // [B + 1] first free-list entry of each request
+  int* old_sh = pg + p.B + 1;        // [B] tokens in the cache
   __shared__ long long warp_sum[2][kTabThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int page = p.page_size;
   const long long room = static_cast<long long>(p.max_pages) * page;
+  auto pages_of = [&](long long n) { return static_cast<int>((n + page - 1) >> page_shift); };
   bool bad = false;
-  long long tok_base = 0, page_base = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kTabThreads) {
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    long long tok = 0, pages = 0;
-    if (b < p.B) {
-      int old = p.old_lens[b], add = p.new_lens[b];
-      if (old < 0 || old > room || add < 0 || old + static_cast<long long>(add) > room) {
-        bad = true;
-        old = old < 0 || old > room ? 0 : old;
-        add = 0;
-      }
-      tok = add;
-      pages = ((old + static_cast<long long>(add) + page - 1) >> page_shift) -
-              ((static_cast<long long>(old) + page - 1) >> page_shift);
-      if (blockIdx.x == 0) p.seq_lens[b] = old + add;
+  wait_for_previous_kernel();
+#pragma unroll 4
+  for (int b = threadIdx.x; b < p.B; b += kTabThreads) {
+    int old = __ldcg(p.old_lens + b), add = __ldcg(p.new_lens + b);
+    if (old < 0 || old > room || add < 0 || old + static_cast<long long>(add) > room) {
+      bad = true;
+      old = old < 0 || old > room ? 0 : old;
+      add = 0;
     }
-    long long ts = tok, ps = pages;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, ts, o), q = __shfl_up_sync(0xffffffffu, ps, o);
-      if (lane >= o) {
-        ts += t;
-        ps += q;
-      }
-    }
-    if (lane == 31) {
-      warp_sum[0][warp] = ts;
-      warp_sum[1][warp] = ps;
-    }
-    __syncthreads();
-    long long tw = 0, pw = 0, tall = 0, pall = 0;
-#pragma unroll
-    for (int w = 0; w < kTabThreads / 32; ++w) {
-      if (w == warp) {
-        tw = tall;
-        pw = pall;
-      }
-      tall += warp_sum[0][w];
-      pall += warp_sum[1][w];
-    }
-    if (b < p.B) {
-      const long long t = tok_base + tw + ts - tok, q = page_base + pw + ps - pages;
-      cu[b] = static_cast<int>(t < 2147483647LL ? t : 2147483647LL);
-      pg[b] = static_cast<int>(q < 2147483647LL ? q : 2147483647LL);
-    }
-    tok_base += tall;
-    page_base += pall;
-    __syncthreads();
+    old_sh[b] = old;
+    cu[b] = add;
+    pg[b] = pages_of(old + static_cast<long long>(add)) - pages_of(old);
   }
-  const int total = static_cast<int>(tok_base < 2147483647LL ? tok_base : 2147483647LL);
-  const int pages_all = static_cast<int>(page_base < 2147483647LL ? page_base : 2147483647LL);
+  __syncthreads();
+  // each thread's own requests, one after the other, then those of the threads before
+  const int per = (p.B + kTabThreads - 1) / kTabThreads;
+  const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
+  long long tok = 0, pages = 0;
+  for (int b = b0; b < b1; ++b) {
+    tok += cu[b];
+    pages += pg[b];
+  }
+  long long ts = tok, ps = pages;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, ts, o), q = __shfl_up_sync(0xffffffffu, ps, o);
+    if (lane >= o) {
+      ts += t;
+      ps += q;
+    }
+  }
+  if (lane == 31) {
+    warp_sum[0][warp] = ts;
+    warp_sum[1][warp] = ps;
+  }
+  __syncthreads();
+  long long tok_all = 0, pages_sum = 0;
+  ts -= tok;
+  ps -= pages;
+#pragma unroll
+  for (int w = 0; w < kTabThreads / 32; ++w) {
+    const long long t = warp_sum[0][w], q = warp_sum[1][w];
+    if (w < warp) {
+      ts += t;
+      ps += q;
+    }
+    tok_all += t;
+    pages_sum += q;
+  }
+  auto clamp = [](long long x) { return static_cast<int>(x < 2147483647LL ? x : 2147483647LL); };
+  for (int b = b0; b < b1; ++b) {
+    const int add = cu[b], need = pg[b];
+    if (blockIdx.x == 0) p.seq_lens[b] = old_sh[b] + add;
+    cu[b] = clamp(ts);
+    pg[b] = clamp(ps);
+    ts += add;
+    ps += need;
+  }
+  const int total = clamp(tok_all), pages_all = clamp(pages_sum);
   if (threadIdx.x == 0) {
     cu[p.B] = total;
     pg[p.B] = pages_all;
@@ -94,7 +105,7 @@ __global__ void __launch_bounds__(kTabThreads)
   if (blockIdx.x == 0) {
     for (int b = threadIdx.x; b <= p.B; b += kTabThreads) p.cu_seqlens[b] = cu[b];
     if (threadIdx.x == 0) p.used[0] = min(pages_all, p.n_free);
-    if (bad || (threadIdx.x == 0 && (tok_base > p.capacity || page_base > p.n_free)))
+    if (bad || (threadIdx.x == 0 && (tok_all > p.capacity || pages_sum > p.n_free)))
       atomicCAS(status, 0, kDevBadTables);
   }
   // request that owns index x of a list whose request b starts at first[b]: the
@@ -108,10 +119,6 @@ __global__ void __launch_bounds__(kTabThreads)
     }
     return lo;
   };
-  auto valid_old = [&](int b) {
-    const int old = p.old_lens[b];
-    return old < 0 || old > room ? 0 : old;
-  };
   const int step = gridDim.x * kTabThreads;
   const int me = blockIdx.x * kTabThreads + threadIdx.x;
   for (long long t = me; t < p.capacity; t += step) {
@@ -119,16 +126,16 @@ __global__ void __launch_bounds__(kTabThreads)
     int pos = -1;
     if (t < total) {
       const int b = owner(cu, static_cast<int>(t));
-      const int old = valid_old(b);
+      const int old = old_sh[b];
       pos = old + (static_cast<int>(t) - cu[b]);
       const int lp = pos >> page_shift;
-      const int have = static_cast<int>((static_cast<long long>(old) + page - 1) >> page_shift);
+      const int have = pages_of(old);
       int phys;
       if (lp < have) {
-        phys = p.block_table[static_cast<size_t>(b) * p.max_pages + lp];
+        phys = __ldcg(p.block_table + static_cast<size_t>(b) * p.max_pages + lp);
       } else {
         const long long e = static_cast<long long>(pg[b]) + (lp - have);
-        phys = e < p.n_free ? p.free_pages[e] : -1;
+        phys = e < p.n_free ? __ldcg(p.free_pages + e) : -1;
       }
       if (phys >= 0) slot = static_cast<long long>(phys) * page + (pos & (page - 1));
     }
@@ -137,9 +144,8 @@ __global__ void __launch_bounds__(kTabThreads)
   }
   for (long long e = me; e < pages_all; e += step) {
     const int b = owner(pg, static_cast<int>(e));
-    const int have = static_cast<int>((static_cast<long long>(valid_old(b)) + page - 1) >> page_shift);
-    p.block_table[static_cast<size_t>(b) * p.max_pages + have + (e - pg[b])] =
-        e < p.n_free ? p.free_pages[e] : -1;
+    p.block_table[static_cast<size_t>(b) * p.max_pages + pages_of(old_sh[b]) + (e - pg[b])] =
+        e < p.n_free ? __ldcg(p.free_pages + e) : -1;
   }
 }
 
@@ -758,17 +764,16 @@ attn_status_t launch_block_tables(const TablesParams& p, cudaStream_t stream) {
   if (p.B > kTabMaxB) return fail(ATTN_ERR_UNSUPPORTED, "block tables: at most 16384 requests");
   int* status = device_status_word();
   if (!status) return fail(ATTN_ERR_CUDA, "status word unavailable");
-  const int smem = 2 * (p.B + 1) * static_cast<int>(sizeof(int));
+  const int smem = (3 * p.B + 2) * static_cast<int>(sizeof(int));
   if (smem > 48 * 1024) {
-    const attn_status_t s = set_smem(reinterpret_cast<const void*>(block_tables_kernel), 2 * (kTabMaxB + 1) * 4);
+    const attn_status_t s = set_smem(reinterpret_cast<const void*>(block_tables_kernel), (3 * kTabMaxB + 2) * 4);
     if (s != ATTN_OK) return s;
   }
   // one thread per token, at most two blocks per SM
   long long blocks = (static_cast<long long>(p.capacity) + kTabThreads - 1) / kTabThreads;
   blocks = blocks < 1 ? 1 : blocks > 304 ? 304 : blocks;
-  block_tables_kernel<<<static_cast<unsigned>(blocks), kTabThreads, smem, stream>>>(p, status,
-                                                                                   shift_of(p.page_size));
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(block_tables_kernel, dim3(static_cast<unsigned>(blocks)), kTabThreads, smem,
+                                         stream, 0, p, status, shift_of(p.page_size));
   if (e != cudaSuccess) return fail_cuda(e, "block table kernel launch");
   return ATTN_OK;
 }
