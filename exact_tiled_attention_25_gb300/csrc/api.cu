@@ -876,9 +876,21 @@ attn_status_t attn_block_tables(int* block_table, const int* old_lens, const int
     if (slots == nullptr || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
       return fail(ATTN_ERR_INVALID_ARG, "slots must be non-null and 8-byte aligned");
   }
-  // every block reads the lengths while the first one writes seq_lens
-  if (seq_lens == old_lens || seq_lens == new_lens)
-    return fail(ATTN_ERR_INVALID_ARG, "seq_lens must not be old_lens or new_lens");
+  // every block reads the inputs while others write
+  struct Range {
+    const void* p;
+    size_t bytes;
+  };
+  const size_t b4 = 4 * static_cast<size_t>(B), cap = static_cast<size_t>(capacity);
+  const Range ins[] = {{old_lens, b4}, {new_lens, b4}, {free_pages, 4 * static_cast<size_t>(n_free)}};
+  const Range outs[] = {{block_table, b4 * max_pages}, {seq_lens, b4}, {cu_seqlens, b4 + 4}, {slots, 8 * cap},
+                        {positions, 4 * cap}, {used, 4}};
+  for (const Range& o : outs)
+    for (const Range& i : ins) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(o.p), y = reinterpret_cast<uintptr_t>(i.p);
+      if (o.bytes > 0 && i.bytes > 0 && x < y + i.bytes && y < x + o.bytes)
+        return fail(ATTN_ERR_INVALID_ARG, "outputs (block_table, seq_lens, ...) must not overlap old_lens, new_lens or free_pages");
+    }
   if ((s = check_device()) != ATTN_OK) return s;
   return launch_block_tables({block_table, old_lens, new_lens, free_pages, seq_lens, cu_seqlens, slots,
                               positions, used, B, max_pages, n_free, page_size, capacity},

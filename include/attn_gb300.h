@@ -673,8 +673,7 @@ attn_status_t attn_rope(const void* q, void* q_out, const void* k, void* k_out, 
  *   new_lens    : int32 [B]: tokens in the cache, tokens this step adds (0 allowed).
  *   free_pages  : int32 [n_free]: free physical pages; new pages take them from the
  *                 front, requests in order, pages of a request in order.
- *   seq_lens    : int32 [B] (written) old_lens + new_lens, for the paged decode;
- *                 must not be old_lens or new_lens.
+ *   seq_lens    : int32 [B] (written) old_lens + new_lens, for the paged decode.
  *   cu_seqlens  : int32 [B + 1] (written) offsets of each request's new tokens.
  *   slots       : int64 [capacity] (written) page * page_size + offset of each new
  *                 token, requests in order; -1 behind the last one.
@@ -686,6 +685,7 @@ attn_status_t attn_rope(const void* q, void* q_out, const void* k, void* k_out, 
  * cannot give become -1 in the table, with slots -1; tokens past `capacity` are
  * left out of slots and positions.  All are reported by attn_get_device_status()
  * as ATTN_ERR_INVALID_ARG.
+ * No output overlaps old_lens, new_lens or free_pages.
  * page_size a power of two in [8, 65536]; B <= 16384; capacity may be 0.
  * Source: the block table of attn_decode_paged ("FlashAttention 3 Hardware
  * Acceleration: ...", section "Memory Fragmentation").

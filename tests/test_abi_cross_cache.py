@@ -100,6 +100,15 @@ def test_block_table_refusals(lib, kwargs, why):
     assert why in lib.attn_last_error().decode()
 
 
+@pytest.mark.parametrize("kwargs", [dict(sl=0x1004), dict(sl=0xFFC), dict(cu=0x2004), dict(used=0x300C), dict(slots=0xFC8),
+                                    dict(pos=0x2000), dict(bt=0xFE4)])
+def test_block_table_outputs_over_inputs(lib, kwargs):
+    """Partial overlaps too: the other blocks of the kernel still read what one writes."""
+    apart = dict(bt=0x10000, old=0x1000, new=0x2000, free=0x3000, sl=0x4000, cu=0x5000, slots=0x6000, pos=0x7000, used=0x8000)
+    assert _tables(lib, **{**apart, **kwargs}) == 1
+    assert "overlap" in lib.attn_last_error().decode()
+
+
 def _append(lib, q=16, qo=16, k=16, v=16, kc=16, vc=16, slots=16, c=16, s=16, pos=16, total=4, H=2, Hkv=1, d=64,
             rot=64, mp=8, pages=4, ps=16, qs=None, ks=None, vs=None, il=0, dt=0):
     return lib.attn_cache_append(q, qo, k, v, kc, vc, slots, c, s, pos, total, H, Hkv, d, rot, mp, pages, ps, qs, ks,
