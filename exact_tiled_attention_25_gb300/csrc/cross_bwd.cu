@@ -632,6 +632,109 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   }
 }
 
+// The pre-pass for at most kFewKeys keys: as bwd_prep_kernel, but D = sum_j P_j dP_j from the
+// keys themselves.  Of one or a few keys O is of V's size, and its rounding weighs in dO . O
+// against the differences dP - D: relative error of dQ and dK in float16 0.00047 (2 keys),
+// 0.00038 (4), 0.00033 (8), 0.00032 (16), so 0.0003; with more keys it tends to 0.0003 either
+// way.  Bound: the products' issue slots, 0.7 us per key and 75 K rows (whole backward pass of
+// those: 28 us with the other pre-pass; 30, 34 and 39 so at 2, 8 and 16 keys).
+constexpr int kFewKeys = 16;
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(256)
+    cross_few_keys_prep_kernel(const XBwdKParams kp, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                               const uint16_t* dout, const float* lse, float* lse2, float* delta, float* dq_acc) {
+  constexpr int L = D / 8;                           // lanes per row, 8 elements each
+  constexpr int ROWS = 256 / L;                      // at a time
+  __shared__ __align__(16) float ks[kFewKeys][D], vs[kFewKeys][D];
+  wait_for_previous_kernel();
+  release_dependents();
+  // 128 rows of one head
+  const int tiles = kp.Npad / 128;
+  const long long bh = blockIdx.x / tiles;
+  const int n0 = static_cast<int>(blockIdx.x % tiles) * 128;
+  const int b = static_cast<int>(bh / kp.H), h = static_cast<int>(bh % kp.H);
+  const int sub = threadIdx.x / L, li = threadIdx.x % L;
+  auto load8 = [](const uint16_t* at, float (&x)[8]) {
+    const uint4 w = __ldcg(reinterpret_cast<const uint4*>(at));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = FP16 ? __half22float2(*reinterpret_cast<const __half2*>(&u[e]))
+                            : make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u));
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
+    }
+  };
+  int keys = kp.Nk;
+  if (kp.kv_lens) {
+    keys = ld_l2_s32(kp.kv_lens + b);
+    if (keys < 0 || keys > kp.Nk) keys = 0;
+  }
+  const size_t kv0 = (static_cast<size_t>(b) * kp.H_kv + h / kp.group) * kp.Nk * D;
+  for (int i = threadIdx.x; i < 2 * keys * L; i += 256) {
+    const int j = i % (keys * L);
+    float x[8];
+    load8((i < keys * L ? k : v) + kv0 + 8 * j, x);
+    float4* dst = reinterpret_cast<float4*>((i < keys * L ? &ks[0][0] : &vs[0][0]) + 8 * j);
+    dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+    dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+  __syncthreads();
+  // four rows per group of L lanes, so that what is read of a key serves them all
+  for (int n1 = n0 + sub; n1 < n0 + 128; n1 += 4 * ROWS) {
+    float qr[4][8] = {}, dr[4][8] = {};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int n = n1 + r * ROWS;
+      if (n >= kp.N) continue;
+      const size_t at = (bh * kp.N + n) * D + 8 * li;
+      load8(q + at, qr[r]);
+      load8(dout + at, dr[r]);
+      float4* z = reinterpret_cast<float4*>(dq_acc + at);
+      z[0] = z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    // of the eight sums (S, dP of four rows) lane i keeps sum i mod 8, the even lanes the rows'
+    const int n = n1 + (li % 8 / 2) * ROWS;
+    const float nl = n < kp.N ? -__ldcg(lse + bh * kp.N + n) * kLog2e : -INFINITY;
+    float sum = 0.f;
+    for (int j = 0; j < keys; ++j) {
+      float x[8], y[8], w[8];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        *reinterpret_cast<float4*>(x + 4 * e) = *reinterpret_cast<const float4*>(&ks[j][8 * li + 4 * e]);
+        *reinterpret_cast<float4*>(y + 4 * e) = *reinterpret_cast<const float4*>(&vs[j][8 * li + 4 * e]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        w[2 * r] = w[2 * r + 1] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          w[2 * r] = fmaf(qr[r][e], x[e], w[2 * r]);
+          w[2 * r + 1] = fmaf(dr[r][e], y[e], w[2 * r + 1]);
+        }
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+          const float send = (li & o) ? w[i] : w[i + o], keep = (li & o) ? w[i + o] : w[i];
+          w[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+      }
+      if (L == 16) w[0] += __shfl_xor_sync(0xffffffffu, w[0], 8);
+      const float dp = __shfl_xor_sync(0xffffffffu, w[0], 1);
+      sum = fmaf(ex2_approx(fmaf(w[0], kp.scale_log2, nl)), dp, sum);
+    }
+    if (li < 8 && li % 2 == 0) {
+      // stored negated, as the other pre-pass does
+      const size_t prow = bh * kp.Npad + n;
+      delta[prow] = n < kp.N ? -sum : 0.f;
+      lse2[prow] = nl;
+    }
+  }
+}
+
 // Blocks [0, join_blocks): kJoinRows keys of a key tile each -- the sum of their partial
 // dK and dV in the order of the CTAs that left them, and zeros behind the keys.  The
 // other blocks: dQ = scale * accumulator, rounded to the 16-bit type.
@@ -739,20 +842,26 @@ attn_status_t launch_cross_bwd_t(const BwdParams& p, float* part, int ctas, cuda
   using C = BwdCfg<D>;
   const int Npad = (p.N + 127) / 128 * 128;
   const long long rows_pad = static_cast<long long>(p.B) * p.H * Npad;
-  cudaError_t e;
-  // 1. pre-pass: row vectors, dQ accumulator zeroed
-  {
-    constexpr int rows_per_block = 8 * (32 / (D / 8));
-    const long long blocks = (rows_pad + rows_per_block - 1) / rows_per_block;
-    e = launch_dependent(bwd_prep_kernel<D, FP16, false, true>, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, 0,
-                         static_cast<const uint16_t*>(p.o), static_cast<const uint16_t*>(p.dout), p.lse, p.lse2,
-                         p.delta, p.dq_acc, p.N, Npad, rows_pad, p.H, nullptr, 0);
-    if (e != cudaSuccess) return fail_cuda(e, "cross-attention backward prep launch");
-  }
   int* status = device_status_word();
   if (!status) return fail(ATTN_ERR_CUDA, "status word unavailable");
   XBwdKParams kp{p.dk, p.dv, part, p.lse2, p.delta, p.kv_lens, status, p.B, p.N, Npad, p.N_k,
                  p.H, p.H_kv, p.H / p.H_kv, p.scale, p.scale * kLog2e};
+  cudaError_t e;
+  // 1. pre-pass: row vectors, dQ accumulator zeroed
+  {
+    auto rows = [](const void* x) { return static_cast<const uint16_t*>(x); };
+    if (p.N_k <= kFewKeys) {
+      e = launch_dependent(cross_few_keys_prep_kernel<D, FP16>, dim3(static_cast<unsigned>(rows_pad / 128)), 256, 0,
+                           stream, 0, kp, rows(p.q), rows(p.k), rows(p.v), rows(p.dout), p.lse, p.lse2, p.delta, p.dq_acc);
+    } else {
+      constexpr int rows_per_block = 8 * (32 / (D / 8));
+      e = launch_dependent(bwd_prep_kernel<D, FP16, false, true>,
+                           dim3(static_cast<unsigned>((rows_pad + rows_per_block - 1) / rows_per_block)), 256, 0, stream,
+                           0, rows(p.o), rows(p.dout), p.lse, p.lse2, p.delta, p.dq_acc, p.N, Npad, rows_pad, p.H,
+                           nullptr, 0);
+    }
+    if (e != cudaSuccess) return fail_cuda(e, "cross-attention backward prep launch");
+  }
   // 2. main
   {
     auto kern = cross_bwd_kernel<D, FP16>;

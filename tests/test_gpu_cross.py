@@ -7,6 +7,8 @@ Tolerances.  u = 2^-8 (bfloat16) or 2^-11 (float16) bounds one rounding.
  dV    = sum_i P~_i dO_i, rounded:   u sum_i p_i |dO_i| + u |dV|.
  dS~   = rnd(P^ (dP - D~)), P^ to 2^-15:  p |dP - D| (u + 2^-14) + p |dD|, and D~ takes
          the rounded O:              |dD_i| <= sum_c |dO_ic| |dO-tolerance_ic|.
+         Up to 16 keys: D = sum_j P_j dP_j in float32, as dP itself; d <= 128 terms each:
+         |d(dP - D)| <= 2 (d + 2) 2^-24 |dO| |v| <= 2^-16 |dO| |v|.
  dQ    = scale sum_j dS~_j k_j, rounded:  scale sum_j |d dS_j| |k_j| + u |dQ|; dK likewise.
 float16 probabilities and dS below 2^-14 are subnormal: each is off by at most
 2^-25 more (the probabilities before the division by l >= 1).  A tenth on top
@@ -54,7 +56,11 @@ def _backward_bounds(q, k, v, do, o, o_tol, grads, scale, lens, dtype):
             p, _, _ = oracle.attention_probs(q[b, h], k[b, j, :n], scale)
             dp = do[b, h] @ v[b, j, :n].T
             gap = np.abs(dp - (do[b, h] * o[b, h]).sum(1, keepdims=True))
-            eds = (u + 2.0 ** -14) * p * gap + p * (np.abs(do[b, h]) * o_tol[b, h]).sum(1, keepdims=True) + sub * (1 + gap)
+            if k.shape[2] <= 16:
+                dD = 2.0 ** -16 * np.abs(do[b, h]) @ np.abs(v[b, j, :n]).T
+            else:
+                dD = (np.abs(do[b, h]) * o_tol[b, h]).sum(1, keepdims=True)
+            eds = (u + 2.0 ** -14) * p * gap + p * dD + sub * (1 + gap)
             tq[b, h] = scale * eds @ np.abs(k[b, j, :n])
             tk[b, j, :n] += scale * eds.T @ np.abs(q[b, h])
             tv[b, j, :n] += (u * p + sub).T @ np.abs(do[b, h])
@@ -115,6 +121,14 @@ def _check(attn, B, H, H_kv, N_q, N_k, d, dtype="bf16", lens=None, seed=900, bac
 @pytest.mark.parametrize("d", [64, 128])
 def test_lengths(attn, N_q, N_k, d):
     _check(attn, 1, 2, 2, N_q, N_k, d)
+
+
+@pytest.mark.parametrize("N_k", [1, 2, 3, 8, 15, 16, 17])
+@pytest.mark.parametrize("d,dtype", [(64, "fp16"), (128, "bf16"), (128, "fp16")])
+def test_few_keys(attn, N_k, d, dtype):
+    """Where the rounding of O would weigh most in the gradients; one, some and no keys seen."""
+    _check(attn, 2, 6, 2, 203, N_k, d, dtype, seed=905)
+    _check(attn, 3, 4, 4, 70, N_k, d, dtype, lens=[N_k, 0, (N_k + 1) // 2], seed=906)
 
 
 @pytest.mark.parametrize("H,H_kv", [(4, 1), (6, 3), (8, 2)])
