@@ -476,12 +476,15 @@ __device__ __forceinline__ float raw_amax(const Raw16& r) {
 // the amax is known (transforming twice measured 62 us against 41 for 16 K rows of 8
 // heads).  Rows of pages beyond 256 are read and transformed again, from L2.
 // Small blocks for small pages, so that an SM holds many in different phases.  8 prompts
-// of 2048 in pages of 16, 32, 64, 128: 73, 65, 66, 71 us; with a sweep as large as the page
-// allows (up to 512 threads) 81, 87, 96, 88.  256 requests that bring 3 or 60 tokens each:
-// 28 and 68.  (Clusters of such blocks for pages of 256: 91 us, one of 512 threads 78.)
+// of 2048 in pages of 16, 32, 64, 128: 65, 58, 59, 66 us; with a sweep as large as the page
+// allows (up to 512 threads) 8 to 30 us more.  256 requests that bring 3 or 60 tokens each:
+// 28 and 68.  (Clusters of such blocks for pages of 256: 13 us more than one
+// of 512 threads.)
 // Query rows are rotated by q_blocks other blocks, bound by DRAM and spread among
 // these.  One of them has to keep HBM busy beside a page's block, so its rows too come
-// through shared memory, seven heads in flight.
+// through shared memory, seven heads in flight, two neighbouring heads of a token at a
+// time (512 bytes in a piece; 2 x 8192 tokens, 32 heads: 73.4 us one by one, 68.6 so, 72.3 by fours).
+constexpr int kQHeads = 2;
 constexpr int kSweeps = 4;
 // 16-byte words of shared memory per thread: three sweeps as float32, the last one raw
 constexpr int kStagedWords = 3 * 4 + 2;
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(kF8MaxThreads, 2)
   const unsigned before_q = static_cast<unsigned>(static_cast<unsigned long long>(blockIdx.x) * q_blocks / gridDim.x);
   const unsigned with_q = static_cast<unsigned>((blockIdx.x + 1ull) * q_blocks / gridDim.x);
   if (with_q > before_q) {
-    rope_block<FP16, MODE == kNeighbours, false, 2, 7>(q, before_q % q_columns, before_q / q_columns, stage);
+    rope_block<FP16, MODE == kNeighbours, false, 2, 7, kQHeads>(q, before_q % q_columns, before_q / q_columns, stage);
     return;
   }
   const unsigned at_site = blockIdx.x - before_q;
@@ -711,7 +714,7 @@ attn_status_t launch_append_t(const AppendFp8Params& p, RopeKParams q, int page_
                                                        : both <= blocks ? kBoth : kBlocks;
   const int threads = how == kBlocks ? page_threads : kF8Threads;
   RopeGrid g{1, 0};
-  if (q.heads[0] > 0) g = rope_grid(&q, threads, how == kBlocks ? 152 * 2 : 152 * 8);
+  if (q.heads[0] > 0) g = rope_grid(&q, threads, how == kBlocks ? 152 * 2 : 152 * 8, how == kBlocks ? kQHeads : 1);
   const long long q_blocks = g.columns * g.chunks;
   const long long own = how == kBlocks ? sites : (sites + kF8Threads / 8 - 1) / (kF8Threads / 8);
   if (own + q_blocks > 2147483647LL) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");

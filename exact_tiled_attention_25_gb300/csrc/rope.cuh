@@ -95,12 +95,14 @@ __device__ __forceinline__ T load_input(const T* p) {
 // them at a time.  SLOTS > 0: rows of the first tensor (no other is given) come through
 // shared memory, SLOTS heads in flight, every thread its own 32 bytes of each; for
 // kernels that cannot give the loads registers (stage: SLOTS * 2 * blockDim words).
-template <bool FP16, bool INTERLEAVED, bool DEPENDENT, int kHeads = 4, int SLOTS = 0>
+// HL neighbouring heads of a token are rotated at a time, by as many groups of lanes.
+template <bool FP16, bool INTERLEAVED, bool DEPENDENT, int kHeads = 4, int SLOTS = 0, int HL = 1>
 __device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, int chunk, uint4* stage = nullptr) {
   const int units = p.d / 16;                       // 4, 8 or 16: divides the block
-  const int tokens = static_cast<int>(blockDim.x) / units;
+  const int tokens = static_cast<int>(blockDim.x) / units / HL;
   const int u = static_cast<int>(threadIdx.x) % units;
-  const long long tk = bx * tokens + static_cast<int>(threadIdx.x) / units;
+  const int hsub = HL > 1 ? static_cast<int>(threadIdx.x) / units % HL : 0;
+  const long long tk = bx * tokens + static_cast<int>(threadIdx.x) / units / HL;
   if (tk >= static_cast<long long>(p.B) * p.N) return;
   const long long b = tk / p.N, n = tk - b * p.N;
   bool turn = p.rotated > 0 && 16 * u < p.rot;
@@ -163,19 +165,20 @@ __device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, i
   int before = 0;                                   // heads of the tensors before
 #pragma unroll
   for (int t = 0; t < 3; ++t) {
-    const int h0 = max(lo - before, 0), h1 = min(hi - before, p.heads[t]);
+    const int h0 = max(lo - before, 0) + hsub, h1 = min(hi - before, p.heads[t]);
     before += p.heads[t];
     if (h0 >= h1 || (p.slots && t > 0 && slot < 0)) continue;
+    const int nh = (h1 - h0 + HL - 1) / HL;          // heads h0, h0 + HL, ... of this thread
     const bool rotate = turn && t < p.rotated;
     const uint16_t* in = p.src[t] + b * p.sb[t] + n * p.st[t] + h0 * p.sh[t];
     const bool cache = p.slots && t > 0;
     uint16_t* out = cache ? p.dst[t] + (slot * p.heads[1] + h0) * p.d
                           : p.dst[t] + b * p.db[t] + n * p.dt[t] + h0 * p.dh[t];
-    const long long step_in = p.sh[t], step_out = cache ? p.d : p.dh[t];
+    const long long step_in = p.sh[t] * HL, step_out = (cache ? p.d : p.dh[t]) * HL;
     if constexpr (SLOTS > 0) {
       const int words = static_cast<int>(blockDim.x);
       auto copy = [&](int k) {
-        if (h0 + k < h1) {
+        if (k < nh) {
           uint4* dst = stage + (k % SLOTS) * 2 * words + threadIdx.x;
           copy16_async(dst, in + k * step_in + off_a, true);
           copy16_async(dst + words, in + k * step_in + off_b, true);
@@ -184,7 +187,7 @@ __device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, i
       };
 #pragma unroll
       for (int k = 0; k < SLOTS; ++k) copy(k);
-      for (int k = 0; k < h1 - h0; ++k) {
+      for (int k = 0; k < nh; ++k) {
         copies_wait<SLOTS - 1>();
         const uint4* src = stage + (k % SLOTS) * 2 * words + threadIdx.x;
         uint4 va = src[0], vb = src[words];
@@ -195,18 +198,18 @@ __device__ __forceinline__ void rope_block(const RopeKParams& p, long long bx, i
       }
       copies_wait<0>();
     } else {
-      for (int h = h0; h < h1; h += kHeads) {
+      for (int k = 0; k < nh; k += kHeads) {
         uint4 va[kHeads], vb[kHeads];
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) {
-          if (h + i >= h1) break;
+          if (k + i >= nh) break;
           va[i] = load_input<DEPENDENT>(reinterpret_cast<const uint4*>(in + i * step_in + off_a));
           vb[i] = load_input<DEPENDENT>(reinterpret_cast<const uint4*>(in + i * step_in + off_b));
         }
         in += kHeads * step_in;
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) {
-          if (h + i >= h1) break;
+          if (k + i >= nh) break;
           if (rotate) rotate16<FP16, INTERLEAVED>(va[i], vb[i], cc, ss, ns);
           *reinterpret_cast<uint4*>(out + i * step_out + off_a) = va[i];
           *reinterpret_cast<uint4*>(out + i * step_out + off_b) = vb[i];
@@ -223,8 +226,8 @@ struct RopeGrid {
   long long columns;
   int chunks;
 };
-inline RopeGrid rope_grid(RopeKParams* p, int threads = kRopeThreads, int least_blocks = 152 * 8) {
-  const int tokens = threads / (p->d / 16);
+inline RopeGrid rope_grid(RopeKParams* p, int threads = kRopeThreads, int least_blocks = 152 * 8, int head_lanes = 1) {
+  const int tokens = threads / (p->d / 16) / head_lanes;
   RopeGrid g;
   g.columns = (static_cast<long long>(p->B) * p->N + tokens - 1) / tokens;
   const int all = p->heads[0] + p->heads[1] + p->heads[2];
