@@ -15,8 +15,12 @@ namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925;
 
-template <bool FP16, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeKParams p) {
+// PER_SM: blocks that an SM is to hold.  Three (80 registers, a few spilled; three or two
+// heads at a time need none and are slower) where there are more than 2 x 152 blocks: 53.8
+// -> 52.3 us for 2 x 8192 tokens of 40 heads, d = 128; two (102) otherwise, for a step of 64
+// requests 2.8 us, 3.0 with three.
+template <bool FP16, bool INTERLEAVED, int PER_SM>
+__global__ void __launch_bounds__(kRopeThreads, PER_SM) rope_kernel(const RopeKParams p) {
   wait_for_previous_kernel();      // a dependent launch: its start overlaps that one's end
   rope_block<FP16, INTERLEAVED, true>(p, blockIdx.x, blockIdx.y);
 }
@@ -101,8 +105,12 @@ attn_status_t launch_rope(RopeKParams p, int fp16, int interleaved, cudaStream_t
   if (g.columns > 2147483647LL || g.chunks > 65535)
     return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
   const dim3 grid(static_cast<unsigned>(g.columns), g.chunks);
-  auto kern = fp16 ? interleaved ? rope_kernel<true, true> : rope_kernel<true, false>
-                   : interleaved ? rope_kernel<false, true> : rope_kernel<false, false>;
+  const bool many = g.columns * g.chunks > 2 * 152;
+  auto pick = [&](auto three, auto two) { return many ? three : two; };
+  auto kern = fp16 ? interleaved ? pick(rope_kernel<true, true, 3>, rope_kernel<true, true, 2>)
+                                 : pick(rope_kernel<true, false, 3>, rope_kernel<true, false, 2>)
+                   : interleaved ? pick(rope_kernel<false, true, 3>, rope_kernel<false, true, 2>)
+                                 : pick(rope_kernel<false, false, 3>, rope_kernel<false, false, 2>);
   const cudaError_t e = launch_dependent(kern, grid, kRopeThreads, 0, stream, 0, p);
   if (e != cudaSuccess) return fail_cuda(e, "rotary kernel launch");
   return ATTN_OK;
