@@ -191,13 +191,19 @@ float scale_of(PyObject* o, int d) {
 attn_dtype_t dtype_of(const at::Tensor& t) { return t.scalar_type() == at::kHalf ? ATTN_FP16 : ATTN_BF16; }
 bool is16(const at::Tensor& t) { return t.scalar_type() == at::kHalf || t.scalar_type() == at::kBFloat16; }
 
-// Run a C entry point without the interpreter's lock; a status other than 0 raises.
+// Run a C entry point without the interpreter's lock; a status other than 0 raises.  The
+// lock is held again before an exception of f (a dimension out of range) leaves.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 template <typename F>
 void call(const char* name, F f) {
   attn_status_t s;
-  Py_BEGIN_ALLOW_THREADS
-  s = f();
-  Py_END_ALLOW_THREADS
+  {
+    const Unlocked unlocked;
+    s = f();
+  }
   if (s == ATTN_OK) return;
   PyObject* r = PyObject_CallFunction(on_error, "is", static_cast<int>(s), name);
   Py_XDECREF(r);

@@ -515,3 +515,18 @@ def test_training_layer(attn):
     # each link rounds its inputs to bfloat16 once more: four roundings' worth
     for x, r in zip((dq, dk, dv, dek, dev_), refs):
         assert rel_rmse(x, r) <= 4 * GRAD_REL_RMSE
+
+
+def test_dimensions_past_32_bits_are_refused(attn):
+    """Found only when the call's arguments are narrowed: a ValueError, and the interpreter goes on."""
+    k = torch.zeros(1, 2, 128, device=dev()).bfloat16()
+    kc = torch.empty(2 ** 31, 0, 2, 128, dtype=torch.bfloat16, device=dev())
+    slots = torch.zeros(1, dtype=torch.int64, device=dev())
+    with pytest.raises(ValueError, match="dimension"):
+        attn.attn_cache_append(k, k, kc, kc, slots)
+    desc = torch.empty(1, 0, device=dev())
+    kc8 = torch.empty(1, 2 ** 31, 0, 128, dtype=torch.uint8, device=dev())
+    none = torch.empty(1, 0, 128, device=dev()).bfloat16()
+    with pytest.raises(ValueError, match="dimension"):
+        attn.attn_cache_append_fp8(none, none, kc8, kc8, desc, desc, _i32([[0]]), _i32([1]), _i32([0, 1]))
+    check_status(attn)
