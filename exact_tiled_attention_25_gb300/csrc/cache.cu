@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(kTabThreads)
 // keys or values), the page's new rows are rotated and transformed (keys); their
 // amax gives
 //   descale' = max(descale, amax / 448)       (a page whose first token is among
-//                                              the new ones starts from 0),
+//                                              the new ones starts from 0; at least
+//                                              2^-90, and 1 where all is 0),
 // codes = e4m3_rn_satfinite(x / descale'); when the descale grows, the codes of
 // the page's older tokens become e4m3_rn(code * (descale / descale')); the
 // unused rest of a page that starts here is cleared, so the decode never meets
@@ -400,9 +401,15 @@ __device__ __forceinline__ float amax16(const float (&x)[16]) {
   return m;
 }
 
+// The least descale of a page that holds anything but zeros, 2^-90.  1 / descale and the
+// quotients' residuals stay normal float32 numbers (from amax = 1.3e-36 down 1 / descale was
+// infinite, and every code NaN), and so do the decode's sums of p / descale over any number of
+// keys.  What it costs: values are off by up to 2^-100.
+constexpr float kMinPageDescale = 0x1p-90f;
+
 __device__ __forceinline__ float new_descale(float before, float amax) {
   const float after = fmaxf(before, __fdiv_rn(amax, 448.f));
-  return after == 0.f ? 1.f : after;
+  return after == 0.f ? 1.f : fmaxf(after, kMinPageDescale);
 }
 
 // Codes of a row, with the quotients rounded as divisions by `after`.

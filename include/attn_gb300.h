@@ -735,11 +735,12 @@ attn_status_t attn_cache_append(const void* q, void* q_out, const void* k, const
  *                 positions.  attn_block_tables writes all three.  A page that
  *                 receives tokens belongs to one request.
  *   For a page and head with new rows x:  descale' = max(descale, amax|x| / 448), the
- *   old descale counting as 0 when the page's first token is among the new ones, and 1
- *   if all is 0;  code = e4m3_rn_satfinite(x / descale').  When the descale grows,
- *   codes of the page's earlier tokens become e4m3_rn(code * (descale / descale')),
- *   one more rounding each time.  The rest of a page that starts here is cleared
- *   to 0; rows behind the new tokens of other pages are left as they are.
+ *   old descale counting as 0 when the page's first token is among the new ones, at
+ *   least 2^-90, and 1 if all is 0;  code = e4m3_rn_satfinite(x / descale').  When the
+ *   descale grows, codes of the page's earlier tokens become
+ *   e4m3_rn(code * (descale / descale')), one more rounding each time.  The rest of a
+ *   page that starts here is cleared to 0; rows behind the new tokens of other pages
+ *   are left as they are.
  *   Values are expected finite.
  * Requests that do not fit (offsets, lengths, pages out of range) are skipped and
  * reported by attn_get_device_status() as ATTN_ERR_INVALID_ARG; keys at or past

@@ -131,7 +131,8 @@ def append_fp8(x, codes, descale, slots):
         for h in range(codes.shape[2]):
             before = np.float32(0.0) if off.min() == 0 else descale[p, h]
             after = max(before, np.float32(np.abs(x[rows, h]).max()) / np.float32(E4M3_MAX))
-            after = after if after > 0 else np.float32(1.0)
+            # a descale of 2^-90 at least, where there is anything but zeros
+            after = max(after, np.float32(2.0 ** -90)) if after > 0 else np.float32(1.0)
             if off.min() == 0:
                 codes[p, :, h] = 0
             elif after > before:

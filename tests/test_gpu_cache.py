@@ -530,3 +530,51 @@ def test_dimensions_past_32_bits_are_refused(attn):
     with pytest.raises(ValueError, match="dimension"):
         attn.attn_cache_append_fp8(none, none, kc8, kc8, desc, desc, _i32([[0]]), _i32([1]), _i32([0, 1]))
     check_status(attn)
+
+
+@pytest.mark.parametrize("size", [1e-24, 1e-30, 1e-37, 2e-40])
+@pytest.mark.parametrize("new", [[1, 3, 0, 2], [300, 5, 70, 16]])
+@pytest.mark.parametrize("signs", [False, True])
+def test_append_fp8_tiny_values(attn, size, new, signs):
+    """bfloat16 rows down to subnormal ones, zeros among them, on fresh pages and behind old
+    tokens: codes and descales of the rule (2^-90 at least), exact without the transform up to the
+    sign of zeros, and a decode over them that stays finite."""
+    H, H_kv, d, page = 4, 2, 128, 64
+    old = [0, 0, 30, 64]
+    bt, (lens, cu, slots, _, _), num, q, k, v = _step(attn, 90, old, new, page, H, H_kv, d, torch.bfloat16)
+    k, v = ((t.double() * size).bfloat16() for t in (k, v))
+    k[::2, :, 5], v[1::3] = 0, 0
+    assert k.any() and v.any()
+    at, sg = slots.cpu().numpy(), _signs() if signs else None
+    rows = (oracle.key_rows(k.double().cpu().numpy(), None, None, None, False, sg.cpu().numpy() if signs else None),
+            v.double().cpu().numpy())
+    # old tokens of one request as tiny, of the other of ordinary size
+    tiny = np.float32(size)
+    state = []
+    for i, x in enumerate(rows):
+        codes, desc = _random_cache(91 + i, num, page, H_kv)
+        if new[2]:
+            desc[bt[2, 0].item()] = tiny
+        c, s = torch.from_numpy(codes).to(dev()), torch.from_numpy(desc).to(dev())
+        state.append((c, s, *oracle.append_fp8(x, codes, desc, at), x, codes))
+    (kc, ks, *_), (vc, vs, *_) = state
+    attn.attn_cache_append_fp8(k, v, kc, vc, ks, vs, bt, lens, cu, hadamard_signs=sg)
+    check_status(attn)
+    for (c, s, ref_c, ref_s, x, codes), plain in zip(state, (not signs, True)):
+        got_c, got_s = c.cpu().numpy(), s.cpu().numpy()
+        if plain:
+            assert np.array_equal(oracle.e4m3_decode(got_c), oracle.e4m3_decode(ref_c)) and np.array_equal(got_s, ref_s)
+            continue
+        # as in test_append_fp8: float32 rows off by 2^-20 of their length, and 2^-140 where subnormal
+        assert np.all(np.abs(got_s - ref_s) <= 2.0 ** -19 * ref_s)
+        val = oracle.e4m3_decode(got_c.reshape(-1, H_kv, d)[at]) * got_s[at // page][:, :, None].astype(np.float64)
+        length = np.linalg.norm(x, axis=2, keepdims=True)
+        tol = np.maximum(np.abs(x) * 2.0 ** -4, 2.0 ** -10 * got_s[at // page][:, :, None]) * (1 + 2.0 ** -10)
+        assert np.all(np.abs(val - x) <= tol + 2.0 ** -19 * length + 2.0 ** -140)
+    o, lse = attn.attn_decode_paged_fp8(q[:4].reshape(4, H, 1, d).contiguous(), kc, vc, ks, vs, bt, lens, int(lens.max()),
+                                        hadamard_signs=sg)
+    check_status(attn)
+    seen = lens.cpu().numpy() > 0
+    assert torch.isfinite(o.float()).all() and torch.isfinite(lse[torch.from_numpy(seen).to(dev())]).all()
+    for p in np.unique(at // page):
+        assert not np.isnan(oracle.e4m3_decode(kc[p].cpu().numpy())).any()

@@ -141,3 +141,16 @@ def test_append_fp8_growing_descale():
         bound = grew * np.maximum(np.abs(x[:t + 1, 0]) * 2.0 ** -4, 2.0 ** -10 * desc[0, 0]) * 1.1
         assert np.all(np.abs(value - x[:t + 1, 0]) <= bound)
     assert grew >= 2
+
+
+@pytest.mark.parametrize("size", [1e-20, 1e-25, 1e-30, 1e-37, 1e-40])
+def test_append_fp8_of_tiny_values(size):
+    """A descale of 2^-90 at least: values within half a step of it, zeros exact."""
+    x = (_normal(7, 16, 2, 8) * size).astype(np.float32)
+    x[3], x[:, 1, 2] = 0, 0
+    codes, desc = oracle.append_fp8(x, np.full((1, 16, 2, 8), 0x7F, np.uint8), np.full((1, 2), np.nan, np.float32),
+                                    np.arange(16))
+    assert np.all(desc >= 2.0 ** -90) and np.all(desc <= max(2.0 ** -90, np.abs(x).max()))
+    value = oracle.e4m3_decode(codes[0]) * desc[0][:, None]
+    assert np.all(np.abs(value - x) <= np.maximum(np.abs(x) * 2.0 ** -4, 2.0 ** -10 * desc[0][:, None]))
+    assert not value[3].any() and not value[:, 1, 2].any()
