@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(Dec8Cfg::THREADS, 1)
       // descale = amax / 448 and code = e4m3(x / descale) with x / descale
       // rounded as an IEEE float32 division (the block quantiser's rule): one
       // division for y = RN(1 / dq), then a corrected product per value.
-      const float dq = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+      const float dq = e4m3_descale(amax);
       const float y = __fdiv_rn(1.f, dq);
       auto quot = [&](float v) -> float { return div_by_recip(v, dq, y); };
       c_q = kp.scale_log2 * dq;
@@ -1292,7 +1292,7 @@ __global__ void __launch_bounds__(Dec8TCfg<CW>::THREADS, 1)
         const bool real = qn < kp.rows_real;
         // descale = amax / 448, code = e4m3(x / descale) with the quotient
         // rounded as an IEEE float32 division (the block quantiser's rule)
-        const float dq = (real && am > 0.f) ? __fdiv_rn(am, 448.f) : 1.f;
+        const float dq = real ? e4m3_descale(am) : 1.f;
         const float yq = __fdiv_rn(1.f, dq);
         uint32_t wq[4];
 #pragma unroll

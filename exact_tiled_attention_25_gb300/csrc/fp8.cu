@@ -31,7 +31,6 @@ namespace attn {
 namespace {
 
 constexpr int kSmemLimit = 232448;
-constexpr float kE4m3Max = 448.f;
 
 // ============================================================== pre-pass ====
 // Mode: 0 = fused block mode (amax + quantise), 1 = block amax only (into
@@ -175,7 +174,7 @@ __global__ void __launch_bounds__(256)
       if (threadIdx.x == 0) desc[static_cast<size_t>(bh) * nblk + blk] = bmax;
       return;
     }
-    descale = bmax > 0.f ? __fdiv_rn(bmax, kE4m3Max) : 1.f;
+    descale = e4m3_descale(bmax);
     if (threadIdx.x == 0) desc[static_cast<size_t>(bh) * nblk + blk] = descale;
   }
   const float rdesc = __fdiv_rn(1.f, descale);
@@ -303,7 +302,7 @@ __global__ void __launch_bounds__(256)
       if (threadIdx.x == 0) desc[static_cast<size_t>(bh) * nblk + blk] = bmax;
       return;
     }
-    descale = bmax > 0.f ? __fdiv_rn(bmax, kE4m3Max) : 1.f;
+    descale = e4m3_descale(bmax);
     if (threadIdx.x == 0) desc[static_cast<size_t>(bh) * nblk + blk] = descale;
   }
   const float rdesc = __fdiv_rn(1.f, descale);
@@ -336,7 +335,7 @@ __global__ void __launch_bounds__(256)
   float gmax = warp_max[0];
 #pragma unroll
   for (int w = 1; w < 8; ++w) gmax = fmaxf(gmax, warp_max[w]);
-  const float descale = gmax > 0.f ? __fdiv_rn(gmax, kE4m3Max) : 1.f;
+  const float descale = e4m3_descale(gmax);
   __syncthreads();
   for (long long i = threadIdx.x; i < count; i += blockDim.x) desc[i] = descale;
 }

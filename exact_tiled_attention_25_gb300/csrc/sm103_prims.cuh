@@ -574,6 +574,13 @@ __device__ __forceinline__ float div_by_recip(float x, float b, float y) {
   return fmaf(fmaf(-b, q0, x), y, q0);
 }
 
+// Scale of values whose largest magnitude is amax, held as e4m3 codes: amax / 448, and 1 if
+// all are 0.  At least 2^-126: div_by_recip needs a normal divisor (1 / descale is infinite
+// below 2^-128).
+__device__ __forceinline__ float e4m3_descale(float amax) {
+  return amax > 0.f ? fmaxf(__fdiv_rn(amax, 448.f), 0x1p-126f) : 1.f;
+}
+
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float m;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));

@@ -351,8 +351,8 @@ attn_status_t attn_decode_paged_fp8(const void* q, const uint8_t* k_cache, const
  *                    forward needs no knowledge of the transform.
  *   q8, k8, v8     : [B, H, N, d] e4m3 bytes (written).
  *   q_descale, k_descale, v_descale : [B, H, ceil(N/128)] float32 (written):
- *                    per 128-row block, descale = amax / 448 (1 if amax = 0) and
- *                    code = e4m3_rn_satfinite(x / descale).
+ *                    per 128-row block, descale = amax / 448 (at least 2^-126,
+ *                    1 if amax = 0) and code = e4m3_rn_satfinite(x / descale).
  *   per_tensor     : 0 = one scale per block; 1 = one scale per whole tensor (all
  *                    b, h, rows; every descale entry holds it) -- the per-tensor
  *                    comparator; hadamard_signs must then be NULL.

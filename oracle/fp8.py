@@ -19,7 +19,8 @@ subnormals are m/8 * 2^-6 (down to 2^-9).
 Readings where the pages are silent (each one is listed in the design notes):
 * A block is one (b, h) head and 128 consecutive rows, over all d columns.
   One scale per block fits one descale per tile of the score contraction.
-* descale = float32(amax) / 448 in float32; amax = 0 gives descale = 1.
+* descale = float32(amax) / 448 in float32, at least 2^-126 (a subnormal scale
+  has no finite reciprocal); amax = 0 gives descale = 1.
 * code = e4m3(round-to-nearest-even(x / descale)), with x / descale an
   IEEE float32 division and magnitudes >= 448 saturated to 448.
 * M = diag(s) H_d / sqrt(d): s is one +-1 vector shared by Q and K and by all
@@ -115,7 +116,8 @@ def quantize_e4m3_blocks(x, block_rows: int = 128, per_tensor: bool = False,
     Steps, in order: optional rotary embedding (rope = (cos, sin) tables) and
     incoherent transform (float64, then rounded to float32, the precision the
     GPU pre-pass holds its values in); amax per
-    block (or per tensor); descale = amax / 448 in float32 (1 when amax is 0);
+    block (or per tensor); descale = amax / 448 in float32 (at least 2^-126, 1
+    when amax is 0);
     code = e4m3(x / descale) with a float32 division.
 
     Returns (codes uint8 [B, H, N, d], descale float32 [B, H, ceil(N/block_rows)]).
@@ -136,7 +138,8 @@ def quantize_e4m3_blocks(x, block_rows: int = 128, per_tensor: bool = False,
     else:
         padded = np.concatenate([absx, np.zeros((B, H, pad, d), np.float32)], axis=2)
         amax = padded.reshape(B, H, nblk, block_rows * d).max(axis=3).astype(np.float32)
-    descale = np.where(amax > 0, amax / np.float32(E4M3_MAX), np.float32(1.0)).astype(np.float32)
+    descale = np.where(amax > 0, np.maximum(amax / np.float32(E4M3_MAX), np.float32(2.0 ** -126)),
+                       np.float32(1.0)).astype(np.float32)
     rows_descale = np.repeat(descale, block_rows, axis=2)[:, :, :N, None]
     scaled = (x / rows_descale).astype(np.float32)           # IEEE float32 division
     return e4m3_encode(scaled), descale

@@ -186,3 +186,22 @@ def test_bad_page_is_reported(attn):
     torch.cuda.synchronize()
     assert attn.attn_get_device_status() == attn.ATTN_ERR_INVALID_ARG
     assert attn.attn_get_device_status() == 0
+
+
+@pytest.mark.parametrize("H,H_kv", [(2, 2), (8, 1), (64, 1)])
+@pytest.mark.parametrize("size", [1e-36, 1e-37, 2e-40])
+def test_tiny_queries(attn, H, H_kv, size):
+    """Query rows whose own descale would be subnormal: the mean of the values."""
+    lens = [300, 64]
+    kc, vc, table = _cache(90, lens, 64, H_kv)
+    k8, kd = oracle.quantize_paged_cache(kc)
+    v8, vd = oracle.quantize_paged_cache(vc)
+    q = torch.from_numpy((workloads.normal(91, (2, H, 1, D)) * size).astype(np.float32)).bfloat16()
+    assert q.any()
+    o, lse = attn.attn_decode_paged_fp8(q.to(dev()), *(torch.from_numpy(np.ascontiguousarray(x)).to(dev())
+                                                       for x in (k8, v8, kd, vd, table.astype(np.int32))),
+                                        torch.tensor(lens, dtype=torch.int32, device=dev()), 300)
+    check_status(attn)
+    ref, rl = oracle.attention_decode_paged_fp8(q.double().numpy(), k8, v8, kd, vd, table, np.array(lens), D ** -0.5, True)
+    assert np.sqrt(np.mean((o.double().cpu().numpy() - ref) ** 2)) <= FP8_RMSE
+    assert np.abs(lse.double().cpu().numpy() - rl).max() <= 1e-3

@@ -319,3 +319,59 @@ def test_fp8_exp2_poly_variant_matches_dequantised_oracle(attn, N, causal, eight
     np.testing.assert_allclose(lse.cpu().numpy(), ref_l, atol=2e-3)
     # and close to the MUFU-only forward
     assert (o.float() - o0.float()).pow(2).mean().sqrt().item() <= 2e-3
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-36, 1e-37, 1e-41])
+@pytest.mark.parametrize("per_tensor", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_quantiser_of_tiny_values(attn, size, per_tensor, bf16):
+    """Blocks whose amax / 448 is subnormal, zeros among them: a descale of 2^-126, finite codes,
+    equal to the oracle's up to the sign of zeros (1e-30: as ever)."""
+    shape = (1, 2, 300, 128)
+    xs = [(x * size).astype(np.float32) for x in workloads.normal(12, shape, 3)]
+    if bf16:
+        xs = [torch.from_numpy(x).bfloat16().float().numpy() for x in xs]
+    for x in xs:
+        x[0, 0, ::3], x[0, 1, 128:256] = 0, 0
+    if bf16:
+        codes, desc = attn.attn_fp8_quantize_bf16(*(torch.from_numpy(x).bfloat16().to(dev()) for x in xs),
+                                                  per_tensor=per_tensor)
+        check_status(attn)
+        codes, desc = [c.cpu().numpy() for c in codes], [d.cpu().numpy() for d in desc]
+    else:
+        codes, desc = _quant(attn, xs, per_tensor=per_tensor)
+    for x, c, d in zip(xs, codes, desc):
+        rc, rd = oracle.quantize_e4m3_blocks(x, per_tensor=per_tensor)
+        np.testing.assert_array_equal(d, rd)
+        np.testing.assert_array_equal(oracle.e4m3_decode(c), oracle.e4m3_decode(rc))
+
+
+@pytest.mark.parametrize("rope", [False, True])
+def test_transformed_tiny_values(attn, rope):
+    """The same through the transform, and the rotation's staged kernel: finite, zero rows zero, and
+    within half a step (2^-136 at descales of 2^-126), the transform's float32 error and 2^-140."""
+    B, H, N, d = 1, 2, 200, 128
+    xs = [(x * 1e-37).astype(np.float32) for x in workloads.normal(13, (B, H, N, d), 3)]
+    for x in xs:
+        x[0, 0, 7] = 0
+    signs = workloads.random_signs(5, d)
+    cos, sin = workloads.rope_tables(N, d)
+    g = [torch.from_numpy(x).to(dev()) for x in xs]
+    sg = torch.from_numpy(signs).to(dev())
+    if rope:
+        codes, desc = attn.attn_fp8_quantize_rope(*g, torch.from_numpy(cos).to(dev()), torch.from_numpy(sin).to(dev()),
+                                                  hadamard_signs=sg)
+    else:
+        codes, desc = attn.attn_fp8_quantize(*g, hadamard_signs=sg)
+    check_status(attn)
+    for which, (x, c, s) in enumerate(zip(xs, codes, desc)):
+        y = x.astype(np.float64)
+        if which < 2:
+            y = oracle.incoherent_transform(oracle.rotary_embed(y, cos, sin) if rope else y, signs)
+        s = s.cpu().numpy()
+        assert np.all(s == np.float32(2.0 ** -126))
+        val = oracle.dequantize_e4m3_blocks(c.cpu().numpy(), s)
+        tol = np.maximum(np.abs(y) * 2.0 ** -4, 2.0 ** -136) * (1 + 2.0 ** -10)
+        tol += 2.0 ** -19 * np.linalg.norm(y, axis=3, keepdims=True) + 2.0 ** -140
+        assert np.all(np.abs(val - y) <= tol)
+        assert not val[0, 0, 7].any()

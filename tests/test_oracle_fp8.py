@@ -136,3 +136,12 @@ def test_fp8_error_ordering_on_outlier_workload():
     r_had = rmse_for(False, s)
     assert r_had < r_block < r_tensor, (r_had, r_block, r_tensor)
     assert r_had < 3e-2
+
+
+def test_tiny_blocks_have_a_normal_descale():
+    x = (np.random.default_rng(3).standard_normal((1, 1, 200, 8)) * 1e-37).astype(np.float32)
+    x[0, 0, 128:] *= np.float32(1e-4)
+    codes, desc = oracle.quantize_e4m3_blocks(x)
+    assert np.all(desc == np.float32(2.0 ** -126))
+    assert np.all(np.abs(oracle.dequantize_e4m3_blocks(codes, desc) - x) <=
+                  np.maximum(np.abs(x) * 2.0 ** -4, 2.0 ** -136))
