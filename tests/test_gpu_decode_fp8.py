@@ -205,3 +205,22 @@ def test_tiny_queries(attn, H, H_kv, size):
     ref, rl = oracle.attention_decode_paged_fp8(q.double().numpy(), k8, v8, kd, vd, table, np.array(lens), D ** -0.5, True)
     assert np.sqrt(np.mean((o.double().cpu().numpy() - ref) ** 2)) <= FP8_RMSE
     assert np.abs(lse.double().cpu().numpy() - rl).max() <= 1e-3
+
+
+@pytest.mark.parametrize("H,H_kv,n_q", [(2, 2, 1), (8, 1, 1), (64, 1, 1), (16, 1, 4)])
+@pytest.mark.parametrize("size", [1e-24, 1e-37])
+def test_tiny_queries_and_keys(attn, H, H_kv, n_q, size):
+    """Products of query and key descales below float32's range, with masked keys in a tile."""
+    lens = [300, 70]
+    kc, vc, table = _cache(92, lens, 64, H_kv)
+    k8, _ = oracle.quantize_paged_cache(kc)
+    kd = np.full((kc.shape[0], H_kv), 2.0 ** -90, np.float32)
+    v8, vd = oracle.quantize_paged_cache(vc)
+    q = torch.from_numpy((workloads.normal(93, (2, H, n_q, D)) * size).astype(np.float32)).bfloat16()
+    o, lse = attn.attn_decode_paged_fp8(q.to(dev()), *(torch.from_numpy(np.ascontiguousarray(x)).to(dev())
+                                                       for x in (k8, v8, kd, vd, table.astype(np.int32))),
+                                        torch.tensor(lens, dtype=torch.int32, device=dev()), 300)
+    check_status(attn)
+    ref, rl = oracle.attention_decode_paged_fp8(q.double().numpy(), k8, v8, kd, vd, table, np.array(lens), D ** -0.5, True)
+    assert np.sqrt(np.mean((o.double().cpu().numpy() - ref) ** 2)) <= FP8_RMSE
+    assert np.abs(lse.double().cpu().numpy() - rl).max() <= 1e-3

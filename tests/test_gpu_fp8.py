@@ -375,3 +375,18 @@ def test_transformed_tiny_values(attn, rope):
         tol += 2.0 ** -19 * np.linalg.norm(y, axis=3, keepdims=True) + 2.0 ** -140
         assert np.all(np.abs(val - y) <= tol)
         assert not val[0, 0, 7].any()
+
+
+@pytest.mark.parametrize("N,causal", [(300, False), (256, True), (130, True)])
+@pytest.mark.parametrize("size", [1e-25, 1e-37])
+def test_forward_of_tiny_scores(attn, N, causal, size):
+    """Products of query and key descales below float32's range, with masked keys in a tile: all
+    seen scores are 0 to float32, so O is the mean of the seen values."""
+    xs = workloads.normal(14, (1, 2, N, 128), 3)
+    xs = [(x * (size if i < 2 else 1.0)).astype(np.float32) for i, x in enumerate(xs)]
+    (o, lse), (q8, k8, v8, qd, kd, vd) = _fp8_forward(attn, *xs, None, False, causal)
+    v = oracle.dequantize_e4m3_blocks(v8, vd)
+    zero = np.zeros_like(v)
+    ref, rl = oracle.attention_forward(zero, zero, v, 128 ** -0.5, causal)
+    assert np.sqrt(np.mean((o.double().cpu().numpy() - ref) ** 2)) <= FP8_RMSE
+    assert np.abs(lse.double().cpu().numpy() - rl).max() <= 1e-3
