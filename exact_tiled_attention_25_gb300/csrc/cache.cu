@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(kTabThreads)
   };
   const int step = gridDim.x * kTabThreads;
   const int me = blockIdx.x * kTabThreads + threadIdx.x;
+  bool lost = false;                 // a new token whose page the table or the free list lacks
   for (long long t = me; t < p.capacity; t += step) {
     long long slot = -1;
     int pos = -1;
@@ -138,10 +139,12 @@ __global__ void __launch_bounds__(kTabThreads)
         phys = e < p.n_free ? __ldcg(p.free_pages + e) : -1;
       }
       if (phys >= 0) slot = static_cast<long long>(phys) * page + (pos & (page - 1));
+      else lost = true;
     }
     p.slots[t] = slot;
     p.positions[t] = pos;
   }
+  if (lost) atomicCAS(status, 0, kDevBadTables);
   for (long long e = me; e < pages_all; e += step) {
     const int b = owner(pg, static_cast<int>(e));
     p.block_table[static_cast<size_t>(b) * p.max_pages + pages_of(old_sh[b]) + (e - pg[b])] =

@@ -682,9 +682,12 @@ attn_status_t attn_rope(const void* q, void* q_out, const void* k, void* k_out, 
  *   used        : int32 [1] (written) free pages taken.
  * A request whose lengths are negative or exceed max_pages * page_size adds nothing
  * (its seq_lens is old_lens, or 0 if that is out of range); pages that free_pages
- * cannot give become -1 in the table, with slots -1; tokens past `capacity` are
- * left out of slots and positions.  All are reported by attn_get_device_status()
- * as ATTN_ERR_INVALID_ARG.
+ * cannot give become -1 in the table; new tokens on a page whose entry is negative
+ * (one that could not be given, in this step or an earlier one, or a negative entry of
+ * free_pages) get slot -1; tokens past `capacity` are left out of slots and positions.
+ * All are reported by attn_get_device_status() as ATTN_ERR_INVALID_ARG.  seq_lens
+ * counts tokens of slot -1 too, so after such a step a request's next old_lens is what
+ * was placed of it, not its seq_lens.
  * No output overlaps old_lens, new_lens or free_pages.
  * page_size a power of two in [8, 65536]; B <= 16384; capacity may be 0.
  * Source: the block table of attn_decode_paged ("FlashAttention 3 Hardware

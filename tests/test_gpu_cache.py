@@ -578,3 +578,26 @@ def test_append_fp8_tiny_values(attn, size, new, signs):
     assert torch.isfinite(o.float()).all() and torch.isfinite(lse[torch.from_numpy(seen).to(dev())]).all()
     for p in np.unique(at // page):
         assert not np.isnan(oracle.e4m3_decode(kc[p].cpu().numpy())).any()
+
+
+def test_tables_report_tokens_on_missing_pages(attn):
+    """After a step that ran out of pages: its seq_lens fed back with new pages at hand put the next
+    tokens on the page that was never given; a negative free page does so too.  Slots -1, reported;
+    with the placed lengths fed back everything fits."""
+    bt = _i32([[3, -1, -1, -1], [-1, -1, -1, -1]])
+    lens, *_ = attn.attn_block_tables(bt, _i32([10, 0]), _i32([10, 20]), _i32([5]), 16, 30)
+    assert attn.attn_get_device_status() == attn.ATTN_ERR_INVALID_ARG
+    assert bt.tolist() == [[3, 5, -1, -1], [-1, -1, -1, -1]] and lens.tolist() == [20, 20]
+    again = bt.clone()
+    _, _, slots, pos, used = attn.attn_block_tables(again, lens, _i32([1, 1]), _i32([7, 8]), 16, 2)
+    assert attn.attn_get_device_status() == attn.ATTN_ERR_INVALID_ARG
+    assert slots.tolist() == [5 * 16 + 4, -1] and pos.tolist() == [20, 20] and used.item() == 0
+    _, _, slots, _, used = attn.attn_block_tables(bt, _i32([20, 0]), _i32([1, 20]), _i32([7, 8]), 16, 21)
+    check_status(attn)
+    assert slots.tolist() == [84] + list(range(7 * 16, 8 * 16)) + list(range(8 * 16, 8 * 16 + 4)) and used.item() == 2
+    _, _, slots, _, used = attn.attn_block_tables(_i32([[-1, -1]]), _i32([0]), _i32([17]), _i32([4, -6]), 16, 17)
+    assert attn.attn_get_device_status() == attn.ATTN_ERR_INVALID_ARG
+    assert slots.tolist() == list(range(64, 80)) + [-1] and used.item() == 2
+    # a missing page that no new token stands on is the reader's to report
+    attn.attn_block_tables(_i32([[-1, 6, -1]]), _i32([20]), _i32([1]), _i32([1]), 16, 1)
+    check_status(attn)
