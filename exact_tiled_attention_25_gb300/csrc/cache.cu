@@ -389,6 +389,14 @@ __device__ __forceinline__ AppendSite append_site(const AppendFp8Params& p, long
   return s;
 }
 
+// Offsets of request i that do not fit are reported here: where they decrease, the search for
+// a unit's owner may pass their request, and tokens of others, over.
+__device__ __forceinline__ void check_offsets(const AppendFp8Params& p, long long i) {
+  if (i >= p.B) return;
+  const int c0 = __ldg(p.cu_seqlens + i), c1 = __ldg(p.cu_seqlens + i + 1);
+  if (c0 < 0 || c1 < c0 || c1 > p.total) atomicCAS(p.status, 0, kDevBadTables);
+}
+
 struct Raw16 {
   uint4 a, b;
 };
@@ -519,6 +527,8 @@ __global__ void __launch_bounds__(kF8MaxThreads, 2)
     return;
   }
   const unsigned at_site = blockIdx.x - before_q;
+  // (MANY: the few-rows kernel beside it checks them)
+  if (!MANY && threadIdx.x == blockDim.x - 1) check_offsets(p, at_site);
   if (warp == 0) {
     const AppendSite found = append_site<MANY>(p, at_site / (2 * p.H_kv), at_site % (2 * p.H_kv), page_shift, u);
     if (lane == 0) site_sh = found;
@@ -647,6 +657,7 @@ __global__ void __launch_bounds__(kF8Threads)
   const int planes = 2 * p.H_kv;
   // past the last site: a unit that no request reaches
   AppendSite s = append_site<false>(p, site < sites ? site / planes : 0, static_cast<int>(site % planes), page_shift, u);
+  check_offsets(p, static_cast<long long>(blockIdx.x) * kF8Threads + threadIdx.x);
   if (site >= sites || s.end - s.first > most_rows) s.ok = false;
   if (!s.ok) s.first = s.end = 0;
   s.src += 8 * u;

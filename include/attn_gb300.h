@@ -746,8 +746,9 @@ attn_status_t attn_cache_append(const void* q, void* q_out, const void* k, const
  *   are left as they are.
  *   Values are expected finite.
  * Requests that do not fit (offsets, lengths, pages out of range) are skipped and
- * reported by attn_get_device_status() as ATTN_ERR_INVALID_ARG; keys at or past
- * max_pos are stored unrotated and reported.
+ * reported by attn_get_device_status() as ATTN_ERR_INVALID_ARG, and where cu_seqlens
+ * decreases, tokens of other requests may be skipped with them; keys at or past max_pos
+ * are stored unrotated and reported.
  * total >= cu_seqlens[B]: rows behind the last request are padding, not stored (their
  * query rows are copied).  total may be 0.
  * d = 128; page_size a power of two in [16, 65536].

@@ -601,3 +601,22 @@ def test_tables_report_tokens_on_missing_pages(attn):
     # a missing page that no new token stands on is the reader's to report
     attn.attn_block_tables(_i32([[-1, 6, -1]]), _i32([20]), _i32([1]), _i32([1]), 16, 1)
     check_status(attn)
+
+
+@pytest.mark.parametrize("B,top", [(3, 200), (64, 64), (64, 640), (300, 300), (9, 2000)])
+def test_append_fp8_decreasing_offsets_are_reported(attn, B, top):
+    """Offsets that rise to `top` and start again from 0, far enough that no unit of the launch
+    falls to the request between: reported, and nothing outside the requests' pages is written."""
+    H_kv, d, page = 2, 128, 16
+    rows = torch.randn(top, H_kv, d, device=dev()).half()
+    cu = [0, top] + [min(i, top) for i in range(B - 1)]
+    lens = [top] + [0] + [1] * (B - 2)
+    width = -(-top // page)
+    bt = torch.arange(B * width, dtype=torch.int32, device=dev()).view(B, width)
+    kc, ck = guarded((B * width, page, H_kv, d), torch.uint8, 0x5A)
+    vc, cv = guarded((B * width, page, H_kv, d), torch.uint8, 0x5A)
+    ks, vs = (torch.ones(B * width, H_kv, device=dev()) for _ in range(2))
+    attn.attn_cache_append_fp8(rows, rows, kc, vc, ks, vs, bt, _i32(lens), _i32(cu))
+    assert attn.attn_get_device_status() == attn.ATTN_ERR_INVALID_ARG
+    ck()
+    cv()
