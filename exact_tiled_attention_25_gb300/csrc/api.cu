@@ -1052,7 +1052,8 @@ attn_status_t attn_get_device_status(cudaStream_t stream) {
   if (value == kDevBadTables)
     return fail(ATTN_ERR_INVALID_ARG,
                 "request lengths, free pages, slots, table entries or positions that do not fit the "
-                "block table, the cache or the rotary tables; those tokens were skipped");
+                "block table, the cache or the rotary tables; those tokens were skipped, rows of "
+                "positions past the rotary tables written unrotated");
   return fail(ATTN_ERR_TIMEOUT, std::string("kernel wait timed out in role ") +
                                     (role < 8 ? roles[role] : "?") + " (code " +
                                     std::to_string(value) + ")");

@@ -27,8 +27,9 @@ enum : int {
   kDevTimeoutSelftest = 0x700, // the wait of attn_selftest_wait_timeout
   kDevBadSeqlens = 0x800,      // cu_seqlens entry outside [0, total], decreasing, or a
                                // sequence longer than max_seqlen: that sequence is skipped
-  kDevBadTables = 0x900,       // request lengths, free pages, slots or positions that do not
-                               // fit their tables: those tokens are skipped
+  kDevBadTables = 0x900,       // request lengths, free pages or slots that do not fit their
+                               // tables: those tokens are skipped; positions past the rotary
+                               // tables: those rows are written unrotated
 };
 
 // Wall-clock budget for any single barrier wait (nanoseconds).  Every

@@ -710,7 +710,8 @@ attn_status_t attn_block_tables(int* block_table, const int* old_lens, const int
  *   slots    : DEVICE int64 [total]; -1 = no row (padding); other values outside the
  *              cache are skipped and reported by attn_get_device_status().  Slots of
  *              one call differ from one another.
- *   rope_cos, rope_sin, positions, interleaved : as attn_rope, positions [total]; both
+ *   rope_cos, rope_sin, positions, interleaved : as attn_rope, positions [total] (a key
+ *              of one at or past max_pos is stored unrotated and reported); both
  *              tables NULL = no rotation (positions unused).
  *   q, q_out : queries to rotate in the same launch, q with {token, head} q_strides,
  *              q_out [total, H, d]; H = 0: none.  Needs the tables.  q_out may be q
@@ -769,8 +770,9 @@ attn_status_t attn_cache_append_fp8(const void* q, void* q_out, const void* k, c
  * attn_get_device_status -- synchronises `stream`, then reads and clears the
  * current device's status word.  ATTN_OK, ATTN_ERR_TIMEOUT (a kernel gave up
  * on an internal wait; attn_last_error() names the role), ATTN_ERR_INVALID_ARG
- * (a call met offsets, lengths, pages, slots or positions out of range and
- * skipped them), ATTN_ERR_ARCH, or ATTN_ERR_CUDA.
+ * (a call met offsets, lengths, pages or slots out of range and skipped them, or
+ * positions past its rotary tables, whose rows it wrote unrotated), ATTN_ERR_ARCH,
+ * or ATTN_ERR_CUDA.
  * Source: the pages list failure modes ("FlashAttention-3: Hopper Asynchrony
  * and FP8 Attention", section "Where It Breaks") and ask that problems be
  * reported as explicit errors rather than silently degraded ("FlashAttention 3

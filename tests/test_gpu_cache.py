@@ -620,3 +620,44 @@ def test_append_fp8_decreasing_offsets_are_reported(attn, B, top):
     assert attn.attn_get_device_status() == attn.ATTN_ERR_INVALID_ARG
     ck()
     cv()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_of_positions_past_the_tables(attn, interleaved):
+    """Reported; the rows are written unrotated, as is padding of a negative position, which is not."""
+    H, H_kv, d, page = 2, 2, 64, 8
+    cos, sin = _rope(8, d)
+    rows = torch.randn(4, H + 2 * H_kv, d, device=dev()).bfloat16()
+    q, k, v = rows[:, :H], rows[:, H:H + H_kv], rows[:, H + H_kv:]
+    slots = torch.tensor([5, 0, 9, 15], device=dev())
+    for last, code in ((-1, 0), (8, attn.ATTN_ERR_INVALID_ARG), (2 ** 31 - 1, attn.ATTN_ERR_INVALID_ARG)):
+        kc, vc = (torch.zeros(2, page, H_kv, d, device=dev()).bfloat16() for _ in range(2))
+        qo = attn.attn_cache_append(k, v, kc, vc, slots, cos, sin, _i32([0, 7, 3, last]), q=q, interleaved=interleaved)
+        assert attn.attn_get_device_status() == code
+        if code:
+            assert "unrotated" in attn.attn_last_error()
+        wq, wk = attn.attn_rope(q[:3], k[:3], cos, sin, positions=_i32([0, 7, 3]), interleaved=interleaved)
+        want, val = torch.zeros_like(kc), torch.zeros_like(vc)
+        want.view(-1, H_kv, d)[slots] = torch.cat([wk, k[3:]])
+        val.view(-1, H_kv, d)[slots] = v
+        assert torch.equal(kc, want) and torch.equal(vc, val) and torch.equal(qo, torch.cat([wq, q[3:]]))
+    check_status(attn)
+
+
+@pytest.mark.parametrize("rot,interleaved", [(128, False), (48, False), (128, True)])
+@pytest.mark.parametrize("new", [4, 60])
+def test_append_fp8_of_positions_past_the_tables(attn, new, rot, interleaved):
+    """The codes, descales and queries of tables whose missing rows turn nothing; reported."""
+    H, H_kv, d, page, old = 4, 2, 128, 64, 6
+    bt, (lens, cu, *_), num, q, k, v = _step(attn, 95, [old], [new], page, H, H_kv, d, torch.bfloat16)
+    rows = old + new - 2                              # the last two positions have none
+    cos, sin = _rope(rows, rot)
+    one, zero = torch.ones(2, rot // 2, device=dev()), torch.zeros(2, rot // 2, device=dev())
+    got = []
+    for c, s, code in ((cos, sin, attn.ATTN_ERR_INVALID_ARG), (torch.cat([cos, one]), torch.cat([sin, zero]), 0)):
+        kc, vc = (torch.full((num, page, H_kv, d), 0x35, dtype=torch.uint8, device=dev()) for _ in range(2))
+        ks, vs = (torch.full((num, H_kv), 0.004, device=dev()) for _ in range(2))
+        qo = attn.attn_cache_append_fp8(k, v, kc, vc, ks, vs, bt, lens, cu, c, s, _signs(), q=q, interleaved=interleaved)
+        assert attn.attn_get_device_status() == code
+        got.append((kc, vc, ks, vs, qo))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
