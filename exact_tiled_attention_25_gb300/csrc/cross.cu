@@ -40,8 +40,9 @@ constexpr int BN = 128;   // keys of a tile
 // FEW: at most 16 query rows.  They are laid into the query tile four times, at rows
 // 0, 32, 64 and 96, so every softmax warp finds them in its own quarter of tensor
 // memory; warp w takes keys [32 w, 32 w + 32) of each tile, with statistics of its
-// own and zeros as its probabilities of the other keys, and the four partial outputs
-// are added when a part ends.  (One warp with all 128 keys of a tile needs some
+// own, its products are written to its quarter only (zeros as its probabilities of the
+// other keys would meet their values: 0 * inf = NaN), and the four partial outputs are
+// added when a part ends.  (One warp with all 128 keys of a tile needs some
 // 1400 cycles a tile, most of them exponentials: at d = 64 that is more than the
 // tile's share of HBM time, 5.0 TB/s.)  The gaps behind the four copies hold the
 // other Q buffer's four.
@@ -387,9 +388,14 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
             break;
           tc_fence_after_sync();
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
-            mma_f16_ts(tmem + o_col, tmem + C::S_COL(n & 1) + 8 * kk, sdesc_add(vdesc, kk * 16 * 128), idPV,
-                       (i > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < BN / 16; ++kk) {
+            const uint32_t p_col = tmem + C::S_COL(n & 1) + 8 * kk;
+            const uint64_t v_at = sdesc_add(vdesc, kk * 16 * 128);
+            if constexpr (FEW)   // 16 keys of warp kk / 2, for its rows only
+              mma_f16_ts_quarter(tmem + o_col, p_col, v_at, idPV, (i > 0 || kk % 2 > 0) ? 1u : 0u, kk / 2);
+            else
+              mma_f16_ts(tmem + o_col, p_col, v_at, idPV, (i > 0 || kk > 0) ? 1u : 0u);
+          }
           mma_commit(&kv_empty[slot]);
           if (i == take - 1) mma_commit(&o_full[part & 1]);
         }
@@ -574,11 +580,6 @@ __global__ void __launch_bounds__(CrossCfg<D, FEW>::THREADS, 1)
             }
             // packed P of keys [k, +32) -> columns [k / 2, +16)
             tmem_st16(tS + k0 / 2 + c0 * 16, pk);
-          }
-          if constexpr (FEW) {
-            const uint32_t zero[16] = {};
-#pragma unroll
-            for (int x = 1; x < 4; ++x) tmem_st16(tS + 16 * ((warp + x) & 3), zero);
           }
           const uint64_t acc = fadd2(acc0, acc1);
           l += lo2(acc) + hi2(acc);

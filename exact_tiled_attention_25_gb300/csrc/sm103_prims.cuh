@@ -367,6 +367,18 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+// The same, written to the 32 TMEM lanes of one quarter (0 .. 3) only.
+__device__ __forceinline__ void mma_f16_ts_quarter(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                   uint32_t idesc, uint32_t accumulate, int quarter) {
+  const uint32_t off = 0xffffffffu;                  // a set bit keeps its lane as it was
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(quarter == 0 ? 0u : off),
+      "r"(quarter == 1 ? 0u : off), "r"(quarter == 2 ? 0u : off), "r"(quarter == 3 ? 0u : off)
+      : "memory");
+}
+
 __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                           uint32_t idesc, uint32_t accumulate) {
   asm volatile(

@@ -582,6 +582,8 @@ size_t attn_cross_workspace_size(int B, int H, int H_kv, int N_q, int N_k, int d
  *                out of range counts as 0 and is reported by
  *                attn_get_device_status() as ATTN_ERR_INVALID_ARG.
  *   A batch entry without keys gets O = 0 and LSE = -inf.
+ *   An infinite value of a seen key makes its column of O infinite (or NaN, beside one
+ *   of the other sign) as long as its probability is not 0 in `dtype`: 0 * inf = NaN.
  *   workspace  : at least attn_cross_workspace_size() bytes, 256-byte aligned;
  *                NULL where that is 0.  Calls that overlap on the GPU (two
  *                streams, two captured graphs) need one each.

@@ -462,3 +462,33 @@ def test_explicit_stream(attn):
     o, lse = attn.attn_cross_fwd(q.cpu(), k.cpu(), v.cpu(), stream=side)
     assert torch.equal(o, want[0].cpu())
     check_status(attn)
+
+
+@pytest.mark.parametrize("H,H_kv,N_q", [(2, 2, 1), (16, 1, 1), (2, 2, 40), (2, 2, 300)])
+@pytest.mark.parametrize("N_k,lens", [(300, None), (300, [300, 190]), (5000, [5000, 4900])])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (64, "fp16")])
+def test_infinite_values_of_seen_keys(attn, H, H_kv, N_q, N_k, lens, d, dtype):
+    """Columns with an infinity in some key's value are infinite, with both signs or a NaN they are
+    NaN, the others as ever; whichever rows and keys share a tile."""
+    q, k, v, _ = _inputs(1030, 2, H, H_kv, N_q, N_k, d, dtype)
+    q = q * 0.5                                       # probabilities far from 0 in float16
+    inf = float("inf")
+    for j, c, x in ((0, 1, inf), (37, 2, -inf), (64, 3, inf), (127, 4, inf), (129, 5, -inf), (180, 6, inf),
+                    (5, 7, inf), (100, 7, inf), (5, 8, inf), (70, 8, -inf), (33, 9, float("nan"))):
+        v[:, :, j, c] = x
+    tl = None if lens is None else torch.tensor(lens, dtype=torch.int32, device=dev())
+    o, lse = attn.attn_cross_fwd(q.to(dev()), k.to(dev()), v.to(dev()), tl)
+    check_status(attn)
+    f = [workloads.as_f64(t) for t in (q, k, v)]
+    with np.errstate(invalid="ignore"):
+        ref, rl = oracle.attention_cross_forward(*f, d ** -0.5, lens)
+    got = o.double().cpu().numpy()
+    special = ~np.isfinite(ref)
+    assert special[..., 1:10].all() and special.sum() == special[..., 1:10].sum()
+    assert np.array_equal(got[..., 1:10], ref[..., 1:10], equal_nan=True)
+    rest = np.r_[0, 10:d]
+    f[2] = np.where(np.isfinite(f[2]), f[2], 0.0)
+    ref, _ = oracle.attention_cross_forward(*f, d ** -0.5, lens)
+    tol = _forward_bound(*f, ref, d ** -0.5, lens, dtype)
+    assert np.all(np.abs(got - ref)[..., rest] <= tol[..., rest])
+    _lse_close(lse, rl)
