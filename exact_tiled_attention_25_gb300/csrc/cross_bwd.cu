@@ -632,31 +632,44 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   }
 }
 
-// The pre-pass for at most kFewKeys keys: as bwd_prep_kernel, but D = sum_j P_j dP_j from the
-// keys themselves.  Of one or a few keys O is of V's size, and its rounding weighs in dO . O
-// against the differences dP - D: relative error of dQ and dK in float16 0.00047 (2 keys),
-// 0.00038 (4), 0.00033 (8), 0.00032 (16), so 0.0003; with more keys it tends to 0.0003 either
-// way.  Bound: the products' issue slots, 0.7 us per key and 75 K rows (whole backward pass of
-// those: 28 us with the other pre-pass; 30, 34 and 39 so at 2, 8 and 16 keys).
+// The pre-pass of batch entries that see at most kFewKeys keys: as bwd_prep_kernel, but D =
+// sum_j P_j dP_j from the keys themselves.  Of one or a few keys O is of V's size, and its
+// rounding weighs in dO . O against the differences dP - D: relative error of dQ and dK in float16
+// 0.00047 (2 keys), 0.00038 (4), 0.00033 (8), 0.00032 (16), so 0.0003; with more keys it tends to
+// 0.0003 either way.  MIXED: entries of other lengths are in the batch too and take dO . O, with
+// bwd_prep_kernel's sums; an entry's gradients do not depend on how far the others pad it.
+// Bound: the products' issue slots, 0.7 us per key and 75 K rows (whole backward pass of
+// those: 28 us with the other pre-pass; 30, 34 and 39 so at 2, 8 and 16 keys); DRAM for dO . O.
 constexpr int kFewKeys = 16;
 
-template <int D, bool FP16>
-__global__ void __launch_bounds__(256)
+// Rows that a group of D / 8 lanes takes at a time, so that what is read of a key serves them
+// all, and rows of a block.  MIXED: few enough for the occupancy that dO . O needs (two rows of a
+// long training step's batch: 64 registers; four, in blocks of 128 rows, took 17 us more).
+template <int D, bool MIXED>
+struct FewKeysCfg {
+  static constexpr int L = D / 8;
+  static constexpr int ROWS = 256 / L;
+  static constexpr int R = MIXED ? 2 : 4;
+  static constexpr int BLOCK_ROWS = MIXED ? R * ROWS : 128;
+};
+
+template <int D, bool FP16, bool MIXED>
+__global__ void __launch_bounds__(256, MIXED ? 4 : 1)
     cross_few_keys_prep_kernel(const XBwdKParams kp, const uint16_t* q, const uint16_t* k, const uint16_t* v,
-                               const uint16_t* dout, const float* lse, float* lse2, float* delta, float* dq_acc) {
-  constexpr int L = D / 8;                           // lanes per row, 8 elements each
-  constexpr int ROWS = 256 / L;                      // at a time
+                               const uint16_t* o, const uint16_t* dout, const float* lse, float* lse2, float* delta,
+                               float* dq_acc) {
+  using C = FewKeysCfg<D, MIXED>;
+  constexpr int L = C::L, ROWS = C::ROWS, R = C::R;
   __shared__ __align__(16) float ks[kFewKeys][D], vs[kFewKeys][D];
   wait_for_previous_kernel();
   release_dependents();
-  // 128 rows of one head
-  const int tiles = kp.Npad / 128;
+  // rows of one head
+  const int tiles = kp.Npad / C::BLOCK_ROWS;
   const long long bh = blockIdx.x / tiles;
-  const int n0 = static_cast<int>(blockIdx.x % tiles) * 128;
+  const int n0 = static_cast<int>(blockIdx.x % tiles) * C::BLOCK_ROWS;
   const int b = static_cast<int>(bh / kp.H), h = static_cast<int>(bh % kp.H);
   const int sub = threadIdx.x / L, li = threadIdx.x % L;
-  auto load8 = [](const uint16_t* at, float (&x)[8]) {
-    const uint4 w = __ldcg(reinterpret_cast<const uint4*>(at));
+  auto widen8 = [](const uint4& w, float (&x)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -666,10 +679,51 @@ __global__ void __launch_bounds__(256)
       x[2 * e + 1] = f.y;
     }
   };
+  auto load8 = [&](const uint16_t* at, float (&x)[8]) { widen8(__ldcg(reinterpret_cast<const uint4*>(at)), x); };
   int keys = kp.Nk;
   if (kp.kv_lens) {
     keys = ld_l2_s32(kp.kv_lens + b);
     if (keys < 0 || keys > kp.Nk) keys = 0;
+  }
+  if constexpr (MIXED) {
+    // D = dO . O: the loads are on their way before the keys' number is known
+    uint4 x[R], y[R];
+    float nl[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int n = n0 + sub + r * ROWS;
+      const size_t at = (bh * kp.N + n) * D + 8 * li;
+      x[r] = y[r] = make_uint4(0u, 0u, 0u, 0u);
+      nl[r] = -INFINITY;
+      if (n >= kp.N) continue;
+      x[r] = __ldcg(reinterpret_cast<const uint4*>(o + at));
+      y[r] = __ldcg(reinterpret_cast<const uint4*>(dout + at));
+      nl[r] = -__ldcg(lse + bh * kp.N + n) * kLog2e;
+    }
+    if (keys > kFewKeys) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int n = n0 + sub + r * ROWS;
+        float a[8], c[8], sum = 0.f;
+        widen8(x[r], a);
+        widen8(y[r], c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(a[e], c[e], sum);
+#pragma unroll
+        for (int off = L / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (n < kp.N) {
+          float4* z = reinterpret_cast<float4*>(dq_acc + (bh * kp.N + n) * D + 8 * li);
+          z[0] = z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (li == 0) {
+          // stored negated, as the other pre-pass does
+          const size_t prow = bh * kp.Npad + n;
+          delta[prow] = n < kp.N ? -sum : 0.f;
+          lse2[prow] = nl[r];
+        }
+      }
+      return;
+    }
   }
   const size_t kv0 = (static_cast<size_t>(b) * kp.H_kv + h / kp.group) * kp.Nk * D;
   for (int i = threadIdx.x; i < 2 * keys * L; i += 256) {
@@ -681,11 +735,10 @@ __global__ void __launch_bounds__(256)
     dst[1] = make_float4(x[4], x[5], x[6], x[7]);
   }
   __syncthreads();
-  // four rows per group of L lanes, so that what is read of a key serves them all
-  for (int n1 = n0 + sub; n1 < n0 + 128; n1 += 4 * ROWS) {
-    float qr[4][8] = {}, dr[4][8] = {};
+  for (int n1 = n0 + sub; n1 < n0 + C::BLOCK_ROWS; n1 += R * ROWS) {
+    float qr[R][8] = {}, dr[R][8] = {};
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
       const int n = n1 + r * ROWS;
       if (n >= kp.N) continue;
       const size_t at = (bh * kp.N + n) * D + 8 * li;
@@ -694,19 +747,19 @@ __global__ void __launch_bounds__(256)
       float4* z = reinterpret_cast<float4*>(dq_acc + at);
       z[0] = z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    // of the eight sums (S, dP of four rows) lane i keeps sum i mod 8, the even lanes the rows'
-    const int n = n1 + (li % 8 / 2) * ROWS;
+    // of the 2 R sums (S, dP of R rows) lane i keeps sum i mod 2 R, the even lanes the rows'
+    const int n = n1 + (li % (2 * R) / 2) * ROWS;
     const float nl = n < kp.N ? -__ldcg(lse + bh * kp.N + n) * kLog2e : -INFINITY;
     float sum = 0.f;
     for (int j = 0; j < keys; ++j) {
-      float x[8], y[8], w[8];
+      float x[8], y[8], w[2 * R];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         *reinterpret_cast<float4*>(x + 4 * e) = *reinterpret_cast<const float4*>(&ks[j][8 * li + 4 * e]);
         *reinterpret_cast<float4*>(y + 4 * e) = *reinterpret_cast<const float4*>(&vs[j][8 * li + 4 * e]);
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < R; ++r) {
         w[2 * r] = w[2 * r + 1] = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -715,19 +768,19 @@ __global__ void __launch_bounds__(256)
         }
       }
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) {
+      for (int off = R; off > 0; off >>= 1) {
 #pragma unroll
-        for (int i = 0; i < o; ++i) {
-          const float send = (li & o) ? w[i] : w[i + o], keep = (li & o) ? w[i + o] : w[i];
-          w[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        for (int i = 0; i < off; ++i) {
+          const float send = (li & off) ? w[i] : w[i + off], keep = (li & off) ? w[i + off] : w[i];
+          w[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
         }
       }
-      if (L == 16) w[0] += __shfl_xor_sync(0xffffffffu, w[0], 8);
+#pragma unroll
+      for (int off = 2 * R; off < L; off <<= 1) w[0] += __shfl_xor_sync(0xffffffffu, w[0], off);
       const float dp = __shfl_xor_sync(0xffffffffu, w[0], 1);
       sum = fmaf(ex2_approx(fmaf(w[0], kp.scale_log2, nl)), dp, sum);
     }
-    if (li < 8 && li % 2 == 0) {
-      // stored negated, as the other pre-pass does
+    if (li < 2 * R && li % 2 == 0) {
       const size_t prow = bh * kp.Npad + n;
       delta[prow] = n < kp.N ? -sum : 0.f;
       lse2[prow] = nl;
@@ -850,9 +903,12 @@ attn_status_t launch_cross_bwd_t(const BwdParams& p, float* part, int ctas, cuda
   // 1. pre-pass: row vectors, dQ accumulator zeroed
   {
     auto rows = [](const void* x) { return static_cast<const uint16_t*>(x); };
-    if (p.N_k <= kFewKeys) {
-      e = launch_dependent(cross_few_keys_prep_kernel<D, FP16>, dim3(static_cast<unsigned>(rows_pad / 128)), 256, 0,
-                           stream, 0, kp, rows(p.q), rows(p.k), rows(p.v), rows(p.dout), p.lse, p.lse2, p.delta, p.dq_acc);
+    if (p.N_k <= kFewKeys || p.kv_lens) {
+      const auto kern = p.N_k <= kFewKeys ? cross_few_keys_prep_kernel<D, FP16, false>
+                                          : cross_few_keys_prep_kernel<D, FP16, true>;
+      const int block_rows = p.N_k <= kFewKeys ? FewKeysCfg<D, false>::BLOCK_ROWS : FewKeysCfg<D, true>::BLOCK_ROWS;
+      e = launch_dependent(kern, dim3(static_cast<unsigned>(rows_pad / block_rows)), 256, 0, stream, 0, kp, rows(p.q),
+                           rows(p.k), rows(p.v), rows(p.o), rows(p.dout), p.lse, p.lse2, p.delta, p.dq_acc);
     } else {
       constexpr int rows_per_block = 8 * (32 / (D / 8));
       e = launch_dependent(bwd_prep_kernel<D, FP16, false, true>,

@@ -492,3 +492,31 @@ def test_infinite_values_of_seen_keys(attn, H, H_kv, N_q, N_k, lens, d, dtype):
     tol = _forward_bound(*f, ref, d ** -0.5, lens, dtype)
     assert np.all(np.abs(got - ref)[..., rest] <= tol[..., rest])
     _lse_close(lse, rl)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "fp16"), (128, "fp16"), (64, "bf16"), (128, "bf16")])
+@pytest.mark.parametrize("N_k", [17, 300])
+def test_few_seen_keys_of_a_padded_batch(attn, N_k, d, dtype):
+    """Batch entries that see 1 to 17 keys beside one that sees all: the bounds of their own
+    lengths, as if the batch were not padded."""
+    B, H, H_kv, N_q, lens = 7, 6, 2, 203, [1, 2, 8, 16, 17, 0, N_k]
+    q, k, v, do = _inputs(1040, B, H, H_kv, N_q, N_k, d, dtype)
+    scale = d ** -0.5
+    g = [t.to(dev()) for t in (q, k, v, do)]
+    for b, n in enumerate(lens):
+        g[1][b, :, n:], g[2][b, :, n:] = float("nan"), float("inf")
+    tl = torch.tensor(lens, dtype=torch.int32, device=dev())
+    o, lse = attn.attn_cross_fwd(*g[:3], tl)
+    got = attn.attn_cross_bwd(*g[:3], o, g[3], lse, tl)
+    check_status(attn)
+    assert not any(x[5].any() for x in got)
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        f = [workloads.as_f64(t[b:b + 1, :, :n] if t.shape[2] == N_k else t[b:b + 1]) for t in (q, k, v, do)]
+        ref, _ = oracle.attention_cross_forward(*f[:3], scale)
+        tol = _forward_bound(*f[:3], ref, scale, None, dtype)
+        grads = oracle.attention_cross_backward(*f, scale)
+        tols = _backward_bounds(*f, ref, tol, grads, scale, None, dtype)
+        for x, r, t, what in zip(got, grads, tols, ("dq", "dk", "dv")):
+            _within(x[b:b + 1, :, :r.shape[2]], r, t, (what, n))
