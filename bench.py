@@ -24,6 +24,7 @@ import argparse
 import json
 import math
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -53,13 +54,28 @@ KERNEL_OF = {"fwd_bf16": "fwd_kernel", "bwd_bf16": "bwd_main_kernel (timed as th
              "fwd_fp8": "fwd_fp8_kernel", "fp8_prepass": "fp8_quant_kernel"}
 
 
-def kernel_source_digest(stage):
-    """First 16 hex digits of the SHA-256 of the stage's kernel source file and
-    the device primitives it includes."""
+CSRC = os.path.join(ROOT, "exact_tiled_attention_25_gb300", "csrc")
+
+
+def kernel_sources(stage, csrc=CSRC):
+    """The stage's kernel source file and every file beside it that it includes,
+    directly or through another, by name.  (The public header, in a folder of its
+    own, declares entry points only.)"""
+    names = [KERNEL_SOURCES[stage]]
+    for name in names:                       # grows while it is walked
+        with open(os.path.join(csrc, name)) as f:
+            for line in f:
+                got = re.match(r'\s*#\s*include\s+"([^"/]+)"', line)
+                if got and got.group(1) not in names:
+                    names.append(got.group(1))
+    return names
+
+
+def kernel_source_digest(stage, csrc=CSRC):
+    """First 16 hex digits of the SHA-256 of the stage's kernel sources."""
     import hashlib
-    csrc = os.path.join(ROOT, "exact_tiled_attention_25_gb300", "csrc")
     h = hashlib.sha256()
-    for name in (KERNEL_SOURCES[stage], "sm103_prims.cuh", "common.h"):
+    for name in kernel_sources(stage, csrc):
         with open(os.path.join(csrc, name), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
