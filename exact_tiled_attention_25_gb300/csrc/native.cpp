@@ -39,6 +39,7 @@ struct Api {
 #undef ATTN_FN
 } api;
 PyObject* on_error = nullptr;      // called with (code, name); raises
+PyObject* out_of_memory = nullptr; // torch.OutOfMemoryError
 
 // A refused argument: becomes a ValueError.
 struct Refused : std::runtime_error {
@@ -237,6 +238,8 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
   } catch (const Raised&) {
   } catch (const Refused& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (const c10::OutOfMemoryError& e) {
+    PyErr_SetString(out_of_memory, e.what_without_backtrace());
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {
@@ -518,6 +521,11 @@ PyObject* bind(PyObject* const* a) {
   ATTN_FN(attn_cache_append);
   ATTN_FN(attn_cache_append_fp8);
 #undef ATTN_FN
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+  Py_XDECREF(torch);
+  if (!type) throw Raised{};
+  Py_XSETREF(out_of_memory, type);
   Py_XSETREF(on_error, Py_NewRef(a[1]));
   return Py_NewRef(Py_None);
 }

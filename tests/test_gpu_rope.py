@@ -227,3 +227,10 @@ def test_rows_and_tables_written_by_the_kernel_before(attn, captured):
     for i in range(6):
         for got, ref in zip(outs, want[i % 3]):
             assert torch.equal(got[i], ref), i
+
+
+def test_outputs_larger_than_the_device(attn):
+    """PyTorch's own error, which its users catch, as from the other calls' allocations."""
+    with pytest.raises(torch.OutOfMemoryError):
+        attn.attn_rope_table(2 ** 31 - 1, 256)
+    check_status(attn)
