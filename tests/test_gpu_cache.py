@@ -661,3 +661,27 @@ def test_append_fp8_of_positions_past_the_tables(attn, new, rot, interleaved):
         assert attn.attn_get_device_status() == code
         got.append((kc, vc, ks, vs, qo))
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dirt", [float("inf"), float("-inf")])
+def test_paged_decode_over_pages_of_infinities(attn, d, dtype, dirt):
+    """Infinities in every slot behind a sequence, in keys and values: the bits of clean pages."""
+    lens, page = [1, 63, 64, 65, 129, 300], 64
+    kc, vc, table = workloads.paged_cache(82, lens, page, 2, d)
+    q = workloads.round_to(workloads.normal(83, (len(lens), 8, 1, d)), dtype).to(dev())
+    unused = torch.ones(kc.shape[:2], dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for t in range(n):
+            unused[table[b, t // page], t % page] = False
+    outs = []
+    for fill in (0.0, dirt):
+        k, v = (workloads.round_to(x, dtype).to(dev()) for x in (kc, vc))
+        k[unused.to(dev())] = fill
+        v[unused.to(dev())] = fill
+        assert fill == 0.0 or (torch.isinf(v).any() and torch.isinf(k).any())
+        outs.append(attn.attn_decode_paged(q, k, v, torch.from_numpy(table).to(dev()), _i32(lens), max(lens)))
+        check_status(attn)
+    assert torch.isfinite(outs[1][0].float()).all()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
