@@ -10,7 +10,8 @@ fallback, and a missing library raises.
 Tensors are [B, H, N, d], contiguous; the ``*_varlen`` calls take a packed
 batch [total, H, d] with int32 sequence offsets ``cu_seqlens`` [B + 1].  Inputs
 on the CPU are accepted: they are copied to the current CUDA device on the
-current stream, and the outputs are copied back to the CPU.
+current stream, and the outputs are copied back to the CPU.  The calls that write a
+cache or a block table in place take CUDA tensors only.
 """
 from __future__ import annotations
 

@@ -448,7 +448,8 @@ __device__ __forceinline__ uint32_t scale_codes(uint32_t w, float ratio) {
 
 // The page's other rows, row x = from, from + by, ...: cleared behind the new ones of
 // a page that starts here, requantised before them when the descale grew.  Lane u of the
-// eight takes codes 16 u .. 16 u + 15.
+// eight takes codes 16 u .. 16 u + 15.  Bound: the latency of a load and its store, row by row
+// (the next load may not pass the store: some 0.16 us a row where one group of lanes walks a page).
 __device__ __forceinline__ void other_rows(const AppendSite& s, float after, int page_size, int from, int by, int u) {
   uint8_t* const at = s.dst + 8 * u;                 // s.dst is at column 8 u
   if (s.first == 0) {
@@ -640,7 +641,10 @@ __global__ void __launch_bounds__(kF8MaxThreads, 2)
 // of a page share a block and its lookups; blocks behind them rotate query rows.  Pages with
 // more than most_rows new rows are left to append_fp8_pages_kernel.  Small blocks spread a
 // few requests' pages, which may have to be cleared or requantised, over the machine (64
-// requests, pages of 64 and of 256: 5.5 and 7.6 us; in blocks of 256 threads 5.7 and 11.7).
+// requests, pages of 64 and of 256, some cleared and none requantised: 5.6 and 7.7 us; in blocks
+// of 256 threads 5.7 and 11.7).  A page whose descale grows has its older rows requantised by
+// its eight lanes, one after the other, and the slowest sets the kernel's time: with descales of
+// N(0, 1) rows, some 16 of the 64 requests' planes growing in a step, 10.5 and 48 us.
 template <bool FP16, int MODE, bool SIGNS>
 __global__ void __launch_bounds__(kF8Threads)
     append_fp8_rows_kernel(const AppendFp8Params p, int page_shift, long long sites, unsigned site_blocks,
@@ -721,7 +725,7 @@ attn_status_t launch_append_t(const AppendFp8Params& p, RopeKParams q, int page_
   // rows one after the other (which page they stand in is not known here; one a page is
   // assumed where there are no more tokens than requests), and their number.  Blocks: as
   // many as fit at a time, those of pages that no token reaches among them.
-  // Pages of 64, us by lanes, by blocks, by both: 64 requests with a token each 5.5, 7.7, -;
+  // Pages of 64 whose descales do not grow, us by lanes, by blocks, by both: 64 requests with a token each 5.5, 7.7, -;
   // 256: 6.7, 22, -; 256 with 4 each 12, 24, 15; 16 of which two bring up to 30 33, 5.4, -; 256 of
   // which 32 bring up to 20 26, 24, 13.
   const int quarter = p.page_size / 4 * 8;           // threads of a sweep of a quarter of the page
