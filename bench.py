@@ -40,13 +40,14 @@ WORKLOAD = "attention step (bf16 fwd + bf16 bwd + fp8 pre-pass + fp8 fwd), B=2 H
 # DRAM bytes (read + write) per launch of each stage's main kernel, measured by
 # ncu (dram__bytes_read.sum + dram__bytes_write.sum of one launch on this
 # workload, non-causal).  "src" is the digest (see kernel_source_digest) of the
-# kernel's source files when the capture was taken; once they change, the
-# figure no longer describes the kernel and the line reports traffic as null.
+# kernel's source files, headers included, when the capture was taken; once they
+# change, the figure no longer describes the kernel and the line reports traffic as
+# null.
 NCU_TRAFFIC = {
-    "fwd_bf16": {"bytes": 247_944_960, "src": "4556e39afb1bcd95"},      # 201.4 MB read + 46.5 MB write
-    "bwd_bf16": {"bytes": 622_878_976, "src": "b46ee46459be4a33"},      # 404.9 MB read + 217.9 MB write
-    "fwd_fp8": {"bytes": 129_437_184, "src": "e467db4535cb85c2"},       # 100.7 MB read + 28.7 MB write
-    "fp8_prepass": {"bytes": 270_651_136, "src": "e467db4535cb85c2"},   # 201.4 MB read + 69.3 MB write
+    "fwd_bf16": {"bytes": 247_182_080, "src": "6cf7a251c0090b0d"},      # 201.4 MB read + 45.8 MB write
+    "bwd_bf16": {"bytes": 623_645_696, "src": "431c3ed7ce4279ba"},      # 405.6 MB read + 218.1 MB write
+    "fwd_fp8": {"bytes": 130_851_328, "src": "f6dada11f6bd672d"},       # 101.1 MB read + 29.8 MB write
+    "fp8_prepass": {"bytes": 267_763_712, "src": "f6dada11f6bd672d"},   # 201.4 MB read + 66.4 MB write
 }
 KERNEL_SOURCES = {"fwd_bf16": "fwd.cu", "bwd_bf16": "bwd.cu", "fwd_fp8": "fp8.cu",
                   "fp8_prepass": "fp8.cu"}
