@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(Dec8Cfg::THREADS, 1)
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
         // not 0 where the product underflows: a masked score's -inf times it stays -inf
-        coef[g] = fmaxf(c_q * __shfl_sync(0xffffffffu, dcur, g), 0x1p-126f);
+        coef[g] = at_least_normal(c_q * __shfl_sync(0xffffffffu, dcur, g));
         lgv[g] = __shfl_sync(0xffffffffu, lgd, 8 + g);
         ivv[g] = __shfl_sync(0xffffffffu, invd, 8 + g);
       }

@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(THREADS8, 1)
     bool ok = true;
     for (int j = 0; j < my_nK; ++j) {
       // not 0 where the product underflows: a masked score's -inf times it stays -inf
-      const float cj = fmaxf(c_q * kdesc[j], 0x1p-126f);
+      const float cj = at_least_normal(c_q * kdesc[j]);
       const float ratio = vdesc[j] * inv_dv_max;          // in (0, 1]
       const float lg_ratio = lg2_approx8(ratio);
       float inv_ratio;

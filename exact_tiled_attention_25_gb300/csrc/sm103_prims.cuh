@@ -600,6 +600,13 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return m;
 }
 
+// max(x, 2^-126), NaN for NaN.
+__device__ __forceinline__ float at_least_normal(float x) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(x), "f"(0x1p-126f));
+  return m;
+}
+
 // Packed pair of fp32 lanes in one 64-bit register.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   return (static_cast<uint64_t>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);

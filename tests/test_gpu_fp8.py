@@ -390,3 +390,17 @@ def test_forward_of_tiny_scores(attn, N, causal, size):
     ref, rl = oracle.attention_forward(zero, zero, v, 128 ** -0.5, causal)
     assert np.sqrt(np.mean((o.double().cpu().numpy() - ref) ** 2)) <= FP8_RMSE
     assert np.abs(lse.double().cpu().numpy() - rl).max() <= 1e-3
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_nan_descales_show(attn, which):
+    """A descale that was never written (NaN) makes the rows that meet it NaN, the others stay."""
+    xs = [torch.from_numpy(x).to(dev()) for x in workloads.normal(15, (1, 2, 300, 128), 3)]
+    codes, desc = attn.attn_fp8_quantize(*xs)
+    desc[which][0, 1, 1] = float("nan")
+    o, lse = attn.attn_fwd_fp8(*codes, *desc)
+    check_status(attn)
+    assert torch.isfinite(o[0, 0].float()).all()
+    met = o[0, 1, 128:256] if which == 0 else o[0, 1]
+    assert met.isnan().all()
+    assert which > 0 or torch.isfinite(torch.cat([o[0, 1, :128], o[0, 1, 256:]]).float()).all()
