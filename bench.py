@@ -44,10 +44,10 @@ WORKLOAD = "attention step (bf16 fwd + bf16 bwd + fp8 pre-pass + fp8 fwd), B=2 H
 # change, the figure no longer describes the kernel and the line reports traffic as
 # null.
 NCU_TRAFFIC = {
-    "fwd_bf16": {"bytes": 247_182_080, "src": "6cf7a251c0090b0d"},      # 201.4 MB read + 45.8 MB write
-    "bwd_bf16": {"bytes": 623_645_696, "src": "431c3ed7ce4279ba"},      # 405.6 MB read + 218.1 MB write
-    "fwd_fp8": {"bytes": 130_851_328, "src": "f6dada11f6bd672d"},       # 101.1 MB read + 29.8 MB write
-    "fp8_prepass": {"bytes": 267_763_712, "src": "f6dada11f6bd672d"},   # 201.4 MB read + 66.4 MB write
+    "fwd_bf16": {"bytes": 248_772_608, "src": "227dd5032ba8c2bd"},      # 201.4 MB read + 47.3 MB write
+    "bwd_bf16": {"bytes": 623_868_160, "src": "a720404894a44eca"},      # 405.7 MB read + 218.2 MB write
+    "fwd_fp8": {"bytes": 131_011_584, "src": "739b188e4c6bbb01"},       # 101.0 MB read + 30.0 MB write
+    "fp8_prepass": {"bytes": 267_818_240, "src": "739b188e4c6bbb01"},   # 201.4 MB read + 66.4 MB write
 }
 KERNEL_SOURCES = {"fwd_bf16": "fwd.cu", "bwd_bf16": "bwd.cu", "fwd_fp8": "fp8.cu",
                   "fp8_prepass": "fp8.cu"}
