@@ -51,7 +51,9 @@ __all__ = ["AttnError", "attn_fwd", "attn_fwd_schedule", "attn_fwd_gqa", "attn_f
            "attn_decode_paged", "attn_decode_paged_fp8", "attn_decode_workspace_size",
            "attn_cross_fwd", "attn_cross_bwd", "attn_cross_workspace_size", "attn_cross_bwd_workspace_size",
            "attn_rope", "attn_rope_table", "attn_block_tables",
-           "attn_cache_append", "attn_cache_append_fp8",
+           "attn_cache_append", "attn_cache_append_fp8", "attn_cache_append_fp4",
+           "attn_decode_paged_fp4", "attn_decode_fp4_workspace_size",
+           "attn_cache_read", "attn_cache_read_fp8", "attn_cache_read_fp4", "attn_merge",
            "attn_get_device_status",
            "attn_status_string", "attn_last_error", "load_library"]
 
@@ -850,3 +852,79 @@ def attn_cache_append_fp8(k, v, k_cache, v_cache, k_descale, v_descale, block_ta
     attn_cache_append.  Returns q_out (None without q)."""
     return _binding().cache_append_fp8(k, v, k_cache, v_cache, k_descale, v_descale, block_table, seq_lens,
                                       cu_seqlens, rope_cos, rope_sin, hadamard_signs, q, interleaved, q_out, stream)
+
+
+def attn_cache_append_fp4(k, v, k_cache, v_cache, k_descale, v_descale, slots, rope_cos=None, rope_sin=None,
+                          positions=None, hadamard_signs=None, q=None, interleaved: bool = False, q_out=None,
+                          stream=None):
+    """Writes new keys and values [total, H_kv, d] to rows slots (int64 [total], -1: none) of a
+    4-bit cache: uint8 [num_pages, H_kv, page_size, d / 2] (two e2m1 codes a byte) with bfloat16
+    descales [num_pages, H_kv, page_size], one per row.  Keys are rotated and transformed
+    when tables (with positions int32 [total]) and signs are given; q is rotated as in
+    attn_cache_append.  Returns q_out (None without q)."""
+    return _binding().cache_append_fp4(k, v, k_cache, v_cache, k_descale, v_descale, slots, rope_cos, rope_sin,
+                                      positions, hadamard_signs, q, interleaved, q_out, stream)
+
+
+def attn_decode_fp4_workspace_size(B: int, H: int, H_kv: int, n_q: int, d: int, max_seqlen: int) -> int:
+    return int(_lib.load().attn_decode_fp4_workspace_size(B, H, H_kv, n_q, d, max_seqlen))
+
+
+def attn_decode_paged_fp4(q, k_cache, v_cache, k_descale, v_descale, block_table, seq_lens, max_seqlen: int,
+                          causal: bool = True, softmax_scale: float | None = None, hadamard_signs=None, o=None,
+                          lse=None, workspace=None, stream=None):
+    """Decode step against the 4-bit cache of attn_cache_append_fp4: q [B, H, n_q, d] bf16/fp16,
+    hadamard_signs (float32 [d]) when the keys were stored transformed.  Returns O (q's
+    dtype) and LSE float32 [B, H, n_q]."""
+    call = _binding().decode_paged_fp4
+    tensors = (q, k_cache, v_cache, k_descale, v_descale, block_table, seq_lens, hadamard_signs)
+    rest = (max_seqlen, causal, softmax_scale, o, lse, workspace, stream)
+    return call(*tensors, *rest) if q.is_cuda else _moved(call, tensors, *rest)
+
+
+def _read(bits, tensors, n, first, cu_seqlens, dtype, k, v, stream):
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be bfloat16 or float16")
+    call = _binding().cache_read
+    if not tensors[0].is_cuda:
+        def moved(*x):      # the tensors first, as _moved() takes them
+            return call(bits, *x[:7], n, *x[7:])
+        return _moved(moved, (*tensors, first, cu_seqlens), k, v, dtype == torch.float16, stream)
+    return call(bits, *tensors, n, first, cu_seqlens, k, v, dtype == torch.float16, stream)
+
+
+def attn_cache_read(k_cache, v_cache, block_table, seq_lens, n: int, first=None, cu_seqlens=None, k=None, v=None,
+                    stream=None):
+    """Positions of a 16-bit paged cache [num_pages, page_size, H_kv, d] as contiguous rows.
+    Returns k, v [B, H_kv, n, d]: row i of request b is position first[b] + i (int32 [B];
+    None: 0), zeros from seq_lens[b] on.  With cu_seqlens (int32 [B + 1]) they are packed
+    [n, H_kv, d]: row cu_seqlens[b] + i is position first[b] + i, rows behind the last
+    request stay as they are."""
+    return _read(16, (k_cache, v_cache, None, None, None, block_table, seq_lens), n, first, cu_seqlens,
+                 torch.bfloat16, k, v, stream)
+
+
+def attn_cache_read_fp8(k_cache, v_cache, k_descale, v_descale, block_table, seq_lens, n: int, first=None,
+                        cu_seqlens=None, hadamard_signs=None, dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """attn_cache_read of an e4m3 cache (uint8 [num_pages, page_size, H_kv, 128], descales
+    float32 [num_pages, H_kv]) into rows of dtype; hadamard_signs undoes the keys' transform."""
+    return _read(8, (k_cache, v_cache, k_descale, v_descale, hadamard_signs, block_table, seq_lens), n, first,
+                 cu_seqlens, dtype, k, v, stream)
+
+
+def attn_cache_read_fp4(k_cache, v_cache, k_descale, v_descale, block_table, seq_lens, n: int, first=None,
+                        cu_seqlens=None, hadamard_signs=None, dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """attn_cache_read of the 4-bit cache of attn_cache_append_fp4 into rows of dtype;
+    hadamard_signs undoes the keys' transform."""
+    return _read(4, (k_cache, v_cache, k_descale, v_descale, hadamard_signs, block_table, seq_lens), n, first,
+                 cu_seqlens, dtype, k, v, stream)
+
+
+def attn_merge(o_a, lse_a, o_b, lse_b, o=None, lse=None, stream=None):
+    """Attention over two disjoint sets of keys from the O and LSE over each: [B, H, N, d] with
+    float32 [B, H, N], or packed [total, H, d] with [H, total].  A part with LSE = -inf is
+    empty.  o and lse may be an input's own.  Returns O, LSE."""
+    call = _binding().merge
+    if not o_a.is_cuda:
+        return _moved(call, (o_a, lse_a, o_b, lse_b), o, lse, stream)
+    return call(o_a, lse_a, o_b, lse_b, o, lse, stream)

@@ -99,6 +99,13 @@ SIGNATURES = {
     "attn_cache_append": (c_int, [c_void_p] * 10 + [c_int] * 8 + [c_strides] * 3 + [c_int, c_int, c_void_p]),
     "attn_cache_append_fp8": (c_int, [c_void_p] * 14 + [c_int] * 10 + [c_strides] * 3 +
                               [c_int, c_int, c_void_p]),
+    "attn_cache_append_fp4": (c_int, [c_void_p] * 13 + [c_int] * 8 + [c_strides] * 3 + [c_int, c_int, c_void_p]),
+    "attn_decode_fp4_workspace_size": (c_size_t, [c_int] * 6),
+    "attn_decode_paged_fp4": (c_int, [c_void_p] * 11 + [c_size_t] + [c_int] * 10 + [c_float, c_int, c_void_p]),
+    "attn_cache_read": (c_int, [c_void_p] * 8 + [c_int] * 8 + [c_void_p]),
+    "attn_cache_read_fp8": (c_int, [c_void_p] * 11 + [c_int] * 8 + [c_void_p]),
+    "attn_cache_read_fp4": (c_int, [c_void_p] * 11 + [c_int] * 8 + [c_void_p]),
+    "attn_merge": (c_int, [c_void_p] * 6 + [c_int] * 6 + [c_void_p]),
     "attn_selftest_wait_timeout": (c_int, [ctypes.c_uint, c_void_p]),
     "attn_get_device_status": (c_int, [c_void_p]),
     "attn_status_string": (c_char_p, [c_int]),

@@ -1010,6 +1010,190 @@ attn_status_t attn_cache_append_fp8(const void* q, void* q_out, const void* k, c
   return launch_append_fp8(a, p, dtype == ATTN_FP16, interleaved, stream);
 }
 
+// Sizes of a paged cache that are shared by the calls below.
+static attn_status_t check_cache(int num_pages, int page_size, int H_kv, int d, int B, int max_pages, int least_page) {
+  attn_status_t s;
+  if (B < 1 || max_pages < 1 || num_pages < 1 || H_kv < 1)
+    return fail(ATTN_ERR_INVALID_ARG, "B, max_pages, num_pages and H_kv must be >= 1");
+  if ((s = check_page_size(page_size, least_page)) != ATTN_OK) return s;
+  if (static_cast<long long>(max_pages) * page_size > 2147483647LL)
+    return fail(ATTN_ERR_INVALID_ARG, "max_pages * page_size must be < 2^31");
+  if (static_cast<double>(num_pages) * page_size * H_kv * d >= 9.0e15)
+    return fail(ATTN_ERR_INVALID_ARG, "cache too large");
+  return ATTN_OK;
+}
+
+attn_status_t attn_cache_append_fp4(const void* q, void* q_out, const void* k, const void* v,
+                                    uint8_t* k_cache, uint8_t* v_cache, void* k_descale, void* v_descale,
+                                    const long long* slots, const float* rope_cos, const float* rope_sin,
+                                    const int* positions, const float* hadamard_signs, int total, int H,
+                                    int H_kv, int d, int rot_dim, int max_pos, int num_pages, int page_size,
+                                    const long long* q_strides, const long long* k_strides,
+                                    const long long* v_strides, int interleaved, attn_dtype_t dtype,
+                                    cudaStream_t stream) {
+  g_last_error.clear();
+  attn_status_t s;
+  if ((s = check_page_size(page_size, 16)) != ATTN_OK) return s;
+  RopeKParams p{};
+  if ((s = append_common(&p, q, q_out, k, v, k_cache, v_cache, rope_cos, rope_sin, total, H, H_kv, d,
+                         rot_dim, max_pos, num_pages, page_size, q_strides, k_strides, v_strides,
+                         interleaved, dtype)) != ATTN_OK)
+    return s;
+  if (d == 256) return fail(ATTN_ERR_UNSUPPORTED, "the 4-bit cache supports d = 64 and 128");
+  if ((s = check_ptrs({k_descale, v_descale})) != ATTN_OK) return s;
+  if (hadamard_signs && !aligned16(hadamard_signs))
+    return fail(ATTN_ERR_INVALID_ARG, "hadamard_signs not 16-byte aligned");
+  if (total > 0) {
+    if (slots == nullptr || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+      return fail(ATTN_ERR_INVALID_ARG, "slots must be non-null and 8-byte aligned");
+    if (rope_cos && (s = check_ints({positions})) != ATTN_OK) return s;
+  }
+  if ((s = check_device()) != ATTN_OK) return s;
+  if (total == 0) return ATTN_OK;
+  const AppendFp4Params a{k, v, p.st[1], p.sh[1], p.st[2], p.sh[2], k_cache, v_cache,
+                          static_cast<uint16_t*>(k_descale), static_cast<uint16_t*>(v_descale), slots, positions,
+                          rope_cos, rope_sin, hadamard_signs, total, H_kv, num_pages, page_size, p.rot, max_pos};
+  p.heads[1] = p.heads[2] = 0;
+  p.positions = positions;
+  return launch_append_fp4(a, p, d, dtype == ATTN_FP16, interleaved, stream);
+}
+
+size_t attn_decode_fp4_workspace_size(int B, int H, int H_kv, int n_q, int d, int max_seqlen) {
+  if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || n_q < 1 || d < 1 || max_seqlen < 1 ||
+      static_cast<long long>(H / H_kv) * n_q > 128)
+    return 0;
+  return fp4_decode_workspace_bytes(fp4_decode_plan(B, H, H_kv, n_q, max_seqlen), d);
+}
+
+attn_status_t attn_decode_paged_fp4(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                    const void* k_descale, const void* v_descale, const float* hadamard_signs,
+                                    const int* block_table, const int* seq_lens, void* o, float* lse,
+                                    void* workspace, size_t workspace_bytes, int B, int H, int H_kv, int n_q,
+                                    int d, int num_pages, int page_size, int max_pages, int max_seqlen,
+                                    int causal, float softmax_scale, attn_dtype_t dtype,
+                                    cudaStream_t stream) {
+  g_last_error.clear();
+  attn_status_t s;
+  if (H < 1 || n_q < 1 || max_seqlen < 1)
+    return fail(ATTN_ERR_INVALID_ARG, "H, n_q and max_seqlen must be >= 1");
+  if ((s = check_cache(num_pages, page_size, H_kv, d, B, max_pages, 16)) != ATTN_OK) return s;
+  if ((s = check_heads(H, H_kv)) != ATTN_OK) return s;
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "the 4-bit decode supports d = 64 and 128");
+  if (causal != 0 && causal != 1) return fail(ATTN_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (static_cast<long long>(H / H_kv) * n_q > 128)
+    return fail(ATTN_ERR_UNSUPPORTED, "(H / H_kv) * n_q must be <= 128");
+  if (static_cast<double>(B) * H * n_q * d >= 2147483648.0)
+    return fail(ATTN_ERR_INVALID_ARG, "B*H*n_q*d must be < 2^31");
+  if ((s = check_ptrs({q, k_cache, v_cache, o, lse, workspace, k_descale, v_descale})) != ATTN_OK) return s;
+  if (hadamard_signs && !aligned16(hadamard_signs))
+    return fail(ATTN_ERR_INVALID_ARG, "hadamard_signs not 16-byte aligned");
+  if ((s = check_ints({block_table, seq_lens})) != ATTN_OK) return s;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(ATTN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (workspace_bytes < attn_decode_fp4_workspace_size(B, H, H_kv, n_q, d, max_seqlen))
+    return fail(ATTN_ERR_INVALID_ARG, "workspace smaller than attn_decode_fp4_workspace_size()");
+  if ((s = check_scale(softmax_scale)) != ATTN_OK) return s;
+  if ((s = check_dtype(dtype)) != ATTN_OK) return s;
+  if ((s = check_device()) != ATTN_OK) return s;
+  return launch_decode_fp4({q, k_cache, v_cache, static_cast<const uint16_t*>(k_descale),
+                            static_cast<const uint16_t*>(v_descale), hadamard_signs, block_table, seq_lens, o, lse,
+                            workspace, B, H, H_kv, n_q, d, num_pages, page_size, max_pages, max_seqlen, causal,
+                            softmax_scale, dtype == ATTN_FP16 ? 1 : 0},
+                           stream);
+}
+
+// The three forms of reading back; bits: 16, 8 or 4 per stored value.
+static attn_status_t cache_read(const void* k_cache, const void* v_cache, const void* k_descale,
+                                const void* v_descale, const float* signs, const int* block_table,
+                                const int* seq_lens, const int* first, const int* cu_seqlens, void* k_out,
+                                void* v_out, int B, int n, int H_kv, int d, int num_pages, int page_size,
+                                int max_pages, int bits, attn_dtype_t dtype, cudaStream_t stream) {
+  attn_status_t s;
+  if (n < 0) return fail(ATTN_ERR_INVALID_ARG, "n must be >= 0");
+  if ((s = check_cache(num_pages, page_size, H_kv, d, B, max_pages, bits == 16 ? 8 : 16)) != ATTN_OK) return s;
+  if (d != 64 && d != 128 && d != 256) return fail(ATTN_ERR_INVALID_ARG, "d must be 64, 128 or 256");
+  if (bits == 8 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "the FP8 cache supports d = 128");
+  if (bits == 4 && d == 256) return fail(ATTN_ERR_UNSUPPORTED, "the 4-bit cache supports d = 64 and 128");
+  if (static_cast<double>(cu_seqlens ? 1 : B) * n * H_kv * d >= 9.0e15)
+    return fail(ATTN_ERR_INVALID_ARG, "output too large");
+  if ((s = check_dtype(dtype)) != ATTN_OK) return s;
+  if ((s = check_ptrs({k_cache, v_cache})) != ATTN_OK) return s;
+  if (bits < 16 && (s = check_ptrs({k_descale, v_descale})) != ATTN_OK) return s;
+  if (n > 0 && (s = check_ptrs({k_out, v_out})) != ATTN_OK) return s;
+  if (signs && !aligned16(signs)) return fail(ATTN_ERR_INVALID_ARG, "hadamard_signs not 16-byte aligned");
+  if ((s = check_ints({block_table, seq_lens})) != ATTN_OK) return s;
+  if (first && (s = check_ints({first})) != ATTN_OK) return s;
+  if (cu_seqlens && (s = check_ints({cu_seqlens})) != ATTN_OK) return s;
+  if ((s = check_device()) != ATTN_OK) return s;
+  if (n == 0) return ATTN_OK;
+  return launch_cache_read({k_cache, v_cache, k_descale, v_descale, signs, block_table, seq_lens, first, cu_seqlens,
+                            k_out, v_out, B, n, H_kv, num_pages, page_size, max_pages},
+                           bits, d, dtype == ATTN_FP16, stream);
+}
+
+attn_status_t attn_cache_read(const void* k_cache, const void* v_cache, const int* block_table,
+                              const int* seq_lens, const int* first, const int* cu_seqlens, void* k_out,
+                              void* v_out, int B, int n, int H_kv, int d, int num_pages, int page_size,
+                              int max_pages, attn_dtype_t dtype, cudaStream_t stream) {
+  g_last_error.clear();
+  return cache_read(k_cache, v_cache, nullptr, nullptr, nullptr, block_table, seq_lens, first, cu_seqlens, k_out, v_out,
+                    B, n, H_kv, d, num_pages, page_size, max_pages, 16, dtype, stream);
+}
+
+attn_status_t attn_cache_read_fp8(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_descale,
+                                  const float* v_descale, const float* hadamard_signs, const int* block_table,
+                                  const int* seq_lens, const int* first, const int* cu_seqlens, void* k_out,
+                                  void* v_out, int B, int n, int H_kv, int d, int num_pages, int page_size,
+                                  int max_pages, attn_dtype_t dtype, cudaStream_t stream) {
+  g_last_error.clear();
+  return cache_read(k_cache, v_cache, k_descale, v_descale, hadamard_signs, block_table, seq_lens, first, cu_seqlens,
+                    k_out, v_out, B, n, H_kv, d, num_pages, page_size, max_pages, 8, dtype, stream);
+}
+
+attn_status_t attn_cache_read_fp4(const uint8_t* k_cache, const uint8_t* v_cache, const void* k_descale,
+                                  const void* v_descale, const float* hadamard_signs, const int* block_table,
+                                  const int* seq_lens, const int* first, const int* cu_seqlens, void* k_out,
+                                  void* v_out, int B, int n, int H_kv, int d, int num_pages, int page_size,
+                                  int max_pages, attn_dtype_t dtype, cudaStream_t stream) {
+  g_last_error.clear();
+  return cache_read(k_cache, v_cache, k_descale, v_descale, hadamard_signs, block_table, seq_lens, first, cu_seqlens,
+                    k_out, v_out, B, n, H_kv, d, num_pages, page_size, max_pages, 4, dtype, stream);
+}
+
+attn_status_t attn_merge(const void* o_a, const float* lse_a, const void* o_b, const float* lse_b, void* o,
+                         float* lse, int B, int H, int N, int d, int packed, attn_dtype_t dtype,
+                         cudaStream_t stream) {
+  g_last_error.clear();
+  attn_status_t s;
+  if ((s = check_shape(B, H, N, d, 0)) != ATTN_OK) return s;
+  if (packed != 0 && packed != 1) return fail(ATTN_ERR_INVALID_ARG, "packed must be 0 or 1");
+  if (packed && B != 1) return fail(ATTN_ERR_INVALID_ARG, "a packed batch has B = 1");
+  if ((s = check_dtype(dtype)) != ATTN_OK) return s;
+  if ((s = check_ptrs({o_a, o_b, o, lse_a, lse_b, lse})) != ATTN_OK) return s;
+  const size_t rows = static_cast<size_t>(B) * H * N;
+  struct Range {
+    const void* p;
+    size_t bytes;
+  };
+  // a result may be an input's own memory, whole, or none of it
+  const Range ins[] = {{o_a, rows * d * 2}, {o_b, rows * d * 2}, {lse_a, rows * 4}, {lse_b, rows * 4}};
+  const Range outs[] = {{o, rows * d * 2}, {lse, rows * 4}};
+  for (int i = 0; i < 2; ++i)
+    for (int k = 0; k < 4; ++k) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(outs[i].p), y = reinterpret_cast<uintptr_t>(ins[k].p);
+      if (x < y + ins[k].bytes && y < x + outs[i].bytes && !(x == y && i == k / 2))
+        return fail(ATTN_ERR_INVALID_ARG, "o and lse must be an input's o or lse, or not overlap the inputs");
+    }
+  {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(o), y = reinterpret_cast<uintptr_t>(lse);
+    if (x < y + outs[1].bytes && y < x + outs[0].bytes)
+      return fail(ATTN_ERR_INVALID_ARG, "o and lse must not overlap");
+  }
+  if ((s = check_device()) != ATTN_OK) return s;
+  return launch_merge({o_a, lse_a, o_b, lse_b, o, lse, static_cast<long long>(rows), H, N, packed}, d,
+                      dtype == ATTN_FP16, stream);
+}
+
 attn_status_t attn_selftest_wait_timeout(unsigned limit_us, cudaStream_t stream) {
   g_last_error.clear();
   attn_status_t s;

@@ -1,0 +1,253 @@
+// Ranges of positions of a paged cache back as 16-bit rows: out of a 16-bit cache, an e4m3
+// one (a descale per page and head) or a 4-bit one (fp4.cuh).  Keys that were stored
+// transformed, x M with M = diag(signs) H_d / sqrt(d), come back as x: M is orthogonal, so
+// x = (x M) M^T = ((x M) H_d / sqrt(d)) o signs.
+//
+// d / 16 lanes hold a row, 16 neighbouring columns each: 8, 16 or 32 bytes in, 32 out.
+// Bound: DRAM, the writes above all (4 d bytes a key and value against d + 4 read from the
+// 4-bit cache).  A dependent launch: it reads past the L1 cache.
+#include "common.h"
+#include "fp4.cuh"
+#include "rope.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 4;          // rows of a thread, loaded before the first is stored
+
+enum : int { k16 = 0, k8 = 1, k4 = 2 };
+
+// Where a row of the output comes from.
+struct Site {
+  int phys;        // page; -1: the row is written as zeros
+  int off;         // row of the page
+};
+
+// Position `pos` of request b, whose range has been checked against its length.
+__device__ __forceinline__ Site site_of(const CacheReadParams& p, int b, int pos) {
+  const int phys = __ldcg(p.block_table + static_cast<size_t>(b) * p.max_pages + (pos >> p.page_shift));
+  if (phys < 0 || phys >= p.num_pages) {
+    atomicCAS(p.status, 0, kDevBadTables);
+    return {-1, 0};
+  }
+  return {phys, pos & (p.page_size - 1)};
+}
+
+// Length and first position of request b: {0, 0} (reported) for what does not fit.
+__device__ __forceinline__ int2 range_of(const CacheReadParams& p, int b) {
+  const int len = __ldcg(p.seq_lens + b), first = p.first ? __ldcg(p.first + b) : 0;
+  if (len < 0 || len > static_cast<long long>(p.max_pages) * p.page_size || first < 0) {
+    atomicCAS(p.status, 0, kDevBadTables);
+    return make_int2(0, 0);
+  }
+  return make_int2(len, first);
+}
+
+template <int FORMAT>
+struct Raw {
+  uint4 a, b;
+};
+template <>
+struct Raw<k8> {
+  uint4 a;
+  float s;
+};
+template <>
+struct Raw<k4> {
+  uint2 a;
+  float s;
+};
+
+template <int D, int FORMAT>
+__device__ __forceinline__ Raw<FORMAT> load_raw(const CacheReadParams& p, bool is_v, int h, Site at, int u) {
+  const uint8_t* cache = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache);
+  if constexpr (FORMAT == k4) {
+    const size_t row = (static_cast<size_t>(at.phys) * p.H_kv + h) * p.page_size + at.off;
+    const uint16_t* s = static_cast<const uint16_t*>(is_v ? p.v_descale : p.k_descale);
+    return {__ldcg(reinterpret_cast<const uint2*>(cache + row * (D / 2)) + u), bf16_bits(__ldcg(s + row))};
+  } else {
+    const size_t row = (static_cast<size_t>(at.phys) * p.page_size + at.off) * p.H_kv + h;
+    if constexpr (FORMAT == k8) {
+      const float* s = static_cast<const float*>(is_v ? p.v_descale : p.k_descale);
+      return {__ldcg(reinterpret_cast<const uint4*>(cache + row * D) + u),
+              __ldcg(s + static_cast<size_t>(at.phys) * p.H_kv + h)};
+    } else {
+      const uint4* x = reinterpret_cast<const uint4*>(cache + row * (2 * D)) + 2 * u;
+      return {__ldcg(x), __ldcg(x + 1)};
+    }
+  }
+}
+
+template <int FORMAT>
+__device__ __forceinline__ void widen(const Raw<FORMAT>& r, float (&x)[16]) {
+  if constexpr (FORMAT == k4) {
+    const uint32_t w[2] = {r.a.x, r.a.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t h[4];
+      e2m1_halves(w[i], h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+        x[8 * i + 2 * e] = f.x * r.s;
+        x[8 * i + 2 * e + 1] = f.y * r.s;
+      }
+    }
+  } else if constexpr (FORMAT == k8) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t h2;
+      const uint16_t c = static_cast<uint16_t>(w[i / 2] >> (i & 1 ? 16 : 0));
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+      x[2 * i] = f.x * r.s;
+      x[2 * i + 1] = f.y * r.s;
+    }
+  }
+}
+
+// (x H_d / sqrt(d)) o signs: spans 1 .. 8 in the lane, 16 .. d / 2 across lanes.
+template <int D>
+__device__ __forceinline__ void restore_row(float (&x)[16], const float* signs, int u) {
+#pragma unroll
+  for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if ((i & h) == 0) {
+        const float a = x[i], b = x[i + h];
+        x[i] = a + b;
+        x[i + h] = a - b;
+      }
+#pragma unroll
+  for (int m = 1; m < D / 16; m <<= 1) {
+    const float sgn = (u & m) ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = fmaf(sgn, x[i], __shfl_xor_sync(0xffffffffu, x[i], m));
+  }
+  const float scale = D == 128 ? 0.08838834764831845f : 0.125f;
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const float4 s = __ldcg(reinterpret_cast<const float4*>(signs + 16 * u + i));
+    x[i] *= scale * s.x;
+    x[i + 1] *= scale * s.y;
+    x[i + 2] *= scale * s.z;
+    x[i + 3] *= scale * s.w;
+  }
+}
+
+// A block: kRows * kThreads / (d / 16) rows of one head of the keys or the values, of one
+// request (padded output) or of the packed batch.
+template <int D, int FORMAT, bool FP16, bool SIGNS>
+__global__ void __launch_bounds__(kThreads)
+    cache_read_kernel(const CacheReadParams p) {
+  constexpr int L = D / 16, G = kThreads / L;
+  const int u = threadIdx.x % L, mine = threadIdx.x / L;
+  const bool is_v = blockIdx.y & 1;
+  const int h = blockIdx.y >> 1;
+  const long long i0 = static_cast<long long>(blockIdx.x) * (G * kRows) + mine;
+  uint16_t* out = static_cast<uint16_t*>(is_v ? p.v_out : p.k_out) + 16 * u;
+  Site at[kRows];
+  bool write[kRows];
+  wait_for_previous_kernel();
+  if (p.cu_seqlens == nullptr) {
+    const int b = blockIdx.z;
+    const int2 r = range_of(p, b);
+    out += (static_cast<size_t>(b) * p.H_kv + h) * p.n * D;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const long long i = i0 + k * G;
+      write[k] = i < p.n;
+      at[k] = write[k] && r.y + i < r.x ? site_of(p, b, static_cast<int>(r.y + i)) : Site{-1, 0};
+    }
+  } else {
+    out += h * D;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const long long i = i0 + k * G;
+      at[k] = {-1, 0};
+      write[k] = false;
+      if (i >= p.n) continue;
+      // the request that owns row i: the last b with cu_seqlens[b] <= i
+      int lo = 0, hi = p.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldcg(p.cu_seqlens + mid) <= i) lo = mid;
+        else hi = mid;
+      }
+      const int c0 = __ldcg(p.cu_seqlens + lo);
+      write[k] = i >= c0 && i < __ldcg(p.cu_seqlens + lo + 1);      // rows behind the last request stay
+      if (!write[k]) continue;
+      const int2 r = range_of(p, lo);
+      const long long pos = r.y + (i - c0);
+      if (pos < r.x) at[k] = site_of(p, lo, static_cast<int>(pos));
+      else atomicCAS(p.status, 0, kDevBadTables);
+    }
+    // offsets that do not fit
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+      for (int b = threadIdx.x; b < p.B; b += kThreads) {
+        const int c0 = __ldcg(p.cu_seqlens + b), c1 = __ldcg(p.cu_seqlens + b + 1);
+        if (c0 < 0 || c1 < c0 || c1 > p.n || (b == 0 && c0 != 0)) atomicCAS(p.status, 0, kDevBadTables);
+      }
+  }
+  Raw<FORMAT> raw[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    raw[k] = Raw<FORMAT>{};
+    if (at[k].phys >= 0) raw[k] = load_raw<D, FORMAT>(p, is_v, h, at[k], u);
+  }
+  const long long step = p.cu_seqlens == nullptr ? D : static_cast<long long>(p.H_kv) * D;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    uint4 a, b;
+    if constexpr (FORMAT == k16) {
+      a = raw[k].a, b = raw[k].b;
+    } else {
+      float x[16];
+      widen<FORMAT>(raw[k], x);
+      if (SIGNS && !is_v) restore_row<D>(x, p.signs, u);
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i] = FP16 ? cvt_pack_f16(x[2 * i], x[2 * i + 1]) : cvt_pack_bf16(x[2 * i], x[2 * i + 1]);
+      a = make_uint4(w[0], w[1], w[2], w[3]);
+      b = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    if (write[k]) {
+      uint4* dst = reinterpret_cast<uint4*>(out + step * (i0 + k * G));
+      dst[0] = a;
+      dst[1] = b;
+    }
+  }
+}
+
+template <int D, int FORMAT, bool FP16, bool SIGNS>
+attn_status_t launch_t(const CacheReadParams& p, cudaStream_t stream) {
+  constexpr int rows = kThreads / (D / 16) * kRows;
+  const dim3 grid((p.n + rows - 1) / rows, 2 * p.H_kv, p.cu_seqlens ? 1 : p.B);
+  const cudaError_t e = launch_dependent(cache_read_kernel<D, FORMAT, FP16, SIGNS>, grid, kThreads, 0, stream, 0, p);
+  return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "cache read kernel launch");
+}
+
+template <int D, int FORMAT>
+attn_status_t launch_f(const CacheReadParams& p, int fp16, cudaStream_t stream) {
+  if (p.signs) return fp16 ? launch_t<D, FORMAT, true, true>(p, stream) : launch_t<D, FORMAT, false, true>(p, stream);
+  return fp16 ? launch_t<D, FORMAT, true, false>(p, stream) : launch_t<D, FORMAT, false, false>(p, stream);
+}
+
+}  // namespace
+
+attn_status_t launch_cache_read(CacheReadParams p, int format_bits, int d, int fp16, cudaStream_t stream) {
+  p.status = device_status_word();
+  if (!p.status) return fail(ATTN_ERR_CUDA, "status word unavailable");
+  if (2LL * p.H_kv > 65535 || p.B > 65535) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
+  p.page_shift = page_shift_of(p.page_size);
+  if (format_bits == 4) return d == 64 ? launch_f<64, k4>(p, fp16, stream) : launch_f<128, k4>(p, fp16, stream);
+  if (format_bits == 8) return launch_f<128, k8>(p, fp16, stream);
+  return d == 64    ? launch_t<64, k16, false, false>(p, stream)      // moves bits: either type
+         : d == 128 ? launch_t<128, k16, false, false>(p, stream)
+                    : launch_t<256, k16, false, false>(p, stream);
+}
+
+}  // namespace attn

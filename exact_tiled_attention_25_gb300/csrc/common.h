@@ -155,6 +155,13 @@ attn_status_t launch_fwd_fp8(const Fp8FwdParams& p, cudaStream_t stream);
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// log2 of a page size (a power of two).
+inline int page_shift_of(int page_size) {
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return s;
+}
+
 // Backward scratch layout: dQ accumulator, then L*log2(e) and D, each padded
 // to a multiple of 128 rows per head; every part 256-byte aligned.
 struct BwdWorkspace {
@@ -241,6 +248,49 @@ inline size_t decode_workspace_bytes(int B, int H, int H_kv, int n_q, int d, int
 }
 
 attn_status_t launch_decode(const DecodeParams& p, cudaStream_t stream);
+
+// Paged decode over a 4-bit cache (decode_fp4.cu): segments of up to 16 query rows of one
+// key/value head with all of a sequence's keys, in tiles; the tiles of all segments dealt
+// out evenly to `ctas` CTAs.
+struct Fp4DecodeParams {
+  const void* q;              // [B, H, n_q, d]
+  const uint8_t* k_cache;     // [num_pages, H_kv, page_size, d / 2]
+  const uint8_t* v_cache;
+  const uint16_t* k_descale;  // bfloat16 [num_pages, H_kv, page_size]
+  const uint16_t* v_descale;
+  const float* signs;         // or nullptr
+  const int* block_table;     // [B, max_pages]
+  const int* seq_lens;        // [B]
+  void* o;                    // [B, H, n_q, d]
+  float* lse;                 // [B, H, n_q]
+  void* workspace;
+  int B, H, H_kv, n_q, d;
+  int num_pages, page_size, max_pages, max_seqlen;
+  int causal;
+  float scale;
+  int fp16;
+};
+constexpr int kFp4Tile = 128;       // keys of a tile: 32 for each of a CTA's four warps
+struct Fp4DecodePlan {
+  int ctas, qtiles, seg_rows;       // query tiles per key/value head, rows of a tile
+};
+// CTAs of an SM: four where a query tile has at most 8 rows, three of the larger ones
+// (registers).
+inline Fp4DecodePlan fp4_decode_plan(int B, int H, int H_kv, int n_q, int max_seqlen) {
+  const int rows = H / H_kv * n_q;
+  const int seg_rows = rows < 16 ? rows : 16;
+  const int qtiles = (rows + 15) / 16;
+  const double tiles = static_cast<double>(B) * H_kv * qtiles * ((max_seqlen + kFp4Tile - 1) / kFp4Tile);
+  const int most = 152 * (rows <= 8 ? 4 : 3);
+  return {tiles < most ? static_cast<int>(tiles) : most, qtiles, seg_rows};
+}
+// float32 partial O and log-sum-exps of up to two segments per CTA, and 16 bytes on the
+// segment that a CTA leaves to the next.
+inline size_t fp4_decode_workspace_bytes(const Fp4DecodePlan& plan, int d) {
+  const size_t rows = 2ull * plan.ctas * plan.seg_rows;
+  return align_up(rows * d * sizeof(float), 256) + align_up(rows * sizeof(float), 256) + align_up(16ull * plan.ctas, 256);
+}
+attn_status_t launch_decode_fp4(const Fp4DecodeParams& p, cudaStream_t stream);
 
 // How a cross-attention forward runs.  ctas > 0: the rows kernel (cross.cu) on tiles of
 // 128 query rows of one key/value head (its G * N_q rows together), that many CTAs

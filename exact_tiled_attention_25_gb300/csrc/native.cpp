@@ -1,6 +1,6 @@
 // Argument marshalling of the short calls, compiled: the functions of
-// exact_tiled_attention_25_gb300 for cross attention, rotary positions, block tables
-// and cache appends check tensor metadata, allocate outputs and call the C ABI
+// exact_tiled_attention_25_gb300 for cross attention, rotary positions, block tables,
+// cache appends and reads, the 4-bit decode and merges check tensor metadata, allocate outputs and call the C ABI
 // here.  Their kernels take 3 to 10 us in a decode step; the same marshalling in
 // Python with ctypes took 20 to 22 us a call on a Grace core, this 5 to 12.
 //
@@ -36,6 +36,13 @@ struct Api {
   ATTN_FN(attn_block_tables);
   ATTN_FN(attn_cache_append);
   ATTN_FN(attn_cache_append_fp8);
+  ATTN_FN(attn_cache_append_fp4);
+  ATTN_FN(attn_decode_fp4_workspace_size);
+  ATTN_FN(attn_decode_paged_fp4);
+  ATTN_FN(attn_cache_read);
+  ATTN_FN(attn_cache_read_fp8);
+  ATTN_FN(attn_cache_read_fp4);
+  ATTN_FN(attn_merge);
 #undef ATTN_FN
 } api;
 PyObject* on_error = nullptr;      // called with (code, name); raises
@@ -426,12 +433,16 @@ PyObject* block_tables(PyObject* const* a) {
 struct Rows {
   int total, H = 0, H_kv, d;
   long long qs[2] = {0, 0}, ks[2], vs[2];
-  Rows(const Arg& k, const Arg& v, const Arg& q, const Arg& qo, const Arg& cache) {
+  Rows(const Arg& k, const Arg& v, const Arg& q, const Arg& qo, const Arg& cache, bool fp4 = false) {
     require(given(k).t.dim() == 3 && given(v).t.sizes() == k.t.sizes() && is16(k.t) && v.t.scalar_type() == k.t.scalar_type(),
             "k and v must be bfloat16 or float16 [total, H_kv, d]");
     total = extent(k.size(0)), H_kv = extent(k.size(1)), d = extent(k.size(2));
-    require(given(cache).t.dim() == 4 && cache.size(2) == H_kv && cache.size(3) == d,
-            "the caches must be [num_pages, page_size, H_kv, d]");
+    if (fp4)
+      require(given(cache).t.dim() == 4 && cache.size(1) == H_kv && 2 * cache.size(3) == d,
+              "the caches must be [num_pages, H_kv, page_size, d / 2]");
+    else
+      require(given(cache).t.dim() == 4 && cache.size(2) == H_kv && cache.size(3) == d,
+              "the caches must be [num_pages, page_size, H_kv, d]");
     strides(k, ks);
     strides(v, vs);
     require(q || !qo, "q_out without q");
@@ -502,6 +513,152 @@ PyObject* cache_append_fp8(PyObject* const* a) {
   return qo ? THPVariable_Wrap(qo.t) : Py_NewRef(Py_None);
 }
 
+// The 4-bit caches and their descales: codes [num_pages, H_kv, page_size, d / 2].
+void fp4_caches(const Arg& kc, const Arg& vc, const Arg& kd, const Arg& vd) {
+  require(given(kc).t.dim() == 4, "the caches must be [num_pages, H_kv, page_size, d / 2]");
+  like(kc, kc.t.sizes(), at::kByte);
+  like(vc, kc.t.sizes(), at::kByte);
+  like(kd, {kc.size(0), kc.size(1), kc.size(2)}, at::kBFloat16);
+  like(vd, {kc.size(0), kc.size(1), kc.size(2)}, at::kBFloat16);
+}
+
+// k, v, k_cache, v_cache, k_descale, v_descale, slots, rope_cos, rope_sin, positions,
+// hadamard_signs, q, interleaved, q_out, stream
+PyObject* cache_append_fp4(PyObject* const* a) {
+  Arg k("k", a[0]), v("v", a[1]), kc("k_cache", a[2]), vc("v_cache", a[3]), kd("k_descale", a[4]), vd("v_descale", a[5]),
+      slots("slots", a[6]), cos("rope_cos", a[7]), sin("rope_sin", a[8]), pos("positions", a[9]), signs("hadamard_signs", a[10]),
+      q("q", a[11]), qo("q_out", a[13]);
+  const Rows r(k, v, q, qo, kc, true);
+  fp4_caches(kc, vc, kd, vd);
+  like(slots, {r.total}, at::kLong);
+  if (signs) like(signs, {r.d}, at::kFloat);
+  const Tables tab(cos, sin);
+  if (cos) {
+    require(static_cast<bool>(pos), "rotation needs positions");
+    like(pos, {r.total}, at::kInt);
+  }
+  const Device dev(a[14], k, v, kc, vc, kd, vd, slots, cos, sin, pos, signs, q, qo);
+  if (q) dev.output(qo, {r.total, r.H, r.d}, k.t.scalar_type());
+  const int inter = truth(a[12]);
+  call("attn_cache_append_fp4", [&] {
+    return api.attn_cache_append_fp4(q.ptr(), qo.ptr(), k.ptr(), v.ptr(), kc.as<uint8_t>(), vc.as<uint8_t>(), kd.ptr(),
+                                     vd.ptr(), slots.as<long long>(), cos.as<float>(), sin.as<float>(), pos.as<int>(),
+                                     signs.as<float>(), r.total, r.H, r.H_kv, r.d, tab.rot, tab.max_pos, extent(kc.size(0)),
+                                     extent(kc.size(2)), r.qs, r.ks, r.vs, inter, dtype_of(k.t), dev.stream);
+  });
+  return qo ? THPVariable_Wrap(qo.t) : Py_NewRef(Py_None);
+}
+
+// q, k_cache, v_cache, k_descale, v_descale, block_table, seq_lens, hadamard_signs, max_seqlen,
+// causal, softmax_scale, o, lse, workspace, stream
+PyObject* decode_paged_fp4(PyObject* const* a) {
+  Arg q("q", a[0]), kc("k_cache", a[1]), vc("v_cache", a[2]), kd("k_descale", a[3]), vd("v_descale", a[4]),
+      bt("block_table", a[5]), lens("seq_lens", a[6]), signs("hadamard_signs", a[7]), o("o", a[11]), lse("lse", a[12]),
+      ws("workspace", a[13]);
+  require(given(q).t.dim() == 4 && is16(q.t), "q must be bfloat16 or float16 [B, H, n_q, d]");
+  require(q.t.is_contiguous(), "q must be contiguous");
+  fp4_caches(kc, vc, kd, vd);
+  const int B = extent(q.size(0)), H = extent(q.size(1)), n_q = extent(q.size(2)), d = extent(q.size(3)),
+            H_kv = extent(kc.size(1));
+  require(2 * kc.size(3) == d, "q and the caches must share d");
+  require(given(bt).t.dim() == 2 && bt.size(0) == B, "block_table must be [B, max_pages]");
+  like(bt, bt.t.sizes(), at::kInt);
+  like(lens, {B}, at::kInt);
+  if (signs) like(signs, {d}, at::kFloat);
+  const int most = small(a[8], "max_seqlen"), causal = truth(a[9]);
+  const float scale = scale_of(a[10], d);
+  const Device dev(a[14], q, kc, vc, kd, vd, bt, lens, signs, o, lse, ws);
+  dev.output(o, q.t.sizes(), q.t.scalar_type());
+  dev.output(lse, {B, H, n_q}, at::kFloat);
+  dev.workspace(ws, api.attn_decode_fp4_workspace_size(B, H, H_kv, n_q, d, most));
+  call("attn_decode_paged_fp4", [&] {
+    return api.attn_decode_paged_fp4(q.ptr(), kc.as<uint8_t>(), vc.as<uint8_t>(), kd.ptr(), vd.ptr(), signs.as<float>(),
+                                     bt.as<int>(), lens.as<int>(), o.ptr(), lse.as<float>(), ws.ptr(), ws ? ws.t.nbytes() : 0,
+                                     B, H, H_kv, n_q, d, extent(kc.size(0)), extent(kc.size(2)), extent(bt.size(1)), most,
+                                     causal, scale, dtype_of(q.t), dev.stream);
+  });
+  return tuple({&o, &lse});
+}
+
+// bits, k_cache, v_cache, k_descale, v_descale, hadamard_signs, block_table, seq_lens, n, first,
+// cu_seqlens, k_out, v_out, float16 (of a quantised cache), stream
+PyObject* cache_read(PyObject* const* a) {
+  const int bits = small(a[0], "bits");
+  Arg kc("k_cache", a[1]), vc("v_cache", a[2]), kd("k_descale", a[3]), vd("v_descale", a[4]), signs("hadamard_signs", a[5]),
+      bt("block_table", a[6]), lens("seq_lens", a[7]), first("first", a[9]), cu("cu_seqlens", a[10]), ko("k", a[11]),
+      vo("v", a[12]);
+  const int n = small(a[8], "n");
+  require(n >= 0, "n must be >= 0");
+  int heads, page, d;
+  at::ScalarType type;
+  if (bits == 4) {
+    fp4_caches(kc, vc, kd, vd);
+    heads = extent(kc.size(1)), page = extent(kc.size(2)), d = extent(2 * kc.size(3));
+  } else {
+    require(given(kc).t.dim() == 4, "the caches must be [num_pages, page_size, H_kv, d]");
+    heads = extent(kc.size(2)), page = extent(kc.size(1)), d = extent(kc.size(3));
+    if (bits == 8) {
+      like(kd, {kc.size(0), heads}, at::kFloat);
+      like(vd, {kc.size(0), heads}, at::kFloat);
+    } else {
+      require(is16(kc.t), "the caches must be bfloat16 or float16");
+    }
+    like(kc, kc.t.sizes(), bits == 8 ? at::kByte : kc.t.scalar_type());
+    like(vc, kc.t.sizes(), kc.t.scalar_type());
+  }
+  type = bits == 16 ? kc.t.scalar_type() : truth(a[13]) ? at::kHalf : at::kBFloat16;
+  require(given(bt).t.dim() == 2, "block_table must be [B, max_pages]");
+  const int B = extent(bt.size(0));
+  like(bt, bt.t.sizes(), at::kInt);
+  like(lens, {B}, at::kInt);
+  if (first) like(first, {B}, at::kInt);
+  if (cu) like(cu, {B + 1}, at::kInt);
+  if (signs) like(signs, {d}, at::kFloat);
+  const Device dev(a[14], kc, vc, kd, vd, signs, bt, lens, first, cu, ko, vo);
+  for (Arg* x : {&ko, &vo}) {
+    if (cu) dev.output(*x, {n, heads, d}, type);
+    else dev.output(*x, {B, heads, n, d}, type);
+  }
+  const attn_dtype_t dt = type == at::kHalf ? ATTN_FP16 : ATTN_BF16;
+  const int pages = extent(kc.size(0)), max_pages = extent(bt.size(1));
+  call(bits == 16 ? "attn_cache_read" : bits == 8 ? "attn_cache_read_fp8" : "attn_cache_read_fp4", [&] {
+    if (bits == 16)
+      return api.attn_cache_read(kc.ptr(), vc.ptr(), bt.as<int>(), lens.as<int>(), first.as<int>(), cu.as<int>(), ko.ptr(),
+                                 vo.ptr(), B, n, heads, d, pages, page, max_pages, dt, dev.stream);
+    if (bits == 8)
+      return api.attn_cache_read_fp8(kc.as<uint8_t>(), vc.as<uint8_t>(), kd.as<float>(), vd.as<float>(), signs.as<float>(),
+                                     bt.as<int>(), lens.as<int>(), first.as<int>(), cu.as<int>(), ko.ptr(), vo.ptr(), B, n,
+                                     heads, d, pages, page, max_pages, dt, dev.stream);
+    return api.attn_cache_read_fp4(kc.as<uint8_t>(), vc.as<uint8_t>(), kd.ptr(), vd.ptr(), signs.as<float>(), bt.as<int>(),
+                                   lens.as<int>(), first.as<int>(), cu.as<int>(), ko.ptr(), vo.ptr(), B, n, heads, d, pages,
+                                   page, max_pages, dt, dev.stream);
+  });
+  return tuple({&ko, &vo});
+}
+
+// o_a, lse_a, o_b, lse_b, o, lse, stream
+PyObject* merge(PyObject* const* a) {
+  Arg oa("o_a", a[0]), la("lse_a", a[1]), ob("o_b", a[2]), lb("lse_b", a[3]), o("o", a[4]), lse("lse", a[5]);
+  const bool packed = given(oa).t.dim() == 3;
+  require(packed || oa.t.dim() == 4, "o_a must be [B, H, N, d] or packed [total, H, d]");
+  require(is16(oa.t), "o_a and o_b must be bfloat16 or float16");
+  like(oa, oa.t.sizes(), oa.t.scalar_type());
+  like(ob, oa.t.sizes(), oa.t.scalar_type());
+  const int B = packed ? 1 : extent(oa.size(0)), H = extent(oa.size(1)), N = extent(oa.size(packed ? 0 : 2)),
+            d = extent(oa.size(-1));
+  const std::vector<int64_t> rows = packed ? std::vector<int64_t>{H, N} : std::vector<int64_t>{B, H, N};
+  like(la, rows, at::kFloat);
+  like(lb, rows, at::kFloat);
+  const Device dev(a[6], oa, la, ob, lb, o, lse);
+  dev.output(o, oa.t.sizes(), oa.t.scalar_type());
+  dev.output(lse, rows, at::kFloat);
+  call("attn_merge", [&] {
+    return api.attn_merge(oa.ptr(), la.as<float>(), ob.ptr(), lb.as<float>(), o.ptr(), lse.as<float>(), B, H, N, d, packed,
+                          dtype_of(oa.t), dev.stream);
+  });
+  return tuple({&o, &lse});
+}
+
 // bind(path of libattn_gb300.so, on_error): before any other call.
 PyObject* bind(PyObject* const* a) {
   const char* path = PyUnicode_AsUTF8(a[0]);
@@ -520,6 +677,13 @@ PyObject* bind(PyObject* const* a) {
   ATTN_FN(attn_block_tables);
   ATTN_FN(attn_cache_append);
   ATTN_FN(attn_cache_append_fp8);
+  ATTN_FN(attn_cache_append_fp4);
+  ATTN_FN(attn_decode_fp4_workspace_size);
+  ATTN_FN(attn_decode_paged_fp4);
+  ATTN_FN(attn_cache_read);
+  ATTN_FN(attn_cache_read_fp8);
+  ATTN_FN(attn_cache_read_fp4);
+  ATTN_FN(attn_merge);
 #undef ATTN_FN
   PyObject* torch = PyImport_ImportModule("torch");
   PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
@@ -535,7 +699,8 @@ PyObject* bind(PyObject* const* a) {
 PyMethodDef methods[] = {
     ATTN_METHOD(bind, 2),        ATTN_METHOD(cross_fwd, 9),     ATTN_METHOD(cross_bwd, 13),
     ATTN_METHOD(rope_table, 12), ATTN_METHOD(rope, 10),         ATTN_METHOD(block_tables, 12),
-    ATTN_METHOD(cache_append, 12), ATTN_METHOD(cache_append_fp8, 16), {nullptr, nullptr, 0, nullptr}};
+    ATTN_METHOD(cache_append, 12), ATTN_METHOD(cache_append_fp8, 16), ATTN_METHOD(cache_append_fp4, 15),
+    ATTN_METHOD(decode_paged_fp4, 15), ATTN_METHOD(cache_read, 15), ATTN_METHOD(merge, 7), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

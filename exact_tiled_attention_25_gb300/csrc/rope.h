@@ -71,4 +71,62 @@ attn_status_t launch_append_fp8(AppendFp8Params p, RopeKParams q, int fp16, int 
                                 cudaStream_t stream);
 attn_status_t launch_rope(RopeKParams p, int fp16, int interleaved, cudaStream_t stream);
 
+// New keys and values [total, H_kv, d] to the slots of a 4-bit paged cache.
+struct AppendFp4Params {
+  const void* k;
+  const void* v;
+  long long kt, kh, vt, vh;      // element strides of tokens and heads
+  uint8_t* k_cache;              // [num_pages, H_kv, page_size, d / 2]
+  uint8_t* v_cache;
+  uint16_t* k_descale;           // bfloat16 [num_pages, H_kv, page_size]
+  uint16_t* v_descale;
+  const long long* slots;        // [total]
+  const int* positions;          // [total], with tables
+  const float* cos;              // or nullptr
+  const float* sin;
+  const float* signs;            // or nullptr
+  int total, H_kv, num_pages, page_size, rot, max_pos;
+  int page_shift = 0;            // set by the launch
+  long long num_slots = 0;
+  int* status = nullptr;
+};
+// q: query rows to rotate in the same launch (heads[0] = 0: none).
+attn_status_t launch_append_fp4(AppendFp4Params p, const RopeKParams& q, int d, int fp16, int interleaved,
+                                cudaStream_t stream);
+
+// Rows of a paged cache back in 16 bits: [B, H_kv, n, d], or packed [n, H_kv, d] with
+// cu_seqlens.
+struct CacheReadParams {
+  const void* k_cache;
+  const void* v_cache;
+  const void* k_descale;         // by format: none, float32 [num_pages, H_kv], or bfloat16
+  const void* v_descale;         // [num_pages, H_kv, page_size]
+  const float* signs;            // of the keys' transform, or nullptr
+  const int* block_table;        // [B, max_pages]
+  const int* seq_lens;           // [B]
+  const int* first;              // [B] first position read, or nullptr (0)
+  const int* cu_seqlens;         // [B + 1], or nullptr
+  void* k_out;
+  void* v_out;
+  int B, n, H_kv, num_pages, page_size, max_pages;
+  int page_shift = 0;            // set by the launch
+  int* status = nullptr;
+};
+// format_bits: 16, 8 (e4m3) or 4 (e2m1).
+attn_status_t launch_cache_read(CacheReadParams p, int format_bits, int d, int fp16, cudaStream_t stream);
+
+struct MergeParams {
+  const void* o_a;
+  const float* lse_a;
+  const void* o_b;
+  const float* lse_b;
+  void* o;
+  float* lse;
+  long long rows;                // B * H * N, or tokens * H
+  int H;
+  long long tokens;              // packed: of the batch
+  int packed;
+};
+attn_status_t launch_merge(const MergeParams& p, int d, int fp16, cudaStream_t stream);
+
 }  // namespace attn

@@ -769,6 +769,123 @@ attn_status_t attn_cache_append_fp8(const void* q, void* q_out, const void* k, c
                                     int interleaved, attn_dtype_t dtype, cudaStream_t stream);
 
 /*
+ * attn_cache_append_fp4 -- new keys and values into a 4-bit paged cache, one descale per
+ * row (a token's key or value head).
+ *   k, v, q, q_out, strides, slots, tables, positions, interleaved : as attn_cache_append.
+ *                 Keys are rotated (tables given), then multiplied by M = diag(signs)
+ *                 H_d / sqrt(d) (hadamard_signs given: DEVICE float32 [d] of +1 / -1), in
+ *                 float32, then quantised.
+ *   k_cache,
+ *   v_cache     : [num_pages, H_kv, page_size, d / 2] bytes, two e2m1 codes each (OCP E2M1:
+ *                 sign and 0, 0.5, 1, 1.5, 2, 3, 4 or 6), element 2 i of a row in the low
+ *                 half of byte i.  Head by head within a page, unlike the wider caches: a
+ *                 reader of one head finds its rows of a page in one piece.
+ *   k_descale,
+ *   v_descale   : bfloat16 [num_pages, H_kv, page_size].  Value = code x descale.
+ *   For a row x:  descale = amax|x| / 6 rounded up to bfloat16, at least 2^-100 (0 where all
+ *   of x is 0);  code = e2m1_rn(x / descale).  A row that holds an infinity or a NaN gets a
+ *   descale of NaN: it reads back as NaN.
+ *   Rows of other slots stay as they are; a row never depends on its page's others.
+ * d = 64 or 128; page_size a power of two in [16, 65536]; total may be 0.
+ * Source: as attn_cache_append_fp8, with the scale of attn_fp8_quantize on blocks of a row.
+ */
+attn_status_t attn_cache_append_fp4(const void* q, void* q_out, const void* k, const void* v,
+                                    uint8_t* k_cache, uint8_t* v_cache, void* k_descale, void* v_descale,
+                                    const long long* slots, const float* rope_cos, const float* rope_sin,
+                                    const int* positions, const float* hadamard_signs, int total, int H,
+                                    int H_kv, int d, int rot_dim, int max_pos, int num_pages, int page_size,
+                                    const long long* q_strides, const long long* k_strides,
+                                    const long long* v_strides, int interleaved, attn_dtype_t dtype,
+                                    cudaStream_t stream);
+
+/*
+ * attn_decode_fp4_workspace_size -- bytes of device scratch attn_decode_paged_fp4 needs
+ * (float32 partial results of sequences that several blocks share).  Returns 0 for
+ * invalid sizes.
+ */
+size_t attn_decode_fp4_workspace_size(int B, int H, int H_kv, int n_q, int d, int max_seqlen);
+
+/*
+ * attn_decode_paged_fp4 -- attn_decode_paged over the cache of attn_cache_append_fp4.
+ *   q              : [B, H, n_q, d] in `dtype` (bf16 or fp16); used as it is (multiplied by
+ *                    M in float32 when hadamard_signs is given), not quantised.
+ *   k_cache, v_cache, k_descale, v_descale : as attn_cache_append_fp4.
+ *   hadamard_signs : DEVICE float32 [d] of +1 / -1 when the keys were stored transformed,
+ *                    or NULL.  Values are never transformed.
+ *   workspace      : at least attn_decode_fp4_workspace_size() bytes, 256-byte aligned;
+ *                    calls that overlap on the GPU need one each.
+ *   max_seqlen     : >= every seq_lens[b] (sizes the launch and its workspace).
+ *   Other arguments, outputs, masking and device-side error reporting as
+ *   attn_decode_paged; a token on a page that is out of range is not seen.  What the slots
+ *   behind a sequence hold does not matter.
+ * Accuracy: that of 16-bit operands; the stored values enter exactly.  Products of a
+ * probability and a value descale below 2^-26 of a query row's largest lose bits (by up to
+ * 2^-37 of that one).
+ * Limits: d = 64 or 128; (H / H_kv) * n_q <= 128; page_size a power of two in [16, 65536].
+ * Source: as attn_decode_paged_fp8.
+ */
+attn_status_t attn_decode_paged_fp4(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                    const void* k_descale, const void* v_descale, const float* hadamard_signs,
+                                    const int* block_table, const int* seq_lens, void* o, float* lse,
+                                    void* workspace, size_t workspace_bytes, int B, int H, int H_kv, int n_q,
+                                    int d, int num_pages, int page_size, int max_pages, int max_seqlen,
+                                    int causal, float softmax_scale, attn_dtype_t dtype,
+                                    cudaStream_t stream);
+
+/*
+ * attn_cache_read, attn_cache_read_fp8, attn_cache_read_fp4 -- positions of a paged cache
+ * back as contiguous 16-bit rows (a prefix for the prompt's next chunk, a cache to be stored).
+ *   k_cache, v_cache, descales : the cache of attn_cache_append, _fp8 or _fp4.
+ *   hadamard_signs : DEVICE float32 [d] when the keys were stored transformed: they come
+ *                    back as before the transform, ((x M) H_d / sqrt(d)) o signs; or NULL.
+ *   block_table    : DEVICE int32 [B, max_pages];  seq_lens : DEVICE int32 [B].
+ *   first          : DEVICE int32 [B], the first position read of each request, or NULL: 0.
+ *   cu_seqlens     : NULL: k_out, v_out are [B, H_kv, n, d]; row i of request b is position
+ *                    first[b] + i where that is before seq_lens[b], else zeros.
+ *                    DEVICE int32 [B + 1]: k_out, v_out are packed [n, H_kv, d]; row
+ *                    cu_seqlens[b] + i is position first[b] + i; rows behind the last
+ *                    request stay as they are.
+ *   k_out, v_out   : in `dtype` (16-bit cache: the cache's).  Code x descale is formed in
+ *                    float32 and rounded once.
+ * Lengths, offsets or first positions that do not fit, packed rows behind a sequence's end
+ * and pages outside the cache are written as zeros (rows that no request owns are left) and
+ * reported by attn_get_device_status() as ATTN_ERR_INVALID_ARG.
+ * n may be 0.  d and page_size: as the cache's append.
+ * Source: the paged cache of attn_decode_paged, and its cache-to-prefill direction: "FlashAttention
+ * 3 Hardware Acceleration: ...", section "Production Inference Engines" (separate prefill
+ * and decode functions).
+ */
+attn_status_t attn_cache_read(const void* k_cache, const void* v_cache, const int* block_table,
+                              const int* seq_lens, const int* first, const int* cu_seqlens, void* k_out,
+                              void* v_out, int B, int n, int H_kv, int d, int num_pages, int page_size,
+                              int max_pages, attn_dtype_t dtype, cudaStream_t stream);
+attn_status_t attn_cache_read_fp8(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_descale,
+                                  const float* v_descale, const float* hadamard_signs, const int* block_table,
+                                  const int* seq_lens, const int* first, const int* cu_seqlens, void* k_out,
+                                  void* v_out, int B, int n, int H_kv, int d, int num_pages, int page_size,
+                                  int max_pages, attn_dtype_t dtype, cudaStream_t stream);
+attn_status_t attn_cache_read_fp4(const uint8_t* k_cache, const uint8_t* v_cache, const void* k_descale,
+                                  const void* v_descale, const float* hadamard_signs, const int* block_table,
+                                  const int* seq_lens, const int* first, const int* cu_seqlens, void* k_out,
+                                  void* v_out, int B, int n, int H_kv, int d, int num_pages, int page_size,
+                                  int max_pages, attn_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * attn_merge -- the attention over two disjoint sets of keys from that over each:
+ *   lse = log(exp(lse_a) + exp(lse_b)),   o = exp(lse_a - lse) o_a + exp(lse_b - lse) o_b.
+ *   packed = 0 : o_a, o_b, o [B, H, N, d] in `dtype`, log-sum-exps float32 [B, H, N];
+ *   packed = 1 : o_a, o_b, o [N, H, d], log-sum-exps [H, N] (B = 1): as the packed forward.
+ * A part with lse = -inf counts as empty, whatever its o holds; two such give o = 0 and
+ * lse = -inf.  o may be o_a or o_b and lse may be lse_a or lse_b, whole; other overlaps are
+ * refused.  d = 64, 128 or 256; B * H * N * d < 2^31.
+ * Source: "FlashAttention-3: Hopper Asynchrony and FP8 Attention", section "Symbol Map" (L
+ * and O of the running softmax): its update rule between two blocks of keys.
+ */
+attn_status_t attn_merge(const void* o_a, const float* lse_a, const void* o_b, const float* lse_b, void* o,
+                         float* lse, int B, int H, int N, int d, int packed, attn_dtype_t dtype,
+                         cudaStream_t stream);
+
+/*
  * attn_get_device_status -- synchronises `stream`, then reads and clears the
  * current device's status word.  ATTN_OK, ATTN_ERR_TIMEOUT (a kernel gave up
  * on an internal wait; attn_last_error() names the role), ATTN_ERR_INVALID_ARG

@@ -26,6 +26,8 @@ from .decode import (attention_decode_paged, attention_decode_paged_fp8,
                      dequantize_paged_cache, quantize_paged_cache)
 from .serving import (append_fp8, attention_cross_backward, attention_cross_forward, block_tables,
                       key_rows, rope_rotate, rope_table)
+from .fp4 import (E2M1_VALUES, append_fp4, dequantize_cache_fp4, e2m1_decode, e2m1_encode, key_rows_f32,
+                  merge_attention, quantize_rows, read_cache, row_descale)
 
 __all__ = [
     "attention_forward", "attention_backward", "attention_probs", "attention_forward_rows",
@@ -37,4 +39,6 @@ __all__ = [
     "attention_decode_paged_fp8", "quantize_paged_cache", "dequantize_paged_cache",
     "append_fp8", "attention_cross_backward", "attention_cross_forward", "block_tables", "key_rows",
     "rope_rotate", "rope_table",
+    "E2M1_VALUES", "append_fp4", "dequantize_cache_fp4", "e2m1_decode", "e2m1_encode", "key_rows_f32",
+    "merge_attention", "quantize_rows", "read_cache", "row_descale",
 ]
