@@ -127,9 +127,12 @@ __device__ __forceinline__ void rotate_row(float (&x)[16], const Turn& t, int ro
 // x -> (x o signs) H_d / sqrt(d), stages by span: 1, 2, 4 in the lane, 8 .. d / 4 across lanes,
 // d / 2 in the lane.
 template <int D>
-__device__ __forceinline__ void transform_row(float (&x)[16], const float (&sg)[16], int u) {
+__device__ __forceinline__ void transform_row(float (&x)[16], const float* signs, int u) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] *= sg[i];
+  for (int i = 0; i < 16; i += 4) {
+    const float4 s = *reinterpret_cast<const float4*>(signs + (i < 8 ? 0 : D / 2 - 8) + 8 * u + i);
+    x[i] *= s.x, x[i + 1] *= s.y, x[i + 2] *= s.z, x[i + 3] *= s.w;
+  }
 #pragma unroll
   for (int h = 1; h < 8; h <<= 1)
 #pragma unroll
@@ -182,10 +185,11 @@ __device__ __forceinline__ void append_block(const AppendFp4Params& p, long long
       if (turn) load_turn<D, MODE>(tab, p, static_cast<size_t>(pos) * (p.rot / 2), u);
     }
   }
-  float sg[16];
+  __shared__ __align__(16) float signs[SIGNS ? D : 4];
   if (SIGNS && !is_v) {
-    load8(p.signs + 8 * u, sg);
-    load8(p.signs + D / 2 + 8 * u, sg + 8);
+    if (threadIdx.x < D / 4)
+      *reinterpret_cast<float4*>(signs + 4 * threadIdx.x) = __ldcg(reinterpret_cast<const float4*>(p.signs) + threadIdx.x);
+    __syncthreads();
   }
   const int h0 = chunk * per, h1 = min(h0 + per, p.H_kv);
   const uint16_t* src = static_cast<const uint16_t*>(is_v ? p.v : p.k) + (is_v ? p.vt : p.kt) * (live ? t : 0) + 8 * u;
@@ -210,7 +214,7 @@ __device__ __forceinline__ void append_block(const AppendFp4Params& p, long long
     }
     if (!is_v) {                                       // the same for the whole block
       rotate_row<D, MODE>(x, tab, p.rot, turn, u);
-      if constexpr (SIGNS) transform_row<D>(x, sg, u);
+      if constexpr (SIGNS) transform_row<D>(x, signs, u);
     }
     uint32_t top = 0u;
 #pragma unroll
@@ -239,15 +243,17 @@ __device__ __forceinline__ void append_block(const AppendFp4Params& p, long long
 // Query rows are rotated by q_blocks other blocks, spread among these (they are bound by
 // DRAM, the keys' transform by instructions).
 template <int D, bool FP16, int MODE, bool SIGNS>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 7)
     append_fp4_kernel(const AppendFp4Params p, int per, int chunks, const RopeKParams q, unsigned q_blocks,
                       unsigned q_columns) {
   wait_for_previous_kernel();      // a dependent launch: it reads past the L1 cache
   const unsigned before_q = static_cast<unsigned>(static_cast<unsigned long long>(blockIdx.x) * q_blocks / gridDim.x);
   const unsigned with_q = static_cast<unsigned>((blockIdx.x + 1ull) * q_blocks / gridDim.x);
-  if (with_q > before_q) {
-    rope_block<FP16, MODE == kNeighbours, true>(q, before_q % q_columns, before_q / q_columns);
-    return;
+  if constexpr (MODE != kPlain) {
+    if (with_q > before_q) {
+      rope_block<FP16, MODE == kNeighbours, true, 2>(q, before_q % q_columns, before_q / q_columns);
+      return;
+    }
   }
   append_block<D, FP16, MODE, SIGNS>(p, blockIdx.x - before_q, per, chunks);
 }

@@ -3,7 +3,9 @@
 // transformed, x M with M = diag(signs) H_d / sqrt(d), come back as x: M is orthogonal, so
 // x = (x M) M^T = ((x M) H_d / sqrt(d)) o signs.
 //
-// d / 16 lanes hold a row, 16 neighbouring columns each: 8, 16 or 32 bytes in, 32 out.
+// d / 16 lanes hold a row: lane u the columns 8 u .. 8 u + 7 and d / 2 + 8 u .., so that a
+// store of the lanes together is whole sectors (with 16 neighbouring columns each, a store
+// wrote every other half of them).
 // Bound: DRAM, the writes above all (4 d bytes a key and value against d + 4 read from the
 // 4-bit cache).  A dependent launch: it reads past the L1 cache.
 #include "common.h"
@@ -50,12 +52,12 @@ struct Raw {
 };
 template <>
 struct Raw<k8> {
-  uint4 a;
+  uint2 a, b;
   float s;
 };
 template <>
 struct Raw<k4> {
-  uint2 a;
+  uint32_t a, b;
   float s;
 };
 
@@ -65,16 +67,17 @@ __device__ __forceinline__ Raw<FORMAT> load_raw(const CacheReadParams& p, bool i
   if constexpr (FORMAT == k4) {
     const size_t row = (static_cast<size_t>(at.phys) * p.H_kv + h) * p.page_size + at.off;
     const uint16_t* s = static_cast<const uint16_t*>(is_v ? p.v_descale : p.k_descale);
-    return {__ldcg(reinterpret_cast<const uint2*>(cache + row * (D / 2)) + u), bf16_bits(__ldcg(s + row))};
+    const uint32_t* x = reinterpret_cast<const uint32_t*>(cache + row * (D / 2)) + u;
+    return {__ldcg(x), __ldcg(x + D / 16), bf16_bits(__ldcg(s + row))};
   } else {
     const size_t row = (static_cast<size_t>(at.phys) * p.page_size + at.off) * p.H_kv + h;
     if constexpr (FORMAT == k8) {
       const float* s = static_cast<const float*>(is_v ? p.v_descale : p.k_descale);
-      return {__ldcg(reinterpret_cast<const uint4*>(cache + row * D) + u),
-              __ldcg(s + static_cast<size_t>(at.phys) * p.H_kv + h)};
+      const uint2* x = reinterpret_cast<const uint2*>(cache + row * D) + u;
+      return {__ldcg(x), __ldcg(x + D / 16), __ldcg(s + static_cast<size_t>(at.phys) * p.H_kv + h)};
     } else {
-      const uint4* x = reinterpret_cast<const uint4*>(cache + row * (2 * D)) + 2 * u;
-      return {__ldcg(x), __ldcg(x + 1)};
+      const uint4* x = reinterpret_cast<const uint4*>(cache + row * (2 * D)) + u;
+      return {__ldcg(x), __ldcg(x + D / 16)};
     }
   }
 }
@@ -82,7 +85,7 @@ __device__ __forceinline__ Raw<FORMAT> load_raw(const CacheReadParams& p, bool i
 template <int FORMAT>
 __device__ __forceinline__ void widen(const Raw<FORMAT>& r, float (&x)[16]) {
   if constexpr (FORMAT == k4) {
-    const uint32_t w[2] = {r.a.x, r.a.y};
+    const uint32_t w[2] = {r.a, r.b};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t h[4];
@@ -95,7 +98,7 @@ __device__ __forceinline__ void widen(const Raw<FORMAT>& r, float (&x)[16]) {
       }
     }
   } else if constexpr (FORMAT == k8) {
-    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+    const uint32_t w[4] = {r.a.x, r.a.y, r.b.x, r.b.y};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t h2;
@@ -108,11 +111,11 @@ __device__ __forceinline__ void widen(const Raw<FORMAT>& r, float (&x)[16]) {
   }
 }
 
-// (x H_d / sqrt(d)) o signs: spans 1 .. 8 in the lane, 16 .. d / 2 across lanes.
+// (x H_d / sqrt(d)) o signs: spans 1, 2, 4 in the lane, 8 .. d / 4 across lanes, d / 2 in the lane.
 template <int D>
 __device__ __forceinline__ void restore_row(float (&x)[16], const float* signs, int u) {
 #pragma unroll
-  for (int h = 1; h < 16; h <<= 1)
+  for (int h = 1; h < 8; h <<= 1)
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if ((i & h) == 0) {
@@ -128,12 +131,16 @@ __device__ __forceinline__ void restore_row(float (&x)[16], const float* signs, 
   }
   const float scale = D == 128 ? 0.08838834764831845f : 0.125f;
 #pragma unroll
-  for (int i = 0; i < 16; i += 4) {
-    const float4 s = __ldcg(reinterpret_cast<const float4*>(signs + 16 * u + i));
-    x[i] *= scale * s.x;
-    x[i + 1] *= scale * s.y;
-    x[i + 2] *= scale * s.z;
-    x[i + 3] *= scale * s.w;
+  for (int i = 0; i < 8; i += 4) {
+    const float4 s = *reinterpret_cast<const float4*>(signs + 8 * u + i);
+    const float4 r = *reinterpret_cast<const float4*>(signs + D / 2 + 8 * u + i);
+    const float sv[4] = {s.x, s.y, s.z, s.w}, rv[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = x[i + e], b = x[8 + i + e];
+      x[i + e] = (a + b) * (scale * sv[e]);
+      x[8 + i + e] = (a - b) * (scale * rv[e]);
+    }
   }
 }
 
@@ -146,14 +153,23 @@ __global__ void __launch_bounds__(kThreads)
   const int u = threadIdx.x % L, mine = threadIdx.x / L;
   const bool is_v = blockIdx.y & 1;
   const int h = blockIdx.y >> 1;
-  const long long i0 = static_cast<long long>(blockIdx.x) * (G * kRows) + mine;
-  uint16_t* out = static_cast<uint16_t*>(is_v ? p.v_out : p.k_out) + 16 * u;
+  const long long row0 = static_cast<long long>(blockIdx.x) * (G * kRows), i0 = row0 + mine;
+  uint16_t* out = static_cast<uint16_t*>(is_v ? p.v_out : p.k_out) + 8 * u;
   Site at[kRows];
   bool write[kRows];
+  // What every row needs comes through shared memory: read from L2 by each warp, the lines
+  // of the signs and the lengths bounded the kernel (571 us for 8 prefixes of up to 16384).
+  __shared__ __align__(16) float signs[SIGNS ? D : 4];
+  __shared__ int2 range_sh[kThreads];                 // of requests from `lo` on (packed)
+  __shared__ int cu_sh[kThreads + 1];
   wait_for_previous_kernel();
+  if (SIGNS && !is_v && threadIdx.x < D / 4)
+    *reinterpret_cast<float4*>(signs + 4 * threadIdx.x) = __ldcg(reinterpret_cast<const float4*>(p.signs) + threadIdx.x);
   if (p.cu_seqlens == nullptr) {
     const int b = blockIdx.z;
-    const int2 r = range_of(p, b);
+    if (threadIdx.x == kThreads - 1) range_sh[0] = range_of(p, b);
+    __syncthreads();
+    const int2 r = range_sh[0];
     out += (static_cast<size_t>(b) * p.H_kv + h) * p.n * D;
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
@@ -163,25 +179,52 @@ __global__ void __launch_bounds__(kThreads)
     }
   } else {
     out += h * D;
+    // the request that owns the block's first row, by a search with all threads until
+    // kThreads requests are left; those are kept
+    int lo = 0, hi = p.B;
+    while (hi - lo > kThreads) {
+      const int step = (hi - lo + kThreads - 1) / kThreads, probe = lo + static_cast<int>(threadIdx.x) * step;
+      const int below = __syncthreads_count(threadIdx.x == 0 || (probe < hi && __ldcg(p.cu_seqlens + probe) <= row0));
+      lo += (below - 1) * step;
+      hi = min(hi, lo + step);
+    }
+    const int have = min(kThreads, p.B - lo);
+    if (static_cast<int>(threadIdx.x) < have) {
+      cu_sh[threadIdx.x] = __ldcg(p.cu_seqlens + lo + threadIdx.x);
+      range_sh[threadIdx.x] = range_of(p, lo + threadIdx.x);
+    }
+    if (threadIdx.x == 0) cu_sh[have] = __ldcg(p.cu_seqlens + lo + have);
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       const long long i = i0 + k * G;
       at[k] = {-1, 0};
       write[k] = false;
       if (i >= p.n) continue;
-      // the request that owns row i: the last b with cu_seqlens[b] <= i
-      int lo = 0, hi = p.B;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldcg(p.cu_seqlens + mid) <= i) lo = mid;
-        else hi = mid;
+      // the last request that starts at or before row i
+      int a = 0, z = have;
+      while (z - a > 1) {
+        const int mid = (a + z) >> 1;
+        if (cu_sh[mid] <= i) a = mid;
+        else z = mid;
       }
-      const int c0 = __ldcg(p.cu_seqlens + lo);
-      write[k] = i >= c0 && i < __ldcg(p.cu_seqlens + lo + 1);      // rows behind the last request stay
+      int b = lo + a, c0 = cu_sh[a], c1 = cu_sh[a + 1];
+      int2 r = range_sh[a];
+      if (i >= c1 && lo + have < p.B) {
+        // behind the requests at hand (many empty ones)
+        int z2 = p.B;
+        while (z2 - b > 1) {
+          const int mid = (b + z2) >> 1;
+          if (__ldcg(p.cu_seqlens + mid) <= i) b = mid;
+          else z2 = mid;
+        }
+        c0 = __ldcg(p.cu_seqlens + b), c1 = __ldcg(p.cu_seqlens + b + 1);
+        r = range_of(p, b);
+      }
+      write[k] = i >= c0 && i < c1;                    // rows behind the last request stay
       if (!write[k]) continue;
-      const int2 r = range_of(p, lo);
       const long long pos = r.y + (i - c0);
-      if (pos < r.x) at[k] = site_of(p, lo, static_cast<int>(pos));
+      if (pos < r.x) at[k] = site_of(p, b, static_cast<int>(pos));
       else atomicCAS(p.status, 0, kDevBadTables);
     }
     // offsets that do not fit
@@ -203,10 +246,12 @@ __global__ void __launch_bounds__(kThreads)
     uint4 a, b;
     if constexpr (FORMAT == k16) {
       a = raw[k].a, b = raw[k].b;
+    } else if (!__any_sync(0xffffffffu, at[k].phys >= 0)) {
+      a = b = make_uint4(0u, 0u, 0u, 0u);
     } else {
       float x[16];
       widen<FORMAT>(raw[k], x);
-      if (SIGNS && !is_v) restore_row<D>(x, p.signs, u);
+      if (SIGNS && !is_v) restore_row<D>(x, signs, u);
       uint32_t w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -217,7 +262,7 @@ __global__ void __launch_bounds__(kThreads)
     if (write[k]) {
       uint4* dst = reinterpret_cast<uint4*>(out + step * (i0 + k * G));
       dst[0] = a;
-      dst[1] = b;
+      dst[L] = b;
     }
   }
 }

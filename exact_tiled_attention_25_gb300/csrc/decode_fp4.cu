@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   __shared__ float stat_t[W][16], stat_m[W][16], stat_l[W][16];
   __shared__ int buf_sh[W];
   __shared__ long long warp_sum[W], start_sh[2];      // prefix sums; first batch entry and tile in its line
+  __shared__ __align__(16) float signs[LO ? D : 4];
   __shared__ int abort_sh;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -230,6 +231,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   wait_for_previous_kernel();
   release_dependents();
   const Abort ab{&abort_sh, p.status};
+  if (LO && threadIdx.x < D / 4)
+    *reinterpret_cast<float4*>(signs + 4 * threadIdx.x) = __ldcg(reinterpret_cast<const float4*>(p.signs) + threadIdx.x);
 
   // ---- tiles of one segment of the entries before each; this CTA's share
   const int per = (p.B + kThreads - 1) / kThreads;
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       if constexpr (LO) {
 #pragma unroll
         for (int i = 0; i < C::VPL; i += 4) {
-          const float4 s = __ldcg(reinterpret_cast<const float4*>(p.signs + t * C::VPL + i));
+          const float4 s = *reinterpret_cast<const float4*>(signs + t * C::VPL + i);
           v[i] *= s.x, v[i + 1] *= s.y, v[i + 2] *= s.z, v[i + 3] *= s.w;
         }
 #pragma unroll
