@@ -190,6 +190,22 @@ attn_status_t make_tmap_3d(CUtensorMap* map, const void* base, int elem_bytes, u
   return ATTN_OK;
 }
 
+attn_status_t make_tmap_fp4(CUtensorMap* map, const void* base, uint64_t rows, uint64_t heads, uint64_t pages,
+                            uint64_t row_bytes, uint64_t head_bytes, uint64_t page_bytes, uint32_t box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t dims[4] = {128, rows, heads, pages};
+  cuuint64_t strides[3] = {row_bytes, head_bytes, page_bytes};
+  cuuint32_t box[4] = {128, box_rows, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 4, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled (4-bit) failed with CUresult " + std::to_string(r));
+  return ATTN_OK;
+}
+
 attn_status_t make_tmap_4d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t inner,
                            uint64_t rows, uint64_t heads, uint64_t batches, uint64_t row_bytes,
                            uint64_t head_bytes, uint64_t batch_bytes, uint32_t box_inner,
@@ -1060,9 +1076,9 @@ attn_status_t attn_cache_append_fp4(const void* q, void* q_out, const void* k, c
 
 size_t attn_decode_fp4_workspace_size(int B, int H, int H_kv, int n_q, int d, int max_seqlen) {
   if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || n_q < 1 || d < 1 || max_seqlen < 1 ||
-      static_cast<long long>(H / H_kv) * n_q > 128)
+      (d != 64 && d != 128) || static_cast<long long>(H / H_kv) * n_q > 128)
     return 0;
-  return fp4_decode_workspace_bytes(fp4_decode_plan(B, H, H_kv, n_q, max_seqlen), d);
+  return fp4_decode_workspace_bytes(fp4_decode_plan(B, H, H_kv, n_q, d, max_seqlen), d);
 }
 
 attn_status_t attn_decode_paged_fp4(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
@@ -1085,6 +1101,8 @@ attn_status_t attn_decode_paged_fp4(const void* q, const uint8_t* k_cache, const
   if (static_cast<double>(B) * H * n_q * d >= 2147483648.0)
     return fail(ATTN_ERR_INVALID_ARG, "B*H*n_q*d must be < 2^31");
   if ((s = check_ptrs({q, k_cache, v_cache, o, lse, workspace, k_descale, v_descale})) != ATTN_OK) return s;
+  if (((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 31u) != 0)
+    return fail(ATTN_ERR_INVALID_ARG, "k_cache and v_cache must be 32-byte aligned");
   if (hadamard_signs && !aligned16(hadamard_signs))
     return fail(ATTN_ERR_INVALID_ARG, "hadamard_signs not 16-byte aligned");
   if ((s = check_ints({block_table, seq_lens})) != ATTN_OK) return s;

@@ -38,6 +38,12 @@ attn_status_t make_tmap_4d(CUtensorMap* map, const void* base, int elem_bytes, u
                            uint64_t head_bytes, uint64_t batch_bytes, uint32_t box_inner,
                            uint32_t box_rows, uint32_t box_heads = 1);
 
+// 4-D map over {128 4-bit codes, rows, heads, pages} with byte strides (multiples of 32; base
+// 32-byte aligned), box {128, box_rows, 1, 1}: a row's 64 bytes become 128 of shared memory, 128-byte
+// swizzle (a barrier counts the 64).
+attn_status_t make_tmap_fp4(CUtensorMap* map, const void* base, uint64_t rows, uint64_t heads, uint64_t pages,
+                            uint64_t row_bytes, uint64_t head_bytes, uint64_t page_bytes, uint32_t box_rows);
+
 // Launch a kernel that may start before the stream's previous kernel has ended (it
 // calls wait_for_previous_kernel() before it uses that one's results), in clusters of
 // `cluster` blocks when that is given.
@@ -251,7 +257,7 @@ attn_status_t launch_decode(const DecodeParams& p, cudaStream_t stream);
 
 // Paged decode over a 4-bit cache (decode_fp4.cu): segments of up to 16 query rows of one
 // key/value head with all of a sequence's keys, in tiles; the tiles of all segments dealt
-// out evenly to `ctas` CTAs.
+// out evenly to the CTAs.
 struct Fp4DecodeParams {
   const void* q;              // [B, H, n_q, d]
   const uint8_t* k_cache;     // [num_pages, H_kv, page_size, d / 2]
@@ -270,19 +276,14 @@ struct Fp4DecodeParams {
   float scale;
   int fp16;
 };
-constexpr int kFp4Tile = 128;       // keys of a tile: 32 for each of a CTA's four warps
 struct Fp4DecodePlan {
-  int ctas, qtiles, seg_rows;       // query tiles per key/value head, rows of a tile
+  int ctas, qtiles, seg_rows;       // CTAs at most, query tiles per key/value head, rows of a tile
 };
-// CTAs of an SM: four where a query tile has at most 8 rows, three of the larger ones
-// (registers).
-inline Fp4DecodePlan fp4_decode_plan(int B, int H, int H_kv, int n_q, int max_seqlen) {
-  const int rows = H / H_kv * n_q;
-  const int seg_rows = rows < 16 ? rows : 16;
+inline Fp4DecodePlan fp4_decode_plan(int B, int H, int H_kv, int n_q, int d, int max_seqlen) {
+  const int rows = H / H_kv * n_q, tile = 128 * 128 / d;
   const int qtiles = (rows + 15) / 16;
-  const double tiles = static_cast<double>(B) * H_kv * qtiles * ((max_seqlen + kFp4Tile - 1) / kFp4Tile);
-  const int most = 152 * (rows <= 8 ? 4 : 3);
-  return {tiles < most ? static_cast<int>(tiles) : most, qtiles, seg_rows};
+  const double tiles = static_cast<double>(B) * H_kv * qtiles * ((max_seqlen - 1) / tile + 1);
+  return {tiles < 2 * 152 ? static_cast<int>(tiles) : 2 * 152, qtiles, rows < 16 ? rows : 16};
 }
 // float32 partial O and log-sum-exps of up to two segments per CTA, and 16 bytes on the
 // segment that a CTA leaves to the next.

@@ -2,36 +2,36 @@
 // grouped-query heads, keys optionally stored transformed.
 //
 //   S_ij = scale q_i . (k^_j s^k_j),   O_i = sum_j softmax(S)_ij (v^_j s^v_j),
-// with k^, v^ the e2m1 values of a row and s^k, s^v its descales.  A step reads d + 4
-// bytes per token and head and has to turn them into operands at HBM's rate: per SM some 45
-// bytes a nanosecond, 24 codes a clock of each, so what bounds this kernel besides HBM is
-// the number of instructions per code.
+// with k^, v^ the e2m1 values of a row and s^k, s^v its descales.  A step reads d + 4 bytes
+// per token and head; at HBM's rate an SM has some 730 clocks for 128 tokens of a head, their
+// keys and values.
 //
-//  * Codes go from shared memory to the registers of mma.sync as float16 (exact) by one
-//    conversion per two codes.  No dequantised tile is written to shared memory: as 16-bit
-//    operands of tcgen05.mma the tiles would be written and read at four times the bytes of
-//    their codes.  The products are small (16 keys x 8 query rows x 16), and take a third of
-//    what the legacy tensor path gives.
-//  * S^T = K Q^T with the keys on the M side and 8 query rows on N; the order of the d
-//    columns within a product is free, so lane t of a group takes the quarter [t d / 4, + d / 4)
-//    of its key rows with one load.  O^T += V^T P^T: its operand pairs neighbouring keys, so
-//    two rows' conversions are joined by two byte permutes.  P^T comes out of the
-//    accumulators of S^T through movmatrix.
-//  * Queries are scaled by a power of two to [2^14, 2^15) and held as float16: exact for
-//    bfloat16 and float16 queries (up to values 2^-28 below a row's largest).  Transformed
-//    ones are held as the sum of two float16 (LO): one would put 2^-12 of each component
-//    into the scores, which shows in the log-sum-exps of short sequences.
-//  * P is held as float16 of 2^(s + log2 s^v - T + 12), T a running reference of that sum: the
-//    value descale is part of the exponent, as in the e4m3 decode, so it is the tokens that
-//    count for the result which have float16's eleven bits, however their descales differ.  One
-//    whose product is 2^-26 of the largest or less loses bits (an error of 2^-37 of that one).
-//    The row sums are float32 sums of 2^(s - M) with a reference of their own, since s^v may
-//    be 0.  References move only when a value exceeds T by 3 or M by 64.
-//  * Every warp walks alone: its own ring of blocks of 32 keys, filled by bulk copies that it
-//    issues itself, its own statistics and accumulators; no barrier in the loop.  A CTA's
-//    four warps take the blocks of a part of a segment in turn and join at its end.
+//  * The codes are operands of the tensor cores as they are: TMA unpacks a row's 64 bytes to 128
+//    of shared memory (eight bytes of codes and a gap of eight), which kind::f8f6f4 reads as
+//    e2m1, the key tile K-major and the value tile MN-major.  Nothing is dequantised.  (The first
+//    version of this kernel converted the codes to float16 operands of mma.sync in registers, 850
+//    instructions for 32 keys: 57 us for 16 x 8192 tokens of 8 heads, where this takes @@.)
+//  * The products run with the keys on the M side, S^T = K^ Q^T and O^T += V^^T P^T, and both
+//    the queries and the probabilities are the other operand, e4m3.  They are held as sums of
+//    several e4m3 terms, each 2^5 finer than the one before, in columns of their own (a product
+//    this narrow costs what its 128 rows of codes cost, so the columns are free).  A term keeps
+//    four bits and the sign of what is left gives a fifth, so n terms are off by 2^(1 - 5 n):
+//    queries take two in bfloat16 and three in float16, which is exact, and four when they are
+//    transformed (2^-19); probabilities two for a bfloat16 result (2^-9, what bfloat16 itself
+//    would round) and three for a float16 one.
+//  * A thread holds the scores of one key (d = 64: two) for every query row: with 4 rows and
+//    128 keys that are 4 exponentials' pairs a thread, and no lane idles.
+//  * The value descale enters the exponent, as in the e4m3 decode: P' = 2^(s + log2 s^v - T + 5),
+//    T a running reference of that sum, so it is the tokens that count for the result whose
+//    probabilities have all their bits, however the descales differ.  What is 2^-11 of the largest
+//    or less loses bits (an error of 2^-20 of that one; three terms: 2^-14 and 2^-25).  The row
+//    sums are float32 sums of 2^(s - M) with a reference of their own, since s^v may be 0.  References move only when
+//    a value exceeds T by 3 or M by 64, by a vote of the softmax warps once a tile.
+//  * d = 64: rows of two neighbouring tokens are one row of the tile.  Their scores are two
+//    products over half the columns each; in O^T the first 64 lanes take the even tokens' columns
+//    and the others the odd ones', and the two halves are added at the end.
 //  * A segment is up to 16 query rows of a key/value head with all keys of a sequence.  The
-//    128-key tiles of all segments stand in one line, dealt out evenly to the CTAs; segments
+//    tiles of all segments stand in one line, dealt out evenly to the CTAs (two to an SM); segments
 //    that cross shares are joined by a second, dependent kernel from float32 partial results
 //    (at most two per CTA).
 #include <cmath>
@@ -43,26 +43,46 @@
 namespace attn {
 namespace {
 
-constexpr int W = 4;                    // warps of a CTA
-constexpr int kThreads = 32 * W;
-constexpr int BK = 32;                  // keys of a block
-constexpr float kPShift = 12.f;         // P' is 2^12 at the reference, 2^15 at most
+constexpr int kSmemPerSm = 232448;
+constexpr float kPShift = 5.f;          // P' is 2^5 at the reference, 2^8 at most (e4m3: 448)
+constexpr int kPStep = 5;               // a term's steps are 2^-5 of those of the one before
 
-template <int D>
+constexpr int pad16(int n) { return (n + 15) / 16 * 16; }
+constexpr int pow2(int n) {
+  int p = 32;
+  while (p < n) p *= 2;
+  return p;
+}
+
+// NR: query rows of a segment.  TQ, TP: e4m3 terms of queries and of probabilities.
+template <int D, int NR, int TQ, int TP>
 struct Cfg {
-  static constexpr int CODES = BK * D / 2;              // of a block's keys or values
-  static constexpr int KD = 2 * CODES;                  // key descales, then value descales
-  static constexpr int STAGE = 2 * CODES + 4 * BK;
-  static constexpr int VPL = D / 4;                     // columns of a lane in S^T
-  static constexpr int VB = D / 16;                     // bytes of a lane's value rows in O^T
+  static constexpr int KP = 128 / D;                     // tokens of a tile's row
+  static constexpr int TILE = 128 * KP;                  // tokens of a tile
+  static constexpr int SLOT = 128 * 128;                 // its keys' or values' codes, unpacked
+  static constexpr int NS = pad16(NR * TQ), NPV = pad16(NR * TP * KP);
+  static constexpr int CW = NR == 16 ? 2 : 1;            // softmax warps per quarter of the keys
+  static constexpr int SW = 4 * CW;
+  static constexpr int NRW = NR / CW;                    // query rows of a softmax thread
+  static constexpr int LOAD = SW, MMA_S = SW + 1, MMA_PV = SW + 2, QUERY = SW + 3;
+  static constexpr int THREADS = (SW + 4) * 32;
+  static constexpr uint32_t S_COLS = KP * NS;            // of one score buffer
+  __host__ __device__ static constexpr uint32_t S_COL(int buf) { return S_COLS * buf; }
+  __host__ __device__ static constexpr uint32_t O_COL(int buf) { return 2 * S_COLS + NPV * buf; }
+  static constexpr int TMEM = pow2(2 * S_COLS + 2 * NPV);
+  static constexpr int CTAS = NR == 16 ? 1 : 2;          // of an SM (16 rows: registers)
+  static constexpr int Q_TILE = NS * 128, P_TILE = NPV * 128;
+  static constexpr int FIXED = 1024 + 2 * Q_TILE + 2 * P_TILE;
+  static constexpr int PER_CTA = kSmemPerSm / CTAS - 4096;   // (static shared memory and what the system takes)
+  static constexpr int FIT = (PER_CTA - FIXED) / (SLOT + 2 * TILE) / 2 * 2;
+  static constexpr int NSLOT = FIT > 12 ? 12 : FIT;      // even: keys in even slots, values in odd ones
+  static constexpr int DESC_OFF = 2 * Q_TILE + 2 * P_TILE + NSLOT * SLOT;
+  static constexpr int SMEM = 1024 + DESC_OFF + NSLOT / 2 * 4 * TILE;
+  static_assert(NSLOT >= 4 && TMEM * CTAS <= 512, "ring or tensor memory");
 };
-// Ring depth by what fits beside the other CTAs of an SM.
-template <int D, int NT>
-constexpr int kStages = (NT == 1 ? 3 : 4) * (D == 64 ? 2 : 1);
 
 struct KParams {
   const uint16_t* q;
-  const uint8_t* codes[2];
   const uint16_t* descale[2];
   const float* signs;
   const int* block_table;
@@ -74,7 +94,7 @@ struct KParams {
   int4* crossing;         // [C]: the segment whose first part CTA c left unfinished
   int* status;
   int B, H, H_kv, n_q, rows, qtiles, segs, seg_rows;
-  int num_pages, page_size, page_shift, max_pages, causal, fp16;
+  int num_pages, page_size, page_shift, max_pages, causal;
   float scale_log2;
 };
 
@@ -84,18 +104,49 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
-// D (16 x 8, float32) += A (16 x 16, float16) B (16 x 8, float16)
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// Two float32 as e4m3 codes (lo: low byte), and two codes as exact float16.
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
 }
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
-  uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-  return d;
+__device__ __forceinline__ uint32_t e4m3_pair_h(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_halves(uint32_t pair) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(pair)));
+  return h2;
+}
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint32_t half2_bits(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+__device__ __forceinline__ void st_shared_u8(uint32_t saddr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+}
+
+// Whether any of the n threads of named barrier `id` says so.
+__device__ __forceinline__ bool any_of(uint32_t id, uint32_t n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %3, 0;\n barrier.cta.red.or.pred p, %1, %2, q;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 4 || N == 8, "columns");
+  if constexpr (N == 8) tmem_ld8(taddr, r);
+  else tmem_ld4(taddr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
+  if constexpr (N == 8) tmem_st_x8(taddr, r);
+  else tmem_st4(taddr, r);
 }
 
 // Tokens of a sequence; one out of range counts as none.
@@ -103,7 +154,8 @@ __device__ __forceinline__ int tokens_of(const KParams& p, int b) {
   const int n = __ldcg(p.seq_lens + b);
   return n < 0 || n > static_cast<long long>(p.max_pages) * p.page_size ? 0 : n;
 }
-__device__ __forceinline__ int tiles_of(int len) { return (len + kFp4Tile - 1) / kFp4Tile; }
+template <int TILE>
+__device__ __forceinline__ int tiles_of(int len) { return static_cast<int>((static_cast<unsigned>(len) + TILE - 1) / TILE); }
 
 // First tile of CTA c's share of T tiles (at most T CTAs get one).
 __device__ __forceinline__ long long share_start(long long c, int C, long long T) {
@@ -112,11 +164,12 @@ __device__ __forceinline__ long long share_start(long long c, int C, long long T
 }
 
 // A walk over the parts of segments in a share.
+template <int TILE>
 struct Cursor {
   int b, y, j;           // sequence, segment of it, first tile
   int len;
   long long left;        // tiles of the share from here on
-  __device__ __forceinline__ int tiles() const { return tiles_of(len); }
+  __device__ __forceinline__ int tiles() const { return tiles_of<TILE>(len); }
   __device__ __forceinline__ int part() const {
     const int rest = tiles() - j;
     return left < rest ? static_cast<int>(left) : rest;
@@ -134,114 +187,73 @@ struct Cursor {
   }
 };
 
-// The warp's side that fills its ring, ahead of the side that reads it.
-template <int D, int S>
-struct Feeder {
-  using C = Cfg<D>;
-  Cursor cur;
-  int kbeg, kend, n;       // keys of the current part, next of this warp's blocks in it
-  int issued;
-  int win, win_next;       // table entries of this warp's next 32 >> split blocks, and of those behind
-  uint8_t* ring;
-  uint64_t* full;
-  int* flags;              // per stage: pieces that were copied
-  int warp, lane, split;   // split: 1 where a block lies on two pages (of 16)
 
-  // lane: entry of the window's block base + lane >> split
-  __device__ __forceinline__ int window(const KParams& p, int base) const {
-    const int key = kbeg + BK * (warp + W * (base + (lane >> split))) + ((lane & split) << 4);
-    if (key >= kend) return -1;
-    return __ldcg(p.block_table + static_cast<size_t>(cur.b) * p.max_pages + (key >> p.page_shift));
-  }
-  __device__ __forceinline__ void enter(const KParams& p) {
-    kbeg = cur.j * kFp4Tile;
-    kend = min((cur.j + cur.part()) * kFp4Tile, cur.len);
-    n = 0;
-    if (kbeg + BK * warp < kend) {
-      win = window(p, 0);
-      win_next = window(p, 32 >> split);
-    }
-  }
-  // One more block of this warp into its ring stage, if the share has one.
-  __device__ __forceinline__ void issue(const KParams& p) {
-    while (cur.left > 0 && kbeg + BK * (warp + W * n) >= kend) {
-      cur.next_part(p);
-      if (cur.left > 0) enter(p);
-    }
-    if (cur.left <= 0) return;
-    const int key0 = kbeg + BK * (warp + W * n);
-    const int stage = issued % S;
-    const int piece = lane & split, kind = lane >> split;        // kind: codes and descales of K and V
-    const int rows = BK >> split, at = piece * rows;
-    const int in_win = n & ((32 >> split) - 1);
-    const int phys = __shfl_sync(0xffffffffu, win, (in_win << split) + piece);
-    const bool wanted = kind < 4 && key0 + at < kend;
-    const bool ok = wanted && phys >= 0 && phys < p.num_pages;
-    if (wanted && !ok && kind == 0) atomicCAS(p.status, 0, kDevBadSeqlens);
-    const uint32_t copied = __ballot_sync(0xffffffffu, ok) & ((1u << (1 << split)) - 1u);
-    uint8_t* const dst = ring + stage * C::STAGE;
-    if (lane == 0) {
-      flags[stage] = static_cast<int>(copied);
-      mbar_arrive_expect_tx(&full[stage], __popc(copied) * rows * (D + 4));
-    }
-    __syncwarp();
-    if (ok) {
-      const int hk = cur.y / p.qtiles;
-      const size_t row = (static_cast<size_t>(phys) * p.H_kv + hk) * p.page_size + ((key0 + at) & (p.page_size - 1));
-      const int kv = kind & 1;
-      if (kind < 2) bulk_load(dst + kv * C::CODES + at * (D / 2), p.codes[kv] + row * (D / 2), rows * (D / 2), &full[stage]);
-      else bulk_load(dst + C::KD + 2 * BK * kv + 2 * at, p.descale[kv] + row, 2 * rows, &full[stage]);
-    }
-    ++issued;
-    ++n;
-    if ((n & ((32 >> split) - 1)) == 0) {
-      win = win_next;
-      win_next = window(p, n + (32 >> split));
-    }
-  }
-};
+template <int D, int NR, int TQ, int TP, bool FP16, bool SIGNS>
+__global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP>::CTAS)
+    decode_fp4_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const KParams p) {
+  using C = Cfg<D, NR, TQ, TP>;
+  constexpr int NSLOT = C::NSLOT, KP = C::KP, TILE = C::TILE, NRW = C::NRW;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* const sQ = smem;                              // two query tiles, NS x 128 bytes
+  uint8_t* const sP = smem + 2 * C::Q_TILE;              // two tiles of P', NPV x 128 bytes (keys)
+  uint8_t* const sKV = sP + 2 * C::P_TILE;
+  uint8_t* const sDesc = smem + C::DESC_OFF;             // per key slot: TILE key descales, TILE value descales
 
-// Key of row r (0 .. 7) of an 8-row half of a product's M side: with this order the four
-// value rows that the lanes of a group read at a time, and the key rows of neighbouring
-// groups, lie in different banks as far as rows of 64 bytes allow (of 32 bytes: wholly).
-__device__ __forceinline__ int key_row(int r) { return r < 4 ? r : r ^ 1; }
-
-template <int D, int NT, bool LO>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
-    decode_fp4_kernel(const KParams p) {
-  using C = Cfg<D>;
-  constexpr int S = kStages<D, NT>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t full[W][S];
-  __shared__ int flags[W][S];
-  __shared__ float stat_t[W][16], stat_m[W][16], stat_l[W][16];
-  __shared__ int buf_sh[W];
-  __shared__ long long warp_sum[W], start_sh[2];      // prefix sums; first batch entry and tile in its line
-  __shared__ __align__(16) float signs[LO ? D : 4];
-  __shared__ int abort_sh;
+  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], kv_full[NSLOT], kv_empty[NSLOT], s_full[2], p_full[2], o_full[2],
+      o_empty[2], drain_bar[2];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh, issued_sh[2];                 // key and value tiles whose copies have been issued
+  __shared__ long long warp_sum[C::THREADS / 32], start_sh[2];
+  __shared__ unsigned there_sh[NSLOT / 2];               // boxes of a key tile that were copied
+  __shared__ float cq_sh[2][NR];                         // score coefficient of a query row
+  __shared__ float red_sh[2][4][NR];                     // maxima of a tile by key quarter; row sums of a part
+  __shared__ float l_sh[2][4][NR];
+  __shared__ float xch_sh[KP == 2 ? NR : 1][KP == 2 ? 64 : 1];
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int g = lane >> 2, t = lane & 3;
   if (threadIdx.x == 0) {
-    for (int w = 0; w < W; ++w)
-      for (int s = 0; s < S; ++s) mbar_init(&full[w][s], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1 + C::SW);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], C::SW);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_empty[i], C::SW);
+      mbar_init(&drain_bar[i], 1);
+    }
+    for (int s = 0; s < NSLOT; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], s & 1 ? 1 : C::SW);
+    }
     abort_sh = 0;
+    issued_sh[0] = issued_sh[1] = 0;
     fence_mbar_init();
   }
+  if (warp == C::MMA_S) {
+    tmem_alloc(&tmem_base_sh, C::TMEM);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == C::LOAD * 32) {
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  // columns that no row of queries or of P' fills stay zero
+  for (int i = threadIdx.x; i < (2 * C::Q_TILE + 2 * C::P_TILE) / 16; i += C::THREADS)
+    reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   wait_for_previous_kernel();
   release_dependents();
-  const Abort ab{&abort_sh, p.status};
-  if (LO && threadIdx.x < D / 4)
-    *reinterpret_cast<float4*>(signs + 4 * threadIdx.x) = __ldcg(reinterpret_cast<const float4*>(p.signs) + threadIdx.x);
 
   // ---- tiles of one segment of the entries before each; this CTA's share
-  const int per = (p.B + kThreads - 1) / kThreads;
+  const int per = (p.B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
   long long sum = 0;
   for (int b = b0; b < b1; ++b) {
     const int len = tokens_of(p, b);
     if (len == 0 && blockIdx.x == 0 && __ldcg(p.seq_lens + b) != 0) atomicCAS(p.status, 0, kDevBadSeqlens);
-    sum += tiles_of(len);
+    sum += tiles_of<TILE>(len);
   }
   long long scan = sum;
 #pragma unroll
@@ -252,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   if (lane == 31) warp_sum[warp] = scan;
   __syncthreads();
   long long base = scan - sum, all = 0;
-  for (int w = 0; w < W; ++w) {
+  for (int w = 0; w < C::THREADS / 32; ++w) {
     if (w < warp) base += warp_sum[w];
     all += warp_sum[w];
   }
@@ -262,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   if (total > 0 && base * p.segs <= g0 && g0 < (base + sum) * p.segs) {
     int b = b0;
     while (true) {
-      const int n = tiles_of(tokens_of(p, b));
+      const int n = tiles_of<TILE>(tokens_of(p, b));
       if (g0 < (base + n) * p.segs) break;
       base += n;
       ++b;
@@ -270,388 +282,542 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     start_sh[0] = b;
     start_sh[1] = g0 - base * p.segs;
   }
+  tc_fence_before_sync();
   __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = tmem_base_sh;
+  const Abort ab{&abort_sh, p.status};
 
   // batch entries without tokens: O = 0, LSE = -inf
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (tokens_of(p, b) != 0) continue;
     const size_t rows_b = static_cast<size_t>(p.H) * p.n_q;
     uint4* dst = reinterpret_cast<uint4*>(p.o + b * rows_b * D);
-    for (size_t i = threadIdx.x; i < rows_b * (D / 8); i += kThreads) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (size_t i = threadIdx.x; i < rows_b; i += kThreads) p.lse[b * rows_b + i] = -INFINITY;
+    for (size_t i = threadIdx.x; i < rows_b * (D / 8); i += C::THREADS) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (size_t i = threadIdx.x; i < rows_b; i += C::THREADS) p.lse[b * rows_b + i] = -INFINITY;
   }
-  int4 crossing = make_int4(0, 0, 0, -1);
-  if (total == 0) {
-    if (threadIdx.x == 0) p.crossing[blockIdx.x] = crossing;
-    return;
-  }
-
-  Cursor cur;
-  cur.b = static_cast<int>(start_sh[0]);
-  cur.len = tokens_of(p, cur.b);
-  cur.left = total;
-  {
+  Cursor<TILE> cur{0, 0, 0, 0, total};
+  if (total > 0) {
+    cur.b = static_cast<int>(start_sh[0]);
+    cur.len = tokens_of(p, cur.b);
     const int n = cur.tiles();
     cur.y = static_cast<int>(start_sh[1] / n);
     cur.j = static_cast<int>(start_sh[1] - static_cast<long long>(cur.y) * n);
   }
-  uint8_t* const ring = smem + warp * S * C::STAGE;
-  Feeder<D, S> feed;
-  feed.cur = cur;
-  feed.issued = 0;
-  feed.ring = ring;
-  feed.full = full[warp];
-  feed.flags = flags[warp];
-  feed.warp = warp;
-  feed.lane = lane;
-  feed.split = p.page_size < BK ? 1 : 0;
-  feed.enter(p);
+  // The ring slot of a tile's keys (even) or values (odd), and the phase of its barriers' use.
+  struct Slot {
+    int at;
+    uint32_t phase;
+    __device__ __forceinline__ void next() {
+      at += 2;
+      if (at >= NSLOT) {
+        at -= NSLOT;
+        phase ^= 1u;
+      }
+    }
+  };
+
+  if (warp == C::LOAD) {
+    // ------------------------------------------------------------ producer
+    // A tile is fetched page by page: a box is min(page_size, TILE) tokens of one page, at most
+    // 16 of them.  Lane x issues box x; of a key tile, lanes 16 + x the descales of both the
+    // keys and the values.  The pages of 32 boxes are read from the block table at a time, the
+    // next 32 while those are in use.  Boxes behind the sequence are left out, as are those on
+    // pages outside the cache (reported): what the slot held before is finite codes, and their
+    // tokens are masked.
+    const int box = min(p.page_size, TILE), nbox = TILE / box;
+    int n = 0;
+    Slot key_slot{0, 0u};
+    bool ok = true;
+    while (ok && cur.left > 0) {
+      const int take = cur.part(), hk = cur.y / p.qtiles, kbeg = cur.j * TILE;   // kbeg < len
+      auto window = [&](int w) -> int {
+        const long long key = kbeg + static_cast<long long>(32 * w + lane) * box;
+        if (key >= cur.len || 32 * w + lane >= take * nbox) return -1;
+        return __ldcg(p.block_table + static_cast<size_t>(cur.b) * p.max_pages + (key >> p.page_shift));
+      };
+      int win = window(0), win_next = window(1);
+      for (int i = 0; ok && i < take; ++i, ++n, key_slot.next()) {
+        if (i > 0 && ((i * nbox) & 31) == 0) {
+          win = win_next;
+          win_next = window(i * nbox / 32 + 1);
+        }
+        const int x = lane & 15;
+        const int phys = __shfl_sync(0xffffffffu, win, (i * nbox + x) & 31);
+        const long long key = static_cast<long long>(kbeg) + i * TILE + x * box;
+        const bool wanted = x < nbox && key < cur.len;
+        const bool good = wanted && phys >= 0 && phys < p.num_pages;
+        if (wanted && !good && lane < 16) atomicCAS(p.status, 0, kDevBadSeqlens);
+        const unsigned there = __ballot_sync(0xffffffffu, good) & 0xffffu;
+        const int off = static_cast<int>(key) & (p.page_size - 1);
+        for (int kv = 0; kv < 2; ++kv) {
+          const int slot = key_slot.at + kv;
+          int go = 1;
+          if (lane == 0) {
+            if (n >= NSLOT / 2 && !mbar_wait(&kv_empty[slot], key_slot.phase ^ 1u, ab, kDevTimeoutLoad)) {
+              go = 0;
+            } else {
+              if (kv == 0) there_sh[slot / 2] = there;
+              mbar_arrive_expect_tx(&kv_full[slot], __popc(there) * box * (D / 2 + (kv == 0 ? 4 : 0)));
+              issued_sh[kv] = n + 1;
+            }
+          }
+          if (!__shfl_sync(0xffffffffu, go, 0)) {
+            ok = false;
+            break;
+          }
+          if (!good) continue;
+          if (lane < 16) {
+            tma_load_4d(sKV + slot * C::SLOT + x * (box / KP) * 128, kv ? &tmV : &tmK, &kv_full[slot], 0, off / KP, hk, phys);
+          } else if (kv == 0) {
+            uint8_t* dst = sDesc + slot / 2 * 4 * TILE + 2 * x * box;
+            const size_t row = (static_cast<size_t>(phys) * p.H_kv + hk) * p.page_size + off;
+            bulk_load(dst, p.descale[0] + row, 2 * box, &kv_full[slot]);
+            bulk_load(dst + 2 * TILE, p.descale[1] + row, 2 * box, &kv_full[slot]);
+          }
+        }
+      }
+      cur.next_part(p);
+    }
+  } else if (warp == C::MMA_S) {
+    // ------------------------------------------------------------ S^T = K^ Q^T
+    // S(n) into buffer n % 2, once P' V(n - 2) has been formed (the phase of that value slot's
+    // empty barrier): the softmax has read the buffer by then, and may overwrite P'(n - 2).
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_e2m1_e4m3(128, C::NS, false);
+      const uint64_t qdesc0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t kdesc0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
+      bool ok = true;
+      int n = 0;
+      Slot key{0, 0u}, old{1, 0u};          // old: the values of tile n - 2
+      for (int part = 0; ok && cur.left > 0; ++part) {
+        const int take = cur.part();
+        if (!(ok = mbar_wait(&q_full[part & 1], (part >> 1) & 1, ab, kDevTimeoutMma))) break;
+        const uint64_t qdesc = opaque(sdesc_add(qdesc0, (part & 1) * C::Q_TILE));
+        for (int i = 0; i < take; ++i, ++n, key.next()) {
+          if (!(ok = mbar_wait(&kv_full[key.at], key.phase, ab, kDevTimeoutMma))) break;
+          if (n >= 2) {
+            if (!(ok = mbar_wait(&kv_empty[old.at], old.phase, ab, kDevTimeoutMma))) break;
+            old.next();
+          }
+          tc_fence_after_sync();
+          const uint64_t kdesc = opaque(sdesc_add(kdesc0, key.at * C::SLOT));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            // d = 64: two 32-column steps for the even tokens, two for the odd ones
+            constexpr int steps = D / 32;
+            mma_f8_ss(tmem + C::S_COL(n & 1) + kk / steps * C::NS, sdesc_add(kdesc, kk * 32),
+                      sdesc_add(qdesc, kk % steps * 32), id, kk % steps > 0 ? 1u : 0u);
+          }
+          mma_commit(&s_full[n & 1]);
+        }
+        if (ok) mma_commit(&q_empty[part & 1]);
+        cur.next_part(p);
+      }
+    }
+  } else if (warp == C::MMA_PV) {
+    // ------------------------------------------------------------ O^T += V^^T P'^T
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_e2m1_e4m3(128, C::NPV, true);
+      const uint64_t pdesc0 = sdesc_sw128(smem_u32(sP), 16, 1024);
+      const uint64_t vdesc0 = sdesc_sw128(smem_u32(sKV), C::SLOT, 1024);
+      bool ok = true;
+      int n = 0;
+      Slot val{1, 0u};
+      for (int part = 0; ok && cur.left > 0; ++part) {
+        const int take = cur.part();
+        const uint32_t o_col = C::O_COL(part & 1);
+        for (int i = 0; i < take; ++i, ++n, val.next()) {
+          if (!(ok = mbar_wait(&kv_full[val.at], val.phase, ab, kDevTimeoutMma))) break;
+          const uint64_t vdesc = opaque(sdesc_add(vdesc0, val.at * C::SLOT));
+          if (!(ok = mbar_wait(&p_full[n & 1], (n >> 1) & 1, ab, kDevTimeoutMma))) break;
+          // the buffer's output of two parts ago has been read
+          if (i == 0 && part >= 2 && !(ok = mbar_wait(&o_empty[part & 1], ((part >> 1) - 1) & 1, ab, kDevTimeoutMma))) break;
+          tc_fence_after_sync();
+          const uint64_t pdesc = sdesc_add(pdesc0, (n & 1) * C::P_TILE);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f8_ss(tmem + o_col, sdesc_add(vdesc, kk * 32 * 128), sdesc_add(pdesc, kk * 32), id,
+                      (i > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&kv_empty[val.at]);      // every use of a value slot gets its phase
+          if (i == take - 1) mma_commit(&o_full[part & 1]);
+        }
+        cur.next_part(p);
+      }
+    }
+  } else if (warp == C::QUERY) {
+    // ------------------------------------------------------------ query rows as e4m3 terms
+    // d / 16 lanes hold a row, 16 neighbouring columns each.
+    constexpr int L = D / 16, PER = 32 / L;
+    const int u = lane % L;
+    bool ok = true;
+    for (int part = 0; ok && cur.left > 0; ++part) {
+      const int buf = part & 1;
+      if (part >= 2 && __any_sync(0xffffffffu, !mbar_wait(&q_empty[buf], ((part >> 1) - 1) & 1, ab, kDevTimeoutLoad))) {
+        ok = false;
+        break;
+      }
+      const int hk = cur.y / p.qtiles, row0 = (cur.y - hk * p.qtiles) * 16;
+      const size_t at0 = (static_cast<size_t>(cur.b) * p.H_kv + hk) * p.rows + row0;
+      const int rows_here = min(NR, p.rows - row0);
 #pragma unroll 1
-  for (int i = 0; i < S; ++i) feed.issue(p);
-
-  int used = 0;                 // blocks that this warp has read
-  bool ok = true;
-  bool first_part = true;
-  long long at_tile = g0;
-  while (cur.left > 0) {
-    const int take = cur.part(), nt_tiles = cur.tiles(), len = cur.len;
-    const int kbeg = cur.j * kFp4Tile, kend = min((cur.j + take) * kFp4Tile, len);
-    const int hk = cur.y / p.qtiles, row0 = (cur.y - hk * p.qtiles) * 16;
-    // rows of a key/value head are contiguous in [B, H, n_q]
-    const size_t at0 = (static_cast<size_t>(cur.b) * p.H_kv + hk) * p.rows + row0;
-    const int rows_here = min(16, p.rows - row0);
-
-    // ---- query rows as operands: lane (g, t) of tile x the columns [t VPL, + VPL) of row 8 x + g
-    uint32_t qh[NT][D / 16][2], ql[LO ? NT : 1][LO ? D / 16 : 1][2];
-    float cq[NT][2];             // score coefficient of the lane's two query columns
-    int vend[NT][2];             // keys [0, vend) visible to them
+      for (int r0 = 0; r0 < NR; r0 += PER) {
+        const int r = r0 + lane / L;
+        const bool live = r < rows_here;
+        float x[16];
+        {
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + (at0 + (live ? r : 0)) * D + 16 * u);
+          float lo[8], hi[8];
+          unpack16<FP16>(__ldcg(src), lo);
+          unpack16<FP16>(__ldcg(src + 1), hi);
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
-      float v[C::VPL];
-      const int r = 8 * x + g;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (at0 + (r < rows_here ? r : 0)) * D + t * C::VPL);
-#pragma unroll
-      for (int i = 0; i < C::VPL / 8; ++i) {
-        const uint4 w = __ldcg(src + i);
-        float f[8];
-        if (p.fp16) unpack16<true>(w, f);
-        else unpack16<false>(w, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 * i + e] = r < rows_here ? f[e] : 0.f;
-      }
-      if constexpr (LO) {
-#pragma unroll
-        for (int i = 0; i < C::VPL; i += 4) {
-          const float4 s = *reinterpret_cast<const float4*>(signs + t * C::VPL + i);
-          v[i] *= s.x, v[i + 1] *= s.y, v[i + 2] *= s.z, v[i + 3] *= s.w;
+          for (int i = 0; i < 8; ++i) x[i] = live ? lo[i] : 0.f, x[8 + i] = live ? hi[i] : 0.f;
         }
+        if constexpr (SIGNS) {
 #pragma unroll
-        for (int h = 1; h < C::VPL; h <<= 1)
-#pragma unroll
-          for (int i = 0; i < C::VPL; ++i)
-            if ((i & h) == 0) {
-              const float a = v[i], b = v[i + h];
-              v[i] = a + b;
-              v[i + h] = a - b;
-            }
-#pragma unroll
-        for (int m = 1; m < 4; m <<= 1) {
-          const float sgn = (t & m) ? -1.f : 1.f;
-#pragma unroll
-          for (int i = 0; i < C::VPL; ++i) v[i] = fmaf(sgn, v[i], __shfl_xor_sync(0xffffffffu, v[i], m));
-        }
-        const float isd = D == 128 ? 0.08838834764831845f : 0.125f;
-#pragma unroll
-        for (int i = 0; i < C::VPL; ++i) v[i] *= isd;
-      }
-      uint32_t top = 0u;
-#pragma unroll
-      for (int i = 0; i < C::VPL; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // times 2^(14 - floor(log2 top)): an infinity stays one
-      const int e = static_cast<int>(top >> 23);
-      const int up = top == 0u ? 127 : min(268 - e, 254);
-      const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
-      const float back = __uint_as_float(static_cast<uint32_t>(max(254 - up, 1)) << 23);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float a = v[4 * kk + 2 * i] * f, b = v[4 * kk + 2 * i + 1] * f;
-          const uint32_t h = cvt_pack_f16(a, b);
-          qh[x][kk][i] = h;
-          if constexpr (LO) {
-            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            ql[x][kk][i] = cvt_pack_f16(a - hf.x, b - hf.y);
+          for (int i = 0; i < 16; i += 4) {
+            const float4 s = __ldcg(reinterpret_cast<const float4*>(p.signs + 16 * u + i));
+            x[i] *= s.x, x[i + 1] *= s.y, x[i + 2] *= s.z, x[i + 3] *= s.w;
           }
-        }
-      const float c_row = p.scale_log2 * back;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        cq[x][i] = __shfl_sync(0xffffffffu, c_row, (2 * t + i) * 4);
-        const int rr = 8 * x + 2 * t + i, tq = (row0 + rr) % p.n_q;
-        vend[x][i] = rr < rows_here ? (p.causal ? min(len, len - p.n_q + tq + 1) : len) : 0;
+          for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if ((i & h) == 0) {
+                const float a = x[i], b = x[i + h];
+                x[i] = a + b;
+                x[i + h] = a - b;
+              }
+#pragma unroll
+          for (int m = 1; m < L; m <<= 1) {
+            const float sgn = (u & m) ? -1.f : 1.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = fmaf(sgn, x[i], __shfl_xor_sync(0xffffffffu, x[i], m));
+          }
+          const float isd = D == 128 ? 0.08838834764831845f : 0.125f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] *= isd;
+        }
+        uint32_t top = 0u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int m = 1; m < L; m <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+        // times 2^(7 - floor(log2 top)); a row with an infinity or a NaN gets a coefficient of NaN
+        const int e = static_cast<int>(top >> 23);
+        const int up = top == 0u ? 127 : min(261 - e, 254);
+        const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
+        const float back = e == 255 ? __uint_as_float(0x7FFFFFFFu)
+                                    : __uint_as_float(static_cast<uint32_t>(max(254 - up, 1)) << 23);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] *= f;
+#pragma unroll
+        for (int k = 0; k < TQ; ++k) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a = e4m3_pair(x[4 * i], x[4 * i + 1]), b = e4m3_pair(x[4 * i + 2], x[4 * i + 3]);
+            w[i] = a | (b << 16);
+            if (k + 1 < TQ) {
+              const float2 fa = __half22float2(as_half2(e4m3_halves(a))), fb = __half22float2(as_half2(e4m3_halves(b)));
+              x[4 * i] = (x[4 * i] - fa.x) * (1 << kPStep);
+              x[4 * i + 1] = (x[4 * i + 1] - fa.y) * (1 << kPStep);
+              x[4 * i + 2] = (x[4 * i + 2] - fb.x) * (1 << kPStep);
+              x[4 * i + 3] = (x[4 * i + 3] - fb.y) * (1 << kPStep);
+            }
+          }
+          const int col = k * NR + r;
+          if (r < NR)
+            st_shared_v4(smem_u32(sQ + buf * C::Q_TILE + col * 128 + ((u ^ (col & 7)) << 4)), w[0], w[1], w[2], w[3]);
+        }
+        if (u == 0 && r < NR) cq_sh[buf][r] = p.scale_log2 * back;
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[buf]);
+      cur.next_part(p);
     }
-
-    float o[C::VB][NT][4];
-    float tref[NT][2], mref[NT][2], lsum[NT][2];
+  } else {
+    // ------------------------------------------------------------ softmax
+    // Thread (quarter, lane): tile row t, of KP tokens; query rows [r0, r0 + NRW); in O^T
+    // the lane t of those rows' columns.
+    const int t = (warp & 3) * 32 + lane, cg = warp >> 2, r0 = cg * NRW;
+    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    constexpr uint32_t BAR = 1, MEMBERS = 32 * C::SW;
+    const int box_shift = min(p.page_shift, KP == 2 ? 8 : 7);
+    const unsigned all_boxes = 0xFFFFu >> (16 - (TILE >> box_shift));
+    const int o_half = KP == 2 && (warp & 2) ? NR * TP : 0;    // columns that hold this lane's sums
+    bool ok = true;
+    int4 crossing = make_int4(0, 0, 0, -1);
+    long long at_tile = g0;
+    // output of a finished part: where it goes, and its rows' references
+    struct Done {
+      int part, rows;
+      bool whole;
+      size_t at0, slot;
+      float tref[NRW], mref[NRW];
+    } done;
+    done.part = -1;
+    // Every softmax thread comes here at the same point, also after giving up (the barriers).
+    auto write_out = [&]() {
+      const int buf = done.part & 1;
+      if (__any_sync(0xffffffffu, !mbar_wait(&o_full[buf], (done.part >> 1) & 1, ab, kDevTimeoutEpilogue))) ok = false;
+      tc_fence_after_sync();
+      float o[NRW];
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
+      for (int i = 0; i < NRW; ++i) o[i] = 0.f;
 #pragma unroll
-      for (int i = 0; i < C::VB; ++i)
+      for (int k = TP - 1; k >= 0; --k) {
+        uint32_t raw[NRW];
+        tmem_ld_cols<NRW>(tmem + lane_addr + C::O_COL(buf) + o_half + k * NR + r0, raw);
+        tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][x][e] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) tref[x][e] = mref[x][e] = -INFINITY, lsum[x][e] = 0.f;
-    }
-
-    bool owed = false;            // the last block's stage is refilled after the part's end
-    for (int key0 = kbeg + BK * warp; key0 < kend; key0 += BK * W) {
-      if (owed && ok) {
-        __syncwarp();
-        feed.issue(p);
+        for (int i = 0; i < NRW; ++i) o[i] = fmaf(o[i], 1.f / (1 << kPStep), __uint_as_float(raw[i]));
       }
-      const int stage = used % S;
-      if (__any_sync(0xffffffffu, !mbar_wait(&full[warp][stage], (used / S) & 1, ab, kDevTimeoutLoad))) ok = false;
-      ++used;
-      owed = true;
-      if (!ok) continue;
-      const uint8_t* blk = ring + stage * C::STAGE;
-      const int got = flags[warp][stage];
-      // ---- S^T of the block's two halves of 16 keys
-      float acc[2][NT][4];
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_empty[buf]);
+      if (KP == 2 && (warp & 2)) {
 #pragma unroll
-      for (int mb = 0; mb < 2; ++mb) {
-#pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[mb][x][e] = 0.f;
-        const uint8_t* ra = blk + (16 * mb + key_row(g)) * (D / 2) + t * (C::VPL / 2);
-        uint32_t wa[C::VPL / 8], wb[C::VPL / 8];
-        if constexpr (D == 128) {
-          const uint4 a = *reinterpret_cast<const uint4*>(ra), b = *reinterpret_cast<const uint4*>(ra + 8 * (D / 2));
-          wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w;
-          wb[0] = b.x, wb[1] = b.y, wb[2] = b.z, wb[3] = b.w;
-        } else {
-          const uint2 a = *reinterpret_cast<const uint2*>(ra), b = *reinterpret_cast<const uint2*>(ra + 8 * (D / 2));
-          wa[0] = a.x, wa[1] = a.y;
-          wb[0] = b.x, wb[1] = b.y;
-        }
-#pragma unroll
-        for (int i = 0; i < C::VPL / 8; ++i) {
-          uint32_t ha[4], hb[4];
-          e2m1_halves(wa[i], ha);
-          e2m1_halves(wb[i], hb);
-#pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2)
-#pragma unroll
-            for (int x = 0; x < NT; ++x) {
-              const int kk = 2 * i + k2;
-              mma_16816(acc[mb][x], ha[2 * k2], hb[2 * k2], ha[2 * k2 + 1], hb[2 * k2 + 1], qh[x][kk][0], qh[x][kk][1]);
-              if constexpr (LO)
-                mma_16816(acc[mb][x], ha[2 * k2], hb[2 * k2], ha[2 * k2 + 1], hb[2 * k2 + 1], ql[x][kk][0],
-                          ql[x][kk][1]);
-            }
-        }
+        for (int i = 0; i < NRW; ++i) xch_sh[KP == 2 ? r0 + i : 0][KP == 2 ? t - 64 : 0] = o[i];
       }
-      // ---- scores in log2 units, and with the value descale's logarithm
-      float y[2][NT][4];
-      const uint16_t* sd = reinterpret_cast<const uint16_t*>(blk + C::KD);
-      bool need = false;
+      named_bar_sync(BAR, MEMBERS);                            // the sums of rows are there, too
+      if (KP == 1 || !(warp & 2)) {
 #pragma unroll
-      for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int kr = 16 * mb + 8 * r + key_row(g);
-          const float ks = bf16_bits(sd[kr]), lv = lg2(bf16_bits(sd[BK + kr]));
-          const bool there = feed.split ? (got >> mb) & 1 : got != 0;
-#pragma unroll
-          for (int x = 0; x < NT; ++x)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const bool seen = there && key0 + kr < vend[x][e];
-              const float s = seen ? acc[mb][x][2 * r + e] * (cq[x][e] * ks) : -INFINITY;
-              acc[mb][x][2 * r + e] = s;
-              y[mb][x][2 * r + e] = seen ? s + lv : -INFINITY;
-              need |= y[mb][x][2 * r + e] > tref[x][e] + 3.f || s > mref[x][e] + 64.f;
-            }
-        }
-      if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float ty = fmaxf(fmaxf(y[0][x][e], y[0][x][2 + e]), fmaxf(y[1][x][e], y[1][x][2 + e]));
-            float ms = fmaxf(fmaxf(acc[0][x][e], acc[0][x][2 + e]), fmaxf(acc[1][x][e], acc[1][x][2 + e]));
-#pragma unroll
-            for (int m = 4; m < 32; m <<= 1) {
-              ty = fmaxf(ty, __shfl_xor_sync(0xffffffffu, ty, m));
-              ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, m));
-            }
-            ty = fmaxf(ty, tref[x][e]);
-            ms = fmaxf(ms, mref[x][e]);
-            const float at = tref[x][e] == -INFINITY ? 0.f : ex2_approx(tref[x][e] - ty);
-            const float am = mref[x][e] == -INFINITY ? 0.f : ex2_approx(mref[x][e] - ms);
-            tref[x][e] = ty;
-            mref[x][e] = ms;
-            lsum[x][e] *= am;
-#pragma unroll
-            for (int i = 0; i < C::VB; ++i) {
-              o[i][x][e] *= at;
-              o[i][x][2 + e] *= at;
-            }
-          }
-      }
-      // ---- probabilities, transposed into operands
-      uint32_t pb[2][NT][2];
-#pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        float tr[2], mr[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          tr[e] = kPShift - (tref[x][e] == -INFINITY ? 0.f : tref[x][e]);
-          mr[e] = mref[x][e] == -INFINITY ? 0.f : mref[x][e];
-        }
-#pragma unroll
-        for (int mb = 0; mb < 2; ++mb) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            lsum[x][0] += ex2_approx(acc[mb][x][2 * r] - mr[0]);
-            lsum[x][1] += ex2_approx(acc[mb][x][2 * r + 1] - mr[1]);
-            pb[mb][x][r] = transpose8x8(
-                cvt_pack_f16(ex2_approx(y[mb][x][2 * r] + tr[0]), ex2_approx(y[mb][x][2 * r + 1] + tr[1])));
-          }
-        }
-      }
-      // ---- O^T += V^T P^T
-#pragma unroll
-      for (int mb = 0; mb < 2; ++mb) {
-        const uint8_t* rv = blk + C::CODES + 16 * mb * (D / 2) + g * C::VB;
-        const int r0 = key_row(2 * t) * (D / 2), r1 = key_row(2 * t + 1) * (D / 2);
-        uint32_t w[4][C::VB / 4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint8_t* src = rv + (r & 1 ? r1 : r0) + (r >> 1) * 8 * (D / 2);
-          if constexpr (D == 128) {
-            const uint2 a = *reinterpret_cast<const uint2*>(src);
-            w[r][0] = a.x, w[r][1] = a.y;
+        for (int i = 0; i < NRW; ++i) {
+          const int r = r0 + i;
+          if (r >= done.rows) break;
+          if constexpr (KP == 2) o[i] += xch_sh[r][t];
+          const float l = ((l_sh[buf][0][r] + l_sh[buf][1][r]) + l_sh[buf][2][r]) + l_sh[buf][3][r];
+          // (a NaN among the scores or descales is in o by now, and stays)
+          const float f = l == 0.f || done.tref[i] == -INFINITY ? 0.f : ex2_approx(done.tref[i] - done.mref[i] - kPShift) / l;
+          const float val = o[i] * f;
+          const float lse = l == 0.f ? -INFINITY : (done.mref[i] + lg2(l)) * 0.69314718055994530942f;
+          if (done.whole) {
+            const uint32_t pk = FP16 ? cvt_pack_f16(val, 0.f) : cvt_pack_bf16(val, 0.f);
+            p.o[(done.at0 + r) * D + t] = static_cast<uint16_t>(pk);
+            if (t == 0) p.lse[done.at0 + r] = lse;
           } else {
-            w[r][0] = *reinterpret_cast<const uint32_t*>(src);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < C::VB / 4; ++i) {
-          uint32_t h[4][4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) e2m1_halves(w[r][i], h[r]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t a0 = __byte_perm(h[0][e], h[1][e], 0x5410), a1 = __byte_perm(h[0][e], h[1][e], 0x7632);
-            const uint32_t a2 = __byte_perm(h[2][e], h[3][e], 0x5410), a3 = __byte_perm(h[2][e], h[3][e], 0x7632);
-#pragma unroll
-            for (int x = 0; x < NT; ++x) mma_16816(o[4 * i + e][x], a0, a1, a2, a3, pb[mb][x][0], pb[mb][x][1]);
+            p.o_part[(done.slot * p.seg_rows + r) * D + t] = val;
+            if (t == 0) p.lse_part[done.slot * p.seg_rows + r] = lse;
           }
         }
       }
-    }
+      if constexpr (KP == 2) named_bar_sync(BAR, MEMBERS);     // xch_sh has been read
+    };
 
-    // ---- the part's end: the warps' results joined.  Each leaves its output in the stage it
-    // read last, 8 rows at a time, 16-byte pieces exchanged within a row so that the four
-    // lanes of a group write to different banks.
-    const int nw = min(W, (kend - kbeg + BK - 1) / BK);          // warps that had a block
+    int n = 0;
+    Slot key{0, 0u}, old{1, 0u};            // old: the values of tile n - 1
+    for (int part = 0; cur.left > 0; ++part) {
+      const int take = cur.part(), len = cur.len;
+      const int hk = cur.y / p.qtiles, row0 = (cur.y - hk * p.qtiles) * 16;
+      const int rows_here = min(NR, p.rows - row0);
+      if (__any_sync(0xffffffffu, !mbar_wait(&q_full[part & 1], (part >> 1) & 1, ab, kDevTimeoutSoftmax))) ok = false;
+      float cq[NRW], tref[NRW], mref[NRW], lsum[NRW];
+      unsigned vend[NRW];          // tokens [0, vend) visible to each row
 #pragma unroll
-    for (int x = 0; x < NT; ++x)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int m = 4; m < 32; m <<= 1) lsum[x][e] += __shfl_xor_sync(0xffffffffu, lsum[x][e], m);
-        if (g == 0) {
-          const int r = 8 * x + 2 * t + e;
-          stat_t[warp][r] = tref[x][e];
-          stat_m[warp][r] = mref[x][e];
-          stat_l[warp][r] = lsum[x][e];
-        }
+      for (int i = 0; i < NRW; ++i) {
+        const int r = r0 + i;
+        cq[i] = cq_sh[part & 1][r];
+        vend[i] = r < rows_here ? max(p.causal ? min(len, len - p.n_q + (row0 + r) % p.n_q + 1) : len, 0) : 0;
+        tref[i] = mref[i] = -INFINITY;
+        lsum[i] = 0.f;
       }
-    if (lane == 0) buf_sh[warp] = (used + S - 1) % S;
-    const bool whole = take == nt_tiles;
-    const size_t slot = 2ull * blockIdx.x + (first_part ? 0 : 1);
-#pragma unroll
-    for (int x = 0; x < NT; ++x) {
-      __syncthreads();                        // statistics are there; the round before has been read
-      if (warp < nw) {
-        float4* dst = reinterpret_cast<float4*>(ring + ((used + S - 1) % S) * C::STAGE);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 2 * t + e;
-          float top = -INFINITY;
-          for (int w = 0; w < nw; ++w) top = fmaxf(top, stat_t[w][8 * x + r]);
-          const float f = tref[x][e] == -INFINITY ? 0.f : ex2_approx(tref[x][e] - top);
-#pragma unroll
-          for (int i = 0; i < C::VB / 2; ++i) {
-            const float4 val = make_float4(o[2 * i][x][e] * f, o[2 * i][x][2 + e] * f, o[2 * i + 1][x][e] * f,
-                                           o[2 * i + 1][x][2 + e] * f);
-            dst[r * (D / 4) + ((g * (C::VB / 2) + i) ^ t)] = val;
-          }
-        }
-      }
-      __syncthreads();
-      const int real = min(8, rows_here - 8 * x);
-      for (int it = threadIdx.x; it < real * (D / 4); it += kThreads) {
-        const int r = it / (D / 4), c4 = it % (D / 4);
-        float top_t = -INFINITY, top_m = -INFINITY, l = 0.f;
-        for (int w = 0; w < nw; ++w) {
-          top_t = fmaxf(top_t, stat_t[w][8 * x + r]);
-          top_m = fmaxf(top_m, stat_m[w][8 * x + r]);
-        }
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < nw; ++w) {
-          const float m = stat_m[w][8 * x + r];
-          if (m != -INFINITY) l += stat_l[w][8 * x + r] * ex2_approx(m - top_m);
-          const float4 v = *(reinterpret_cast<const float4*>(smem + w * S * C::STAGE + buf_sh[w] * C::STAGE) +
-                             r * (D / 4) + (c4 ^ (r >> 1)));
-          a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-        }
-        // (a NaN among the scores or descales is in a by now, and stays)
-        const float f = l == 0.f || top_t == -INFINITY ? 0.f : ex2_approx(top_t - top_m - kPShift) / l;
-        a.x *= f, a.y *= f, a.z *= f, a.w *= f;
-        const float lse = l == 0.f ? -INFINITY : (top_m + lg2(l)) * 0.69314718055994530942f;
-        if (whole) {
-          const uint2 pk = p.fp16 ? make_uint2(cvt_pack_f16(a.x, a.y), cvt_pack_f16(a.z, a.w))
-                                  : make_uint2(cvt_pack_bf16(a.x, a.y), cvt_pack_bf16(a.z, a.w));
-          *reinterpret_cast<uint2*>(p.o + (at0 + 8 * x + r) * D + 4 * c4) = pk;
-          if (c4 == 0) p.lse[at0 + 8 * x + r] = lse;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_empty[part & 1]);
+      const unsigned vis_all = max(p.causal ? len - p.n_q + 1 : len, 0);   // seen by every row
+      for (int i = 0; i < take; ++i, ++n, key.next()) {
+        const int buf = n & 1, kslot = key.at;
+        if (n >= 2) old.next();
+        // (the descales and the list of boxes came with the key tile)
+        if (__any_sync(0xffffffffu, !mbar_wait(&kv_full[kslot], key.phase, ab, kDevTimeoutSoftmax))) ok = false;
+        uint32_t ks2, vs2;         // descales of the thread's tokens (d = 64: two)
+        const uint8_t* desc = sDesc + kslot / 2 * 4 * TILE;
+        if constexpr (KP == 2) {
+          ks2 = *reinterpret_cast<const uint32_t*>(desc + 4 * t);
+          vs2 = *reinterpret_cast<const uint32_t*>(desc + 2 * TILE + 4 * t);
         } else {
-          const size_t pr = slot * p.seg_rows + 8 * x + r;
-          *reinterpret_cast<float4*>(p.o_part + pr * D + 4 * c4) = a;
-          if (c4 == 0) p.lse_part[pr] = lse;
+          ks2 = *reinterpret_cast<const uint16_t*>(desc + 2 * t);
+          vs2 = *reinterpret_cast<const uint16_t*>(desc + 2 * TILE + 2 * t);
         }
+        const unsigned tile0 = static_cast<unsigned>(cur.j + i) * TILE, key0 = tile0 + KP * t;
+        const unsigned boxes = there_sh[kslot / 2];
+        const bool there = (boxes >> (KP * t >> box_shift)) & 1u;
+        const bool open = tile0 + TILE <= vis_all && boxes == all_boxes;
+        if (__any_sync(0xffffffffu, !mbar_wait(&s_full[buf], (n >> 1) & 1, ab, kDevTimeoutSoftmax))) ok = false;
+        tc_fence_after_sync();
+        uint32_t raw[KP][TQ][NRW];
+#pragma unroll
+        for (int h = 0; h < KP; ++h)
+#pragma unroll
+          for (int k = 0; k < TQ; ++k)
+            tmem_ld_cols<NRW>(tmem + lane_addr + C::S_COL(buf) + h * C::NS + k * NR + r0, raw[h][k]);
+        tmem_ld_wait();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_empty[kslot]);
+        // scores in log2 units, and with the value descale's logarithm
+        float s[KP][NRW], y[KP][NRW];
+        bool need = false;
+#pragma unroll
+        for (int h = 0; h < KP; ++h) {
+          const float ks = h ? __uint_as_float(ks2 & 0xFFFF0000u) : bf16_bits(ks2);
+          const float lv = lg2(h ? __uint_as_float(vs2 & 0xFFFF0000u) : bf16_bits(vs2));
+          const uint64_t ks_2 = pack2(ks, ks), lv_2 = pack2(lv, lv), step = pack2(1.f / (1 << kPStep), 1.f / (1 << kPStep));
+#pragma unroll
+          for (int e = 0; e < NRW; e += 2) {
+            auto pair = [&](int k) { return pack2(__uint_as_float(raw[h][k][e]), __uint_as_float(raw[h][k][e + 1])); };
+            uint64_t a = pair(TQ - 1);
+#pragma unroll
+            for (int k = TQ - 2; k >= 0; --k) a = ffma2(a, step, pair(k));
+            a = fmul2(a, fmul2(pack2(cq[e], cq[e + 1]), ks_2));
+            const uint64_t b = fadd2(a, lv_2);
+            s[h][e] = lo2(a), s[h][e + 1] = hi2(a);
+            y[h][e] = lo2(b), y[h][e + 1] = hi2(b);
+          }
+          if (!open) {
+#pragma unroll
+            for (int e = 0; e < NRW; ++e) {
+              const bool seen = there && key0 + h < vend[e];
+              s[h][e] = seen ? s[h][e] : -INFINITY;
+              y[h][e] = seen ? y[h][e] : -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < NRW; ++e) need |= y[h][e] > tref[e] + 3.f || s[h][e] > mref[e] + 64.f;
+        }
+        if (any_of(BAR, MEMBERS, need)) {
+          // references move to the maxima over the tile
+          float my[NRW], ms[NRW];
+#pragma unroll
+          for (int e = 0; e < NRW; ++e) {
+            const float a = KP == 2 ? fmaxf(y[0][e], y[KP - 1][e]) : y[0][e];
+            const float b = KP == 2 ? fmaxf(s[0][e], s[KP - 1][e]) : s[0][e];
+            asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(my[e]) : "f"(a));
+            asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(ms[e]) : "f"(b));
+          }
+          if (lane == 0) {
+#pragma unroll
+            for (int e = 0; e < NRW; ++e) {
+              red_sh[0][warp & 3][r0 + e] = my[e];
+              red_sh[1][warp & 3][r0 + e] = ms[e];
+            }
+          }
+          named_bar_sync(BAR, MEMBERS);
+          float alpha[NRW];
+          bool grew = false;
+#pragma unroll
+          for (int e = 0; e < NRW; ++e) {
+            const int r = r0 + e;
+            const float ty = fmaxf(fmaxf(fmaxf(red_sh[0][0][r], red_sh[0][1][r]), fmaxf(red_sh[0][2][r], red_sh[0][3][r])), tref[e]);
+            const float tm = fmaxf(fmaxf(fmaxf(red_sh[1][0][r], red_sh[1][1][r]), fmaxf(red_sh[1][2][r], red_sh[1][3][r])), mref[e]);
+            alpha[e] = tref[e] == -INFINITY ? (ty == -INFINITY ? 1.f : 0.f) : ex2_approx(tref[e] - ty);
+            grew |= ty > tref[e];
+            lsum[e] *= mref[e] == -INFINITY ? 0.f : ex2_approx(mref[e] - tm);
+            tref[e] = ty;
+            mref[e] = tm;
+          }
+          if (i > 0 && grew) {
+            // O^T times alpha once P' V(n - 1) is in it (the phase of its value slot's empty barrier)
+            if (__any_sync(0xffffffffu, !mbar_wait(&kv_empty[old.at], old.phase, ab, kDevTimeoutSoftmax))) ok = false;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int k = 0; k < TP; ++k) {
+              uint32_t o[NRW];
+              const uint32_t at = tmem + lane_addr + C::O_COL(part & 1) + o_half + k * NR + r0;
+              tmem_ld_cols<NRW>(at, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < NRW; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[e]);
+              tmem_st_cols<NRW>(at, o);
+            }
+            tmem_st_wait();
+          }
+          named_bar_sync(BAR, MEMBERS);                        // red_sh has been read
+        }
+        // probabilities as e4m3 terms, bytes of their rows' columns
+        const uint32_t pbase = smem_u32(sP + buf * C::P_TILE) + (t & 15);
+#pragma unroll
+        for (int h = 0; h < KP; ++h)
+#pragma unroll
+          for (int e = 0; e < NRW; e += 2) {
+            const uint64_t tr = pack2(kPShift - (tref[e] == -INFINITY ? 0.f : tref[e]),
+                                      kPShift - (tref[e + 1] == -INFINITY ? 0.f : tref[e + 1]));
+            const uint64_t mr = pack2(mref[e] == -INFINITY ? 0.f : -mref[e], mref[e + 1] == -INFINITY ? 0.f : -mref[e + 1]);
+            const uint64_t a = fadd2(pack2(s[h][e], s[h][e + 1]), mr), b = fadd2(pack2(y[h][e], y[h][e + 1]), tr);
+            lsum[e] += ex2_approx(lo2(a));
+            lsum[e + 1] += ex2_approx(hi2(a));
+            __half2 x = as_half2(cvt_pack_f16(ex2_approx(lo2(b)), ex2_approx(hi2(b))));
+#pragma unroll
+            for (int k = 0; k < TP; ++k) {
+              const uint32_t c = e4m3_pair_h(half2_bits(x));
+              if (k + 1 < TP) x = __hmul2(__hsub2(x, as_half2(e4m3_halves(c))), __float2half2_rn(1 << kPStep));
+              const int col = h * NR * TP + k * NR + r0 + e;
+              st_shared_u8(pbase + col * 128 + ((((t >> 4) ^ col) & 7) << 4), c & 0xFFu);
+              st_shared_u8(pbase + (col + 1) * 128 + ((((t >> 4) ^ (col + 1)) & 7) << 4), c >> 8);
+            }
+          }
+        fence_proxy_async_smem();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[buf]);
+        // the part before this one, while this tile's products run
+        if (i == 0 && part > 0) write_out();
       }
+      // this part's row sums, and what its output needs
+#pragma unroll
+      for (int e = 0; e < NRW; ++e) {
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) lsum[e] += __shfl_xor_sync(0xffffffffu, lsum[e], m);
+        if (lane == 0) l_sh[part & 1][warp & 3][r0 + e] = lsum[e];
+        done.tref[e] = tref[e];
+        done.mref[e] = mref[e];
+      }
+      done.part = part;
+      done.rows = rows_here;
+      done.whole = take == cur.tiles();
+      done.at0 = (static_cast<size_t>(cur.b) * p.H_kv + hk) * p.rows + row0;
+      done.slot = 2ull * blockIdx.x + (part > 0 ? 1 : 0);
+      if (!done.whole && cur.j == 0) {
+        // CTA whose share holds the segment's last tile: the last c with c T / n <= it
+        const long long ctas = T < gridDim.x ? T : gridDim.x, last = at_tile + cur.tiles() - 1;
+        crossing = make_int4(static_cast<int>(done.at0), rows_here, static_cast<int>(((last + 1) * ctas - 1) / T),
+                             static_cast<int>(done.slot));
+      }
+      at_tile += take;
+      cur.next_part(p);
     }
-    if (!whole && cur.j == 0) {
-      // CTA whose share holds the segment's last tile: the last c with c T / n <= it
-      const long long n = T < gridDim.x ? T : gridDim.x, last = at_tile + nt_tiles - 1;
-      crossing = make_int4(static_cast<int>(at0), rows_here, static_cast<int>(((last + 1) * n - 1) / T),
-                           static_cast<int>(slot));
-    }
-    fence_proxy_async_smem();                 // before copies land in the stages again
-    __syncthreads();
-    if (owed && ok) feed.issue(p);
-    first_part = false;
-    at_tile += take;
-    cur.next_part(p);
+    if (done.part >= 0) write_out();
+    if (threadIdx.x == 0) p.crossing[blockIdx.x] = crossing;
   }
-  if (threadIdx.x == 0) p.crossing[blockIdx.x] = crossing;
-  if (!ok)       // let the copies in flight land before the memory goes away
-    for (int i = max(0, feed.issued - S); i < feed.issued; ++i) mbar_wait_drain(&full[warp][i % S], (i / S) & 1);
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before_sync();
+  __syncthreads();
+  if (abort_sh) {
+    // let every copy and product this CTA issued land before the memory goes away
+    if (warp == C::LOAD && lane < 2) {
+      const int kv = lane, n = issued_sh[kv];
+      for (int i = n - 1; i >= 0 && i >= n - NSLOT / 2; --i)
+        mbar_wait_drain(&kv_full[2 * (i % (NSLOT / 2)) + kv], (i / (NSLOT / 2)) & 1);
+    }
+    if ((warp == C::MMA_S || warp == C::MMA_PV) && lane == 0) {
+      uint64_t* bar = &drain_bar[warp == C::MMA_S ? 0 : 1];
+      mma_commit(bar);
+      mbar_wait_drain(bar, 0);
+    }
+    __syncthreads();
+  }
+  if (warp == C::MMA_S) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, C::TMEM);
+  }
 }
 
 // Segments that cross shares: LSE = log sum_c exp(lse_c), O = sum_c exp(lse_c - LSE) O_c over
 // CTAs c0 .. c1, whose partial results are c0's slot and the others' first ones.  A block for
 // every CTA that left a segment unfinished (4 rows of it), D / 4 threads per row.
 constexpr int kMergeThreads = 128;
-template <int D>
+template <int D, bool FP16>
 __global__ void __launch_bounds__(kMergeThreads) decode_fp4_merge_kernel(const KParams p) {
   wait_for_previous_kernel();
   const int4 seg = __ldcg(p.crossing + blockIdx.x);
@@ -689,32 +855,47 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_merge_kernel(const K
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const size_t at = static_cast<size_t>(seg.x) + r;
-  const uint2 pk = p.fp16 ? make_uint2(cvt_pack_f16(acc.x * inv, acc.y * inv), cvt_pack_f16(acc.z * inv, acc.w * inv))
+  const uint2 pk = FP16 ? make_uint2(cvt_pack_f16(acc.x * inv, acc.y * inv), cvt_pack_f16(acc.z * inv, acc.w * inv))
                           : make_uint2(cvt_pack_bf16(acc.x * inv, acc.y * inv), cvt_pack_bf16(acc.z * inv, acc.w * inv));
   *reinterpret_cast<uint2*>(p.o + at * D + col) = pk;
   if (col == 0) p.lse[at] = sum == 0.f ? -INFINITY : m + logf(sum);
 }
 
-template <int D, int NT, bool LO>
-attn_status_t launch_t(const KParams& p, int ctas, cudaStream_t stream) {
-  constexpr int smem = W * kStages<D, NT> * Cfg<D>::STAGE;
-  static_assert(Cfg<D>::STAGE >= 8 * D * 4, "a stage holds the output of 8 rows");
-  auto kern = decode_fp4_kernel<D, NT, LO>;
-  const attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), smem);
+template <int D, int NR, int TQ, int TP, bool FP16, bool SIGNS>
+attn_status_t launch_t(const Fp4DecodeParams& a, const KParams& p, int ctas, cudaStream_t stream) {
+  using C = Cfg<D, NR, TQ, TP>;
+  if (ctas > 152 * C::CTAS) ctas = 152 * C::CTAS;
+  auto kern = decode_fp4_kernel<D, NR, TQ, TP, FP16, SIGNS>;
+  attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), C::SMEM);
   if (s != ATTN_OK) return s;
-  cudaError_t e = launch_dependent(kern, dim3(ctas), kThreads, smem, stream, 0, p);
+  // {128 codes of one or two tokens, rows of a page, heads, pages}
+  CUtensorMap tk, tv;
+  const int box = (p.page_size < C::TILE ? p.page_size : C::TILE) / C::KP;
+  const uint64_t head_b = static_cast<uint64_t>(p.page_size) * (D / 2);
+  if ((s = make_tmap_fp4(&tk, a.k_cache, p.page_size / C::KP, p.H_kv, p.num_pages, 64, head_b, head_b * p.H_kv, box)) != ATTN_OK)
+    return s;
+  if ((s = make_tmap_fp4(&tv, a.v_cache, p.page_size / C::KP, p.H_kv, p.num_pages, 64, head_b, head_b * p.H_kv, box)) != ATTN_OK)
+    return s;
+  cudaError_t e = launch_dependent(kern, dim3(ctas), C::THREADS, C::SMEM, stream, 0, tk, tv, p);
   if (e != cudaSuccess) return fail_cuda(e, "4-bit decode kernel launch");
   if (ctas == 1) return ATTN_OK;
   constexpr int rows = kMergeThreads / (D / 4);
-  e = launch_dependent(decode_fp4_merge_kernel<D>, dim3(ctas, (p.seg_rows + rows - 1) / rows), kMergeThreads, 0, stream,
+  e = launch_dependent(decode_fp4_merge_kernel<D, FP16>, dim3(ctas, (p.seg_rows + rows - 1) / rows), kMergeThreads, 0, stream,
                        0, p);
   return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "4-bit decode merge kernel launch");
 }
 
+template <int D, int NR>
+attn_status_t launch_r(const Fp4DecodeParams& a, const KParams& p, int ctas, cudaStream_t stream) {
+  if (a.fp16)
+    return p.signs ? launch_t<D, NR, 4, 3, true, true>(a, p, ctas, stream) : launch_t<D, NR, 3, 3, true, false>(a, p, ctas, stream);
+  return p.signs ? launch_t<D, NR, 4, 2, false, true>(a, p, ctas, stream) : launch_t<D, NR, 2, 2, false, false>(a, p, ctas, stream);
+}
+
 template <int D>
-attn_status_t launch_d(const KParams& p, int ctas, cudaStream_t stream) {
-  if (p.rows <= 8) return p.signs ? launch_t<D, 1, true>(p, ctas, stream) : launch_t<D, 1, false>(p, ctas, stream);
-  return p.signs ? launch_t<D, 2, true>(p, ctas, stream) : launch_t<D, 2, false>(p, ctas, stream);
+attn_status_t launch_d(const Fp4DecodeParams& a, const KParams& p, int ctas, cudaStream_t stream) {
+  return p.rows <= 4 ? launch_r<D, 4>(a, p, ctas, stream) : p.rows <= 8 ? launch_r<D, 8>(a, p, ctas, stream)
+                                                                         : launch_r<D, 16>(a, p, ctas, stream);
 }
 
 }  // namespace
@@ -722,18 +903,18 @@ attn_status_t launch_d(const KParams& p, int ctas, cudaStream_t stream) {
 attn_status_t launch_decode_fp4(const Fp4DecodeParams& p, cudaStream_t stream) {
   int* status = device_status_word();
   if (!status) return fail(ATTN_ERR_CUDA, "status word unavailable");
-  const Fp4DecodePlan plan = fp4_decode_plan(p.B, p.H, p.H_kv, p.n_q, p.max_seqlen);
+  const Fp4DecodePlan plan = fp4_decode_plan(p.B, p.H, p.H_kv, p.n_q, p.d, p.max_seqlen);
   const int rows = p.H / p.H_kv * p.n_q;
   const size_t part_rows = 2ull * plan.ctas * plan.seg_rows;
   char* ws = static_cast<char*>(p.workspace);
   char* const lse_part = ws + align_up(part_rows * p.d * sizeof(float), 256);
   char* const crossing = lse_part + align_up(part_rows * sizeof(float), 256);
-  const KParams kp{static_cast<const uint16_t*>(p.q), {p.k_cache, p.v_cache}, {p.k_descale, p.v_descale}, p.signs,
+  const KParams kp{static_cast<const uint16_t*>(p.q), {p.k_descale, p.v_descale}, p.signs,
                    p.block_table, p.seq_lens, static_cast<uint16_t*>(p.o), p.lse, reinterpret_cast<float*>(ws),
                    reinterpret_cast<float*>(lse_part), reinterpret_cast<int4*>(crossing), status, p.B, p.H, p.H_kv, p.n_q,
                    rows, plan.qtiles, p.H_kv * plan.qtiles, plan.seg_rows, p.num_pages, p.page_size,
-                   page_shift_of(p.page_size), p.max_pages, p.causal, p.fp16, p.scale * 1.4426950408889634f};
-  return p.d == 64 ? launch_d<64>(kp, plan.ctas, stream) : launch_d<128>(kp, plan.ctas, stream);
+                   page_shift_of(p.page_size), p.max_pages, p.causal, p.scale * 1.4426950408889634f};
+  return p.d == 64 ? launch_d<64>(p, kp, plan.ctas, stream) : launch_d<128>(p, kp, plan.ctas, stream);
 }
 
 }  // namespace attn

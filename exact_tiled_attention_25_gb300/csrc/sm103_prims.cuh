@@ -347,6 +347,12 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N, bool a
          ((M >> 4) << 24);
 }
 
+// kind::f8f6f4 with A e2m1 (format code 5) and B e4m3, K-major B.  A's codes stand in shared
+// memory as TMA's 4-bit unpacking leaves them: 16 of them in eight bytes, then eight bytes unused.
+__host__ __device__ constexpr uint32_t idesc_e2m1_e4m3(uint32_t M, uint32_t N, bool a_mn) {
+  return idesc_e4m3(M, N, a_mn, false) | (5u << 7);
+}
+
 // D(tmem) (+)= A(smem) * B(smem)
 __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                            uint32_t idesc, uint32_t accumulate) {

@@ -809,7 +809,8 @@ size_t attn_decode_fp4_workspace_size(int B, int H, int H_kv, int n_q, int d, in
  * attn_decode_paged_fp4 -- attn_decode_paged over the cache of attn_cache_append_fp4.
  *   q              : [B, H, n_q, d] in `dtype` (bf16 or fp16); used as it is (multiplied by
  *                    M in float32 when hadamard_signs is given), not quantised.
- *   k_cache, v_cache, k_descale, v_descale : as attn_cache_append_fp4.
+ *   k_cache, v_cache, k_descale, v_descale : as attn_cache_append_fp4; the caches 32-byte
+ *                    aligned.
  *   hadamard_signs : DEVICE float32 [d] of +1 / -1 when the keys were stored transformed,
  *                    or NULL.  Values are never transformed.
  *   workspace      : at least attn_decode_fp4_workspace_size() bytes, 256-byte aligned;
@@ -818,9 +819,9 @@ size_t attn_decode_fp4_workspace_size(int B, int H, int H_kv, int n_q, int d, in
  *   Other arguments, outputs, masking and device-side error reporting as
  *   attn_decode_paged; a token on a page that is out of range is not seen.  What the slots
  *   behind a sequence hold does not matter.
- * Accuracy: that of 16-bit operands; the stored values enter exactly.  Products of a
- * probability and a value descale below 2^-26 of a query row's largest lose bits (by up to
- * 2^-37 of that one).
+ * Accuracy: the stored values enter exactly, queries to 2^-19.  The product of a probability
+ * and a value descale is held to half a step of `dtype`, and to 2^-20 (bf16) or 2^-25
+ * (fp16) of the query row's largest one.  A query row with an infinity or a NaN gives NaN.
  * Limits: d = 64 or 128; (H / H_kv) * n_q <= 128; page_size a power of two in [16, 65536].
  * Source: as attn_decode_paged_fp8.
  */

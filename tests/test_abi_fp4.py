@@ -38,7 +38,7 @@ def test_unsupported_head_sizes(lib):
     assert _read(lib, 4, d=256) == 2 and _read(lib, 8, d=64) == 2
 
 
-def _decode(lib, q=16, kc=16, vc=16, kd=16, vd=16, sg=16, bt=16, sl=16, o=16, l=16, ws=256, wsb=1 << 40, B=2, H=8, Hkv=2, nq=1,
+def _decode(lib, q=16, kc=32, vc=64, kd=16, vd=16, sg=16, bt=16, sl=16, o=16, l=16, ws=256, wsb=1 << 40, B=2, H=8, Hkv=2, nq=1,
             d=128, pages=9, ps=16, maxp=4, ms=64, causal=1, scale=0.1, dt=0):
     return lib.attn_decode_paged_fp4(q, kc, vc, kd, vd, sg, bt, sl, o, l, ws, wsb, B, H, Hkv, nq, d, pages, ps, maxp, ms, causal,
                                      scale, dt, None)
@@ -48,7 +48,7 @@ def _decode(lib, q=16, kc=16, vc=16, kd=16, vd=16, sg=16, bt=16, sl=16, o=16, l=
     (dict(B=0), "B"), (dict(H=0), "H"), (dict(nq=0), "n_q"), (dict(ms=0), "max_seqlen"), (dict(Hkv=3), "H_kv"), (dict(Hkv=0), "H_kv"),
     (dict(ps=8), "page_size"), (dict(ps=24), "page_size"), (dict(maxp=0), "max_pages"), (dict(maxp=1 << 28), "max_pages"),
     (dict(pages=2 ** 31 - 1, ps=65536, maxp=4, Hkv=8), "too large"), (dict(causal=2), "causal"), (dict(scale=0.0), "scale"),
-    (dict(scale=float("inf")), "scale"), (dict(dt=2), "dtype"), (dict(q=0), "null"), (dict(kc=8), "aligned"), (dict(kd=0), "null"),
+    (dict(scale=float("inf")), "scale"), (dict(dt=2), "dtype"), (dict(q=0), "null"), (dict(kc=8), "aligned"), (dict(vc=48), "32-byte"), (dict(kd=0), "null"),
     (dict(sg=8), "hadamard"), (dict(bt=0), "integer"), (dict(sl=2), "integer"), (dict(ws=16), "256-byte"), (dict(ws=0), "null"),
     (dict(wsb=16), "workspace"), (dict(B=1 << 28), "2^31"),
 ])

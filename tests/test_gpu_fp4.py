@@ -8,14 +8,15 @@ float32 steps (2^-20 of the row's length) and the rounding (half a step: bf16 2^
 
 Decode.  With A_i = scale sum_j |q_i||k_j| over the components of the largest score: a score is
 off by at most e = 2^-16 max_j A_ij (128 float32 sums of exact products, the transform's steps
-and the second float16 part of q, each below 2^-21 of the products' sizes; the exponent's
+and the last e4m3 term of q, each below 2^-18 of the products' sizes; the exponent's
 sums add 2^-22 of a score of at most A).  LSE: e + 2^-20 (1 + |LSE|) (ex2, lg2 and sums).
-O: with V_i = sum_j P_ij |v_j|, probabilities off by 2 e and rounded to float16 (2^-11), float32
-sums and factors (2^-16), then the output's rounding: (2^-11 + 2 e + 2^-16) V + u |O| + 2^-24,
-u = 2^-8 (bf16) or 2^-11 (fp16).  A product P_ij s_j (s_j the value descale) is a float16 that
-is 2^12 at a reference T no larger than the largest of them, so where it is subnormal it is off by
-2^-25 / 2^12 = 2^-37 of that largest one, whatever its own size: 2^-37 max_j(P_ij s_j) sum_j |code_j|
-more, which shows where a column's own values are some 2^-30 of the row's largest."""
+O: with V_i = sum_j P_ij |v_j|, probabilities off by 2 e and held to w, float32 sums and factors
+(2^-16), then the output's rounding u: (w + 2 e + 2^-16) V + u |O| + 2^-24.  fp16: u = w = 2^-11
+(a float16, which three e4m3 terms of four bits and a sign hold exactly).  bf16: u = 2^-8, and two
+terms leave 2^-9 of the float16: w = 2^-9 + 2^-11.  P_ij s_j (s_j the value descale) is
+2^5 at a reference no larger than the largest of them and its last term's step is 2^-9 2^-5 (bf16) or 2^-9 2^-10
+(fp16), so where it is small it is off by half of that over 2^5, 2^-20 or 2^-25 of the largest, whatever
+its own size: that times max_j(P_ij s_j) sum_j |code_j| more."""
 import numpy as np
 import pytest
 import torch
@@ -26,6 +27,8 @@ from gpu_util import check_status, dev, guarded, lib
 
 pytestmark = pytest.mark.gpu
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+PROB = {torch.bfloat16: 2.0 ** -9 + 2.0 ** -11, torch.float16: 2.0 ** -11}
+LAST = {torch.bfloat16: 2.0 ** -20, torch.float16: 2.0 ** -25}
 
 
 @pytest.fixture(scope="module")
@@ -214,7 +217,7 @@ def _decode_ref(q, cache, causal, signs, scale):
             e[b, h] = scale * (np.abs(qq[b, h]) @ np.abs(k[:, h // G]).T).max(1) * 2.0 ** -16
             x = qq[b, h] @ k[:, h // G].T * scale
             p = np.exp(np.minimum(x - np.where(np.isfinite(lse[b, h]), lse[b, h], np.inf)[:, None], 0.0))
-            low[b, h] = 2.0 ** -37 * (p * sv[pages, h // G, rows]).max(1)[:, None] * total[h // G]
+            low[b, h] = LAST[q.dtype] * (p * sv[pages, h // G, rows]).max(1)[:, None] * total[h // G]
     return o, lse, va, e, low
 
 
@@ -225,7 +228,7 @@ def _check_decode(q, o, lse, ref, what=""):
     assert np.array_equal(np.isfinite(got_l), seen) and np.all(got_l[~seen] == -np.inf) and np.all(got_o[~seen] == 0)
     off = np.abs(got_l[seen] - ref_l[seen])
     assert np.all(off <= e[seen] + 2.0 ** -20 * (1 + np.abs(ref_l[seen]))), (what, off.max())
-    tol = (2.0 ** -11 + 2.0 ** -16 + 2 * e[..., None]) * va + HALF[q.dtype] * np.abs(ref_o) + low + 2.0 ** -24
+    tol = (PROB[q.dtype] + 2.0 ** -16 + 2 * e[..., None]) * va + HALF[q.dtype] * np.abs(ref_o) + low + 2.0 ** -24
     assert np.all(np.abs(got_o - ref_o)[seen] <= tol[seen]), (what, np.abs(got_o - ref_o).max())
 
 
