@@ -44,6 +44,7 @@ namespace attn {
 namespace {
 
 constexpr int kSmemPerSm = 232448;
+constexpr float kFar = 3e38f;
 constexpr float kPShift = 5.f;          // P' is 2^5 at the reference, 2^8 at most (e4m3: 448)
 constexpr int kPStep = 5;               // a term's steps are 2^-5 of those of the one before
 
@@ -66,19 +67,22 @@ struct Cfg {
   static constexpr int NRW = NR / CW;                    // query rows of a softmax thread
   static constexpr int LOAD = SW, MMA_S = SW + 1, MMA_PV = SW + 2, QUERY = SW + 3;
   static constexpr int THREADS = (SW + 4) * 32;
-  static constexpr uint32_t S_COLS = KP * NS;            // of one score buffer
-  __host__ __device__ static constexpr uint32_t S_COL(int buf) { return S_COLS * buf; }
-  __host__ __device__ static constexpr uint32_t O_COL(int buf) { return 2 * S_COLS + NPV * buf; }
-  static constexpr int TMEM = pow2(2 * S_COLS + 2 * NPV);
   static constexpr int CTAS = NR == 16 ? 1 : 2;          // of an SM (16 rows: registers)
   static constexpr int Q_TILE = NS * 128, P_TILE = NPV * 128;
-  static constexpr int FIXED = 1024 + 2 * Q_TILE + 2 * P_TILE;
+  static constexpr int PB = NR == 4 && KP == 1 ? 3 : 2;  // buffers of P'
+  static constexpr int FIXED = 1024 + 2 * Q_TILE + PB * P_TILE;
   static constexpr int PER_CTA = kSmemPerSm / CTAS - 4096;   // (static shared memory and what the system takes)
   static constexpr int FIT = (PER_CTA - FIXED) / (SLOT + 2 * TILE) / 2 * 2;
   static constexpr int NSLOT = FIT > 12 ? 12 : FIT;      // even: keys in even slots, values in odd ones
-  static constexpr int DESC_OFF = 2 * Q_TILE + 2 * P_TILE + NSLOT * SLOT;
+  static constexpr uint32_t S_COLS = KP * NS;            // of one score buffer
+  static constexpr int SB_FIT = (512 / CTAS - 2 * NPV) / S_COLS;
+  static constexpr int SB = SB_FIT < NSLOT / 2 ? SB_FIT : NSLOT / 2;   // score buffers
+  __host__ __device__ static constexpr uint32_t S_COL(int buf) { return S_COLS * buf; }
+  __host__ __device__ static constexpr uint32_t O_COL(int buf) { return SB * S_COLS + NPV * buf; }
+  static constexpr int TMEM = pow2(SB * S_COLS + 2 * NPV);
+  static constexpr int DESC_OFF = 2 * Q_TILE + PB * P_TILE + NSLOT * SLOT;
   static constexpr int SMEM = 1024 + DESC_OFF + NSLOT / 2 * 4 * TILE;
-  static_assert(NSLOT >= 4 && TMEM * CTAS <= 512, "ring or tensor memory");
+  static_assert(NSLOT >= 2 * PB && SB >= 2 && TMEM * CTAS <= 512, "ring or tensor memory");
 };
 
 struct KParams {
@@ -122,8 +126,8 @@ __device__ __forceinline__ uint32_t e4m3_halves(uint32_t pair) {
 }
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 __device__ __forceinline__ uint32_t half2_bits(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
-__device__ __forceinline__ void st_shared_u8(uint32_t saddr, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+__device__ __forceinline__ void st_shared_v2(uint32_t saddr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(saddr), "r"(a), "r"(b) : "memory");
 }
 
 // Whether any of the n threads of named barrier `id` says so.
@@ -139,8 +143,10 @@ __device__ __forceinline__ bool any_of(uint32_t id, uint32_t n, bool v) {
 
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
-  static_assert(N == 4 || N == 8, "columns");
-  if constexpr (N == 8) tmem_ld8(taddr, r);
+  static_assert(N == 4 || N == 8 || N == 16 || N == 32, "columns");
+  if constexpr (N == 32) tmem_ld32(taddr, r);
+  else if constexpr (N == 16) tmem_ld16(taddr, r);
+  else if constexpr (N == 8) tmem_ld8(taddr, r);
   else tmem_ld4(taddr, r);
 }
 template <int N>
@@ -188,6 +194,21 @@ struct Cursor {
 };
 
 
+// A place in a ring of N buffers, used every STEP-th (a tile's keys stand in even slots, its values
+// in odd ones), and the phase of its barriers' use.
+template <int N, int STEP = 1>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    at += STEP;
+    if (at >= N) {
+      at -= N;
+      phase ^= 1u;
+    }
+  }
+};
+
 template <int D, int NR, int TQ, int TP, bool FP16, bool SIGNS>
 __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP>::CTAS)
     decode_fp4_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const KParams p) {
@@ -197,19 +218,21 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const sQ = smem;                              // two query tiles, NS x 128 bytes
-  uint8_t* const sP = smem + 2 * C::Q_TILE;              // two tiles of P', NPV x 128 bytes (keys)
-  uint8_t* const sKV = sP + 2 * C::P_TILE;
+  // PB tiles of P': a key's 16 columns side by side, the tile's 128 keys, the next 16 columns
+  uint8_t* const sP = smem + 2 * C::Q_TILE;
+  uint8_t* const sKV = sP + C::PB * C::P_TILE;
   uint8_t* const sDesc = smem + C::DESC_OFF;             // per key slot: TILE key descales, TILE value descales
 
-  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], kv_full[NSLOT], kv_empty[NSLOT], s_full[2], p_full[2], o_full[2],
-      o_empty[2], drain_bar[2];
+  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], kv_full[NSLOT], kv_empty[NSLOT], s_full[C::SB], p_full[C::PB],
+      o_full[2], o_empty[2], drain_bar[2];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, issued_sh[2];                 // key and value tiles whose copies have been issued
-  __shared__ long long warp_sum[C::THREADS / 32], start_sh[2];
+  __shared__ long long warp_sum[C::THREADS / 32], start_sh[3];
   __shared__ unsigned there_sh[NSLOT / 2];               // boxes of a key tile that were copied
-  __shared__ float cq_sh[2][NR];                         // score coefficient of a query row
-  __shared__ float red_sh[2][4][NR];                     // maxima of a tile by key quarter; row sums of a part
-  __shared__ float l_sh[2][4][NR];
+  __shared__ __align__(16) float cq_sh[2][NR];           // of a part's query rows: score coefficients,
+  __shared__ unsigned vend_sh[2][NR];                    // ends of the visible tokens,
+  __shared__ float ref_sh[2][2][NR], l_sh[2][4][NR];     // references at its end, and sums by key quarter
+  __shared__ float red_sh[2][4][NR];                     // maxima of a tile by key quarter
   __shared__ float xch_sh[KP == 2 ? NR : 1][KP == 2 ? 64 : 1];
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -217,12 +240,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1 + C::SW);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], C::SW);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_empty[i], C::SW);
       mbar_init(&drain_bar[i], 1);
     }
+    for (int i = 0; i < C::SB; ++i) mbar_init(&s_full[i], 1);
+    for (int i = 0; i < C::PB; ++i) mbar_init(&p_full[i], C::SW);
     for (int s = 0; s < NSLOT; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], s & 1 ? 1 : C::SW);
@@ -240,7 +263,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     prefetch_tmap(&tmV);
   }
   // columns that no row of queries or of P' fills stay zero
-  for (int i = threadIdx.x; i < (2 * C::Q_TILE + 2 * C::P_TILE) / 16; i += C::THREADS)
+  for (int i = threadIdx.x; i < (2 * C::Q_TILE + C::PB * C::P_TILE) / 16; i += C::THREADS)
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   wait_for_previous_kernel();
@@ -250,8 +273,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   const int per = (p.B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
   long long sum = 0;
+  int len = 0;
   for (int b = b0; b < b1; ++b) {
-    const int len = tokens_of(p, b);
+    len = tokens_of(p, b);
     if (len == 0 && blockIdx.x == 0 && __ldcg(p.seq_lens + b) != 0) atomicCAS(p.status, 0, kDevBadSeqlens);
     sum += tiles_of<TILE>(len);
   }
@@ -273,14 +297,15 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   const long long total = share_start(blockIdx.x + 1ll, gridDim.x, T) - g0;
   if (total > 0 && base * p.segs <= g0 && g0 < (base + sum) * p.segs) {
     int b = b0;
-    while (true) {
-      const int n = tiles_of<TILE>(tokens_of(p, b));
+    for (; b1 - b0 > 1; ++b) {
+      len = tokens_of(p, b);
+      const int n = tiles_of<TILE>(len);
       if (g0 < (base + n) * p.segs) break;
       base += n;
-      ++b;
     }
     start_sh[0] = b;
     start_sh[1] = g0 - base * p.segs;
+    start_sh[2] = len;
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -288,34 +313,14 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   const uint32_t tmem = tmem_base_sh;
   const Abort ab{&abort_sh, p.status};
 
-  // batch entries without tokens: O = 0, LSE = -inf
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (tokens_of(p, b) != 0) continue;
-    const size_t rows_b = static_cast<size_t>(p.H) * p.n_q;
-    uint4* dst = reinterpret_cast<uint4*>(p.o + b * rows_b * D);
-    for (size_t i = threadIdx.x; i < rows_b * (D / 8); i += C::THREADS) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (size_t i = threadIdx.x; i < rows_b; i += C::THREADS) p.lse[b * rows_b + i] = -INFINITY;
-  }
   Cursor<TILE> cur{0, 0, 0, 0, total};
   if (total > 0) {
     cur.b = static_cast<int>(start_sh[0]);
-    cur.len = tokens_of(p, cur.b);
+    cur.len = static_cast<int>(start_sh[2]);
     const int n = cur.tiles();
     cur.y = static_cast<int>(start_sh[1] / n);
     cur.j = static_cast<int>(start_sh[1] - static_cast<long long>(cur.y) * n);
   }
-  // The ring slot of a tile's keys (even) or values (odd), and the phase of its barriers' use.
-  struct Slot {
-    int at;
-    uint32_t phase;
-    __device__ __forceinline__ void next() {
-      at += 2;
-      if (at >= NSLOT) {
-        at -= NSLOT;
-        phase ^= 1u;
-      }
-    }
-  };
 
   if (warp == C::LOAD) {
     // ------------------------------------------------------------ producer
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     // tokens are masked.
     const int box = min(p.page_size, TILE), nbox = TILE / box;
     int n = 0;
-    Slot key_slot{0, 0u};
+    Ring<NSLOT, 2> key_slot;
     bool ok = true;
     while (ok && cur.left > 0) {
       const int take = cur.part(), hk = cur.y / p.qtiles, kbeg = cur.j * TILE;   // kbeg < len
@@ -381,22 +386,24 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     }
   } else if (warp == C::MMA_S) {
     // ------------------------------------------------------------ S^T = K^ Q^T
-    // S(n) into buffer n % 2, once P' V(n - 2) has been formed (the phase of that value slot's
-    // empty barrier): the softmax has read the buffer by then, and may overwrite P'(n - 2).
+    // S(n) into buffer n % SB, which the softmax has read: it hands a key slot back when it has
+    // read that tile's scores, so a key tile that came into a slot used before says so for all
+    // tiles before the slot's last one.
     if (lane == 0) {
-      constexpr uint32_t id = idesc_e2m1_e4m3(128, C::NS, false);
+      constexpr uint32_t id = idesc_e2m1_e4m3(128, C::NS, false, false);
       const uint64_t qdesc0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t kdesc0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
       bool ok = true;
       int n = 0;
-      Slot key{0, 0u}, old{1, 0u};          // old: the values of tile n - 2
+      Ring<NSLOT, 2> key, old;              // old: the keys of tile n - SB
+      Ring<C::SB> buf;
       for (int part = 0; ok && cur.left > 0; ++part) {
         const int take = cur.part();
         if (!(ok = mbar_wait(&q_full[part & 1], (part >> 1) & 1, ab, kDevTimeoutMma))) break;
         const uint64_t qdesc = opaque(sdesc_add(qdesc0, (part & 1) * C::Q_TILE));
-        for (int i = 0; i < take; ++i, ++n, key.next()) {
+        for (int i = 0; i < take; ++i, ++n, key.next(), buf.next()) {
           if (!(ok = mbar_wait(&kv_full[key.at], key.phase, ab, kDevTimeoutMma))) break;
-          if (n >= 2) {
+          if (C::SB < NSLOT / 2 && n >= C::SB) {
             if (!(ok = mbar_wait(&kv_empty[old.at], old.phase, ab, kDevTimeoutMma))) break;
             old.next();
           }
@@ -406,10 +413,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
           for (int kk = 0; kk < 4; ++kk) {
             // d = 64: two 32-column steps for the even tokens, two for the odd ones
             constexpr int steps = D / 32;
-            mma_f8_ss(tmem + C::S_COL(n & 1) + kk / steps * C::NS, sdesc_add(kdesc, kk * 32),
+            mma_f8_ss(tmem + C::S_COL(buf.at) + kk / steps * C::NS, sdesc_add(kdesc, kk * 32),
                       sdesc_add(qdesc, kk % steps * 32), id, kk % steps > 0 ? 1u : 0u);
           }
-          mma_commit(&s_full[n & 1]);
+          mma_commit(&s_full[buf.at]);
         }
         if (ok) mma_commit(&q_empty[part & 1]);
         cur.next_part(p);
@@ -418,28 +425,28 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   } else if (warp == C::MMA_PV) {
     // ------------------------------------------------------------ O^T += V^^T P'^T
     if (lane == 0) {
-      constexpr uint32_t id = idesc_e2m1_e4m3(128, C::NPV, true);
-      const uint64_t pdesc0 = sdesc_sw128(smem_u32(sP), 16, 1024);
+      constexpr uint32_t id = idesc_e2m1_e4m3(128, C::NPV, true, true);
+      const uint64_t pdesc0 = sdesc_mn_plain(smem_u32(sP), 128 * 16, 128);     // MN-major
       const uint64_t vdesc0 = sdesc_sw128(smem_u32(sKV), C::SLOT, 1024);
       bool ok = true;
-      int n = 0;
-      Slot val{1, 0u};
+      Ring<NSLOT, 2> val;                   // (the odd slot behind)
+      Ring<C::PB> pb;
       for (int part = 0; ok && cur.left > 0; ++part) {
         const int take = cur.part();
         const uint32_t o_col = C::O_COL(part & 1);
-        for (int i = 0; i < take; ++i, ++n, val.next()) {
-          if (!(ok = mbar_wait(&kv_full[val.at], val.phase, ab, kDevTimeoutMma))) break;
-          const uint64_t vdesc = opaque(sdesc_add(vdesc0, val.at * C::SLOT));
-          if (!(ok = mbar_wait(&p_full[n & 1], (n >> 1) & 1, ab, kDevTimeoutMma))) break;
+        for (int i = 0; i < take; ++i, val.next(), pb.next()) {
+          if (!(ok = mbar_wait(&kv_full[val.at + 1], val.phase, ab, kDevTimeoutMma))) break;
+          const uint64_t vdesc = opaque(sdesc_add(vdesc0, (val.at + 1) * C::SLOT));
+          if (!(ok = mbar_wait(&p_full[pb.at], pb.phase, ab, kDevTimeoutMma))) break;
           // the buffer's output of two parts ago has been read
           if (i == 0 && part >= 2 && !(ok = mbar_wait(&o_empty[part & 1], ((part >> 1) - 1) & 1, ab, kDevTimeoutMma))) break;
           tc_fence_after_sync();
-          const uint64_t pdesc = sdesc_add(pdesc0, (n & 1) * C::P_TILE);
+          const uint64_t pdesc = sdesc_add(pdesc0, pb.at * C::P_TILE);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_f8_ss(tmem + o_col, sdesc_add(vdesc, kk * 32 * 128), sdesc_add(pdesc, kk * 32), id,
+            mma_f8_ss(tmem + o_col, sdesc_add(vdesc, kk * 32 * 128), sdesc_add(pdesc, kk * 32 * 16), id,
                       (i > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&kv_empty[val.at]);      // every use of a value slot gets its phase
+          mma_commit(&kv_empty[val.at + 1]);  // every use of a value slot gets its phase
           if (i == take - 1) mma_commit(&o_full[part & 1]);
         }
         cur.next_part(p);
@@ -451,6 +458,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     constexpr int L = D / 16, PER = 32 / L;
     const int u = lane % L;
     bool ok = true;
+    long long at_tile = g0;
+    int4 crossing = make_int4(0, 0, 0, -1);            // a segment that this share begins and does not end
     for (int part = 0; ok && cur.left > 0; ++part) {
       const int buf = part & 1;
       if (part >= 2 && __any_sync(0xffffffffu, !mbar_wait(&q_empty[buf], ((part >> 1) - 1) & 1, ab, kDevTimeoutLoad))) {
@@ -530,12 +539,31 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
           if (r < NR)
             st_shared_v4(smem_u32(sQ + buf * C::Q_TILE + col * 128 + ((u ^ (col & 7)) << 4)), w[0], w[1], w[2], w[3]);
         }
-        if (u == 0 && r < NR) cq_sh[buf][r] = p.scale_log2 * back;
+        if (u == 0 && r < NR) {
+          cq_sh[buf][r] = p.scale_log2 * back;
+          vend_sh[buf][r] = live ? max(p.causal ? min(cur.len, cur.len - p.n_q + (row0 + r) % p.n_q + 1) : cur.len, 0) : 0;
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[buf]);
+      if (cur.j == 0 && cur.part() < cur.tiles()) {
+        // CTA whose share holds the segment's last tile: the last c with c T / n <= it
+        const long long n = T < gridDim.x ? T : gridDim.x, last = at_tile + cur.tiles() - 1;
+        crossing = make_int4(static_cast<int>(at0), rows_here, static_cast<int>(((last + 1) * n - 1) / T),
+                             static_cast<int>(2 * blockIdx.x + (part > 0 ? 1 : 0)));
+      }
+      at_tile += cur.part();
       cur.next_part(p);
+    }
+    if (lane == 0) p.crossing[blockIdx.x] = crossing;
+    // batch entries without tokens: O = 0, LSE = -inf
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+      if (tokens_of(p, b) != 0) continue;
+      const size_t rows_b = static_cast<size_t>(p.H) * p.n_q;
+      uint4* dst = reinterpret_cast<uint4*>(p.o + b * rows_b * D);
+      for (size_t i = lane; i < rows_b * (D / 8); i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (size_t i = lane; i < rows_b; i += 32) p.lse[b * rows_b + i] = -INFINITY;
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -547,21 +575,20 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     const int box_shift = min(p.page_shift, KP == 2 ? 8 : 7);
     const unsigned all_boxes = 0xFFFFu >> (16 - (TILE >> box_shift));
     const int o_half = KP == 2 && (warp & 2) ? NR * TP : 0;    // columns that hold this lane's sums
-    bool ok = true;
-    int4 crossing = make_int4(0, 0, 0, -1);
-    long long at_tile = g0;
+    // A wait that gives up sets the CTA's abort flag, on which all others end at once; these
+    // warps go on through their barriers, and what they write is reported as invalid.
     // output of a finished part: where it goes, and its rows' references
     struct Done {
       int part, rows;
       bool whole;
-      size_t at0, slot;
-      float tref[NRW], mref[NRW];
+      size_t at0;
     } done;
     done.part = -1;
     // Every softmax thread comes here at the same point, also after giving up (the barriers).
     auto write_out = [&]() {
       const int buf = done.part & 1;
-      if (__any_sync(0xffffffffu, !mbar_wait(&o_full[buf], (done.part >> 1) & 1, ab, kDevTimeoutEpilogue))) ok = false;
+      mbar_wait(&o_full[buf], (done.part >> 1) & 1, ab, kDevTimeoutEpilogue);
+      __syncwarp();
       tc_fence_after_sync();
       float o[NRW];
 #pragma unroll
@@ -589,17 +616,18 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
           if (r >= done.rows) break;
           if constexpr (KP == 2) o[i] += xch_sh[r][t];
           const float l = ((l_sh[buf][0][r] + l_sh[buf][1][r]) + l_sh[buf][2][r]) + l_sh[buf][3][r];
+          const float tt = ref_sh[buf][0][r], mm = ref_sh[buf][1][r];
           // (a NaN among the scores or descales is in o by now, and stays)
-          const float f = l == 0.f || done.tref[i] == -INFINITY ? 0.f : ex2_approx(done.tref[i] - done.mref[i] - kPShift) / l;
-          const float val = o[i] * f;
-          const float lse = l == 0.f ? -INFINITY : (done.mref[i] + lg2(l)) * 0.69314718055994530942f;
+          const float val = o[i] * (l == 0.f ? 0.f : ex2_approx(mm - tt) / l);
+          const float lse = l == 0.f ? -INFINITY : (lg2(l) - mm) * 0.69314718055994530942f;
           if (done.whole) {
             const uint32_t pk = FP16 ? cvt_pack_f16(val, 0.f) : cvt_pack_bf16(val, 0.f);
             p.o[(done.at0 + r) * D + t] = static_cast<uint16_t>(pk);
             if (t == 0) p.lse[done.at0 + r] = lse;
           } else {
-            p.o_part[(done.slot * p.seg_rows + r) * D + t] = val;
-            if (t == 0) p.lse_part[done.slot * p.seg_rows + r] = lse;
+            const size_t at = (2ull * blockIdx.x + (done.part > 0 ? 1 : 0)) * p.seg_rows + r;
+            p.o_part[at * D + t] = val;
+            if (t == 0) p.lse_part[at] = lse;
           }
         }
       }
@@ -607,30 +635,43 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     };
 
     int n = 0;
-    Slot key{0, 0u}, old{1, 0u};            // old: the values of tile n - 1
+    // SAME: scores and P' of a tile are in the buffers of its slot's number
+    constexpr bool SAME = C::SB == NSLOT / 2 && C::PB == NSLOT / 2;
+    Ring<NSLOT, 2> key, last, used;         // last: tile n - 1; used: tile n - PB
+    Ring<C::SB> sb;
+    Ring<C::PB> pb;
     for (int part = 0; cur.left > 0; ++part) {
       const int take = cur.part(), len = cur.len;
       const int hk = cur.y / p.qtiles, row0 = (cur.y - hk * p.qtiles) * 16;
-      const int rows_here = min(NR, p.rows - row0);
-      if (__any_sync(0xffffffffu, !mbar_wait(&q_full[part & 1], (part >> 1) & 1, ab, kDevTimeoutSoftmax))) ok = false;
-      float cq[NRW], tref[NRW], mref[NRW], lsum[NRW];
-      unsigned vend[NRW];          // tokens [0, vend) visible to each row
+      mbar_wait(&q_full[part & 1], (part >> 1) & 1, ab, kDevTimeoutSoftmax);
+      __syncwarp();
+      // The references, as they are added to exponents: tt = 5 - T and mm = -M, at first so
+      // large that any finite score moves them.
+      float tt[NRW], mm[NRW], lsum[NRW];
 #pragma unroll
       for (int i = 0; i < NRW; ++i) {
-        const int r = r0 + i;
-        cq[i] = cq_sh[part & 1][r];
-        vend[i] = r < rows_here ? max(p.causal ? min(len, len - p.n_q + (row0 + r) % p.n_q + 1) : len, 0) : 0;
-        tref[i] = mref[i] = -INFINITY;
+        tt[i] = mm[i] = kFar;
         lsum[i] = 0.f;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_empty[part & 1]);
       const unsigned vis_all = max(p.causal ? len - p.n_q + 1 : len, 0);   // seen by every row
-      for (int i = 0; i < take; ++i, ++n, key.next()) {
-        const int buf = n & 1, kslot = key.at;
-        if (n >= 2) old.next();
-        // (the descales and the list of boxes came with the key tile)
-        if (__any_sync(0xffffffffu, !mbar_wait(&kv_full[kslot], key.phase, ab, kDevTimeoutSoftmax))) ok = false;
+      for (int i = 0; i < take; ++i, ++n) {
+        const int kslot = key.at, sbuf = SAME ? kslot / 2 : sb.at;
+        mbar_wait(&s_full[sbuf], SAME ? key.phase : sb.phase, ab, kDevTimeoutSoftmax);
+        mbar_test_wait(&kv_full[kslot], key.phase);        // complete: what came with the key tile is seen
+        __syncwarp();
+        tc_fence_after_sync();
+        constexpr int LD = C::CW == 1 ? C::NS : TQ * NRW;      // columns read
+        uint32_t raw[KP][LD];
+#pragma unroll
+        for (int h = 0; h < KP; ++h) {
+          const uint32_t at = tmem + lane_addr + C::S_COL(sbuf) + h * C::NS;
+          if constexpr (C::CW == 1) {
+            tmem_ld_cols<LD>(at, raw[h]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < TQ; ++k) tmem_ld_cols<NRW>(at + k * NR + r0, *reinterpret_cast<uint32_t(*)[NRW]>(&raw[h][k * NRW]));
+          }
+        }
         uint32_t ks2, vs2;         // descales of the thread's tokens (d = 64: two)
         const uint8_t* desc = sDesc + kslot / 2 * 4 * TILE;
         if constexpr (KP == 2) {
@@ -644,19 +685,13 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         const unsigned boxes = there_sh[kslot / 2];
         const bool there = (boxes >> (KP * t >> box_shift)) & 1u;
         const bool open = tile0 + TILE <= vis_all && boxes == all_boxes;
-        if (__any_sync(0xffffffffu, !mbar_wait(&s_full[buf], (n >> 1) & 1, ab, kDevTimeoutSoftmax))) ok = false;
-        tc_fence_after_sync();
-        uint32_t raw[KP][TQ][NRW];
-#pragma unroll
-        for (int h = 0; h < KP; ++h)
-#pragma unroll
-          for (int k = 0; k < TQ; ++k)
-            tmem_ld_cols<NRW>(tmem + lane_addr + C::S_COL(buf) + h * C::NS + k * NR + r0, raw[h][k]);
         tmem_ld_wait();
+        tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&kv_empty[kslot]);
-        // scores in log2 units, and with the value descale's logarithm
+        // scores in log2 units, s, and with the value descale's logarithm, y; a, b: with the references
         float s[KP][NRW], y[KP][NRW];
+        uint64_t a[KP][NRW / 2], b[KP][NRW / 2];
         bool need = false;
 #pragma unroll
         for (int h = 0; h < KP; ++h) {
@@ -665,41 +700,54 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
           const uint64_t ks_2 = pack2(ks, ks), lv_2 = pack2(lv, lv), step = pack2(1.f / (1 << kPStep), 1.f / (1 << kPStep));
 #pragma unroll
           for (int e = 0; e < NRW; e += 2) {
-            auto pair = [&](int k) { return pack2(__uint_as_float(raw[h][k][e]), __uint_as_float(raw[h][k][e + 1])); };
-            uint64_t a = pair(TQ - 1);
+            auto pair = [&](int k) {
+              const int c = k * (C::CW == 1 ? NR : NRW) + e;
+              return pack2(__uint_as_float(raw[h][c]), __uint_as_float(raw[h][c + 1]));
+            };
+            uint64_t x = pair(TQ - 1);
 #pragma unroll
-            for (int k = TQ - 2; k >= 0; --k) a = ffma2(a, step, pair(k));
-            a = fmul2(a, fmul2(pack2(cq[e], cq[e + 1]), ks_2));
-            const uint64_t b = fadd2(a, lv_2);
-            s[h][e] = lo2(a), s[h][e + 1] = hi2(a);
-            y[h][e] = lo2(b), y[h][e + 1] = hi2(b);
+            for (int k = TQ - 2; k >= 0; --k) x = ffma2(x, step, pair(k));
+            const float2 cq = *reinterpret_cast<const float2*>(&cq_sh[part & 1][r0 + e]);
+            x = fmul2(x, fmul2(pack2(cq.x, cq.y), ks_2));
+            const uint64_t z = fadd2(x, lv_2);
+            s[h][e] = lo2(x), s[h][e + 1] = hi2(x);
+            y[h][e] = lo2(z), y[h][e + 1] = hi2(z);
           }
           if (!open) {
 #pragma unroll
             for (int e = 0; e < NRW; ++e) {
-              const bool seen = there && key0 + h < vend[e];
+              const bool seen = there && key0 + h < vend_sh[part & 1][r0 + e];
               s[h][e] = seen ? s[h][e] : -INFINITY;
               y[h][e] = seen ? y[h][e] : -INFINITY;
             }
           }
-#pragma unroll
-          for (int e = 0; e < NRW; ++e) need |= y[h][e] > tref[e] + 3.f || s[h][e] > mref[e] + 64.f;
         }
+        auto exponents = [&]() {
+#pragma unroll
+          for (int h = 0; h < KP; ++h)
+#pragma unroll
+            for (int e = 0; e < NRW; e += 2) {
+              a[h][e / 2] = fadd2(pack2(s[h][e], s[h][e + 1]), pack2(mm[e], mm[e + 1]));
+              b[h][e / 2] = fadd2(pack2(y[h][e], y[h][e + 1]), pack2(tt[e], tt[e + 1]));
+            }
+        };
+        exponents();
+#pragma unroll
+        for (int h = 0; h < KP; ++h)
+#pragma unroll
+          for (int e = 0; e < NRW / 2; ++e)
+            need |= fmaxf(lo2(b[h][e]), hi2(b[h][e])) > kPShift + 3.f || fmaxf(lo2(a[h][e]), hi2(a[h][e])) > 64.f;
         if (any_of(BAR, MEMBERS, need)) {
           // references move to the maxima over the tile
-          float my[NRW], ms[NRW];
 #pragma unroll
           for (int e = 0; e < NRW; ++e) {
-            const float a = KP == 2 ? fmaxf(y[0][e], y[KP - 1][e]) : y[0][e];
-            const float b = KP == 2 ? fmaxf(s[0][e], s[KP - 1][e]) : s[0][e];
-            asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(my[e]) : "f"(a));
-            asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(ms[e]) : "f"(b));
-          }
-          if (lane == 0) {
-#pragma unroll
-            for (int e = 0; e < NRW; ++e) {
-              red_sh[0][warp & 3][r0 + e] = my[e];
-              red_sh[1][warp & 3][r0 + e] = ms[e];
+            float my = KP == 2 ? fmaxf(y[0][e], y[KP - 1][e]) : y[0][e];
+            float ms = KP == 2 ? fmaxf(s[0][e], s[KP - 1][e]) : s[0][e];
+            asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(my) : "f"(my));
+            asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(ms) : "f"(ms));
+            if (lane == 0) {
+              red_sh[0][warp & 3][r0 + e] = my;
+              red_sh[1][warp & 3][r0 + e] = ms;
             }
           }
           named_bar_sync(BAR, MEMBERS);
@@ -708,17 +756,20 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
 #pragma unroll
           for (int e = 0; e < NRW; ++e) {
             const int r = r0 + e;
-            const float ty = fmaxf(fmaxf(fmaxf(red_sh[0][0][r], red_sh[0][1][r]), fmaxf(red_sh[0][2][r], red_sh[0][3][r])), tref[e]);
-            const float tm = fmaxf(fmaxf(fmaxf(red_sh[1][0][r], red_sh[1][1][r]), fmaxf(red_sh[1][2][r], red_sh[1][3][r])), mref[e]);
-            alpha[e] = tref[e] == -INFINITY ? (ty == -INFINITY ? 1.f : 0.f) : ex2_approx(tref[e] - ty);
-            grew |= ty > tref[e];
-            lsum[e] *= mref[e] == -INFINITY ? 0.f : ex2_approx(mref[e] - tm);
-            tref[e] = ty;
-            mref[e] = tm;
+            const float ty = fmaxf(fmaxf(red_sh[0][0][r], red_sh[0][1][r]), fmaxf(red_sh[0][2][r], red_sh[0][3][r]));
+            const float tm = fmaxf(fmaxf(red_sh[1][0][r], red_sh[1][1][r]), fmaxf(red_sh[1][2][r], red_sh[1][3][r]));
+            const float t_new = fminf(tt[e], kPShift - ty), m_new = fminf(mm[e], -tm);
+            alpha[e] = ex2_approx(t_new - tt[e]);
+            lsum[e] *= ex2_approx(m_new - mm[e]);
+            grew |= t_new < tt[e];
+            tt[e] = t_new;
+            mm[e] = m_new;
           }
+          exponents();
           if (i > 0 && grew) {
             // O^T times alpha once P' V(n - 1) is in it (the phase of its value slot's empty barrier)
-            if (__any_sync(0xffffffffu, !mbar_wait(&kv_empty[old.at], old.phase, ab, kDevTimeoutSoftmax))) ok = false;
+            mbar_wait(&kv_empty[last.at + 1], last.phase, ab, kDevTimeoutSoftmax);
+            __syncwarp();
             tc_fence_after_sync();
 #pragma unroll
             for (int k = 0; k < TP; ++k) {
@@ -734,32 +785,61 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
           }
           named_bar_sync(BAR, MEMBERS);                        // red_sh has been read
         }
-        // probabilities as e4m3 terms, bytes of their rows' columns
-        const uint32_t pbase = smem_u32(sP + buf * C::P_TILE) + (t & 15);
+        if (n >= C::PB) {
+          // P' of tile n - PB has been multiplied
+          if constexpr (SAME) {
+            mbar_wait(&kv_empty[kslot + 1], key.phase ^ 1u, ab, kDevTimeoutSoftmax);
+          } else {
+            mbar_wait(&kv_empty[used.at + 1], used.phase, ab, kDevTimeoutSoftmax);
+            used.next();
+          }
+        }
+        // probabilities as e4m3 terms: column (h TP + k) NR + row, four of them a word
+        uint32_t w[KP][TP][NRW / 4];
 #pragma unroll
         for (int h = 0; h < KP; ++h)
 #pragma unroll
           for (int e = 0; e < NRW; e += 2) {
-            const uint64_t tr = pack2(kPShift - (tref[e] == -INFINITY ? 0.f : tref[e]),
-                                      kPShift - (tref[e + 1] == -INFINITY ? 0.f : tref[e + 1]));
-            const uint64_t mr = pack2(mref[e] == -INFINITY ? 0.f : -mref[e], mref[e + 1] == -INFINITY ? 0.f : -mref[e + 1]);
-            const uint64_t a = fadd2(pack2(s[h][e], s[h][e + 1]), mr), b = fadd2(pack2(y[h][e], y[h][e + 1]), tr);
-            lsum[e] += ex2_approx(lo2(a));
-            lsum[e + 1] += ex2_approx(hi2(a));
-            __half2 x = as_half2(cvt_pack_f16(ex2_approx(lo2(b)), ex2_approx(hi2(b))));
+            lsum[e] += ex2_approx(lo2(a[h][e / 2]));
+            lsum[e + 1] += ex2_approx(hi2(a[h][e / 2]));
+            __half2 x = as_half2(cvt_pack_f16(ex2_approx(lo2(b[h][e / 2])), ex2_approx(hi2(b[h][e / 2]))));
 #pragma unroll
             for (int k = 0; k < TP; ++k) {
               const uint32_t c = e4m3_pair_h(half2_bits(x));
               if (k + 1 < TP) x = __hmul2(__hsub2(x, as_half2(e4m3_halves(c))), __float2half2_rn(1 << kPStep));
-              const int col = h * NR * TP + k * NR + r0 + e;
-              st_shared_u8(pbase + col * 128 + ((((t >> 4) ^ col) & 7) << 4), c & 0xFFu);
-              st_shared_u8(pbase + (col + 1) * 128 + ((((t >> 4) ^ (col + 1)) & 7) << 4), c >> 8);
+              w[h][k][e / 4] = e & 2 ? w[h][k][e / 4] | (c << 16) : c;
             }
           }
+        {
+          const uint32_t at = smem_u32(sP + (SAME ? key.at / 2 : pb.at) * C::P_TILE) + t * 16;
+          if constexpr (C::CW == 1) {
+            // all columns of the key: words 4 i .. 4 i + 3 are its i-th 16
+            constexpr int n_words = KP * TP * NR / 4;
+            const uint32_t* const ws = &w[0][0][0];
+#pragma unroll
+            for (int i = 0; i < n_words; i += 4) {
+              const uint32_t dst = at + i / 4 * 128 * 16;
+              if (n_words - i >= 4) st_shared_v4(dst, ws[i], ws[i + 1], ws[i + 2], ws[i + 3]);
+              else if (n_words - i == 3) st_shared_v4(dst, ws[i], ws[i + 1], ws[i + 2], 0u);
+              else st_shared_v2(dst, ws[i], ws[i + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < KP; ++h)
+#pragma unroll
+              for (int k = 0; k < TP; ++k) st_shared_v2(at + (h * TP + k) * 128 * 16 + r0, w[h][k][0], w[h][k][1]);
+          }
+        }
         fence_proxy_async_smem();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[buf]);
+        if (lane == 0) mbar_arrive(&p_full[SAME ? key.at / 2 : pb.at]);
+        last = key;
+        key.next();
+        if constexpr (!SAME) {
+          sb.next();
+          pb.next();
+        }
         // the part before this one, while this tile's products run
         if (i == 0 && part > 0) write_out();
       }
@@ -768,26 +848,21 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       for (int e = 0; e < NRW; ++e) {
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) lsum[e] += __shfl_xor_sync(0xffffffffu, lsum[e], m);
-        if (lane == 0) l_sh[part & 1][warp & 3][r0 + e] = lsum[e];
-        done.tref[e] = tref[e];
-        done.mref[e] = mref[e];
+        if (lane == 0) {
+          l_sh[part & 1][warp & 3][r0 + e] = lsum[e];
+          ref_sh[part & 1][0][r0 + e] = tt[e];
+          ref_sh[part & 1][1][r0 + e] = mm[e];
+        }
       }
+      // the part's coefficients and ends have been read
+      if (lane == 0) mbar_arrive(&q_empty[part & 1]);
       done.part = part;
-      done.rows = rows_here;
+      done.rows = min(NR, p.rows - row0);
       done.whole = take == cur.tiles();
       done.at0 = (static_cast<size_t>(cur.b) * p.H_kv + hk) * p.rows + row0;
-      done.slot = 2ull * blockIdx.x + (part > 0 ? 1 : 0);
-      if (!done.whole && cur.j == 0) {
-        // CTA whose share holds the segment's last tile: the last c with c T / n <= it
-        const long long ctas = T < gridDim.x ? T : gridDim.x, last = at_tile + cur.tiles() - 1;
-        crossing = make_int4(static_cast<int>(done.at0), rows_here, static_cast<int>(((last + 1) * ctas - 1) / T),
-                             static_cast<int>(done.slot));
-      }
-      at_tile += take;
       cur.next_part(p);
     }
     if (done.part >= 0) write_out();
-    if (threadIdx.x == 0) p.crossing[blockIdx.x] = crossing;
   }
 
   // ------------------------------------------------------------ teardown
@@ -819,6 +894,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
 constexpr int kMergeThreads = 128;
 template <int D, bool FP16>
 __global__ void __launch_bounds__(kMergeThreads) decode_fp4_merge_kernel(const KParams p) {
+  release_dependents();
   wait_for_previous_kernel();
   const int4 seg = __ldcg(p.crossing + blockIdx.x);
   const int r = blockIdx.y * (kMergeThreads / (D / 4)) + threadIdx.x / (D / 4), col = threadIdx.x % (D / 4) * 4;

@@ -309,6 +309,14 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo_byt
   return d;
 }
 
+// MN-major operand of 8-bit values without swizzle: each k's 16 values along M/N side by side,
+// the k one behind the other; mn_bytes from one 16 along M/N to the next, k_bytes from one
+// group of 8 k to the next.
+__device__ __forceinline__ uint64_t sdesc_mn_plain(uint32_t saddr, uint32_t mn_bytes, uint32_t k_bytes) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>((k_bytes >> 4) & 0x3FFFu) << 16 |
+         static_cast<uint64_t>((mn_bytes >> 4) & 0x3FFFu) << 32 | 1ull << 46;
+}
+
 // Descriptor of the same operand `byte_off` bytes further on.  The start
 // address field holds address >> 4 in 14 bits, and every shared-memory address
 // here is below 256 KB, so the add cannot carry into the next field.
@@ -349,8 +357,8 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N, bool a
 
 // kind::f8f6f4 with A e2m1 (format code 5) and B e4m3, K-major B.  A's codes stand in shared
 // memory as TMA's 4-bit unpacking leaves them: 16 of them in eight bytes, then eight bytes unused.
-__host__ __device__ constexpr uint32_t idesc_e2m1_e4m3(uint32_t M, uint32_t N, bool a_mn) {
-  return idesc_e4m3(M, N, a_mn, false) | (5u << 7);
+__host__ __device__ constexpr uint32_t idesc_e2m1_e4m3(uint32_t M, uint32_t N, bool a_mn, bool b_mn) {
+  return idesc_e4m3(M, N, a_mn, b_mn) | (5u << 7);
 }
 
 // D(tmem) (+)= A(smem) * B(smem)
