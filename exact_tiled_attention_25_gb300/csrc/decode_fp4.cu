@@ -68,10 +68,12 @@ struct Cfg {
   static constexpr int LOAD = SW, MMA_S = SW + 1, MMA_PV = SW + 2, QUERY = SW + 3;
   static constexpr int THREADS = (SW + 4) * 32;
   static constexpr int CTAS = NR == 16 ? 1 : 2;          // of an SM (16 rows: registers)
-  static constexpr int Q_TILE = NS * 128, P_TILE = NPV * 128;
+  // The two query tiles (NS rows of D bytes); of d = 64 they are the halves of one of 128 bytes a row.
+  static constexpr int Q_BYTES = 2 * NS * D, P_TILE = NPV * 128;
+  static constexpr int Q_STEP = KP == 2 ? 64 : NS * 128;
   static constexpr int PB = NR == 4 && KP == 1 ? 3 : 2;  // buffers of P'
-  static constexpr int FIXED = 1024 + 2 * Q_TILE + PB * P_TILE;
-  static constexpr int PER_CTA = kSmemPerSm / CTAS - 4096;   // (static shared memory and what the system takes)
+  static constexpr int FIXED = 1024 + Q_BYTES + PB * P_TILE;
+  static constexpr int PER_CTA = kSmemPerSm / CTAS - 3072;   // (static shared memory and what the system takes)
   static constexpr int FIT = (PER_CTA - FIXED) / (SLOT + 2 * TILE) / 2 * 2;
   static constexpr int NSLOT = FIT > 12 ? 12 : FIT;      // even: keys in even slots, values in odd ones
   static constexpr uint32_t S_COLS = KP * NS;            // of one score buffer
@@ -80,7 +82,7 @@ struct Cfg {
   __host__ __device__ static constexpr uint32_t S_COL(int buf) { return S_COLS * buf; }
   __host__ __device__ static constexpr uint32_t O_COL(int buf) { return SB * S_COLS + NPV * buf; }
   static constexpr int TMEM = pow2(SB * S_COLS + 2 * NPV);
-  static constexpr int DESC_OFF = 2 * Q_TILE + PB * P_TILE + NSLOT * SLOT;
+  static constexpr int DESC_OFF = Q_BYTES + PB * P_TILE + NSLOT * SLOT;
   static constexpr int SMEM = 1024 + DESC_OFF + NSLOT / 2 * 4 * TILE;
   static_assert(NSLOT >= 2 * PB && SB >= 2 && TMEM * CTAS <= 512, "ring or tensor memory");
 };
@@ -217,9 +219,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* const sQ = smem;                              // two query tiles, NS x 128 bytes
+  uint8_t* const sQ = smem;                              // two query tiles
   // PB tiles of P': a key's 16 columns side by side, the tile's 128 keys, the next 16 columns
-  uint8_t* const sP = smem + 2 * C::Q_TILE;
+  uint8_t* const sP = smem + C::Q_BYTES;
   uint8_t* const sKV = sP + C::PB * C::P_TILE;
   uint8_t* const sDesc = smem + C::DESC_OFF;             // per key slot: TILE key descales, TILE value descales
 
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     for (int i = 0; i < C::SB; ++i) mbar_init(&s_full[i], 1);
     for (int i = 0; i < C::PB; ++i) mbar_init(&p_full[i], C::SW);
     for (int s = 0; s < NSLOT; ++s) {
-      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_full[s], s & 1 ? 1 : 33);            // keys: the tile's bytes, and each lane's descales
       mbar_init(&kv_empty[s], s & 1 ? 1 : C::SW);
     }
     abort_sh = 0;
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     prefetch_tmap(&tmV);
   }
   // columns that no row of queries or of P' fills stay zero
-  for (int i = threadIdx.x; i < (2 * C::Q_TILE + C::PB * C::P_TILE) / 16; i += C::THREADS)
+  for (int i = threadIdx.x; i < (C::Q_BYTES + C::PB * C::P_TILE) / 16; i += C::THREADS)
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   wait_for_previous_kernel();
@@ -325,8 +327,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   if (warp == C::LOAD) {
     // ------------------------------------------------------------ producer
     // A tile is fetched page by page: a box is min(page_size, TILE) tokens of one page, at most
-    // 16 of them.  Lane x issues box x; of a key tile, lanes 16 + x the descales of both the
-    // keys and the values.  The pages of 32 boxes are read from the block table at a time, the
+    // 16 of them.  Lane x issues box x (a copy costs its warp some hundred clocks).  The descales of
+    // the tile's keys and values come with its keys, by 16-byte copies of all lanes (8 tokens each; a
+    // bulk copy for each page took as long as the codes' own).  The pages of 32 boxes are read from the block table at a time, the
     // next 32 while those are in use.  Boxes behind the sequence are left out, as are those on
     // pages outside the cache (reported): what the slot held before is finite codes, and their
     // tokens are masked.
@@ -347,13 +350,13 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
           win = win_next;
           win_next = window(i * nbox / 32 + 1);
         }
-        const int x = lane & 15;
-        const int phys = __shfl_sync(0xffffffffu, win, (i * nbox + x) & 31);
-        const long long key = static_cast<long long>(kbeg) + i * TILE + x * box;
-        const bool wanted = x < nbox && key < cur.len;
+        const int box_at = (i * nbox) & 31;
+        const int phys = __shfl_sync(0xffffffffu, win, (box_at + lane) & 31);
+        const long long key = static_cast<long long>(kbeg) + i * TILE + lane * box;
+        const bool wanted = lane < nbox && key < cur.len;
         const bool good = wanted && phys >= 0 && phys < p.num_pages;
-        if (wanted && !good && lane < 16) atomicCAS(p.status, 0, kDevBadSeqlens);
-        const unsigned there = __ballot_sync(0xffffffffu, good) & 0xffffu;
+        if (wanted && !good) atomicCAS(p.status, 0, kDevBadSeqlens);
+        const unsigned there = __ballot_sync(0xffffffffu, good);
         const int off = static_cast<int>(key) & (p.page_size - 1);
         for (int kv = 0; kv < 2; ++kv) {
           const int slot = key_slot.at + kv;
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
               go = 0;
             } else {
               if (kv == 0) there_sh[slot / 2] = there;
-              mbar_arrive_expect_tx(&kv_full[slot], __popc(there) * box * (D / 2 + (kv == 0 ? 4 : 0)));
+              mbar_arrive_expect_tx(&kv_full[slot], __popc(there) * box * (D / 2));
               issued_sh[kv] = n + 1;
             }
           }
@@ -371,14 +374,18 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
             ok = false;
             break;
           }
-          if (!good) continue;
-          if (lane < 16) {
-            tma_load_4d(sKV + slot * C::SLOT + x * (box / KP) * 128, kv ? &tmV : &tmK, &kv_full[slot], 0, off / KP, hk, phys);
-          } else if (kv == 0) {
-            uint8_t* dst = sDesc + slot / 2 * 4 * TILE + 2 * x * box;
-            const size_t row = (static_cast<size_t>(phys) * p.H_kv + hk) * p.page_size + off;
-            bulk_load(dst, p.descale[0] + row, 2 * box, &kv_full[slot]);
-            bulk_load(dst + 2 * TILE, p.descale[1] + row, 2 * box, &kv_full[slot]);
+          if (good)
+            tma_load_4d(sKV + slot * C::SLOT + lane * (box / KP) * 128, kv ? &tmV : &tmK, &kv_full[slot], 0, off / KP, hk, phys);
+          if (kv == 0) {
+            uint8_t* dst = sDesc + slot / 2 * 4 * TILE;
+#pragma unroll
+            for (int c = lane; c < TILE / 4; c += 32) {          // 16 bytes: keys' first, then values'
+              const int tok = c % (TILE / 8) * 8, x = tok / box;
+              const int page = __shfl_sync(0xffffffffu, phys, x);
+              const size_t row = (static_cast<size_t>(page) * p.H_kv + hk) * p.page_size + ((kbeg + i * TILE + tok) & (p.page_size - 1));
+              if ((there >> x) & 1u) copy16_async(dst + c * 16, p.descale[c / (TILE / 8)] + row, true);
+            }
+            copies_arrive(&kv_full[slot]);
           }
         }
       }
@@ -400,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       for (int part = 0; ok && cur.left > 0; ++part) {
         const int take = cur.part();
         if (!(ok = mbar_wait(&q_full[part & 1], (part >> 1) & 1, ab, kDevTimeoutMma))) break;
-        const uint64_t qdesc = opaque(sdesc_add(qdesc0, (part & 1) * C::Q_TILE));
+        const uint64_t qdesc = opaque(sdesc_add(qdesc0, (part & 1) * C::Q_STEP));
         for (int i = 0; i < take; ++i, ++n, key.next(), buf.next()) {
           if (!(ok = mbar_wait(&kv_full[key.at], key.phase, ab, kDevTimeoutMma))) break;
           if (C::SB < NSLOT / 2 && n >= C::SB) {
@@ -537,7 +544,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
           }
           const int col = k * NR + r;
           if (r < NR)
-            st_shared_v4(smem_u32(sQ + buf * C::Q_TILE + col * 128 + ((u ^ (col & 7)) << 4)), w[0], w[1], w[2], w[3]);
+            {
+            const int piece = KP == 2 ? 4 * buf + u : u;         // of the row's eight
+            uint8_t* tile = KP == 2 ? sQ : sQ + buf * C::Q_STEP;
+            st_shared_v4(smem_u32(tile + col * 128 + ((piece ^ (col & 7)) << 4)), w[0], w[1], w[2], w[3]);
+          }
         }
         if (u == 0 && r < NR) {
           cq_sh[buf][r] = p.scale_log2 * back;
