@@ -165,27 +165,34 @@ __device__ __forceinline__ int tokens_of(const KParams& p, int b) {
 template <int TILE>
 __device__ __forceinline__ int tiles_of(int len) { return static_cast<int>((static_cast<unsigned>(len) + TILE - 1) / TILE); }
 
-// First tile of CTA c's share of T tiles (at most T CTAs get one).
+// First unit of CTA c's share of T units (at most T CTAs get one).
 __device__ __forceinline__ long long share_start(long long c, int C, long long T) {
   const long long n = T < C ? T : C;
   return c >= n ? T : c * T / n;
 }
 
-// A walk over the parts of segments in a share.
+// A walk over the parts of segments in a share.  A segment is `extra` units for its start and its
+// end, then one for each tile but that the first comes with the start: a share that begins in
+// the extra ones begins at tile 1.
 template <int TILE>
 struct Cursor {
-  int b, y, j;           // sequence, segment of it, first tile
+  int b, y;              // sequence, segment of it
   int len;
-  long long left;        // tiles of the share from here on
+  int at;                // first unit in the segment
+  int extra;
+  long long left;        // units of the share from here on
   __device__ __forceinline__ int tiles() const { return tiles_of<TILE>(len); }
-  __device__ __forceinline__ int part() const {
-    const int rest = tiles() - j;
+  __device__ __forceinline__ int units() const {
+    const int rest = tiles() + extra - at;
     return left < rest ? static_cast<int>(left) : rest;
   }
+  __device__ __forceinline__ int tile_at(int u) const { return u == 0 ? 0 : max(1, u - extra); }
+  __device__ __forceinline__ int first() const { return tile_at(at); }           // tile
+  __device__ __forceinline__ int part() const { return tile_at(at + units()) - first(); }   // tiles
   __device__ __forceinline__ void next_part(const KParams& p) {
-    left -= part();
+    left -= units();
     if (left <= 0) return;
-    j = 0;
+    at = 0;
     if (++y == p.segs) {
       y = 0;
       do {
@@ -194,7 +201,6 @@ struct Cursor {
     }
   }
 };
-
 
 // A place in a ring of N buffers, used every STEP-th (a tile's keys stand in even slots, its values
 // in odd ones), and the phase of its barriers' use.
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       o_full[2], o_empty[2], drain_bar[2];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, issued_sh[2];                 // key and value tiles whose copies have been issued
-  __shared__ long long warp_sum[C::THREADS / 32], start_sh[3];
+  __shared__ long long warp_sum[2][C::THREADS / 32], start_sh[3];
   __shared__ unsigned there_sh[NSLOT / 2];               // boxes of a key tile that were copied
   __shared__ __align__(16) float cq_sh[2][NR];           // of a part's query rows: score coefficients,
   __shared__ unsigned vend_sh[2][NR];                    // ends of the visible tokens,
@@ -271,37 +277,56 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   wait_for_previous_kernel();
   release_dependents();
 
-  // ---- tiles of one segment of the entries before each; this CTA's share
+  // ---- units of one segment of the entries before each; this CTA's share
   const int per = (p.B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
   long long sum = 0;
-  int len = 0;
+  int len = 0, some = 0;                    // some: entries with tokens
   for (int b = b0; b < b1; ++b) {
     len = tokens_of(p, b);
     if (len == 0 && blockIdx.x == 0 && __ldcg(p.seq_lens + b) != 0) atomicCAS(p.status, 0, kDevBadSeqlens);
     sum += tiles_of<TILE>(len);
+    some += len > 0;
   }
   long long scan = sum;
+  int scan_some = some;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += x;
+    const int z = __shfl_up_sync(0xffffffffu, scan_some, o);
+    if (lane >= o) {
+      scan += x;
+      scan_some += z;
+    }
   }
-  if (lane == 31) warp_sum[warp] = scan;
+  if (lane == 31) {
+    warp_sum[0][warp] = scan;
+    warp_sum[1][warp] = scan_some;
+  }
   __syncthreads();
-  long long base = scan - sum, all = 0;
+  long long base = scan - sum, all = 0, base_some = scan_some - some, all_some = 0;
   for (int w = 0; w < C::THREADS / 32; ++w) {
-    if (w < warp) base += warp_sum[w];
-    all += warp_sum[w];
+    if (w < warp) {
+      base += warp_sum[0][w];
+      base_some += warp_sum[1][w];
+    }
+    all += warp_sum[0][w];
+    all_some += warp_sum[1][w];
   }
-  const long long T = all * p.segs;
+  // A part's start and end take some two tiles' time (64 sequences of up to 16384, d = 64: without
+  // them counted the CTA with the shortest ones ended 10 us after the others).  A share of 8 tiles
+  // and more cannot lie within them.
+  const int extra = all * p.segs >= 8ll * gridDim.x ? 2 : 0;
+  base += extra * base_some;
+  sum += extra * some;
+  const long long T = (all + extra * all_some) * p.segs;
   const long long g0 = share_start(blockIdx.x, gridDim.x, T);
   const long long total = share_start(blockIdx.x + 1ll, gridDim.x, T) - g0;
   if (total > 0 && base * p.segs <= g0 && g0 < (base + sum) * p.segs) {
     int b = b0;
     for (; b1 - b0 > 1; ++b) {
       len = tokens_of(p, b);
-      const int n = tiles_of<TILE>(len);
+      const int n = len > 0 ? tiles_of<TILE>(len) + extra : 0;
       if (g0 < (base + n) * p.segs) break;
       base += n;
     }
@@ -315,13 +340,14 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   const uint32_t tmem = tmem_base_sh;
   const Abort ab{&abort_sh, p.status};
 
-  Cursor<TILE> cur{0, 0, 0, 0, total};
+  Cursor<TILE> cur{0, 0, 0, 0, extra, total};
   if (total > 0) {
     cur.b = static_cast<int>(start_sh[0]);
     cur.len = static_cast<int>(start_sh[2]);
-    const int n = cur.tiles();
+    const int n = cur.tiles() + extra;
     cur.y = static_cast<int>(start_sh[1] / n);
-    cur.j = static_cast<int>(start_sh[1] - static_cast<long long>(cur.y) * n);
+    cur.at = static_cast<int>(start_sh[1] - static_cast<long long>(cur.y) * n);
+    if (cur.part() == 0) cur.next_part(p);            // a single tile, of the CTA before
   }
 
   if (warp == C::LOAD) {
@@ -338,7 +364,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     Ring<NSLOT, 2> key_slot;
     bool ok = true;
     while (ok && cur.left > 0) {
-      const int take = cur.part(), hk = cur.y / p.qtiles, kbeg = cur.j * TILE;   // kbeg < len
+      const int take = cur.part(), hk = cur.y / p.qtiles, kbeg = cur.first() * TILE;   // kbeg < len
       auto window = [&](int w) -> int {
         const long long key = kbeg + static_cast<long long>(32 * w + lane) * box;
         if (key >= cur.len || 32 * w + lane >= take * nbox) return -1;
@@ -465,7 +491,6 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     constexpr int L = D / 16, PER = 32 / L;
     const int u = lane % L;
     bool ok = true;
-    long long at_tile = g0;
     int4 crossing = make_int4(0, 0, 0, -1);            // a segment that this share begins and does not end
     for (int part = 0; ok && cur.left > 0; ++part) {
       const int buf = part & 1;
@@ -476,16 +501,23 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       const int hk = cur.y / p.qtiles, row0 = (cur.y - hk * p.qtiles) * 16;
       const size_t at0 = (static_cast<size_t>(cur.b) * p.H_kv + hk) * p.rows + row0;
       const int rows_here = min(NR, p.rows - row0);
-#pragma unroll 1
-      for (int r0 = 0; r0 < NR; r0 += PER) {
-        const int r = r0 + lane / L;
+      uint4 raw[(NR + PER - 1) / PER][2];
+#pragma unroll
+      for (int x = 0; x < (NR + PER - 1) / PER; ++x) {
+        const int r = x * PER + lane / L;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (at0 + (r < rows_here ? r : 0)) * D + 16 * u);
+        raw[x][0] = __ldcg(src);
+        raw[x][1] = __ldcg(src + 1);
+      }
+#pragma unroll
+      for (int pass = 0; pass < (NR + PER - 1) / PER; ++pass) {
+        const int r = pass * PER + lane / L;
         const bool live = r < rows_here;
         float x[16];
         {
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + (at0 + (live ? r : 0)) * D + 16 * u);
           float lo[8], hi[8];
-          unpack16<FP16>(__ldcg(src), lo);
-          unpack16<FP16>(__ldcg(src + 1), hi);
+          unpack16<FP16>(raw[pass][0], lo);
+          unpack16<FP16>(raw[pass][1], hi);
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = live ? lo[i] : 0.f, x[8 + i] = live ? hi[i] : 0.f;
         }
@@ -558,13 +590,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[buf]);
-      if (cur.j == 0 && cur.part() < cur.tiles()) {
-        // CTA whose share holds the segment's last tile: the last c with c T / n <= it
-        const long long n = T < gridDim.x ? T : gridDim.x, last = at_tile + cur.tiles() - 1;
+      if (cur.first() == 0 && cur.part() < cur.tiles()) {
+        // CTA whose share holds the segment's last unit: the last c with c T / n <= it
+        const long long n = T < gridDim.x ? T : gridDim.x, last = g0 + (total - cur.left) - cur.at + cur.tiles() + extra - 1;
         crossing = make_int4(static_cast<int>(at0), rows_here, static_cast<int>(((last + 1) * n - 1) / T),
                              static_cast<int>(2 * blockIdx.x + (part > 0 ? 1 : 0)));
       }
-      at_tile += cur.part();
       cur.next_part(p);
     }
     if (lane == 0) p.crossing[blockIdx.x] = crossing;
@@ -652,7 +683,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     Ring<C::SB> sb;
     Ring<C::PB> pb;
     for (int part = 0; cur.left > 0; ++part) {
-      const int take = cur.part(), len = cur.len;
+      const int take = cur.part(), len = cur.len, first_tile = cur.first();
       const int hk = cur.y / p.qtiles, row0 = (cur.y - hk * p.qtiles) * 16;
       mbar_wait(&q_full[part & 1], (part >> 1) & 1, ab, kDevTimeoutSoftmax);
       __syncwarp();
@@ -692,7 +723,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
           ks2 = *reinterpret_cast<const uint16_t*>(desc + 2 * t);
           vs2 = *reinterpret_cast<const uint16_t*>(desc + 2 * TILE + 2 * t);
         }
-        const unsigned tile0 = static_cast<unsigned>(cur.j + i) * TILE, key0 = tile0 + KP * t;
+        const unsigned tile0 = static_cast<unsigned>(first_tile + i) * TILE, key0 = tile0 + KP * t;
         const unsigned boxes = there_sh[kslot / 2];
         const bool there = (boxes >> (KP * t >> box_shift)) & 1u;
         const bool open = tile0 + TILE <= vis_all && boxes == all_boxes;
