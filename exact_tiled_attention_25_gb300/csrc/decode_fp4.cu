@@ -157,6 +157,32 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)
   else tmem_st4(taddr, r);
 }
 
+// Sums of N values over the warp's lanes: in each round a lane sends half of the values it still
+// holds to the lane `step` away and adds what it gets to the others.  Lane l ends with the sum of
+// value `which`, the first bits of l from above.
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N], int lane, int* which) {
+  int held = N, first = 0;
+#pragma unroll
+  for (int step = 16; step > 0; step >>= 1) {
+    if (held > 1) {
+      held /= 2;
+      const bool up = (lane & step) != 0;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i >= held) break;
+        const float send = up ? v[i] : v[i + held], keep = up ? v[i + held] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, step);
+      }
+      if (up) first += held;
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], step);
+    }
+  }
+  *which = first;
+  return v[0];
+}
+
 // Tokens of a sequence; one out of range counts as none.
 __device__ __forceinline__ int tokens_of(const KParams& p, int b) {
   const int n = __ldcg(p.seq_lens + b);
@@ -240,7 +266,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   __shared__ __align__(16) float cq_sh[2][NR];           // of a part's query rows: score coefficients,
   __shared__ unsigned vend_sh[2][NR];                    // ends of the visible tokens,
   __shared__ float ref_sh[2][2][NR], l_sh[2][4][NR];     // references at its end, and sums by key quarter
-  __shared__ float red_sh[2][4][NR];                     // maxima of a tile by key quarter
+  __shared__ float red_sh[2][2][4][NR];                  // maxima of a tile (by parity) by key quarter
   __shared__ float xch_sh[KP == 2 ? NR : 1][KP == 2 ? 64 : 1];
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -652,24 +678,27 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       }
       named_bar_sync(BAR, MEMBERS);                            // the sums of rows are there, too
       if (KP == 1 || !(warp & 2)) {
+        // lane i: factor and log-sum-exp of row i
+        const int mine = r0 + (lane & (NRW - 1));
+        const float l = ((l_sh[buf][0][mine] + l_sh[buf][1][mine]) + l_sh[buf][2][mine]) + l_sh[buf][3][mine];
+        const float tt = ref_sh[buf][0][mine], mm = ref_sh[buf][1][mine];
+        // (a NaN among the scores or descales is in o by now, and stays)
+        const float f = l == 0.f ? 0.f : ex2_approx(mm - tt) / l;
+        const float lse = l == 0.f ? -INFINITY : (lg2(l) - mm) * 0.69314718055994530942f;
+        const size_t at = done.whole ? done.at0 : (2ull * blockIdx.x + (done.part > 0 ? 1 : 0)) * p.seg_rows;
+        if ((warp & 3) == 0 && lane < NRW && mine < done.rows) (done.whole ? p.lse : p.lse_part)[at + mine] = lse;
 #pragma unroll
         for (int i = 0; i < NRW; ++i) {
           const int r = r0 + i;
-          if (r >= done.rows) break;
+          const float fi = __shfl_sync(0xffffffffu, f, i);
+          if (r >= done.rows) continue;
           if constexpr (KP == 2) o[i] += xch_sh[r][t];
-          const float l = ((l_sh[buf][0][r] + l_sh[buf][1][r]) + l_sh[buf][2][r]) + l_sh[buf][3][r];
-          const float tt = ref_sh[buf][0][r], mm = ref_sh[buf][1][r];
-          // (a NaN among the scores or descales is in o by now, and stays)
-          const float val = o[i] * (l == 0.f ? 0.f : ex2_approx(mm - tt) / l);
-          const float lse = l == 0.f ? -INFINITY : (lg2(l) - mm) * 0.69314718055994530942f;
+          const float val = o[i] * fi;
           if (done.whole) {
             const uint32_t pk = FP16 ? cvt_pack_f16(val, 0.f) : cvt_pack_bf16(val, 0.f);
-            p.o[(done.at0 + r) * D + t] = static_cast<uint16_t>(pk);
-            if (t == 0) p.lse[done.at0 + r] = lse;
+            p.o[(at + r) * D + t] = static_cast<uint16_t>(pk);
           } else {
-            const size_t at = (2ull * blockIdx.x + (done.part > 0 ? 1 : 0)) * p.seg_rows + r;
-            p.o_part[at * D + t] = val;
-            if (t == 0) p.lse_part[at] = lse;
+            p.o_part[(at + r) * D + t] = val;
           }
         }
       }
@@ -788,8 +817,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
             asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(my) : "f"(my));
             asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(ms) : "f"(ms));
             if (lane == 0) {
-              red_sh[0][warp & 3][r0 + e] = my;
-              red_sh[1][warp & 3][r0 + e] = ms;
+              red_sh[n & 1][0][warp & 3][r0 + e] = my;
+              red_sh[n & 1][1][warp & 3][r0 + e] = ms;
             }
           }
           named_bar_sync(BAR, MEMBERS);
@@ -798,8 +827,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
 #pragma unroll
           for (int e = 0; e < NRW; ++e) {
             const int r = r0 + e;
-            const float ty = fmaxf(fmaxf(red_sh[0][0][r], red_sh[0][1][r]), fmaxf(red_sh[0][2][r], red_sh[0][3][r]));
-            const float tm = fmaxf(fmaxf(red_sh[1][0][r], red_sh[1][1][r]), fmaxf(red_sh[1][2][r], red_sh[1][3][r]));
+            const float(*red)[4][NR] = red_sh[n & 1];
+            const float ty = fmaxf(fmaxf(red[0][0][r], red[0][1][r]), fmaxf(red[0][2][r], red[0][3][r]));
+            const float tm = fmaxf(fmaxf(red[1][0][r], red[1][1][r]), fmaxf(red[1][2][r], red[1][3][r]));
             const float t_new = fminf(tt[e], kPShift - ty), m_new = fminf(mm[e], -tm);
             alpha[e] = ex2_approx(t_new - tt[e]);
             lsum[e] *= ex2_approx(m_new - mm[e]);
@@ -825,7 +855,6 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
             }
             tmem_st_wait();
           }
-          named_bar_sync(BAR, MEMBERS);                        // red_sh has been read
         }
         if (n >= C::PB) {
           // P' of tile n - PB has been multiplied
@@ -886,16 +915,15 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         if (i == 0 && part > 0) write_out();
       }
       // this part's row sums, and what its output needs
+      int which;
+      const float row_sum = warp_sums<NRW>(lsum, lane, &which);
+      l_sh[part & 1][warp & 3][r0 + which] = row_sum;          // (several lanes, the same value)
 #pragma unroll
-      for (int e = 0; e < NRW; ++e) {
-#pragma unroll
-        for (int m = 16; m > 0; m >>= 1) lsum[e] += __shfl_xor_sync(0xffffffffu, lsum[e], m);
-        if (lane == 0) {
-          l_sh[part & 1][warp & 3][r0 + e] = lsum[e];
+      for (int e = 0; e < NRW; ++e)
+        if (lane == e) {
           ref_sh[part & 1][0][r0 + e] = tt[e];
           ref_sh[part & 1][1][r0 + e] = mm[e];
         }
-      }
       // the part's coefficients and ends have been read
       if (lane == 0) mbar_arrive(&q_empty[part & 1]);
       done.part = part;
