@@ -33,7 +33,9 @@
 //  * A segment is up to 16 query rows of a key/value head with all keys of a sequence.  The
 //    tiles of all segments stand in one line, dealt out evenly to the CTAs (two to an SM); segments
 //    that cross shares are joined by a second, dependent kernel from float32 partial results
-//    (at most two per CTA).
+//    (at most two per CTA).  With few segments a cluster of up to eight CTAs takes each instead and
+//    joins its partial results through distributed shared memory: one launch, no scratch, no prefix
+//    sums (one request of 1500 tokens, 8 heads: 10.4 us by shares, 8.0 so).
 #include <cmath>
 
 #include "common.h"
@@ -101,6 +103,8 @@ struct KParams {
   int* status;
   int B, H, H_kv, n_q, rows, qtiles, segs, seg_rows;
   int num_pages, page_size, page_shift, max_pages, causal;
+  int cluster;            // CTAs of a segment's cluster, or 0: shares of the line
+  int solo;               // shares of whole segments only
   float scale_log2;
 };
 
@@ -206,13 +210,14 @@ struct Cursor {
   int len;
   int at;                // first unit in the segment
   int extra;
+  int solo;              // a segment is all of the share's in which it begins
   long long left;        // units of the share from here on
   __device__ __forceinline__ int tiles() const { return tiles_of<TILE>(len); }
   __device__ __forceinline__ int units() const {
     const int rest = tiles() + extra - at;
     return left < rest ? static_cast<int>(left) : rest;
   }
-  __device__ __forceinline__ int tile_at(int u) const { return u == 0 ? 0 : max(1, u - extra); }
+  __device__ __forceinline__ int tile_at(int u) const { return u == 0 ? 0 : solo ? tiles() : max(1, u - extra); }
   __device__ __forceinline__ int first() const { return tile_at(at); }           // tile
   __device__ __forceinline__ int part() const { return tile_at(at + units()) - first(); }   // tiles
   __device__ __forceinline__ void next_part(const KParams& p) {
@@ -267,6 +272,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   __shared__ unsigned vend_sh[2][NR];                    // ends of the visible tokens,
   __shared__ float ref_sh[2][2][NR], l_sh[2][4][NR];     // references at its end, and sums by key quarter
   __shared__ float red_sh[2][2][4][NR];                  // maxima of a tile (by parity) by key quarter
+  __shared__ float part_lse[NR];                         // of the partial results of a cluster's CTA
   __shared__ float xch_sh[KP == 2 ? NR : 1][KP == 2 ? 64 : 1];
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -303,62 +309,74 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   wait_for_previous_kernel();
   release_dependents();
 
-  // ---- units of one segment of the entries before each; this CTA's share
-  const int per = (p.B + C::THREADS - 1) / C::THREADS;
-  const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
-  long long sum = 0;
-  int len = 0, some = 0;                    // some: entries with tokens
-  for (int b = b0; b < b1; ++b) {
-    len = tokens_of(p, b);
-    if (len == 0 && blockIdx.x == 0 && __ldcg(p.seq_lens + b) != 0) atomicCAS(p.status, 0, kDevBadSeqlens);
-    sum += tiles_of<TILE>(len);
-    some += len > 0;
-  }
-  long long scan = sum;
-  int scan_some = some;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, scan, o);
-    const int z = __shfl_up_sync(0xffffffffu, scan_some, o);
-    if (lane >= o) {
-      scan += x;
-      scan_some += z;
+  long long T = 0, g0 = 0, total = 0;       // units of all, first of this CTA and its number
+  int extra = 0;
+  const int ranks = p.cluster > 0 ? p.cluster : 1, seg = static_cast<int>(blockIdx.x) / ranks;
+  const int rank = static_cast<int>(blockIdx.x) - seg * ranks;
+  if (p.cluster > 0) {
+    if (threadIdx.x == 0) {
+      const int b = seg / p.segs, len = tokens_of(p, b);
+      if (len == 0 && seg % p.segs == 0 && rank == 0 && __ldcg(p.seq_lens + b) != 0) atomicCAS(p.status, 0, kDevBadSeqlens);
+      start_sh[2] = len;
     }
-  }
-  if (lane == 31) {
-    warp_sum[0][warp] = scan;
-    warp_sum[1][warp] = scan_some;
-  }
-  __syncthreads();
-  long long base = scan - sum, all = 0, base_some = scan_some - some, all_some = 0;
-  for (int w = 0; w < C::THREADS / 32; ++w) {
-    if (w < warp) {
-      base += warp_sum[0][w];
-      base_some += warp_sum[1][w];
-    }
-    all += warp_sum[0][w];
-    all_some += warp_sum[1][w];
-  }
-  // A part's start and end take some two tiles' time (64 sequences of up to 16384, d = 64: without
-  // them counted the CTA with the shortest ones ended 10 us after the others).  A share of 8 tiles
-  // and more cannot lie within them.
-  const int extra = all * p.segs >= 8ll * gridDim.x ? 2 : 0;
-  base += extra * base_some;
-  sum += extra * some;
-  const long long T = (all + extra * all_some) * p.segs;
-  const long long g0 = share_start(blockIdx.x, gridDim.x, T);
-  const long long total = share_start(blockIdx.x + 1ll, gridDim.x, T) - g0;
-  if (total > 0 && base * p.segs <= g0 && g0 < (base + sum) * p.segs) {
-    int b = b0;
-    for (; b1 - b0 > 1; ++b) {
+  } else {
+    // ---- units of one segment of the entries before each; this CTA's share
+    const int per = (p.B + C::THREADS - 1) / C::THREADS;
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
+    long long sum = 0;
+    int len = 0, some = 0;                    // some: entries with tokens
+    for (int b = b0; b < b1; ++b) {
       len = tokens_of(p, b);
-      const int n = len > 0 ? tiles_of<TILE>(len) + extra : 0;
-      if (g0 < (base + n) * p.segs) break;
-      base += n;
+      if (len == 0 && blockIdx.x == 0 && __ldcg(p.seq_lens + b) != 0) atomicCAS(p.status, 0, kDevBadSeqlens);
+      sum += tiles_of<TILE>(len);
+      some += len > 0;
     }
-    start_sh[0] = b;
-    start_sh[1] = g0 - base * p.segs;
-    start_sh[2] = len;
+    long long scan = sum;
+    int scan_some = some;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, scan, o);
+      const int z = __shfl_up_sync(0xffffffffu, scan_some, o);
+      if (lane >= o) {
+        scan += x;
+        scan_some += z;
+      }
+    }
+    if (lane == 31) {
+      warp_sum[0][warp] = scan;
+      warp_sum[1][warp] = scan_some;
+    }
+    __syncthreads();
+    long long base = scan - sum, all = 0, base_some = scan_some - some, all_some = 0;
+    for (int w = 0; w < C::THREADS / 32; ++w) {
+      if (w < warp) {
+        base += warp_sum[0][w];
+        base_some += warp_sum[1][w];
+      }
+      all += warp_sum[0][w];
+      all_some += warp_sum[1][w];
+    }
+    // A part's start and end take some two tiles' time (64 sequences of up to 16384, d = 64: without
+    // them counted the CTA with the shortest ones ended 10 us after the others).  A share of 8 tiles
+    // and more cannot lie within them.
+    extra = all * p.segs >= 8ll * gridDim.x ? 2 : 0;
+    base += extra * base_some;
+    sum += extra * some;
+    T = (all + extra * all_some) * p.segs;
+    g0 = share_start(blockIdx.x, gridDim.x, T);
+    total = share_start(blockIdx.x + 1ll, gridDim.x, T) - g0;
+    if (total > 0 && base * p.segs <= g0 && g0 < (base + sum) * p.segs) {
+      int b = b0;
+      for (; b1 - b0 > 1; ++b) {
+        len = tokens_of(p, b);
+        const int n = len > 0 ? tiles_of<TILE>(len) + extra : 0;
+        if (g0 < (base + n) * p.segs) break;
+        base += n;
+      }
+      start_sh[0] = b;
+      start_sh[1] = g0 - base * p.segs;
+      start_sh[2] = len;
+    }
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -366,15 +384,24 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   const uint32_t tmem = tmem_base_sh;
   const Abort ab{&abort_sh, p.status};
 
-  Cursor<TILE> cur{0, 0, 0, 0, extra, total};
-  if (total > 0) {
+  Cursor<TILE> cur{0, 0, 0, 0, extra, p.solo, 0};
+  if (p.cluster > 0) {
+    cur.b = seg / p.segs;
+    cur.y = seg - cur.b * p.segs;
+    cur.len = static_cast<int>(start_sh[2]);
+    const long long n = cur.tiles();
+    cur.at = static_cast<int>(rank * n / ranks);
+    cur.left = (rank + 1) * n / ranks - cur.at;
+  } else if (total > 0) {
+    cur.left = total;
     cur.b = static_cast<int>(start_sh[0]);
     cur.len = static_cast<int>(start_sh[2]);
     const int n = cur.tiles() + extra;
     cur.y = static_cast<int>(start_sh[1] / n);
     cur.at = static_cast<int>(start_sh[1] - static_cast<long long>(cur.y) * n);
-    if (cur.part() == 0) cur.next_part(p);            // a single tile, of the CTA before
+    if (cur.part() == 0) cur.next_part(p);            // its tiles are the CTA's before
   }
+  const Cursor<TILE> begin = cur;
 
   if (warp == C::LOAD) {
     // ------------------------------------------------------------ producer
@@ -616,7 +643,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[buf]);
-      if (cur.first() == 0 && cur.part() < cur.tiles()) {
+      if (p.cluster == 0 && cur.first() == 0 && cur.part() < cur.tiles()) {
         // CTA whose share holds the segment's last unit: the last c with c T / n <= it
         const long long n = T < gridDim.x ? T : gridDim.x, last = g0 + (total - cur.left) - cur.at + cur.tiles() + extra - 1;
         crossing = make_int4(static_cast<int>(at0), rows_here, static_cast<int>(((last + 1) * n - 1) / T),
@@ -624,9 +651,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       }
       cur.next_part(p);
     }
-    if (lane == 0) p.crossing[blockIdx.x] = crossing;
-    // batch entries without tokens: O = 0, LSE = -inf
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (lane == 0 && p.cluster == 0) p.crossing[blockIdx.x] = crossing;
+    // batch entries without tokens: O = 0, LSE = -inf (a cluster's joining finds them)
+    for (int b = blockIdx.x; p.cluster == 0 && b < p.B; b += gridDim.x) {
       if (tokens_of(p, b) != 0) continue;
       const size_t rows_b = static_cast<size_t>(p.H) * p.n_q;
       uint4* dst = reinterpret_cast<uint4*>(p.o + b * rows_b * D);
@@ -685,8 +712,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         // (a NaN among the scores or descales is in o by now, and stays)
         const float f = l == 0.f ? 0.f : ex2_approx(mm - tt) / l;
         const float lse = l == 0.f ? -INFINITY : (lg2(l) - mm) * 0.69314718055994530942f;
-        const size_t at = done.whole ? done.at0 : (2ull * blockIdx.x + (done.part > 0 ? 1 : 0)) * p.seg_rows;
-        if ((warp & 3) == 0 && lane < NRW && mine < done.rows) (done.whole ? p.lse : p.lse_part)[at + mine] = lse;
+        // (a cluster's partial results: in its ring's place, which is free by then)
+        const size_t at = done.whole ? done.at0 : p.cluster > 0 ? 0 : (2ull * blockIdx.x + (done.part > 0 ? 1 : 0)) * p.seg_rows;
+        float* const o_part = p.cluster > 0 ? reinterpret_cast<float*>(sKV) : p.o_part;
+        if ((warp & 3) == 0 && lane < NRW && mine < done.rows)
+          (done.whole ? p.lse : p.cluster > 0 ? part_lse : p.lse_part)[at + mine] = lse;
 #pragma unroll
         for (int i = 0; i < NRW; ++i) {
           const int r = r0 + i;
@@ -698,7 +728,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
             const uint32_t pk = FP16 ? cvt_pack_f16(val, 0.f) : cvt_pack_bf16(val, 0.f);
             p.o[(at + r) * D + t] = static_cast<uint16_t>(pk);
           } else {
-            p.o_part[(at + r) * D + t] = val;
+            o_part[(at + r) * D + t] = val;
           }
         }
       }
@@ -928,7 +958,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       if (lane == 0) mbar_arrive(&q_empty[part & 1]);
       done.part = part;
       done.rows = min(NR, p.rows - row0);
-      done.whole = take == cur.tiles();
+      done.whole = p.cluster == 0 && take == cur.tiles();
       done.at0 = (static_cast<size_t>(cur.b) * p.H_kv + hk) * p.rows + row0;
       cur.next_part(p);
     }
@@ -955,6 +985,40 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   if (warp == C::MMA_S) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, C::TMEM);
+  }
+  if (p.cluster > 0) {
+    // Every thread of every CTA comes here, after an abort too.  The cluster's threads share the
+    // segment's rows, four columns each.
+    if (begin.left <= 0 && threadIdx.x < NR) part_lse[threadIdx.x] = -INFINITY;
+    cluster_sync();
+    const int hk = begin.y / p.qtiles, row0 = (begin.y - hk * p.qtiles) * 16;
+    const size_t at0 = (static_cast<size_t>(begin.b) * p.H_kv + hk) * p.rows + row0;
+    const int items = min(NR, p.rows - row0) * (D / 4);
+    for (int x = rank * C::THREADS + static_cast<int>(threadIdx.x); x < items; x += ranks * C::THREADS) {
+      const int r = x / (D / 4), c4 = x % (D / 4);
+      float lse[8], m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lse[i] = i < ranks ? ld_cluster_f32(smem_u32(part_lse + r), i) : -INFINITY;
+        m = fmaxf(m, lse[i]);
+      }
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (lse[i] == -INFINITY) continue;           // no keys: nothing was written there
+        const float w = expf(lse[i] - m);
+        const float4 o = ld_cluster_v4(smem_u32(reinterpret_cast<float*>(sKV) + r * D + 4 * c4), i);
+        sum += w;
+        acc = make_float4(fmaf(w, o.x, acc.x), fmaf(w, o.y, acc.y), fmaf(w, o.z, acc.z), fmaf(w, o.w, acc.w));
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const uint2 pk = FP16 ? make_uint2(cvt_pack_f16(acc.x * inv, acc.y * inv), cvt_pack_f16(acc.z * inv, acc.w * inv))
+                            : make_uint2(cvt_pack_bf16(acc.x * inv, acc.y * inv), cvt_pack_bf16(acc.z * inv, acc.w * inv));
+      *reinterpret_cast<uint2*>(p.o + (at0 + r) * D + 4 * c4) = pk;
+      if (c4 == 0) p.lse[at0 + r] = sum == 0.f ? -INFINITY : m + logf(sum);
+    }
+    cluster_sync();                                  // the others may still be reading here
   }
 }
 
@@ -1007,10 +1071,33 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_merge_kernel(const K
   if (col == 0) p.lse[at] = sum == 0.f ? -INFINITY : m + logf(sum);
 }
 
+// CTAs of the cluster that takes a segment, or 0: all segments' tiles dealt out in one line.  The
+// smaller modelled time, in microseconds: a start, the tiles of one CTA, and the joining (the line's
+// second kernel); clusters only as far as all of them run at a time (with one CTA to an SM and
+// with two: a multiprocessor group's SMs are not a multiple of every size).
+inline int cluster_of(int B, int segs, int tiles, int per_sm) {
+  constexpr int at_a_time[2][9] = {{0, 152, 76, 46, 36, 28, 23, 15, 15}, {0, 304, 152, 97, 74, 58, 46, 38, 36}};
+  const double n = static_cast<double>(B) * segs, line = 3.0 + 0.6 * std::ceil(n * tiles / (152.0 * per_sm));
+  int best = 0;
+  double least = line;
+  for (int c = 1; c <= 8; ++c) {
+    if (n > at_a_time[per_sm - 1][c]) break;
+    const double t = 0.7 + 0.6 * ((tiles + c - 1) / c);
+    if (t < least) {
+      least = t;
+      best = c;
+    }
+  }
+  return best;
+}
+
 template <int D, int NR, int TQ, int TP, bool FP16, bool SIGNS>
-attn_status_t launch_t(const Fp4DecodeParams& a, const KParams& p, int ctas, cudaStream_t stream) {
+attn_status_t launch_t(const Fp4DecodeParams& a, KParams p, int ctas, cudaStream_t stream) {
   using C = Cfg<D, NR, TQ, TP>;
-  if (ctas > 152 * C::CTAS) ctas = 152 * C::CTAS;
+  p.cluster = cluster_of(p.B, p.segs, (a.max_seqlen - 1) / C::TILE + 1, C::CTAS);
+  p.solo = a.max_seqlen <= C::TILE ? 1 : 0;
+  if (p.cluster > 0) ctas = p.B * p.segs * p.cluster;
+  else if (ctas > 152 * C::CTAS) ctas = 152 * C::CTAS;
   auto kern = decode_fp4_kernel<D, NR, TQ, TP, FP16, SIGNS>;
   attn_status_t s = set_smem(reinterpret_cast<const void*>(kern), C::SMEM);
   if (s != ATTN_OK) return s;
@@ -1022,9 +1109,9 @@ attn_status_t launch_t(const Fp4DecodeParams& a, const KParams& p, int ctas, cud
     return s;
   if ((s = make_tmap_fp4(&tv, a.v_cache, p.page_size / C::KP, p.H_kv, p.num_pages, 64, head_b, head_b * p.H_kv, box)) != ATTN_OK)
     return s;
-  cudaError_t e = launch_dependent(kern, dim3(ctas), C::THREADS, C::SMEM, stream, 0, tk, tv, p);
+  cudaError_t e = launch_dependent(kern, dim3(ctas), C::THREADS, C::SMEM, stream, p.cluster, tk, tv, p);
   if (e != cudaSuccess) return fail_cuda(e, "4-bit decode kernel launch");
-  if (ctas == 1) return ATTN_OK;
+  if (ctas == 1 || p.cluster > 0 || p.solo) return ATTN_OK;            // no segment crosses shares
   constexpr int rows = kMergeThreads / (D / 4);
   e = launch_dependent(decode_fp4_merge_kernel<D, FP16>, dim3(ctas, (p.seg_rows + rows - 1) / rows), kMergeThreads, 0, stream,
                        0, p);
@@ -1059,7 +1146,7 @@ attn_status_t launch_decode_fp4(const Fp4DecodeParams& p, cudaStream_t stream) {
                    p.block_table, p.seq_lens, static_cast<uint16_t*>(p.o), p.lse, reinterpret_cast<float*>(ws),
                    reinterpret_cast<float*>(lse_part), reinterpret_cast<int4*>(crossing), status, p.B, p.H, p.H_kv, p.n_q,
                    rows, plan.qtiles, p.H_kv * plan.qtiles, plan.seg_rows, p.num_pages, p.page_size,
-                   page_shift_of(p.page_size), p.max_pages, p.causal, p.scale * 1.4426950408889634f};
+                   page_shift_of(p.page_size), p.max_pages, p.causal, 0, 0, p.scale * 1.4426950408889634f};
   return p.d == 64 ? launch_d<64>(p, kp, plan.ctas, stream) : launch_d<128>(p, kp, plan.ctas, stream);
 }
 
