@@ -45,7 +45,7 @@
 namespace attn {
 namespace {
 
-constexpr int kSmemPerSm = 232448;
+constexpr int kSmemLimit = 232448;      // of one CTA; with two to an SM each has half of 1024 more, less 1024
 constexpr float kFar = 3e38f;
 constexpr float kPShift = 5.f;          // P' is 2^5 at the reference, 2^8 at most (e4m3: 448)
 constexpr int kPStep = 5;               // a term's steps are 2^-5 of those of the one before
@@ -75,7 +75,8 @@ struct Cfg {
   static constexpr int Q_STEP = KP == 2 ? 64 : NS * 128;
   static constexpr int PB = NR == 4 && KP == 1 ? 3 : 2;  // buffers of P'
   static constexpr int FIXED = 1024 + Q_BYTES + PB * P_TILE;
-  static constexpr int PER_CTA = kSmemPerSm / CTAS - 3072;   // (static shared memory and what the system takes)
+  static constexpr int STATIC = 1024 + NR * 140 + (KP == 2 ? NR * 256 : 0);   // at most
+  static constexpr int PER_CTA = (CTAS == 1 ? kSmemLimit : (kSmemLimit + 1024) / 2 - 1024) - STATIC;
   static constexpr int FIT = (PER_CTA - FIXED) / (SLOT + 2 * TILE) / 2 * 2;
   static constexpr int NSLOT = FIT > 12 ? 12 : FIT;      // even: keys in even slots, values in odd ones
   static constexpr uint32_t S_COLS = KP * NS;            // of one score buffer

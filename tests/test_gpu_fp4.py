@@ -265,6 +265,16 @@ def test_decode_heads_and_query_tokens(attn, H, H_kv, n_q, signs, d):
     _decode_case(attn, [300, 1025, 64, 0, 3], 32, H, H_kv, n_q, d, True, torch.float16, signs)
 
 
+@pytest.mark.parametrize("G", [1, 5, 8, 11, 16, 40])
+@pytest.mark.parametrize("signs", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_every_kernel_in_bfloat16(attn, G, signs, d):
+    """4, 8 and 16 rows, by clusters and (many sequences) by shares that segments cross."""
+    _decode_case(attn, [700, 0, 129], 64, 2 * G, 2, 1, d, True, torch.bfloat16, signs)
+    lens = np.random.default_rng(G).integers(0, 900, 90).tolist()
+    _decode_case(attn, lens, 16, 4 * G, 4, 1, d, False, torch.bfloat16, signs)
+
+
 @pytest.mark.parametrize("signs", [False, True])
 def test_decode_long_sequences_are_shared(attn, signs):
     _decode_case(attn, [9000, 20000, 1], 64, 8, 2, 1, 128, True, torch.bfloat16, signs)
