@@ -67,6 +67,7 @@ struct Cfg {
   static constexpr int CW = NR == 16 ? 2 : 1;            // softmax warps per quarter of the keys
   static constexpr int SW = 4 * CW;
   static constexpr int NRW = NR / CW;                    // query rows of a softmax thread
+  static constexpr int PART = NR == 4 ? 3 : NR == 8 ? 4 : 6;   // tiles that take the time of a part's start and end
   static constexpr int LOAD = SW, MMA_S = SW + 1, MMA_PV = SW + 2, QUERY = SW + 3;
   static constexpr int THREADS = (SW + 4) * 32;
   static constexpr int CTAS = NR == 16 ? 1 : 2;          // of an SM (16 rows: registers)
@@ -196,11 +197,26 @@ __device__ __forceinline__ int tokens_of(const KParams& p, int b) {
 template <int TILE>
 __device__ __forceinline__ int tiles_of(int len) { return static_cast<int>((static_cast<unsigned>(len) + TILE - 1) / TILE); }
 
-// First unit of CTA c's share of T units (at most T CTAs get one).
-__device__ __forceinline__ long long share_start(long long c, int C, long long T) {
-  const long long n = T < C ? T : C;
-  return c >= n ? T : c * T / n;
-}
+// T units dealt out to the first n of C CTAs (n = min(T, C)), one more to the first `rest` of them.
+struct Shares {
+  long long per, rest, T;
+  __device__ __forceinline__ Shares(long long T_, int C) : T(T_) {
+    const int n = T < C ? static_cast<int>(T) : C;
+    // (a division of 64 bits takes some hundred instructions)
+    per = n == 0 ? 0 : T < 0x80000000ll ? static_cast<unsigned>(T) / static_cast<unsigned>(n) : T / n;
+    rest = T - per * n;
+  }
+  // first unit of CTA c's (T behind the last that gets one)
+  __device__ __forceinline__ long long start(long long c) const {
+    const long long u = c * per + (c < rest ? c : rest);
+    return u < T ? u : T;
+  }
+  // the CTA that has unit u
+  __device__ __forceinline__ int owner(long long u) const {
+    const long long more = rest * (per + 1);
+    return static_cast<int>(u < more ? u / (per + 1) : rest + (u - more) / per);
+  }
+};
 
 // A walk over the parts of segments in a share.  A segment is `extra` units for its start and its
 // end, then one for each tile but that the first comes with the start: a share that begins in
@@ -357,15 +373,15 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       all += warp_sum[0][w];
       all_some += warp_sum[1][w];
     }
-    // A part's start and end take some two tiles' time (64 sequences of up to 16384, d = 64: without
-    // them counted the CTA with the shortest ones ended 10 us after the others).  A share of 8 tiles
-    // and more cannot lie within them.
-    extra = all * p.segs >= 8ll * gridDim.x ? 2 : 0;
+    // A part's start and end are counted as tiles (64 sequences of up to 16384, d = 64: without them the
+    // CTA with the shortest ones ended 10 us after the others), as far as a share has four times as many.
+    extra = static_cast<int>(min(static_cast<long long>(C::PART), all * p.segs / (4ll * gridDim.x)));
     base += extra * base_some;
     sum += extra * some;
     T = (all + extra * all_some) * p.segs;
-    g0 = share_start(blockIdx.x, gridDim.x, T);
-    total = share_start(blockIdx.x + 1ll, gridDim.x, T) - g0;
+    const Shares shares(T, gridDim.x);
+    g0 = shares.start(blockIdx.x);
+    total = shares.start(blockIdx.x + 1ll) - g0;
     if (total > 0 && base * p.segs <= g0 && g0 < (base + sum) * p.segs) {
       int b = b0;
       for (; b1 - b0 > 1; ++b) {
@@ -622,10 +638,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
             w[i] = a | (b << 16);
             if (k + 1 < TQ) {
               const float2 fa = __half22float2(as_half2(e4m3_halves(a))), fb = __half22float2(as_half2(e4m3_halves(b)));
-              x[4 * i] = (x[4 * i] - fa.x) * (1 << kPStep);
-              x[4 * i + 1] = (x[4 * i + 1] - fa.y) * (1 << kPStep);
-              x[4 * i + 2] = (x[4 * i + 2] - fb.x) * (1 << kPStep);
-              x[4 * i + 3] = (x[4 * i + 3] - fb.y) * (1 << kPStep);
+              const uint64_t up = pack2(1 << kPStep, 1 << kPStep), down = pack2(-(1 << kPStep), -(1 << kPStep));
+              const uint64_t ra = ffma2(pack2(x[4 * i], x[4 * i + 1]), up, fmul2(pack2(fa.x, fa.y), down));
+              const uint64_t rb = ffma2(pack2(x[4 * i + 2], x[4 * i + 3]), up, fmul2(pack2(fb.x, fb.y), down));
+              x[4 * i] = lo2(ra), x[4 * i + 1] = hi2(ra), x[4 * i + 2] = lo2(rb), x[4 * i + 3] = hi2(rb);
             }
           }
           const int col = k * NR + r;
@@ -645,9 +661,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[buf]);
       if (p.cluster == 0 && cur.first() == 0 && cur.part() < cur.tiles()) {
-        // CTA whose share holds the segment's last unit: the last c with c T / n <= it
-        const long long n = T < gridDim.x ? T : gridDim.x, last = g0 + (total - cur.left) - cur.at + cur.tiles() + extra - 1;
-        crossing = make_int4(static_cast<int>(at0), rows_here, static_cast<int>(((last + 1) * n - 1) / T),
+        // the CTA whose share holds the segment's last unit
+        const long long last = g0 + (total - cur.left) - cur.at + cur.tiles() + extra - 1;
+        crossing = make_int4(static_cast<int>(at0), rows_here, Shares(T, gridDim.x).owner(last),
                              static_cast<int>(2 * blockIdx.x + (part > 0 ? 1 : 0)));
       }
       cur.next_part(p);
