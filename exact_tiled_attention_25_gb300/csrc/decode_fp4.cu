@@ -21,12 +21,12 @@
 //    would round) and three for a float16 one.
 //  * A thread holds the scores of one key (d = 64: two) for every query row: with 4 rows and
 //    128 keys that are 4 exponentials' pairs a thread, and no lane idles.
-//  * The value descale enters the exponent, as in the e4m3 decode: P' = 2^(s + log2 s^v - T + 5),
-//    T a running reference of that sum, so it is the tokens that count for the result whose
-//    probabilities have all their bits, however the descales differ.  What is 2^-11 of the largest
-//    or less loses bits (an error of 2^-20 of that one; three terms: 2^-14 and 2^-25).  The row
-//    sums are float32 sums of 2^(s - M) with a reference of their own, since s^v may be 0.  References move only when
-//    a value exceeds T by 3 or M by 64, by a vote of the softmax warps once a tile.
+//  * p = 2^(s - M), M a running reference of the scores; the row sums add p in float32, and what meets the
+//    codes is P' = p s^v c with c = 2^(M - T + 5), T a running reference of s + log2 s^v: it is
+//    the tokens that count for the result whose probabilities have all their bits, however the
+//    descales differ.  What is 2^-11 of the largest or less loses bits (an error of 2^-20 of that
+//    one; three terms: 2^-14 and 2^-25).  The references move only when a score exceeds M by 64 or P'
+//    would exceed 2^8, by a vote of the softmax warps once a tile.
 //  * d = 64: rows of two neighbouring tokens are one row of the tile.  Their scores are two
 //    products over half the columns each; in O^T the first 64 lanes take the even tokens' columns
 //    and the others the odd ones', and the two halves are added at the end.
@@ -46,8 +46,10 @@ namespace attn {
 namespace {
 
 constexpr int kSmemLimit = 232448;      // of one CTA; with two to an SM each has half of 1024 more, less 1024
-constexpr float kFar = 3e38f;
-constexpr float kPShift = 5.f;          // P' is 2^5 at the reference, 2^8 at most (e4m3: 448)
+constexpr float kFar = 3e38f;           // -M before the first token
+constexpr float kPTop = 256.f;          // P' at most (e4m3: 448); 2^5 at its reference
+constexpr float kPShift = 5.f;
+constexpr float kMostC = 120.f;         // log2 of c at most: values of 2^-115 of the largest scores' and less count as that
 constexpr int kPStep = 5;               // a term's steps are 2^-5 of those of the one before
 
 constexpr int pad16(int n) { return (n + 15) / 16 * 16; }
@@ -68,8 +70,9 @@ struct Cfg {
   static constexpr int SW = 4 * CW;
   static constexpr int NRW = NR / CW;                    // query rows of a softmax thread
   static constexpr int PART = NR == 4 ? 3 : NR == 8 ? 4 : 6;   // tiles that take the time of a part's start and end
+  static constexpr int QW = NR == 16 ? NR * D / 512 : 1; // query warps: of 16 rows one for each 512 values
   static constexpr int LOAD = SW, MMA_S = SW + 1, MMA_PV = SW + 2, QUERY = SW + 3;
-  static constexpr int THREADS = (SW + 4) * 32;
+  static constexpr int THREADS = (SW + 3 + QW) * 32;
   static constexpr int CTAS = NR == 16 ? 1 : 2;          // of an SM (16 rows: registers)
   // The two query tiles (NS rows of D bytes); of d = 64 they are the halves of one of 128 bytes a row.
   static constexpr int Q_BYTES = 2 * NS * D, P_TILE = NPV * 128;
@@ -197,13 +200,17 @@ __device__ __forceinline__ int tokens_of(const KParams& p, int b) {
 template <int TILE>
 __device__ __forceinline__ int tiles_of(int len) { return static_cast<int>((static_cast<unsigned>(len) + TILE - 1) / TILE); }
 
+// a / b for a >= 0; mostly of 32 bits (one of 64 takes some hundred instructions).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : static_cast<unsigned>(a) / static_cast<unsigned>(b);
+}
+
 // T units dealt out to the first n of C CTAs (n = min(T, C)), one more to the first `rest` of them.
 struct Shares {
   long long per, rest, T;
   __device__ __forceinline__ Shares(long long T_, int C) : T(T_) {
     const int n = T < C ? static_cast<int>(T) : C;
-    // (a division of 64 bits takes some hundred instructions)
-    per = n == 0 ? 0 : T < 0x80000000ll ? static_cast<unsigned>(T) / static_cast<unsigned>(n) : T / n;
+    per = n == 0 ? 0 : quotient(T, n);
     rest = T - per * n;
   }
   // first unit of CTA c's (T behind the last that gets one)
@@ -214,7 +221,7 @@ struct Shares {
   // the CTA that has unit u
   __device__ __forceinline__ int owner(long long u) const {
     const long long more = rest * (per + 1);
-    return static_cast<int>(u < more ? u / (per + 1) : rest + (u - more) / per);
+    return static_cast<int>(u < more ? quotient(u, per + 1) : rest + quotient(u - more, per));
   }
 };
 
@@ -283,7 +290,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       o_full[2], o_empty[2], drain_bar[2];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, issued_sh[2];                 // key and value tiles whose copies have been issued
-  __shared__ long long warp_sum[2][C::THREADS / 32], start_sh[3];
+  __shared__ long long warp_sum[2][C::THREADS / 32];
+  __shared__ int start_sh[4];                            // where the share begins
   __shared__ unsigned there_sh[NSLOT / 2];               // boxes of a key tile that were copied
   __shared__ __align__(16) float cq_sh[2][NR];           // of a part's query rows: score coefficients,
   __shared__ unsigned vend_sh[2][NR];                    // ends of the visible tokens,
@@ -295,7 +303,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 1);
+      mbar_init(&q_full[i], C::QW);
       mbar_init(&q_empty[i], 1 + C::SW);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_empty[i], C::SW);
@@ -375,7 +383,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     }
     // A part's start and end are counted as tiles (64 sequences of up to 16384, d = 64: without them the
     // CTA with the shortest ones ended 10 us after the others), as far as a share has four times as many.
-    extra = static_cast<int>(min(static_cast<long long>(C::PART), all * p.segs / (4ll * gridDim.x)));
+    extra = static_cast<int>(fminf(C::PART, __fdividef(static_cast<float>(all * p.segs), 4.f * gridDim.x)));
     base += extra * base_some;
     sum += extra * some;
     T = (all + extra * all_some) * p.segs;
@@ -390,9 +398,13 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         if (g0 < (base + n) * p.segs) break;
         base += n;
       }
+      const int n = tiles_of<TILE>(len) + extra;
+      const long long in = g0 - base * p.segs;
+      const int y = static_cast<int>(quotient(in, n));
       start_sh[0] = b;
-      start_sh[1] = g0 - base * p.segs;
+      start_sh[1] = y;
       start_sh[2] = len;
+      start_sh[3] = static_cast<int>(in - static_cast<long long>(y) * n);
     }
   }
   tc_fence_before_sync();
@@ -405,17 +417,16 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   if (p.cluster > 0) {
     cur.b = seg / p.segs;
     cur.y = seg - cur.b * p.segs;
-    cur.len = static_cast<int>(start_sh[2]);
-    const long long n = cur.tiles();
-    cur.at = static_cast<int>(rank * n / ranks);
+    cur.len = start_sh[2];
+    const unsigned n = cur.tiles();
+    cur.at = rank * n / ranks;
     cur.left = (rank + 1) * n / ranks - cur.at;
   } else if (total > 0) {
     cur.left = total;
-    cur.b = static_cast<int>(start_sh[0]);
-    cur.len = static_cast<int>(start_sh[2]);
-    const int n = cur.tiles() + extra;
-    cur.y = static_cast<int>(start_sh[1] / n);
-    cur.at = static_cast<int>(start_sh[1] - static_cast<long long>(cur.y) * n);
+    cur.b = start_sh[0];
+    cur.y = start_sh[1];
+    cur.len = start_sh[2];
+    cur.at = start_sh[3];
     if (cur.part() == 0) cur.next_part(p);            // its tiles are the CTA's before
   }
   const Cursor<TILE> begin = cur;
@@ -555,11 +566,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         cur.next_part(p);
       }
     }
-  } else if (warp == C::QUERY) {
+  } else if (warp >= C::QUERY) {
     // ------------------------------------------------------------ query rows as e4m3 terms
     // d / 16 lanes hold a row, 16 neighbouring columns each.
-    constexpr int L = D / 16, PER = 32 / L;
-    const int u = lane % L;
+    constexpr int L = D / 16, PER = 32 / L, PASSES = (NR + PER - 1) / PER / C::QW;
+    const int u = lane % L, first_row = (warp - C::QUERY) * PASSES * PER;
     bool ok = true;
     int4 crossing = make_int4(0, 0, 0, -1);            // a segment that this share begins and does not end
     for (int part = 0; ok && cur.left > 0; ++part) {
@@ -571,17 +582,17 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       const int hk = cur.y / p.qtiles, row0 = (cur.y - hk * p.qtiles) * 16;
       const size_t at0 = (static_cast<size_t>(cur.b) * p.H_kv + hk) * p.rows + row0;
       const int rows_here = min(NR, p.rows - row0);
-      uint4 raw[(NR + PER - 1) / PER][2];
+      uint4 raw[PASSES][2];
 #pragma unroll
-      for (int x = 0; x < (NR + PER - 1) / PER; ++x) {
-        const int r = x * PER + lane / L;
+      for (int x = 0; x < PASSES; ++x) {
+        const int r = first_row + x * PER + lane / L;
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (at0 + (r < rows_here ? r : 0)) * D + 16 * u);
         raw[x][0] = __ldcg(src);
         raw[x][1] = __ldcg(src + 1);
       }
 #pragma unroll
-      for (int pass = 0; pass < (NR + PER - 1) / PER; ++pass) {
-        const int r = pass * PER + lane / L;
+      for (int pass = 0; pass < PASSES; ++pass) {
+        const int r = first_row + pass * PER + lane / L;
         const bool live = r < rows_here;
         float x[16];
         {
@@ -668,9 +679,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       }
       cur.next_part(p);
     }
-    if (lane == 0 && p.cluster == 0) p.crossing[blockIdx.x] = crossing;
+    if (lane == 0 && warp == C::QUERY && p.cluster == 0) p.crossing[blockIdx.x] = crossing;
     // batch entries without tokens: O = 0, LSE = -inf (a cluster's joining finds them)
-    for (int b = blockIdx.x; p.cluster == 0 && b < p.B; b += gridDim.x) {
+    for (int b = blockIdx.x; p.cluster == 0 && warp == C::QUERY && b < p.B; b += gridDim.x) {
       if (tokens_of(p, b) != 0) continue;
       const size_t rows_b = static_cast<size_t>(p.H) * p.n_q;
       uint4* dst = reinterpret_cast<uint4*>(p.o + b * rows_b * D);
@@ -725,9 +736,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         // lane i: factor and log-sum-exp of row i
         const int mine = r0 + (lane & (NRW - 1));
         const float l = ((l_sh[buf][0][mine] + l_sh[buf][1][mine]) + l_sh[buf][2][mine]) + l_sh[buf][3][mine];
-        const float tt = ref_sh[buf][0][mine], mm = ref_sh[buf][1][mine];
+        const float c = ref_sh[buf][0][mine], mm = ref_sh[buf][1][mine];
         // (a NaN among the scores or descales is in o by now, and stays)
-        const float f = l == 0.f ? 0.f : ex2_approx(mm - tt) / l;
+        const float f = l == 0.f ? 0.f : 1.f / c / l;
         const float lse = l == 0.f ? -INFINITY : (lg2(l) - mm) * 0.69314718055994530942f;
         // (a cluster's partial results: in its ring's place, which is free by then)
         const size_t at = done.whole ? done.at0 : p.cluster > 0 ? 0 : (2ull * blockIdx.x + (done.part > 0 ? 1 : 0)) * p.seg_rows;
@@ -763,12 +774,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       const int hk = cur.y / p.qtiles, row0 = (cur.y - hk * p.qtiles) * 16;
       mbar_wait(&q_full[part & 1], (part >> 1) & 1, ab, kDevTimeoutSoftmax);
       __syncwarp();
-      // The references, as they are added to exponents: tt = 5 - T and mm = -M, at first so
-      // large that any finite score moves them.
-      float tt[NRW], mm[NRW], lsum[NRW];
+      // mm = -M, at first so large that any finite score moves it.
+      float c[NRW], mm[NRW], lsum[NRW];
 #pragma unroll
       for (int i = 0; i < NRW; ++i) {
-        tt[i] = mm[i] = kFar;
+        c[i] = 1.f;
+        mm[i] = kFar;
         lsum[i] = 0.f;
       }
       const unsigned vis_all = max(p.causal ? len - p.n_q + 1 : len, 0);   // seen by every row
@@ -807,15 +818,13 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&kv_empty[kslot]);
-        // scores in log2 units, s, and with the value descale's logarithm, y; a, b: with the references
-        float s[KP][NRW], y[KP][NRW];
-        uint64_t a[KP][NRW / 2], b[KP][NRW / 2];
-        bool need = false;
+        // scores in log2 units
+        float s[KP][NRW], sv[KP];
 #pragma unroll
         for (int h = 0; h < KP; ++h) {
           const float ks = h ? __uint_as_float(ks2 & 0xFFFF0000u) : bf16_bits(ks2);
-          const float lv = lg2(h ? __uint_as_float(vs2 & 0xFFFF0000u) : bf16_bits(vs2));
-          const uint64_t ks_2 = pack2(ks, ks), lv_2 = pack2(lv, lv), step = pack2(1.f / (1 << kPStep), 1.f / (1 << kPStep));
+          sv[h] = h ? __uint_as_float(vs2 & 0xFFFF0000u) : bf16_bits(vs2);
+          const uint64_t ks_2 = pack2(ks, ks), step = pack2(1.f / (1 << kPStep), 1.f / (1 << kPStep));
 #pragma unroll
           for (int e = 0; e < NRW; e += 2) {
             auto pair = [&](int k) {
@@ -827,40 +836,45 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
             for (int k = TQ - 2; k >= 0; --k) x = ffma2(x, step, pair(k));
             const float2 cq = *reinterpret_cast<const float2*>(&cq_sh[part & 1][r0 + e]);
             x = fmul2(x, fmul2(pack2(cq.x, cq.y), ks_2));
-            const uint64_t z = fadd2(x, lv_2);
             s[h][e] = lo2(x), s[h][e + 1] = hi2(x);
-            y[h][e] = lo2(z), y[h][e + 1] = hi2(z);
           }
           if (!open) {
+            // (a slot without a token may hold any descale)
+            if (!there || key0 + h >= static_cast<unsigned>(len)) sv[h] = 0.f;
 #pragma unroll
             for (int e = 0; e < NRW; ++e) {
               const bool seen = there && key0 + h < vend_sh[part & 1][r0 + e];
               s[h][e] = seen ? s[h][e] : -INFINITY;
-              y[h][e] = seen ? y[h][e] : -INFINITY;
             }
           }
         }
-        auto exponents = [&]() {
+        uint64_t pr[KP][NRW / 2], pv[KP][NRW / 2];             // p and P'
+        bool need = false;
+        auto weigh = [&]() {
+          need = false;
 #pragma unroll
           for (int h = 0; h < KP; ++h)
 #pragma unroll
             for (int e = 0; e < NRW; e += 2) {
-              a[h][e / 2] = fadd2(pack2(s[h][e], s[h][e + 1]), pack2(mm[e], mm[e + 1]));
-              b[h][e / 2] = fadd2(pack2(y[h][e], y[h][e + 1]), pack2(tt[e], tt[e + 1]));
+              const uint64_t a = fadd2(pack2(s[h][e], s[h][e + 1]), pack2(mm[e], mm[e + 1]));
+              pr[h][e / 2] = pack2(ex2_approx(lo2(a)), ex2_approx(hi2(a)));
+              pv[h][e / 2] = fmul2(pr[h][e / 2], fmul2(pack2(c[e], c[e + 1]), pack2(sv[h], sv[h])));
+              need |= fmaxf(lo2(pv[h][e / 2]), hi2(pv[h][e / 2])) > kPTop || fmaxf(lo2(a), hi2(a)) > 64.f;
             }
         };
-        exponents();
-#pragma unroll
-        for (int h = 0; h < KP; ++h)
-#pragma unroll
-          for (int e = 0; e < NRW / 2; ++e)
-            need |= fmaxf(lo2(b[h][e]), hi2(b[h][e])) > kPShift + 3.f || fmaxf(lo2(a[h][e]), hi2(a[h][e])) > 64.f;
+        weigh();
         if (any_of(BAR, MEMBERS, need)) {
           // references move to the maxima over the tile
+          float lv[KP];
+#pragma unroll
+          for (int h = 0; h < KP; ++h) lv[h] = lg2(sv[h]);
 #pragma unroll
           for (int e = 0; e < NRW; ++e) {
-            float my = KP == 2 ? fmaxf(y[0][e], y[KP - 1][e]) : y[0][e];
-            float ms = KP == 2 ? fmaxf(s[0][e], s[KP - 1][e]) : s[0][e];
+            float my = s[0][e] + lv[0], ms = s[0][e];
+            if constexpr (KP == 2) {
+              my = fmaxf(my, s[KP - 1][e] + lv[KP - 1]);
+              ms = fmaxf(ms, s[KP - 1][e]);
+            }
             asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(my) : "f"(my));
             asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(ms) : "f"(ms));
             if (lane == 0) {
@@ -877,14 +891,22 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
             const float(*red)[4][NR] = red_sh[n & 1];
             const float ty = fmaxf(fmaxf(red[0][0][r], red[0][1][r]), fmaxf(red[0][2][r], red[0][3][r]));
             const float tm = fmaxf(fmaxf(red[1][0][r], red[1][1][r]), fmaxf(red[1][2][r], red[1][3][r]));
-            const float t_new = fminf(tt[e], kPShift - ty), m_new = fminf(mm[e], -tm);
-            alpha[e] = ex2_approx(t_new - tt[e]);
-            lsum[e] *= ex2_approx(m_new - mm[e]);
-            grew |= t_new < tt[e];
-            tt[e] = t_new;
+            const float m_new = fminf(mm[e], -tm);
+            if (m_new == kFar) {
+              alpha[e] = 1.f;                                    // no token yet
+              continue;
+            }
+            const float by = ex2_approx(m_new - mm[e]);          // 0 at the first token
+            const float t_old = mm[e] == kFar ? -INFINITY : kPShift - mm[e] - lg2(c[e]);
+            const float t_new = fmaxf(fmaxf(t_old, ty), kPShift - kMostC - m_new);
+            const float c_new = ex2_approx(kPShift - m_new - t_new);
+            alpha[e] = by * (c_new / c[e]);
+            grew |= t_new > t_old;
+            lsum[e] *= by;
             mm[e] = m_new;
+            c[e] = c_new;
           }
-          exponents();
+          weigh();
           if (i > 0 && grew) {
             // O^T times alpha once P' V(n - 1) is in it (the phase of its value slot's empty barrier)
             mbar_wait(&kv_empty[last.at + 1], last.phase, ab, kDevTimeoutSoftmax);
@@ -918,14 +940,14 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         for (int h = 0; h < KP; ++h)
 #pragma unroll
           for (int e = 0; e < NRW; e += 2) {
-            lsum[e] += ex2_approx(lo2(a[h][e / 2]));
-            lsum[e + 1] += ex2_approx(hi2(a[h][e / 2]));
-            __half2 x = as_half2(cvt_pack_f16(ex2_approx(lo2(b[h][e / 2])), ex2_approx(hi2(b[h][e / 2]))));
+            lsum[e] += lo2(pr[h][e / 2]);
+            lsum[e + 1] += hi2(pr[h][e / 2]);
+            __half2 x = as_half2(cvt_pack_f16(lo2(pv[h][e / 2]), hi2(pv[h][e / 2])));
 #pragma unroll
             for (int k = 0; k < TP; ++k) {
-              const uint32_t c = e4m3_pair_h(half2_bits(x));
-              if (k + 1 < TP) x = __hmul2(__hsub2(x, as_half2(e4m3_halves(c))), __float2half2_rn(1 << kPStep));
-              w[h][k][e / 4] = e & 2 ? w[h][k][e / 4] | (c << 16) : c;
+              const uint32_t code = e4m3_pair_h(half2_bits(x));
+              if (k + 1 < TP) x = __hmul2(__hsub2(x, as_half2(e4m3_halves(code))), __float2half2_rn(1 << kPStep));
+              w[h][k][e / 4] = e & 2 ? w[h][k][e / 4] | (code << 16) : code;
             }
           }
         {
@@ -968,7 +990,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
 #pragma unroll
       for (int e = 0; e < NRW; ++e)
         if (lane == e) {
-          ref_sh[part & 1][0][r0 + e] = tt[e];
+          ref_sh[part & 1][0][r0 + e] = c[e];
           ref_sh[part & 1][1][r0 + e] = mm[e];
         }
       // the part's coefficients and ends have been read
