@@ -37,6 +37,7 @@
 //    joins its partial results through distributed shared memory: one launch, no scratch, no prefix
 //    sums (one request of 1500 tokens, 8 heads: 10.4 us by shares, 8.0 so).
 #include <cmath>
+#include <type_traits>
 
 #include "common.h"
 #include "fp4.cuh"
@@ -1074,11 +1075,12 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_merge_kernel(const K
   if (seg.w < 0 || r >= seg.y) return;
   float m = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = blockIdx.x; c <= seg.z; c += 4) {
-    float lse[4];
-    float4 o[4];
+  auto take = [&](int c, auto some) {                // the results of CTAs c .. c + some - 1
+    constexpr int N = decltype(some)::value;
+    float lse[N];
+    float4 o[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       lse[i] = -INFINITY;
       o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c + i <= seg.z) {
@@ -1087,12 +1089,14 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_merge_kernel(const K
         o[i] = __ldcg(reinterpret_cast<const float4*>(p.o_part + at * D + col));
       }
     }
-    const float m_new = fmaxf(m, fmaxf(fmaxf(lse[0], lse[1]), fmaxf(lse[2], lse[3])));
+    float m_new = m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m_new = fmaxf(m_new, lse[i]);
     const float keep = m == -INFINITY ? 0.f : expf(m - m_new);
     sum *= keep;
     acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       const float w = lse[i] == -INFINITY ? 0.f : expf(lse[i] - m_new);
       sum += w;
       acc.x = fmaf(w, o[i].x, acc.x);
@@ -1101,7 +1105,10 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_merge_kernel(const K
       acc.w = fmaf(w, o[i].w, acc.w);
     }
     m = m_new;
-  }
+  };
+  int c = blockIdx.x;
+  for (; seg.z - c >= 4; c += 16) take(c, std::integral_constant<int, 16>());
+  if (c <= seg.z) take(c, std::integral_constant<int, 4>());
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const size_t at = static_cast<size_t>(seg.x) + r;
   const uint2 pk = FP16 ? make_uint2(cvt_pack_f16(acc.x * inv, acc.y * inv), cvt_pack_f16(acc.z * inv, acc.w * inv))
