@@ -1100,6 +1100,10 @@ attn_status_t attn_decode_paged_fp4(const void* q, const uint8_t* k_cache, const
     return fail(ATTN_ERR_UNSUPPORTED, "(H / H_kv) * n_q must be <= 128");
   if (static_cast<double>(B) * H * n_q * d >= 2147483648.0)
     return fail(ATTN_ERR_INVALID_ARG, "B*H*n_q*d must be < 2^31");
+  if (static_cast<double>(B) * H_kv * ((H / H_kv * n_q + 15) / 16) * (static_cast<double>(max_pages) * page_size / 128 + 8.0) >=
+      2147483648.0)
+    return fail(ATTN_ERR_UNSUPPORTED,
+                "B * H_kv * ceil((H / H_kv) * n_q / 16) * (max_pages * page_size / 128 + 8) must be < 2^31");
   if ((s = check_ptrs({q, k_cache, v_cache, o, lse, workspace, k_descale, v_descale})) != ATTN_OK) return s;
   if (((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 31u) != 0)
     return fail(ATTN_ERR_INVALID_ARG, "k_cache and v_cache must be 32-byte aligned");

@@ -36,6 +36,7 @@
 //    (at most two per CTA).  With few segments a cluster of up to eight CTAs takes each instead and
 //    joins its partial results through distributed shared memory: one launch, no scratch, no prefix
 //    sums (one request of 1500 tokens, 8 heads: 10.4 us by shares, 8.0 so).
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -111,6 +112,7 @@ struct KParams {
   int num_pages, page_size, page_shift, max_pages, causal;
   int cluster;            // CTAs of a segment's cluster, or 0: shares of the line
   int solo;               // shares of whole segments only
+  int most_tokens;        // of a sequence
   float scale_log2;
 };
 
@@ -193,36 +195,30 @@ __device__ __forceinline__ float warp_sums(float (&v)[N], int lane, int* which) 
   return v[0];
 }
 
-// Tokens of a sequence; one out of range counts as none.
+// Tokens of a sequence; a count out of range is none.
 __device__ __forceinline__ int tokens_of(const KParams& p, int b) {
   const int n = __ldcg(p.seq_lens + b);
-  return n < 0 || n > static_cast<long long>(p.max_pages) * p.page_size ? 0 : n;
+  return n < 0 || n > p.most_tokens ? 0 : n;
 }
 template <int TILE>
 __device__ __forceinline__ int tiles_of(int len) { return static_cast<int>((static_cast<unsigned>(len) + TILE - 1) / TILE); }
 
-// a / b for a >= 0; mostly of 32 bits (one of 64 takes some hundred instructions).
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return (a | b) >> 32 ? a / b : static_cast<unsigned>(a) / static_cast<unsigned>(b);
-}
-
 // T units dealt out to the first n of C CTAs (n = min(T, C)), one more to the first `rest` of them.
+// The host keeps T below 2^31: the dealing out stands before all else that a CTA does, and in 64 bits
+// it took half a microsecond more.
 struct Shares {
-  long long per, rest, T;
-  __device__ __forceinline__ Shares(long long T_, int C) : T(T_) {
-    const int n = T < C ? static_cast<int>(T) : C;
-    per = n == 0 ? 0 : quotient(T, n);
-    rest = T - per * n;
+  int per, rest, T;
+  __device__ __forceinline__ Shares(int T_, int C) : T(T_) {
+    const unsigned n = max(1, min(T, C));
+    per = static_cast<int>(T / n);
+    rest = static_cast<int>(T - per * n);
   }
   // first unit of CTA c's (T behind the last that gets one)
-  __device__ __forceinline__ long long start(long long c) const {
-    const long long u = c * per + (c < rest ? c : rest);
-    return u < T ? u : T;
-  }
+  __device__ __forceinline__ int start(int c) const { return min(T, c * per + min(c, rest)); }
   // the CTA that has unit u
-  __device__ __forceinline__ int owner(long long u) const {
-    const long long more = rest * (per + 1);
-    return static_cast<int>(u < more ? quotient(u, per + 1) : rest + quotient(u - more, per));
+  __device__ __forceinline__ int owner(int u) const {
+    const int more = rest * (per + 1);
+    return u < more ? static_cast<unsigned>(u) / (per + 1) : rest + static_cast<unsigned>(u - more) / per;
   }
 };
 
@@ -236,11 +232,11 @@ struct Cursor {
   int at;                // first unit in the segment
   int extra;
   int solo;              // a segment is all of the share's in which it begins
-  long long left;        // units of the share from here on
+  int left;              // units of the share from here on
   __device__ __forceinline__ int tiles() const { return tiles_of<TILE>(len); }
   __device__ __forceinline__ int units() const {
     const int rest = tiles() + extra - at;
-    return left < rest ? static_cast<int>(left) : rest;
+    return left < rest ? left : rest;
   }
   __device__ __forceinline__ int tile_at(int u) const { return u == 0 ? 0 : solo ? tiles() : max(1, u - extra); }
   __device__ __forceinline__ int first() const { return tile_at(at); }           // tile
@@ -291,7 +287,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       o_full[2], o_empty[2], drain_bar[2];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, issued_sh[2];                 // key and value tiles whose copies have been issued
-  __shared__ long long warp_sum[2][C::THREADS / 32];
+  __shared__ int warp_sum[2][C::THREADS / 32];
   __shared__ int start_sh[4];                            // where the share begins
   __shared__ unsigned there_sh[NSLOT / 2];               // boxes of a key tile that were copied
   __shared__ __align__(16) float cq_sh[2][NR];           // of a part's query rows: score coefficients,
@@ -335,7 +331,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   wait_for_previous_kernel();
   release_dependents();
 
-  long long T = 0, g0 = 0, total = 0;       // units of all, first of this CTA and its number
+  int T = 0, g0 = 0, total = 0;       // units of all, first of this CTA and its number
   int extra = 0;
   const int ranks = p.cluster > 0 ? p.cluster : 1, seg = static_cast<int>(blockIdx.x) / ranks;
   const int rank = static_cast<int>(blockIdx.x) - seg * ranks;
@@ -347,34 +343,36 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     }
   } else {
     // ---- units of one segment of the entries before each; this CTA's share
-    const int per = (p.B + C::THREADS - 1) / C::THREADS;
+    const int per = (p.B + C::THREADS - 1) / C::THREADS, warps = (p.B + 32 * per - 1) / (32 * per);
     const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
-    long long sum = 0;
-    int len = 0, some = 0;                    // some: entries with tokens
-    for (int b = b0; b < b1; ++b) {
-      len = tokens_of(p, b);
-      if (len == 0 && blockIdx.x == 0 && __ldcg(p.seq_lens + b) != 0) atomicCAS(p.status, 0, kDevBadSeqlens);
-      sum += tiles_of<TILE>(len);
-      some += len > 0;
-    }
-    long long scan = sum;
-    int scan_some = some;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, scan, o);
-      const int z = __shfl_up_sync(0xffffffffu, scan_some, o);
-      if (lane >= o) {
-        scan += x;
-        scan_some += z;
+    int sum = 0, len = 0, some = 0;           // some: entries with tokens
+    int base = 0, base_some = 0, all = 0, all_some = 0;
+    if (warp < warps) {
+      for (int b = b0; b < b1; ++b) {
+        len = tokens_of(p, b);
+        if (len == 0 && blockIdx.x == 0 && __ldcg(p.seq_lens + b) != 0) atomicCAS(p.status, 0, kDevBadSeqlens);
+        sum += tiles_of<TILE>(len);
+        some += len > 0;
       }
-    }
-    if (lane == 31) {
-      warp_sum[0][warp] = scan;
-      warp_sum[1][warp] = scan_some;
+      base = sum;
+      base_some = some;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, base, o), z = __shfl_up_sync(0xffffffffu, base_some, o);
+        if (lane >= o) {
+          base += x;
+          base_some += z;
+        }
+      }
+      if (lane == 31) {
+        warp_sum[0][warp] = base;
+        warp_sum[1][warp] = base_some;
+      }
+      base -= sum;
+      base_some -= some;
     }
     __syncthreads();
-    long long base = scan - sum, all = 0, base_some = scan_some - some, all_some = 0;
-    for (int w = 0; w < C::THREADS / 32; ++w) {
+    for (int w = 0; w < warps; ++w) {
       if (w < warp) {
         base += warp_sum[0][w];
         base_some += warp_sum[1][w];
@@ -384,13 +382,13 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     }
     // A part's start and end are counted as tiles (64 sequences of up to 16384, d = 64: without them the
     // CTA with the shortest ones ended 10 us after the others), as far as a share has four times as many.
-    extra = static_cast<int>(fminf(C::PART, __fdividef(static_cast<float>(all * p.segs), 4.f * gridDim.x)));
+    extra = static_cast<int>(fminf(C::PART, __fdividef(static_cast<float>(all) * p.segs, 4.f * gridDim.x)));
     base += extra * base_some;
     sum += extra * some;
     T = (all + extra * all_some) * p.segs;
     const Shares shares(T, gridDim.x);
     g0 = shares.start(blockIdx.x);
-    total = shares.start(blockIdx.x + 1ll) - g0;
+    total = shares.start(blockIdx.x + 1) - g0;
     if (total > 0 && base * p.segs <= g0 && g0 < (base + sum) * p.segs) {
       int b = b0;
       for (; b1 - b0 > 1; ++b) {
@@ -400,12 +398,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         base += n;
       }
       const int n = tiles_of<TILE>(len) + extra;
-      const long long in = g0 - base * p.segs;
-      const int y = static_cast<int>(quotient(in, n));
+      const int in = g0 - base * p.segs, y = in / n;
       start_sh[0] = b;
       start_sh[1] = y;
       start_sh[2] = len;
-      start_sh[3] = static_cast<int>(in - static_cast<long long>(y) * n);
+      start_sh[3] = in - y * n;
     }
   }
   tc_fence_before_sync();
@@ -674,7 +671,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       if (lane == 0) mbar_arrive(&q_full[buf]);
       if (p.cluster == 0 && cur.first() == 0 && cur.part() < cur.tiles()) {
         // the CTA whose share holds the segment's last unit
-        const long long last = g0 + (total - cur.left) - cur.at + cur.tiles() + extra - 1;
+        const int last = g0 + (total - cur.left) - cur.at + cur.tiles() + extra - 1;
         crossing = make_int4(static_cast<int>(at0), rows_here, Shares(T, gridDim.x).owner(last),
                              static_cast<int>(2 * blockIdx.x + (part > 0 ? 1 : 0)));
       }
@@ -1188,11 +1185,12 @@ attn_status_t launch_decode_fp4(const Fp4DecodeParams& p, cudaStream_t stream) {
   char* ws = static_cast<char*>(p.workspace);
   char* const lse_part = ws + align_up(part_rows * p.d * sizeof(float), 256);
   char* const crossing = lse_part + align_up(part_rows * sizeof(float), 256);
+  const int most = static_cast<int>(std::min(2147483647ll, static_cast<long long>(p.max_pages) * p.page_size));
   const KParams kp{static_cast<const uint16_t*>(p.q), {p.k_descale, p.v_descale}, p.signs,
                    p.block_table, p.seq_lens, static_cast<uint16_t*>(p.o), p.lse, reinterpret_cast<float*>(ws),
                    reinterpret_cast<float*>(lse_part), reinterpret_cast<int4*>(crossing), status, p.B, p.H, p.H_kv, p.n_q,
                    rows, plan.qtiles, p.H_kv * plan.qtiles, plan.seg_rows, p.num_pages, p.page_size,
-                   page_shift_of(p.page_size), p.max_pages, p.causal, 0, 0, p.scale * 1.4426950408889634f};
+                   page_shift_of(p.page_size), p.max_pages, p.causal, 0, 0, most, p.scale * 1.4426950408889634f};
   return p.d == 64 ? launch_d<64>(p, kp, plan.ctas, stream) : launch_d<128>(p, kp, plan.ctas, stream);
 }
 

@@ -815,14 +815,16 @@ size_t attn_decode_fp4_workspace_size(int B, int H, int H_kv, int n_q, int d, in
  *                    or NULL.  Values are never transformed.
  *   workspace      : at least attn_decode_fp4_workspace_size() bytes, 256-byte aligned;
  *                    calls that overlap on the GPU need one each.
- *   max_seqlen     : >= every seq_lens[b] (sizes the launch and its workspace).
+ *   max_seqlen     : >= every seq_lens[b] (sizes the launch and its workspace; a smaller
+ *                    number costs time, not results).
  *   Other arguments, outputs, masking and device-side error reporting as
  *   attn_decode_paged; a token on a page that is out of range is not seen.  What the slots
  *   behind a sequence hold does not matter.
  * Accuracy: the stored values enter exactly, queries to 2^-19.  The product of a probability
  * and a value descale is held to half a step of `dtype`, and to 2^-20 (bf16) or 2^-25
  * (fp16) of the query row's largest one.  A query row with an infinity or a NaN gives NaN.
- * Limits: d = 64 or 128; (H / H_kv) * n_q <= 128; page_size a power of two in [16, 65536].
+ * Limits: d = 64 or 128; (H / H_kv) * n_q <= 128; page_size a power of two in [16, 65536];
+ * B * H_kv * ceil((H / H_kv) * n_q / 16) * (max_pages * page_size / 128 + 8) < 2^31.
  * Source: as attn_decode_paged_fp8.
  */
 attn_status_t attn_decode_paged_fp4(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,

@@ -60,6 +60,7 @@ def test_decode_refusals(lib, kwargs, why):
 def test_decode_row_limit_and_workspace(lib):
     assert _decode(lib, H=64, Hkv=1, nq=3) == 2 and b"128" in lib.attn_last_error()
     assert _decode(lib, H=2, Hkv=1, nq=2 ** 31 - 1) == 2
+    assert _decode(lib, B=1 << 15, H=8, Hkv=8, maxp=1 << 17, ps=16) == 2 and b"2^31" in lib.attn_last_error()
     size = lib.attn_decode_fp4_workspace_size
     assert size(1, 8, 3, 1, 128, 100) == 0 and size(0, 8, 2, 1, 128, 100) == 0 and size(1, 8, 2, 33, 128, 100) == 0
     need = size(2, 8, 2, 1, 128, 64)
