@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   __shared__ __align__(16) float cq_sh[2][NR];           // of a part's query rows: score coefficients,
   __shared__ unsigned vend_sh[2][NR];                    // ends of the visible tokens,
   __shared__ float ref_sh[2][2][NR], l_sh[2][4][NR];     // references at its end, and sums by key quarter
-  __shared__ float red_sh[2][2][4][NR];                  // maxima of a tile (by parity) by key quarter
+  __shared__ __align__(16) float red_sh[2][2][NR][4];    // maxima of a tile (by parity) by key quarter
   __shared__ float part_lse[NR];                         // of the partial results of a cluster's CTA
   __shared__ float xch_sh[KP == 2 ? NR : 1][KP == 2 ? 64 : 1];
 
@@ -876,33 +876,35 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
             asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(my) : "f"(my));
             asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(ms) : "f"(ms));
             if (lane == 0) {
-              red_sh[n & 1][0][warp & 3][r0 + e] = my;
-              red_sh[n & 1][1][warp & 3][r0 + e] = ms;
+              red_sh[n & 1][0][r0 + e][warp & 3] = my;
+              red_sh[n & 1][1][r0 + e][warp & 3] = ms;
             }
           }
           named_bar_sync(BAR, MEMBERS);
-          float alpha[NRW];
-          bool grew = false;
+          // lane x: row x % NRW
+          const int mine = lane & (NRW - 1);
+          float m_old = mm[0], c_old = c[0];
+#pragma unroll
+          for (int e = 1; e < NRW; ++e) {
+            m_old = mine == e ? mm[e] : m_old;
+            c_old = mine == e ? c[e] : c_old;
+          }
+          const float4 y4 = *reinterpret_cast<const float4*>(red_sh[n & 1][0][r0 + mine]);
+          const float4 m4 = *reinterpret_cast<const float4*>(red_sh[n & 1][1][r0 + mine]);
+          const float ty = fmaxf(fmaxf(y4.x, y4.y), fmaxf(y4.z, y4.w));
+          const float m_new = fminf(m_old, -fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)));
+          const bool none = m_new == kFar;                       // no token yet
+          const float by = ex2_approx(m_new - m_old);            // 0 at the first token
+          const float t_old = m_old == kFar ? -INFINITY : kPShift - m_old - lg2(c_old);
+          const float t_new = fmaxf(fmaxf(t_old, ty), kPShift - kMostC - m_new);
+          const float c_new = none ? 1.f : ex2_approx(kPShift - m_new - t_new);
+          const float alpha = by * __fdividef(c_new, c_old);     // (c: 2^-123 .. 2^120)
+          const bool grew = __any_sync(0xffffffffu, !none && t_new > t_old);
 #pragma unroll
           for (int e = 0; e < NRW; ++e) {
-            const int r = r0 + e;
-            const float(*red)[4][NR] = red_sh[n & 1];
-            const float ty = fmaxf(fmaxf(red[0][0][r], red[0][1][r]), fmaxf(red[0][2][r], red[0][3][r]));
-            const float tm = fmaxf(fmaxf(red[1][0][r], red[1][1][r]), fmaxf(red[1][2][r], red[1][3][r]));
-            const float m_new = fminf(mm[e], -tm);
-            if (m_new == kFar) {
-              alpha[e] = 1.f;                                    // no token yet
-              continue;
-            }
-            const float by = ex2_approx(m_new - mm[e]);          // 0 at the first token
-            const float t_old = mm[e] == kFar ? -INFINITY : kPShift - mm[e] - lg2(c[e]);
-            const float t_new = fmaxf(fmaxf(t_old, ty), kPShift - kMostC - m_new);
-            const float c_new = ex2_approx(kPShift - m_new - t_new);
-            alpha[e] = by * (c_new / c[e]);
-            grew |= t_new > t_old;
-            lsum[e] *= by;
-            mm[e] = m_new;
-            c[e] = c_new;
+            mm[e] = __shfl_sync(0xffffffffu, m_new, e);
+            c[e] = __shfl_sync(0xffffffffu, c_new, e);
+            lsum[e] *= __shfl_sync(0xffffffffu, by, e);
           }
           weigh();
           if (i > 0 && grew) {
@@ -917,7 +919,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
               tmem_ld_cols<NRW>(at, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < NRW; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[e]);
+              for (int e = 0; e < NRW; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * __shfl_sync(0xffffffffu, alpha, e));
               tmem_st_cols<NRW>(at, o);
             }
             tmem_st_wait();
