@@ -71,7 +71,7 @@ struct Cfg {
   static constexpr int CW = NR == 16 ? 2 : 1;            // softmax warps per quarter of the keys
   static constexpr int SW = 4 * CW;
   static constexpr int NRW = NR / CW;                    // query rows of a softmax thread
-  static constexpr int PART = NR == 4 ? 3 : NR == 8 ? 4 : 6;   // tiles that take the time of a part's start and end
+  static constexpr int PART = NR == 4 ? 1 : 2;       // tiles that take the time of a part's start and end
   static constexpr int QW = NR == 16 ? NR * D / 512 : 1; // query warps: of 16 rows one for each 512 values
   static constexpr int LOAD = SW, MMA_S = SW + 1, MMA_PV = SW + 2, QUERY = SW + 3;
   static constexpr int THREADS = (SW + 3 + QW) * 32;
@@ -380,8 +380,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       all += warp_sum[0][w];
       all_some += warp_sum[1][w];
     }
-    // A part's start and end are counted as tiles (64 sequences of up to 16384, d = 64: without them the
-    // CTA with the shortest ones ended 10 us after the others), as far as a share has four times as many.
+    // A part's start and end are counted as tiles, as far as a share has four times as many (64
+    // sequences of up to 16384 tokens, d = 64: 75 us without them, 66.6 so; two tiles instead of one 67.0).
     extra = static_cast<int>(fminf(C::PART, __fdividef(static_cast<float>(all) * p.segs, 4.f * gridDim.x)));
     base += extra * base_some;
     sum += extra * some;
