@@ -292,7 +292,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   __shared__ unsigned there_sh[NSLOT / 2];               // boxes of a key tile that were copied
   __shared__ __align__(16) float cq_sh[2][NR];           // of a part's query rows: score coefficients,
   __shared__ unsigned vend_sh[2][NR];                    // ends of the visible tokens,
-  __shared__ float ref_sh[2][2][NR], l_sh[2][4][NR];     // references at its end, and sums by key quarter
+  __shared__ float2 ref_sh[2][NR];                       // c and -M at its end,
+  __shared__ __align__(16) float l_sh[2][NR][4];         // sums by key quarter
   __shared__ __align__(16) float red_sh[2][2][NR][4];    // maxima of a tile (by parity) by key quarter
   __shared__ float part_lse[NR];                         // of the partial results of a cluster's CTA
   __shared__ float xch_sh[KP == 2 ? NR : 1][KP == 2 ? 64 : 1];
@@ -714,14 +715,14 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       float o[NRW];
 #pragma unroll
       for (int i = 0; i < NRW; ++i) o[i] = 0.f;
+      uint32_t raw[TP][NRW];
 #pragma unroll
-      for (int k = TP - 1; k >= 0; --k) {
-        uint32_t raw[NRW];
-        tmem_ld_cols<NRW>(tmem + lane_addr + C::O_COL(buf) + o_half + k * NR + r0, raw);
-        tmem_ld_wait();
+      for (int k = 0; k < TP; ++k) tmem_ld_cols<NRW>(tmem + lane_addr + C::O_COL(buf) + o_half + k * NR + r0, raw[k]);
+      tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < NRW; ++i) o[i] = fmaf(o[i], 1.f / (1 << kPStep), __uint_as_float(raw[i]));
-      }
+      for (int k = TP - 1; k >= 0; --k)
+#pragma unroll
+        for (int i = 0; i < NRW; ++i) o[i] = fmaf(o[i], 1.f / (1 << kPStep), __uint_as_float(raw[k][i]));
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_empty[buf]);
@@ -733,11 +734,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       if (KP == 1 || !(warp & 2)) {
         // lane i: factor and log-sum-exp of row i
         const int mine = r0 + (lane & (NRW - 1));
-        const float l = ((l_sh[buf][0][mine] + l_sh[buf][1][mine]) + l_sh[buf][2][mine]) + l_sh[buf][3][mine];
-        const float c = ref_sh[buf][0][mine], mm = ref_sh[buf][1][mine];
+        const float4 l4 = *reinterpret_cast<const float4*>(l_sh[buf][mine]);
+        const float l = ((l4.x + l4.y) + l4.z) + l4.w;
+        const float2 ref = ref_sh[buf][mine];
         // (a NaN among the scores or descales is in o by now, and stays)
-        const float f = l == 0.f ? 0.f : 1.f / c / l;
-        const float lse = l == 0.f ? -INFINITY : (lg2(l) - mm) * 0.69314718055994530942f;
+        const float f = l == 0.f ? 0.f : __fdividef(__fdividef(1.f, ref.x), l);     // (all below 2^126)
+        const float lse = l == 0.f ? -INFINITY : (lg2(l) - ref.y) * 0.69314718055994530942f;
         // (a cluster's partial results: in its ring's place, which is free by then)
         const size_t at = done.whole ? done.at0 : p.cluster > 0 ? 0 : (2ull * blockIdx.x + (done.part > 0 ? 1 : 0)) * p.seg_rows;
         float* const o_part = p.cluster > 0 ? reinterpret_cast<float*>(sKV) : p.o_part;
@@ -860,8 +862,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
               need |= fmaxf(lo2(pv[h][e / 2]), hi2(pv[h][e / 2])) > kPTop || fmaxf(lo2(a), hi2(a)) > 64.f;
             }
         };
-        weigh();
-        if (any_of(BAR, MEMBERS, need)) {
+        if (i > 0) weigh();
+        if (i == 0 || any_of(BAR, MEMBERS, need)) {
           // references move to the maxima over the tile
           float lv[KP];
 #pragma unroll
@@ -986,13 +988,14 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       // this part's row sums, and what its output needs
       int which;
       const float row_sum = warp_sums<NRW>(lsum, lane, &which);
-      l_sh[part & 1][warp & 3][r0 + which] = row_sum;          // (several lanes, the same value)
+      l_sh[part & 1][r0 + which][warp & 3] = row_sum;          // (several lanes, the same value)
+      float c_mine = c[0], mm_mine = mm[0];
 #pragma unroll
-      for (int e = 0; e < NRW; ++e)
-        if (lane == e) {
-          ref_sh[part & 1][0][r0 + e] = c[e];
-          ref_sh[part & 1][1][r0 + e] = mm[e];
-        }
+      for (int e = 1; e < NRW; ++e) {
+        c_mine = (lane & (NRW - 1)) == e ? c[e] : c_mine;
+        mm_mine = (lane & (NRW - 1)) == e ? mm[e] : mm_mine;
+      }
+      ref_sh[part & 1][r0 + (lane & (NRW - 1))] = make_float2(c_mine, mm_mine);
       // the part's coefficients and ends have been read
       if (lane == 0) mbar_arrive(&q_empty[part & 1]);
       done.part = part;
