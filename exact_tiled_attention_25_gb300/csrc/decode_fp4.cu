@@ -227,7 +227,7 @@ struct Shares {
 // the extra ones begins at tile 1.
 template <int TILE>
 struct Cursor {
-  int b, y;              // sequence, segment of it
+  int b, hk, qt;         // sequence, key/value head, 16 query rows of it
   int len;
   int at;                // first unit in the segment
   int extra;
@@ -245,11 +245,14 @@ struct Cursor {
     left -= units();
     if (left <= 0) return;
     at = 0;
-    if (++y == p.segs) {
-      y = 0;
-      do {
-        len = tokens_of(p, ++b);
-      } while (len == 0);
+    if (++qt == p.qtiles) {
+      qt = 0;
+      if (++hk == p.H_kv) {
+        hk = 0;
+        do {
+          len = tokens_of(p, ++b);
+        } while (len == 0);
+      }
     }
   }
 };
@@ -412,10 +415,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   const uint32_t tmem = tmem_base_sh;
   const Abort ab{&abort_sh, p.status};
 
-  Cursor<TILE> cur{0, 0, 0, 0, extra, p.solo, 0};
+  Cursor<TILE> cur{0, 0, 0, 0, 0, extra, p.solo, 0};
   if (p.cluster > 0) {
     cur.b = seg / p.segs;
-    cur.y = seg - cur.b * p.segs;
+    cur.hk = (seg - cur.b * p.segs) / p.qtiles;
+    cur.qt = seg - cur.b * p.segs - cur.hk * p.qtiles;
     cur.len = start_sh[2];
     const unsigned n = cur.tiles();
     cur.at = rank * n / ranks;
@@ -423,7 +427,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   } else if (total > 0) {
     cur.left = total;
     cur.b = start_sh[0];
-    cur.y = start_sh[1];
+    cur.hk = start_sh[1] / p.qtiles;
+    cur.qt = start_sh[1] - cur.hk * p.qtiles;
     cur.len = start_sh[2];
     cur.at = start_sh[3];
     if (cur.part() == 0) cur.next_part(p);            // its tiles are the CTA's before
@@ -444,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     Ring<NSLOT, 2> key_slot;
     bool ok = true;
     while (ok && cur.left > 0) {
-      const int take = cur.part(), hk = cur.y / p.qtiles, kbeg = cur.first() * TILE;   // kbeg < len
+      const int take = cur.part(), hk = cur.hk, kbeg = cur.first() * TILE;   // kbeg < len
       auto window = [&](int w) -> int {
         const long long key = kbeg + static_cast<long long>(32 * w + lane) * box;
         if (key >= cur.len || 32 * w + lane >= take * nbox) return -1;
@@ -570,6 +575,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     // d / 16 lanes hold a row, 16 neighbouring columns each.
     constexpr int L = D / 16, PER = 32 / L, PASSES = (NR + PER - 1) / PER / C::QW;
     const int u = lane % L, first_row = (warp - C::QUERY) * PASSES * PER;
+    float4 sgn[4];
+    if constexpr (SIGNS) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sgn[i] = __ldcg(reinterpret_cast<const float4*>(p.signs + 16 * u) + i);
+    }
     bool ok = true;
     int4 crossing = make_int4(0, 0, 0, -1);            // a segment that this share begins and does not end
     for (int part = 0; ok && cur.left > 0; ++part) {
@@ -578,8 +588,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         ok = false;
         break;
       }
-      const int hk = cur.y / p.qtiles, row0 = (cur.y - hk * p.qtiles) * 16;
-      const size_t at0 = (static_cast<size_t>(cur.b) * p.H_kv + hk) * p.rows + row0;
+      const int row0 = cur.qt * 16;
+      const size_t at0 = (static_cast<size_t>(cur.b) * p.H_kv + cur.hk) * p.rows + row0;
       const int rows_here = min(NR, p.rows - row0);
       uint4 raw[PASSES][2];
 #pragma unroll
@@ -604,7 +614,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         if constexpr (SIGNS) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
-            const float4 s = __ldcg(reinterpret_cast<const float4*>(p.signs + 16 * u + i));
+            const float4 s = sgn[i / 4];
             x[i] *= s.x, x[i + 1] *= s.y, x[i + 2] *= s.z, x[i + 3] *= s.w;
           }
 #pragma unroll
@@ -618,9 +628,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
               }
 #pragma unroll
           for (int m = 1; m < L; m <<= 1) {
-            const float sgn = (u & m) ? -1.f : 1.f;
+            const float minus = (u & m) ? -1.f : 1.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = fmaf(sgn, x[i], __shfl_xor_sync(0xffffffffu, x[i], m));
+            for (int i = 0; i < 16; ++i) x[i] = fmaf(minus, x[i], __shfl_xor_sync(0xffffffffu, x[i], m));
           }
           const float isd = D == 128 ? 0.08838834764831845f : 0.125f;
 #pragma unroll
@@ -655,8 +665,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
             }
           }
           const int col = k * NR + r;
-          if (r < NR)
-            {
+          if (r < NR) {
             const int piece = KP == 2 ? 4 * buf + u : u;         // of the row's eight
             uint8_t* tile = KP == 2 ? sQ : sQ + buf * C::Q_STEP;
             st_shared_v4(smem_u32(tile + col * 128 + ((piece ^ (col & 7)) << 4)), w[0], w[1], w[2], w[3]);
@@ -742,22 +751,24 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         const float lse = l == 0.f ? -INFINITY : (lg2(l) - ref.y) * 0.69314718055994530942f;
         // (a cluster's partial results: in its ring's place, which is free by then)
         const size_t at = done.whole ? done.at0 : p.cluster > 0 ? 0 : (2ull * blockIdx.x + (done.part > 0 ? 1 : 0)) * p.seg_rows;
-        float* const o_part = p.cluster > 0 ? reinterpret_cast<float*>(sKV) : p.o_part;
         if ((warp & 3) == 0 && lane < NRW && mine < done.rows)
           (done.whole ? p.lse : p.cluster > 0 ? part_lse : p.lse_part)[at + mine] = lse;
 #pragma unroll
         for (int i = 0; i < NRW; ++i) {
-          const int r = r0 + i;
-          const float fi = __shfl_sync(0xffffffffu, f, i);
-          if (r >= done.rows) continue;
-          if constexpr (KP == 2) o[i] += xch_sh[r][t];
-          const float val = o[i] * fi;
-          if (done.whole) {
-            const uint32_t pk = FP16 ? cvt_pack_f16(val, 0.f) : cvt_pack_bf16(val, 0.f);
-            p.o[(at + r) * D + t] = static_cast<uint16_t>(pk);
-          } else {
-            o_part[(at + r) * D + t] = val;
-          }
+          if constexpr (KP == 2) o[i] += xch_sh[r0 + i][t];
+          o[i] *= __shfl_sync(0xffffffffu, f, i);
+        }
+        const int rows = done.rows - r0;
+        if (done.whole) {
+          uint16_t* const dst = p.o + (at + r0) * D + t;
+#pragma unroll
+          for (int i = 0; i < NRW; ++i)
+            if (i < rows) dst[i * D] = static_cast<uint16_t>(FP16 ? cvt_pack_f16(o[i], 0.f) : cvt_pack_bf16(o[i], 0.f));
+        } else {
+          float* const dst = (p.cluster > 0 ? reinterpret_cast<float*>(sKV) : p.o_part) + (at + r0) * D + t;
+#pragma unroll
+          for (int i = 0; i < NRW; ++i)
+            if (i < rows) dst[i * D] = o[i];
         }
       }
       if constexpr (KP == 2) named_bar_sync(BAR, MEMBERS);     // xch_sh has been read
@@ -771,7 +782,6 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     Ring<C::PB> pb;
     for (int part = 0; cur.left > 0; ++part) {
       const int take = cur.part(), len = cur.len, first_tile = cur.first();
-      const int hk = cur.y / p.qtiles, row0 = (cur.y - hk * p.qtiles) * 16;
       mbar_wait(&q_full[part & 1], (part >> 1) & 1, ab, kDevTimeoutSoftmax);
       __syncwarp();
       // mm = -M, at first so large that any finite score moves it.
@@ -999,9 +1009,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       // the part's coefficients and ends have been read
       if (lane == 0) mbar_arrive(&q_empty[part & 1]);
       done.part = part;
-      done.rows = min(NR, p.rows - row0);
+      done.rows = min(NR, p.rows - cur.qt * 16);
       done.whole = p.cluster == 0 && take == cur.tiles();
-      done.at0 = (static_cast<size_t>(cur.b) * p.H_kv + hk) * p.rows + row0;
+      done.at0 = (static_cast<size_t>(cur.b) * p.H_kv + cur.hk) * p.rows + cur.qt * 16;
       cur.next_part(p);
     }
     if (done.part >= 0) write_out();
@@ -1033,8 +1043,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     // segment's rows, four columns each.
     if (begin.left <= 0 && threadIdx.x < NR) part_lse[threadIdx.x] = -INFINITY;
     cluster_sync();
-    const int hk = begin.y / p.qtiles, row0 = (begin.y - hk * p.qtiles) * 16;
-    const size_t at0 = (static_cast<size_t>(begin.b) * p.H_kv + hk) * p.rows + row0;
+    const int row0 = begin.qt * 16;
+    const size_t at0 = (static_cast<size_t>(begin.b) * p.H_kv + begin.hk) * p.rows + row0;
     const int items = min(NR, p.rows - row0) * (D / 4);
     for (int x = rank * C::THREADS + static_cast<int>(threadIdx.x); x < items; x += ranks * C::THREADS) {
       const int r = x / (D / 4), c4 = x % (D / 4);
