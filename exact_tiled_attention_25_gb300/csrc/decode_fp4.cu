@@ -440,11 +440,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     // A tile is fetched page by page: a box is min(page_size, TILE) tokens of one page, at most
     // 16 of them.  Lane x issues box x (a copy costs its warp some hundred clocks).  The descales of
     // the tile's keys and values come with its keys, by 16-byte copies of all lanes (8 tokens each; a
-    // bulk copy for each page took as long as the codes' own).  The pages of 32 boxes are read from the block table at a time, the
-    // next 32 while those are in use.  Boxes behind the sequence are left out, as are those on
-    // pages outside the cache (reported): what the slot held before is finite codes, and their
-    // tokens are masked.
-    const int box = min(p.page_size, TILE), nbox = TILE / box;
+    // bulk copy for each page took as long as the codes' own).  The pages of 32 boxes are read from
+    // the block table at a time, the next 32 while those are in use.  Boxes behind the sequence are
+    // left out, as are those on pages outside the cache (reported): what the slot held before is
+    // finite codes, and their tokens are masked.
+    const int box_shift = min(p.page_shift, KP == 2 ? 8 : 7), box = 1 << box_shift, nbox = TILE >> box_shift;
     int n = 0;
     Ring<NSLOT, 2> key_slot;
     bool ok = true;
@@ -471,29 +471,27 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         const int off = static_cast<int>(key) & (p.page_size - 1);
         for (int kv = 0; kv < 2; ++kv) {
           const int slot = key_slot.at + kv;
-          int go = 1;
-          if (lane == 0) {
-            if (n >= NSLOT / 2 && !mbar_wait(&kv_empty[slot], key_slot.phase ^ 1u, ab, kDevTimeoutLoad)) {
-              go = 0;
-            } else {
-              if (kv == 0) there_sh[slot / 2] = there;
-              mbar_arrive_expect_tx(&kv_full[slot], __popc(there) * box * (D / 2));
-              issued_sh[kv] = n + 1;
-            }
-          }
-          if (!__shfl_sync(0xffffffffu, go, 0)) {
+          const bool free = n < NSLOT / 2 || mbar_wait(&kv_empty[slot], key_slot.phase ^ 1u, ab, kDevTimeoutLoad);
+          if (!__all_sync(0xffffffffu, free)) {
             ok = false;
             break;
           }
+          if (lane == 0) {
+            if (kv == 0) there_sh[slot / 2] = there;
+            mbar_arrive_expect_tx(&kv_full[slot], __popc(there) * box * (D / 2));
+            issued_sh[kv] = n + 1;
+          }
+          __syncwarp();
           if (good)
             tma_load_4d(sKV + slot * C::SLOT + lane * (box / KP) * 128, kv ? &tmV : &tmK, &kv_full[slot], 0, off / KP, hk, phys);
           if (kv == 0) {
             uint8_t* dst = sDesc + slot / 2 * 4 * TILE;
 #pragma unroll
             for (int c = lane; c < TILE / 4; c += 32) {          // 16 bytes: keys' first, then values'
-              const int tok = c % (TILE / 8) * 8, x = tok / box;
+              const int tok = c % (TILE / 8) * 8, x = tok >> box_shift;
               const int page = __shfl_sync(0xffffffffu, phys, x);
-              const size_t row = (static_cast<size_t>(page) * p.H_kv + hk) * p.page_size + ((kbeg + i * TILE + tok) & (p.page_size - 1));
+              const size_t row = ((static_cast<size_t>(page) * p.H_kv + hk) << p.page_shift) +
+                                 ((kbeg + i * TILE + tok) & (p.page_size - 1));
               if ((there >> x) & 1u) copy16_async(dst + c * 16, p.descale[c / (TILE / 8)] + row, true);
             }
             copies_arrive(&kv_full[slot]);
