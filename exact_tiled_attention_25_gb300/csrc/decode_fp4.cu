@@ -73,8 +73,11 @@ struct Cfg {
   static constexpr int NRW = NR / CW;                    // query rows of a softmax thread
   static constexpr int PART = NR == 4 ? 1 : 2;       // tiles that take the time of a part's start and end
   static constexpr int QW = NR == 16 ? NR * D / 512 : 1; // query warps: of 16 rows one for each 512 values
-  static constexpr int LOAD = SW, MMA_S = SW + 1, MMA_PV = SW + 2, QUERY = SW + 3;
-  static constexpr int THREADS = (SW + 3 + QW) * 32;
+  // Copying warps: with two one has the keys, one the values (16 x 8192 tokens in pages of 16: 38.2 us with one,
+  // 31.9 with two).  Of 8 rows one: with 18 warps on an SM there are 96 registers a thread (33.4 us; two: 34.6).
+  static constexpr int LW = NR == 8 ? 1 : 2;
+  static constexpr int LOAD = SW, MMA_S = SW + LW, MMA_PV = MMA_S + 1, QUERY = MMA_PV + 1;
+  static constexpr int THREADS = (QUERY + QW) * 32;
   static constexpr int CTAS = NR == 16 ? 1 : 2;          // of an SM (16 rows: registers)
   // The two query tiles (NS rows of D bytes); of d = 64 they are the halves of one of 128 bytes a row.
   static constexpr int Q_BYTES = 2 * NS * D, P_TILE = NPV * 128;
@@ -435,7 +438,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   }
   const Cursor<TILE> begin = cur;
 
-  if (warp == C::LOAD) {
+  if (warp >= C::LOAD && warp < C::LOAD + C::LW) {
     // ------------------------------------------------------------ producer
     // A tile is fetched page by page: a box is min(page_size, TILE) tokens of one page, at most
     // 16 of them.  Lane x issues box x (a copy costs its warp some hundred clocks).  The descales of
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         if (wanted && !good) atomicCAS(p.status, 0, kDevBadSeqlens);
         const unsigned there = __ballot_sync(0xffffffffu, good);
         const int off = static_cast<int>(key) & (p.page_size - 1);
-        for (int kv = 0; kv < 2; ++kv) {
+        for (int kv = warp - C::LOAD; kv < 2; kv += C::LW) {
           const int slot = key_slot.at + kv;
           const bool free = n < NSLOT / 2 || mbar_wait(&kv_empty[slot], key_slot.phase ^ 1u, ab, kDevTimeoutLoad);
           if (!__all_sync(0xffffffffu, free)) {
@@ -700,7 +703,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     // the lane t of those rows' columns.
     const int t = (warp & 3) * 32 + lane, cg = warp >> 2, r0 = cg * NRW;
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    constexpr uint32_t BAR = 1, MEMBERS = 32 * C::SW;
+    const uint32_t bar = 1 + cg;          // of the four warps that have the same query rows
+    constexpr uint32_t MEMBERS = 128;
     const int box_shift = min(p.page_shift, KP == 2 ? 8 : 7);
     const unsigned all_boxes = 0xFFFFu >> (16 - (TILE >> box_shift));
     const int o_half = KP == 2 && (warp & 2) ? NR * TP : 0;    // columns that hold this lane's sums
@@ -737,7 +741,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
 #pragma unroll
         for (int i = 0; i < NRW; ++i) xch_sh[KP == 2 ? r0 + i : 0][KP == 2 ? t - 64 : 0] = o[i];
       }
-      named_bar_sync(BAR, MEMBERS);                            // the sums of rows are there, too
+      named_bar_sync(bar, MEMBERS);                            // the sums of rows are there, too
       if (KP == 1 || !(warp & 2)) {
         // lane i: factor and log-sum-exp of row i
         const int mine = r0 + (lane & (NRW - 1));
@@ -769,7 +773,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
             if (i < rows) dst[i * D] = o[i];
         }
       }
-      if constexpr (KP == 2) named_bar_sync(BAR, MEMBERS);     // xch_sh has been read
+      if constexpr (KP == 2) named_bar_sync(bar, MEMBERS);     // xch_sh has been read
     };
 
     int n = 0;
@@ -793,8 +797,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
       const unsigned vis_all = max(p.causal ? len - p.n_q + 1 : len, 0);   // seen by every row
       for (int i = 0; i < take; ++i, ++n) {
         const int kslot = key.at, sbuf = SAME ? kslot / 2 : sb.at;
-        mbar_wait(&s_full[sbuf], SAME ? key.phase : sb.phase, ab, kDevTimeoutSoftmax);
-        mbar_test_wait(&kv_full[kslot], key.phase);        // complete: what came with the key tile is seen
+        // (the keys' barrier is complete then: what came with them is seen)
+        const bool ready = mbar_test_wait(&s_full[sbuf], SAME ? key.phase : sb.phase), seen_too = mbar_test_wait(&kv_full[kslot], key.phase);
+        if (!(ready && seen_too)) {
+          mbar_wait(&s_full[sbuf], SAME ? key.phase : sb.phase, ab, kDevTimeoutSoftmax);
+          mbar_test_wait(&kv_full[kslot], key.phase);
+        }
         __syncwarp();
         tc_fence_after_sync();
         constexpr int LD = C::CW == 1 ? C::NS : TQ * NRW;      // columns read
@@ -871,7 +879,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
             }
         };
         if (i > 0) weigh();
-        if (i == 0 || any_of(BAR, MEMBERS, need)) {
+        if (i == 0 || any_of(bar, MEMBERS, need)) {
           // references move to the maxima over the tile
           float lv[KP];
 #pragma unroll
@@ -890,7 +898,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
               red_sh[n & 1][1][r0 + e][warp & 3] = ms;
             }
           }
-          named_bar_sync(BAR, MEMBERS);
+          named_bar_sync(bar, MEMBERS);
           // lane x: row x % NRW
           const int mine = lane & (NRW - 1);
           float m_old = mm[0], c_old = c[0];
