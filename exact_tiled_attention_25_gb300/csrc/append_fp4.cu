@@ -198,13 +198,16 @@ __device__ __forceinline__ void append_block(const AppendFp4Params& p, long long
   const long long row0 = (slot >> p.page_shift) * p.H_kv * p.page_size + (slot & (p.page_size - 1));
   uint8_t* const codes = is_v ? p.v_cache : p.k_cache;
   uint16_t* const descale = is_v ? p.v_descale : p.k_descale;
-  for (int h = h0; h < h1; ++h) {
-    float x[16];
-    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-    if (live) {
+  uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+  auto load = [&](int h) {
+    if (live && h < h1) {
       a = __ldcg(reinterpret_cast<const uint4*>(src + sh * h));
       b = __ldcg(reinterpret_cast<const uint4*>(src + sh * h + D / 2));
     }
+  };
+  load(h0);
+  for (int h = h0; h < h1; ++h) {
+    float x[16];
     {
       float lo[8], hi[8];
       unpack16<FP16>(a, lo);
@@ -212,6 +215,7 @@ __device__ __forceinline__ void append_block(const AppendFp4Params& p, long long
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = lo[i], x[8 + i] = hi[i];
     }
+    load(h + 1);
     if (!is_v) {                                       // the same for the whole block
       rotate_row<D, MODE>(x, tab, p.rot, turn, u);
       if constexpr (SIGNS) transform_row<D>(x, signs, u);
