@@ -15,8 +15,7 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRows = 4;          // rows of a thread, loaded before the first is stored
+constexpr int kThreads = 128;
 
 enum : int { k16 = 0, k8 = 1, k4 = 2 };
 
@@ -144,19 +143,20 @@ __device__ __forceinline__ void restore_row(float (&x)[16], const float* signs, 
   }
 }
 
-// A block: kRows * kThreads / (d / 16) rows of one head of the keys or the values, of one
+// A block: ROWS * kThreads / (d / 16) rows of one head of the keys or the values, of one
 // request (padded output) or of the packed batch.
-template <int D, int FORMAT, bool FP16, bool SIGNS>
+// ROWS: of a thread, loaded before the first is stored.
+template <int D, int FORMAT, bool FP16, bool SIGNS, int ROWS>
 __global__ void __launch_bounds__(kThreads)
     cache_read_kernel(const CacheReadParams p) {
   constexpr int L = D / 16, G = kThreads / L;
   const int u = threadIdx.x % L, mine = threadIdx.x / L;
   const bool is_v = blockIdx.y & 1;
   const int h = blockIdx.y >> 1;
-  const long long row0 = static_cast<long long>(blockIdx.x) * (G * kRows), i0 = row0 + mine;
+  const long long row0 = static_cast<long long>(blockIdx.x) * (G * ROWS), i0 = row0 + mine;
   uint16_t* out = static_cast<uint16_t*>(is_v ? p.v_out : p.k_out) + 8 * u;
-  Site at[kRows];
-  bool write[kRows];
+  Site at[ROWS];
+  bool write[ROWS];
   // What every row needs comes through shared memory: read from L2 by each warp, the lines
   // of the signs and the lengths bounded the kernel (571 us for 8 prefixes of up to 16384).
   __shared__ __align__(16) float signs[SIGNS ? D : 4];
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads)
     const int2 r = range_sh[0];
     out += (static_cast<size_t>(b) * p.H_kv + h) * p.n * D;
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
+    for (int k = 0; k < ROWS; ++k) {
       const long long i = i0 + k * G;
       write[k] = i < p.n;
       at[k] = write[k] && r.y + i < r.x ? site_of(p, b, static_cast<int>(r.y + i)) : Site{-1, 0};
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads)
     if (threadIdx.x == 0) cu_sh[have] = __ldcg(p.cu_seqlens + lo + have);
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
+    for (int k = 0; k < ROWS; ++k) {
       const long long i = i0 + k * G;
       at[k] = {-1, 0};
       write[k] = false;
@@ -234,15 +234,15 @@ __global__ void __launch_bounds__(kThreads)
         if (c0 < 0 || c1 < c0 || c1 > p.n || (b == 0 && c0 != 0)) atomicCAS(p.status, 0, kDevBadTables);
       }
   }
-  Raw<FORMAT> raw[kRows];
+  Raw<FORMAT> raw[ROWS];
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
+  for (int k = 0; k < ROWS; ++k) {
     raw[k] = Raw<FORMAT>{};
     if (at[k].phys >= 0) raw[k] = load_raw<D, FORMAT>(p, is_v, h, at[k], u);
   }
   const long long step = p.cu_seqlens == nullptr ? D : static_cast<long long>(p.H_kv) * D;
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
+  for (int k = 0; k < ROWS; ++k) {
     uint4 a, b;
     if constexpr (FORMAT == k16) {
       a = raw[k].a, b = raw[k].b;
@@ -267,12 +267,21 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+template <int D, int FORMAT, bool FP16, bool SIGNS, int ROWS>
+attn_status_t launch_rows(const CacheReadParams& p, cudaStream_t stream) {
+  constexpr int rows = kThreads / (D / 16) * ROWS;
+  const dim3 grid((p.n + rows - 1) / rows, 2 * p.H_kv, p.cu_seqlens ? 1 : p.B);
+  const cudaError_t e = launch_dependent(cache_read_kernel<D, FORMAT, FP16, SIGNS, ROWS>, grid, kThreads, 0, stream, 0, p);
+  return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "cache read kernel launch");
+}
+
+// Four rows of a thread for long ranges, one where all blocks of one run at a time (16 to an SM): a
+// prefix of 509 tokens, 8 heads 3.0 us with one, 5.0 with four; 8 of up to 16384 119 and 102.
 template <int D, int FORMAT, bool FP16, bool SIGNS>
 attn_status_t launch_t(const CacheReadParams& p, cudaStream_t stream) {
-  constexpr int rows = kThreads / (D / 16) * kRows;
-  const dim3 grid((p.n + rows - 1) / rows, 2 * p.H_kv, p.cu_seqlens ? 1 : p.B);
-  const cudaError_t e = launch_dependent(cache_read_kernel<D, FORMAT, FP16, SIGNS>, grid, kThreads, 0, stream, 0, p);
-  return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "cache read kernel launch");
+  constexpr int rows = kThreads / (D / 16);
+  const long long blocks = ((p.n + rows - 1LL) / rows) * 2 * p.H_kv * (p.cu_seqlens ? 1 : p.B);
+  return blocks <= 152 * 16 ? launch_rows<D, FORMAT, FP16, SIGNS, 1>(p, stream) : launch_rows<D, FORMAT, FP16, SIGNS, 4>(p, stream);
 }
 
 template <int D, int FORMAT>
