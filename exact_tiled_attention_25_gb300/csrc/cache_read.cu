@@ -143,42 +143,36 @@ __device__ __forceinline__ void restore_row(float (&x)[16], const float* signs, 
   }
 }
 
-// A block: ROWS * kThreads / (d / 16) rows of one head of the keys or the values, of one
-// request (padded output) or of the packed batch.
-// ROWS: of a thread, loaded before the first is stored.
-template <int D, int FORMAT, bool FP16, bool SIGNS, int ROWS>
+// A block: kThreads / (d / 16) rows, a row of a thread, of one request (padded output) or of the
+// packed batch, in `per` planes: keys and values of head 0, of head 1, ...  What a row needs is
+// looked up once for all of them, and a plane's row is loaded before the last one's is stored.
+template <int D, int FORMAT, bool FP16, bool SIGNS>
 __global__ void __launch_bounds__(kThreads)
-    cache_read_kernel(const CacheReadParams p) {
+    cache_read_kernel(const CacheReadParams p, int per) {
   constexpr int L = D / 16, G = kThreads / L;
-  const int u = threadIdx.x % L, mine = threadIdx.x / L;
-  const bool is_v = blockIdx.y & 1;
-  const int h = blockIdx.y >> 1;
-  const long long row0 = static_cast<long long>(blockIdx.x) * (G * ROWS), i0 = row0 + mine;
-  uint16_t* out = static_cast<uint16_t*>(is_v ? p.v_out : p.k_out) + 8 * u;
-  Site at[ROWS];
-  bool write[ROWS];
+  const int u = threadIdx.x % L;
+  const long long row0 = static_cast<long long>(blockIdx.x) * G, i = row0 + threadIdx.x / L;
+  size_t out0 = 8 * u;                                // of head 0's row i
+  Site at{-1, 0};
+  bool write = false;
   // What every row needs comes through shared memory: read from L2 by each warp, the lines
   // of the signs and the lengths bounded the kernel (571 us for 8 prefixes of up to 16384).
   __shared__ __align__(16) float signs[SIGNS ? D : 4];
   __shared__ int2 range_sh[kThreads];                 // of requests from `lo` on (packed)
   __shared__ int cu_sh[kThreads + 1];
   wait_for_previous_kernel();
-  if (SIGNS && !is_v && threadIdx.x < D / 4)
+  if (SIGNS && threadIdx.x < D / 4)
     *reinterpret_cast<float4*>(signs + 4 * threadIdx.x) = __ldcg(reinterpret_cast<const float4*>(p.signs) + threadIdx.x);
   if (p.cu_seqlens == nullptr) {
     const int b = blockIdx.z;
     if (threadIdx.x == kThreads - 1) range_sh[0] = range_of(p, b);
     __syncthreads();
     const int2 r = range_sh[0];
-    out += (static_cast<size_t>(b) * p.H_kv + h) * p.n * D;
-#pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-      const long long i = i0 + k * G;
-      write[k] = i < p.n;
-      at[k] = write[k] && r.y + i < r.x ? site_of(p, b, static_cast<int>(r.y + i)) : Site{-1, 0};
-    }
+    out0 += (static_cast<size_t>(b) * p.H_kv * p.n + i) * D;
+    write = i < p.n;
+    if (write && r.y + i < r.x) at = site_of(p, b, static_cast<int>(r.y + i));
   } else {
-    out += h * D;
+    out0 += static_cast<size_t>(i) * p.H_kv * D;
     // the request that owns the block's first row, by a search with all threads until
     // kThreads requests are left; those are kept
     int lo = 0, hi = p.B;
@@ -195,12 +189,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (threadIdx.x == 0) cu_sh[have] = __ldcg(p.cu_seqlens + lo + have);
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-      const long long i = i0 + k * G;
-      at[k] = {-1, 0};
-      write[k] = false;
-      if (i >= p.n) continue;
+    if (i < p.n) {
       // the last request that starts at or before row i
       int a = 0, z = have;
       while (z - a > 1) {
@@ -221,11 +210,12 @@ __global__ void __launch_bounds__(kThreads)
         c0 = __ldcg(p.cu_seqlens + b), c1 = __ldcg(p.cu_seqlens + b + 1);
         r = range_of(p, b);
       }
-      write[k] = i >= c0 && i < c1;                    // rows behind the last request stay
-      if (!write[k]) continue;
-      const long long pos = r.y + (i - c0);
-      if (pos < r.x) at[k] = site_of(p, b, static_cast<int>(pos));
-      else atomicCAS(p.status, 0, kDevBadTables);
+      write = i >= c0 && i < c1;                       // rows behind the last request stay
+      if (write) {
+        const long long pos = r.y + (i - c0);
+        if (pos < r.x) at = site_of(p, b, static_cast<int>(pos));
+        else atomicCAS(p.status, 0, kDevBadTables);
+      }
     }
     // offsets that do not fit
     if (blockIdx.x == 0 && blockIdx.y == 0)
@@ -234,54 +224,52 @@ __global__ void __launch_bounds__(kThreads)
         if (c0 < 0 || c1 < c0 || c1 > p.n || (b == 0 && c0 != 0)) atomicCAS(p.status, 0, kDevBadTables);
       }
   }
-  Raw<FORMAT> raw[ROWS];
-#pragma unroll
-  for (int k = 0; k < ROWS; ++k) {
-    raw[k] = Raw<FORMAT>{};
-    if (at[k].phys >= 0) raw[k] = load_raw<D, FORMAT>(p, is_v, h, at[k], u);
-  }
-  const long long step = p.cu_seqlens == nullptr ? D : static_cast<long long>(p.H_kv) * D;
-#pragma unroll
-  for (int k = 0; k < ROWS; ++k) {
+  const size_t head = p.cu_seqlens == nullptr ? static_cast<size_t>(p.n) * D : D;
+  const int plane0 = blockIdx.y * per, plane1 = min(plane0 + per, 2 * p.H_kv);
+  const bool some = __any_sync(0xffffffffu, at.phys >= 0);
+  Raw<FORMAT> next{};
+  if (at.phys >= 0) next = load_raw<D, FORMAT>(p, plane0 & 1, plane0 >> 1, at, u);
+  for (int plane = plane0; plane < plane1; ++plane) {
+    const bool is_v = plane & 1;
+    const Raw<FORMAT> raw = next;
+    if (at.phys >= 0 && plane + 1 < plane1) next = load_raw<D, FORMAT>(p, (plane + 1) & 1, (plane + 1) >> 1, at, u);
     uint4 a, b;
     if constexpr (FORMAT == k16) {
-      a = raw[k].a, b = raw[k].b;
-    } else if (!__any_sync(0xffffffffu, at[k].phys >= 0)) {
+      a = raw.a, b = raw.b;
+    } else if (!some) {
       a = b = make_uint4(0u, 0u, 0u, 0u);
     } else {
       float x[16];
-      widen<FORMAT>(raw[k], x);
+      widen<FORMAT>(raw, x);
       if (SIGNS && !is_v) restore_row<D>(x, signs, u);
       uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        w[i] = FP16 ? cvt_pack_f16(x[2 * i], x[2 * i + 1]) : cvt_pack_bf16(x[2 * i], x[2 * i + 1]);
+      for (int e = 0; e < 8; ++e)
+        w[e] = FP16 ? cvt_pack_f16(x[2 * e], x[2 * e + 1]) : cvt_pack_bf16(x[2 * e], x[2 * e + 1]);
       a = make_uint4(w[0], w[1], w[2], w[3]);
       b = make_uint4(w[4], w[5], w[6], w[7]);
     }
-    if (write[k]) {
-      uint4* dst = reinterpret_cast<uint4*>(out + step * (i0 + k * G));
+    if (write) {
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? p.v_out : p.k_out) + out0 + (plane >> 1) * head);
       dst[0] = a;
       dst[L] = b;
     }
   }
 }
 
-template <int D, int FORMAT, bool FP16, bool SIGNS, int ROWS>
-attn_status_t launch_rows(const CacheReadParams& p, cudaStream_t stream) {
-  constexpr int rows = kThreads / (D / 16) * ROWS;
-  const dim3 grid((p.n + rows - 1) / rows, 2 * p.H_kv, p.cu_seqlens ? 1 : p.B);
-  const cudaError_t e = launch_dependent(cache_read_kernel<D, FORMAT, FP16, SIGNS, ROWS>, grid, kThreads, 0, stream, 0, p);
-  return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "cache read kernel launch");
-}
-
-// Four rows of a thread for long ranges, one where all blocks of one run at a time (16 to an SM): a
-// prefix of 509 tokens, 8 heads 3.0 us with one, 5.0 with four; 8 of up to 16384 119 and 102.
+// A plane a block where that is one wave (16 blocks to an SM) or less, several as long as a wave is
+// left.  16,000 packed rows of 16 requests, 8 heads: a plane each 30 us, so 23.7, in half a wave 27;
+// 8 ranges of up to 16384 tokens 101 (6.0 TB/s); one of 509 tokens 3.2; e4m3, 65,536 packed rows of 4
+// heads 37.1.  Four rows of a thread instead, a plane each, took 28, 102, 5.0 and 38.6.
 template <int D, int FORMAT, bool FP16, bool SIGNS>
 attn_status_t launch_t(const CacheReadParams& p, cudaStream_t stream) {
   constexpr int rows = kThreads / (D / 16);
-  const long long blocks = ((p.n + rows - 1LL) / rows) * 2 * p.H_kv * (p.cu_seqlens ? 1 : p.B);
-  return blocks <= 152 * 16 ? launch_rows<D, FORMAT, FP16, SIGNS, 1>(p, stream) : launch_rows<D, FORMAT, FP16, SIGNS, 4>(p, stream);
+  const long long columns = (p.n + rows - 1LL) / rows, entries = p.cu_seqlens ? 1 : p.B;
+  int per = 1;
+  while (per < 2 * p.H_kv && columns * entries * 2 * p.H_kv / (2 * per) >= 152 * 16) per *= 2;
+  const dim3 grid(static_cast<unsigned>(columns), (2 * p.H_kv + per - 1) / per, static_cast<unsigned>(entries));
+  const cudaError_t e = launch_dependent(cache_read_kernel<D, FORMAT, FP16, SIGNS>, grid, kThreads, 0, stream, 0, p, per);
+  return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "cache read kernel launch");
 }
 
 template <int D, int FORMAT>
