@@ -10,7 +10,7 @@
 //    of shared memory (eight bytes of codes and a gap of eight), which kind::f8f6f4 reads as
 //    e2m1, the key tile K-major and the value tile MN-major.  Nothing is dequantised.  (The first
 //    version of this kernel converted the codes to float16 operands of mma.sync in registers, 850
-//    instructions for 32 keys: 57 us for 16 x 8192 tokens of 8 heads, where this takes @@.)
+//    instructions for 32 keys: 57 us for 16 x 8192 tokens of 8 heads, where this takes 30.)
 //  * The products run with the keys on the M side, S^T = K^ Q^T and O^T += V^^T P^T, and both
 //    the queries and the probabilities are the other operand, e4m3.  They are held as sums of
 //    several e4m3 terms, each 2^5 finer than the one before, in columns of their own (a product
@@ -19,8 +19,7 @@
 //    queries take two in bfloat16 and three in float16, which is exact, and four when they are
 //    transformed (2^-19); probabilities two for a bfloat16 result (2^-9, what bfloat16 itself
 //    would round) and three for a float16 one.
-//  * A thread holds the scores of one key (d = 64: two) for every query row: with 4 rows and
-//    128 keys that are 4 exponentials' pairs a thread, and no lane idles.
+//  * A thread holds the scores of one key (d = 64: two) for four or eight query rows, so no lane idles.
 //  * p = 2^(s - M), M a running reference of the scores; the row sums add p in float32, and what meets the
 //    codes is P' = p s^v c with c = 2^(M - T + 5), T a running reference of s + log2 s^v: it is
 //    the tokens that count for the result whose probabilities have all their bits, however the
@@ -35,7 +34,10 @@
 //    that cross shares are joined by a second, dependent kernel from float32 partial results
 //    (at most two per CTA).  With few segments a cluster of up to eight CTAs takes each instead and
 //    joins its partial results through distributed shared memory: one launch, no scratch, no prefix
-//    sums (one request of 1500 tokens, 8 heads: 10.4 us by shares, 8.0 so).
+//    sums (one request of 1500 tokens, 8 heads: 10.4 us by shares when this took 8.0; 7.4 now).
+//  * Measured: 16 x 8192 tokens, 8 heads of d = 128, 4 query rows each 29.5 us (4.8 TB/s; some 9 us
+//    are the dealing out, the first tile, the last one and the joining), 8 rows 33.3, 16 rows 51 (bound by
+//    the chain of a tile's softmax); 64 sequences of up to 16384 tokens, d = 64: 58.2 us (4.9 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -336,7 +338,6 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   wait_for_previous_kernel();
-  release_dependents();
 
   int T = 0, g0 = 0, total = 0;       // units of all, first of this CTA and its number
   int extra = 0;
@@ -415,6 +416,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  release_dependents();       // not before this CTA has its tensor memory: the next kernel may want some
   const uint32_t tmem = tmem_base_sh;
   const Abort ab{&abort_sh, p.status};
 
