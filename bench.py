@@ -44,10 +44,10 @@ WORKLOAD = "attention step (bf16 fwd + bf16 bwd + fp8 pre-pass + fp8 fwd), B=2 H
 # change, the figure no longer describes the kernel and the line reports traffic as
 # null.
 NCU_TRAFFIC = {
-    "fwd_bf16": {"bytes": 248_772_608, "src": "227dd5032ba8c2bd"},      # 201.4 MB read + 47.3 MB write
-    "bwd_bf16": {"bytes": 623_868_160, "src": "a720404894a44eca"},      # 405.7 MB read + 218.2 MB write
-    "fwd_fp8": {"bytes": 131_011_584, "src": "739b188e4c6bbb01"},       # 101.0 MB read + 30.0 MB write
-    "fp8_prepass": {"bytes": 267_818_240, "src": "739b188e4c6bbb01"},   # 201.4 MB read + 66.4 MB write
+    "fwd_bf16": {"bytes": 248_209_408, "src": "8d70bfc659620f5c"},      # 201.5 MB read + 46.7 MB write
+    "bwd_bf16": {"bytes": 622_810_112, "src": "4b76974f6904bef6"},      # 404.9 MB read + 217.9 MB write
+    "fwd_fp8": {"bytes": 130_534_144, "src": "c403ecab8e58b72b"},       # 100.7 MB read + 29.8 MB write
+    "fp8_prepass": {"bytes": 267_815_680, "src": "c403ecab8e58b72b"},   # 201.4 MB read + 66.4 MB write
 }
 KERNEL_SOURCES = {"fwd_bf16": "fwd.cu", "bwd_bf16": "bwd.cu", "fwd_fp8": "fp8.cu",
                   "fp8_prepass": "fp8.cu"}
