@@ -144,6 +144,30 @@ def test_append_shapes(attn, total, H, H_kv, page):
     _append_case(attn, 2, total, H, H_kv, 128, page, torch.bfloat16, 64, False, True)
 
 
+@pytest.mark.parametrize("d,rot,interleaved,signs", [(64, 32, False, True), (128, 128, False, True), (128, 128, True, False)])
+def test_append_of_many_rows_is_that_of_few(attn, d, rot, interleaved, signs):
+    """A block of a long append walks over several heads, one of a short append over a single one: the same bits."""
+    total, H, H_kv, page, pages = 12000, 4, 5, 64, 200
+    k, v = (torch.randn(total, H_kv, d, device=dev()).bfloat16() for _ in range(2))
+    q = torch.randn(total, H, d, device=dev()).bfloat16()
+    slots = torch.randperm(pages * page, device=dev())[:total]
+    slots[5::97] = -1
+    pos = torch.randint(0, 500, (total,), device=dev(), dtype=torch.int32)
+    cos, sin = attn.attn_rope_table(500, rot)
+    kw = dict(hadamard_signs=_signs(d) if signs else None, interleaved=interleaved)
+    got = []
+    for step in (total, 100):
+        cache = [torch.full((pages, H_kv, page, d // 2), 0x55, dtype=torch.uint8, device=dev()) for _ in range(2)]
+        des = [torch.ones(pages, H_kv, page, device=dev()).bfloat16() for _ in range(2)]
+        qs = []
+        for a in range(0, total, step):
+            at = slice(a, a + step)
+            qs.append(attn.attn_cache_append_fp4(k[at], v[at], *cache, *des, slots[at], cos, sin, pos[at], q=q[at], **kw))
+        got.append((*cache, *des, torch.cat(qs)))
+    check_status(attn)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_append_of_rows_that_have_no_scale(attn):
     """Zeros, the smallest and the largest values, infinities and NaN: each row by itself."""
     d, H_kv, page = 128, 2, 16
@@ -495,6 +519,35 @@ def test_read_other_caches(attn, bits, d):
         _close_rows(got, want, dtype, s is None)
         want = undo(np.concatenate(oracle.read_cache(val, table, lens, [40, 0, 0, 0], [30, 1, 0, 33])))
         _close_rows(packed[:64], want, dtype, s is None)
+
+
+@pytest.mark.parametrize("bits,d", [(16, 64), (16, 256), (8, 128), (4, 64), (4, 128)])
+def test_read_of_many_rows_is_that_of_few(attn, bits, d):
+    """A block of a long range takes several planes (keys and values of 5 heads: not a multiple of them), one
+    of a short range a single one: the same bits, padded and packed."""
+    lens, page, H_kv, n = [9000, 0, 7001], 32, 5, 9000
+    if bits == 4:
+        c = Cache(35, lens, page, H_kv, d)
+        args, kw, call = c.args(), dict(hadamard_signs=_signs(d)), attn.attn_cache_read_fp4
+    else:
+        rng = np.random.default_rng(36)
+        table, pages = _table(rng, lens, page)
+        shape = (pages, page, H_kv, d)
+        kc, vc = (torch.randn(shape, device=dev()).bfloat16() if bits == 16 else
+                  torch.randint(0, 120, shape, device=dev(), dtype=torch.uint8) for _ in range(2))
+        scales = [torch.rand(pages, H_kv, device=dev()) + 0.5 for _ in range(2)] if bits == 8 else []
+        args = (kc, vc, *scales, _i32(table), _i32(lens))
+        kw, call = (dict(hadamard_signs=_signs(d)), attn.attn_cache_read_fp8) if bits == 8 else ({}, attn.attn_cache_read)
+    k, v = call(*args, n, **kw)
+    for at in (0, 4000, 7000, 8970):
+        few = call(*args, 30, first=_i32([at] * 3), **kw)
+        assert torch.equal(k[:, :, at:at + 30], few[0]) and torch.equal(v[:, :, at:at + 30], few[1])
+    assert torch.all(k[1] == 0) and torch.all(v[2, :, 7001:] == 0) and torch.any(v[0, :, 8999] != 0)
+    cu = _i32(np.concatenate([[0], np.cumsum(lens)]))
+    kp, vp = call(*args, sum(lens), cu_seqlens=cu, **kw)
+    check_status(attn)
+    for packed, padded in ((kp, k), (vp, v)):
+        assert torch.equal(packed[:9000], padded[0].transpose(0, 1)) and torch.equal(packed[9000:], padded[2, :, :7001].transpose(0, 1))
 
 
 def test_read_reports_what_does_not_fit(attn):
