@@ -1138,17 +1138,21 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_merge_kernel(const K
 }
 
 // CTAs of the cluster that takes a segment, or 0: all segments' tiles dealt out in one line.  The
-// smaller modelled time, in microseconds: a start, the tiles of one CTA, and the joining (the line's
-// second kernel); clusters only as far as all of them run at a time (with one CTA to an SM and
-// with two: a multiprocessor group's SMs are not a multiple of every size).
+// smaller modelled time, in microseconds, fitted to 4 and 16 rows of d = 128, 1 to 32 sequences of 500 to
+// 16384 tokens: a start and an end, the tiles of one CTA (less with an SM to itself), and for the line
+// the joining of a segment's CTAs (of 34 shapes one took 11 % more than the other way, the rest at
+// most 4).  One sequence of 4096 tokens, 8 heads: 8.5 by clusters, 12.3 in line; of 16384 14.7 and 15.9;
+// 16 of 8192 in line 29.5.  Clusters only as far as all of them run at a time (with one CTA to an SM
+// and with two: a multiprocessor group's SMs are not a multiple of every size).
 inline int cluster_of(int B, int segs, int tiles, int per_sm) {
   constexpr int at_a_time[2][9] = {{0, 152, 76, 46, 36, 28, 23, 15, 15}, {0, 304, 152, 97, 74, 58, 46, 38, 36}};
-  const double n = static_cast<double>(B) * segs, line = 3.0 + 0.6 * std::ceil(n * tiles / (152.0 * per_sm));
+  const double n = static_cast<double>(B) * segs, ctas = 152.0 * per_sm, tile = per_sm == 1 ? 0.9 : 0.7;
   int best = 0;
-  double least = line;
+  double least = 8.6 + tile * std::ceil(n * tiles / ctas) + 0.1 * std::min<double>(tiles, ctas / n);
   for (int c = 1; c <= 8; ++c) {
     if (n > at_a_time[per_sm - 1][c]) break;
-    const double t = 0.7 + 0.6 * ((tiles + c - 1) / c);
+    const double each = per_sm == 1 ? 0.9 : n * c <= 152 ? 0.52 : 0.8;
+    const double t = (per_sm == 1 ? 7.0 : 6.3) + each * ((tiles + c - 1) / c);
     if (t < least) {
       least = t;
       best = c;
