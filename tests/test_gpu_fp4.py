@@ -404,12 +404,12 @@ def test_decode_offsets_beyond_32_bits(attn):
     assert torch.equal(big[0][-1, :, -1], big[1][-1, :, -1]) and torch.isfinite(des[0][-1, :, -1].float()).all()
 
 
-def test_decode_runs_alike_in_graphs_on_other_streams_and_again(attn):
+@pytest.mark.parametrize("lens", [[3000, 17, 0, 900], [3000, 0, *range(5, 3000, 31)]], ids=["clusters", "shares"])
+def test_decode_runs_alike_in_graphs_on_other_streams_and_again(attn, lens):
     """The same bits from a second call, from another stream and from two captured graphs that
     replay at the same time, each with its own workspace."""
-    lens = [3000, 17, 0, 900]
     c = Cache(25, lens, 32, 2, 128)
-    q = torch.randn(4, 8, 1, 128, device=dev()).bfloat16()
+    q = torch.randn(len(lens), 8, 1, 128, device=dev()).bfloat16()
     args, sg = c.args(), _signs(128)
     ref = attn.attn_decode_paged_fp4(q, *args, 3000, hadamard_signs=sg)
     side = torch.cuda.Stream()
