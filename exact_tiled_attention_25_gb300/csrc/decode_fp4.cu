@@ -876,7 +876,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
             for (int e = 0; e < NRW; e += 2) {
               const uint64_t a = fadd2(pack2(s[h][e], s[h][e + 1]), pack2(mm[e], mm[e + 1]));
               pr[h][e / 2] = pack2(ex2_approx(lo2(a)), ex2_approx(hi2(a)));
-              pv[h][e / 2] = fmul2(pr[h][e / 2], fmul2(pack2(c[e], c[e + 1]), pack2(sv[h], sv[h])));
+              // (c s^v may overflow where p is 0; p s^v, once p is 1 at most, does not)
+              pv[h][e / 2] = fmul2(fmul2(pr[h][e / 2], pack2(sv[h], sv[h])), pack2(c[e], c[e + 1]));
               need |= fmaxf(lo2(pv[h][e / 2]), hi2(pv[h][e / 2])) > kPTop || fmaxf(lo2(a), hi2(a)) > 64.f;
             }
         };

@@ -339,6 +339,73 @@ def test_decode_value_descales_that_differ(attn):
     _decode_case(attn, lens, 16, 4, 2, 1, 128, cache=c)
 
 
+def _one_hot(c, lens, d, n_heads, dtype, size, n_q=1, signs=None):
+    """Makes one key of each request and head the only one with a component of 6 in column 0, the others have
+    none there, and returns queries of `size` in that column (transformed ones where signs are given) and that
+    key's position: every other key's score is `size` x 6 x its descale lower."""
+    c.codes[0][..., 0] &= 0xF0
+    at = [n // 2 for n in lens]
+    for b, t in enumerate(at):
+        if lens[b]:
+            c.codes[0][c.table[b, t // c.page], :, t % c.page, 0] |= 7
+            c.descale[0][c.table[b, t // c.page], :, t % c.page] = 1
+    q = torch.zeros(len(lens), n_heads, n_q, d, device=dev())
+    if signs is None:
+        q[..., 0] = size
+    else:
+        q[:] = size / np.sqrt(d) * signs
+    return q.to(dtype), at
+
+
+SHAPES = [([300, 40, 1000, 1], 2), (list(range(3, 550, 6)), 4)]        # by clusters; by shares (92 sequences, 4 heads)
+TYPES = [(64, torch.bfloat16), (128, torch.bfloat16), (128, torch.float16)]
+
+
+@pytest.mark.parametrize("lens,H_kv", SHAPES, ids=["clusters", "shares"])
+@pytest.mark.parametrize("G", [1, 8, 16])
+@pytest.mark.parametrize("d,dtype", TYPES)
+def test_decode_large_values_of_far_lower_scores(attn, lens, H_kv, G, d, dtype):
+    """The key with the largest score has values of zero, the others (196 or more below in powers of two) large
+    ones: their weights are 0, whatever the values are."""
+    c = Cache(51, lens, 16, H_kv, d)
+    c.descale[1] = np.where(c.owned, np.float32(1024), c.descale[1])
+    q, at = _one_hot(c, lens, d, G * H_kv, dtype, 256.0)
+    for b, t in enumerate(at):
+        c.descale[1][c.table[b, t // 16], :, t % 16] = 0
+    _decode_case(attn, lens, 16, G * H_kv, H_kv, 1, d, cache=c, q=q)
+
+
+@pytest.mark.parametrize("lens,H_kv", SHAPES, ids=["clusters", "shares"])
+@pytest.mark.parametrize("G", [1, 2, 4])
+@pytest.mark.parametrize("d,dtype", TYPES)
+def test_decode_large_values_of_unseen_tokens(attn, lens, H_kv, G, d, dtype):
+    """The first query tokens see values of zero only, the last ones large values too."""
+    c = Cache(52, lens, 16, H_kv, d)
+    for b, n in enumerate(lens):
+        at = np.arange(n)
+        c.descale[1][c.table[b][at // 16], :, at % 16] = np.where(at < n - 2, 0, np.where(at < n - 1, 0.25, 1024))[:, None]
+    q = torch.from_numpy(workloads.normal(53, (len(lens), G * H_kv, 4, d))).to(dev(), dtype)
+    _, _, o, _ = _decode_case(attn, lens, 16, G * H_kv, H_kv, 4, d, cache=c, q=q)
+    assert torch.all(o[:, :, :2] == 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_value_descales_130_powers_of_two_apart(attn, d):
+    """The key that has all the weight has the smallest descale: O is its row, exact but for the last e4m3
+    term, the factors' and the output's rounding."""
+    lens, dtype = [300, 40, 1000, 1], torch.bfloat16
+    c = Cache(54, lens, 16, 2, d)
+    c.descale[1] = np.where(c.owned, np.float32(2.0 ** 30), c.descale[1])
+    q, at = _one_hot(c, lens, d, 4, dtype, 256.0)
+    for b, t in enumerate(at):
+        c.descale[1][c.table[b, t // 16], :, t % 16] = 2.0 ** -100
+    o, lse = attn.attn_decode_paged_fp4(q, *c.args(), 1000)
+    check_status(attn)
+    v = c.values()[1]
+    want = np.stack([np.repeat(v[c.table[b, t // 16], t % 16], 2, 0) for b, t in enumerate(at)])[:, :, None]
+    assert np.all(np.abs(_np(o) - want) <= (PROB[dtype] + 2.0 ** -16 + HALF[dtype]) * np.abs(want))
+
+
 def test_decode_nan_rows_show(attn):
     lens = [300, 40]
     for which in (0, 1):
