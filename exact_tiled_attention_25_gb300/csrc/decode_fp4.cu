@@ -200,6 +200,13 @@ __device__ __forceinline__ float warp_sums(float (&v)[N], int lane, int* which) 
   return v[0];
 }
 
+// Rows that see a key (it stands before their ends) get this mark.  Not inlined: unrolled within the
+// softmax it cost 16 query rows 4 % (16 x 8192 tokens 50.5 -> 52.5 us; so 51.0).
+__device__ __noinline__ void mark_nan(int* marks, const unsigned* ends, unsigned key, int rows, int mark) {
+  for (int e = 0; e < rows; ++e)
+    if (key < ends[e]) marks[e] = mark;
+}
+
 // Tokens of a sequence; a count out of range is none.
 __device__ __forceinline__ int tokens_of(const KParams& p, int b) {
   const int n = __ldcg(p.seq_lens + b);
@@ -303,6 +310,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   __shared__ float2 ref_sh[2][NR];                       // c and -M at its end,
   __shared__ __align__(16) float l_sh[2][NR][4];         // sums by key quarter
   __shared__ __align__(16) float red_sh[2][2][NR][4];    // maxima of a tile (by parity) by key quarter
+  // part + 1 where a row sees a NaN among the values that not all rows see.  (Of four parts: a warp may be in the
+  // part after the next while another still writes one out.)
+  __shared__ int nan_sh[4][NR];
   __shared__ float part_lse[NR];                         // of the partial results of a cluster's CTA
   __shared__ float xch_sh[KP == 2 ? NR : 1][KP == 2 ? 64 : 1];
 
@@ -336,6 +346,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
   // columns that no row of queries or of P' fills stay zero
   for (int i = threadIdx.x; i < (C::Q_BYTES + C::PB * C::P_TILE) / 16; i += C::THREADS)
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (threadIdx.x < 4 * NR) nan_sh[0][threadIdx.x] = 0;
   fence_proxy_async_smem();
   wait_for_previous_kernel();
 
@@ -750,8 +761,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         const float4 l4 = *reinterpret_cast<const float4*>(l_sh[buf][mine]);
         const float l = ((l4.x + l4.y) + l4.z) + l4.w;
         const float2 ref = ref_sh[buf][mine];
-        // (a NaN among the scores or descales is in o by now, and stays)
-        const float f = l == 0.f ? 0.f : __fdividef(__fdividef(1.f, ref.x), l);     // (all below 2^126)
+        // (a NaN among the scores or the descales that all rows see is in o by now, and stays)
+        const float f = nan_sh[done.part & 3][mine] == done.part + 1 ? __uint_as_float(0x7FFFFFFFu)
+                        : l == 0.f                                   ? 0.f
+                                                                     : __fdividef(__fdividef(1.f, ref.x), l);   // (all below 2^126)
         const float lse = l == 0.f ? -INFINITY : (lg2(l) - ref.y) * 0.69314718055994530942f;
         // (a cluster's partial results: in its ring's place, which is free by then)
         const size_t at = done.whole ? done.at0 : p.cluster > 0 ? 0 : (2ull * blockIdx.x + (done.part > 0 ? 1 : 0)) * p.seg_rows;
@@ -859,6 +872,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
           if (!open) {
             // (a slot without a token may hold any descale)
             if (!there || key0 + h >= static_cast<unsigned>(len)) sv[h] = 0.f;
+            // 0 times NaN is NaN: of a token that only some rows see, NaN goes to those when they are written
+            if (__builtin_expect(key0 + h >= vis_all && sv[h] != sv[h], 0)) {
+              mark_nan(&nan_sh[part & 3][r0], &vend_sh[part & 1][r0], key0 + h, NRW, part + 1);
+              sv[h] = 0.f;
+            }
 #pragma unroll
             for (int e = 0; e < NRW; ++e) {
               const bool seen = there && key0 + h < vend_sh[part & 1][r0 + e];

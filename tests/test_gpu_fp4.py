@@ -406,6 +406,28 @@ def test_decode_value_descales_130_powers_of_two_apart(attn, d):
     assert np.all(np.abs(_np(o) - want) <= (PROB[dtype] + 2.0 ** -16 + HALF[dtype]) * np.abs(want))
 
 
+@pytest.mark.parametrize("lens,H_kv", SHAPES, ids=["clusters", "shares"])
+@pytest.mark.parametrize("G", [1, 2, 4])
+@pytest.mark.parametrize("d,dtype", TYPES)
+def test_decode_nan_values_of_unseen_tokens(attn, lens, H_kv, G, d, dtype):
+    """The last token's value rows are NaN: only the last query token, which sees it, shows that."""
+    lens = [*lens, 2]                    # (the first two of four query tokens see nothing)
+    c = Cache(55, lens, 16, H_kv, d)
+    q = torch.from_numpy(workloads.normal(56, (len(lens), G * H_kv, 4, d))).to(dev(), dtype)
+    got = []
+    for last in (0.0, np.nan):
+        for b, n in enumerate(lens):
+            c.descale[1][c.table[b, (n - 1) // 16], :, (n - 1) % 16] = last
+        got.append(attn.attn_decode_paged_fp4(q, *c.args(), max(lens)))
+        if last == 0:
+            ref = _decode_ref(q, c, True, None, 1 / np.sqrt(d))
+    check_status(attn)
+    _check_decode(q, *got[0], ref)
+    assert torch.isnan(got[1][0][:, :, 3].float()).all()
+    got[1][0][:, :, 3] = got[0][0][:, :, 3]
+    _check_decode(q, *got[1], ref)
+
+
 def test_decode_nan_rows_show(attn):
     lens = [300, 40]
     for which in (0, 1):
