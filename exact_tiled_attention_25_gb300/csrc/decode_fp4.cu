@@ -655,12 +655,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
 #pragma unroll
         for (int m = 1; m < L; m <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-        // times 2^(7 - floor(log2 top)); a row with an infinity or a NaN gets a coefficient of NaN
+        // times f = 2^(7 - floor(log2 top)), at most 2^126, so that 1 / f is a normal number too; a row with an
+        // infinity or a NaN gets a coefficient of NaN
         const int e = static_cast<int>(top >> 23);
-        const int up = top == 0u ? 127 : min(261 - e, 254);
+        const int up = top == 0u ? 127 : min(261 - e, 253);
         const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
-        const float back = e == 255 ? __uint_as_float(0x7FFFFFFFu)
-                                    : __uint_as_float(static_cast<uint32_t>(max(254 - up, 1)) << 23);
+        const float back = e == 255 ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] *= f;
 #pragma unroll

@@ -325,6 +325,18 @@ def test_decode_scales_of_queries(attn, factor, signs):
     _decode_case(attn, [40, 333, 1000], 16, 4, 2, 1, 128, q=q, signs=signs)
 
 
+@pytest.mark.parametrize("exponent", [-118, -121, -125])
+@pytest.mark.parametrize("signs", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_tiny_queries_and_large_keys(attn, exponent, signs, d):
+    """Queries near the smallest normal number and keys as much above 1: ordinary scores."""
+    lens = [40, 333, 1000]
+    c = Cache(57, lens, 16, 2, d)
+    c.descale[0] = c.descale[0] * np.float32(2.0 ** -exponent)
+    q = torch.from_numpy(workloads.normal(58, (3, 4, 1, d)) * 2.0 ** exponent).to(dev(), torch.bfloat16)
+    _decode_case(attn, lens, 16, 4, 2, 1, d, cache=c, q=q, signs=signs)
+
+
 def test_decode_value_descales_that_differ(attn):
     """Rows of values of 0, of 2^-90 and of 2^60 beside ordinary ones, wherever they stand."""
     lens = [5, 200, 900]
