@@ -628,8 +628,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
         if constexpr (SIGNS) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
+            // of x / d, so that the sums stay in range, and sqrt(d) at their end: the same bits
             const float4 s = sgn[i / 4];
-            x[i] *= s.x, x[i + 1] *= s.y, x[i + 2] *= s.z, x[i + 3] *= s.w;
+            const uint64_t down = pack2(1.f / D, 1.f / D);
+            const uint64_t a = fmul2(fmul2(pack2(x[i], x[i + 1]), pack2(s.x, s.y)), down);
+            const uint64_t b = fmul2(fmul2(pack2(x[i + 2], x[i + 3]), pack2(s.z, s.w)), down);
+            x[i] = lo2(a), x[i + 1] = hi2(a), x[i + 2] = lo2(b), x[i + 3] = hi2(b);
           }
 #pragma unroll
           for (int h = 1; h < 16; h <<= 1)
@@ -646,9 +650,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, TQ, TP>::THREADS, Cfg<D, NR, TQ, TP
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = fmaf(minus, x[i], __shfl_xor_sync(0xffffffffu, x[i], m));
           }
-          const float isd = D == 128 ? 0.08838834764831845f : 0.125f;
+          const float root = D == 128 ? 11.313708498984761f : 8.f;      // sqrt(d)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] *= isd;
+          for (int i = 0; i < 16; ++i) x[i] *= root;
         }
         uint32_t top = 0u;
 #pragma unroll

@@ -337,6 +337,22 @@ def test_decode_tiny_queries_and_large_keys(attn, exponent, signs, d):
     _decode_case(attn, lens, 16, 4, 2, 1, d, cache=c, q=q, signs=signs)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_transforms_large_queries(attn, d):
+    """Queries of up to 2^127: the transform's sums stay in range.  All else is a power of two away: the same bits."""
+    lens = [40, 333, 1000]
+    c = Cache(59, lens, 16, 2, d)
+    q = torch.from_numpy(workloads.normal(60, (3, 4, 2, d))).to(dev(), torch.bfloat16)
+    got = []
+    for up, down in ((1.0, 1.0), (2.0 ** 125, 2.0 ** -100)):
+        kc, vc, kd, vd, bt, n = c.args()
+        got.append(attn.attn_decode_paged_fp4(q * up, kc, vc, kd * down, vd, bt, n, 1000, hadamard_signs=_signs(d),
+                                              softmax_scale=1 / np.sqrt(d) / (up * down)))
+    check_status(attn)
+    assert torch.isfinite(got[0][0].float()).all()
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def test_decode_value_descales_that_differ(attn):
     """Rows of values of 0, of 2^-90 and of 2^60 beside ordinary ones, wherever they stand."""
     lens = [5, 200, 900]
