@@ -125,12 +125,13 @@ __device__ __forceinline__ void rotate_row(float (&x)[16], const Turn& t, int ro
 }
 
 // x -> (x o signs) H_d / sqrt(d), stages by span: 1, 2, 4 in the lane, 8 .. d / 4 across lanes,
-// d / 2 in the lane.
-template <int D>
-__device__ __forceinline__ void transform_row(float (&x)[16], const float* signs, int u) {
+// d / 2 in the lane.  The sums are of x / d, in range for every x, and sqrt(d) comes last; a
+// power of two either way, so the bits are those of the plain formula.
+template <int D>      // signs_d: signs / d
+__device__ __forceinline__ void transform_row(float (&x)[16], const float* signs_d, int u) {
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
-    const float4 s = *reinterpret_cast<const float4*>(signs + (i < 8 ? 0 : D / 2 - 8) + 8 * u + i);
+    const float4 s = *reinterpret_cast<const float4*>(signs_d + (i < 8 ? 0 : D / 2 - 8) + 8 * u + i);
     x[i] *= s.x, x[i + 1] *= s.y, x[i + 2] *= s.z, x[i + 3] *= s.w;
   }
 #pragma unroll
@@ -148,12 +149,12 @@ __device__ __forceinline__ void transform_row(float (&x)[16], const float* signs
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = fmaf(sgn, x[i], __shfl_xor_sync(0xffffffffu, x[i], m));
   }
-  const float scale = D == 128 ? 0.08838834764831845f : 0.125f;
+  const float root = D == 128 ? 11.313708498984761f : 8.f;      // sqrt(d)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float a = x[i], b = x[8 + i];
-    x[i] = (a + b) * scale;
-    x[8 + i] = (a - b) * scale;
+    x[i] = (a + b) * root;
+    x[8 + i] = (a - b) * root;
   }
 }
 
@@ -187,10 +188,12 @@ __device__ __forceinline__ void append_block(const AppendFp4Params& p, long long
       if (turn) load_turn<D, MODE>(tab, p, static_cast<size_t>(pos) * (p.rot / 2), u);
     }
   }
-  __shared__ __align__(16) float signs[SIGNS ? D : 4];
+  __shared__ __align__(16) float signs_d[SIGNS ? D : 4];
   if (SIGNS && !is_v) {
-    if (threadIdx.x < D / 4)
-      *reinterpret_cast<float4*>(signs + 4 * threadIdx.x) = __ldcg(reinterpret_cast<const float4*>(p.signs) + threadIdx.x);
+    if (threadIdx.x < D / 4) {
+      const float4 s = __ldcg(reinterpret_cast<const float4*>(p.signs) + threadIdx.x);
+      *reinterpret_cast<float4*>(signs_d + 4 * threadIdx.x) = make_float4(s.x / D, s.y / D, s.z / D, s.w / D);
+    }
     __syncthreads();
   }
   const int h0 = chunk * per, h1 = min(h0 + per, p.H_kv);
@@ -220,7 +223,7 @@ __device__ __forceinline__ void append_block(const AppendFp4Params& p, long long
     load(h + 1);
     if (!is_v) {                                       // the same for the whole block
       rotate_row<D, MODE>(x, tab, p.rot, turn, u);
-      if constexpr (SIGNS) transform_row<D>(x, signs, u);
+      if constexpr (SIGNS) transform_row<D>(x, signs_d, u);
     }
     uint32_t top = 0u;
 #pragma unroll

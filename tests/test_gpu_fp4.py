@@ -168,6 +168,28 @@ def test_append_of_many_rows_is_that_of_few(attn, d, rot, interleaved, signs):
     assert all(torch.equal(a, b) for a, b in zip(*got))
 
 
+@pytest.mark.parametrize("d,rot", [(64, None), (64, 48), (128, 128)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_transforms_large_keys(attn, d, rot, interleaved):
+    """Keys of up to 2^126: the transform's sums stay in range.  The codes of rows a power of two smaller, and
+    that power in the descales."""
+    k = torch.from_numpy(workloads.normal(43, (20, 2, d))).to(dev(), torch.bfloat16)
+    kw = {}
+    if rot:
+        cos, sin = attn.attn_rope_table(32, rot)
+        kw = dict(rope_cos=cos, rope_sin=sin, positions=torch.arange(20, device=dev(), dtype=torch.int32), interleaved=interleaved)
+    got = []
+    for x in (k, k * 2.0 ** 124):
+        c = [torch.zeros(2, 2, 16, d // 2, dtype=torch.uint8, device=dev()) for _ in range(2)]
+        s = [torch.zeros(2, 2, 16, device=dev()).bfloat16() for _ in range(2)]
+        attn.attn_cache_append_fp4(x, x, *c, *s, torch.arange(20, device=dev()), hadamard_signs=_signs(d), **kw)
+        got.append((c, s))
+    check_status(attn)
+    (c0, s0), (c1, s1) = got
+    assert torch.any(s0[0] != 0) and all(torch.equal(a, b) for a, b in zip(c0, c1))
+    assert all(torch.equal(a * 2.0 ** 124, b) for a, b in zip(s0, s1))
+
+
 def test_append_of_rows_that_have_no_scale(attn):
     """Zeros, the smallest and the largest values, infinities and NaN: each row by itself."""
     d, H_kv, page = 128, 2, 16
