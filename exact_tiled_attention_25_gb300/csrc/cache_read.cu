@@ -110,7 +110,8 @@ __device__ __forceinline__ void widen(const Raw<FORMAT>& r, float (&x)[16]) {
   }
 }
 
-// (x H_d / sqrt(d)) o signs: spans 1, 2, 4 in the lane, 8 .. d / 4 across lanes, d / 2 in the lane.
+// (x H_d / sqrt(d)) o signs of x / d, whose sums are in range for every x (a power of two: the
+// same bits): spans 1, 2, 4 in the lane, 8 .. d / 4 across lanes, d / 2 in the lane.
 template <int D>
 __device__ __forceinline__ void restore_row(float (&x)[16], const float* signs, int u) {
 #pragma unroll
@@ -128,7 +129,7 @@ __device__ __forceinline__ void restore_row(float (&x)[16], const float* signs, 
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = fmaf(sgn, x[i], __shfl_xor_sync(0xffffffffu, x[i], m));
   }
-  const float scale = D == 128 ? 0.08838834764831845f : 0.125f;
+  const float root = D == 128 ? 11.313708498984761f : 8.f;      // sqrt(d)
 #pragma unroll
   for (int i = 0; i < 8; i += 4) {
     const float4 s = *reinterpret_cast<const float4*>(signs + 8 * u + i);
@@ -137,8 +138,8 @@ __device__ __forceinline__ void restore_row(float (&x)[16], const float* signs, 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float a = x[i + e], b = x[8 + i + e];
-      x[i + e] = (a + b) * (scale * sv[e]);
-      x[8 + i + e] = (a - b) * (scale * rv[e]);
+      x[i + e] = (a + b) * (root * sv[e]);
+      x[8 + i + e] = (a - b) * (root * rv[e]);
     }
   }
 }
@@ -240,7 +241,9 @@ __global__ void __launch_bounds__(kThreads)
       a = b = make_uint4(0u, 0u, 0u, 0u);
     } else {
       float x[16];
-      widen<FORMAT>(raw, x);
+      Raw<FORMAT> part = raw;
+      if (SIGNS && !is_v) part.s /= D;
+      widen<FORMAT>(part, x);
       if (SIGNS && !is_v) restore_row<D>(x, signs, u);
       uint32_t w[8];
 #pragma unroll

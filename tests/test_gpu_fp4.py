@@ -627,6 +627,29 @@ def test_read_fp4(attn, d, page, signs, dtype):
         assert torch.all(got[cu[-1]:] == -7.0)
 
 
+@pytest.mark.parametrize("bits,d", [(4, 64), (4, 128), (8, 128)])
+def test_read_restores_large_keys(attn, bits, d):
+    """Keys of up to 2^127: the transform's sums stay in range.  All is a power of two larger, the same bits."""
+    lens, page = [70, 1, 33], 16
+    if bits == 4:
+        c = Cache(44, lens, page, 2, d)
+        c.descale = [np.nan_to_num(s) for s in c.descale]
+        kc, vc, kd, vd, bt, n = c.args()
+        read = attn.attn_cache_read_fp4
+    else:
+        rng = np.random.default_rng(45)
+        table, num = _table(rng, lens, page)
+        (kc, kd), (vc, vd) = (oracle.quantize_paged_cache(rng.standard_normal((num, page, 2, d)).astype(np.float32)) for _ in range(2))
+        kc, kd, vc, vd = (torch.from_numpy(np.ascontiguousarray(x)).to(dev()) for x in (kc, kd, vc, vd))
+        bt, n, read = _i32(table), _i32(lens), attn.attn_cache_read_fp8
+    k, v = read(kc, vc, kd, vd, bt, n, 70, hadamard_signs=_signs(d))
+    up = 2.0 ** 125
+    big_k, big_v = read(kc, vc, kd * up, vd * up, bt, n, 70, hadamard_signs=_signs(d))
+    check_status(attn)
+    assert torch.isfinite((k * up).float()).all() and torch.any(k != 0)
+    assert torch.equal(k * up, big_k) and torch.equal(v * up, big_v)
+
+
 @pytest.mark.parametrize("bits", [16, 8])
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_read_other_caches(attn, bits, d):
