@@ -1146,6 +1146,22 @@ static attn_status_t cache_read(const void* k_cache, const void* v_cache, const 
   if ((s = check_ints({block_table, seq_lens})) != ATTN_OK) return s;
   if (first && (s = check_ints({first})) != ATTN_OK) return s;
   if (cu_seqlens && (s = check_ints({cu_seqlens})) != ATTN_OK) return s;
+  // blocks read the caches and the rest while others write
+  const size_t rows = static_cast<size_t>(num_pages) * page_size * H_kv, out_bytes = (cu_seqlens ? 1ull : B) * n * H_kv * d * 2;
+  const size_t scales = bits == 16 ? 0 : bits == 8 ? 4ull * num_pages * H_kv : 2 * rows, b4 = 4 * static_cast<size_t>(B);
+  struct Range {
+    const void* p;
+    size_t bytes;
+  };
+  const Range all[] = {{k_out, out_bytes}, {v_out, out_bytes}, {k_cache, rows * d * bits / 8}, {v_cache, rows * d * bits / 8},
+                       {k_descale, scales}, {v_descale, scales}, {signs, signs ? 4ull * d : 0}, {block_table, b4 * max_pages},
+                       {seq_lens, b4}, {first, first ? b4 : 0}, {cu_seqlens, cu_seqlens ? b4 + 4 : 0}};
+  for (int i = 0; i < 2; ++i)
+    for (int k = i + 1; k < 11; ++k) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(all[i].p), y = reinterpret_cast<uintptr_t>(all[k].p);
+      if (all[i].bytes > 0 && all[k].bytes > 0 && x < y + all[k].bytes && y < x + all[i].bytes)
+        return fail(ATTN_ERR_INVALID_ARG, "k_out and v_out must not overlap each other or the inputs");
+    }
   if ((s = check_device()) != ATTN_OK) return s;
   if (n == 0) return ATTN_OK;
   return launch_cache_read({k_cache, v_cache, k_descale, v_descale, signs, block_table, seq_lens, first, cu_seqlens,

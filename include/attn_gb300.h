@@ -849,7 +849,8 @@ attn_status_t attn_decode_paged_fp4(const void* q, const uint8_t* k_cache, const
  *                    cu_seqlens[b] + i is position first[b] + i; rows behind the last
  *                    request stay as they are.
  *   k_out, v_out   : in `dtype` (16-bit cache: the cache's).  Code x descale is formed in
- *                    float32 and rounded once.
+ *                    float32 and rounded once.  They overlap neither each other nor an
+ *                    input.
  * Lengths, offsets or first positions that do not fit, packed rows behind a sequence's end
  * and pages outside the cache are written as zeros (rows that no request owns are left) and
  * reported by attn_get_device_status() as ATTN_ERR_INVALID_ARG.

@@ -96,6 +96,26 @@ def test_read_refusals_of_quantised_caches(lib):
         assert _read(lib, bits, ps=8) == 1 and b"page_size" in lib.attn_last_error()
 
 
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_read_refuses_outputs_that_overlap(lib, bits):
+    """Each other or an input, in part too: blocks read while others write.  (Sizes: caches of 9 x 16 x 2
+    rows, outputs of 2 x 2 x 10 rows of 256 bytes, 10 x 2 rows packed.)"""
+    far = dict(kc=1 << 20, vc=2 << 20, kd=3 << 20, vd=4 << 20, sg=5 << 20, bt=6 << 20, sl=7 << 20, first=8 << 20, cu=0,
+               ko=10 << 20, vo=11 << 20)
+    cache = 9 * 16 * 2 * 128 * bits // 8
+    out = 2 * 2 * 10 * 256
+    cases = [dict(ko=far["vo"]), dict(ko=far["vo"] - out + 16), dict(vo=far["ko"] + out - 16), dict(ko=far["kc"]),
+             dict(vo=far["kc"] + cache - 16), dict(ko=far["vc"] - out + 16), dict(vo=far["vc"] + 4096), dict(ko=far["bt"] + 16),
+             dict(vo=far["bt"] - out + 16), dict(ko=far["sl"]), dict(vo=far["first"] - 16),
+             dict(cu=9 << 20, ko=9 << 20), dict(cu=9 << 20, vo=(9 << 20) - out // 2 + 16)]
+    if bits < 16:
+        scales = 9 * 2 * 4 if bits == 8 else 9 * 16 * 2 * 2
+        cases += [dict(ko=far["kd"] + (scales - 1) // 16 * 16), dict(vo=far["vd"] - 16), dict(ko=far["sg"] + 496)]
+    for case in cases:
+        assert _read(lib, bits, **{**far, **case}) == 1, case
+        assert "overlap" in lib.attn_last_error().decode(), case
+
+
 def _merge(lib, oa=0x10000, la=0x20000, ob=0x30000, lb=0x40000, o=0x50000, l=0x60000, B=1, H=2, N=8, d=128, packed=0, dt=0):
     return lib.attn_merge(oa, la, ob, lb, o, l, B, H, N, d, packed, dt, None)
 
