@@ -286,7 +286,9 @@ attn_status_t launch_f(const CacheReadParams& p, int fp16, cudaStream_t stream) 
 attn_status_t launch_cache_read(CacheReadParams p, int format_bits, int d, int fp16, cudaStream_t stream) {
   p.status = device_status_word();
   if (!p.status) return fail(ATTN_ERR_CUDA, "status word unavailable");
-  if (2LL * p.H_kv > 65535 || p.B > 65535) return fail(ATTN_ERR_UNSUPPORTED, "grid dimension limit exceeded");
+  // (a packed read's grid has no dimension for the requests)
+  if (2LL * p.H_kv > 65535 || (p.cu_seqlens == nullptr && p.B > 65535))
+    return fail(ATTN_ERR_UNSUPPORTED, "H_kv must be <= 32767, and B <= 65535 where the output is padded");
   p.page_shift = page_shift_of(p.page_size);
   if (format_bits == 4) return d == 64 ? launch_f<64, k4>(p, fp16, stream) : launch_f<128, k4>(p, fp16, stream);
   if (format_bits == 8) return launch_f<128, k8>(p, fp16, stream);

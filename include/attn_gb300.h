@@ -854,7 +854,7 @@ attn_status_t attn_decode_paged_fp4(const void* q, const uint8_t* k_cache, const
  * Lengths, offsets or first positions that do not fit, packed rows behind a sequence's end
  * and pages outside the cache are written as zeros (rows that no request owns are left) and
  * reported by attn_get_device_status() as ATTN_ERR_INVALID_ARG.
- * n may be 0.  d and page_size: as the cache's append.
+ * n may be 0.  d and page_size: as the cache's append.  H_kv <= 32767; padded outputs: B <= 65535.
  * Source: the paged cache of attn_decode_paged, and its cache-to-prefill direction: "FlashAttention
  * 3 Hardware Acceleration: ...", section "Production Inference Engines" (separate prefill
  * and decode functions).

@@ -712,6 +712,24 @@ def test_read_of_many_rows_is_that_of_few(attn, bits, d):
         assert torch.equal(packed[:9000], padded[0].transpose(0, 1)) and torch.equal(packed[9000:], padded[2, :, :7001].transpose(0, 1))
 
 
+def test_read_of_very_many_requests(attn):
+    """Packed outputs take any number of requests, padded ones up to 65,535 (a dimension of the grid)."""
+    B, page, H_kv, d = 70000, 16, 1, 64
+    rng = np.random.default_rng(37)
+    lens = rng.integers(0, 3, B)
+    lens[30000:30500] = 0                         # more empty ones than a block keeps at hand
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    kc, vc = (torch.randn(50, page, H_kv, d, device=dev()).bfloat16() for _ in range(2))
+    table = rng.integers(0, 50, (B, 1))
+    k, v = attn.attn_cache_read(kc, vc, _i32(table), _i32(lens), int(cu[-1]), cu_seqlens=_i32(cu))
+    check_status(attn)
+    b = np.repeat(np.arange(B), lens)
+    at = torch.from_numpy(table[b, 0]).to(dev()), torch.from_numpy(np.arange(cu[-1]) - cu[b]).to(dev())
+    assert torch.equal(k, kc[at]) and torch.equal(v, vc[at])
+    with pytest.raises(attn.AttnError, match="65535"):
+        attn.attn_cache_read(kc, vc, _i32(table), _i32(lens), 1)
+
+
 def test_read_reports_what_does_not_fit(attn):
     c = Cache(33, [40, 40], 16, 2, 64)
     kc, vc, kd, vd, bt, lens = c.args()
