@@ -61,10 +61,10 @@ __global__ void __launch_bounds__(kThreads)
     float fa[8], fb[8], x[8];
     unpack16<FP16>(a[k], fa);
     unpack16<FP16>(b[k], fb);
-    // what a part of weight 0 holds does not matter
+    // what an empty part holds does not matter; of another, however small its weight, infinities and NaN show
+    const bool has_a = xa[k] != -INFINITY, has_b = xb[k] != -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = (w.a == 0.f ? 0.f : w.a * fa[i]) + (w.b == 0.f ? 0.f : w.b * fb[i]);
+    for (int i = 0; i < 8; ++i) x[i] = (has_a ? w.a * fa[i] : 0.f) + (has_b ? w.b * fb[i] : 0.f);
     uint32_t p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)

@@ -880,7 +880,8 @@ attn_status_t attn_cache_read_fp4(const uint8_t* k_cache, const uint8_t* v_cache
  *   packed = 0 : o_a, o_b, o [B, H, N, d] in `dtype`, log-sum-exps float32 [B, H, N];
  *   packed = 1 : o_a, o_b, o [N, H, d], log-sum-exps [H, N] (B = 1): as the packed forward.
  * A part with lse = -inf counts as empty, whatever its o holds; two such give o = 0 and
- * lse = -inf.  o may be o_a or o_b and lse may be lse_a or lse_b, whole; other overlaps are
+ * lse = -inf.  An infinity or a NaN of another part's o gives an infinity or a NaN, however
+ * small its weight (0 * inf = NaN), and an lse of +inf or NaN gives NaN.  o may be o_a or o_b and lse may be lse_a or lse_b, whole; other overlaps are
  * refused.  d = 64, 128 or 256; B * H * N * d < 2^31.
  * Source: "FlashAttention-3: Hopper Asynchrony and FP8 Attention", section "Symbol Map" (L
  * and O of the running softmax): its update rule between two blocks of keys.

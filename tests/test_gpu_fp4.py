@@ -814,6 +814,31 @@ def test_merge_of_unusual_log_sum_exps(attn):
     assert torch.all(got[0, 0, 1:] == 1) and lse[0, 0, 1] == 1e30 and lse[0, 0, 2] == -1e30
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_merge_of_infinities_and_nan(attn, d, packed, dtype):
+    """They show unless their part is empty, also where its weight is 0 in float32; an lse of +inf is NaN."""
+    inf, nan = float("inf"), float("nan")
+    la = torch.tensor([0.0, 0.0, 0.0, 0.0, -inf, inf, inf, 0.0], device=dev())
+    lb = torch.tensor([-5.0, -150.0, -900.0, -150.0, 0.0, 0.0, inf, 0.0], device=dev())
+    oa, ob = (torch.ones(8, 1, d, device=dev()).to(dtype) for _ in range(2))
+    ob[0:3, :, 7] = inf
+    ob[3, :, 7] = nan
+    oa[4] = nan
+    shape = (lambda x: x) if packed else (lambda x: x.transpose(0, 1)[None])
+    rows = (lambda x: x[None]) if packed else (lambda x: x[None, None])
+    want_bad = torch.zeros(8, d, dtype=torch.bool)
+    want_bad[0:4, 7] = True
+    want_bad[5:7] = True
+    for first, second in (((oa, la), (ob, lb)), ((ob, lb), (oa, la))):
+        o, lse = attn.attn_merge(shape(first[0]), rows(first[1]), shape(second[0]), rows(second[1]))
+        check_status(attn)
+        o, lse = o.reshape(8, d).float().cpu(), lse.ravel().cpu()
+        assert torch.equal(~torch.isfinite(o), want_bad) and torch.all(o[~want_bad] == 1)
+        assert torch.equal(torch.isnan(lse), want_bad[:, 0]) and lse[4] == 0
+
+
 # ---------------------------------------------------------------------- together ----
 @pytest.mark.parametrize("d,signs", [(128, True), (64, False)])
 def test_prompts_in_chunks_then_tokens(attn, d, signs):
