@@ -426,6 +426,30 @@ def test_decode_large_values_of_far_lower_scores(attn, lens, H_kv, G, d, dtype):
 
 
 @pytest.mark.parametrize("lens,H_kv", SHAPES, ids=["clusters", "shares"])
+@pytest.mark.parametrize("G", [1, 8, 16])
+@pytest.mark.parametrize("signs", [False, True])
+@pytest.mark.parametrize("d,dtype", TYPES)
+def test_decode_of_one_key_with_all_the_weight(attn, lens, H_kv, G, signs, d, dtype):
+    """Queries of 2^14 against keys of which one has a component there: the others' weights are below
+    2^-10000.  O is that key's value row but for its own weight (1: the terms of 1 x descale), factors and
+    rounding; a row of zeros, half of the row or another key's fail."""
+    c = Cache(61, lens, 16, H_kv, d)
+    c.codes[1] |= 0x22                   # magnitudes 1, 1.5, 4 and 6: no zeros
+    sg = _signs(d) if signs else None
+    q, at = _one_hot(c, lens, d, G * H_kv, dtype, 2.0 ** 14, signs=sg)
+    o, lse = attn.attn_decode_paged_fp4(q, *c.args(), max(lens), hadamard_signs=sg)
+    check_status(attn)
+    v = c.values()[1]
+    want = np.stack([np.repeat(v[c.table[b, t // 16], t % 16], G, 0) for b, t in enumerate(at)])[:, :, None]
+    assert np.abs(want).min() > 0
+    assert np.all(np.abs(_np(o) - want) <= (PROB[dtype] + 2.0 ** -16 + HALF[dtype]) * np.abs(want))
+    # the score as the queries are rounded; the transform's float32 steps are each off by 2^-24
+    x = _np(q)
+    x = (x if sg is None else oracle.incoherent_transform(x, sg.cpu().numpy()))[..., 0] * 6 / np.sqrt(d)
+    assert np.all(np.abs(_np(lse) - x) <= 2.0 ** -18 * x)
+
+
+@pytest.mark.parametrize("lens,H_kv", SHAPES, ids=["clusters", "shares"])
 @pytest.mark.parametrize("G", [1, 2, 4])
 @pytest.mark.parametrize("d,dtype", TYPES)
 def test_decode_large_values_of_unseen_tokens(attn, lens, H_kv, G, d, dtype):
@@ -812,6 +836,32 @@ def test_merge_of_unusual_log_sum_exps(attn):
     check_status(attn)
     assert torch.isnan(got[0, 0, 0]).all() and torch.isnan(lse[0, 0, 0])
     assert torch.all(got[0, 0, 1:] == 1) and lse[0, 0, 1] == 1e30 and lse[0, 0, 2] == -1e30
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1), (3, 8, 130)])
+@pytest.mark.parametrize("d,dtype", [(64, torch.bfloat16), (128, torch.float16), (256, torch.float16)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_merge_of_the_other_types(attn, shape, d, dtype, packed):
+    """The kernels that test_merge does not run, in place too."""
+    B, H, N = shape
+    rng = np.random.default_rng(71 + B * N)
+    full, rows = ((N, H, d), (H, N)) if packed else ((B, H, N, d), (B, H, N))
+    oa, ob = (torch.from_numpy(rng.standard_normal(full)).to(dev(), dtype) for _ in range(2))
+    la, lb = (torch.from_numpy(5 * rng.standard_normal(rows)).float().to(dev()) for _ in range(2))
+    la[..., ::7], lb[..., ::5] = -float("inf"), -float("inf")
+    host = lambda o: _np(o).swapaxes(0, 1) if packed else _np(o)
+    ref_o, ref_l = oracle.merge_attention(host(oa), _np(la), host(ob), _np(lb))
+    o, lse = attn.attn_merge(oa, la, ob, lb)
+    check_status(attn)
+    tol = HALF[dtype] * np.abs(ref_o) + 2.0 ** -20 * (np.abs(host(oa)) + np.abs(host(ob))) + 2.0 ** -25
+    assert np.all(np.abs(host(o) - ref_o) <= tol)
+    fin = np.isfinite(ref_l)
+    assert np.array_equal(_np(lse)[~fin], ref_l[~fin])
+    assert np.all(np.abs(_np(lse)[fin] - ref_l[fin]) <= 2.0 ** -21 * (2 + np.abs(ref_l[fin])))
+    for xo, xl, a, b in ((oa.clone(), la.clone(), None, (ob, lb)), (ob.clone(), lb.clone(), (oa, la), None)):
+        attn.attn_merge(*(a or (xo, xl)), *(b or (xo, xl)), o=xo, lse=xl)
+        assert torch.equal(xo, o) and torch.equal(xl, lse)
+    check_status(attn)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
