@@ -273,7 +273,7 @@ attn_status_t launch_t(const AppendFp4Params& p, RopeKParams q, cudaStream_t str
   constexpr int tokens = kThreads / (D / 16);
   const long long columns = (static_cast<long long>(p.total) + tokens - 1) / tokens;
   // heads per block: all of a token's share its table entries, as long as the machine is
-  // filled (8 blocks of 4 warps per SM)
+  // filled (152 x 8 blocks; an SM holds 7 at a time)
   int per = p.H_kv;
   while (per > 1 && columns * 2 * ((p.H_kv + per - 1) / per) < 152 * 8) per = (per + 1) / 2;
   const int chunks = (p.H_kv + per - 1) / per;

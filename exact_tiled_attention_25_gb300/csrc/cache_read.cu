@@ -260,10 +260,12 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// A plane a block where that is one wave (16 blocks to an SM) or less, several as long as a wave is
-// left.  16,000 packed rows of 16 requests, 8 heads: a plane each 30 us, so 23.7, in half a wave 27;
-// 8 ranges of up to 16384 tokens 101 (6.0 TB/s); one of 509 tokens 3.2; e4m3, 65,536 packed rows of 4
-// heads 37.1.  Four rows of a thread instead, a plane each, took 28, 102, 5.0 and 38.6.
+// A plane a block, and several where 152 x 16 blocks are left so: a threshold found by trying, not
+// a wave (of 128 threads with 40 to 56 registers 9 to 12 blocks fit on an SM).  16,000 packed rows of 16
+// requests, 8 heads: a plane each 30 us, so 24.0, with half of the blocks 27; 8 ranges of up to 16384
+// tokens 100.8 (6.0 TB/s); one of 509 tokens 3.2; e4m3, 65,536 packed rows of 4 heads 37.0.  Four rows of a
+// thread instead, a plane each, took 28, 102, 5.0 and 38.6.  The 8 ranges of a 16-bit cache 121.5, packed 82
+// (6.6 and 6.3 TB/s).
 template <int D, int FORMAT, bool FP16, bool SIGNS>
 attn_status_t launch_t(const CacheReadParams& p, cudaStream_t stream) {
   constexpr int rows = kThreads / (D / 16);

@@ -34,10 +34,10 @@
 //    that cross shares are joined by a second, dependent kernel from float32 partial results
 //    (at most two per CTA).  With few segments a cluster of up to eight CTAs takes each instead and
 //    joins its partial results through distributed shared memory: one launch, no scratch, no prefix
-//    sums (one request of 1500 tokens, 8 heads: 10.4 us by shares when this took 8.0; 7.4 now).
-//  * Measured: 16 x 8192 tokens, 8 heads of d = 128, 4 query rows each 29.5 us (4.8 TB/s; some 9 us
-//    are the dealing out, the first tile, the last one and the joining), 8 rows 33.3, 16 rows 51 (bound by
-//    the chain of a tile's softmax); 64 sequences of up to 16384 tokens, d = 64: 58.2 us (4.9 TB/s).
+//    sums (one request of 1500 tokens, 8 heads: 10.4 us by shares when this took 8.0; 7.2 now).
+//  * Measured: 16 x 8192 tokens, 8 heads of d = 128, 4 query rows each 29.7 us (4.7 TB/s; some 9 us
+//    are the dealing out, the first tile, the last one and the joining), 8 rows 33.5, 16 rows 51.0 (bound by
+//    the chain of a tile's softmax); 64 sequences of up to 16384 tokens, d = 64: 58.9 us (4.9 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -1162,10 +1162,10 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp4_merge_kernel(const K
 
 // CTAs of the cluster that takes a segment, or 0: all segments' tiles dealt out in one line.  The
 // smaller modelled time, in microseconds, fitted to 4 and 16 rows of d = 128, 1 to 32 sequences of 500 to
-// 16384 tokens: a start and an end, the tiles of one CTA (less with an SM to itself), and for the line
+// 16384 tokens (8 rows and d = 64 take it as it is): a start and an end, the tiles of one CTA (less with an SM to itself), and for the line
 // the joining of a segment's CTAs (of 34 shapes one took 11 % more than the other way, the rest at
 // most 4).  One sequence of 4096 tokens, 8 heads: 8.5 by clusters, 12.3 in line; of 16384 14.7 and 15.9;
-// 16 of 8192 in line 29.5.  Clusters only as far as all of them run at a time (with one CTA to an SM
+// 16 of 8192 in line 29.7.  Clusters only as far as all of them run at a time (with one CTA to an SM
 // and with two: a multiprocessor group's SMs are not a multiple of every size).
 inline int cluster_of(int B, int segs, int tiles, int per_sm) {
   constexpr int at_a_time[2][9] = {{0, 152, 76, 46, 36, 28, 23, 15, 15}, {0, 304, 152, 97, 74, 58, 46, 38, 36}};

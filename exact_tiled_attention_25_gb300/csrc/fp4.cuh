@@ -19,7 +19,7 @@ namespace attn {
 
 constexpr float kMinRowDescale = 0x1p-100f;   // 1 / s and the quotients' residuals stay normal numbers
 
-// Two float32 -> a byte of two codes (lo: low half), round to nearest even, largest 6.
+// Eight float32 -> a word of eight codes (element 0 in the lowest four bits), round to nearest even, largest 6.
 __device__ __forceinline__ uint32_t e2m1_word(const float (&x)[8]) {
   uint32_t w;
   asm("{\n .reg .b8 a, b, c, d;\n"

@@ -3,7 +3,7 @@
 //
 // A row's d / 8 threads (16 bytes of each output) are lanes of one warp and read the two
 // log-sum-exps before one of them stores L, so the results may replace either input.
-// Bound: DRAM, 6 d + 12 bytes a row: 262,144 rows of d = 128 take 30.0 us (6.8 TB/s), 2048 rows 1.8.
+// Bound: DRAM, 6 d + 12 bytes a row: 262,144 rows of d = 128 take 30.7 us (6.7 TB/s), 2048 rows 1.8.
 #include <cmath>
 
 #include "common.h"

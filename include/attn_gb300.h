@@ -822,7 +822,12 @@ size_t attn_decode_fp4_workspace_size(int B, int H, int H_kv, int n_q, int d, in
  *   behind a sequence hold does not matter.
  * Accuracy: the stored values enter exactly, queries to 2^-19.  The product of a probability
  * and a value descale is held to half a step of `dtype`, and to 2^-20 (bf16) or 2^-25
- * (fp16) of the query row's largest one.  A query row with an infinity or a NaN gives NaN.
+ * (fp16) of the query row's largest one; O's own rounding to `dtype` comes on top.  A query
+ * row with an infinity or a NaN gives NaN; a key or value row whose descale is NaN (none is
+ * infinite) gives NaN to the query rows that see its token.
+ * Scores are float32 numbers, a sum of products with the query row scaled to 2^7 times one
+ * factor: a row whose largest magnitude times softmax_scale is below 2^-119 loses bits, and
+ * where that times a key descale passes 2^134 the row may be NaN.
  * Limits: d = 64 or 128; (H / H_kv) * n_q <= 128; page_size a power of two in [16, 65536];
  * B * H_kv * ceil((H / H_kv) * n_q / 16) * (max_pages * page_size / 128 + 8) < 2^31.
  * Source: as attn_decode_paged_fp8.
