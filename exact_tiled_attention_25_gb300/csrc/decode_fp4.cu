@@ -24,8 +24,9 @@
 //    codes is P' = p s^v c with c = 2^(M - T + 5), T a running reference of s + log2 s^v: it is
 //    the tokens that count for the result whose probabilities have all their bits, however the
 //    descales differ.  What is 2^-11 of the largest or less loses bits (an error of 2^-20 of that
-//    one; three terms: 2^-14 and 2^-25).  The references move only when a score exceeds M by 64 or P'
-//    would exceed 2^8, by a vote of the softmax warps once a tile.
+//    one; three terms: 2^-14 and 2^-25; float16, from which the terms are taken, adds up to 2^-30).
+//    The references move only when a score exceeds M by 64 or P' would exceed 2^8, by a vote of the
+//    softmax warps once a tile.
 //  * d = 64: rows of two neighbouring tokens are one row of the tile.  Their scores are two
 //    products over half the columns each; in O^T the first 64 lanes take the even tokens' columns
 //    and the others the odd ones', and the two halves are added at the end.

@@ -821,8 +821,8 @@ size_t attn_decode_fp4_workspace_size(int B, int H, int H_kv, int n_q, int d, in
  *   attn_decode_paged; a token on a page that is out of range is not seen.  What the slots
  *   behind a sequence hold does not matter.
  * Accuracy: the stored values enter exactly, queries to 2^-19.  The product of a probability
- * and a value descale is held to half a step of `dtype`, and to 2^-20 (bf16) or 2^-25
- * (fp16) of the query row's largest one; O's own rounding to `dtype` comes on top.  A query
+ * and a value descale is held to half a step of `dtype`, and to 1.04 x 2^-20 (bf16) or
+ * 1.04 x 2^-25 (fp16) of the query row's largest one; O's own rounding to `dtype` comes on top.  A query
  * row with an infinity or a NaN gives NaN; a key or value row whose descale is NaN (none is
  * infinite) gives NaN to the query rows that see its token.
  * Scores are float32 numbers, a sum of products with the query row scaled to 2^7 times one
